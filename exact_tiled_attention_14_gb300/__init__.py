@@ -5,8 +5,9 @@ This module only marshals arguments to the C ABI in ``include/fa.h``
 ``fa_fwd_ws``, ``fa_fwd_static``, ``fa_fwd_kv``, ``fa_fwd_varlen`` and their
 ``_dropout`` forms; the backward ``fa_bwd``, ``fa_bwd_kv``, ``fa_bwd_varlen``,
 their ``_dropout`` forms, ``fa_bwd_onepass`` and ``fa_bwd_onepass_dropout``;
-``fa_decode``; the workspace sizes, status and settings), under the same
-names.  Every step of
+``fa_decode``; the sliding-window ``fa_fwd_window``, ``fa_bwd_window`` and
+``fa_decode_window`` and the drafted-tree ``fa_decode_tree``; the workspace
+sizes, status and settings), under the same names.  Every step of
 the attention computation runs in the CUDA kernels of ``_build/libfa.so``;
 there is no CPU or PyTorch fallback.  When the library has not been built,
 every call raises.
@@ -18,10 +19,15 @@ current CUDA stream.  ``attention_backward`` does the same for ``fa_bwd``
 (dQ, dK, dV and the D scratch), ``attention_decode`` for ``fa_decode``,
 ``attention_forward_kv`` for ``fa_fwd_kv``, ``attention_forward_varlen`` for
 ``fa_fwd_varlen``, ``attention_backward_onepass`` for ``fa_bwd_onepass``
-(and ``fa_bwd_onepass_dropout``).  ``flash_attention``, ``flash_attention_kv`` and
-``flash_attention_varlen`` wrap the forward and backward entry points in
+(and ``fa_bwd_onepass_dropout``), ``attention_forward_window`` for
+``fa_fwd_window``, ``attention_backward_window`` for ``fa_bwd_window``,
+``attention_decode_window`` for ``fa_decode_window`` and
+``attention_decode_tree`` for ``fa_decode_tree``.  ``flash_attention``,
+``flash_attention_kv``, ``flash_attention_varlen`` and
+``flash_attention_window`` wrap the forward and backward entry points in
 torch.autograd functions.
 """
+import contextlib
 import ctypes
 import math
 import os
@@ -52,7 +58,10 @@ EXPORTS = ("fa_fwd", "fa_fwd_kv", "fa_fwd_varlen", "fa_fwd_dropout", "fa_bwd_dro
            "fa_bwd_varlen_dropout",
            "fa_fwd_ws", "fa_fwd_workspace_size", "fa_fwd_static", "fa_bwd",
            "fa_bwd_onepass", "fa_bwd_onepass_workspace_size", "fa_bwd_onepass_dropout",
-           "fa_decode", "fa_decode_workspace_size", "fa_strerror", "fa_status",
+           "fa_decode", "fa_decode_workspace_size",
+           "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_workspace_size",
+           "fa_decode_window", "fa_decode_tree", "fa_decode_window_workspace_size",
+           "fa_strerror", "fa_status",
            "fa_set_watchdog_ns", "fa_set_unit_group", "fa_watchdog_selftest", "fa_work_tiles",
            "fa_version")
 
@@ -121,6 +130,19 @@ def load_library(path=None):
     lib.fa_decode.restype = i
     lib.fa_decode_workspace_size.argtypes = [i] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.fa_decode_workspace_size.restype = i
+    lib.fa_fwd_window.argtypes = [vp] * 5 + [i] * 9 + [vp, f, i, vp]
+    lib.fa_fwd_window.restype = i
+    lib.fa_bwd_window.argtypes = [vp] * 10 + [i] * 9 + [vp, f, i, vp, ctypes.c_size_t, vp]
+    lib.fa_bwd_window.restype = i
+    lib.fa_bwd_window_workspace_size.argtypes = [i] * 7 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_bwd_window_workspace_size.restype = i
+    lib.fa_decode_window.argtypes = [vp] * 5 + [i] * 8 + [vp, f, i, vp, ctypes.c_size_t, vp]
+    lib.fa_decode_window.restype = i
+    lib.fa_decode_tree.argtypes = ([vp] * 5 + [i] * 6 + [vp, i, i, vp, f, i, vp, ctypes.c_size_t,
+                                                         vp])
+    lib.fa_decode_tree.restype = i
+    lib.fa_decode_window_workspace_size.argtypes = [i] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_decode_window_workspace_size.restype = i
     lib.fa_strerror.argtypes = [i]
     lib.fa_strerror.restype = ctypes.c_char_p
     lib.fa_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
@@ -352,6 +374,69 @@ def fa_decode_workspace_size(B, H, Nq, Nk, d):
                                                    ctypes.byref(out))
     if code:
         raise FaError(code, "fa_decode_workspace_size")
+    return out.value
+
+
+def fa_fwd_window(q, k, v, o, lse, B, H, Hk, Nq, Nk, d, causal, window, sinks, seqlens_k, scale,
+                  dtype, stream=None):
+    """Raw C call of the sliding-window forward (H query heads on Hk key/value
+    heads; causal 1 upper-left, 2 bottom-right); returns the code."""
+    lib = load_library()
+    return lib.fa_fwd_window(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), int(B), int(H),
+                             int(Hk), int(Nq), int(Nk), int(d), int(causal), int(window),
+                             int(sinks), _addr(seqlens_k), float(scale), int(dtype),
+                             _stream(stream))
+
+
+def fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, delta, B, H, Hk, Nq, Nk, d, causal, window,
+                  sinks, seqlens_k, scale, dtype, workspace, workspace_bytes, stream=None):
+    """Raw C call of the backward pass of fa_fwd_window; returns the code."""
+    lib = load_library()
+    return lib.fa_bwd_window(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(dout),
+                             _addr(dq), _addr(dk), _addr(dv), _addr(delta), int(B), int(H),
+                             int(Hk), int(Nq), int(Nk), int(d), int(causal), int(window),
+                             int(sinks), _addr(seqlens_k), float(scale), int(dtype),
+                             _addr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, sinks):
+    """Workspace bytes fa_bwd_window needs for this shape."""
+    out = ctypes.c_size_t(0)
+    code = load_library().fa_bwd_window_workspace_size(int(B), int(H), int(Hk), int(Nq), int(Nk),
+                                                       int(d), int(sinks), ctypes.byref(out))
+    if code:
+        raise FaError(code, "fa_bwd_window_workspace_size")
+    return out.value
+
+
+def fa_decode_window(q, k, v, o, lse, B, H, Hk, Nq, Nk, d, window, sinks, seqlens_k, scale, dtype,
+                     workspace, workspace_bytes, stream=None):
+    """Raw C call of sliding-window decoding; returns the code."""
+    lib = load_library()
+    return lib.fa_decode_window(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), int(B), int(H),
+                                int(Hk), int(Nq), int(Nk), int(d), int(window), int(sinks),
+                                _addr(seqlens_k), float(scale), int(dtype), _addr(workspace),
+                                int(workspace_bytes), _stream(stream))
+
+
+def fa_decode_tree(q, k, v, o, lse, B, H, Hk, Nq, Nk, d, tree, window, sinks, seqlens_k, scale,
+                   dtype, workspace, workspace_bytes, stream=None):
+    """Raw C call of drafted-tree decoding; returns the code."""
+    lib = load_library()
+    return lib.fa_decode_tree(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), int(B), int(H),
+                              int(Hk), int(Nq), int(Nk), int(d), _addr(tree), int(window),
+                              int(sinks), _addr(seqlens_k), float(scale), int(dtype),
+                              _addr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fa_decode_window_workspace_size(B, H, Hk, Nq, Nk, d):
+    """Workspace bytes fa_decode_window and fa_decode_tree need for this shape
+    on the current device."""
+    out = ctypes.c_size_t(0)
+    code = load_library().fa_decode_window_workspace_size(int(B), int(H), int(Hk), int(Nq),
+                                                          int(Nk), int(d), ctypes.byref(out))
+    if code:
+        raise FaError(code, "fa_decode_window_workspace_size")
     return out.value
 
 
@@ -838,6 +923,235 @@ def attention_decode(q, k, v, causal=False, scale=None, out=None, lse=None, work
     return out, lse
 
 
+# ---------------------------------------------------------------- windows, trees
+# Calls with a sliding window and sinks, or a tree of drafted tokens.  Key/value
+# heads may be shared: q has H heads, k and v Hk, H a multiple of Hk.  They
+# run on the tensors' device and, with ``stream`` given, allocate what they
+# return on that stream.
+
+def _window_args(q, k, v, window, sinks, seqlens_k, what):
+    """Checks shared by the window and tree calls; returns
+    (B, H, Hk, Nq, Nk, d)."""
+    import torch
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError(f"dtypes differ: {q.dtype}, {k.dtype}, {v.dtype}")
+    dtype_code(q.dtype)
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError(f"{what}: q must be [B, H, Nq, d] and k, v [B, Hk, Nk, d]")
+    B, H, Nq, d = q.shape
+    Hk, Nk = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != d:
+        raise ValueError(f"{what}: q and k differ in batch or head width")
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"{what}: {H} query heads are not a multiple of {Hk} key/value heads")
+    if window < 1:
+        raise ValueError(f"{what}: window must be at least 1")
+    if sinks < 0:
+        raise ValueError(f"{what}: sinks must not be negative")
+    if not all(t.is_cuda and t.device == q.device for t in (q, k, v)):
+        raise ValueError(f"{what}: q, k, v must be CUDA tensors of one device")
+    if not all(t.is_contiguous() for t in (q, k, v)):
+        raise ValueError(f"{what}: q, k, v must be contiguous")
+    if seqlens_k is not None:
+        if (seqlens_k.dtype != torch.int32 or seqlens_k.shape != (B,)
+                or seqlens_k.device != q.device or not seqlens_k.is_contiguous()):
+            raise ValueError(f"{what}: seqlens_k must be a contiguous int32 tensor [B] on q's device")
+    return B, H, Hk, Nq, Nk, d
+
+
+def _check_buffer(t, shape, dtype, device, name):
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def attention_forward_window(q, k, v, window, sinks=0, causal="bottom_right", seqlens_k=None,
+                             scale=None, out=None, lse=None, stream=None):
+    """O [B, H, Nq, d], LSE [B, H, Nq] of queries q [B, H, Nq, d] against keys
+    and values k, v [B, Hk, Nk, d] (CUDA, contiguous, one 16-bit dtype, d 64
+    or 128) under a sliding window with sinks: the query at position p sees
+    key j when j <= p and (j > p - window or j < sinks).
+
+    ``causal``: "bottom_right" (query i at position len_b - Nq + i) or
+    "upper_left" (at position i).  ``seqlens_k``: None or int32 [B] key counts.
+    Query head h reads key/value head h // (H // Hk).  A query that sees no
+    key gets O = 0 and LSE = -inf.  Calls ``fa_fwd_window`` on ``stream``
+    (default: current stream).
+    """
+    import torch
+    B, H, Hk, Nq, Nk, d = _window_args(q, k, v, window, sinks, seqlens_k,
+                                       "attention_forward_window")
+    if causal not in ("upper_left", "bottom_right"):
+        raise ValueError("causal must be 'upper_left' or 'bottom_right'")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with torch.cuda.device(q.device), _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _check_buffer(out, (B, H, Nq, d), q.dtype, q.device, "out")
+        if lse is None:
+            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        else:
+            _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
+        rc = fa_fwd_window(q, k, v, out, lse, B, H, Hk, Nq, Nk, d, CAUSAL_MODES[causal],
+                           _int32(window), _int32(sinks), seqlens_k, scale, dtype_code(q.dtype),
+                           _current(stream, q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_window")
+    return out, lse
+
+
+def attention_backward_window(q, k, v, o, lse, dout, window, sinks=0, causal="bottom_right",
+                              seqlens_k=None, scale=None, workspace=None, stream=None):
+    """dQ, dK, dV of sum(dout * O) for O, LSE = attention_forward_window(q, k, v,
+    window, sinks, causal, seqlens_k) (``fa_bwd_window``; dK and dV summed
+    over the query heads of each group).  ``workspace``: a uint8 CUDA tensor
+    of at least ``fa_bwd_window_workspace_size`` bytes; allocated here when
+    None."""
+    import torch
+    B, H, Hk, Nq, Nk, d = _window_args(q, k, v, window, sinks, seqlens_k,
+                                       "attention_backward_window")
+    if causal not in ("upper_left", "bottom_right"):
+        raise ValueError("causal must be 'upper_left' or 'bottom_right'")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _check_buffer(o, (B, H, Nq, d), q.dtype, q.device, "o")
+    _check_buffer(dout, (B, H, Nq, d), q.dtype, q.device, "dout")
+    _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
+    with torch.cuda.device(q.device), _on(stream):
+        if workspace is None:
+            need = fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, _int32(sinks))
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        delta = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        rc = fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, delta, B, H, Hk, Nq, Nk, d,
+                           CAUSAL_MODES[causal], _int32(window), _int32(sinks), seqlens_k, scale,
+                           dtype_code(q.dtype), workspace, ws_bytes, _current(stream, q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_bwd_window")
+    return dq, dk, dv
+
+
+def make_decode_workspace(q, k):
+    """A workspace (uint8 tensor on q's device) for attention_decode_window and
+    attention_decode_tree calls with q [B, H, Nq, d] and a cache k
+    [B, Hk, Nk, d].  Calls that may run at the same time, on two streams or in
+    two captured graphs, need one each."""
+    import torch
+    B, H, Nq, d = q.shape
+    with torch.cuda.device(q.device):
+        n = fa_decode_window_workspace_size(B, H, k.shape[1], Nq, k.shape[2], d)
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def _decode(fn, where, q, k, v, tree, window, sinks, seqlens_k, scale, out, lse, workspace, stream,
+            dims):
+    import torch
+    B, H, Hk, Nq, Nk, d = dims
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with torch.cuda.device(q.device), _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _check_buffer(out, (B, H, Nq, d), q.dtype, q.device, "out")
+        if lse is None:
+            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        else:
+            _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
+        if workspace is None:
+            workspace = make_decode_workspace(q, k)
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+        rc = fn(q, k, v, out, lse, B, H, Hk, Nq, Nk, d, *tree, _int32(window), _int32(sinks),
+                seqlens_k, scale, dtype_code(q.dtype), workspace, ws_bytes, _current(stream, q))
+    if rc != FA_OK:
+        raise FaError(rc, where)
+    return out, lse
+
+
+def attention_decode_window(q, k, v, window, sinks=0, seqlens_k=None, scale=None, out=None,
+                            lse=None, workspace=None, stream=None):
+    """O, LSE of the last Nq (1 .. 16) tokens of each sequence, q [B, H, Nq, d],
+    against its cache k, v [B, Hk, Nk, d] under attention_forward_window's
+    mask: token i sits at position len_b - Nq + i, where len_b is
+    ``seqlens_k[b]`` (int32 [B], counting the new tokens' own keys) or Nk.
+    Calls ``fa_decode_window``.  ``workspace``: see ``make_decode_workspace``;
+    None allocates one.
+    """
+    dims = _window_args(q, k, v, window, sinks, seqlens_k, "attention_decode_window")
+    return _decode(fa_decode_window, "fa_decode_window", q, k, v, (), window, sinks, seqlens_k,
+                   scale, out, lse, workspace, stream, dims)
+
+
+def attention_decode_tree(q, k, v, tree, seqlens_k=None, window=None, sinks=0, scale=None,
+                          out=None, lse=None, workspace=None, stream=None):
+    """O, LSE of Nq (1 .. 64) drafted tokens of each sequence, q [B, H, Nq, d],
+    against its cache k, v [B, Hk, Nk, d]: the history fills slots
+    0 .. c_b - 1, drafted token j slot c_b + j, with c_b = ``seqlens_k[b]``
+    (int32 [B]) or Nk - Nq.
+
+    ``tree``: int64 [B, Nq]; bit j of row i marks drafted token j as seen by
+    token i (its ancestors and itself; see ``tree_rows``).  A token's position
+    is c_b - 1 plus the number of tokens its row marks.  ``window`` (None: no
+    limit) and ``sinks`` as in attention_forward_window, by position.  Calls
+    ``fa_decode_tree``.
+    """
+    import torch
+    dims = _window_args(q, k, v, 1 if window is None else window, sinks, seqlens_k,
+                        "attention_decode_tree")
+    if tree.dtype != torch.int64 or tree.shape != q.shape[:1] + q.shape[2:3] \
+            or tree.device != q.device or not tree.is_contiguous():
+        raise ValueError("attention_decode_tree: tree must be a contiguous int64 tensor [B, Nq] "
+                         "on q's device")
+    return _decode(fa_decode_tree, "fa_decode_tree", q, k, v, (tree,),
+                   0 if window is None else window, sinks, seqlens_k, scale, out, lse, workspace,
+                   stream, dims)
+
+
+def tree_rows(parents):
+    """The int64 rows of attention_decode_tree for drafted tokens given by
+    ``parents`` (integer [B, Nq], Nq <= 64): parents[b, i] is the index of
+    token i's parent among the drafted tokens, less than i, or -1 for the
+    last committed token.  Token i's row marks itself and its ancestors."""
+    import torch
+    if parents.dim() != 2 or parents.shape[1] > 64:
+        raise ValueError("parents must be [B, Nq] with Nq <= 64")
+    B, Nq = parents.shape
+    at = torch.arange(Nq, device=parents.device)
+    if bool(((parents >= at) | (parents < -1)).any()):
+        raise ValueError("a parent must be -1 or an earlier drafted token")
+    rows = torch.zeros((B, Nq + 1), dtype=torch.int64, device=parents.device)   # last: parent -1
+    bit = torch.ones((), dtype=torch.int64, device=parents.device)
+    for i in range(Nq):
+        up = parents[:, i].long().remainder(Nq + 1)
+        rows[:, i] = rows.gather(1, up[:, None])[:, 0] | (bit << i)
+    return rows[:, :Nq].contiguous()
+
+
+def _int32(x):
+    """A count clamped to int32 (larger windows and sinks hide nothing more)."""
+    return min(int(x), 2**31 - 1)
+
+
+def _on(stream):
+    """Context in which a call's results are allocated: the given stream."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _current(stream, q):
+    import torch
+    return torch.cuda.current_stream(q.device) if stream is None else stream
+
+
 # ---------------------------------------------------------------- autograd
 # torch.autograd wrappers: the forward entry point in forward(), the matching
 # backward entry point in backward(), so a PyTorch training step can call
@@ -916,7 +1230,26 @@ def _autograd():
                                           seed=seed, offset=offset)
             return g[0], g[1], g[2], None, None, None, None, None, None, None, None, None
 
-    return _FlashAttention, _FlashAttentionKv, _FlashAttentionVarlen
+    class _FlashAttentionWindow(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, window, sinks, causal, seqlens_k, scale):
+            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+            o, lse = attention_forward_window(q, k, v, window, sinks, causal=causal,
+                                              seqlens_k=seqlens_k, scale=scale)
+            ctx.save_for_backward(q, k, v, o, lse, seqlens_k)
+            ctx.args = (window, sinks, causal, scale)
+            ctx.mark_non_differentiable(lse)
+            return o, lse
+
+        @staticmethod
+        def backward(ctx, do, _dlse):
+            q, k, v, o, lse, seqlens_k = ctx.saved_tensors
+            window, sinks, causal, scale = ctx.args
+            g = attention_backward_window(q, k, v, o, lse, do.contiguous(), window, sinks,
+                                          causal=causal, seqlens_k=seqlens_k, scale=scale)
+            return g[0], g[1], g[2], None, None, None, None, None
+
+    return _FlashAttention, _FlashAttentionKv, _FlashAttentionVarlen, _FlashAttentionWindow
 
 
 _AUTOGRAD = None
@@ -959,3 +1292,18 @@ def flash_attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, ma
     return _fns()[2].apply(q, k, v, cu_seqlens_q, cu_seqlens_k, int(max_seqlen_q),
                            int(max_seqlen_k), causal, float(scale), float(dropout_p), int(seed),
                            int(offset))
+
+
+def flash_attention_window(q, k, v, window, sinks=0, causal="bottom_right", seqlens_k=None,
+                           scale=None):
+    """Differentiable O, LSE of attention_forward_window (fa_fwd_window /
+    fa_bwd_window): q [B, H, Nq, d] on k, v [B, Hk, Nk, d].
+
+    To capture forward and backward in a CUDA graph, use leaves that no eager
+    autograd graph still refers to (drop the eager outputs first): torch runs
+    a leaf's accumulation on the stream it was first used on, and work on
+    another stream than the capturing one ends the capture.
+    """
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return _fns()[3].apply(q, k, v, int(window), int(sinks), causal, seqlens_k, float(scale))

@@ -52,6 +52,12 @@
 //   dq    dS goes to TMEM columns of its own (two buffers after dQ), so
 //         S_{j+1} and dP_{j+1} are issued as soon as the element-wise warps
 //         have read S_j and dP_j, and dQ_i += dS_j K_j when dS_j is written.
+//
+// Sliding-window calls (kWin: the query at position p sees the keys j <= p
+// with j > p - win or j < sinks; H query heads share Hk key/value heads)
+// walk only the tile pairs that hold a visible (query, key): a dQ item the
+// sink tiles and the tiles of its rows' windows, a dK/dV item the query
+// tiles of every head of its group that see the key tile.
 #pragma once
 
 #include <cuda.h>
@@ -142,6 +148,14 @@ struct BwdParams {
   // CTAs) are dealt in groups of item_group heads, tile by tile within a
   // group, so the CTAs at work share a few heads' streamed tiles in L2.
   int item_group;
+  // Sliding window (kWin variants, which are kKv and kCausal): window and
+  // sink counts (win >= 1), key/value heads per batch Hk (K, V, dK, dV are
+  // [BHk, Nk, d]) and the G = H / Hk query heads that share each.
+  int win;
+  int sinks;
+  int Hk;
+  int G;
+  int BHk;
 };
 
 // Tile index and head of work item `blk` among BH * n_tiles items dealt in
@@ -179,6 +193,39 @@ __device__ __forceinline__ BwdHead bwd_kv_head(const BwdParams& p, int bh, bool 
   }
   h.off = (causal && p.align_br) ? h.len - h.lenq : 0;
   return h;
+}
+
+// Sliding window (kWin): one past the last query tile of a head (n_tiles in
+// all, query i at position i + off) that sees a key of key tile kt of a
+// batch of len keys.  Unless the tile holds a sink, the last query that sees
+// its last key sits win - 1 positions after it.
+__host__ __device__ __forceinline__ int bwd_win_q_end(int kt, int len, int off, int n_tiles,
+                                                      int win, int sinks) {
+  if (kt * kBwdTile < sinks) return n_tiles;
+  const int key = (kt + 1) * kBwdTile < len ? (kt + 1) * kBwdTile - 1 : len - 1;
+  const int last = key + win - 1 - off;
+  if (last < 0) return 0;
+  return last / kBwdTile + 1 < n_tiles ? last / kBwdTile + 1 : n_tiles;
+}
+// Sliding window: the key tiles that the query tile with rows r0 .. r1 - 1
+// walks, of the n_end tiles up to its last row: ns sink tiles, then those
+// from wa on, count in all.  Of the keys in them some row sees those below
+// min(sinks, hi) and lo .. hi - 1.
+struct BwdWinKeys {
+  int ns, wa, count, lo, hi;
+};
+__host__ __device__ __forceinline__ BwdWinKeys bwd_win_keys(int r0, int r1, int len, int off,
+                                                            int n_end, int win, int sinks) {
+  BwdWinKeys k;
+  const int used = sinks < len ? sinks : len;
+  const int n_sink = (used + kBwdTile - 1) / kBwdTile;
+  const int lo = r0 + off - win + 1, end = r1 + off;
+  k.lo = lo > 0 ? lo : 0;
+  k.hi = end < 0 ? 0 : (end < len ? end : len);
+  k.ns = n_sink < n_end ? n_sink : n_end;
+  k.wa = k.lo / kBwdTile > n_sink ? k.lo / kBwdTile : n_sink;
+  k.count = k.ns + (n_end > k.wa ? n_end - k.wa : 0);
+  return k;
 }
 
 // Row indices of head bh (h = bh % H): of query row qrow in Q, dO, dQ (rows
@@ -416,6 +463,16 @@ struct DqBuf {
   }
 };
 
+// Zero rows [r0, r1) of a 128-row tile (64-column chunks of 128-byte rows),
+// 16 bytes at a time, by threads tid of nthreads.  The swizzle permutes the
+// 16-byte pieces within a row, so whole rows need no address arithmetic.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int chunks, int r0, int r1, int tid,
+                                          int nthreads) {
+  for (int i = r0 * 8 + tid; i < r1 * 8; i += nthreads)
+    for (int c = 0; c < chunks; ++c)
+      *reinterpret_cast<uint4*>(tile + c * (kBwdTile * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // Write columns [c0, c0 + nc) (nc a multiple of 32) of one row of a TMEM
 // accumulator (fp32), times `mul`, to global memory in the storage dtype, in
 // rows of `width` values (rows past N are skipped).
@@ -539,6 +596,51 @@ __device__ __forceinline__ void bwd_producer(uint32_t sbase, const CUtensorMap* 
     ptx::wait_drain(bar(L::bFullB + l % L::kStagesB), (l / L::kStagesB) & 1, drain);
 }
 
+// The same with tiles named by functions: res(y, z) and str(it, y, z) give
+// the row and head coordinates of the resident pair and of the it-th
+// streamed pair (kWin: tiles and heads are not consecutive).
+template <class L, class Res, class Str>
+__device__ __forceinline__ void bwd_producer_map(uint32_t sbase, const CUtensorMap* res_a,
+                                                 const CUtensorMap* res_b, Res res,
+                                                 const CUtensorMap* str_a,
+                                                 const CUtensorMap* str_b, Str str, int count,
+                                                 const ptx::Watchdog& wd) {
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
+  int y, z;
+  res(y, z);
+  ptx::mbar_arrive_expect_tx(bar(L::bRes), 2 * L::kTile);
+  for (int c = 0; c < L::kChunks; ++c) {
+    ptx::tma_load_3d(sbase + L::kRes + c * L::kChunkBytes, res_a, bar(L::bRes), c * 64, y, z);
+    ptx::tma_load_3d(sbase + L::kRes + L::kTile + c * L::kChunkBytes, res_b, bar(L::bRes), c * 64,
+                     y, z);
+  }
+  int na = 0, nb = 0;   // tiles issued into ring A / B
+  for (int it = 0; it < count; ++it) {
+    str(it, y, z);
+    const int sa = it % L::kStagesA, ua = it / L::kStagesA;
+    if (ua > 0 && !ptx::wait_bounded(bar(L::bEmptyA + sa), (ua - 1) & 1, wd, kSiteBwdEmpty)) break;
+    ptx::mbar_arrive_expect_tx(bar(L::bFullA + sa), L::kTile);
+    for (int c = 0; c < L::kChunks; ++c)
+      ptx::tma_load_3d(sbase + L::kRingA + sa * L::kTile + c * L::kChunkBytes, str_a,
+                       bar(L::bFullA + sa), c * 64, y, z);
+    ++na;
+    const int sb = it % L::kStagesB, ub = it / L::kStagesB;
+    if (ub > 0 && !ptx::wait_bounded(bar(L::bEmptyB + sb), (ub - 1) & 1, wd, kSiteBwdEmpty)) break;
+    ptx::mbar_arrive_expect_tx(bar(L::bFullB + sb), L::kTile);
+    for (int c = 0; c < L::kChunks; ++c)
+      ptx::tma_load_3d(sbase + L::kRingB + sb * L::kTile + c * L::kChunkBytes, str_b,
+                       bar(L::bFullB + sb), c * 64, y, z);
+    ++nb;
+  }
+  // Drain: every issued copy has landed before the CTA can exit.
+  const unsigned long long drain = 200000000ull;
+  ptx::wait_drain(bar(L::bRes), 0, drain);
+  for (int l = na > L::kStagesA ? na - L::kStagesA : 0; l < na; ++l)
+    ptx::wait_drain(bar(L::bFullA + l % L::kStagesA), (l / L::kStagesA) & 1, drain);
+  for (int l = nb > L::kStagesB ? nb - L::kStagesB : 0; l < nb; ++l)
+    ptx::wait_drain(bar(L::bFullB + l % L::kStagesB), (l / L::kStagesB) & 1, drain);
+}
+
 // ---------------------------------------------------------------- dK, dV
 // Per-query vectors of the dkdv kernel: one buffer at d = 128 (shared memory
 // is full), two at d = 64.
@@ -549,7 +651,7 @@ struct DkdvVec {
 };
 
 // One CTA of the dK/dV pass: block `blk` of BH * n_tiles.
-template <int D, bool kBf16, bool kCausal, bool kDrop, bool kKv>
+template <int D, bool kBf16, bool kCausal, bool kDrop, bool kKv, bool kWin = false>
 __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32_t tmem_base) {
   using L = BwdSmem<D, DkdvVec<D>::kBytes>;
   using X = DkdvBars;
@@ -564,8 +666,13 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
 
   // Key tile kt of head bh; for causal runs the first key tiles of a group
   // of heads (the most query tiles to visit) are dealt first.
-  int kt, bh;
-  bwd_item(p, blk, p.n_ktiles, kt, bh);
+  int kt, bh;                                // kWin: bh is the key/value head
+  if constexpr (kWin) {
+    bh = blk / p.n_ktiles;
+    kt = blk - bh * p.n_ktiles;
+  } else {
+    bwd_item(p, blk, p.n_ktiles, kt, bh);
+  }
   int i0 = kCausal ? kt : 0;                 // query tiles i >= kt see this key tile
   int len = p.N, off = 0;                    // keys of this head, query offset (kKv)
   int n_q = p.n_tiles;                       // query tiles of this head
@@ -573,7 +680,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
   BwdHead hd{p.N, 0, p.N, 0, 0};
   if constexpr (kKv) {
     // the first query that sees key kt * 128 sits at row kt * 128 - off
-    hd = bwd_kv_head(p, bh, kCausal);
+    hd = bwd_kv_head(p, kWin ? bh / p.Hk * p.H : bh, kCausal);
     len = hd.len;
     off = hd.off;
     if (tok) n_q = (hd.lenq + kBwdTile - 1) / kBwdTile;
@@ -581,11 +688,18 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     i0 = !kCausal || first <= 0 ? 0 : first / kBwdTile;
     if (kt * kBwdTile >= len) i0 = n_q;      // padding: no query sees these keys
   }
+  if constexpr (kWin) n_q = bwd_win_q_end(kt, len, off, n_q, p.win, p.sinks);
   // key rows this CTA owns: padded keys are written (as zeros); a packed
   // sequence's rows end at its key count
   const int key_rows = tok ? len : p.Nk;
   const int q_rows = tok ? hd.lenq : p.N;
-  const int nq = n_q - i0;
+  const int nq1 = n_q - i0;                        // query tiles of one head
+  const int nq = kWin ? max(nq1, 0) * p.G : nq1;   // ... of every head that reads this one
+  // query tile and head of step it
+  auto q_tile = [&](int it) { return kWin ? i0 + it % nq1 : i0 + it; };
+  auto q_head = [&](int it) {
+    return kWin ? bh / p.Hk * p.H + bh % p.Hk * p.G + it / nq1 : bh;
+  };
   if (kKv && nq <= 0) {
     // no query sees this key tile: its dK and dV rows are zero
     if (threadIdx.x < kBwdEwThreads) {
@@ -611,9 +725,16 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
 
   if (warp == kBwdLoadWarp) {
-    if (lane == 0)
+    if constexpr (kWin) {
+      if (lane == 0)
+        bwd_producer_map<L>(
+            sbase, &p.tm_k, &p.tm_v, [&](int& y, int& z) { y = kt * kBwdTile; z = bh; }, &p.tm_q,
+            &p.tm_do, [&](int it, int& y, int& z) { y = q_tile(it) * kBwdTile; z = q_head(it); },
+            nq, wd);
+    } else if (lane == 0) {
       bwd_producer<L>(sbase, &p.tm_k, &p.tm_v, kt, &p.tm_q, &p.tm_do, i0, nq, bh, wd,
                       tok ? bh % p.H : -1, hd.k0, hd.q0, p.width_qk / 64, p.width_v / 64);
+    }
     __syncwarp();
   } else if (warp == kBwdMmaWarp) {
     if (lane == 0) {
@@ -709,16 +830,17 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     // staged, so the warps do not wait for them; a query past N then gets
     // -LSE = -inf, so its P is 0, and D = 0.
     bool in_next = false;
-    auto fetch = [&](int i, float& lse, float& dd) {
-      const int qrow = i * kBwdTile + t;
+    auto fetch = [&](int it, float& lse, float& dd) {
+      const int qrow = q_tile(it) * kBwdTile + t, qh = q_head(it);
       in_next = qrow < q_rows;
       const int qr = in_next ? qrow : 0;
-      const long long qi = bwd_lse_at(p, tok, hd, bh, qr);
+      const long long qi = bwd_lse_at(p, tok, hd, qh, qr);
       lse = p.lse[qi];
-      dd = p.delta[tok ? bwd_qrow(p, tok, hd, bh, qr) : qi];
+      dd = p.delta[tok ? bwd_qrow(p, tok, hd, qh, qr) : qi];
     };
     float lse_next = 0.f, d_next = 0.f;
-    if (half == 0) fetch(i0, lse_next, d_next);
+    if (half == 0) fetch(0, lse_next, d_next);
+    int win_lo = 0, win_hi = 64;   // kWin: this key's queries of the thread's 64, phases 1 to 2
     float pf[64];          // P^T of the current tile, from phase 1 to phase 2
     // dropout: keep bits of this key against the thread's 64 queries, from
     // the quad's words (zw[2 k2 + m]: word m of lane k2, blocks 8m + 4h + k2
@@ -740,14 +862,14 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       if (half == 0) {
         vec[t] = in_next ? -lse_next * 1.4426950408889634f : -INFINITY;   // -LSE, log2 units
         vec[128 + t] = in_next ? d_next : 0.f;
-        if (it + 1 < nq) fetch(i0 + it + 1, lse_next, d_next);
+        if (it + 1 < nq) fetch(it + 1, lse_next, d_next);
       }
       ptx::named_bar_sync(2, kBwdEwThreads);
     };
 
     // ---- phase 1: P^T = 2^(S^T c - LSE) over this thread's 64 queries
     auto phase1 = [&](int it) {
-      const int i = i0 + it;
+      const int i = q_tile(it);
       const float4* nl4 = reinterpret_cast<const float4*>(vec_of(it)) + half * 16;
       ptx::wait_bounded(xbar(X::kSFull), it & 1, wd, kSiteBwdSFull);
       __syncwarp();
@@ -771,7 +893,36 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
           pf[e + 3] = ptx::ex2(x3);
         }
       }
-      if constexpr (kKv) {
+      if constexpr (kWin) {
+        // queries q with key <= q + off < key + win (sinks: no upper bound);
+        // padding keys see none
+        const int qb = i * kBwdTile + half * 64;
+        win_lo = key >= len ? 64 : static_cast<int>(key) - off - qb;
+        win_hi = key < p.sinks ? 64 : static_cast<int>(key) + p.win - off - qb;
+        if (win_lo > 0 || win_hi < 64) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e < win_lo || e >= win_hi) pf[e] = 0.f;
+        }
+        // Rows at negative positions see no key, nor (without sinks) do rows
+        // whose window starts past the batch's keys.  Whatever their Q and dO
+        // hold, the weights 0 that they meet in dV and dK must give 0, so
+        // these rows are cleared once S^T and dP^T have read them.
+        const int pos0 = i * kBwdTile + off;
+        const int r_lo = min(max(-pos0, 0), kBwdTile);
+        const int r_hi = p.sinks > 0 ? kBwdTile : min(max(len + p.win - 1 - pos0, r_lo), kBwdTile);
+        if (r_lo > 0 || r_hi < kBwdTile) {
+          ptx::wait_bounded(xbar(X::kDpFull), it & 1, wd, kSiteBwdDpFull);
+          __syncwarp();
+          uint8_t* qt = sgen + L::kRingA + (it % L::kStagesA) * L::kTile;
+          uint8_t* dt = sgen + L::kRingB + (it % L::kStagesB) * L::kTile;
+          zero_rows(qt, L::kChunks, 0, r_lo, threadIdx.x, kBwdEwThreads);
+          zero_rows(qt, L::kChunks, r_hi, kBwdTile, threadIdx.x, kBwdEwThreads);
+          zero_rows(dt, L::kChunks, 0, r_lo, threadIdx.x, kBwdEwThreads);
+          zero_rows(dt, L::kChunks, r_hi, kBwdTile, threadIdx.x, kBwdEwThreads);
+          ptx::fence_proxy_async_smem();
+        }
+      } else if constexpr (kKv) {
         // padding keys see nothing; with causal masking query q sees this
         // key once q + off >= key
         const int qb = i * kBwdTile + half * 64;
@@ -855,6 +1006,17 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
           dk[f / 2 + 1] = ptx::pack2<kBf16>(d2, d3);
         }
       }
+      if constexpr (kWin) {
+        // a select, not a product with the masked P: dP - D of a key outside
+        // its batch's count need not be finite
+        if (win_lo > 0 || win_hi < 64) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (2 * e < win_lo || 2 * e >= win_hi) dk[e] &= 0xffff0000u;
+            if (2 * e + 1 < win_lo || 2 * e + 1 >= win_hi) dk[e] &= 0xffffu;
+          }
+        }
+      }
       ptx::tmem_st16(tDp, dk);           // over dP^T columns this warp has read
       ptx::tmem_st16(tDp + 16, dk + 16);
       ptx::tmem_wait_st();
@@ -890,7 +1052,7 @@ __device__ __forceinline__ uint32_t dq_ds_col(int b) {
 }
 
 // One CTA of the dQ pass: block `blk` of BH * n_tiles.
-template <int D, bool kBf16, bool kCausal, bool kDrop, bool kKv>
+template <int D, bool kBf16, bool kCausal, bool kDrop, bool kKv, bool kWin = false>
 __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t tmem_base) {
   using L = BwdSmem<D, 0>;
   using X = DqBars;
@@ -923,6 +1085,15 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
     const int last = min(qt * kBwdTile + kBwdTile, hd.lenq) - 1 + off;
     nk = !kCausal ? nkv : (last < 0 ? 0 : min(last / kBwdTile + 1, nkv));
   }
+  // kWin: of the key tiles 0 .. nk - 1 only the sink tiles and those from the
+  // first row's window on are walked
+  BwdWinKeys wk{};
+  if constexpr (kWin) {
+    wk = bwd_win_keys(qt * kBwdTile, min(qt * kBwdTile + kBwdTile, hd.lenq), len, off, nk, p.win,
+                      p.sinks);
+    nk = wk.count;
+  }
+  auto k_tile = [&](int j) { return kWin && j >= wk.ns ? wk.wa + (j - wk.ns) : j; };
   const int q_rows = tok ? hd.lenq : p.N;
   if (kKv && nk <= 0) {
     // no query of this tile sees a key: its dQ rows are zero
@@ -952,9 +1123,17 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
 
   if (warp == kBwdLoadWarp) {
-    if (lane == 0)
+    if constexpr (kWin) {
+      if (lane == 0) {
+        const int kvh = bh / p.H * p.Hk + bh % p.H / p.G;
+        bwd_producer_map<L>(
+            sbase, &p.tm_q, &p.tm_do, [&](int& y, int& z) { y = qt * kBwdTile; z = bh; }, &p.tm_k,
+            &p.tm_v, [&](int it, int& y, int& z) { y = k_tile(it) * kBwdTile; z = kvh; }, nk, wd);
+      }
+    } else if (lane == 0) {
       bwd_producer<L>(sbase, &p.tm_q, &p.tm_do, qt, &p.tm_k, &p.tm_v, 0, nk, bh, wd,
                       tok ? bh % p.H : -1, hd.q0, hd.k0, p.width_qk / 64, p.width_v / 64);
+    }
     __syncwarp();
   } else if (warp == kBwdMmaWarp) {
     if (lane == 0) {
@@ -1028,7 +1207,24 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
       // keys past N, and on the diagonal tile keys after this query, are
       // masked (limits relative to this thread's first key column)
       int lim = p.N - j * kBwdTile - half * 64;
-      if constexpr (kKv) {
+      int lo = 0;              // kWin: keys of the thread's 64 before the window, sinks aside
+      if constexpr (kWin) {
+        const int key0 = k_tile(j) * kBwdTile, pos = static_cast<int>(qrow) + off;
+        lim = min(len, pos + 1) - key0 - half * 64;
+        lo = pos - p.win + 1 - key0 - half * 64;
+        // Keys of this tile that no row sees get dS = 0; their rows of K are
+        // cleared so that the product with them is 0 whatever they hold (S
+        // and dP have read the tile).
+        const int r_hi = min(max(wk.hi - key0, 0), kBwdTile);
+        const int r_lo = min(max(wk.lo - key0, 0), r_hi);
+        const int r_sink = min(max(p.sinks - key0, 0), r_lo);
+        if (r_sink < r_lo || r_hi < kBwdTile) {
+          uint8_t* kt = sgen + L::kRingA + (j % L::kStagesA) * L::kTile;
+          zero_rows(kt, L::kChunks, r_sink, r_lo, threadIdx.x, kBwdEwThreads);
+          zero_rows(kt, L::kChunks, r_hi, kBwdTile, threadIdx.x, kBwdEwThreads);
+          ptx::fence_proxy_async_smem();
+        }
+      } else if constexpr (kKv) {
         // keys past this head's count, and with causal masking keys after
         // this query's position
         lim = len - j * kBwdTile - half * 64;
@@ -1069,8 +1265,10 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(__uint_as_float(sr[kc]), __uint_as_float(sr[kc + 1])),
                                   c2, nl2), x0, x1);
         float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-        if (kc >= lim) p0 = 0.f;
-        if (kc + 1 >= lim) p1 = 0.f;
+        if constexpr (!kWin) {
+          if (kc >= lim) p0 = 0.f;
+          if (kc + 1 >= lim) p1 = 0.f;
+        }
         float g0 = __uint_as_float(dpr[kc]), g1 = __uint_as_float(dpr[kc + 1]);
         uint64_t gd;
         if constexpr (kDrop) {   // Z dP 256 / t - D
@@ -1085,6 +1283,19 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         float d0, d1;
         ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(p0, p1), gd), d0, d1);
         dk[kc / 2] = ptx::pack2<kBf16>(d0, d1);
+      }
+      if constexpr (kWin) {
+        // masked keys by selection (dP of a key outside its batch's count
+        // need not be finite): past the position, or before the window and
+        // not a sink
+        const int sink = p.sinks - k_tile(j) * kBwdTile - half * 64;
+        if (lim < 64 || (lo > 0 && sink < 64)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (2 * e >= lim || (2 * e < lo && 2 * e >= sink)) dk[e] &= 0xffff0000u;
+            if (2 * e + 1 >= lim || (2 * e + 1 < lo && 2 * e + 1 >= sink)) dk[e] &= 0xffffu;
+          }
+        }
       }
       // dS to its TMEM buffer once the tensor core has read what it held
       // (dQ of key tile j - 2)
@@ -1119,7 +1330,7 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
 // and a CTA that stays resident across items skips the relaunch and the
 // TMEM allocation of every item after its first.  Shared memory is sized
 // for the larger layout.
-template <int D, bool kBf16, bool kCausal, bool kDrop = false, bool kKv = false>
+template <int D, bool kBf16, bool kCausal, bool kDrop = false, bool kKv = false, bool kWin = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
   __shared__ uint32_t s_tmem_base;
@@ -1132,13 +1343,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
-  const int per_pass = p.BH * p.n_ktiles;   // dK/dV items, one per key tile
+  const int per_pass = (kWin ? p.BHk : p.BH) * p.n_ktiles;   // dK/dV items, one per key tile
   const int total = per_pass + p.BH * p.n_tiles;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     if (item < per_pass)
-      bwd_dkdv_cta<D, kBf16, kCausal, kDrop, kKv>(p, item, tmem_base);
+      bwd_dkdv_cta<D, kBf16, kCausal, kDrop, kKv, kWin>(p, item, tmem_base);
     else
-      bwd_dq_cta<D, kBf16, kCausal, kDrop, kKv>(p, item - per_pass, tmem_base);
+      bwd_dq_cta<D, kBf16, kCausal, kDrop, kKv, kWin>(p, item - per_pass, tmem_base);
   }
   ptx::tc_fence_before();
   __syncthreads();

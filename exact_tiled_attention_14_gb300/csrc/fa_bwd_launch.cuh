@@ -70,7 +70,7 @@ cudaError_t launch_bwd_grid(Kernel kernel, const BwdParams& p, long long items, 
 
 // D = rowsum(dO * O), then one grid of dK/dV CTAs (one per key tile) and dQ
 // CTAs (one per query tile), all on `stream`.  `o`, `dout` are [BH, N, D] in the storage dtype.
-template <int D, bool kBf16, bool kCausal, bool kDrop = false, bool kKv = false>
+template <int D, bool kBf16, bool kCausal, bool kDrop = false, bool kKv = false, bool kWin = false>
 cudaError_t launch_bwd_variant(const BwdParams& p, const void* o, const void* dout, float* delta,
                                int sms, cudaStream_t stream) {
   cudaError_t e = launch_bwd_delta<kBf16>(p, o, dout, delta, sms, stream);
@@ -80,11 +80,12 @@ cudaError_t launch_bwd_variant(const BwdParams& p, const void* o, const void* do
   constexpr int kAllocKv = BwdSmem<D, DkdvVec<D>::kBytes>::kAlloc;
   constexpr int kAllocQ = BwdSmem<D, 0>::kAlloc;
   constexpr int kAlloc = kAllocKv > kAllocQ ? kAllocKv : kAllocQ;
-  e = bwd_smem_attr(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv>, done, kAlloc);
+  e = bwd_smem_attr(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv, kWin>, done, kAlloc);
   if (e != cudaSuccess) return e;
   // dK/dV items (one per key tile) then dQ items (one per query tile)
-  const long long items = static_cast<long long>(p.BH) * (p.n_ktiles + p.n_tiles);
-  return launch_bwd_grid(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv>, p, items, kAlloc, sms,
+  const long long items = static_cast<long long>(kWin ? p.BHk : p.BH) * p.n_ktiles +
+                          static_cast<long long>(p.BH) * p.n_tiles;
+  return launch_bwd_grid(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv, kWin>, p, items, kAlloc, sms,
                          stream);
 }
 
@@ -151,5 +152,9 @@ cudaError_t launch_bwd_kv_d64(const BwdParams& p, const void* o, const void* dou
                               bool bf16, bool causal, int sms, cudaStream_t stream);
 cudaError_t launch_bwd_kv_d128(const BwdParams& p, const void* o, const void* dout, float* delta,
                                bool bf16, bool causal, int sms, cudaStream_t stream);
+// Sliding-window calls with sinks and shared key/value heads (the kKv,
+// kCausal, kWin variants).
+cudaError_t launch_bwd_win(const BwdParams& p, const void* o, const void* dout, float* delta, int d,
+                           bool bf16, int sms, cudaStream_t stream);
 
 }  // namespace fa

@@ -136,14 +136,14 @@ const DeviceInfo* device_info(int* dev_out) {
   return &g_dev[dev];
 }
 
-bool make_tmap(CUtensorMap* m, const void* ptr, int BH, int N, int d, bool bf16) {
+bool make_tmap(CUtensorMap* m, const void* ptr, int BH, int N, int d, bool bf16, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N),
                               static_cast<cuuint64_t>(BH)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                                  static_cast<cuuint64_t>(N) * static_cast<cuuint64_t>(d) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(fa::kBM), 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t elem_strides[3] = {1, 1, 1};
   const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                         3, const_cast<void*>(ptr), dims, strides, box, elem_strides,
@@ -179,7 +179,7 @@ int drop_threshold(float p) {
 
 extern "C" {
 
-int fa_version(void) { return 104; }
+int fa_version(void) { return 105; }
 
 const char* fa_strerror(int code) {
   switch (code) {
@@ -195,7 +195,7 @@ const char* fa_strerror(int code) {
     case FA_ERR_LAUNCH: return "kernel launch failed";
     case FA_ERR_TIMEOUT: return "a bounded wait in a kernel ran out (watchdog)";
     case FA_ERR_CUDA: return "CUDA runtime error";
-    case FA_ERR_WORKSPACE: return "workspace smaller than fa_fwd_workspace_size reports";
+    case FA_ERR_WORKSPACE: return "workspace missing or smaller than the workspace_size function reports";
     case FA_ERR_DROPOUT: return "dropout probability must be in [0, 1) and keep at least 1/256";
     default: return "unknown error code";
   }

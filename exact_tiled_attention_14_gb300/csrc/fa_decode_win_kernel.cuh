@@ -1,0 +1,863 @@
+// fa_decode_win_kernel.cuh — a few new queries per sequence against its
+// key/value cache, on the tensor cores: the last tokens of a sequence under
+// a sliding window with sinks, or the tokens of a drafted tree.
+//
+// For one (batch, key/value head) the G query heads that share the head and
+// their Nq tokens are R = G * Nq rows of one problem, O = softmax(Q K^T) V
+// with a mask per row, and every key and value of the span that some row
+// sees is read once for all of them.  The cache is what the call reads:
+// 4 * d bytes a key against 4 * d * R operations, so up to a few hundred
+// rows HBM bounds it.  A tile of 128 keys is 64 KB at d = 128 and takes an
+// SM 1.5 us at its share of 6.8 TB/s; the products of 128 rows with it take
+// 0.3 us and their softmax about 0.5 us, so rows are simply padded to the
+// 128 lanes of TMEM and the tile's work hides behind the next tile's load.
+//
+// Split.  The key tiles of all units (a unit: batch, key/value head, block
+// of 128 * kTiles rows) are laid end to end and cut into equal runs, one
+// per CTA, so every SM reads the same amount whatever the sequences'
+// lengths, which only the device knows.  A unit that lies in one run is
+// finished there; of a cut unit each CTA writes the unnormalised output and
+// the softmax statistics of its part, and a second kernel adds the parts up
+// by the rescale identity ("FlashAttention: The Matrix You Never Have to
+// Write Down", section "What it doesn't solve", on splitting the key axis
+// and combining partial results) in the order of the runs: no atomics.
+//
+// Keys.  A unit's keys are the sinks before the window, padded to whole
+// boxes of 16, and then the span lo .. hi - 1: tile 0 usually holds both, so
+// a few sinks cost one box, not a tile.  Only boxes that hold a needed key
+// are loaded.
+//
+// One CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8
+// issues S = Q K^T, warp 9 the TMA loads, warp 10 O += P V.  With up to 128
+// rows (kTiles = 1) the groups take alternate key tiles, each with its own
+// S, P, O and statistics, and are merged at the end of the unit; with more
+// (kTiles = 2) each group owns a row tile and both take every key tile.
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "ptx_sm103.cuh"
+
+namespace fa {
+
+constexpr int kDwThreads = 384;
+constexpr int kDwTile = 128;          // keys per tile, rows per row tile
+constexpr int kDwBox = 16;            // rows of the small load box
+constexpr int kDwSWarp = 8, kDwLoadWarp = 9, kDwPvWarp = 10;
+constexpr uint32_t kDwSoftmaxRegs = 208, kDwIssueRegs = 88;
+static_assert(2 * 128 * kDwSoftmaxRegs + 128 * kDwIssueRegs <= 168 * kDwThreads, "register split");
+constexpr float kDwTau = 8.0f;        // lazy-rescale threshold, log2 units
+constexpr int kDwMaxTree = 64;        // drafted tokens (bits of a row's mask)
+constexpr int kDwMaxTokens = 16;      // new tokens of a window call
+
+enum DwWaitSite : uint32_t {
+  kSiteDwQEmpty = 40, kSiteDwKvEmpty = 41, kSiteDwQFull = 42, kSiteDwKvFull = 43,
+  kSiteDwPFull = 44, kSiteDwOFree = 45, kSiteDwSFull = 46, kSiteDwSFree = 47, kSiteDwPvDone = 48
+};
+
+struct DecWinParams {
+  CUtensorMap tm_q;        // [B * Hk, R, d], boxes of 128 rows x 64 columns, 128-byte swizzle
+  CUtensorMap tm_k;        // [B * Hk, Nk, d], the same boxes
+  CUtensorMap tm_v;
+  CUtensorMap tm_k16;      // the same tensors in boxes of 16 rows
+  CUtensorMap tm_v16;
+  void* o;                 // [B * Hk, R, d]
+  float* lse;              // [B * Hk, R]
+  float* part_o;           // [2 * grid, slot_rows, d] unnormalised parts
+  float2* part_ml;         // [2 * grid, slot_rows] (-m in log2 units, l)
+  unsigned int* status;
+  unsigned long long watchdog_cycles;
+  const int* seqlens;      // [B] or NULL: every count is len_all
+  const unsigned long long* tree;   // [B, Nq] visible drafted tokens, NULL for a window call
+  int len_all;
+  int B, Hk, Nq, Nk;
+  int R;                   // rows of a unit's head: G * Nq, row g * Nq + i
+  int row_span;            // rows of a unit: 128 * kTiles
+  int row_blocks;          // units per head: ceil(R / row_span)
+  int slot_rows;
+  int grid;
+  int win;                 // >= 1; larger than every position: no window
+  int sinks;
+  float scale_log2;
+};
+
+// Keys of batch b: count len (window: keys with the new tokens, tree:
+// history), the span lo .. hi - 1, the sinks before it and the rows they
+// take in the list (whole boxes).
+struct DecSpan {
+  int len, lo, hi, sink, sink_rows;
+};
+__host__ __device__ __forceinline__ DecSpan dec_span(int count, int Nk, int Nq, int win, int sinks,
+                                                     bool tree) {
+  DecSpan s;
+  s.len = count < 0 ? 0 : (count > Nk ? Nk : count);
+  if (tree) {
+    s.hi = s.len + Nq < Nk ? s.len + Nq : Nk;
+    s.lo = s.len - win;              // a row that marks no drafted token sits at len - 1
+  } else {
+    s.hi = s.len;
+    s.lo = s.len - Nq - win + 1;     // the first token's window
+  }
+  if (s.lo < 0) s.lo = 0;
+  s.sink = sinks < s.lo ? sinks : s.lo;
+  s.sink_rows = (s.sink + kDwBox - 1) / kDwBox * kDwBox;
+  return s;
+}
+// Key tiles of a unit: at least one, so that every unit has a writer.
+__host__ __device__ __forceinline__ int dec_tiles(const DecSpan& s) {
+  const int rows = s.sink_rows + (s.hi - s.lo);
+  return rows <= kDwTile ? 1 : (rows + kDwTile - 1) / kDwTile;
+}
+// Tile t of the list: ns rows of sinks from key sink0 on, then the span from
+// key key0 on, nw of whose rows are keys.
+struct DecTile {
+  int ns, sink0, key0, nw;
+};
+__host__ __device__ __forceinline__ DecTile dec_tile(const DecSpan& s, int t) {
+  DecTile d;
+  d.sink0 = t * kDwTile;
+  const int left = s.sink_rows - d.sink0;
+  d.ns = left < 0 ? 0 : (left > kDwTile ? kDwTile : left);
+  d.key0 = s.lo + d.sink0 + d.ns - s.sink_rows;
+  const int nw = s.hi - d.key0;
+  d.nw = nw < 0 ? 0 : (nw > kDwTile - d.ns ? kDwTile - d.ns : nw);
+  return d;
+}
+
+__device__ __forceinline__ DecSpan dec_span_of(const DecWinParams& p, int b) {
+  return dec_span(p.seqlens ? p.seqlens[b] : p.len_all, p.Nk, p.Nq, p.win, p.sinks,
+                  p.tree != nullptr);
+}
+
+// Sum of the key tiles of batches [0, n) and of all batches, by one warp.
+__device__ __forceinline__ void dec_tile_sums(const DecWinParams& p, int n, long long& before,
+                                              long long& total) {
+  const long long units = static_cast<long long>(p.Hk) * p.row_blocks;
+  long long bsum = 0, tsum = 0;
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+    const long long t = dec_tiles(dec_span_of(p, b)) * units;
+    tsum += t;
+    if (b < n) bsum += t;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    tsum += __shfl_xor_sync(0xffffffffu, tsum, off);
+    bsum += __shfl_xor_sync(0xffffffffu, bsum, off);
+  }
+  before = bsum;
+  total = tsum;
+}
+__host__ __device__ __forceinline__ long long dec_run_start(long long total, int cta, int grid) {
+  return total / grid * cta + total % grid * cta / grid;
+}
+
+// A CTA's place in its run: batch, unit within the batch, tile within the
+// unit, tiles left.
+struct DecCursor {
+  int b, unit, tile;
+  long long left;
+  int n_done;          // pieces taken so far
+};
+struct DecPiece {
+  int b, unit, t0, n;  // tiles t0 .. t0 + n - 1 of the unit
+  bool whole;
+  int slot;            // where a part goes: 0 the run's first piece, 1 its last
+  DecSpan s;
+};
+__device__ __forceinline__ bool dec_next(const DecWinParams& p, DecCursor& c, DecPiece& pc) {
+  if (c.left <= 0) return false;
+  pc.b = c.b;
+  pc.unit = c.unit;
+  pc.t0 = c.tile;
+  pc.s = dec_span_of(p, c.b);
+  const int nt = dec_tiles(pc.s);
+  const long long n = nt - c.tile < c.left ? nt - c.tile : c.left;
+  pc.n = static_cast<int>(n);
+  pc.whole = c.tile == 0 && pc.n == nt;
+  pc.slot = c.n_done == 0 ? 0 : 1;
+  c.left -= n;
+  ++c.n_done;
+  c.tile = 0;
+  if (++c.unit == p.Hk * p.row_blocks) {
+    c.unit = 0;
+    ++c.b;
+  }
+  return true;
+}
+
+// Shared memory: kTiles query tiles, a ring of K and V tiles, two P tiles.
+template <int D, int kTiles>
+struct DwLayout {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTile = kDwTile * D * 2;
+  static constexpr int kChunkBytes = kDwTile * 128;
+  static constexpr int kPTile = kDwTile * kDwTile * 2;
+  static constexpr int kStages = (D == 128) ? (kTiles == 2 ? 3 : 4) : 8;
+  static constexpr int kQ = 0;
+  static constexpr int kKV = kQ + kTiles * kTile;
+  static constexpr int kP = kKV + kStages * kTile;
+  static constexpr int kBar = kP + 2 * kPTile;
+  static constexpr int bQFull = 0, bQEmpty = 1, bKvFull = 2, bKvEmpty = bKvFull + kStages,
+                       bSFull = bKvEmpty + kStages, bSFree = bSFull + 2, bPFull = bSFree + 2,
+                       bPvDone = bPFull + 2, bOFree = bPvDone + 2, bFinalS = bOFree + 2,
+                       bFinalPv = bFinalS + 1, kNumBars = bFinalPv + 1;
+  static constexpr int kMisc = kBar + 8 * kNumBars;           // tmem base, abort flag, cursor
+  static constexpr int kBytes = kMisc + 48;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 232448, "shared memory budget");
+};
+
+// Bits [a, b) of 128 as four words.
+__host__ __device__ __forceinline__ void or_range(uint32_t* w, int a, int b) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int lo = a - 32 * k, hi = b - 32 * k;
+    lo = lo < 0 ? 0 : (lo > 32 ? 32 : lo);
+    hi = hi < 0 ? 0 : (hi > 32 ? 32 : hi);
+    const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+    const uint32_t below_lo = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
+    w[k] |= below_hi & ~below_lo;
+  }
+}
+// 64 bits m at bit position at (-63 .. 127) of 128, cut to [0, 128).
+__host__ __device__ __forceinline__ void or_bits(uint32_t* w, unsigned long long m, int at) {
+  unsigned long long lo = 0, hi = 0;
+  if (at <= -64 || at >= kDwTile) return;
+  if (at < 0) {
+    lo = m >> -at;
+  } else if (at == 0) {
+    lo = m;
+  } else if (at < 64) {
+    lo = m << at;
+    hi = m >> (64 - at);
+  } else {
+    hi = m << (at - 64);
+  }
+  w[0] |= static_cast<uint32_t>(lo);
+  w[1] |= static_cast<uint32_t>(lo >> 32);
+  w[2] |= static_cast<uint32_t>(hi);
+  w[3] |= static_cast<uint32_t>(hi >> 32);
+}
+
+// What one row sees: its position and, of a tree, the drafted tokens.
+struct DecRow {
+  int pos;
+  unsigned long long bits;
+};
+__host__ __device__ __forceinline__ int dec_popc(unsigned long long x) {
+#ifdef __CUDA_ARCH__
+  return __popcll(x);
+#else
+  return __builtin_popcountll(x);
+#endif
+}
+// Token i of a batch with count len (rows: its tree, NULL for a window call).
+__host__ __device__ __forceinline__ DecRow dec_row(const unsigned long long* rows, int i, int Nq,
+                                                   int len, int win, int sinks) {
+  DecRow r;
+  r.bits = 0;
+  if (rows == nullptr) {
+    r.pos = len - Nq + i;
+    return r;
+  }
+  const unsigned long long used = Nq == 64 ? ~0ull : (1ull << Nq) - 1ull;   // later bits: nothing
+  r.bits = rows[i] & used;
+  r.pos = len + dec_popc(r.bits) - 1;
+  if (win < kDwMaxTree) {
+    // drop drafted tokens that lie before the row's window and are no sinks
+    unsigned long long in = 0;
+    for (int j = 0; j < Nq; ++j) {
+      const int pj = len + dec_popc(rows[j] & used) - 1;
+      if (pj > r.pos - win || pj < sinks) in |= 1ull << j;
+    }
+    r.bits &= in;
+  }
+  return r;
+}
+// Visible columns of tile tl for a row, as 128 bits; true when all are.
+// seen: keys of the span part up to the row's position (tree: its history).
+__host__ __device__ __forceinline__ bool dec_visible(const DecSpan& s, const DecTile& tl,
+                                                     const DecRow& r, bool tree, int win, int sinks,
+                                                     uint32_t* vis) {
+  const int upto = (tree ? s.len : r.pos + 1) - tl.key0;
+  const int seen = tl.nw < upto ? tl.nw : upto;
+  const int first = r.pos - win + 1 - tl.key0;
+  if (tl.ns == 0 && seen == kDwTile && first <= 0) return true;
+  vis[0] = vis[1] = vis[2] = vis[3] = 0u;
+  const int ns = s.sink - tl.sink0 < tl.ns ? s.sink - tl.sink0 : tl.ns;
+  or_range(vis, 0, ns);                                           // the sinks before the span
+  or_range(vis, tl.ns + (first > 0 ? first : 0), tl.ns + seen);   // the row's window
+  or_range(vis, tl.ns, tl.ns + (sinks - tl.key0 < seen ? sinks - tl.key0 : seen));
+  if (tree) {
+    // drafted token 0 sits at column ns + len - key0
+    uint32_t dv[4] = {0u, 0u, 0u, 0u}, in[4] = {0u, 0u, 0u, 0u};
+    const int at = tl.ns + s.len - tl.key0;
+    or_bits(dv, r.bits, at);
+    or_range(in, tl.ns, tl.ns + tl.nw);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) vis[k] |= dv[k] & in[k];
+  }
+  return false;
+}
+
+template <int D, bool kBf16, int kTiles>
+__global__ void __launch_bounds__(kDwThreads, 1)
+    fa_decode_win_kernel(const __grid_constant__ DecWinParams p) {
+  using L = DwLayout<D, kTiles>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = ptx::smem_u32(smem_raw);
+  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - raw_base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
+  uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
+  int* cursor_s = reinterpret_cast<int*>(sgen + L::kMisc + 8);                 // batch, unit, tile
+  long long* left_s = reinterpret_cast<long long*>(sgen + L::kMisc + 24);
+
+  // the combine kernel may be scheduled once every CTA has started (it waits
+  // for this grid to complete before reading the parts)
+  ptx::griddep_launch_dependents();
+  if (warp == kDwSWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_base_ptr), 512);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == kDwLoadWarp * 32) {
+    *abort_flag = 0;
+    ptx::mbar_init(bar(L::bQFull), 1);
+    ptx::mbar_init(bar(L::bQEmpty), 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      ptx::mbar_init(bar(L::bKvFull + s), 1);
+      ptx::mbar_init(bar(L::bKvEmpty + s), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      ptx::mbar_init(bar(L::bSFull + w), 1);
+      ptx::mbar_init(bar(L::bSFree + w), 128);
+      ptx::mbar_init(bar(L::bPFull + w), 128);
+      ptx::mbar_init(bar(L::bPvDone + w), 1);
+      ptx::mbar_init(bar(L::bOFree + w), kTiles == 1 ? 256 : 128);
+    }
+    ptx::mbar_init(bar(L::bFinalS), 1);
+    ptx::mbar_init(bar(L::bFinalPv), 1);
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+    ptx::prefetch_tmap(&p.tm_q);
+    ptx::prefetch_tmap(&p.tm_k);
+    ptx::prefetch_tmap(&p.tm_v);
+    ptx::prefetch_tmap(&p.tm_k16);
+    ptx::prefetch_tmap(&p.tm_v16);
+  }
+  if (warp == kDwPvWarp) {
+    // this CTA's run and the batch, unit and tile that it starts in
+    long long before, total;
+    dec_tile_sums(p, 0, before, total);
+    const long long start = dec_run_start(total, blockIdx.x, p.grid);
+    const long long end = dec_run_start(total, blockIdx.x + 1, p.grid);
+    const int units = p.Hk * p.row_blocks;
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int nt = b < p.B ? dec_tiles(dec_span_of(p, b)) : 0;
+      const long long mine = static_cast<long long>(nt) * units;
+      long long incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
+      }
+      const long long first = base + incl - mine;
+      if (mine > 0 && first <= start && start < first + mine) {
+        cursor_s[0] = b;
+        cursor_s[1] = static_cast<int>((start - first) / nt);
+        cursor_s[2] = static_cast<int>((start - first) % nt);
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+      if (base > start) break;
+    }
+    if (lane == 0) *left_s = end - start;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_base_ptr;
+  const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
+  DecCursor cu{cursor_s[0], cursor_s[1], cursor_s[2], *left_s, 0};
+  DecPiece pc;
+  // rows of row tile w of a piece (kTiles == 1: both groups share tile 0)
+  auto rows_of = [&](const DecPiece& x, int w) {
+    const int first = (kTiles * (x.unit % p.row_blocks) + (kTiles == 2 ? w : 0)) * kDwTile;
+    return min(max(p.R - first, 0), kDwTile);
+  };
+  // whether group w computes tile j of the piece
+  auto takes = [&](const DecPiece& x, int w, int j) {
+    return kTiles == 1 ? (j & 1) == w : rows_of(x, w) > 0;
+  };
+  const uint32_t tS0 = tmem_base, tO0 = tmem_base + 256;
+
+  if (warp >= 8) {
+    ptx::setmaxnreg_dec<kDwIssueRegs>();
+    if (warp == kDwLoadWarp) {
+      // ============================================================ TMA producer
+      if (lane == 0) {
+        uint32_t loads = 0, pieces = 0;
+        bool alive = true;
+        while (alive && dec_next(p, cu, pc)) {
+          const int head = pc.b * p.Hk + pc.unit / p.row_blocks;
+          auto load_kv = [&](bool v, int j) {
+            const uint32_t slot = loads % L::kStages, use = loads / L::kStages;
+            if (use > 0)
+              alive = alive && ptx::wait_bounded(bar(L::bKvEmpty + slot), (use - 1) & 1, wd,
+                                                 kSiteDwKvEmpty);
+            if (!alive) return;
+            const DecTile t = dec_tile(pc.s, pc.t0 + j);
+            const uint32_t dst = sbase + L::kKV + slot * L::kTile, full = bar(L::bKvFull + slot);
+            if (t.nw > kDwTile - kDwBox) {   // no sinks in it: one box of 128 rows
+              ptx::mbar_arrive_expect_tx(full, L::kTile);
+              for (int c = 0; c < L::kChunks; ++c)
+                ptx::tma_load_3d(dst + c * L::kChunkBytes, v ? &p.tm_v : &p.tm_k, full, c * 64,
+                                 t.key0, head);
+            } else {
+              // boxes of 16 rows; a tile without keys still loads one box,
+              // whose rows are masked
+              const int bs = t.ns / kDwBox;
+              const int bw = max((t.nw + kDwBox - 1) / kDwBox, bs == 0 ? 1 : 0);
+              const CUtensorMap* tm = v ? &p.tm_v16 : &p.tm_k16;
+              ptx::mbar_arrive_expect_tx(full, (bs + bw) * kDwBox * 128 * L::kChunks);
+              for (int c = 0; c < L::kChunks; ++c) {
+                for (int i = 0; i < bs; ++i)
+                  ptx::tma_load_3d(dst + c * L::kChunkBytes + i * kDwBox * 128, tm, full, c * 64,
+                                   t.sink0 + i * kDwBox, head);
+                for (int i = 0; i < bw; ++i)
+                  ptx::tma_load_3d(dst + c * L::kChunkBytes + (bs + i) * kDwBox * 128, tm, full,
+                                   c * 64, t.key0 + i * kDwBox, head);
+              }
+            }
+            ++loads;
+          };
+          load_kv(false, 0);
+          if (pieces > 0)
+            alive = alive && ptx::wait_bounded(bar(L::bQEmpty), (pieces - 1) & 1, wd, kSiteDwQEmpty);
+          if (!alive) break;
+          {
+            const int nq = kTiles == 2 && rows_of(pc, 1) > 0 ? 2 : 1;
+            const int row0 = kTiles * (pc.unit % p.row_blocks) * kDwTile;
+            ptx::mbar_arrive_expect_tx(bar(L::bQFull), nq * L::kTile);
+            for (int w = 0; w < nq; ++w)
+              for (int c = 0; c < L::kChunks; ++c)
+                ptx::tma_load_3d(sbase + L::kQ + w * L::kTile + c * L::kChunkBytes, &p.tm_q,
+                                 bar(L::bQFull), c * 64, row0 + w * kDwTile, head);
+            ++pieces;
+          }
+          for (int j = 0; alive && j < pc.n; ++j) {
+            if (j + 1 < pc.n) load_kv(false, j + 1);
+            load_kv(true, j);
+          }
+        }
+        // Drain: every issued copy has landed before the CTA can exit.
+        const unsigned long long drain = 200000000ull;
+        for (uint32_t l = loads > (uint32_t)L::kStages ? loads - L::kStages : 0; l < loads; ++l)
+          ptx::wait_drain(bar(L::bKvFull + l % L::kStages), (l / L::kStages) & 1, drain);
+        if (pieces > 0) ptx::wait_drain(bar(L::bQFull), (pieces - 1) & 1, drain);
+      }
+      __syncwarp();
+    } else if (warp == kDwSWarp) {
+      // ============================================================ S = Q K^T
+      if (lane == 0) {
+        constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, kDwTile, kBf16 ? 1 : 0, 0);
+        const uint32_t q_lo = ptx::desc_lo(sbase + L::kQ, 16);
+        const uint32_t k_lo = ptx::desc_lo(sbase + L::kKV, 16);
+        uint32_t base = 0, pieces = 0, sc[2] = {0, 0};
+        bool alive = true, issued = false;
+        while (dec_next(p, cu, pc)) {
+          alive = alive && ptx::wait_bounded(bar(L::bQFull), pieces & 1, wd, kSiteDwQFull);
+          for (int j = 0; j < pc.n; ++j) {
+            const uint32_t pos = base + (j == 0 ? 0u : 2u * j - 1u), slot = pos % L::kStages;
+            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), (pos / L::kStages) & 1, wd,
+                                               kSiteDwKvFull);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (!takes(pc, w, j)) continue;
+              if (sc[w] > 0)   // the softmax has read the previous S of this group
+                alive = alive && ptx::wait_bounded(bar(L::bSFree + w), (sc[w] - 1) & 1, wd,
+                                                   kSiteDwSFree);
+              ++sc[w];
+              ptx::tc_fence_after();
+              if (!alive) continue;
+              const uint32_t a = q_lo + (kTiles == 2 ? w : 0) * (L::kTile >> 4);
+              const uint32_t b = k_lo + slot * (L::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off =
+                    static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+                ptx::mma_ss(tS0 + w * 128, ptx::desc_sw128(a + off), ptx::desc_sw128(b + off), idesc,
+                            kk > 0);
+              }
+              ptx::mma_commit(bar(L::bSFull + w));
+              issued = true;
+            }
+            if (alive) {
+              ptx::mma_commit(bar(L::bKvEmpty + slot));
+              if (j + 1 == pc.n) ptx::mma_commit(bar(L::bQEmpty));
+            }
+          }
+          base += 2u * pc.n;
+          ++pieces;
+        }
+        if (issued) {
+          ptx::mma_commit(bar(L::bFinalS));
+          ptx::wait_drain(bar(L::bFinalS), 0, 200000000ull);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kDwPvWarp) {
+      // ============================================================ O += P V
+      // The whole warp walks the tiles.  Rows of V that are no key some row
+      // sees (box padding, past the keys, drafted slots that no row marks)
+      // meet weights 0, but 0 times a value that is not finite is not 0, so
+      // they are overwritten with zeros.  Lane 0 alone waits on barriers and
+      // the warp joins it afterwards: a lane that polled on its own could miss
+      // a phase that lane 0's progress lets pass twice.
+      constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, D, kBf16 ? 1 : 0, 1);
+      const uint32_t p_lo = ptx::desc_lo(sbase + L::kP, 16);
+      const uint32_t v_lo = ptx::desc_lo(sbase + L::kKV, L::kChunkBytes);
+      uint32_t base = 0, pcn[2] = {0, 0}, units[2] = {0, 0};
+      bool alive = true, issued = false;
+      while (dec_next(p, cu, pc)) {
+        int done[2] = {0, 0};
+        // a tree's keys below `from` are before the window of its shallowest
+        // token; `holes` are the drafted tokens that no row marks
+        int from = 0;
+        unsigned long long holes = 0;
+        if (p.tree) {
+          const unsigned long long* rows = p.tree + static_cast<size_t>(pc.b) * p.Nq;
+          const unsigned long long used = p.Nq == 64 ? ~0ull : (1ull << p.Nq) - 1ull;
+          const unsigned long long r0 = lane < p.Nq ? rows[lane] & used : 0ull;
+          const unsigned long long r1 = lane + 32 < p.Nq ? rows[lane + 32] & used : 0ull;
+          const int depth = min(lane < p.Nq ? dec_popc(r0) : 64, lane + 32 < p.Nq ? dec_popc(r1) : 64);
+          from = pc.s.len + __reduce_min_sync(0xffffffffu, depth) - p.win;
+          const unsigned long long any = r0 | r1;
+          const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+          const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
+          holes = used & ~((static_cast<unsigned long long>(hi) << 32) | lo);
+        }
+        for (int j = 0; j < pc.n; ++j) {
+          const uint32_t pos = base + (j + 1 < pc.n ? 2u * j + 2u : 2u * pc.n - 1u);
+          const uint32_t slot = pos % L::kStages;
+          if (lane == 0)
+            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), (pos / L::kStages) & 1, wd,
+                                               kSiteDwKvFull);
+          __syncwarp();
+          const DecTile t = dec_tile(pc.s, pc.t0 + j);
+          const int s_end = min(max(pc.s.sink - t.sink0, 0), t.ns);   // sinks end in the tile
+          // span rows [lead0, lead1) before every window, and drafted slots
+          const int lead1 = min(min(from, pc.s.len) - t.key0, t.nw);
+          const int lead0 = max(p.sinks - t.key0, 0);
+          const bool drafted = holes != 0 && t.key0 + t.nw > pc.s.len;
+          if (s_end < t.ns || t.ns + t.nw < kDwTile || lead0 < lead1 || drafted) {
+            auto clear = [&](int r0, int r1) {
+              for (int c = 0; c < L::kChunks; ++c) {
+                uint4* rows = reinterpret_cast<uint4*>(sgen + L::kKV + slot * L::kTile +
+                                                       c * L::kChunkBytes);
+                for (int i = r0 * 8 + lane; i < r1 * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+              }
+            };
+            clear(s_end, t.ns);
+            clear(t.ns + t.nw, kDwTile);
+            clear(t.ns + lead0, t.ns + lead1);
+            if (drafted)
+              for (int i = max(pc.s.len - t.key0, 0); i < t.nw; ++i)
+                if (holes >> (t.key0 + i - pc.s.len) & 1) clear(t.ns + i, t.ns + i + 1);
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!takes(pc, w, j)) continue;
+            const bool first = done[w]++ == 0;
+            if (lane != 0) continue;
+            if (first && units[w] > 0)   // the previous unit's O has been read
+              alive = alive && ptx::wait_bounded(bar(L::bOFree + w), (units[w] - 1) & 1, wd,
+                                                 kSiteDwOFree);
+            alive = alive && ptx::wait_bounded(bar(L::bPFull + w), pcn[w] & 1, wd, kSiteDwPFull);
+            ++pcn[w];
+            ptx::tc_fence_after();
+            if (alive) {
+#pragma unroll
+              for (int kk = 0; kk < kDwTile / 16; ++kk) {
+                const uint32_t off =
+                    static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+                ptx::mma_ss(tO0 + w * D, ptx::desc_sw128(p_lo + w * (L::kPTile >> 4) + off),
+                            ptx::desc_sw128(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4)),
+                            idesc, (kk > 0 || !first) ? 1u : 0u);
+              }
+              ptx::mma_commit(bar(L::bPvDone + w));
+              issued = true;
+            }
+          }
+          if (alive && lane == 0) ptx::mma_commit(bar(L::bKvEmpty + slot));
+        }
+        // kTiles == 1: both groups read both outputs, and arrive for a group
+        // that had no tile too
+        units[0] += kTiles == 1 || done[0] > 0;
+        units[1] += kTiles == 1 || done[1] > 0;
+        base += 2u * pc.n;
+      }
+      if (issued) {   // lane 0 only
+        ptx::mma_commit(bar(L::bFinalPv));
+        ptx::wait_drain(bar(L::bFinalPv), 0, 200000000ull);
+      }
+      __syncwarp();
+    }
+  } else {
+    ptx::setmaxnreg_inc<kDwSoftmaxRegs>();
+    // ============================================================ softmax
+    const int w = warp >> 2, t = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tS0 + lane_off + w * 128;
+    const float c = p.scale_log2;
+    // statistics of group g's rows at the end of a piece, in its idle P tile
+    auto ml_s = [&](int g) { return reinterpret_cast<float2*>(sgen + L::kP + g * L::kPTile); };
+    uint32_t scnt = 0, pvcnt = 0;
+    while (dec_next(p, cu, pc)) {
+      const int nrows = rows_of(pc, w);
+      if (kTiles == 2 && nrows == 0) continue;
+      const bool has = (warp & 3) * 32 < nrows;     // this warp holds rows
+      const int row = (kTiles * (pc.unit % p.row_blocks) + (kTiles == 2 ? w : 0)) * kDwTile + t;
+      const DecRow me =
+          dec_row(p.tree ? p.tree + static_cast<size_t>(pc.b) * p.Nq : nullptr,
+                  min(row, p.R - 1) % p.Nq, p.Nq, pc.s.len, p.win, p.sinks);
+      float m_ref = -INFINITY, neg_m = 0.f, l = 0.f;
+      int it = 0;                                   // tiles of this group so far
+      for (int j = 0; j < pc.n; ++j) {
+        if (!takes(pc, w, j)) continue;
+        ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
+        ++scnt;
+        __syncwarp();
+        ptx::tc_fence_after();
+        float sv[kDwTile];
+        if (has) {
+          uint32_t sr[kDwTile];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld32(tS + q4 * 32, sr + q4 * 32);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kDwTile; ++e) sv[e] = __uint_as_float(sr[e]);
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
+        bool rescale = false;
+        float alpha = 1.f;
+        uint32_t pk[kDwTile / 2];
+        if (has) {
+          uint32_t vis[4];
+          if (!dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), me, p.tree != nullptr, p.win, p.sinks,
+                           vis)) {
+#pragma unroll
+            for (int e = 0; e < kDwTile; ++e)
+              if (!((vis[e >> 5] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
+          }
+          float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kDwTile; e += 8) {
+            a0 = ptx::max3(a0, sv[e + 0], sv[e + 1]);
+            a1 = ptx::max3(a1, sv[e + 2], sv[e + 3]);
+            a2 = ptx::max3(a2, sv[e + 4], sv[e + 5]);
+            a3 = ptx::max3(a3, sv[e + 6], sv[e + 7]);
+          }
+          const float mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+          // lazy rescale, as in the prompt kernel: the reference moves only
+          // when a tile exceeds it by 2^kDwTau
+          const bool grow = (mx - m_ref) * c > kDwTau;
+          if (grow) {
+            const float nm = -mx * c;
+            alpha = (m_ref == -INFINITY) ? 0.f : ptx::ex2(nm - neg_m);
+            l *= alpha;
+            m_ref = mx;
+            neg_m = nm;
+          }
+          rescale = it > 0 && __any_sync(0xffffffffu, grow);
+          const uint64_t c2 = ptx::f2_pack(c, c), nm2 = ptx::f2_pack(neg_m, neg_m);
+          uint64_t acc0 = ptx::f2_pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+          for (int e = 0; e < kDwTile / 2; e += 2) {
+            float x0, x1, x2, x3;
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(sv[2 * e + 0], sv[2 * e + 1]), c2, nm2), x0, x1);
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(sv[2 * e + 2], sv[2 * e + 3]), c2, nm2), x2, x3);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1), p2 = ptx::ex2(x2), p3 = ptx::ex2(x3);
+            acc0 = ptx::fadd2(acc0, ptx::f2_pack(p0, p1));
+            acc1 = ptx::fadd2(acc1, ptx::f2_pack(p2, p3));
+            // weights to 16 bits, the operand type of the tensor core; their
+            // sum l stays fp32
+            pk[e] = ptx::pack2<kBf16>(p0, p1);
+            pk[e + 1] = ptx::pack2<kBf16>(p2, p3);
+          }
+          float s0, s1, s2, s3;
+          ptx::f2_unpack(acc0, s0, s1);
+          ptx::f2_unpack(acc1, s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+        }
+        // P_w and O_w are in use until the group's previous product is done
+        if (it > 0) {
+          ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSiteDwPvDone);
+          ++pvcnt;
+          __syncwarp();
+          ptx::tc_fence_after();
+        }
+        if (rescale) {
+#pragma unroll 1
+          for (int q4 = 0; q4 < D / 32; ++q4) {
+            uint32_t orr[32];
+            ptx::tmem_ld32(tO0 + lane_off + w * D + q4 * 32, orr);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+            ptx::tmem_st32(tO0 + lane_off + w * D + q4 * 32, orr);
+          }
+          ptx::tmem_wait_st();
+        }
+        if (has) {
+          uint8_t* prow = sgen + L::kP + w * L::kPTile + t * 128;
+#pragma unroll
+          for (int k = 0; k < kDwTile / 8; ++k)
+            *reinterpret_cast<uint4*>(prow + (k >> 3) * L::kChunkBytes + (((k & 7) ^ (t & 7)) << 4)) =
+                make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+          ptx::fence_proxy_async_smem();
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(L::bPFull + w));
+        ++it;
+      }
+      // ---- end of the piece: the group's last product
+      if (it > 0) {
+        ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSiteDwPvDone);
+        ++pvcnt;
+        __syncwarp();
+      }
+      ptx::tc_fence_after();
+      const size_t head = static_cast<size_t>(pc.b) * p.Hk + pc.unit / p.row_blocks;
+      const size_t out_row = head * p.R + row;
+      const size_t slot = 2ull * blockIdx.x + pc.slot;
+      const int srow = kTiles == 2 ? w * kDwTile + t : t;
+      float f0 = 1.f, f1 = 0.f;
+      int c0 = 0, c1 = D;                            // columns this thread writes
+      if constexpr (kTiles == 1) {
+        // merge the two groups' parts of the keys; group w writes half w of
+        // the columns (both groups' warps reach the same TMEM lanes)
+        ml_s(w)[t] = make_float2(neg_m, l);
+        ptx::tc_fence_before();
+        ptx::named_bar_sync(1, 256);
+        ptx::tc_fence_after();
+        const float2 o0 = ml_s(0)[t], o1 = ml_s(1)[t];
+        neg_m = o0.y > 0.f ? (o1.y > 0.f ? fminf(o0.x, o1.x) : o0.x) : (o1.y > 0.f ? o1.x : 0.f);
+        f0 = o0.y > 0.f ? ptx::ex2(neg_m - o0.x) : 0.f;
+        f1 = o1.y > 0.f ? ptx::ex2(neg_m - o1.x) : 0.f;
+        l = f0 * o0.y + f1 * o1.y;
+        c0 = w * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      if (has) {
+#pragma unroll 1
+        for (int col = c0; col < c1; col += 32) {
+          uint32_t a[32];
+          ptx::tmem_ld32(tO0 + lane_off + (kTiles == 2 ? w * D : 0) + col, a);
+          ptx::tmem_wait_ld();
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = f0 > 0.f ? __uint_as_float(a[e]) * f0 : 0.f;
+          if (kTiles == 1 && pc.n > 1) {
+            ptx::tmem_ld32(tO0 + lane_off + D + col, a);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e] = f1 > 0.f ? fmaf(__uint_as_float(a[e]), f1, x[e]) : x[e];
+          }
+          if (t < nrows) {
+            if (pc.whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + col);
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                dst[v] = make_uint4(ptx::pack2<kBf16>(x[8 * v] * inv, x[8 * v + 1] * inv),
+                                    ptx::pack2<kBf16>(x[8 * v + 2] * inv, x[8 * v + 3] * inv),
+                                    ptx::pack2<kBf16>(x[8 * v + 4] * inv, x[8 * v + 5] * inv),
+                                    ptx::pack2<kBf16>(x[8 * v + 6] * inv, x[8 * v + 7] * inv));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.slot_rows + srow) * D + col);
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+            }
+          }
+        }
+        if (t < nrows && (kTiles == 2 || w == 0)) {
+          if (pc.whole)
+            p.lse[out_row] =
+                l > 0.f ? (ptx::lg2(l) - neg_m) * 0.693147180559945309f : -INFINITY;
+          else
+            p.part_ml[slot * p.slot_rows + srow] = make_float2(neg_m, l);
+        }
+      }
+      ptx::tc_fence_before();
+      if constexpr (kTiles == 1) {
+        // the statistics may be overwritten, and both outputs
+        ptx::named_bar_sync(1, 256);
+        ptx::mbar_arrive(bar(L::bOFree + 0));
+        ptx::mbar_arrive(bar(L::bOFree + 1));
+      } else {
+        ptx::mbar_arrive(bar(L::bOFree + w));
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kDwSWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// One block of D threads per (head, row), thread c owning output column c:
+// rows of units that one CTA finished are left alone; the parts of a cut
+// unit are scaled to the largest maximum, added in the order of the runs and
+// divided once.  A row without a visible key has no live part: O = 0 and
+// LSE = -inf.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(D)
+    fa_decode_win_combine_kernel(const __grid_constant__ DecWinParams p) {
+  const int row = blockIdx.x % p.R, head = blockIdx.x / p.R;
+  const int b = head / p.Hk, rb = row / p.row_span;
+  const int c = threadIdx.x;
+  long long before, total;
+  dec_tile_sums(p, b, before, total);
+  const int nt = dec_tiles(dec_span_of(p, b));
+  const long long s = before + static_cast<long long>((head - b * p.Hk) * p.row_blocks + rb) * nt;
+  const long long e = s + nt;
+  int cta = static_cast<int>(s * p.grid / total);       // the run that holds tile s
+  while (cta > 0 && dec_run_start(total, cta, p.grid) > s) --cta;
+  while (dec_run_start(total, cta + 1, p.grid) <= s) ++cta;
+  ptx::griddep_wait();   // the parts are complete, and this grid ends after the main one
+  if (dec_run_start(total, cta + 1, p.grid) >= e) return;
+  float nm = INFINITY, l = 0.f, acc = 0.f;
+  for (long long st; (st = dec_run_start(total, cta, p.grid)) < e; ++cta) {
+    if (dec_run_start(total, cta + 1, p.grid) == st) continue;   // an empty run
+    const size_t part = (2ull * cta + (st >= s ? 0 : 1)) * p.slot_rows + (row - rb * p.row_span);
+    const float2 ml = p.part_ml[part];
+    const float x = p.part_o[part * D + c];
+    if (!(ml.y > 0.f)) continue;
+    const float m = fminf(nm, ml.x);
+    const float fo = nm == INFINITY ? 0.f : ptx::ex2(m - nm), fn = ptx::ex2(m - ml.x);
+    acc = fmaf(fn, x, fo * acc);
+    l = fmaf(fn, ml.y, fo * l);
+    nm = m;
+  }
+  const size_t out = static_cast<size_t>(head) * p.R + row;
+  const uint32_t pk = ptx::pack2<kBf16>(l > 0.f ? acc / l : 0.f, 0.f);
+  static_cast<uint16_t*>(p.o)[out * D + c] = static_cast<uint16_t>(pk & 0xffffu);
+  if (c == 0) p.lse[out] = l > 0.f ? (ptx::lg2(l) - nm) * 0.693147180559945309f : -INFINITY;
+}
+
+}  // namespace fa

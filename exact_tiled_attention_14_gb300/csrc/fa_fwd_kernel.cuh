@@ -41,6 +41,14 @@
 // a thread that waits on a barrier stalls until the tensor core has taken
 // every MMA it queued before, and with two issuers one thread's waits
 // overlap the other's queued work.
+//
+// Sliding-window calls (kWin) keep for the query at position p the keys
+// j <= p with j > p - win or j < sinks.  A unit streams only the key tiles
+// that one of its rows can see: the tiles of the sinks, then the tiles of
+// the union of its rows' windows; of these each query tile computes its own
+// (win_active), so a unit of 256 rows costs about (win + 128) / 128 + the
+// sink tiles per query tile whatever the length.  H query heads may share
+// Hk key/value heads.
 #pragma once
 
 #include <cuda.h>
@@ -150,6 +158,12 @@ struct FwdParams {
   uint32_t drop_k0, drop_k1;
   uint32_t drop_off;
   float drop_scale;
+  // Sliding window (kWin variants only, with kKv and kCausal): window and
+  // sink counts (win >= 1), and the key/value heads: K and V are
+  // [B * Hk, Nk, d] and query head h reads key/value head h / (H / Hk).
+  int win;
+  int sinks;
+  int Hk;
 };
 
 // ---------------------------------------------------------------- tracing
@@ -281,6 +295,12 @@ struct Unit {
   int bh, mblk, n0, n1;
   int len, off;   // keys of this head; position of query row r is r + off (kKv)
   int lenq, q0, k0;   // queries of this head; first query and key token (varlen)
+  // kWin: the list of key tiles the unit streams is the sink tiles 0 .. ns - 1,
+  // then wa, wa + 1, ... (nl tiles in all); query tile w computes the ones
+  // win_active() names: sink tiles below n_sink and tiles a_w .. e_w - 1.  Of
+  // the keys in them some row of the unit sees those below min(sinks, hi)
+  // and lo .. hi - 1.
+  int ns, wa, nl, n_sink, a0, a1, e0, e1, lo, hi;
 };
 
 // A piece of work: key tiles [kb, kb + n_w) of query tile w of one unit.
@@ -289,7 +309,21 @@ struct Unit {
 struct Piece {
   int bh, mblk, kb, n0, n1, tail, slot;
   int len, off, lenq, q0, k0;   // as in Unit
+  int ns, wa, nl, n_sink, a0, a1, e0, e1, lo, hi;   // as in Unit (kWin)
 };
+
+// Key tile at position j of a piece's list (kWin), and whether query tile w
+// computes it.
+__host__ __device__ __forceinline__ int win_tile(const Piece& u, int j) {
+  return j < u.ns ? j : u.wa + (j - u.ns);
+}
+__host__ __device__ __forceinline__ bool win_active(const Piece& u, int w, int kt) {
+  return kt < (w ? u.e1 : u.e0) && (kt < u.n_sink || kt >= (w ? u.a1 : u.a0));
+}
+// Key/value head of query head bh (kWin: Hk heads shared by groups).
+__host__ __device__ __forceinline__ int kv_head(const FwdParams& p, int bh) {
+  return (bh / p.H) * p.Hk + (bh % p.H) / (p.H / p.Hk);
+}
 
 // Floats of one workspace slot: unnormalised O of both query tiles stored
 // column by column (element (col, row) of tile w at (w*D + col)*128 + row,
@@ -317,7 +351,7 @@ __host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : 
 // tiles each of its two query tiles streams.  Host code calls it too
 // (fa_work_tiles counts the tile pairs of a head with it), so the count the
 // host reports is the loop bound the kernel runs.
-template <bool kCausal, bool kKv = false>
+template <bool kCausal, bool kKv = false, bool kWin = false>
 __host__ __device__ __forceinline__ Unit decode_unit(int s, const FwdParams& p) {
   Unit u;
   {
@@ -359,6 +393,29 @@ __host__ __device__ __forceinline__ Unit decode_unit(int s, const FwdParams& p) 
     }
     u.n0 = n[0];
     u.n1 = n[1];
+    if constexpr (kWin) {
+      // tile w's window starts in tile a_w and its last row's position lies
+      // in tile e_w - 1 (or the keys end there); e_w = 0 without rows
+      const int n_sink = (imin(p.sinks, len) + kBN - 1) / kBN;
+      int a[2], e[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int first = (t0 + w) * kBM;
+        e[w] = n[w];
+        a[w] = imin(imax(first + u.off - p.win + 1, 0) / kBN, e[w]);
+        n[w] = imin(n_sink, e[w]) + imax(0, e[w] - imax(a[w], n_sink));
+      }
+      u.n0 = n[0];
+      u.n1 = n[1];
+      const int end = imax(e[0], e[1]);
+      u.n_sink = n_sink;
+      u.a0 = a[0]; u.a1 = a[1]; u.e0 = e[0]; u.e1 = e[1];
+      u.ns = imin(n_sink, end);
+      u.wa = imax(e[0] == 0 ? a[1] : (e[1] == 0 ? a[0] : imin(a[0], a[1])), n_sink);
+      u.nl = u.ns + imax(0, end - u.wa);
+      u.lo = imax(t0 * kBM + u.off - p.win + 1, 0);
+      u.hi = imin(len, imax(imin((t0 + 2) * kBM, lenq) + u.off, 0));
+    }
   } else {
     u.len = p.N;
     u.off = 0;
@@ -399,17 +456,22 @@ __device__ __forceinline__ void cursor_init(const FwdParams& p, int cta, int gri
   cu.end = kSplit ? tail_start(p, cta + 1, grid) : 0;
   cu.first_t = kSplit ? static_cast<int>(cu.pos / p.n_kv) : 0;
 }
-template <bool kCausal, bool kSplit, bool kKv = false>
+template <bool kCausal, bool kSplit, bool kKv = false, bool kWin = false>
 __device__ __forceinline__ bool next_piece(const FwdParams& p, int cta, int grid, Cursor& cu,
                                            Piece& pc) {
   if (!kSplit || cu.r < p.full_rounds) {
     const int s = unit_at(cu.r, cta, grid);
     if (!kSplit && s >= p.num_units) return false;
     ++cu.r;
-    const Unit u = decode_unit<kCausal, kKv>(s, p);
+    const Unit u = decode_unit<kCausal, kKv, kWin>(s, p);
     pc.bh = u.bh; pc.mblk = u.mblk; pc.kb = 0; pc.n0 = u.n0; pc.n1 = u.n1;
     pc.tail = -1; pc.slot = 0; pc.len = u.len; pc.off = u.off;
     pc.lenq = u.lenq; pc.q0 = u.q0; pc.k0 = u.k0;
+    if constexpr (kWin) {
+      pc.ns = u.ns; pc.wa = u.wa; pc.nl = u.nl; pc.n_sink = u.n_sink;
+      pc.a0 = u.a0; pc.a1 = u.a1; pc.e0 = u.e0; pc.e1 = u.e1;
+      pc.lo = u.lo; pc.hi = u.hi;
+    }
     return true;
   }
   if (cu.pos >= cu.end) return false;
@@ -485,7 +547,10 @@ __device__ __forceinline__ size_t lse_at(const FwdParams& p, const Piece& u, int
 // kKv: queries against a key set of their own length, per-batch key counts
 // and a causal alignment (see FwdParams); square calls compile none of it.
 // kDrop: dropout on the attention weights (with kKv on square shapes).
-template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool kDrop = false>
+// kWin: sliding window with sinks and shared key/value heads (with kKv and
+// kCausal).
+template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool kDrop = false,
+          bool kWin = false>
 __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using L = Smem<D, kDrop>;
@@ -566,7 +631,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       Cursor cu;
       cursor_init<kSplit>(p, cta, grid, cu);
       Piece u;
-      while (next_piece<kCausal, kSplit, kKv>(p, cta, grid, cu, u)) {
+      while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
         const int nkv = max(u.n0, u.n1);
         for (int j = 0; j < nkv; ++j) {
           for (int w = 0; w < 2; ++w) {
@@ -603,8 +668,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       Cursor cu;
       cursor_init<kSplit>(p, cta, grid, cu);
       Piece u;
-      while (next_piece<kCausal, kSplit, kKv>(p, cta, grid, cu, u)) {
-        const int nkv = max(u.n0, u.n1);
+      while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
+        const int nkv = kWin ? u.nl : max(u.n0, u.n1);
         if (kKv && nkv == 0) continue;   // no visible key: the softmax warps write the rows
         // Q of this piece may only overwrite the buffer once the previous
         // piece's last S MMA has read it; the first K tile does not wait for
@@ -642,6 +707,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             ptx::mbar_arrive_expect_tx(bar(L::bKvFull + slot), nc * L::kChunkBytes);
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
+            if constexpr (kWin) { y = win_tile(u, j) * kBN; z = kv_head(p, u.bh); }
             if (kKv && p.varlen) { z = u.k0 + y; y = u.bh % p.H; }   // head, token
             for (int c = 0; c < nc; ++c)
               ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm,
@@ -674,8 +740,10 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     // The issue loop has to keep up with the tensor core (an M128 x N128 x
     // K16 MMA lasts ~64 cycles), so descriptors are precomputed: per MMA only
     // the 32-bit address word changes, by a compile-time offset.
-    // Warp 8 issues the S = Q K^T products, warp 10 the O += P V products.
-    if (lane == 0) {
+    // Warp 8 issues the S = Q K^T products, warp 10 the O += P V products,
+    // each from its first lane.  In the kWin variants all of warp 10 walks
+    // the tiles, since it also clears rows of V (below).
+    if (lane == 0 || (kWin && warp == kPvWarp)) {
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBM, kBN, fmt, 0);  // Q (K-major) x K (K-major)
       constexpr uint32_t idesc_o_full = ptx::idesc_f16(kBM, D, fmt, 1);  // P x V (MN-major)
@@ -791,8 +859,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       uint32_t base = 0;
       if (warp == kMmaWarp) {
         // S = Q K^T for both query tiles, one key tile ahead of the softmax
-        while (next_piece<kCausal, kSplit, kKv>(p, cta, grid, cu, u)) {
-          const int nkv = max(u.n0, u.n1);
+        while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
+          const int nkv = kWin ? u.nl : max(u.n0, u.n1);
           if (kKv && nkv == 0) continue;
           pf.lap(6);
           const uint32_t qb = k_units % L::kQBufs;
@@ -803,8 +871,14 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           ptx::tc_fence_after();
           for (int j = 0; j < nkv; ++j) {
             const uint32_t kslot = ring_wait(base + (j == 0 ? 0u : 2u * j - 1u));
-            if (j < u.n0) issue_s_own(0, kslot);
-            if (j < u.n1) issue_s_own(1, kslot);
+            if constexpr (kWin) {
+              const int kt = win_tile(u, j);
+              if (win_active(u, 0, kt)) issue_s_own(0, kslot);
+              if (win_active(u, 1, kt)) issue_s_own(1, kslot);
+            } else {
+              if (j < u.n0) issue_s_own(0, kslot);
+              if (j < u.n1) issue_s_own(1, kslot);
+            }
             if (alive) {
               ptx::mma_commit(bar(L::bKvEmpty + kslot));
               if (j + 1 == nkv) ptx::mma_commit(bar(L::bQEmpty + qb));  // last use of Q
@@ -814,9 +888,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           base += 2u * nkv;
           ++k_units;
         }
-      } else {
+      } else if constexpr (!kWin) {
         // O += P V for both query tiles, as soon as the softmax has written P
-        while (next_piece<kCausal, kSplit, kKv>(p, cta, grid, cu, u)) {
+        while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
           const int nkv = max(u.n0, u.n1);
           if (kKv && nkv == 0) continue;
           for (int j = 0; j < nkv; ++j) {
@@ -827,6 +901,58 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             if (j < u.n1) issue_pv_own(1, j, v_lo);
             if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
             issued_any = true;
+          }
+          if (u.n0 > 0) ++ucnt0;
+          if (u.n1 > 0) ++ucnt1;
+          base += 2u * nkv;
+        }
+      } else {
+        // The same over the window's tiles.  A key that no row of the unit
+        // sees (past its batch's key count, between the sinks and the
+        // windows, after its last row) has weight 0, but 0 times a value
+        // that is not finite (stale or unwritten cache) is not 0: the rows
+        // of such keys in the loaded V tile are overwritten with zeros first.
+        // These are the first and last tiles of the list and the last sink
+        // tile; the tensor core meanwhile works on S and the softmax on P.
+        // Lane 0 alone waits on barriers and the warp joins it afterwards: a
+        // lane that polled on its own could miss a phase that lane 0's
+        // progress lets pass twice.
+        while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
+          const int nkv = u.nl;
+          if (nkv == 0) continue;
+          int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
+          for (int j = 0; j < nkv; ++j) {
+            const uint32_t vpos = base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u);
+            const uint32_t vslot = vpos % L::kStages;
+            if (lane == 0) ring_wait(vpos);
+            __syncwarp();
+            const int kt = win_tile(u, j), key0 = kt * kBN;
+            const bool past = key0 + kBN > u.hi, before = key0 < u.lo && key0 + kBN > p.sinks;
+            if (past || before) {
+              const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
+              const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
+              const int r_sink = min(max(p.sinks - key0, 0), r_lo);
+              uint8_t* vt = sgen + L::kKV + vslot * L::kTile;
+              for (int ch = 0; ch < L::kChunks; ++ch) {
+                uint4* rows = reinterpret_cast<uint4*>(vt + ch * L::kChunkBytes);
+                for (int i = r_sink * 8 + lane; i < r_lo * 8; i += 32)
+                  rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = r_hi * 8 + lane; i < kBN * 8; i += 32)
+                  rows[i] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
+              __syncwarp();
+            }
+            const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
+            const bool act0 = win_active(u, 0, kt), act1 = win_active(u, 1, kt);
+            if (lane == 0) {
+              if (act0) issue_pv_own(0, it0, v_lo);
+              if (act1) issue_pv_own(1, it1, v_lo);
+              if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
+              issued_any = true;
+            }
+            it0 += act0;
+            it1 += act1;
           }
           if (u.n0 > 0) ++ucnt0;
           if (u.n1 > 0) ++ucnt1;
@@ -868,8 +994,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     Cursor cu;
     cursor_init<kSplit>(p, cta, grid, cu);
     Piece u;
-    while (next_piece<kCausal, kSplit, kKv>(p, cta, grid, cu, u)) {
-      const int n = w ? u.n1 : u.n0;
+    while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
+      const int n = w ? u.n1 : u.n0;          // key tiles of this query tile
+      const int nlist = kWin ? u.nl : n;      // key tiles streamed (kWin: some for the other tile)
       const int tile = 2 * u.mblk + w;
       const int row = tile * kBM + t;
       if (n == 0) {
@@ -889,7 +1016,12 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       float m_ref = -INFINITY;  // reference maximum of the raw scores q.k
       float neg_m = 0.f;        // -m_ref * c (0 while m_ref is -inf)
       float l = 0.f;            // running sum of 2^(s*c + neg_m)
-      for (int j = 0; j < n; ++j) {
+      int j = -1;               // key tiles of this query tile before the current one
+      for (int jl = 0; jl < nlist; ++jl) {
+        if constexpr (kWin) {
+          if (!win_active(u, w, win_tile(u, jl))) continue;
+        }
+        ++j;
         pf.lap(7);
         ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteSFull);
         pf.lap(0);
@@ -910,8 +1042,18 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         pf.lap(1);
 
         // mask: keys past N, and on the diagonal tile keys after this row
-        const int kj = u.kb + j;                 // key tile index
-        if constexpr (kKv) {
+        const int kj = kWin ? win_tile(u, jl) : u.kb + jl;   // key tile index
+        if constexpr (kWin) {
+          // keys lo .. lim - 1 of the window and, of those before it, the sinks
+          const int pos = row + u.off, key0 = kj * kBN;
+          const int lim = min(kBN, min(u.len, pos + 1) - key0);
+          const int lo = pos - p.win + 1 - key0, sink = p.sinks - key0;
+          if (lim < kBN || (lo > 0 && sink < kBN)) {
+#pragma unroll
+            for (int i = 0; i < kBN; ++i)
+              if (i >= lim || (i < lo && i >= sink)) sv[i] = -INFINITY;
+          }
+        } else if constexpr (kKv) {
           // keys past this batch's count, and keys after this row's position
           int lim = min(kBN, u.len - kj * kBN);
           if (kCausal) lim = min(lim, row + u.off - kj * kBN + 1);

@@ -40,9 +40,10 @@ int check_forward_args(const void* q, const void* k, const void* v, const void* 
                        const float* lse, int B, int H, int N, int d, float scale, int dtype,
                        bool* empty);
 
-// 3-D view [BH, N, d] of a contiguous [B, H, N, d] tensor; boxes of 128 rows x
+// 3-D view [BH, N, d] of a contiguous [B, H, N, d] tensor; boxes of 128 (or box_rows) rows x
 // 64 columns (128 bytes), 128-byte swizzle, zero fill past N.
-bool make_tmap(CUtensorMap* m, const void* ptr, int BH, int N, int d, bool bf16);
+bool make_tmap(CUtensorMap* m, const void* ptr, int BH, int N, int d, bool bf16,
+               int box_rows = 128);
 // A packed token-major tensor [tokens, H, width] as a (column, head, token)
 // map: a box of 64 columns x 1 head x 128 tokens fills shared memory exactly
 // like a 128 x 64 tile of the [B, H, N, d] layout.

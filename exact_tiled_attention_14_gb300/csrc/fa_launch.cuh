@@ -10,8 +10,9 @@
 
 namespace fa {
 
-// Launch fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop> with `grid` persistent CTAs.
-template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool kDrop = false>
+// Launch fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin> with `grid` persistent CTAs.
+template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool kDrop = false,
+          bool kWin = false>
 cudaError_t launch_variant(const FwdParams& p, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};  // devices on which the smem limit was raised
   int dev = 0;
@@ -19,13 +20,13 @@ cudaError_t launch_variant(const FwdParams& p, int grid, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
-    e = cudaFuncSetAttribute(fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop>,
+    e = cudaFuncSetAttribute(fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, kDrop>::kAlloc);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
-  fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop><<<grid, threads_of<D, kDrop>(), Smem<D, kDrop>::kAlloc,
-                                                         stream>>>(p);
+  fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin>
+      <<<grid, threads_of<D, kDrop>(), Smem<D, kDrop>::kAlloc, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -43,5 +44,8 @@ cudaError_t launch_fwd_drop_d64(const FwdParams& p, int grid, bool bf16, bool ca
                                 cudaStream_t stream);
 cudaError_t launch_fwd_drop_d128(const FwdParams& p, int grid, bool bf16, bool causal,
                                  cudaStream_t stream);
+// Sliding-window calls with sinks and shared key/value heads (the kKv,
+// kCausal, kWin variants).
+cudaError_t launch_fwd_win(const FwdParams& p, int grid, int d, bool bf16, cudaStream_t stream);
 
 }  // namespace fa

@@ -25,6 +25,10 @@
  *    through a caller's fp32 scratch);
  *  - decoding: fa_decode (a few queries against a long cache, key axis
  *    split across the GPU);
+ *  - sliding windows with sinks, key/value heads shared by groups of query
+ *    heads: fa_fwd_window, fa_bwd_window (prompts, chunks after a cache,
+ *    training), fa_decode_window (the last tokens of each cache),
+ *    fa_decode_tree (the tokens of a drafted tree behind each cache);
  *  - status and settings: fa_strerror, fa_status, fa_set_watchdog_ns,
  *    fa_set_unit_group, fa_watchdog_selftest, fa_work_tiles, fa_version.
  *
@@ -73,7 +77,7 @@ enum {
   FA_ERR_LAUNCH = 9,         /* the launch itself failed (CUDA error)          */
   FA_ERR_TIMEOUT = 10,       /* a kernel's bounded wait ran out (fa_status)    */
   FA_ERR_CUDA = 11,          /* a CUDA runtime call failed (fa_status)         */
-  FA_ERR_WORKSPACE = 12,     /* workspace smaller than fa_fwd_workspace_size   */
+  FA_ERR_WORKSPACE = 12,     /* workspace missing or smaller than its size call says */
   FA_ERR_DROPOUT = 13        /* dropout probability outside [0, 1 - 1/512)     */
 };
 
@@ -548,6 +552,143 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
  * FA_ERR_NULLPTR, FA_ERR_SHAPE, FA_ERR_UNSUPPORTED_D or FA_ERR_DEVICE.
  */
 int fa_decode_workspace_size(int B, int H, int Nq, int Nk, int d, size_t *bytes);
+
+/*
+ * fa_fwd_window — exact attention under a sliding window with sinks, with
+ * key/value heads that groups of query heads may share.
+ *
+ * The pages leave masks other than the causal one out ("FlashAttention: The
+ * Matrix You Never Have to Write Down", section "Two things this
+ * deliberately doesn't do"); this entry point is fa_fwd_kv's causal form
+ * with two more of them, by the same tiled online softmax.  The query at
+ * position p sees key j of its batch iff
+ *     j < len_b,  j <= p,  and  (j > p - window  or  j < sinks):
+ * the last `window` keys up to its own position, and the first `sinks` keys.
+ * Key tiles that no row of a query block sees are never loaded, so the cost
+ * grows with Nq * (window + sinks), not with Nq * Nk.
+ *
+ *   q, o      : [B, H, Nq, d], dtype `dtype`, 16-byte aligned (o written).
+ *   k, v      : [B, Hk, Nk, d], 16-byte aligned (may be NULL when Nk = 0).
+ *   lse       : [B, H, Nq] float32, 4-byte aligned (written).
+ *   H, Hk     : query and key/value heads, H a multiple of Hk; query head h
+ *               reads key/value head h / (H / Hk).
+ *   causal    : 1 upper-left (query i at position i) or 2 bottom-right (query
+ *               i at position len_b - Nq + i).
+ *   window    : >= 1 (a window past every length hides nothing).
+ *   sinks     : >= 0.
+ *   seqlens_k : NULL (len_b = Nk) or B int32 key counts on the device, 4-byte
+ *               aligned, clamped to [0, Nk].
+ *   d, scale, dtype, stream : as fa_fwd.
+ * A row that sees no key gets O = 0 and LSE = -inf.  Keys and values past a
+ * batch's count, and those no query of a 256-row block sees, may hold
+ * anything (NaN included).  A value that some row of the block sees must be
+ * finite for the block's other rows to be, as in every entry point here.
+ * Errors as fa_fwd; FA_ERR_SHAPE also for H not a multiple of Hk, causal
+ * other than 1 or 2, window < 1, sinks < 0, and Nq + Nk, B * H or B * H
+ * times the 128-row tiles of both over 2^30.  B * H * Nq == 0 writes nothing.
+ */
+int fa_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
+                  int Hk, int Nq, int Nk, int d, int causal, int window, int sinks,
+                  const int *seqlens_k, float scale, int dtype, cudaStream_t stream);
+
+/*
+ * fa_bwd_window — the backward pass of fa_fwd_window: dQ, dK, dV of
+ * sum(dO * O) for O, LSE of the same arguments (formulas as fa_bwd, the sums
+ * for dK and dV running over every query head of a group).
+ *
+ *   q, o, dout, dq : [B, H, Nq, d];  k, v, dk, dv : [B, Hk, Nk, d];
+ *   lse, delta     : [B, H, Nq] float32 (delta is scratch, as in fa_bwd).
+ *   workspace, workspace_bytes : device buffer, 256-byte aligned, at least
+ *                    fa_bwd_window_workspace_size bytes (may be NULL when that
+ *                    is 0), owned by the caller; contents need no
+ *                    initialisation.  Calls that share one must not overlap.
+ *   Keys that no query sees get dK = dV = 0, rows that see no key dQ = 0, and
+ *   their Q, dO, K and V may hold anything.  Results are deterministic.
+ * Errors as fa_bwd and fa_fwd_window, plus FA_ERR_WORKSPACE.  q, o, lse,
+ * dout, dq and delta may be NULL when Nq = 0, k, v, dk and dv when Nk = 0.
+ */
+int fa_bwd_window(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                  const void *dout, void *dq, void *dk, void *dv, float *delta, int B, int H,
+                  int Hk, int Nq, int Nk, int d, int causal, int window, int sinks,
+                  const int *seqlens_k, float scale, int dtype, void *workspace,
+                  size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_bwd_window_workspace_size — bytes of workspace fa_bwd_window needs for
+ * this shape.  Host-only.  Returns FA_ERR_NULLPTR, FA_ERR_SHAPE or
+ * FA_ERR_UNSUPPORTED_D.
+ */
+int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, int sinks,
+                                 size_t *bytes);
+
+/*
+ * fa_decode_window — the last Nq tokens of each sequence against its cache
+ * under fa_fwd_window's mask (bottom-right: token i of batch b at position
+ * len_b - Nq + i), the keys of all batches split evenly across the GPU
+ * (the pages on decoding: see fa_decode).
+ *
+ *   q, o      : [B, H, Nq, d], 1 <= Nq <= 16, 16-byte aligned (o written).
+ *   k, v      : [B, Hk, Nk, d], the cache, 16-byte aligned (may be NULL when
+ *               Nk = 0).  Only the keys that some token sees are read (and up
+ *               to 15 more rows at each end of them, which may hold anything).
+ *   lse       : [B, H, Nq] float32.
+ *   H, Hk, window, sinks, seqlens_k : as fa_fwd_window; len_b counts the new
+ *               tokens' own keys.
+ *   workspace, workspace_bytes : device buffer, 256-byte aligned, at least
+ *               fa_decode_window_workspace_size bytes, owned by the caller;
+ *               contents need no initialisation.  Calls that share one must
+ *               not overlap on the GPU.
+ *   d, scale, dtype, stream : as fa_fwd.
+ * A token that sees no key (Nq > len_b) gets O = 0 and LSE = -inf.  Results
+ * do not depend on the order CTAs run in.
+ * Errors: FA_ERR_SHAPE (also for H not a multiple of Hk, Nq outside 1 .. 16,
+ * Nk or B * H * Nq over 2^30), FA_ERR_UNSUPPORTED_D, FA_ERR_SHAPE for
+ * window < 1 or sinks < 0, FA_ERR_DTYPE, FA_ERR_SCALE, then B * H == 0
+ * returns FA_OK, then FA_ERR_NULLPTR, FA_ERR_ALIGN, FA_ERR_DEVICE,
+ * FA_ERR_WORKSPACE, FA_ERR_TENSORMAP, FA_ERR_LAUNCH.
+ */
+int fa_decode_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
+                     int Hk, int Nq, int Nk, int d, int window, int sinks, const int *seqlens_k,
+                     float scale, int dtype, void *workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
+/*
+ * fa_decode_tree — Nq drafted tokens of each sequence, which branch from its
+ * last committed token, against its cache in one call (the pages on
+ * decoding: see fa_decode).
+ *
+ * Batch b's history is the keys 0 .. c_b - 1 of its cache; drafted token j's
+ * key and value are in slot c_b + j.  Row i of `tree` marks with bit j each
+ * drafted token j that token i sees: its ancestors and itself.  The position
+ * of token i is c_b - 1 plus the tokens its row marks (its depth in the
+ * tree).  Token i at position p sees
+ *     history key j  iff  j > p - window or j < sinks (always, window = 0);
+ *     drafted token j  iff  bit j of its row is set and the same holds for
+ *                           token j's position.
+ *   q, o      : [B, H, Nq, d], 1 <= Nq <= 64, 16-byte aligned (o written).
+ *   k, v      : [B, Hk, Nk, d], Nk >= Nq.
+ *   tree      : [B, Nq] 64-bit rows on the device, 8-byte aligned.  Bits from
+ *               Nq on are ignored; a row of 0 (padding) sees the history.
+ *               Slots that no row marks, and keys before every row's
+ *               window, may hold anything.
+ *   seqlens_k : NULL (c_b = Nk - Nq) or B int32 history counts, clamped to
+ *               [0, Nk]; drafted tokens whose slot is past Nk are not seen.
+ *   window    : >= 1, or 0 for none.
+ *   Other arguments, workspace and errors as fa_decode_window (FA_ERR_SHAPE
+ *   also for Nk < Nq); FA_ERR_ALIGN also for a misaligned tree.
+ */
+int fa_decode_tree(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
+                   int Hk, int Nq, int Nk, int d, const unsigned long long *tree, int window,
+                   int sinks, const int *seqlens_k, float scale, int dtype, void *workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_decode_window_workspace_size — bytes of workspace that fa_decode_window
+ * and fa_decode_tree need for this shape (1 <= Nq <= 64) on the current
+ * device (0 when B * H == 0).  Returns FA_ERR_NULLPTR, FA_ERR_SHAPE,
+ * FA_ERR_UNSUPPORTED_D or FA_ERR_DEVICE.
+ */
+int fa_decode_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, size_t *bytes);
 
 /*
  * fa_strerror — human-readable name of a return code (a static string, never
