@@ -56,6 +56,7 @@ cudaError_t launch_variant(const DecWinParams& p, cudaStream_t stream) {
 }
 
 constexpr long long kMaxCount = 1ll << 30;
+constexpr long long kMaxRowTiles = 1ll << 31;
 
 // Sizes and widths, in the documented order.
 int check_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int max_q) {
@@ -64,6 +65,8 @@ int check_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int max_q) {
   if (Nq < 1 || Nq > max_q) return FA_ERR_SHAPE;
   const long long heads = static_cast<long long>(B) * H;
   if (Nk > kMaxCount || heads > kMaxCount || heads * Nq > kMaxCount) return FA_ERR_SHAPE;
+  // rows times the key tiles of a whole cache: the tiles of all units fit in int
+  if (heads * Nq * ((Nk + kDwTile - 1ll) / kDwTile + 1) > kMaxRowTiles) return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
   return FA_OK;
 }

@@ -48,6 +48,7 @@ constexpr int kDwSWarp = 8, kDwLoadWarp = 9, kDwPvWarp = 10;
 constexpr uint32_t kDwSoftmaxRegs = 208, kDwIssueRegs = 88;
 static_assert(2 * 128 * kDwSoftmaxRegs + 128 * kDwIssueRegs <= 168 * kDwThreads, "register split");
 constexpr float kDwTau = 8.0f;        // lazy-rescale threshold, log2 units
+constexpr int kDwCombine = 10;        // parts of a row that are loaded together
 constexpr int kDwMaxTree = 64;        // drafted tokens (bits of a row's mask)
 constexpr int kDwMaxTokens = 16;      // new tokens of a window call
 
@@ -130,33 +131,50 @@ __device__ __forceinline__ DecSpan dec_span_of(const DecWinParams& p, int b) {
                   p.tree != nullptr);
 }
 
-// Sum of the key tiles of batches [0, n) and of all batches, by one warp.
-__device__ __forceinline__ void dec_tile_sums(const DecWinParams& p, int n, long long& before,
-                                              long long& total) {
-  const long long units = static_cast<long long>(p.Hk) * p.row_blocks;
-  long long bsum = 0, tsum = 0;
+// The deal of `total` key tiles to `grid` CTAs: the first `extra` runs have
+// per + 1 tiles, the others per; with fewer tiles than CTAs the CTAs past the
+// last tile have none (total < 2^31, see the host's check).
+struct DecDeal {
+  int per, extra, runs;
+};
+__host__ __device__ __forceinline__ DecDeal dec_deal(int total, int grid) {
+  DecDeal d;
+  d.runs = total < grid ? total : grid;
+  d.per = total / d.runs;
+  d.extra = total - d.per * d.runs;
+  return d;
+}
+__host__ __device__ __forceinline__ int dec_run_start(const DecDeal& d, int run) {
+  return run * d.per + (run < d.extra ? run : d.extra);
+}
+__host__ __device__ __forceinline__ int dec_run_of(const DecDeal& d, int tile) {
+  const int longer = d.extra * (d.per + 1);
+  return tile < longer ? tile / (d.per + 1) : d.extra + (tile - longer) / d.per;
+}
+// Key tiles of batches [0, n) and of all batches, by one warp.
+__device__ __forceinline__ void dec_tile_sums(const DecWinParams& p, int n, int& before,
+                                              int& total) {
+  const int units = p.Hk * p.row_blocks;
+  int bsum = 0, tsum = 0;
+  if (p.seqlens == nullptr) {   // all batches alike
+    const int t = dec_tiles(dec_span_of(p, 0)) * units;
+    before = n * t;
+    total = p.B * t;
+    return;
+  }
   for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-    const long long t = dec_tiles(dec_span_of(p, b)) * units;
+    const int t = dec_tiles(dec_span_of(p, b)) * units;
     tsum += t;
     if (b < n) bsum += t;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    tsum += __shfl_xor_sync(0xffffffffu, tsum, off);
-    bsum += __shfl_xor_sync(0xffffffffu, bsum, off);
-  }
-  before = bsum;
-  total = tsum;
-}
-__host__ __device__ __forceinline__ long long dec_run_start(long long total, int cta, int grid) {
-  return total / grid * cta + total % grid * cta / grid;
+  before = __reduce_add_sync(0xffffffffu, bsum);
+  total = __reduce_add_sync(0xffffffffu, tsum);
 }
 
 // A CTA's place in its run: batch, unit within the batch, tile within the
 // unit, tiles left.
 struct DecCursor {
-  int b, unit, tile;
-  long long left;
+  int b, unit, tile, left;
   int n_done;          // pieces taken so far
 };
 struct DecPiece {
@@ -172,11 +190,10 @@ __device__ __forceinline__ bool dec_next(const DecWinParams& p, DecCursor& c, De
   pc.t0 = c.tile;
   pc.s = dec_span_of(p, c.b);
   const int nt = dec_tiles(pc.s);
-  const long long n = nt - c.tile < c.left ? nt - c.tile : c.left;
-  pc.n = static_cast<int>(n);
+  pc.n = nt - c.tile < c.left ? nt - c.tile : c.left;
   pc.whole = c.tile == 0 && pc.n == nt;
   pc.slot = c.n_done == 0 ? 0 : 1;
-  c.left -= n;
+  c.left -= pc.n;
   ++c.n_done;
   c.tile = 0;
   if (++c.unit == p.Hk * p.row_blocks) {
@@ -313,8 +330,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
   uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
-  int* cursor_s = reinterpret_cast<int*>(sgen + L::kMisc + 8);                 // batch, unit, tile
-  long long* left_s = reinterpret_cast<long long*>(sgen + L::kMisc + 24);
+  int* cursor_s = reinterpret_cast<int*>(sgen + L::kMisc + 8);   // batch, unit, tile, tiles left
 
   // the combine kernel may be scheduled once every CTA has started (it waits
   // for this grid to complete before reading the parts)
@@ -350,39 +366,52 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   }
   if (warp == kDwPvWarp) {
     // this CTA's run and the batch, unit and tile that it starts in
-    long long before, total;
-    dec_tile_sums(p, 0, before, total);
-    const long long start = dec_run_start(total, blockIdx.x, p.grid);
-    const long long end = dec_run_start(total, blockIdx.x + 1, p.grid);
     const int units = p.Hk * p.row_blocks;
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      const int nt = b < p.B ? dec_tiles(dec_span_of(p, b)) : 0;
-      const long long mine = static_cast<long long>(nt) * units;
-      long long incl = mine;
+    int before, total;
+    dec_tile_sums(p, 0, before, total);
+    const DecDeal deal = dec_deal(total, p.grid);
+    const int run = blockIdx.x;
+    const int start = dec_run_start(deal, run);
+    const int left = run < deal.runs ? dec_run_start(deal, run + 1) - start : 0;
+    if (left > 0) {
+      if (p.seqlens == nullptr) {
+        const int nt = dec_tiles(dec_span_of(p, 0));
+        const int unit = start / nt;
+        if (lane == 0) {
+          cursor_s[0] = unit / units;
+          cursor_s[1] = unit % units;
+          cursor_s[2] = start - unit * nt;
+        }
+      } else {
+        int base = 0;
+        for (int b0 = 0; base <= start; b0 += 32) {
+          const int b = b0 + lane;
+          const int nt = b < p.B ? dec_tiles(dec_span_of(p, b)) : 0;
+          const int mine = nt * units;
+          int incl = mine;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += up;
+          for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += up;
+          }
+          const int first = base + incl - mine;
+          if (first <= start && start < first + mine) {
+            cursor_s[0] = b;
+            cursor_s[1] = (start - first) / nt;
+            cursor_s[2] = (start - first) % nt;
+          }
+          base += __shfl_sync(0xffffffffu, incl, 31);
+        }
       }
-      const long long first = base + incl - mine;
-      if (mine > 0 && first <= start && start < first + mine) {
-        cursor_s[0] = b;
-        cursor_s[1] = static_cast<int>((start - first) / nt);
-        cursor_s[2] = static_cast<int>((start - first) % nt);
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
-      if (base > start) break;
     }
-    if (lane == 0) *left_s = end - start;
+    if (lane == 0) cursor_s[3] = left;
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_base_ptr;
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
-  DecCursor cu{cursor_s[0], cursor_s[1], cursor_s[2], *left_s, 0};
+  DecCursor cu{cursor_s[0], cursor_s[1], cursor_s[2], cursor_s[3], 0};
   DecPiece pc;
   // rows of row tile w of a piece (kTiles == 1: both groups share tile 0)
   auto rows_of = [&](const DecPiece& x, int w) {
@@ -632,28 +661,38 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       int it = 0;                                   // tiles of this group so far
       for (int j = 0; j < pc.n; ++j) {
         if (!takes(pc, w, j)) continue;
-        ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
-        ++scnt;
-        __syncwarp();
-        ptx::tc_fence_after();
-        float sv[kDwTile];
-        if (has) {
+        // P_w and O_w are in use until the group's previous product is done
+        auto wait_pv = [&]() {
+          if (it > 0) {
+            ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSiteDwPvDone);
+            ++pvcnt;
+            __syncwarp();
+            ptx::tc_fence_after();
+          }
+        };
+        if (!has) {   // a warp without rows only keeps the order
+          ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
+          ++scnt;
+          ptx::mbar_arrive(bar(L::bSFree + w));
+          wait_pv();
+        } else {
+          uint32_t vis[4];
+          const bool all = dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), me, p.tree != nullptr, p.win,
+                                       p.sinks, vis);
+          ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
+          ++scnt;
+          __syncwarp();
+          ptx::tc_fence_after();
           uint32_t sr[kDwTile];
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld32(tS + q4 * 32, sr + q4 * 32);
           ptx::tmem_wait_ld();
+          float sv[kDwTile];
 #pragma unroll
           for (int e = 0; e < kDwTile; ++e) sv[e] = __uint_as_float(sr[e]);
-        }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
-        bool rescale = false;
-        float alpha = 1.f;
-        uint32_t pk[kDwTile / 2];
-        if (has) {
-          uint32_t vis[4];
-          if (!dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), me, p.tree != nullptr, p.win, p.sinks,
-                           vis)) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
+          if (!all) {
 #pragma unroll
             for (int e = 0; e < kDwTile; ++e)
               if (!((vis[e >> 5] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
@@ -670,6 +709,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           // lazy rescale, as in the prompt kernel: the reference moves only
           // when a tile exceeds it by 2^kDwTau
           const bool grow = (mx - m_ref) * c > kDwTau;
+          float alpha = 1.f;
           if (grow) {
             const float nm = -mx * c;
             alpha = (m_ref == -INFINITY) ? 0.f : ptx::ex2(nm - neg_m);
@@ -677,9 +717,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             m_ref = mx;
             neg_m = nm;
           }
-          rescale = it > 0 && __any_sync(0xffffffffu, grow);
+          const bool rescale = it > 0 && __any_sync(0xffffffffu, grow);
           const uint64_t c2 = ptx::f2_pack(c, c), nm2 = ptx::f2_pack(neg_m, neg_m);
           uint64_t acc0 = ptx::f2_pack(0.f, 0.f), acc1 = acc0;
+          uint32_t pk[kDwTile / 2];
 #pragma unroll
           for (int e = 0; e < kDwTile / 2; e += 2) {
             float x0, x1, x2, x3;
@@ -693,31 +734,26 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             pk[e] = ptx::pack2<kBf16>(p0, p1);
             pk[e + 1] = ptx::pack2<kBf16>(p2, p3);
           }
-          float s0, s1, s2, s3;
-          ptx::f2_unpack(acc0, s0, s1);
-          ptx::f2_unpack(acc1, s2, s3);
-          l += (s0 + s1) + (s2 + s3);
-        }
-        // P_w and O_w are in use until the group's previous product is done
-        if (it > 0) {
-          ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSiteDwPvDone);
-          ++pvcnt;
-          __syncwarp();
-          ptx::tc_fence_after();
-        }
-        if (rescale) {
-#pragma unroll 1
-          for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t orr[32];
-            ptx::tmem_ld32(tO0 + lane_off + w * D + q4 * 32, orr);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-            ptx::tmem_st32(tO0 + lane_off + w * D + q4 * 32, orr);
+          {
+            float s0, s1, s2, s3;
+            ptx::f2_unpack(acc0, s0, s1);
+            ptx::f2_unpack(acc1, s2, s3);
+            l += (s0 + s1) + (s2 + s3);
           }
-          ptx::tmem_wait_st();
-        }
-        if (has) {
+          wait_pv();
+          if (rescale) {
+#pragma unroll 1
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              uint32_t orr[32];
+              ptx::tmem_ld32(tO0 + lane_off + w * D + q4 * 32, orr);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+              ptx::tmem_st32(tO0 + lane_off + w * D + q4 * 32, orr);
+            }
+            ptx::tmem_wait_st();
+          }
           uint8_t* prow = sgen + L::kP + w * L::kPTile + t * 128;
 #pragma unroll
           for (int k = 0; k < kDwTile / 8; ++k)
@@ -831,28 +867,48 @@ __global__ void __launch_bounds__(D)
   const int row = blockIdx.x % p.R, head = blockIdx.x / p.R;
   const int b = head / p.Hk, rb = row / p.row_span;
   const int c = threadIdx.x;
-  long long before, total;
+  int before, total;
   dec_tile_sums(p, b, before, total);
+  const DecDeal deal = dec_deal(total, p.grid);
   const int nt = dec_tiles(dec_span_of(p, b));
-  const long long s = before + static_cast<long long>((head - b * p.Hk) * p.row_blocks + rb) * nt;
-  const long long e = s + nt;
-  int cta = static_cast<int>(s * p.grid / total);       // the run that holds tile s
-  while (cta > 0 && dec_run_start(total, cta, p.grid) > s) --cta;
-  while (dec_run_start(total, cta + 1, p.grid) <= s) ++cta;
+  const int s = before + ((head - b * p.Hk) * p.row_blocks + rb) * nt;
+  const int first = dec_run_of(deal, s), last = dec_run_of(deal, s + nt - 1);
   ptx::griddep_wait();   // the parts are complete, and this grid ends after the main one
-  if (dec_run_start(total, cta + 1, p.grid) >= e) return;
+  if (first == last) return;
+  // the first run's part is its last piece unless the run starts with the
+  // unit; every later run starts with it
+  const int first_slot = 2 * first + (dec_run_start(deal, first) >= s ? 0 : 1);
+  const size_t srow = row - rb * p.row_span;
+  auto part_of = [&](int run) {
+    return static_cast<size_t>(run == first ? first_slot : 2 * run) * p.slot_rows + srow;
+  };
   float nm = INFINITY, l = 0.f, acc = 0.f;
-  for (long long st; (st = dec_run_start(total, cta, p.grid)) < e; ++cta) {
-    if (dec_run_start(total, cta + 1, p.grid) == st) continue;   // an empty run
-    const size_t part = (2ull * cta + (st >= s ? 0 : 1)) * p.slot_rows + (row - rb * p.row_span);
-    const float2 ml = p.part_ml[part];
-    const float x = p.part_o[part * D + c];
-    if (!(ml.y > 0.f)) continue;
-    const float m = fminf(nm, ml.x);
-    const float fo = nm == INFINITY ? 0.f : ptx::ex2(m - nm), fn = ptx::ex2(m - ml.x);
-    acc = fmaf(fn, x, fo * acc);
-    l = fmaf(fn, ml.y, fo * l);
+  for (int run0 = first; run0 <= last; run0 += kDwCombine) {
+    // a batch of parts, their loads in flight together
+    float2 ml[kDwCombine];
+    float x[kDwCombine];
+#pragma unroll
+    for (int i = 0; i < kDwCombine; ++i) {
+      const size_t part = part_of(min(run0 + i, last));
+      ml[i] = p.part_ml[part];
+      x[i] = p.part_o[part * D + c];
+      if (run0 + i > last) ml[i].y = 0.f;
+    }
+    float m = nm;
+#pragma unroll
+    for (int i = 0; i < kDwCombine; ++i)
+      if (ml[i].y > 0.f) m = fminf(m, ml[i].x);
+    const float fo = nm == INFINITY ? 0.f : ptx::ex2(m - nm);
+    acc *= fo;
+    l *= fo;
     nm = m;
+#pragma unroll
+    for (int i = 0; i < kDwCombine; ++i)
+      if (ml[i].y > 0.f) {
+        const float f = ptx::ex2(m - ml[i].x);
+        acc = fmaf(f, x[i], acc);
+        l = fmaf(f, ml[i].y, l);
+      }
   }
   const size_t out = static_cast<size_t>(head) * p.R + row;
   const uint32_t pk = ptx::pack2<kBf16>(l > 0.f ? acc / l : 0.f, 0.f);

@@ -178,13 +178,17 @@ int main() {
       return 1;
     }
   }
-  for (long long total : {1ll, 7ll, 151ll, 152ll, 153ll, 100000ll, 40000000000ll})
+  for (int total : {1, 7, 151, 152, 153, 100000, 2000000000})
     for (int grid : {1, 7, 152}) {
-      long long prev = 0;
-      for (int i = 0; i <= grid; ++i) {
-        const long long st = fa::dec_run_start(total, i, grid);
-        if (st < prev || (i == 0 && st) || (i == grid && st != total)) BAD("run %lld %d", total, i);
-        if (i && st - prev > total / grid + 1) BAD("uneven run");
+      const fa::DecDeal d = fa::dec_deal(total, grid);
+      if (d.runs < 1 || d.runs > grid || d.runs > total) BAD("runs %d %d", total, grid);
+      int prev = 0;
+      for (int i = 0; i <= d.runs; ++i) {
+        const int st = fa::dec_run_start(d, i);
+        if ((i == 0 && st) || (i == d.runs && st != total)) BAD("run %d %d", total, i);
+        if (i && (st <= prev || st - prev > d.per + 1)) BAD("uneven run");
+        if (i && (fa::dec_run_of(d, prev) != i - 1 || fa::dec_run_of(d, st - 1) != i - 1))
+          BAD("run of tile %d", prev);
         prev = st;
       }
     }
