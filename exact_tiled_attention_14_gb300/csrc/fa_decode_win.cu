@@ -18,10 +18,13 @@ using namespace fa::host;
 namespace fa {
 namespace {
 
-template <int D, bool kBf16, int kTiles>
+// Copies of the rows in the query tile (see the kernel's header).
+int copies_of(int R) { return R <= kDwTile / 4 ? 4 : (R <= kDwTile / 2 ? 2 : 1); }
+
+template <int D, bool kBf16, int kTiles, int kCopies>
 cudaError_t launch_main(const DecWinParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};   // devices on which the smem limit was raised
-  auto kernel = fa_decode_win_kernel<D, kBf16, kTiles>;
+  auto kernel = fa_decode_win_kernel<D, kBf16, kTiles, kCopies>;
   constexpr int kAlloc = DwLayout<D, kTiles>::kAlloc;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -38,14 +41,18 @@ cudaError_t launch_main(const DecWinParams& p, cudaStream_t stream) {
 
 template <int D, bool kBf16>
 cudaError_t launch_variant(const DecWinParams& p, cudaStream_t stream) {
-  cudaError_t e = p.row_span == kDwTile ? launch_main<D, kBf16, 1>(p, stream)
-                                        : launch_main<D, kBf16, 2>(p, stream);
+  const int copies = copies_of(p.R);
+  cudaError_t e = p.row_span > kDwTile ? launch_main<D, kBf16, 2, 1>(p, stream)
+                  : copies == 4        ? launch_main<D, kBf16, 1, 4>(p, stream)
+                  : copies == 2        ? launch_main<D, kBf16, 1, 2>(p, stream)
+                                       : launch_main<D, kBf16, 1, 1>(p, stream);
   if (e != cudaSuccess) return e;
   // Programmatic dependent launch: the combine grid is set up while the main
   // kernel runs its last CTAs, and waits on the device for the parts.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hk * p.R));
-  cfg.blockDim = dim3(D);
+  const int rows = kDwCombineThreads / (D / 4);   // rows a block
+  cfg.gridDim = dim3(p.grid, (p.slot_rows + rows - 1) / rows);
+  cfg.blockDim = dim3(kDwCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -72,10 +79,10 @@ int check_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int max_q) {
 }
 
 // Grid (one CTA per SM, or one per key tile where there are fewer) and the
-// workspace: two parts per CTA, each the rows of a unit.
+// workspace: two parts per CTA, each the rows of a unit, and the run table.
 struct Plan {
   int row_span, row_blocks, slot_rows, grid;
-  size_t o_bytes, bytes;
+  size_t o_bytes, ml_bytes, bytes;
 };
 Plan make_plan(int B, int H, int Hk, int Nq, int Nk, int d, int sms) {
   Plan pl{};
@@ -89,7 +96,8 @@ Plan make_plan(int B, int H, int Hk, int Nq, int Nk, int d, int sms) {
   pl.grid = static_cast<int>(std::min<long long>(units * tiles, sms));
   const size_t rows = 2 * static_cast<size_t>(pl.grid) * pl.slot_rows;
   pl.o_bytes = (rows * d * sizeof(float) + 255) / 256 * 256;
-  pl.bytes = pl.o_bytes + (rows * sizeof(float2) + 255) / 256 * 256;
+  pl.ml_bytes = (rows * sizeof(float2) + 255) / 256 * 256;
+  pl.bytes = pl.o_bytes + pl.ml_bytes + (pl.grid * sizeof(int4) + 255) / 256 * 256;
   return pl;
 }
 
@@ -128,7 +136,8 @@ int decode(const void* q, const void* k, const void* v, void* o, float* lse, int
   const void* kp = has_k ? k : q;
   const void* vp = has_k ? v : q;
   const int kh = has_k ? bhk : 1, kn = has_k ? Nk : 1;
-  if (!make_tmap(&p.tm_q, q, bhk, R, d, bf16) || !make_tmap(&p.tm_k, kp, kh, kn, d, bf16) ||
+  const int q_box = R <= kDwTile ? kDwTile / copies_of(R) : kDwTile;
+  if (!make_tmap(&p.tm_q, q, bhk, R, d, bf16, q_box) || !make_tmap(&p.tm_k, kp, kh, kn, d, bf16) ||
       !make_tmap(&p.tm_v, vp, kh, kn, d, bf16) ||
       !make_tmap(&p.tm_k16, kp, kh, kn, d, bf16, kDwBox) ||
       !make_tmap(&p.tm_v16, vp, kh, kn, d, bf16, kDwBox))
@@ -137,6 +146,7 @@ int decode(const void* q, const void* k, const void* v, void* o, float* lse, int
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + pl.o_bytes);
+  p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + pl.o_bytes + pl.ml_bytes);
   p.status = info->status;
   const unsigned long long wd = g_watchdog_ns.load();
   p.watchdog_cycles = (wd ? wd : kDefaultWatchdogNs) * 21ull / 10ull;

@@ -27,11 +27,20 @@
 // a few sinks cost one box, not a tile.  Only boxes that hold a needed key
 // are loaded.
 //
-// One CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8
-// issues S = Q K^T, warp 9 the TMA loads, warp 10 O += P V.  With up to 128
-// rows (kTiles = 1) the groups take alternate key tiles, each with its own
-// S, P, O and statistics, and are merged at the end of the unit; with more
-// (kTiles = 2) each group owns a row tile and both take every key tile.
+// One CTA: warps 0-3 and 4-7 are two softmax groups, warp 8 issues S = Q K^T,
+// warp 9 the TMA loads, warp 10 O += P V.  With up to 128 rows (kTiles = 1)
+// the groups take alternate key tiles, each with its own S, P, O and
+// statistics, and are merged at the end of the unit; with more (kTiles = 2)
+// each group owns a row tile and both take every key tile.
+//
+// Copies.  A thread works on the lane its warp owns, and one row's 128 scores
+// of a tile take a thread about 2000 cycles from S to P, which two groups
+// cannot hide behind the loads at d = 64 (0.9 us a tile of 32 KB against 0.73
+// at the HBM rate, with 1 row or 128).  So with few rows the query tile holds
+// kCopies copies of them (4 up to 32 rows, 2 up to 64), S comes out once per
+// copy, and copy g weighs only keys g * 128 / kCopies ...: its rows of P are
+// zero elsewhere, and its O is the part of those keys.  The copies are parts
+// like the groups' and are merged with them.
 #pragma once
 
 #include <cuda.h>
@@ -48,7 +57,7 @@ constexpr int kDwSWarp = 8, kDwLoadWarp = 9, kDwPvWarp = 10;
 constexpr uint32_t kDwSoftmaxRegs = 208, kDwIssueRegs = 88;
 static_assert(2 * 128 * kDwSoftmaxRegs + 128 * kDwIssueRegs <= 168 * kDwThreads, "register split");
 constexpr float kDwTau = 8.0f;        // lazy-rescale threshold, log2 units
-constexpr int kDwCombine = 10;        // parts of a row that are loaded together
+constexpr int kDwCombine = 8;         // parts of a row that are loaded together
 constexpr int kDwMaxTree = 64;        // drafted tokens (bits of a row's mask)
 constexpr int kDwMaxTokens = 16;      // new tokens of a window call
 
@@ -58,8 +67,8 @@ enum DwWaitSite : uint32_t {
 };
 
 struct DecWinParams {
-  CUtensorMap tm_q;        // [B * Hk, R, d], boxes of 128 rows x 64 columns, 128-byte swizzle
-  CUtensorMap tm_k;        // [B * Hk, Nk, d], the same boxes
+  CUtensorMap tm_q;        // [B * Hk, R, d], boxes of 128 / kCopies rows x 64 columns, 128-byte swizzle
+  CUtensorMap tm_k;        // [B * Hk, Nk, d], boxes of 128 rows
   CUtensorMap tm_v;
   CUtensorMap tm_k16;      // the same tensors in boxes of 16 rows
   CUtensorMap tm_v16;
@@ -67,6 +76,8 @@ struct DecWinParams {
   float* lse;              // [B * Hk, R]
   float* part_o;           // [2 * grid, slot_rows, d] unnormalised parts
   float2* part_ml;         // [2 * grid, slot_rows] (-m in log2 units, l)
+  int4* cut;               // [grid] the cut unit that starts in the run: (head, row block,
+                           // slot of its first part, run of its last part), run -1: none
   unsigned int* status;
   unsigned long long watchdog_cycles;
   const int* seqlens;      // [B] or NULL: every count is len_all
@@ -203,26 +214,36 @@ __device__ __forceinline__ bool dec_next(const DecWinParams& p, DecCursor& c, De
   return true;
 }
 
-// Shared memory: kTiles query tiles, a ring of K and V tiles, two P tiles.
+// Shared memory: query tiles (two buffers, so a unit's queries load while the
+// previous unit runs; one at d = 128 with two row tiles, where there is no
+// room) and a ring of K and V tiles.  TMEM: S of the two groups in columns
+// 0-127 and 128-255, their O from 256 on, and P (16 bit, 64 columns a group):
+// behind O at d = 64; at d = 128, where S and O fill all 512 columns, over the
+// S it was formed from, and the group's next S waits for the product that
+// reads P.
 template <int D, int kTiles>
 struct DwLayout {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = kDwTile * D * 2;
   static constexpr int kChunkBytes = kDwTile * 128;
-  static constexpr int kPTile = kDwTile * kDwTile * 2;
-  static constexpr int kStages = (D == 128) ? (kTiles == 2 ? 3 : 4) : 8;
+  static constexpr bool kOwnP = D == 64;
+  static constexpr int kQBufs = (D == 128 && kTiles == 2) ? 1 : 2;
+  static constexpr int kStages = (D == 128) ? 5 : (kTiles == 2 ? 10 : 12);
   static constexpr int kQ = 0;
-  static constexpr int kKV = kQ + kTiles * kTile;
-  static constexpr int kP = kKV + kStages * kTile;
-  static constexpr int kBar = kP + 2 * kPTile;
-  static constexpr int bQFull = 0, bQEmpty = 1, bKvFull = 2, bKvEmpty = bKvFull + kStages,
-                       bSFull = bKvEmpty + kStages, bSFree = bSFull + 2, bPFull = bSFree + 2,
-                       bPvDone = bPFull + 2, bOFree = bPvDone + 2, bFinalS = bOFree + 2,
-                       bFinalPv = bFinalS + 1, kNumBars = bFinalPv + 1;
-  static constexpr int kMisc = kBar + 8 * kNumBars;           // tmem base, abort flag, cursor
+  static constexpr int kKV = kQ + kQBufs * kTiles * kTile;
+  static constexpr int kBar = kKV + kStages * kTile;
+  static constexpr int bQFull = 0, bQEmpty = kQBufs, bKvFull = 2 * kQBufs,
+                       bKvEmpty = bKvFull + kStages, bSFull = bKvEmpty + kStages,
+                       bSFree = bSFull + 2, bPFull = bSFree + 2, bPvDone = bPFull + 2,
+                       bOFree = bPvDone + 2, bFinalS = bOFree + 2, bFinalPv = bFinalS + 1,
+                       kNumBars = bFinalPv + 1;
+  static constexpr int kMisc = kBar + 8 * kNumBars;   // tmem base, abort flag, cursor, deal
   static constexpr int kBytes = kMisc + 48;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget");
+  static constexpr uint32_t s_col(int w) { return 128u * w; }
+  static constexpr uint32_t o_col(int w) { return 256u + static_cast<uint32_t>(D) * w; }
+  static constexpr uint32_t p_col(int w) { return kOwnP ? 256u + 2u * D + 64u * w : 128u * w; }
 };
 
 // Bits [a, b) of 128 as four words.
@@ -318,10 +339,12 @@ __host__ __device__ __forceinline__ bool dec_visible(const DecSpan& s, const Dec
   return false;
 }
 
-template <int D, bool kBf16, int kTiles>
+template <int D, bool kBf16, int kTiles, int kCopies>
 __global__ void __launch_bounds__(kDwThreads, 1)
     fa_decode_win_kernel(const __grid_constant__ DecWinParams p) {
   using L = DwLayout<D, kTiles>;
+  constexpr int kRows = kDwTile / kCopies;     // rows of a copy
+  static_assert(kTiles == 1 || kCopies == 1, "copies of one row tile");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -330,7 +353,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
   uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
-  int* cursor_s = reinterpret_cast<int*>(sgen + L::kMisc + 8);   // batch, unit, tile, tiles left
+  // batch, unit, tile, tiles left, and the deal's per, extra, runs
+  int* cursor_s = reinterpret_cast<int*>(sgen + L::kMisc + 8);
 
   // the combine kernel may be scheduled once every CTA has started (it waits
   // for this grid to complete before reading the parts)
@@ -341,8 +365,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   }
   if (threadIdx.x == kDwLoadWarp * 32) {
     *abort_flag = 0;
-    ptx::mbar_init(bar(L::bQFull), 1);
-    ptx::mbar_init(bar(L::bQEmpty), 1);
+    for (int i = 0; i < L::kQBufs; ++i) {
+      ptx::mbar_init(bar(L::bQFull + i), 1);
+      // the last S has read the buffer, and (kTiles == 1) every softmax
+      // thread is done with it as the scratch of the unit's merge
+      ptx::mbar_init(bar(L::bQEmpty + i), kTiles == 1 ? 257 : 1);
+    }
     for (int s = 0; s < L::kStages; ++s) {
       ptx::mbar_init(bar(L::bKvFull + s), 1);
       ptx::mbar_init(bar(L::bKvEmpty + s), 1);
@@ -404,7 +432,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         }
       }
     }
-    if (lane == 0) cursor_s[3] = left;
+    if (lane == 0) {
+      cursor_s[3] = left;
+      cursor_s[4] = deal.per;
+      cursor_s[5] = deal.extra;
+      cursor_s[6] = deal.runs;
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -422,7 +455,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   auto takes = [&](const DecPiece& x, int w, int j) {
     return kTiles == 1 ? (j & 1) == w : rows_of(x, w) > 0;
   };
-  const uint32_t tS0 = tmem_base, tO0 = tmem_base + 256;
 
   if (warp >= 8) {
     ptx::setmaxnreg_dec<kDwIssueRegs>();
@@ -465,17 +497,24 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             ++loads;
           };
           load_kv(false, 0);
-          if (pieces > 0)
-            alive = alive && ptx::wait_bounded(bar(L::bQEmpty), (pieces - 1) & 1, wd, kSiteDwQEmpty);
+          const uint32_t qb = pieces % L::kQBufs, quse = pieces / L::kQBufs;
+          if (quse > 0)
+            alive = alive && ptx::wait_bounded(bar(L::bQEmpty + qb), (quse - 1) & 1, wd,
+                                               kSiteDwQEmpty);
           if (!alive) break;
           {
-            const int nq = kTiles == 2 && rows_of(pc, 1) > 0 ? 2 : 1;
+            // the rows of each row tile, or every copy of them
+            const int nq = kTiles == 2 ? (rows_of(pc, 1) > 0 ? 2 : 1) : kCopies;
             const int row0 = kTiles * (pc.unit % p.row_blocks) * kDwTile;
-            ptx::mbar_arrive_expect_tx(bar(L::bQFull), nq * L::kTile);
+            const uint32_t dst = sbase + L::kQ + qb * kTiles * L::kTile;
+            ptx::mbar_arrive_expect_tx(bar(L::bQFull + qb),
+                                       kTiles == 2 ? nq * L::kTile : L::kTile);
             for (int w = 0; w < nq; ++w)
               for (int c = 0; c < L::kChunks; ++c)
-                ptx::tma_load_3d(sbase + L::kQ + w * L::kTile + c * L::kChunkBytes, &p.tm_q,
-                                 bar(L::bQFull), c * 64, row0 + w * kDwTile, head);
+                ptx::tma_load_3d(dst + (kTiles == 2 ? w * L::kTile : w * kRows * 128) +
+                                     c * L::kChunkBytes,
+                                 &p.tm_q, bar(L::bQFull + qb), c * 64,
+                                 kTiles == 2 ? row0 + w * kDwTile : row0, head);
             ++pieces;
           }
           for (int j = 0; alive && j < pc.n; ++j) {
@@ -487,7 +526,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         const unsigned long long drain = 200000000ull;
         for (uint32_t l = loads > (uint32_t)L::kStages ? loads - L::kStages : 0; l < loads; ++l)
           ptx::wait_drain(bar(L::bKvFull + l % L::kStages), (l / L::kStages) & 1, drain);
-        if (pieces > 0) ptx::wait_drain(bar(L::bQFull), (pieces - 1) & 1, drain);
+        for (uint32_t i = pieces > (uint32_t)L::kQBufs ? pieces - L::kQBufs : 0; i < pieces; ++i)
+          ptx::wait_drain(bar(L::bQFull + i % L::kQBufs), (i / L::kQBufs) & 1, drain);
       }
       __syncwarp();
     } else if (warp == kDwSWarp) {
@@ -499,7 +539,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         uint32_t base = 0, pieces = 0, sc[2] = {0, 0};
         bool alive = true, issued = false;
         while (dec_next(p, cu, pc)) {
-          alive = alive && ptx::wait_bounded(bar(L::bQFull), pieces & 1, wd, kSiteDwQFull);
+          const uint32_t qb = pieces % L::kQBufs;
+          alive = alive && ptx::wait_bounded(bar(L::bQFull + qb), (pieces / L::kQBufs) & 1, wd,
+                                             kSiteDwQFull);
           for (int j = 0; j < pc.n; ++j) {
             const uint32_t pos = base + (j == 0 ? 0u : 2u * j - 1u), slot = pos % L::kStages;
             alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), (pos / L::kStages) & 1, wd,
@@ -508,19 +550,20 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               if (!takes(pc, w, j)) continue;
-              if (sc[w] > 0)   // the softmax has read the previous S of this group
-                alive = alive && ptx::wait_bounded(bar(L::bSFree + w), (sc[w] - 1) & 1, wd,
-                                                   kSiteDwSFree);
+              if (sc[w] > 0)   // the softmax has read this group's previous S (over
+                               // which, at d = 128, P was written and must be read too)
+                alive = alive && ptx::wait_bounded(bar((L::kOwnP ? L::bSFree : L::bPvDone) + w),
+                                                   (sc[w] - 1) & 1, wd, kSiteDwSFree);
               ++sc[w];
               ptx::tc_fence_after();
               if (!alive) continue;
-              const uint32_t a = q_lo + (kTiles == 2 ? w : 0) * (L::kTile >> 4);
+              const uint32_t a = q_lo + (qb * kTiles + (kTiles == 2 ? w : 0)) * (L::kTile >> 4);
               const uint32_t b = k_lo + slot * (L::kTile >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off =
                     static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-                ptx::mma_ss(tS0 + w * 128, ptx::desc_sw128(a + off), ptx::desc_sw128(b + off), idesc,
+                ptx::mma_ss(tmem_base + L::s_col(w), ptx::desc_sw128(a + off), ptx::desc_sw128(b + off), idesc,
                             kk > 0);
               }
               ptx::mma_commit(bar(L::bSFull + w));
@@ -528,7 +571,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             }
             if (alive) {
               ptx::mma_commit(bar(L::bKvEmpty + slot));
-              if (j + 1 == pc.n) ptx::mma_commit(bar(L::bQEmpty));
+              if (j + 1 == pc.n) ptx::mma_commit(bar(L::bQEmpty + qb));
             }
           }
           base += 2u * pc.n;
@@ -549,10 +592,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // the warp joins it afterwards: a lane that polled on its own could miss
       // a phase that lane 0's progress lets pass twice.
       constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, D, kBf16 ? 1 : 0, 1);
-      const uint32_t p_lo = ptx::desc_lo(sbase + L::kP, 16);
       const uint32_t v_lo = ptx::desc_lo(sbase + L::kKV, L::kChunkBytes);
       uint32_t base = 0, pcn[2] = {0, 0}, units[2] = {0, 0};
-      bool alive = true, issued = false;
+      bool alive = true, issued = false, cut_here = false;
       while (dec_next(p, cu, pc)) {
         int done[2] = {0, 0};
         // a tree's keys below `from` are before the window of its shallowest
@@ -614,13 +656,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             ptx::tc_fence_after();
             if (alive) {
 #pragma unroll
-              for (int kk = 0; kk < kDwTile / 16; ++kk) {
-                const uint32_t off =
-                    static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-                ptx::mma_ss(tO0 + w * D, ptx::desc_sw128(p_lo + w * (L::kPTile >> 4) + off),
+              for (int kk = 0; kk < kDwTile / 16; ++kk)
+                ptx::mma_ts(tmem_base + L::o_col(w), tmem_base + L::p_col(w) + kk * 8,
                             ptx::desc_sw128(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4)),
                             idesc, (kk > 0 || !first) ? 1u : 0u);
-              }
               ptx::mma_commit(bar(L::bPvDone + w));
               issued = true;
             }
@@ -632,7 +671,17 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         units[0] += kTiles == 1 || done[0] > 0;
         units[1] += kTiles == 1 || done[1] > 0;
         base += 2u * pc.n;
+        // a unit that starts here and ends in a later run: its parts' place
+        if (pc.t0 == 0 && !pc.whole && lane == 0) {
+          const DecDeal deal{cursor_s[4], cursor_s[5], cursor_s[6]};
+          const int end_tile = dec_run_start(deal, blockIdx.x + 1) - pc.n + dec_tiles(pc.s) - 1;
+          p.cut[blockIdx.x] = make_int4(pc.b * p.Hk + pc.unit / p.row_blocks,
+                                        pc.unit % p.row_blocks, 2 * blockIdx.x + pc.slot,
+                                        dec_run_of(deal, end_tile));
+          cut_here = true;
+        }
       }
+      if (lane == 0 && !cut_here) p.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
       if (issued) {   // lane 0 only
         ptx::mma_commit(bar(L::bFinalPv));
         ptx::wait_drain(bar(L::bFinalPv), 0, 200000000ull);
@@ -642,30 +691,39 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   } else {
     ptx::setmaxnreg_inc<kDwSoftmaxRegs>();
     // ============================================================ softmax
+    constexpr int kCols = kDwTile / kCopies;     // key columns of a thread
     const int w = warp >> 2, t = threadIdx.x & 127;
+    const int seg = t / kRows, r = t % kRows;    // copy (and its keys), row of the row tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tS0 + lane_off + w * 128;
+    const uint32_t tS = tmem_base + lane_off + L::s_col(w) + seg * kCols;
+    const uint32_t tP = tmem_base + lane_off + L::p_col(w);
+    const uint32_t tO = tmem_base + lane_off + L::o_col(w);
     const float c = p.scale_log2;
-    // statistics of group g's rows at the end of a piece, in its idle P tile
-    auto ml_s = [&](int g) { return reinterpret_cast<float2*>(sgen + L::kP + g * L::kPTile); };
-    uint32_t scnt = 0, pvcnt = 0;
+    constexpr uint32_t kZero[16] = {};
+    if constexpr (kCopies > 1 && L::kOwnP) {     // P outside the copy's keys stays zero
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ptx::tmem_st16(tP + 16 * k, kZero);
+      ptx::tmem_wait_st();
+    }
+    uint32_t scnt = 0, pieces = 0;
     while (dec_next(p, cu, pc)) {
       const int nrows = rows_of(pc, w);
+      const uint32_t qb = pieces++ % L::kQBufs;
       if (kTiles == 2 && nrows == 0) continue;
-      const bool has = (warp & 3) * 32 < nrows;     // this warp holds rows
-      const int row = (kTiles * (pc.unit % p.row_blocks) + (kTiles == 2 ? w : 0)) * kDwTile + t;
+      const bool has = (kCopies > 1 ? (warp & 3) * 32 % kRows : (warp & 3) * 32) < nrows;
+      const int row = (kTiles * (pc.unit % p.row_blocks) + (kTiles == 2 ? w : 0)) * kDwTile + r;
       const DecRow me =
           dec_row(p.tree ? p.tree + static_cast<size_t>(pc.b) * p.Nq : nullptr,
                   min(row, p.R - 1) % p.Nq, p.Nq, pc.s.len, p.win, p.sinks);
       float m_ref = -INFINITY, neg_m = 0.f, l = 0.f;
-      int it = 0;                                   // tiles of this group so far
+      int it = 0;                                // tiles of this group so far
       for (int j = 0; j < pc.n; ++j) {
         if (!takes(pc, w, j)) continue;
         // P_w and O_w are in use until the group's previous product is done
+        // (at d = 128 this S could only come after it)
         auto wait_pv = [&]() {
-          if (it > 0) {
-            ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSiteDwPvDone);
-            ++pvcnt;
+          if (L::kOwnP && it > 0) {
+            ptx::wait_bounded(bar(L::bPvDone + w), (scnt - 2) & 1, wd, kSiteDwPvDone);
             __syncwarp();
             ptx::tc_fence_after();
           }
@@ -673,33 +731,40 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         if (!has) {   // a warp without rows only keeps the order
           ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
           ++scnt;
-          ptx::mbar_arrive(bar(L::bSFree + w));
+          if (L::kOwnP) ptx::mbar_arrive(bar(L::bSFree + w));
           wait_pv();
         } else {
           uint32_t vis[4];
           const bool all = dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), me, p.tree != nullptr, p.win,
                                        p.sinks, vis);
+          if constexpr (kCopies == 4) vis[0] = seg < 2 ? (seg ? vis[1] : vis[0]) : (seg == 2 ? vis[2] : vis[3]);
+          if constexpr (kCopies == 2) {
+            vis[0] = seg ? vis[2] : vis[0];
+            vis[1] = seg ? vis[3] : vis[1];
+          }
           ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
           ++scnt;
           __syncwarp();
           ptx::tc_fence_after();
-          uint32_t sr[kDwTile];
+          uint32_t sr[kCols];
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld32(tS + q4 * 32, sr + q4 * 32);
+          for (int q4 = 0; q4 < kCols / 32; ++q4) ptx::tmem_ld32(tS + q4 * 32, sr + q4 * 32);
           ptx::tmem_wait_ld();
-          float sv[kDwTile];
+          float sv[kCols];
 #pragma unroll
-          for (int e = 0; e < kDwTile; ++e) sv[e] = __uint_as_float(sr[e]);
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
+          for (int e = 0; e < kCols; ++e) sv[e] = __uint_as_float(sr[e]);
+          if (L::kOwnP) {
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
+          }
           if (!all) {
 #pragma unroll
-            for (int e = 0; e < kDwTile; ++e)
+            for (int e = 0; e < kCols; ++e)
               if (!((vis[e >> 5] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
           }
           float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < kDwTile; e += 8) {
+          for (int e = 0; e < kCols; e += 8) {
             a0 = ptx::max3(a0, sv[e + 0], sv[e + 1]);
             a1 = ptx::max3(a1, sv[e + 2], sv[e + 3]);
             a2 = ptx::max3(a2, sv[e + 4], sv[e + 5]);
@@ -720,9 +785,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           const bool rescale = it > 0 && __any_sync(0xffffffffu, grow);
           const uint64_t c2 = ptx::f2_pack(c, c), nm2 = ptx::f2_pack(neg_m, neg_m);
           uint64_t acc0 = ptx::f2_pack(0.f, 0.f), acc1 = acc0;
-          uint32_t pk[kDwTile / 2];
+          uint32_t pk[kCols / 2];
 #pragma unroll
-          for (int e = 0; e < kDwTile / 2; e += 2) {
+          for (int e = 0; e < kCols / 2; e += 2) {
             float x0, x1, x2, x3;
             ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(sv[2 * e + 0], sv[2 * e + 1]), c2, nm2), x0, x1);
             ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(sv[2 * e + 2], sv[2 * e + 3]), c2, nm2), x2, x3);
@@ -745,21 +810,36 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 #pragma unroll 1
             for (int q4 = 0; q4 < D / 32; ++q4) {
               uint32_t orr[32];
-              ptx::tmem_ld32(tO0 + lane_off + w * D + q4 * 32, orr);
+              ptx::tmem_ld32(tO + q4 * 32, orr);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-              ptx::tmem_st32(tO0 + lane_off + w * D + q4 * 32, orr);
+              ptx::tmem_st32(tO + q4 * 32, orr);
             }
-            ptx::tmem_wait_st();
           }
-          uint8_t* prow = sgen + L::kP + w * L::kPTile + t * 128;
+          if constexpr (kCopies == 1) {
+            ptx::tmem_st32(tP, pk);
+            ptx::tmem_st32(tP + 32, pk + 32);
+          } else {
+            // this copy's keys; the others' columns hold zeros (at d = 128
+            // the scores of this lane, until they are overwritten here)
 #pragma unroll
-          for (int k = 0; k < kDwTile / 8; ++k)
-            *reinterpret_cast<uint4*>(prow + (k >> 3) * L::kChunkBytes + (((k & 7) ^ (t & 7)) << 4)) =
-                make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-          ptx::fence_proxy_async_smem();
+            for (int k = 0; k < kCopies; ++k) {
+              if (k == seg) {   // the same for the whole warp
+                if constexpr (kCopies == 2) {
+                  ptx::tmem_st32(tP + 32 * k, pk);
+                } else {
+                  ptx::tmem_st16(tP + 16 * k, pk);
+                }
+              } else if (!L::kOwnP) {
+#pragma unroll
+                for (int i = 0; i < 4 / kCopies; ++i)
+                  ptx::tmem_st16(tP + (64 / kCopies) * k + 16 * i, kZero);
+              }
+            }
+          }
+          ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(L::bPFull + w));
@@ -767,81 +847,176 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       }
       // ---- end of the piece: the group's last product
       if (it > 0) {
-        ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSiteDwPvDone);
-        ++pvcnt;
+        ptx::wait_bounded(bar(L::bPvDone + w), (scnt - 1) & 1, wd, kSiteDwPvDone);
         __syncwarp();
       }
       ptx::tc_fence_after();
       const size_t head = static_cast<size_t>(pc.b) * p.Hk + pc.unit / p.row_blocks;
-      const size_t out_row = head * p.R + row;
       const size_t slot = 2ull * blockIdx.x + pc.slot;
-      const int srow = kTiles == 2 ? w * kDwTile + t : t;
-      float f0 = 1.f, f1 = 0.f;
-      int c0 = 0, c1 = D;                            // columns this thread writes
       if constexpr (kTiles == 1) {
-        // merge the two groups' parts of the keys; group w writes half w of
-        // the columns (both groups' warps reach the same TMEM lanes)
-        ml_s(w)[t] = make_float2(neg_m, l);
+        // Merge the parts of a row, two groups times kCopies, to their largest
+        // maximum.  The statistics go through the unit's query buffer, which
+        // S no longer reads; group w then handles half w of the columns of
+        // both groups' O (both groups' warps reach the same TMEM lanes).
+        uint8_t* scratch = sgen + L::kQ + qb * L::kTile;
+        float2* ml_s = reinterpret_cast<float2*>(scratch);
+        ptx::named_bar_sync(1, 256);             // both groups have their last S
+        ml_s[w * kDwTile + t] = make_float2(neg_m, l);
         ptx::tc_fence_before();
         ptx::named_bar_sync(1, 256);
         ptx::tc_fence_after();
-        const float2 o0 = ml_s(0)[t], o1 = ml_s(1)[t];
-        neg_m = o0.y > 0.f ? (o1.y > 0.f ? fminf(o0.x, o1.x) : o0.x) : (o1.y > 0.f ? o1.x : 0.f);
-        f0 = o0.y > 0.f ? ptx::ex2(neg_m - o0.x) : 0.f;
-        f1 = o1.y > 0.f ? ptx::ex2(neg_m - o1.x) : 0.f;
-        l = f0 * o0.y + f1 * o1.y;
-        c0 = w * (D / 2);
-        c1 = c0 + D / 2;
-      }
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
-      if (has) {
-#pragma unroll 1
-        for (int col = c0; col < c1; col += 32) {
-          uint32_t a[32];
-          ptx::tmem_ld32(tO0 + lane_off + (kTiles == 2 ? w * D : 0) + col, a);
-          ptx::tmem_wait_ld();
-          float x[32];
+        float nm = INFINITY, lt = 0.f;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = f0 > 0.f ? __uint_as_float(a[e]) * f0 : 0.f;
-          if (kTiles == 1 && pc.n > 1) {
-            ptx::tmem_ld32(tO0 + lane_off + D + col, a);
+        for (int g = 0; g < 2 * kCopies; ++g) {
+          const float2 x = ml_s[g * kRows + r];
+          if (x.y > 0.f) nm = fminf(nm, x.x);
+        }
+#pragma unroll
+        for (int g = 0; g < 2 * kCopies; ++g) {
+          const float2 x = ml_s[g * kRows + r];
+          if (x.y > 0.f) lt = fmaf(ptx::ex2(nm - x.x), x.y, lt);
+        }
+        // this lane's parts
+        const float2 y0 = ml_s[t], y1 = ml_s[kDwTile + t];
+        // (a finished unit's are divided by l here)
+        const float inv = pc.whole && lt > 0.f ? 1.0f / lt : 1.f;
+        const float f0 = y0.y > 0.f ? ptx::ex2(nm - y0.x) * inv : 0.f;
+        const float f1 = y1.y > 0.f ? ptx::ex2(nm - y1.x) * inv : 0.f;
+        const size_t out_row = head * p.R + row;
+        const bool two = pc.n > 1;               // the second group had a tile
+        // 16 columns of this lane, both groups' parts added
+        auto load16 = [&](int col, float* x) {
+          uint32_t a[16];
+          ptx::tmem_ld16(tmem_base + lane_off + L::o_col(0) + col, a);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = f0 > 0.f ? __uint_as_float(a[e]) * f0 : 0.f;
+          if (two) {
+            ptx::tmem_ld16(tmem_base + lane_off + L::o_col(1) + col, a);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               x[e] = f1 > 0.f ? fmaf(__uint_as_float(a[e]), f1, x[e]) : x[e];
           }
-          if (t < nrows) {
-            if (pc.whole) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + col);
+        };
+        if (r < nrows && seg == 0 && w == 0) {
+          if (pc.whole)
+            p.lse[out_row] = lt > 0.f ? (ptx::lg2(lt) - nm) * 0.693147180559945309f : -INFINITY;
+          else
+            p.part_ml[slot * p.slot_rows + r] = make_float2(lt > 0.f ? nm : 0.f, lt);
+        }
+        if constexpr (kCopies == 1) {
+          if (has) {
+#pragma unroll 1
+            for (int col = w * (D / 2); col < (w + 1) * (D / 2); col += 16) {
+              float x[16];
+              load16(col, x);
+              if (r < nrows) {
+                if (pc.whole) {
+                  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + col);
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                dst[v] = make_uint4(ptx::pack2<kBf16>(x[8 * v] * inv, x[8 * v + 1] * inv),
-                                    ptx::pack2<kBf16>(x[8 * v + 2] * inv, x[8 * v + 3] * inv),
-                                    ptx::pack2<kBf16>(x[8 * v + 4] * inv, x[8 * v + 5] * inv),
-                                    ptx::pack2<kBf16>(x[8 * v + 6] * inv, x[8 * v + 7] * inv));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.slot_rows + srow) * D + col);
+                  for (int v = 0; v < 2; ++v)
+                    dst[v] = make_uint4(ptx::pack2<kBf16>(x[8 * v], x[8 * v + 1]),
+                                        ptx::pack2<kBf16>(x[8 * v + 2], x[8 * v + 3]),
+                                        ptx::pack2<kBf16>(x[8 * v + 4], x[8 * v + 5]),
+                                        ptx::pack2<kBf16>(x[8 * v + 6], x[8 * v + 7]));
+                } else {
+                  float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.slot_rows + r) * D + col);
 #pragma unroll
-              for (int v = 0; v < 8; ++v)
-                dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+                  for (int v = 0; v < 4; ++v)
+                    dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+                }
+              }
+            }
+          }
+        } else {
+          // The copies' rows meet in the scratch, D / 2 columns at a time
+          // (D / 4 of each group's half): [lane][D / 2] floats, 16-byte pieces
+          // permuted by the lane so that lanes a row apart use other banks.
+          // Then every thread adds the copies of a few pieces and writes them.
+          constexpr int kPieces = D / 8;         // 16-byte pieces of a lane's row
+          float4* sc4 = reinterpret_cast<float4*>(scratch);
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            ptx::named_bar_sync(1, 256);         // the scratch's last use is over
+            if (has) {
+#pragma unroll
+              for (int q = 0; q < D / 64; ++q) {
+                float x[16];
+                load16(w * (D / 2) + pass * (D / 4) + q * 16, x);
+                if (r < nrows) {
+#pragma unroll
+                  for (int v = 0; v < 4; ++v)
+                    sc4[t * kPieces + ((w * (kPieces / 2) + q * 4 + v) ^ (t & 7))] =
+                        make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+                }
+              }
+            }
+            ptx::named_bar_sync(1, 256);
+            for (int i = threadIdx.x; i < nrows * kPieces; i += 256) {
+              const int rr = i / kPieces, v = i % kPieces;
+              float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int g = 0; g < kCopies; ++g) {
+                const int ln = g * kRows + rr;
+                const float4 x = sc4[ln * kPieces + (v ^ (ln & 7))];
+                sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+              }
+              const int half = v / (kPieces / 2);
+              const int col = half * (D / 2) + pass * (D / 4) + (v % (kPieces / 2)) * 4;
+              if (pc.whole) {
+                uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) +
+                                                      (head * p.R + rr) * D + col);
+                *dst = make_uint2(ptx::pack2<kBf16>(sum.x, sum.y), ptx::pack2<kBf16>(sum.z, sum.w));
+              } else {
+                *reinterpret_cast<float4*>(p.part_o + (slot * p.slot_rows + rr) * D + col) = sum;
+              }
             }
           }
         }
-        if (t < nrows && (kTiles == 2 || w == 0)) {
-          if (pc.whole)
-            p.lse[out_row] =
-                l > 0.f ? (ptx::lg2(l) - neg_m) * 0.693147180559945309f : -INFINITY;
-          else
-            p.part_ml[slot * p.slot_rows + srow] = make_float2(neg_m, l);
-        }
-      }
-      ptx::tc_fence_before();
-      if constexpr (kTiles == 1) {
-        // the statistics may be overwritten, and both outputs
-        ptx::named_bar_sync(1, 256);
+        ptx::fence_proxy_async_smem();           // the next queries may be loaded over the scratch
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(L::bQEmpty + qb));
         ptx::mbar_arrive(bar(L::bOFree + 0));
         ptx::mbar_arrive(bar(L::bOFree + 1));
       } else {
+        const size_t out_row = head * p.R + row;
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        if (has) {
+#pragma unroll 1
+          for (int col = 0; col < D; col += 32) {
+            uint32_t a[32];
+            ptx::tmem_ld32(tO + col, a);
+            ptx::tmem_wait_ld();
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = l > 0.f ? __uint_as_float(a[e]) : 0.f;
+            if (r < nrows) {
+              if (pc.whole) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + col);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  dst[v] = make_uint4(ptx::pack2<kBf16>(x[8 * v] * inv, x[8 * v + 1] * inv),
+                                      ptx::pack2<kBf16>(x[8 * v + 2] * inv, x[8 * v + 3] * inv),
+                                      ptx::pack2<kBf16>(x[8 * v + 4] * inv, x[8 * v + 5] * inv),
+                                      ptx::pack2<kBf16>(x[8 * v + 6] * inv, x[8 * v + 7] * inv));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(
+                    p.part_o + (slot * p.slot_rows + w * kDwTile + r) * D + col);
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                  dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+              }
+            }
+          }
+          if (r < nrows) {
+            if (pc.whole)
+              p.lse[out_row] = l > 0.f ? (ptx::lg2(l) - neg_m) * 0.693147180559945309f : -INFINITY;
+            else
+              p.part_ml[slot * p.slot_rows + w * kDwTile + r] = make_float2(neg_m, l);
+          }
+        }
+        ptx::tc_fence_before();
         ptx::mbar_arrive(bar(L::bOFree + w));
       }
     }
@@ -856,63 +1031,69 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   }
 }
 
-// One block of D threads per (head, row), thread c owning output column c:
-// rows of units that one CTA finished are left alone; the parts of a cut
-// unit are scaled to the largest maximum, added in the order of the runs and
+// The cut units: block (run, y) adds up the parts of rows of the unit that
+// starts in that run and ends in a later one (most runs have one, the run
+// table says which), D / 4 threads a row with 4 columns each: every part is
+// scaled to the largest maximum, added in the order of the runs, and the sum
 // divided once.  A row without a visible key has no live part: O = 0 and
 // LSE = -inf.
+constexpr int kDwCombineThreads = 128;
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(kDwCombineThreads)
     fa_decode_win_combine_kernel(const __grid_constant__ DecWinParams p) {
-  const int row = blockIdx.x % p.R, head = blockIdx.x / p.R;
-  const int b = head / p.Hk, rb = row / p.row_span;
-  const int c = threadIdx.x;
-  int before, total;
-  dec_tile_sums(p, b, before, total);
-  const DecDeal deal = dec_deal(total, p.grid);
-  const int nt = dec_tiles(dec_span_of(p, b));
-  const int s = before + ((head - b * p.Hk) * p.row_blocks + rb) * nt;
-  const int first = dec_run_of(deal, s), last = dec_run_of(deal, s + nt - 1);
+  constexpr int kPer = D / 4;
   ptx::griddep_wait();   // the parts are complete, and this grid ends after the main one
-  if (first == last) return;
-  // the first run's part is its last piece unless the run starts with the
-  // unit; every later run starts with it
-  const int first_slot = 2 * first + (dec_run_start(deal, first) >= s ? 0 : 1);
-  const size_t srow = row - rb * p.row_span;
+  const int run0 = blockIdx.x;
+  const int4 cut = p.cut[run0];
+  if (cut.w < 0) return;
+  const int srow = blockIdx.y * (kDwCombineThreads / kPer) + threadIdx.x / kPer;
+  const int row = cut.y * p.row_span + srow, c = threadIdx.x % kPer;
+  if (srow >= p.slot_rows || row >= p.R) return;
+  // the unit's first part is the last piece of its run, the others are the
+  // first of theirs
   auto part_of = [&](int run) {
-    return static_cast<size_t>(run == first ? first_slot : 2 * run) * p.slot_rows + srow;
+    return static_cast<size_t>(run == run0 ? cut.z : 2 * run) * p.slot_rows + srow;
   };
-  float nm = INFINITY, l = 0.f, acc = 0.f;
-  for (int run0 = first; run0 <= last; run0 += kDwCombine) {
+  float nm = INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int run = run0; run <= cut.w; run += kDwCombine) {
     // a batch of parts, their loads in flight together
     float2 ml[kDwCombine];
-    float x[kDwCombine];
+    float4 x[kDwCombine];
 #pragma unroll
     for (int i = 0; i < kDwCombine; ++i) {
-      const size_t part = part_of(min(run0 + i, last));
-      ml[i] = p.part_ml[part];
-      x[i] = p.part_o[part * D + c];
-      if (run0 + i > last) ml[i].y = 0.f;
+      if (run + i <= cut.w) {
+        const size_t part = part_of(run + i);
+        ml[i] = p.part_ml[part];
+        x[i] = reinterpret_cast<const float4*>(p.part_o + part * D)[c];
+      } else {
+        ml[i] = make_float2(0.f, 0.f);
+      }
     }
     float m = nm;
 #pragma unroll
     for (int i = 0; i < kDwCombine; ++i)
       if (ml[i].y > 0.f) m = fminf(m, ml[i].x);
     const float fo = nm == INFINITY ? 0.f : ptx::ex2(m - nm);
-    acc *= fo;
+    acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
     l *= fo;
     nm = m;
 #pragma unroll
     for (int i = 0; i < kDwCombine; ++i)
       if (ml[i].y > 0.f) {
         const float f = ptx::ex2(m - ml[i].x);
-        acc = fmaf(f, x[i], acc);
+        acc.x = fmaf(f, x[i].x, acc.x);
+        acc.y = fmaf(f, x[i].y, acc.y);
+        acc.z = fmaf(f, x[i].z, acc.z);
+        acc.w = fmaf(f, x[i].w, acc.w);
         l = fmaf(f, ml[i].y, l);
       }
   }
-  const size_t out = static_cast<size_t>(head) * p.R + row;
-  const uint32_t pk = ptx::pack2<kBf16>(l > 0.f ? acc / l : 0.f, 0.f);
-  static_cast<uint16_t*>(p.o)[out * D + c] = static_cast<uint16_t>(pk & 0xffffu);
+  const size_t out = static_cast<size_t>(cut.x) * p.R + row;
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D)[c] =
+      make_uint2(ptx::pack2<kBf16>(acc.x * inv, acc.y * inv),
+                 ptx::pack2<kBf16>(acc.z * inv, acc.w * inv));
   if (c == 0) p.lse[out] = l > 0.f ? (ptx::lg2(l) - nm) * 0.693147180559945309f : -INFINITY;
 }
 
