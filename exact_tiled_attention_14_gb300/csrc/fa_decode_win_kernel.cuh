@@ -246,6 +246,19 @@ struct DwLayout {
   static constexpr uint32_t p_col(int w) { return kOwnP ? 256u + 2u * D + 64u * w : 128u * w; }
 };
 
+// Place in the ring: slot and the parity of its current use.
+template <int kStages>
+struct DwRing {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void step(uint32_t n = 1) {
+    slot += n;
+    if (slot >= kStages) {
+      slot -= kStages;
+      parity ^= 1u;
+    }
+  }
+};
+
 // Bits [a, b) of 128 as four words.
 __host__ __device__ __forceinline__ void or_range(uint32_t* w, int a, int b) {
 #pragma unroll
@@ -313,15 +326,32 @@ __host__ __device__ __forceinline__ DecRow dec_row(const unsigned long long* row
   }
   return r;
 }
-// Visible columns of tile tl for a row, as 128 bits; true when all are.
+// Tiles [from, to) of the list whose 128 columns a row sees whole: no sinks
+// before the span in them, from the row's window on, up to its position (of
+// a tree: up to the history's end).
+struct DecWhole {
+  int from, to;
+};
+__host__ __device__ __forceinline__ DecWhole dec_whole(const DecSpan& s, const DecRow& r, bool tree,
+                                                       int win) {
+  // key0 of a tile without sinks is lo - sink_rows + 128 t
+  const int base = s.lo - s.sink_rows, first = r.pos - win + 1;
+  int upto = tree ? s.len : r.pos + 1;
+  if (upto > s.hi) upto = s.hi;
+  const int skip = first - base > s.sink_rows ? first - base : s.sink_rows;
+  DecWhole w;
+  w.from = (skip + kDwTile - 1) / kDwTile;
+  w.to = upto <= base ? 0 : (upto - base) / kDwTile;
+  return w;
+}
+// Visible columns of tile tl for a row, as 128 bits.
 // seen: keys of the span part up to the row's position (tree: its history).
-__host__ __device__ __forceinline__ bool dec_visible(const DecSpan& s, const DecTile& tl,
+__host__ __device__ __forceinline__ void dec_visible(const DecSpan& s, const DecTile& tl,
                                                      const DecRow& r, bool tree, int win, int sinks,
                                                      uint32_t* vis) {
   const int upto = (tree ? s.len : r.pos + 1) - tl.key0;
   const int seen = tl.nw < upto ? tl.nw : upto;
   const int first = r.pos - win + 1 - tl.key0;
-  if (tl.ns == 0 && seen == kDwTile && first <= 0) return true;
   vis[0] = vis[1] = vis[2] = vis[3] = 0u;
   const int ns = s.sink - tl.sink0 < tl.ns ? s.sink - tl.sink0 : tl.ns;
   or_range(vis, 0, ns);                                           // the sinks before the span
@@ -336,7 +366,6 @@ __host__ __device__ __forceinline__ bool dec_visible(const DecSpan& s, const Dec
 #pragma unroll
     for (int k = 0; k < 4; ++k) vis[k] |= dv[k] & in[k];
   }
-  return false;
 }
 
 template <int D, bool kBf16, int kTiles, int kCopies>
@@ -462,13 +491,14 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // ============================================================ TMA producer
       if (lane == 0) {
         uint32_t loads = 0, pieces = 0;
+        DwRing<L::kStages> ring;
         bool alive = true;
         while (alive && dec_next(p, cu, pc)) {
           const int head = pc.b * p.Hk + pc.unit / p.row_blocks;
           auto load_kv = [&](bool v, int j) {
-            const uint32_t slot = loads % L::kStages, use = loads / L::kStages;
-            if (use > 0)
-              alive = alive && ptx::wait_bounded(bar(L::bKvEmpty + slot), (use - 1) & 1, wd,
+            const uint32_t slot = ring.slot;
+            if (loads >= (uint32_t)L::kStages)   // the slot's previous use is over
+              alive = alive && ptx::wait_bounded(bar(L::bKvEmpty + slot), ring.parity ^ 1u, wd,
                                                  kSiteDwKvEmpty);
             if (!alive) return;
             const DecTile t = dec_tile(pc.s, pc.t0 + j);
@@ -495,6 +525,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
               }
             }
             ++loads;
+            ring.step();
           };
           load_kv(false, 0);
           const uint32_t qb = pieces % L::kQBufs, quse = pieces / L::kQBufs;
@@ -536,16 +567,19 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, kDwTile, kBf16 ? 1 : 0, 0);
         const uint32_t q_lo = ptx::desc_lo(sbase + L::kQ, 16);
         const uint32_t k_lo = ptx::desc_lo(sbase + L::kKV, 16);
-        uint32_t base = 0, pieces = 0, sc[2] = {0, 0};
+        // K tiles sit at ring positions 0, 1, 3, 5, ... of a piece's 2 n
+        DwRing<L::kStages> ring;
+        uint32_t pieces = 0, sc[2] = {0, 0};
         bool alive = true, issued = false;
         while (dec_next(p, cu, pc)) {
           const uint32_t qb = pieces % L::kQBufs;
           alive = alive && ptx::wait_bounded(bar(L::bQFull + qb), (pieces / L::kQBufs) & 1, wd,
                                              kSiteDwQFull);
           for (int j = 0; j < pc.n; ++j) {
-            const uint32_t pos = base + (j == 0 ? 0u : 2u * j - 1u), slot = pos % L::kStages;
-            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), (pos / L::kStages) & 1, wd,
+            const uint32_t slot = ring.slot;
+            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), ring.parity, wd,
                                                kSiteDwKvFull);
+            ring.step(j == 0 ? (pc.n == 1 ? 2 : 1) : (j + 1 == pc.n ? 3 : 2));
             ptx::tc_fence_after();
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -574,7 +608,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
               if (j + 1 == pc.n) ptx::mma_commit(bar(L::bQEmpty + qb));
             }
           }
-          base += 2u * pc.n;
           ++pieces;
         }
         if (issued) {
@@ -593,7 +626,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // a phase that lane 0's progress lets pass twice.
       constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, D, kBf16 ? 1 : 0, 1);
       const uint32_t v_lo = ptx::desc_lo(sbase + L::kKV, L::kChunkBytes);
-      uint32_t base = 0, pcn[2] = {0, 0}, units[2] = {0, 0};
+      // V tiles sit at ring positions 2, 4, ..., 2 n - 2 and 2 n - 1 of a piece's 2 n
+      DwRing<L::kStages> ring;
+      uint32_t pcn[2] = {0, 0}, units[2] = {0, 0};
       bool alive = true, issued = false, cut_here = false;
       while (dec_next(p, cu, pc)) {
         int done[2] = {0, 0};
@@ -614,11 +649,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           holes = used & ~((static_cast<unsigned long long>(hi) << 32) | lo);
         }
         for (int j = 0; j < pc.n; ++j) {
-          const uint32_t pos = base + (j + 1 < pc.n ? 2u * j + 2u : 2u * pc.n - 1u);
-          const uint32_t slot = pos % L::kStages;
+          ring.step(j + 1 < pc.n ? 2 : 1);
+          const uint32_t slot = ring.slot;
           if (lane == 0)
-            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), (pos / L::kStages) & 1, wd,
+            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), ring.parity, wd,
                                                kSiteDwKvFull);
+          if (j + 1 == pc.n) ring.step();
           __syncwarp();
           const DecTile t = dec_tile(pc.s, pc.t0 + j);
           const int s_end = min(max(pc.s.sink - t.sink0, 0), t.ns);   // sinks end in the tile
@@ -670,7 +706,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         // that had no tile too
         units[0] += kTiles == 1 || done[0] > 0;
         units[1] += kTiles == 1 || done[1] > 0;
-        base += 2u * pc.n;
         // a unit that starts here and ends in a later run: its parts' place
         if (pc.t0 == 0 && !pc.whole && lane == 0) {
           const DecDeal deal{cursor_s[4], cursor_s[5], cursor_s[6]};
@@ -712,9 +747,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       if (kTiles == 2 && nrows == 0) continue;
       const bool has = (kCopies > 1 ? (warp & 3) * 32 % kRows : (warp & 3) * 32) < nrows;
       const int row = (kTiles * (pc.unit % p.row_blocks) + (kTiles == 2 ? w : 0)) * kDwTile + r;
-      const DecRow me =
-          dec_row(p.tree ? p.tree + static_cast<size_t>(pc.b) * p.Nq : nullptr,
-                  min(row, p.R - 1) % p.Nq, p.Nq, pc.s.len, p.win, p.sinks);
+      // what the row sees: most tiles whole, the others column by column
+      auto my_row = [&]() {
+        return dec_row(p.tree ? p.tree + static_cast<size_t>(pc.b) * p.Nq : nullptr,
+                       min(row, p.R - 1) % p.Nq, p.Nq, pc.s.len, p.win, p.sinks);
+      };
+      const DecWhole whole = dec_whole(pc.s, my_row(), p.tree != nullptr, p.win);
       float m_ref = -INFINITY, neg_m = 0.f, l = 0.f;
       int it = 0;                                // tiles of this group so far
       for (int j = 0; j < pc.n; ++j) {
@@ -734,14 +772,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           if (L::kOwnP) ptx::mbar_arrive(bar(L::bSFree + w));
           wait_pv();
         } else {
-          uint32_t vis[4];
-          const bool all = dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), me, p.tree != nullptr, p.win,
-                                       p.sinks, vis);
-          if constexpr (kCopies == 4) vis[0] = seg < 2 ? (seg ? vis[1] : vis[0]) : (seg == 2 ? vis[2] : vis[3]);
-          if constexpr (kCopies == 2) {
-            vis[0] = seg ? vis[2] : vis[0];
-            vis[1] = seg ? vis[3] : vis[1];
-          }
           ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteDwSFull);
           ++scnt;
           __syncwarp();
@@ -757,7 +787,16 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
           }
-          if (!all) {
+          if (pc.t0 + j < whole.from || pc.t0 + j >= whole.to) {
+            uint32_t vis[4];
+            dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), my_row(), p.tree != nullptr, p.win, p.sinks,
+                        vis);
+            if constexpr (kCopies == 4)
+              vis[0] = seg < 2 ? (seg ? vis[1] : vis[0]) : (seg == 2 ? vis[2] : vis[3]);
+            if constexpr (kCopies == 2) {
+              vis[0] = seg ? vis[2] : vis[0];
+              vis[1] = seg ? vis[3] : vis[1];
+            }
 #pragma unroll
             for (int e = 0; e < kCols; ++e)
               if (!((vis[e >> 5] >> (e & 31)) & 1u)) sv[e] = -INFINITY;

@@ -141,8 +141,13 @@ static int check_decode(int Nq, int Nk, int count, int win, int sinks, int tree)
     if (bs == 0 && bw == 0 && d.key0 < 0) BAD("negative empty load");
     if (d.ns && d.sink0 + d.ns > s.sink_rows) BAD("sink rows");
     for (int i = 0; i < Nq; ++i) {
-      uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+      uint32_t vis[4];
       fa::dec_visible(s, d, me[i], tree != 0, win, sinks, vis);
+      const fa::DecWhole w = fa::dec_whole(s, me[i], tree != 0, win);
+      const bool all = vis[0] == ~0u && vis[1] == ~0u && vis[2] == ~0u && vis[3] == ~0u;
+      if (t >= w.from && t < w.to && !all) BAD("tile %d is not whole", t);
+      if (all && d.ns == 0 && !(t >= w.from && t < w.to) && sinks == 0 && !tree)
+        BAD("whole tile %d missed", t);
       for (int c = 0; c < 128; ++c) {
         if (!(vis[c >> 5] >> (c & 31) & 1)) continue;
         const int key = c < d.ns ? d.sink0 + c : d.key0 + c - d.ns;
