@@ -137,6 +137,21 @@ __host__ __device__ __forceinline__ DecTile dec_tile(const DecSpan& s, int t) {
   return d;
 }
 
+// Tiles [from, to) that hold 128 span keys from max(lo, first) to min(hi,
+// last) and no sinks before the span: tile t's keys start at base + 128 t.
+struct DecRange {
+  int from, to, base;
+};
+__host__ __device__ __forceinline__ DecRange dec_plain(const DecSpan& s, int first, int last) {
+  DecRange r;
+  r.base = s.lo - s.sink_rows;
+  const int skip = first - r.base > s.sink_rows ? first - r.base : s.sink_rows;
+  const int end = last < s.hi ? last : s.hi;
+  r.from = (skip + kDwTile - 1) / kDwTile;
+  r.to = end <= r.base ? 0 : (end - r.base) / kDwTile;
+  return r;
+}
+
 __device__ __forceinline__ DecSpan dec_span_of(const DecWinParams& p, int b) {
   return dec_span(p.seqlens ? p.seqlens[b] : p.len_all, p.Nk, p.Nq, p.win, p.sinks,
                   p.tree != nullptr);
@@ -214,26 +229,39 @@ __device__ __forceinline__ bool dec_next(const DecWinParams& p, DecCursor& c, De
   return true;
 }
 
+// Where P is.  S of the two groups fills TMEM columns 0-255, their O the
+// columns from 256 on.  At d = 64 there is room behind O for P (16 bit, 64
+// columns a group).  At d = 128 TMEM is full: with one row tile P goes over
+// the S it was formed from, and the group's next S waits for the product that
+// reads P (the loads bound these calls, not that chain); with two row tiles
+// P goes to shared memory, which costs two ring stages but lets the next S
+// be formed during the softmax (measured for 256 rows: 2.07 us a tile with P
+// over S, the chain of softmax and both products, against the figure in
+// the header of fa_decode_win_kernel).
+//
 // Shared memory: query tiles (two buffers, so a unit's queries load while the
 // previous unit runs; one at d = 128 with two row tiles, where there is no
-// room) and a ring of K and V tiles.  TMEM: S of the two groups in columns
-// 0-127 and 128-255, their O from 256 on, and P (16 bit, 64 columns a group):
-// behind O at d = 64; at d = 128, where S and O fill all 512 columns, over the
-// S it was formed from, and the group's next S waits for the product that
-// reads P.
+// room), a ring of K and V tiles, and P where it is there.
 template <int D, int kTiles>
 struct DwLayout {
   static constexpr int kChunks = D / 64;
   static constexpr int kTile = kDwTile * D * 2;
   static constexpr int kChunkBytes = kDwTile * 128;
-  static constexpr bool kOwnP = D == 64;
+  static constexpr int kPTile = kDwTile * kDwTile * 2;
+  static constexpr bool kSmemP = D == 128 && kTiles == 2;
+  static constexpr bool kOwnP = D == 64 || kSmemP;     // P is not over S
   static constexpr int kQBufs = (D == 128 && kTiles == 2) ? 1 : 2;
-  static constexpr int kStages = (D == 128) ? 5 : (kTiles == 2 ? 10 : 12);
+  static constexpr int kStages = (D == 128) ? (kSmemP ? 3 : 5) : (kTiles == 2 ? 10 : 12);
   static constexpr int kQ = 0;
   static constexpr int kKV = kQ + kQBufs * kTiles * kTile;
-  static constexpr int kBar = kKV + kStages * kTile;
-  static constexpr int bQFull = 0, bQEmpty = kQBufs, bKvFull = 2 * kQBufs,
-                       bKvEmpty = bKvFull + kStages, bSFull = bKvEmpty + kStages,
+  static constexpr int kP = kKV + kStages * kTile;
+  static constexpr int kBar = kP + (kSmemP ? 2 * kPTile : 0);
+  // K and V uses of a ring slot have a full barrier each: a wait by parity is
+  // only sound where the waiting thread waits for every phase, and the S warp
+  // waits for K tiles, the P V warp for V tiles.
+  static constexpr int bQFull = 0, bQEmpty = kQBufs, bKFull = 2 * kQBufs,
+                       bVFull = bKFull + kStages, bKvEmpty = bVFull + kStages,
+                       bSFull = bKvEmpty + kStages,
                        bSFree = bSFull + 2, bPFull = bSFree + 2, bPvDone = bPFull + 2,
                        bOFree = bPvDone + 2, bFinalS = bOFree + 2, bFinalPv = bFinalS + 1,
                        kNumBars = bFinalPv + 1;
@@ -326,23 +354,11 @@ __host__ __device__ __forceinline__ DecRow dec_row(const unsigned long long* row
   }
   return r;
 }
-// Tiles [from, to) of the list whose 128 columns a row sees whole: no sinks
-// before the span in them, from the row's window on, up to its position (of
-// a tree: up to the history's end).
-struct DecWhole {
-  int from, to;
-};
-__host__ __device__ __forceinline__ DecWhole dec_whole(const DecSpan& s, const DecRow& r, bool tree,
+// Tiles whose 128 columns a row sees whole: from its window on, up to its
+// position (of a tree: up to the history's end).
+__host__ __device__ __forceinline__ DecRange dec_whole(const DecSpan& s, const DecRow& r, bool tree,
                                                        int win) {
-  // key0 of a tile without sinks is lo - sink_rows + 128 t
-  const int base = s.lo - s.sink_rows, first = r.pos - win + 1;
-  int upto = tree ? s.len : r.pos + 1;
-  if (upto > s.hi) upto = s.hi;
-  const int skip = first - base > s.sink_rows ? first - base : s.sink_rows;
-  DecWhole w;
-  w.from = (skip + kDwTile - 1) / kDwTile;
-  w.to = upto <= base ? 0 : (upto - base) / kDwTile;
-  return w;
+  return dec_plain(s, r.pos - win + 1, tree ? s.len : r.pos + 1);
 }
 // Visible columns of tile tl for a row, as 128 bits.
 // seen: keys of the span part up to the row's position (tree: its history).
@@ -401,7 +417,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       ptx::mbar_init(bar(L::bQEmpty + i), kTiles == 1 ? 257 : 1);
     }
     for (int s = 0; s < L::kStages; ++s) {
-      ptx::mbar_init(bar(L::bKvFull + s), 1);
+      ptx::mbar_init(bar(L::bKFull + s), 1);
+      ptx::mbar_init(bar(L::bVFull + s), 1);
       ptx::mbar_init(bar(L::bKvEmpty + s), 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -480,10 +497,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     const int first = (kTiles * (x.unit % p.row_blocks) + (kTiles == 2 ? w : 0)) * kDwTile;
     return min(max(p.R - first, 0), kDwTile);
   };
-  // whether group w computes tile j of the piece
-  auto takes = [&](const DecPiece& x, int w, int j) {
-    return kTiles == 1 ? (j & 1) == w : rows_of(x, w) > 0;
-  };
 
   if (warp >= 8) {
     ptx::setmaxnreg_dec<kDwIssueRegs>();
@@ -491,24 +504,29 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // ============================================================ TMA producer
       if (lane == 0) {
         uint32_t loads = 0, pieces = 0;
+        uint32_t k_odd = 0, v_odd = 0, k_used = 0, v_used = 0;   // per slot, as in the waits below
         DwRing<L::kStages> ring;
         bool alive = true;
         while (alive && dec_next(p, cu, pc)) {
           const int head = pc.b * p.Hk + pc.unit / p.row_blocks;
+          const DecRange plain = dec_plain(pc.s, 0, pc.s.hi);
           auto load_kv = [&](bool v, int j) {
             const uint32_t slot = ring.slot;
             if (loads >= (uint32_t)L::kStages)   // the slot's previous use is over
               alive = alive && ptx::wait_bounded(bar(L::bKvEmpty + slot), ring.parity ^ 1u, wd,
                                                  kSiteDwKvEmpty);
             if (!alive) return;
-            const DecTile t = dec_tile(pc.s, pc.t0 + j);
-            const uint32_t dst = sbase + L::kKV + slot * L::kTile, full = bar(L::bKvFull + slot);
-            if (t.nw > kDwTile - kDwBox) {   // no sinks in it: one box of 128 rows
+            const uint32_t dst = sbase + L::kKV + slot * L::kTile, full = bar((v ? L::bVFull : L::bKFull) + slot);
+            (v ? v_odd : k_odd) ^= 1u << slot;
+            (v ? v_used : k_used) |= 1u << slot;
+            if (pc.t0 + j >= plain.from && pc.t0 + j < plain.to) {   // one box of 128 rows
               ptx::mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
               for (int c = 0; c < L::kChunks; ++c)
                 ptx::tma_load_3d(dst + c * L::kChunkBytes, v ? &p.tm_v : &p.tm_k, full, c * 64,
-                                 t.key0, head);
+                                 plain.base + (pc.t0 + j) * kDwTile, head);
             } else {
+              const DecTile t = dec_tile(pc.s, pc.t0 + j);
               // boxes of 16 rows; a tile without keys still loads one box,
               // whose rows are masked
               const int bs = t.ns / kDwBox;
@@ -555,8 +573,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         }
         // Drain: every issued copy has landed before the CTA can exit.
         const unsigned long long drain = 200000000ull;
-        for (uint32_t l = loads > (uint32_t)L::kStages ? loads - L::kStages : 0; l < loads; ++l)
-          ptx::wait_drain(bar(L::bKvFull + l % L::kStages), (l / L::kStages) & 1, drain);
+        for (int s = 0; s < L::kStages; ++s) {
+          if ((k_used >> s) & 1u)
+            ptx::wait_drain(bar(L::bKFull + s), ((k_odd >> s) & 1u) ^ 1u, drain);
+          if ((v_used >> s) & 1u)
+            ptx::wait_drain(bar(L::bVFull + s), ((v_odd >> s) & 1u) ^ 1u, drain);
+        }
         for (uint32_t i = pieces > (uint32_t)L::kQBufs ? pieces - L::kQBufs : 0; i < pieces; ++i)
           ptx::wait_drain(bar(L::bQFull + i % L::kQBufs), (i / L::kQBufs) & 1, drain);
       }
@@ -569,21 +591,23 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         const uint32_t k_lo = ptx::desc_lo(sbase + L::kKV, 16);
         // K tiles sit at ring positions 0, 1, 3, 5, ... of a piece's 2 n
         DwRing<L::kStages> ring;
-        uint32_t pieces = 0, sc[2] = {0, 0};
+        uint32_t pieces = 0, sc[2] = {0, 0}, odd = 0;
         bool alive = true, issued = false;
         while (dec_next(p, cu, pc)) {
           const uint32_t qb = pieces % L::kQBufs;
           alive = alive && ptx::wait_bounded(bar(L::bQFull + qb), (pieces / L::kQBufs) & 1, wd,
                                              kSiteDwQFull);
+          const bool second = kTiles == 2 && rows_of(pc, 1) > 0;
           for (int j = 0; j < pc.n; ++j) {
             const uint32_t slot = ring.slot;
-            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), ring.parity, wd,
+            alive = alive && ptx::wait_bounded(bar(L::bKFull + slot), (odd >> slot) & 1u, wd,
                                                kSiteDwKvFull);
+            odd ^= 1u << slot;   // per slot: parity of its K tiles so far
             ring.step(j == 0 ? (pc.n == 1 ? 2 : 1) : (j + 1 == pc.n ? 3 : 2));
             ptx::tc_fence_after();
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              if (!takes(pc, w, j)) continue;
+              if (kTiles == 1 ? (j & 1) != w : w == 1 && !second) continue;
               if (sc[w] > 0)   // the softmax has read this group's previous S (over
                                // which, at d = 128, P was written and must be read too)
                 alive = alive && ptx::wait_bounded(bar((L::kOwnP ? L::bSFree : L::bPvDone) + w),
@@ -626,12 +650,11 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // a phase that lane 0's progress lets pass twice.
       constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, D, kBf16 ? 1 : 0, 1);
       const uint32_t v_lo = ptx::desc_lo(sbase + L::kKV, L::kChunkBytes);
-      // V tiles sit at ring positions 2, 4, ..., 2 n - 2 and 2 n - 1 of a piece's 2 n
+      const uint32_t p_lo = ptx::desc_lo(sbase + L::kP, 16);   // where P is in shared memory
       DwRing<L::kStages> ring;
-      uint32_t pcn[2] = {0, 0}, units[2] = {0, 0};
+      uint32_t pcn[2] = {0, 0}, units[2] = {0, 0}, odd = 0;
       bool alive = true, issued = false, cut_here = false;
       while (dec_next(p, cu, pc)) {
-        int done[2] = {0, 0};
         // a tree's keys below `from` are before the window of its shallowest
         // token; `holes` are the drafted tokens that no row marks
         int from = 0;
@@ -648,42 +671,20 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
           holes = used & ~((static_cast<unsigned long long>(hi) << 32) | lo);
         }
-        for (int j = 0; j < pc.n; ++j) {
-          ring.step(j + 1 < pc.n ? 2 : 1);
-          const uint32_t slot = ring.slot;
-          if (lane == 0)
-            alive = alive && ptx::wait_bounded(bar(L::bKvFull + slot), ring.parity, wd,
-                                               kSiteDwKvFull);
-          if (j + 1 == pc.n) ring.step();
-          __syncwarp();
-          const DecTile t = dec_tile(pc.s, pc.t0 + j);
-          const int s_end = min(max(pc.s.sink - t.sink0, 0), t.ns);   // sinks end in the tile
-          // span rows [lead0, lead1) before every window, and drafted slots
-          const int lead1 = min(min(from, pc.s.len) - t.key0, t.nw);
-          const int lead0 = max(p.sinks - t.key0, 0);
-          const bool drafted = holes != 0 && t.key0 + t.nw > pc.s.len;
-          if (s_end < t.ns || t.ns + t.nw < kDwTile || lead0 < lead1 || drafted) {
-            auto clear = [&](int r0, int r1) {
-              for (int c = 0; c < L::kChunks; ++c) {
-                uint4* rows = reinterpret_cast<uint4*>(sgen + L::kKV + slot * L::kTile +
-                                                       c * L::kChunkBytes);
-                for (int i = r0 * 8 + lane; i < r1 * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
-              }
-            };
-            clear(s_end, t.ns);
-            clear(t.ns + t.nw, kDwTile);
-            clear(t.ns + lead0, t.ns + lead1);
-            if (drafted)
-              for (int i = max(pc.s.len - t.key0, 0); i < t.nw; ++i)
-                if (holes >> (t.key0 + i - pc.s.len) & 1) clear(t.ns + i, t.ns + i + 1);
-            ptx::fence_proxy_async_smem();
-          }
-          __syncwarp();
+        const int lead = min(from, pc.s.len);          // keys before every window end here
+        const DecRange plain = dec_plain(pc.s, lead, holes ? pc.s.len : pc.s.hi);
+        const bool second = kTiles == 2 && rows_of(pc, 1) > 0;
+        // tile j's product for the groups that take it, by lane 0
+        auto wait_v = [&](uint32_t slot) {
+          alive = alive && ptx::wait_bounded(bar(L::bVFull + slot), (odd >> slot) & 1u, wd,
+                                             kSiteDwKvFull);
+          odd ^= 1u << slot;   // per slot: parity of its V tiles so far
+        };
+        auto issue = [&](int j, uint32_t slot) {
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (!takes(pc, w, j)) continue;
-            const bool first = done[w]++ == 0;
-            if (lane != 0) continue;
+            if (kTiles == 1 ? (j & 1) != w : w == 1 && !second) continue;
+            const bool first = kTiles == 1 ? j == w : j == 0;
             if (first && units[w] > 0)   // the previous unit's O has been read
               alive = alive && ptx::wait_bounded(bar(L::bOFree + w), (units[w] - 1) & 1, wd,
                                                  kSiteDwOFree);
@@ -692,20 +693,61 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             ptx::tc_fence_after();
             if (alive) {
 #pragma unroll
-              for (int kk = 0; kk < kDwTile / 16; ++kk)
-                ptx::mma_ts(tmem_base + L::o_col(w), tmem_base + L::p_col(w) + kk * 8,
-                            ptx::desc_sw128(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4)),
-                            idesc, (kk > 0 || !first) ? 1u : 0u);
+              for (int kk = 0; kk < kDwTile / 16; ++kk) {
+                const uint64_t vd =
+                    ptx::desc_sw128(v_lo + slot * (L::kTile >> 4) + kk * (2048 >> 4));
+                const uint32_t acc = (kk > 0 || !first) ? 1u : 0u;
+                if constexpr (L::kSmemP) {   // K-major, 64 keys to a chunk
+                  const uint32_t off = (kk >> 2) * L::kChunkBytes + (kk & 3) * 32;
+                  ptx::mma_ss(tmem_base + L::o_col(w),
+                              ptx::desc_sw128(p_lo + ((w * L::kPTile + off) >> 4)), vd, idesc, acc);
+                } else {
+                  ptx::mma_ts(tmem_base + L::o_col(w), tmem_base + L::p_col(w) + kk * 8, vd, idesc,
+                              acc);
+                }
+              }
               ptx::mma_commit(bar(L::bPvDone + w));
               issued = true;
             }
           }
-          if (alive && lane == 0) ptx::mma_commit(bar(L::bKvEmpty + slot));
+          if (alive) ptx::mma_commit(bar(L::bKvEmpty + slot));
+        };
+        // V tiles sit at ring positions 2, 4, ..., 2 n - 2 and 2 n - 1 of the
+        // piece's 2 n.  The other lanes join lane 0 only at tiles with rows to
+        // clear: sinks' padding, past the keys, before every window, drafted
+        // slots.
+        for (int j = 0; j < pc.n; ++j) {
+          ring.step(j + 1 < pc.n ? 2 : 1);
+          const bool keep = pc.t0 + j >= plain.from && pc.t0 + j < plain.to;
+          if (keep && lane != 0) continue;
+          if (lane == 0) wait_v(ring.slot);
+          if (!keep) {
+            __syncwarp();
+            const DecTile t = dec_tile(pc.s, pc.t0 + j);
+            auto clear = [&](int r0, int r1) {
+              for (int c = 0; c < L::kChunks; ++c) {
+                uint4* rows = reinterpret_cast<uint4*>(sgen + L::kKV + ring.slot * L::kTile +
+                                                       c * L::kChunkBytes);
+                for (int i = r0 * 8 + lane; i < r1 * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+              }
+            };
+            clear(min(max(pc.s.sink - t.sink0, 0), t.ns), t.ns);
+            clear(t.ns + t.nw, kDwTile);
+            clear(t.ns + max(p.sinks - t.key0, 0), t.ns + min(lead - t.key0, t.nw));
+            if (holes)
+              for (int i = max(pc.s.len - t.key0, 0); i < t.nw; ++i)
+                if (holes >> (t.key0 + i - pc.s.len) & 1) clear(t.ns + i, t.ns + i + 1);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) issue(j, ring.slot);
         }
+        ring.step();
+        __syncwarp();
         // kTiles == 1: both groups read both outputs, and arrive for a group
         // that had no tile too
-        units[0] += kTiles == 1 || done[0] > 0;
-        units[1] += kTiles == 1 || done[1] > 0;
+        ++units[0];
+        units[1] += kTiles == 1 || second;
         // a unit that starts here and ends in a later run: its parts' place
         if (pc.t0 == 0 && !pc.whole && lane == 0) {
           const DecDeal deal{cursor_s[4], cursor_s[5], cursor_s[6]};
@@ -752,11 +794,11 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         return dec_row(p.tree ? p.tree + static_cast<size_t>(pc.b) * p.Nq : nullptr,
                        min(row, p.R - 1) % p.Nq, p.Nq, pc.s.len, p.win, p.sinks);
       };
-      const DecWhole whole = dec_whole(pc.s, my_row(), p.tree != nullptr, p.win);
+      const DecRange whole = dec_whole(pc.s, my_row(), p.tree != nullptr, p.win);
       float m_ref = -INFINITY, neg_m = 0.f, l = 0.f;
       int it = 0;                                // tiles of this group so far
       for (int j = 0; j < pc.n; ++j) {
-        if (!takes(pc, w, j)) continue;
+        if (kTiles == 1 && (j & 1) != w) continue;
         // P_w and O_w are in use until the group's previous product is done
         // (at d = 128 this S could only come after it)
         auto wait_pv = [&]() {
@@ -857,7 +899,15 @@ __global__ void __launch_bounds__(kDwThreads, 1)
               ptx::tmem_st32(tO + q4 * 32, orr);
             }
           }
-          if constexpr (kCopies == 1) {
+          if constexpr (L::kSmemP) {
+            uint8_t* prow = sgen + L::kP + w * L::kPTile + t * 128;   // 128-byte swizzle
+#pragma unroll
+            for (int k = 0; k < kDwTile / 8; ++k)
+              *reinterpret_cast<uint4*>(prow + (k >> 3) * L::kChunkBytes +
+                                        (((k & 7) ^ (t & 7)) << 4)) =
+                  make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+            ptx::fence_proxy_async_smem();
+          } else if constexpr (kCopies == 1) {
             ptx::tmem_st32(tP, pk);
             ptx::tmem_st32(tP + 32, pk + 32);
           } else {

@@ -246,7 +246,7 @@ struct OwnP {
 // buffers of kMaskBytes (128 rows x 128 keys, one bit each); they take the
 // room of one K/V stage, and the ring keeps two (a key step with dropout
 // lasts several microseconds, longer than a tile's load).
-template <int D, bool kDrop = false>
+template <int D, bool kDrop = false, bool kWin = false>
 struct Smem {
   static constexpr bool kGen = has_gen<D, kDrop>();
   static constexpr int kChunks = D / 64;             // 128-byte swizzle columns per row
@@ -269,9 +269,17 @@ struct Smem {
   static constexpr int kMask = kP + (OwnP<D>::kSmem ? 2 * kBM * kBN * 2 : 0);  // mask rings
   static constexpr int kBar = kMask + (kGen ? 2 * kMaskStages * kMaskBytes : 0);
   // barrier indices (the mask barriers, [query tile][stage], only with the generator)
-  static constexpr int bQFull = 0, bQEmpty = kQBufs, bKvFull = 2 * kQBufs,
-                       bKvEmpty = bKvFull + kStages, bSFull = bKvFull + 2 * kStages,
-                       bPFull = bSFull + 2,
+  // kWin: a ring slot has one full barrier for its uses as a K tile and one
+  // for its uses as a V tile.  K tiles are waited for by the S issuer, V tiles
+  // by the P V issuer, and a wait by parity is only sound while the barrier is
+  // at most one phase behind the waiting thread: polling use u of a slot
+  // while the other issuer's use u - 1 is still in flight would pass on the
+  // parity of use u - 2.  The other variants share one barrier a slot: where
+  // the ring is short enough for that (see ring_order) their issuers order
+  // their waits so that use u - 1 is known to be over.
+  static constexpr int bQFull = 0, bQEmpty = kQBufs, bKFull = 2 * kQBufs,
+                       bVFull = bKFull + (kWin ? kStages : 0), bKvEmpty = bVFull + kStages,
+                       bSFull = bKvEmpty + kStages, bPFull = bSFull + 2,
                        bOFree = bPFull + 2, bSFree = bOFree + 2, bPvDone = bSFree + 2,
                        bFinal = bPvDone + 2, bFinalPv = bFinal + 1, bMaskFull = bFinalPv + 1,
                        bMaskEmpty = bMaskFull + 2 * kMaskStages,
@@ -553,7 +561,7 @@ template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool k
           bool kWin = false>
 __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
-  using L = Smem<D, kDrop>;
+  using L = Smem<D, kDrop, kWin>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -578,7 +586,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       ptx::mbar_init(bar(L::bQEmpty + qb), 1);
     }
     for (int s = 0; s < L::kStages; ++s) {
-      ptx::mbar_init(bar(L::bKvFull + s), 1);
+      ptx::mbar_init(bar(L::bKFull + s), 1);
+      if (kWin) ptx::mbar_init(bar(L::bVFull + s), 1);
       ptx::mbar_init(bar(L::bKvEmpty + s), 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -662,6 +671,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     if (lane == 0) {
       uint32_t tr = 0;          // trace events recorded
       uint32_t loads = 0;       // K/V tiles issued (ring position)
+      uint32_t k_odd = 0, v_odd = 0;     // per slot: parity of the K / V tiles issued into it
+      uint32_t k_used = 0, v_used = 0;   // per slot: any K / V tile issued
       uint32_t q_issued = 0;    // units whose Q load was issued
       uint32_t k_units = 0;     // pieces walked
       bool alive = true;
@@ -704,14 +715,19 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           if (alive) {
             // kKv: only the chunks of the tensor's own width (d for K, dv for V)
             const int nc = kKv ? (kv ? p.dv : p.dqk) / 64 : L::kChunks;
-            ptx::mbar_arrive_expect_tx(bar(L::bKvFull + slot), nc * L::kChunkBytes);
+            const uint32_t full = bar((kv ? L::bVFull : L::bKFull) + slot);
+            if constexpr (kWin) {
+              (kv ? v_odd : k_odd) ^= 1u << slot;
+              (kv ? v_used : k_used) |= 1u << slot;
+            }
+            ptx::mbar_arrive_expect_tx(full, nc * L::kChunkBytes);
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
             if constexpr (kWin) { y = win_tile(u, j) * kBN; z = kv_head(p, u.bh); }
             if (kKv && p.varlen) { z = u.k0 + y; y = u.bh % p.H; }   // head, token
             for (int c = 0; c < nc; ++c)
-              ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm,
-                               bar(L::bKvFull + slot), c * 64, y, z);
+              ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm, full,
+                               c * 64, y, z);
             trace_event(p, 3, tr, kv ? kEvLoadV : kEvLoadK, j);
             ++loads;
           }
@@ -729,8 +745,14 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       // Drain: make sure every issued copy has landed before the CTA can exit.
       const unsigned long long drain = 200000000ull;   // cycles (~0.1 s)
       const uint32_t first = loads > (uint32_t)L::kStages ? loads - L::kStages : 0;
-      for (uint32_t l = first; l < loads; ++l)
-        ptx::wait_drain(bar(L::bKvFull + l % L::kStages), (l / L::kStages) & 1, drain);
+      for (uint32_t l = first; !kWin && l < loads; ++l)
+        ptx::wait_drain(bar(L::bKFull + l % L::kStages), (l / L::kStages) & 1, drain);
+      for (int s = 0; kWin && s < L::kStages; ++s) {
+        if ((k_used >> s) & 1u)
+          ptx::wait_drain(bar(L::bKFull + s), ((k_odd >> s) & 1u) ^ 1u, drain);
+        if ((v_used >> s) & 1u)
+          ptx::wait_drain(bar(L::bVFull + s), ((v_odd >> s) & 1u) ^ 1u, drain);
+      }
       for (uint32_t q = q_issued > (uint32_t)L::kQBufs ? q_issued - L::kQBufs : 0; q < q_issued; ++q)
         ptx::wait_drain(bar(L::bQFull + q % L::kQBufs), (q / L::kQBufs) & 1, drain);
     }
@@ -846,12 +868,17 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       };
       // The producer fills the ring with K0 K1 V0 K2 V1 ... K_{n-1} V_{n-2}
       // V_{n-1} for a piece of n key tiles: 2n loads from ring position
-      // `base`; each issuer waits only for the tiles it reads.
+      // `base`; each issuer waits only for the tiles it reads (kWin: on its own
+      // full barrier of the slot; odd: per slot, parity of its tiles so far).
+      const uint32_t full0 = bar(warp == kMmaWarp ? L::bKFull : L::bVFull);
+      uint32_t odd = 0;
       auto ring_wait = [&](uint32_t pos) -> uint32_t {
         const uint32_t sl = pos % L::kStages;
         pf.lap(6);
-        alive = ptx::wait_bounded(bar(L::bKvFull + sl), (pos / L::kStages) & 1, wd, kSiteKvFull) &&
-                alive;
+        alive = ptx::wait_bounded(full0 + 8u * sl,
+                                  kWin ? (odd >> sl) & 1u : (pos / L::kStages) & 1u, wd,
+                                  kSiteKvFull) && alive;
+        if (kWin) odd ^= 1u << sl;
         pf.lap(0);
         ptx::tc_fence_after();
         return sl;

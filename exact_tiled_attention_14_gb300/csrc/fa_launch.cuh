@@ -21,12 +21,12 @@ cudaError_t launch_variant(const FwdParams& p, int grid, cudaStream_t stream) {
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load() & bit)) {
     e = cudaFuncSetAttribute(fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, kDrop>::kAlloc);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, kDrop, kWin>::kAlloc);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
   fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin>
-      <<<grid, threads_of<D, kDrop>(), Smem<D, kDrop>::kAlloc, stream>>>(p);
+      <<<grid, threads_of<D, kDrop>(), Smem<D, kDrop, kWin>::kAlloc, stream>>>(p);
   return cudaGetLastError();
 }
 

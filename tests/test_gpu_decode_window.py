@@ -279,3 +279,31 @@ def test_no_keys():
     o, lse = fa.attention_decode_window(q, k, k, 8)
     status_ok()
     assert not o.any() and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,Nq", [(1, 1), (3, 15), (2, 50), (4, 64), (5, 60)])
+def test_long_runs_of_tiles(G, Nq, d):
+    """Many tiles and several units a CTA, from HBM, for every number of rows'
+    variant (1, 45, 100, 256, 300 rows): first, last and a cut unit against the
+    definition, and the same call again bit for bit."""
+    B, Hk, Nk = 2, 50, 6000
+    g = torch.Generator(device="cuda").manual_seed(7)
+    dt = torch.float16
+    k = torch.randn(B, Hk, Nk, d, generator=g, device="cuda", dtype=dt)
+    v = torch.randn(B, Hk, Nk, d, generator=g, device="cuda", dtype=dt)
+    q = torch.randn(B, G * Hk, Nq, d, generator=g, device="cuda", dtype=dt)
+    rows = fa.tree_rows(random_parents(B, Nq, 3))
+    lens = [Nk - Nq, 4321]
+    args = (q, k, v, rows.cuda())
+    o, lse = fa.attention_decode_tree(*args, seqlens_k=counts(lens))
+    for _ in range(20):      # back to back: the last one is compared
+        o2, lse2 = fa.attention_decode_tree(*args, seqlens_k=counts(lens))
+    status_ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for b, hk in ((0, 0), (0, 31), (1, 20), (1, Hk - 1)):
+        hq = slice(hk * G, hk * G + G)
+        masks = [wc.tree_mask(rows[b].tolist(), Nk, lens[b], None, 0)]
+        val, tol = wc.reference(q[b:b + 1, hq].cpu(), k[b:b + 1, hk:hk + 1].cpu(),
+                                v[b:b + 1, hk:hk + 1].cpu(), masks, wc.scale_of(d), "fp16")
+        wc.check(dict(o=o[b:b + 1, hq], lse=lse[b:b + 1, hq]), val, tol, f"batch {b} head {hk}")

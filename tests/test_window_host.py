@@ -143,8 +143,10 @@ static int check_decode(int Nq, int Nk, int count, int win, int sinks, int tree)
     for (int i = 0; i < Nq; ++i) {
       uint32_t vis[4];
       fa::dec_visible(s, d, me[i], tree != 0, win, sinks, vis);
-      const fa::DecWhole w = fa::dec_whole(s, me[i], tree != 0, win);
+      const fa::DecRange w = fa::dec_whole(s, me[i], tree != 0, win);
       const bool all = vis[0] == ~0u && vis[1] == ~0u && vis[2] == ~0u && vis[3] == ~0u;
+      if (t >= w.from && t < w.to && (d.ns || d.nw != 128 || d.key0 != w.base + 128 * t))
+        BAD("tile %d is not plain", t);
       if (t >= w.from && t < w.to && !all) BAD("tile %d is not whole", t);
       if (all && d.ns == 0 && !(t >= w.from && t < w.to) && sinks == 0 && !tree)
         BAD("whole tile %d missed", t);
