@@ -134,7 +134,7 @@ def load_library(path=None):
     lib.fa_fwd_window.restype = i
     lib.fa_bwd_window.argtypes = [vp] * 10 + [i] * 9 + [vp, f, i, vp, ctypes.c_size_t, vp]
     lib.fa_bwd_window.restype = i
-    lib.fa_bwd_window_workspace_size.argtypes = [i] * 7 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_bwd_window_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.fa_bwd_window_workspace_size.restype = i
     lib.fa_decode_window.argtypes = [vp] * 5 + [i] * 8 + [vp, f, i, vp, ctypes.c_size_t, vp]
     lib.fa_decode_window.restype = i
@@ -399,11 +399,12 @@ def fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, delta, B, H, Hk, Nq, Nk, d,
                              _addr(workspace), int(workspace_bytes), _stream(stream))
 
 
-def fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, sinks):
+def fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, window, sinks):
     """Workspace bytes fa_bwd_window needs for this shape."""
     out = ctypes.c_size_t(0)
     code = load_library().fa_bwd_window_workspace_size(int(B), int(H), int(Hk), int(Nq), int(Nk),
-                                                       int(d), int(sinks), ctypes.byref(out))
+                                                       int(d), int(window), int(sinks),
+                                                       ctypes.byref(out))
     if code:
         raise FaError(code, "fa_bwd_window_workspace_size")
     return out.value
@@ -1021,7 +1022,8 @@ def attention_backward_window(q, k, v, o, lse, dout, window, sinks=0, causal="bo
     _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
     with torch.cuda.device(q.device), _on(stream):
         if workspace is None:
-            need = fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, _int32(sinks))
+            need = fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, _int32(window),
+                                                _int32(sinks))
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
         elif workspace.device != q.device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")

@@ -156,6 +156,14 @@ struct BwdParams {
   int Hk;
   int G;
   int BHk;
+  // Sink tiles (key tiles 0 .. split_tiles - 1 of each key/value head) are
+  // seen by every later query tile, many times the steps of a window's tile,
+  // so each is cut into split_parts items of equal steps that leave fp32 dK
+  // and dV in split_ws ([BHk, split_tiles, split_parts, 128, 2 d]); a last
+  // kernel adds the parts up in order.  split_tiles = 0: nothing is cut.
+  int split_tiles;
+  int split_parts;
+  float* split_ws;
 };
 
 // Tile index and head of work item `blk` among BH * n_tiles items dealt in
@@ -497,6 +505,50 @@ __device__ __forceinline__ void store_acc_cols(uint32_t t_acc, int c0, int nc, i
   }
 }
 
+// One row of a TMEM accumulator (D fp32 columns), times `mul`, to 16-byte
+// aligned fp32.
+template <int D>
+__device__ __forceinline__ void store_acc_f32(uint32_t t_acc, float mul, float* out) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t r[32];
+    ptx::tmem_ld32(t_acc + c, r);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      reinterpret_cast<float4*>(out + c)[v] =
+          make_float4(__uint_as_float(r[4 * v]) * mul, __uint_as_float(r[4 * v + 1]) * mul,
+                      __uint_as_float(r[4 * v + 2]) * mul, __uint_as_float(r[4 * v + 3]) * mul);
+  }
+}
+
+// Adds up the parts of the cut sink tiles (BwdParams::split_ws) in their order
+// and writes dK and dV in the storage dtype: one thread per 4 columns of a
+// row's dK and dV, blocks over (head, sink tile).
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256) fa_bwd_win_parts_kernel(const __grid_constant__ BwdParams p) {
+  constexpr int kPer = 2 * D / 4;   // threads of a row
+  const int bh = blockIdx.x / p.split_tiles, kt = blockIdx.x % p.split_tiles;
+  const int r = blockIdx.y * (256 / kPer) + threadIdx.x / kPer, c = threadIdx.x % kPer * 4;
+  const long long key = static_cast<long long>(kt) * kBwdTile + r;
+  if (key >= p.Nk) return;
+  const float4* src = reinterpret_cast<const float4*>(
+      p.split_ws + (static_cast<size_t>(blockIdx.x) * p.split_parts * kBwdTile + r) * (2 * D) + c);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < p.split_parts; ++i) {
+    const float4 x = src[static_cast<size_t>(i) * (kBwdTile * 2 * D / 4)];
+    a.x += x.x;
+    a.y += x.y;
+    a.z += x.z;
+    a.w += x.w;
+  }
+  uint16_t* out = static_cast<uint16_t*>(c < D ? p.dk : p.dv) +
+                  (static_cast<size_t>(bh) * p.Nk + key) * D + c % D;
+  *reinterpret_cast<uint2*>(out) =
+      make_uint2(ptx::pack2<kBf16>(a.x, a.y), ptx::pack2<kBf16>(a.z, a.w));
+}
+
 // Shared setup of one work item of the tensor-core grid: the ring barriers
 // and, through `init_x(bar)`, the item's own barriers, initialised by the
 // load thread.  The CTA's TMEM is allocated once for all its items.
@@ -667,9 +719,19 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
   // Key tile kt of head bh; for causal runs the first key tiles of a group
   // of heads (the most query tiles to visit) are dealt first.
   int kt, bh;                                // kWin: bh is the key/value head
+  int part = 0, parts = 1;                   // kWin: of a cut sink tile
   if constexpr (kWin) {
-    bh = blk / p.n_ktiles;
-    kt = blk - bh * p.n_ktiles;
+    const int cut = p.BHk * p.split_tiles * p.split_parts;
+    if (blk < cut) {
+      parts = p.split_parts;
+      part = blk % parts;
+      kt = blk / parts % p.split_tiles;
+      bh = blk / (parts * p.split_tiles);
+    } else {
+      const int rest = p.n_ktiles - p.split_tiles;
+      bh = (blk - cut) / rest;
+      kt = p.split_tiles + (blk - cut) - bh * rest;
+    }
   } else {
     bwd_item(p, blk, p.n_ktiles, kt, bh);
   }
@@ -693,13 +755,44 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
   // sequence's rows end at its key count
   const int key_rows = tok ? len : p.Nk;
   const int q_rows = tok ? hd.lenq : p.N;
-  const int nq1 = n_q - i0;                        // query tiles of one head
-  const int nq = kWin ? max(nq1, 0) * p.G : nq1;   // ... of every head that reads this one
-  // query tile and head of step it
-  auto q_tile = [&](int it) { return kWin ? i0 + it % nq1 : i0 + it; };
-  auto q_head = [&](int it) {
-    return kWin ? bh / p.Hk * p.H + bh % p.Hk * p.G + it / nq1 : bh;
+  // Steps: the query tiles i0 .. n_q - 1; kWin: of every head that reads this
+  // one, head after head, and of those the part's share.
+  const int nq1 = n_q - i0;
+  int nq = nq1, it0 = 0;
+  if constexpr (kWin) {
+    const int all = max(nq1, 0) * p.G;
+    it0 = static_cast<int>(static_cast<long long>(all) * part / parts);
+    nq = static_cast<int>(static_cast<long long>(all) * (part + 1) / parts) - it0;
+  }
+  struct Step {
+    int tile, head;   // query tile and head
   };
+  auto first_step = [&]() -> Step {
+    if constexpr (kWin) {
+      if (nq <= 0) return {0, 0};
+      const int g = it0 / nq1;
+      return {i0 + it0 - g * nq1, bh / p.Hk * p.H + bh % p.Hk * p.G + g};
+    }
+    return {i0, bh};
+  };
+  auto next_step = [&](Step& x) {
+    if (++x.tile == n_q && kWin) {
+      x.tile = i0;
+      ++x.head;
+    }
+  };
+  // a cut tile's part: rows of dK (d floats) and dV
+  float* part_ws = nullptr;
+  if constexpr (kWin) {
+    if (parts > 1)
+      part_ws = p.split_ws + ((static_cast<size_t>(bh) * p.split_tiles + kt) * parts + part) *
+                                 (kBwdTile * 2 * D);
+  }
+  if (kWin && nq <= 0 && part_ws != nullptr) {
+    for (int i = threadIdx.x; i < kBwdTile * 2 * D / 4; i += kBwdThreads)
+      reinterpret_cast<float4*>(part_ws)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
   if (kKv && nq <= 0) {
     // no query sees this key tile: its dK and dV rows are zero
     if (threadIdx.x < kBwdEwThreads) {
@@ -726,11 +819,18 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
 
   if (warp == kBwdLoadWarp) {
     if constexpr (kWin) {
-      if (lane == 0)
+      if (lane == 0) {
+        Step at = first_step();
         bwd_producer_map<L>(
             sbase, &p.tm_k, &p.tm_v, [&](int& y, int& z) { y = kt * kBwdTile; z = bh; }, &p.tm_q,
-            &p.tm_do, [&](int it, int& y, int& z) { y = q_tile(it) * kBwdTile; z = q_head(it); },
+            &p.tm_do,
+            [&](int, int& y, int& z) {
+              y = at.tile * kBwdTile;
+              z = at.head;
+              next_step(at);
+            },
             nq, wd);
+      }
     } else if (lane == 0) {
       bwd_producer<L>(sbase, &p.tm_k, &p.tm_v, kt, &p.tm_q, &p.tm_do, i0, nq, bh, wd,
                       tok ? bh % p.H : -1, hd.k0, hd.q0, p.width_qk / 64, p.width_v / 64);
@@ -830,8 +930,9 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     // staged, so the warps do not wait for them; a query past N then gets
     // -LSE = -inf, so its P is 0, and D = 0.
     bool in_next = false;
-    auto fetch = [&](int it, float& lse, float& dd) {
-      const int qrow = q_tile(it) * kBwdTile + t, qh = q_head(it);
+    Step cur = first_step(), nxt = cur;   // the step at work and the one fetched
+    auto fetch = [&](const Step& x, float& lse, float& dd) {
+      const int qrow = x.tile * kBwdTile + t, qh = x.head;
       in_next = qrow < q_rows;
       const int qr = in_next ? qrow : 0;
       const long long qi = bwd_lse_at(p, tok, hd, qh, qr);
@@ -839,7 +940,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       dd = p.delta[tok ? bwd_qrow(p, tok, hd, qh, qr) : qi];
     };
     float lse_next = 0.f, d_next = 0.f;
-    if (half == 0) fetch(0, lse_next, d_next);
+    if (half == 0) fetch(nxt, lse_next, d_next);
     int win_lo = 0, win_hi = 64;   // kWin: this key's queries of the thread's 64, phases 1 to 2
     float pf[64];          // P^T of the current tile, from phase 1 to phase 2
     // dropout: keep bits of this key against the thread's 64 queries, from
@@ -862,14 +963,16 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       if (half == 0) {
         vec[t] = in_next ? -lse_next * 1.4426950408889634f : -INFINITY;   // -LSE, log2 units
         vec[128 + t] = in_next ? d_next : 0.f;
-        if (it + 1 < nq) fetch(it + 1, lse_next, d_next);
       }
+      cur = nxt;
+      next_step(nxt);
+      if (half == 0 && it + 1 < nq) fetch(nxt, lse_next, d_next);
       ptx::named_bar_sync(2, kBwdEwThreads);
     };
 
     // ---- phase 1: P^T = 2^(S^T c - LSE) over this thread's 64 queries
     auto phase1 = [&](int it) {
-      const int i = q_tile(it);
+      const int i = cur.tile;
       const float4* nl4 = reinterpret_cast<const float4*>(vec_of(it)) + half * 16;
       ptx::wait_bounded(xbar(X::kSFull), it & 1, wd, kSiteBwdSFull);
       __syncwarp();
@@ -1034,7 +1137,11 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     __syncwarp();
     ptx::tc_fence_after();
     const long long row = bwd_krow(p, tok, hd, bh, key);
-    if (half == 0)
+    if (part_ws != nullptr)
+      store_acc_f32<D>(tmem_base + lane_off + kColAcc + (half == 0 ? 0 : D),
+                       half == 0 ? 1.f : p.scale,
+                       part_ws + static_cast<size_t>(t) * 2 * D + (half == 0 ? D : 0));
+    else if (half == 0)
       store_acc_cols<kBf16>(tmem_base + lane_off + kColAcc, 0, p.width_v, p.width_v,
                             kDrop ? p.drop_scale : 1.f, p.dv, row, key < key_rows);
     else
@@ -1343,7 +1450,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
-  const int per_pass = (kWin ? p.BHk : p.BH) * p.n_ktiles;   // dK/dV items, one per key tile
+  // dK/dV items, one per key tile (kWin: more for the cut sink tiles)
+  const int per_pass =
+      kWin ? p.BHk * (p.n_ktiles + p.split_tiles * (p.split_parts - 1)) : p.BH * p.n_ktiles;
   const int total = per_pass + p.BH * p.n_tiles;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     if (item < per_pass)

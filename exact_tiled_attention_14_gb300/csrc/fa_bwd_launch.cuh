@@ -83,10 +83,18 @@ cudaError_t launch_bwd_variant(const BwdParams& p, const void* o, const void* do
   e = bwd_smem_attr(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv, kWin>, done, kAlloc);
   if (e != cudaSuccess) return e;
   // dK/dV items (one per key tile) then dQ items (one per query tile)
-  const long long items = static_cast<long long>(kWin ? p.BHk : p.BH) * p.n_ktiles +
-                          static_cast<long long>(p.BH) * p.n_tiles;
-  return launch_bwd_grid(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv, kWin>, p, items, kAlloc, sms,
-                         stream);
+  const long long k_items =
+      kWin ? static_cast<long long>(p.BHk) * (p.n_ktiles + p.split_tiles * (p.split_parts - 1))
+           : static_cast<long long>(p.BH) * p.n_ktiles;
+  const long long items = k_items + static_cast<long long>(p.BH) * p.n_tiles;
+  e = launch_bwd_grid(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv, kWin>, p, items, kAlloc, sms,
+                      stream);
+  if (e != cudaSuccess || !kWin || p.split_tiles == 0) return e;
+  if constexpr (kWin) {
+    const dim3 blocks(static_cast<unsigned>(p.BHk * p.split_tiles), kBwdTile * 2 * D / 4 / 256);
+    fa_bwd_win_parts_kernel<D, kBf16><<<blocks, 256, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 // The one-pass backward (square calls): the fp32 dQ accumulator p.dq_acc

@@ -30,11 +30,33 @@ int check_window_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int causal, 
   const long long bh = static_cast<long long>(B) * H;
   const long long tiles = (static_cast<long long>(Nq) + fa::kBM - 1) / fa::kBM +
                           (static_cast<long long>(Nk) + fa::kBN - 1) / fa::kBN;
-  if (bh > kMaxLen || bh * tiles > kMaxLen) return FA_ERR_SHAPE;
+  // (a sink tile is cut into at most 64 parts, each a work item)
+  if (bh > kMaxLen || bh * tiles > kMaxLen / 64) return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_SCALE;
   return FA_OK;
+}
+
+// Cut of the sink tiles of the backward pass: every query tile after a sink
+// tile visits it, where a window's tile is visited by about window / 128 + 2,
+// and the CTAs' work is dealt by items.  So a sink tile is cut into as many
+// parts as give each the steps of a window's tile (measured on B1 H32/8 N16384
+// window 2048, 64 sinks: uncut, 8 of 152 CTAs hold one item with half of a
+// CTA's whole share, figures in fa_bwd_win.cu).
+struct SinkSplit {
+  int tiles = 0, parts = 1;
+};
+SinkSplit sink_split(int Nq, int Nk, int window, int sinks) {
+  SinkSplit s;
+  const long long q_tiles = (static_cast<long long>(Nq) + fa::kBwdTile - 1) / fa::kBwdTile;
+  const long long per = static_cast<long long>(window) / fa::kBwdTile + 2;
+  const long long parts = std::min<long long>((q_tiles + per - 1) / per, 64);
+  const int used = std::min(sinks, Nk);
+  if (used == 0 || parts < 2) return s;
+  s.tiles = (used + fa::kBwdTile - 1) / fa::kBwdTile;
+  s.parts = static_cast<int>(parts);
+  return s;
 }
 
 bool misaligned(const void* p, uintptr_t bytes) {
@@ -109,12 +131,13 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
   return fa::launch_fwd_win(p, grid, d, bf16, stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, int sinks,
+int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, int window, int sinks,
                                  size_t* bytes) {
   if (!bytes) return FA_ERR_NULLPTR;
-  const int rc = check_window_sizes(B, H, Hk, Nq, Nk, d, 1, 1, sinks, 1.0f, FA_BF16);
+  const int rc = check_window_sizes(B, H, Hk, Nq, Nk, d, 1, window, sinks, 1.0f, FA_BF16);
   if (rc != FA_OK) return rc;
-  *bytes = 0;
+  const SinkSplit sp = sink_split(Nq, Nk, window, sinks);
+  *bytes = static_cast<size_t>(B) * Hk * sp.tiles * sp.parts * fa::kBwdTile * 2 * d * sizeof(float);
   return FA_OK;
 }
 
@@ -133,7 +156,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
       misaligned(lse, 4) || misaligned(delta, 4) || misaligned(seqlens_k, 4))
     return FA_ERR_ALIGN;
   size_t need = 0;
-  fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, sinks, &need);
+  fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, window, sinks, &need);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return FA_ERR_ALIGN;
@@ -181,6 +204,10 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   p.Hk = Hk;
   p.G = H / Hk;
   p.BHk = bhk;
+  const SinkSplit sp = sink_split(Nq, Nk, window, sinks);
+  p.split_tiles = sp.tiles;
+  p.split_parts = sp.parts;
+  p.split_ws = static_cast<float*>(workspace);
   return fa::launch_bwd_win(p, o, dout, delta, d, bf16, info->sms, stream) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;

@@ -584,8 +584,8 @@ int fa_decode_workspace_size(int B, int H, int Nq, int Nk, int d, size_t *bytes)
  * anything (NaN included).  A value that some row of the block sees must be
  * finite for the block's other rows to be, as in every entry point here.
  * Errors as fa_fwd; FA_ERR_SHAPE also for H not a multiple of Hk, causal
- * other than 1 or 2, window < 1, sinks < 0, and Nq + Nk, B * H or B * H
- * times the 128-row tiles of both over 2^30.  B * H * Nq == 0 writes nothing.
+ * other than 1 or 2, window < 1, sinks < 0, Nq + Nk or B * H over 2^30, and
+ * B * H times the 128-row tiles of both over 2^24.  B * H * Nq == 0 writes nothing.
  */
 int fa_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
                   int Hk, int Nq, int Nk, int d, int causal, int window, int sinks,
@@ -615,10 +615,11 @@ int fa_bwd_window(const void *q, const void *k, const void *v, const void *o, co
 
 /*
  * fa_bwd_window_workspace_size — bytes of workspace fa_bwd_window needs for
- * this shape.  Host-only.  Returns FA_ERR_NULLPTR, FA_ERR_SHAPE or
+ * this shape: fp32 parts of dK and dV of the sink tiles, 0 without sinks or
+ * for short queries.  Host-only.  Returns FA_ERR_NULLPTR, FA_ERR_SHAPE or
  * FA_ERR_UNSUPPORTED_D.
  */
-int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, int sinks,
+int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, int window, int sinks,
                                  size_t *bytes);
 
 /*
