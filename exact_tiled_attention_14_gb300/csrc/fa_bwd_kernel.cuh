@@ -1002,10 +1002,14 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
         const int qb = i * kBwdTile + half * 64;
         win_lo = key >= len ? 64 : static_cast<int>(key) - off - qb;
         win_hi = key < p.sinks ? 64 : static_cast<int>(key) + p.win - off - qb;
-        if (win_lo > 0 || win_hi < 64) {
+        // (one compare and one select a query and end; no short circuits)
+        if (win_lo > 0) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < win_lo || e >= win_hi) pf[e] = 0.f;
+          for (int e = 0; e < 64; ++e) pf[e] = e < win_lo ? 0.f : pf[e];
+        }
+        if (win_hi < 64) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) pf[e] = e >= win_hi ? 0.f : pf[e];
         }
         // Rows at negative positions see no key, nor (without sinks) do rows
         // whose window starts past the batch's keys.  Whatever their Q and dO
@@ -1112,12 +1116,15 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       if constexpr (kWin) {
         // a select, not a product with the masked P: dP - D of a key outside
         // its batch's count need not be finite
-        if (win_lo > 0 || win_hi < 64) {
+        if (win_lo > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (2 * e < win_lo || 2 * e >= win_hi) dk[e] &= 0xffff0000u;
-            if (2 * e + 1 < win_lo || 2 * e + 1 >= win_hi) dk[e] &= 0xffffu;
-          }
+          for (int e = 0; e < 32; ++e)
+            dk[e] &= (2 * e < win_lo ? 0u : 0xffffu) | (2 * e + 1 < win_lo ? 0u : 0xffff0000u);
+        }
+        if (win_hi < 64) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            dk[e] &= (2 * e >= win_hi ? 0u : 0xffffu) | (2 * e + 1 >= win_hi ? 0u : 0xffff0000u);
         }
       }
       ptx::tmem_st16(tDp, dk);           // over dP^T columns this warp has read
@@ -1396,12 +1403,17 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         // need not be finite): past the position, or before the window and
         // not a sink
         const int sink = p.sinks - k_tile(j) * kBwdTile - half * 64;
-        if (lim < 64 || (lo > 0 && sink < 64)) {
+        if (lo >= 64) lim = min(lim, sink);
+        if (lim < 64) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (2 * e >= lim || (2 * e < lo && 2 * e >= sink)) dk[e] &= 0xffff0000u;
-            if (2 * e + 1 >= lim || (2 * e + 1 < lo && 2 * e + 1 >= sink)) dk[e] &= 0xffffu;
-          }
+          for (int e = 0; e < 32; ++e)
+            dk[e] &= (2 * e >= lim ? 0u : 0xffffu) | (2 * e + 1 >= lim ? 0u : 0xffff0000u);
+        }
+        if (lo > 0 && lo < 64) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            dk[e] &= ((2 * e < lo) & (2 * e >= sink) ? 0u : 0xffffu) |
+                     ((2 * e + 1 < lo) & (2 * e + 1 >= sink) ? 0u : 0xffff0000u);
         }
       }
       // dS to its TMEM buffer once the tensor core has read what it held

@@ -287,38 +287,6 @@ struct DwRing {
   }
 };
 
-// Bits [a, b) of 128 as four words.
-__host__ __device__ __forceinline__ void or_range(uint32_t* w, int a, int b) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int lo = a - 32 * k, hi = b - 32 * k;
-    lo = lo < 0 ? 0 : (lo > 32 ? 32 : lo);
-    hi = hi < 0 ? 0 : (hi > 32 ? 32 : hi);
-    const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
-    const uint32_t below_lo = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
-    w[k] |= below_hi & ~below_lo;
-  }
-}
-// 64 bits m at bit position at (-63 .. 127) of 128, cut to [0, 128).
-__host__ __device__ __forceinline__ void or_bits(uint32_t* w, unsigned long long m, int at) {
-  unsigned long long lo = 0, hi = 0;
-  if (at <= -64 || at >= kDwTile) return;
-  if (at < 0) {
-    lo = m >> -at;
-  } else if (at == 0) {
-    lo = m;
-  } else if (at < 64) {
-    lo = m << at;
-    hi = m >> (64 - at);
-  } else {
-    hi = m << (at - 64);
-  }
-  w[0] |= static_cast<uint32_t>(lo);
-  w[1] |= static_cast<uint32_t>(lo >> 32);
-  w[2] |= static_cast<uint32_t>(hi);
-  w[3] |= static_cast<uint32_t>(hi >> 32);
-}
-
 // What one row sees: its position and, of a tree, the drafted tokens.
 struct DecRow {
   int pos;
@@ -360,28 +328,29 @@ __host__ __device__ __forceinline__ DecRange dec_whole(const DecSpan& s, const D
                                                        int win) {
   return dec_plain(s, r.pos - win + 1, tree ? s.len : r.pos + 1);
 }
-// Visible columns of tile tl for a row, as 128 bits.
+// Visible columns 32 q .. 32 q + 31 of tile tl for a row, as bits.
 // seen: keys of the span part up to the row's position (tree: its history).
-__host__ __device__ __forceinline__ void dec_visible(const DecSpan& s, const DecTile& tl,
-                                                     const DecRow& r, bool tree, int win, int sinks,
-                                                     uint32_t* vis) {
+__host__ __device__ __forceinline__ uint32_t dec_visible(const DecSpan& s, const DecTile& tl,
+                                                         const DecRow& r, bool tree, int win,
+                                                         int sinks, int q) {
+  const int c = 32 * q;
   const int upto = (tree ? s.len : r.pos + 1) - tl.key0;
   const int seen = tl.nw < upto ? tl.nw : upto;
   const int first = r.pos - win + 1 - tl.key0;
-  vis[0] = vis[1] = vis[2] = vis[3] = 0u;
   const int ns = s.sink - tl.sink0 < tl.ns ? s.sink - tl.sink0 : tl.ns;
-  or_range(vis, 0, ns);                                           // the sinks before the span
-  or_range(vis, tl.ns + (first > 0 ? first : 0), tl.ns + seen);   // the row's window
-  or_range(vis, tl.ns, tl.ns + (sinks - tl.key0 < seen ? sinks - tl.key0 : seen));
+  const int sk = sinks - tl.key0 < seen ? sinks - tl.key0 : seen;
+  uint32_t vis = ptx::bit_range(-c, ns - c) |                              // sinks before the span
+                 ptx::bit_range(tl.ns + (first > 0 ? first : 0) - c, tl.ns + seen - c) |   // window
+                 ptx::bit_range(tl.ns - c, tl.ns + sk - c);                // sinks in the span
   if (tree) {
     // drafted token 0 sits at column ns + len - key0
-    uint32_t dv[4] = {0u, 0u, 0u, 0u}, in[4] = {0u, 0u, 0u, 0u};
-    const int at = tl.ns + s.len - tl.key0;
-    or_bits(dv, r.bits, at);
-    or_range(in, tl.ns, tl.ns + tl.nw);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) vis[k] |= dv[k] & in[k];
+    const long long at = static_cast<long long>(tl.ns) + s.len - tl.key0 - c;
+    uint32_t dv = 0;
+    if (at > -64 && at <= 0) dv = static_cast<uint32_t>(r.bits >> -at);
+    if (at > 0 && at < 32) dv = static_cast<uint32_t>(r.bits) << at;
+    vis |= dv & ptx::bit_range(tl.ns - c, tl.ns + tl.nw - c);
   }
+  return vis;
 }
 
 template <int D, bool kBf16, int kTiles, int kCopies>
@@ -818,6 +787,14 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           ++scnt;
           __syncwarp();
           ptx::tc_fence_after();
+          if (__any_sync(0xffffffffu, pc.t0 + j < whole.from || pc.t0 + j >= whole.to)) {
+            const DecTile tl = dec_tile(pc.s, pc.t0 + j);
+            const DecRow me = my_row();
+            ptx::tmem_mask_scores(tS, kCols / 32, [&](int q) {
+              return dec_visible(pc.s, tl, me, p.tree != nullptr, p.win, p.sinks,
+                                 seg * (kCols / 32) + q);
+            });
+          }
           uint32_t sr[kCols];
 #pragma unroll
           for (int q4 = 0; q4 < kCols / 32; ++q4) ptx::tmem_ld32(tS + q4 * 32, sr + q4 * 32);
@@ -828,20 +805,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           if (L::kOwnP) {
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar(L::bSFree + w));       // S_w may be overwritten now
-          }
-          if (pc.t0 + j < whole.from || pc.t0 + j >= whole.to) {
-            uint32_t vis[4];
-            dec_visible(pc.s, dec_tile(pc.s, pc.t0 + j), my_row(), p.tree != nullptr, p.win, p.sinks,
-                        vis);
-            if constexpr (kCopies == 4)
-              vis[0] = seg < 2 ? (seg ? vis[1] : vis[0]) : (seg == 2 ? vis[2] : vis[3]);
-            if constexpr (kCopies == 2) {
-              vis[0] = seg ? vis[2] : vis[0];
-              vis[1] = seg ? vis[3] : vis[1];
-            }
-#pragma unroll
-            for (int e = 0; e < kCols; ++e)
-              if (!((vis[e >> 5] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
           }
           float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll

@@ -1095,6 +1095,16 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         if (tracer) trace_event(p, w, tr, kEvSReady, j);
         __syncwarp();
         ptx::tc_fence_after();
+        if constexpr (kWin) {
+          // keys lo .. lim - 1 of the window and, of those before it, the sinks
+          const int pos = row + u.off, key0 = win_tile(u, jl) * kBN;
+          const int lim = min(u.len, pos + 1) - key0, lo = pos - p.win + 1 - key0;
+          const int sink = min(p.sinks - key0, lim);
+          if (__any_sync(0xffffffffu, lim < kBN || (lo > 0 && sink < kBN)))
+            ptx::tmem_mask_scores(tS, kBN / 32, [&](int q) {
+              return ptx::bit_range(lo - 32 * q, lim - 32 * q) | ptx::bit_range(0, sink - 32 * q);
+            });
+        }
         uint32_t sr[kBN];
 #pragma unroll
         for (int q4 = 0; q4 < kBN / 32; ++q4) ptx::tmem_ld32(tS + q4 * 32, sr + q4 * 32);
@@ -1109,15 +1119,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         // mask: keys past N, and on the diagonal tile keys after this row
         const int kj = kWin ? win_tile(u, jl) : u.kb + jl;   // key tile index
         if constexpr (kWin) {
-          // keys lo .. lim - 1 of the window and, of those before it, the sinks
-          const int pos = row + u.off, key0 = kj * kBN;
-          const int lim = min(kBN, min(u.len, pos + 1) - key0);
-          const int lo = pos - p.win + 1 - key0, sink = p.sinks - key0;
-          if (lim < kBN || (lo > 0 && sink < kBN)) {
-#pragma unroll
-            for (int i = 0; i < kBN; ++i)
-              if (i >= lim || (i < lo && i >= sink)) sv[i] = -INFINITY;
-          }
+          // masked in TMEM, before the scores were read
         } else if constexpr (kKv) {
           // keys past this batch's count, and keys after this row's position
           int lim = min(kBN, u.len - kj * kBN);

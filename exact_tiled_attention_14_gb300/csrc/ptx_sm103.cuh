@@ -255,6 +255,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+// Bits [a, b) of a word (any a, b).
+__host__ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
+  a = a < 0 ? 0 : (a > 32 ? 32 : a);
+  b = b < 0 ? 0 : (b > 32 ? 32 : b);
+  const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u;
+  const uint32_t below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
 // registers -> 32 consecutive 32-bit TMEM columns of this thread's lane.
 // 32 lanes x 16 columns of 32 bits from 16 registers per thread (this warp's lanes).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -276,6 +285,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+// Overwrite with -inf the scores of this thread's lane whose bit is clear:
+// word(q) holds the bits of columns 32 q .. 32 q + 31 of the 32 * chunks from
+// taddr on.  A rolled loop through TMEM: one unrolled over 128 score
+// registers is some 8 KB of code that only masked tiles run, and fetching it
+// costs more than the round trip.
+template <class Word>
+__device__ __forceinline__ void tmem_mask_scores(uint32_t taddr, int chunks, Word word) {
+#pragma unroll 1
+  for (int q = 0; q < chunks; ++q) {
+    uint32_t r[32];
+    tmem_ld32(taddr + 32 * q, r);
+    const uint32_t keep = word(q);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r[e] = (keep >> e) & 1u ? r[e] : 0xff800000u;
+    tmem_st32(taddr + 32 * q, r);
+  }
+  tmem_wait_st();
 }
 
 // ---------------------------------------------------------------- descriptors

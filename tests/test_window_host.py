@@ -142,7 +142,8 @@ static int check_decode(int Nq, int Nk, int count, int win, int sinks, int tree)
     if (d.ns && d.sink0 + d.ns > s.sink_rows) BAD("sink rows");
     for (int i = 0; i < Nq; ++i) {
       uint32_t vis[4];
-      fa::dec_visible(s, d, me[i], tree != 0, win, sinks, vis);
+      for (int q = 0; q < 4; ++q)
+        vis[q] = fa::dec_visible(s, d, me[i], tree != 0, win, sinks, q);
       const fa::DecRange w = fa::dec_whole(s, me[i], tree != 0, win);
       const bool all = vis[0] == ~0u && vis[1] == ~0u && vis[2] == ~0u && vis[3] == ~0u;
       if (t >= w.from && t < w.to && (d.ns || d.nw != 128 || d.key0 != w.base + 128 * t))
