@@ -538,16 +538,16 @@ struct TailWalk {
 // Output row of query row `row` of piece u (O is addressed in rows of the
 // value width) and its LSE element: [B, H, N, .] and [B, H, N], or with
 // packed batches [total_q, H, .] and [H, total_q].
-template <bool kKv>
+template <bool kKv, bool kWin = false>
 __device__ __forceinline__ size_t out_row(const FwdParams& p, const Piece& u, int row) {
-  if constexpr (kKv) {
+  if constexpr (kKv && !kWin) {
     if (p.varlen) return static_cast<size_t>(u.q0 + row) * p.H + (u.bh % p.H);
   }
   return static_cast<size_t>(u.bh) * p.N + row;
 }
-template <bool kKv>
+template <bool kKv, bool kWin = false>
 __device__ __forceinline__ size_t lse_at(const FwdParams& p, const Piece& u, int row) {
-  if constexpr (kKv) {
+  if constexpr (kKv && !kWin) {
     if (p.varlen) return static_cast<size_t>(u.bh % p.H) * p.total_q + u.q0 + row;
   }
   return static_cast<size_t>(u.bh) * p.N + row;
@@ -697,11 +697,11 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             const int ntile = u.n1 > 0 ? 2 : 1;
             // kKv with d < D: only the chunks of Q's own columns are loaded
             // (the S products never read the others)
-            const int qc = kKv ? p.dqk / 64 : L::kChunks;
+            const int qc = kKv && !kWin ? p.dqk / 64 : L::kChunks;
             ptx::mbar_arrive_expect_tx(bar(L::bQFull + qb), ntile * qc * L::kChunkBytes);
             for (int w = 0; w < ntile; ++w) {
               int y = (2 * u.mblk + w) * kBM, z = u.bh;      // row, batch*head
-              if (kKv && p.varlen) { z = u.q0 + y; y = u.bh % p.H; }   // head, token
+              if (kKv && !kWin && p.varlen) { z = u.q0 + y; y = u.bh % p.H; }   // head, token
               for (int c = 0; c < qc; ++c)
                 ptx::tma_load_3d(sbase + L::kQ + (qb * 2 + w) * L::kTile + c * L::kChunkBytes,
                                  &p.tm_q, bar(L::bQFull + qb), c * 64, y, z);
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
                     alive;
           if (alive) {
             // kKv: only the chunks of the tensor's own width (d for K, dv for V)
-            const int nc = kKv ? (kv ? p.dv : p.dqk) / 64 : L::kChunks;
+            const int nc = kKv && !kWin ? (kv ? p.dv : p.dqk) / 64 : L::kChunks;
             const uint32_t full = bar((kv ? L::bVFull : L::bKFull) + slot);
             if constexpr (L::kTwoFull) {
               (kv ? v_odd : k_odd) ^= 1u << slot;
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
             if constexpr (kWin) { y = win_tile(u, j) * kBN; z = kv_head(p, u.bh); }
-            if (kKv && p.varlen) { z = u.k0 + y; y = u.bh % p.H; }   // head, token
+            if (kKv && !kWin && p.varlen) { z = u.k0 + y; y = u.bh % p.H; }   // head, token
             for (int c = 0; c < nc; ++c)
               ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm, full,
                                c * 64, y, z);
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       constexpr uint32_t idesc_o_full = ptx::idesc_f16(kBM, D, fmt, 1);  // P x V (MN-major)
       // a value width below D (kKv) computes only dv columns of O
       const uint32_t idesc_o =
-          (kKv && p.dv < D) ? ptx::idesc_f16(kBM, 64, fmt, 1) : idesc_o_full;
+          (kKv && !kWin && p.dv < D) ? ptx::idesc_f16(kBM, 64, fmt, 1) : idesc_o_full;
       // Address words of the shared-memory descriptors (start >> 4 | LBO >> 4 << 16).
       const uint32_t q_lo0 = ptx::desc_lo(sbase + L::kQ, 16);
       const uint32_t q_lo1 = ptx::desc_lo(sbase + L::kQ + L::kTile, 16);
@@ -787,11 +787,11 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       // S = Q_w K^T over the head width: K-major operands, 128-byte swizzle;
       // a K step of 16 columns moves 32 bytes inside a swizzle row, and every
       // 64 columns start a new chunk.
-      const int s_steps = kKv ? p.dqk / 16 : D / 16;   // K steps of S (columns of Q, K / 16)
+      const int s_steps = kKv && !kWin ? p.dqk / 16 : D / 16;   // K steps of S (columns of Q, K / 16)
       auto issue_s = [&](uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          if (kKv && kk >= s_steps) break;
+          if (kKv && !kWin && kk >= s_steps) break;
           const uint32_t off = static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
           ptx::mma_ss(d_tmem, ptx::desc_sw128(q_lo + off), ptx::desc_sw128(k_lo + off), idesc_s,
                       kk > 0);
@@ -979,21 +979,22 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         // of such keys in the loaded V tile are overwritten with zeros first.
         // These are the first and last tiles of the list and the last sink
         // tile; the tensor core meanwhile works on S and the softmax on P.
-        // Lane 0 alone waits on barriers and the warp joins it afterwards: a
-        // lane that polled on its own could miss a phase that lane 0's
-        // progress lets pass twice.
+        // Lane 0 alone waits on barriers, and the other lanes join it only at
+        // such tiles: a lane that polled on its own could miss a phase that
+        // lane 0's progress lets pass twice.
         while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
           const int nkv = u.nl;
           if (nkv == 0) continue;
           int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
           for (int j = 0; j < nkv; ++j) {
+            const int kt = win_tile(u, j), key0 = kt * kBN;
+            const bool cut = key0 + kBN > u.hi || (key0 < u.lo && key0 + kBN > p.sinks);
+            if (!cut && lane != 0) continue;
             const uint32_t vpos = base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u);
             const uint32_t vslot = vpos % L::kStages;
             if (lane == 0) ring_wait(vpos);
-            __syncwarp();
-            const int kt = win_tile(u, j), key0 = kt * kBN;
-            const bool past = key0 + kBN > u.hi, before = key0 < u.lo && key0 + kBN > p.sinks;
-            if (past || before) {
+            if (cut) {
+              __syncwarp();
               const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
               const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
               const int r_sink = min(max(p.sinks - key0, 0), r_lo);
@@ -1008,17 +1009,14 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
               ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
               __syncwarp();
             }
+            if (lane != 0) continue;
             const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
-            const bool act0 = win_active(u, 0, kt), act1 = win_active(u, 1, kt);
-            if (lane == 0) {
-              if (act0) issue_pv_own(0, it0, v_lo);
-              if (act1) issue_pv_own(1, it1, v_lo);
-              if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
-              issued_any = true;
-            }
-            it0 += act0;
-            it1 += act1;
+            if (win_active(u, 0, kt)) issue_pv_own(0, it0++, v_lo);
+            if (win_active(u, 1, kt)) issue_pv_own(1, it1++, v_lo);
+            if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
+            issued_any = true;
           }
+          __syncwarp();
           if (u.n0 > 0) ++ucnt0;
           if (u.n1 > 0) ++ucnt1;
           base += 2u * nkv;
@@ -1061,18 +1059,27 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     Piece u;
     while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
       const int n = w ? u.n1 : u.n0;          // key tiles of this query tile
-      const int nlist = kWin ? u.nl : n;      // key tiles streamed (kWin: some for the other tile)
       const int tile = 2 * u.mblk + w;
       const int row = tile * kBM + t;
+      // kWin: its key tiles are the sink tiles 0 .. win_ns - 1, then j + win_skip;
+      // this row sees keys win_lo .. win_lim - 1 and the sinks before them
+      int win_ns = 0, win_skip = 0, win_lim = 0, win_lo = 0;
+      if constexpr (kWin) {
+        win_ns = min(u.n_sink, w ? u.e1 : u.e0);
+        win_skip = max(w ? u.a1 : u.a0, u.n_sink) - win_ns;
+        win_lim = min(u.len, row + u.off + 1);
+        win_lo = row + u.off - p.win + 1;
+      }
+      const int rows_q = kWin ? p.N : u.lenq;   // queries of this head (kWin is never packed)
       if (n == 0) {
         if constexpr (kKv) {
           // a query tile that sees no key: O = 0 and LSE = -inf (the policy
           // for an empty key set)
-          if (row < u.lenq) {
+          if (row < rows_q) {
             uint4* orow = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) +
-                                                   out_row<kKv>(p, u, row) * (p.dv * 2));
+                                                   out_row<kKv, kWin>(p, u, row) * (p.dv * 2));
             for (int v = 0; v < p.dv / 8; ++v) orow[v] = make_uint4(0u, 0u, 0u, 0u);
-            p.lse[lse_at<kKv>(p, u, row)] = -INFINITY;
+            p.lse[lse_at<kKv, kWin>(p, u, row)] = -INFINITY;
           }
         }
         continue;
@@ -1081,12 +1088,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       float m_ref = -INFINITY;  // reference maximum of the raw scores q.k
       float neg_m = 0.f;        // -m_ref * c (0 while m_ref is -inf)
       float l = 0.f;            // running sum of 2^(s*c + neg_m)
-      int j = -1;               // key tiles of this query tile before the current one
-      for (int jl = 0; jl < nlist; ++jl) {
-        if constexpr (kWin) {
-          if (!win_active(u, w, win_tile(u, jl))) continue;
-        }
-        ++j;
+      for (int j = 0; j < n; ++j) {
         pf.lap(7);
         ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteSFull);
         pf.lap(0);
@@ -1097,8 +1099,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         ptx::tc_fence_after();
         if constexpr (kWin) {
           // keys lo .. lim - 1 of the window and, of those before it, the sinks
-          const int pos = row + u.off, key0 = win_tile(u, jl) * kBN;
-          const int lim = min(u.len, pos + 1) - key0, lo = pos - p.win + 1 - key0;
+          const int key0 = (j < win_ns ? j : j + win_skip) * kBN;
+          const int lim = win_lim - key0, lo = win_lo - key0;
           const int sink = min(p.sinks - key0, lim);
           if (__any_sync(0xffffffffu, lim < kBN || (lo > 0 && sink < kBN)))
             ptx::tmem_mask_scores(tS, kBN / 32, [&](int q) {
@@ -1117,7 +1119,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         pf.lap(1);
 
         // mask: keys past N, and on the diagonal tile keys after this row
-        const int kj = kWin ? win_tile(u, jl) : u.kb + jl;   // key tile index
+        const int kj = u.kb + j;                 // key tile index
         if constexpr (kWin) {
           // masked in TMEM, before the scores were read
         } else if constexpr (kKv) {
@@ -1420,7 +1422,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           pf.lap(13);
         }
         pf.count(15);
-      } else if (L::kTmaStore && !(kKv && p.varlen)) {
+      } else if (L::kTmaStore && (kWin || !(kKv && p.varlen))) {
         // through a swizzled staging tile and a TMA store (rows past N
         // clipped; packed batches, whose tiles end mid-tensor, store directly)
         if (t == 0) ptx::bulk_wait_group_read0();   // staging tile free again
@@ -1458,10 +1460,10 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       } else {
         // straight from registers: each thread writes its own row (of dv
         // columns in the kKv variants)
-        const int ocols = kKv ? p.dv : D;
+        const int ocols = kKv && !kWin ? p.dv : D;
         uint4* orow = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.o) +
-                                               out_row<kKv>(p, u, row) * (ocols * 2));
-        const int nrows = kKv ? u.lenq : p.N;
+                                               out_row<kKv, kWin>(p, u, row) * (ocols * 2));
+        const int nrows = kKv ? rows_q : p.N;
 #pragma unroll 1
         for (int q4 = 0; q4 < ocols / 32; ++q4) {
           uint32_t orr[32];
@@ -1486,8 +1488,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(L::bOFree + w));        // O_w may be overwritten now
       }
-      if ((!kSplit || u.tail < 0) && row < (kKv ? u.lenq : p.N))
-        p.lse[lse_at<kKv>(p, u, row)] = l > 0.f ? (ptx::lg2(l) - neg_m) * kLn2 : -INFINITY;
+      if ((!kSplit || u.tail < 0) && row < (kKv ? rows_q : p.N))
+        p.lse[lse_at<kKv, kWin>(p, u, row)] = l > 0.f ? (ptx::lg2(l) - neg_m) * kLn2 : -INFINITY;
       if (tracer) trace_event(p, w, tr, kEvEpiEnd, ucnt - 1);
       pf.lap(6);
     }
