@@ -710,6 +710,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             trace_event(p, 3, tr, kEvLoadQ, k_units);
           }
         };
+        const int kvh = kWin ? kv_head(p, u.bh) : 0;   // divisions once a unit
         auto load_kv = [&](int kv, int j) {
           const uint32_t slot = loads % L::kStages, use = loads / L::kStages;
           if (use > 0)
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             ptx::mbar_arrive_expect_tx(full, nc * L::kChunkBytes);
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
-            if constexpr (kWin) { y = win_tile(u, j) * kBN; z = kv_head(p, u.bh); }
+            if constexpr (kWin) { y = win_tile(u, j) * kBN; z = kvh; }
             if (kKv && !kWin && p.varlen) { z = u.k0 + y; y = u.bh % p.H; }   // head, token
             for (int c = 0; c < nc; ++c)
               ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm, full,
@@ -1097,15 +1098,26 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         if (tracer) trace_event(p, w, tr, kEvSReady, j);
         __syncwarp();
         ptx::tc_fence_after();
+        // kWin: keys lo .. lim - 1 of the window and, of those before it, the
+        // sinks.  Applied to the scores in registers at d = 64 and in TMEM,
+        // before they are read, at d = 128 (B4 H16/4 N4096 d64 window 1024:
+        // 126.6 us against 132.0 through TMEM; B1 H32/8 N16384 d128 window
+        // 2048: 464 us through TMEM against 482).
+        constexpr bool kMaskTmem = kWin && D == 128;
+        int key0 = 0, lim = 0, lo = 0, sink = 0;
+        bool cut = false;
         if constexpr (kWin) {
-          // keys lo .. lim - 1 of the window and, of those before it, the sinks
-          const int key0 = (j < win_ns ? j : j + win_skip) * kBN;
-          const int lim = win_lim - key0, lo = win_lo - key0;
-          const int sink = min(p.sinks - key0, lim);
-          if (__any_sync(0xffffffffu, lim < kBN || (lo > 0 && sink < kBN)))
-            ptx::tmem_mask_scores(tS, kBN / 32, [&](int q) {
-              return ptx::bit_range(lo - 32 * q, lim - 32 * q) | ptx::bit_range(0, sink - 32 * q);
-            });
+          key0 = (j < win_ns ? j : j + win_skip) * kBN;
+          lim = win_lim - key0;
+          lo = win_lo - key0;
+          sink = min(p.sinks - key0, lim);
+          cut = lim < kBN || (lo > 0 && sink < kBN);
+        }
+        auto keep_word = [&](int q) {
+          return ptx::bit_range(lo - 32 * q, lim - 32 * q) | ptx::bit_range(0, sink - 32 * q);
+        };
+        if constexpr (kMaskTmem) {
+          if (__any_sync(0xffffffffu, cut)) ptx::tmem_mask_scores(tS, kBN / 32, keep_word);
         }
         uint32_t sr[kBN];
 #pragma unroll
@@ -1121,7 +1133,15 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         // mask: keys past N, and on the diagonal tile keys after this row
         const int kj = u.kb + j;                 // key tile index
         if constexpr (kWin) {
-          // masked in TMEM, before the scores were read
+          if (!kMaskTmem && cut) {
+#pragma unroll
+            for (int q = 0; q < kBN / 32; ++q) {
+              const uint32_t keep = keep_word(q);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                sv[32 * q + e] = (keep >> e) & 1u ? sv[32 * q + e] : -INFINITY;
+            }
+          }
         } else if constexpr (kKv) {
           // keys past this batch's count, and keys after this row's position
           int lim = min(kBN, u.len - kj * kBN);

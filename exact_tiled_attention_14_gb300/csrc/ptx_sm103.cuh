@@ -296,9 +296,10 @@ template <class Word>
 __device__ __forceinline__ void tmem_mask_scores(uint32_t taddr, int chunks, Word word) {
 #pragma unroll 1
   for (int q = 0; q < chunks; ++q) {
+    const uint32_t keep = word(q);
+    if (!__any_sync(0xffffffffu, keep != 0xffffffffu)) continue;   // the warp sees them all
     uint32_t r[32];
     tmem_ld32(taddr + 32 * q, r);
-    const uint32_t keep = word(q);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 32; ++e) r[e] = (keep >> e) & 1u ? r[e] : 0xff800000u;
