@@ -302,16 +302,19 @@ __device__ __forceinline__ uint32_t o_col(int w) { return 256u + (w ? D : 0); }
 template <int D>
 __device__ __forceinline__ uint32_t p_col(int w) { return 256u + 2u * D + (w ? 64u : 0u); }
 
+__host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
+
 struct Unit {
   int bh, mblk, n0, n1;
   int len, off;   // keys of this head; position of query row r is r + off (kKv)
   int lenq, q0, k0;   // queries of this head; first query and key token (varlen)
   // kWin: the list of key tiles the unit streams is the sink tiles 0 .. ns - 1,
-  // then wa, wa + 1, ... (nl tiles in all); query tile w computes the ones
-  // win_active() names: sink tiles below n_sink and tiles a_w .. e_w - 1.  Of
-  // the keys in them some row of the unit sees those below min(sinks, hi)
-  // and lo .. hi - 1.
-  int ns, wa, nl, n_sink, a0, a1, e0, e1, lo, hi;
+  // then wa, wa + 1, ... (nl tiles in all).  Query tile 0 computes the first
+  // n0 of them, query tile 1 (when n1 > 0) all but the one at position gap
+  // (-1: all): its window may start a tile later.  Of the keys in them some
+  // row of the unit sees those below min(sinks, hi) and lo .. hi - 1.
+  int ns, wa, nl, gap, lo, hi;
 };
 
 // A piece of work: key tiles [kb, kb + n_w) of query tile w of one unit.
@@ -320,16 +323,33 @@ struct Unit {
 struct Piece {
   int bh, mblk, kb, n0, n1, tail, slot;
   int len, off, lenq, q0, k0;   // as in Unit
-  int ns, wa, nl, n_sink, a0, a1, e0, e1, lo, hi;   // as in Unit (kWin)
+  int ns, wa, nl, gap, lo, hi;    // as in Unit (kWin)
 };
 
-// Key tile at position j of a piece's list (kWin), and whether query tile w
-// computes it.
+// Key tile at position j of a piece's list (kWin), whether query tile w
+// computes it, and the list position of query tile w's j-th tile.
 __host__ __device__ __forceinline__ int win_tile(const Piece& u, int j) {
   return j < u.ns ? j : u.wa + (j - u.ns);
 }
-__host__ __device__ __forceinline__ bool win_active(const Piece& u, int w, int kt) {
-  return kt < (w ? u.e1 : u.e0) && (kt < u.n_sink || kt >= (w ? u.a1 : u.a0));
+__host__ __device__ __forceinline__ bool win_active(const Piece& u, int w, int j) {
+  return w ? u.n1 > 0 && j != u.gap : j < u.n0;
+}
+__host__ __device__ __forceinline__ int win_pos(const Piece& u, int w, int j) {
+  return w && u.gap >= 0 && j >= u.gap ? j + 1 : j;
+}
+// Whether the tile at list position j holds keys that no row of the unit
+// sees: only the last sink tile, the first tile of the windows and the last
+// tile can.
+__host__ __device__ __forceinline__ bool win_cut(const Piece& u, int j, int sinks) {
+  const int key0 = win_tile(u, j) * kBN;
+  return key0 + kBN > u.hi || imax(key0, sinks) < imin(u.lo, key0 + kBN);
+}
+// First list position >= from of a tile with such keys, nl if there is none.
+__host__ __device__ __forceinline__ int win_next_cut(const Piece& u, int from, int sinks) {
+  if (from < u.ns && win_cut(u, u.ns - 1, sinks)) return u.ns - 1;
+  if (from <= u.ns && u.ns < u.nl && win_cut(u, u.ns, sinks)) return u.ns;
+  if (from < u.nl && win_cut(u, u.nl - 1, sinks)) return u.nl - 1;
+  return u.nl;
 }
 // Key/value head of query head bh (kWin: Hk heads shared by groups).
 __host__ __device__ __forceinline__ int kv_head(const FwdParams& p, int bh) {
@@ -355,8 +375,6 @@ __device__ __forceinline__ int unit_at(int round, int cta, int grid) {
   return round * grid + ((round & 1) ? (grid - 1 - cta) : cta);
 }
 
-__host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
-__host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
 
 // Unit s of the schedule: its (batch*head, query block) and the number of key
 // tiles each of its two query tiles streams.  Host code calls it too
@@ -419,11 +437,10 @@ __host__ __device__ __forceinline__ Unit decode_unit(int s, const FwdParams& p) 
       u.n0 = n[0];
       u.n1 = n[1];
       const int end = imax(e[0], e[1]);
-      u.n_sink = n_sink;
-      u.a0 = a[0]; u.a1 = a[1]; u.e0 = e[0]; u.e1 = e[1];
       u.ns = imin(n_sink, end);
       u.wa = imax(e[0] == 0 ? a[1] : (e[1] == 0 ? a[0] : imin(a[0], a[1])), n_sink);
       u.nl = u.ns + imax(0, end - u.wa);
+      u.gap = e[1] > 0 && imax(a[1], n_sink) > u.wa ? u.ns : -1;
       u.lo = imax(t0 * kBM + u.off - p.win + 1, 0);
       u.hi = imin(len, imax(imin((t0 + 2) * kBM, lenq) + u.off, 0));
     }
@@ -479,8 +496,7 @@ __device__ __forceinline__ bool next_piece(const FwdParams& p, int cta, int grid
     pc.tail = -1; pc.slot = 0; pc.len = u.len; pc.off = u.off;
     pc.lenq = u.lenq; pc.q0 = u.q0; pc.k0 = u.k0;
     if constexpr (kWin) {
-      pc.ns = u.ns; pc.wa = u.wa; pc.nl = u.nl; pc.n_sink = u.n_sink;
-      pc.a0 = u.a0; pc.a1 = u.a1; pc.e0 = u.e0; pc.e1 = u.e1;
+      pc.ns = u.ns; pc.wa = u.wa; pc.nl = u.nl; pc.gap = u.gap;
       pc.lo = u.lo; pc.hi = u.hi;
     }
     return true;
@@ -928,9 +944,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
               if (w == 0 && j < u.n1) issue_s_own(1, kslot);
             } else if constexpr (kWin) {
               kslot = ring_wait(kpos);
-              const int kt = win_tile(u, j);
-              if (win_active(u, 0, kt)) issue_s_own(0, kslot);
-              if (win_active(u, 1, kt)) issue_s_own(1, kslot);
+              if (win_active(u, 0, j)) issue_s_own(0, kslot);
+              if (win_active(u, 1, j)) issue_s_own(1, kslot);
             } else {
               kslot = ring_wait(kpos);
               if (j < u.n0) issue_s_own(0, kslot);
@@ -987,37 +1002,42 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           const int nkv = u.nl;
           if (nkv == 0) continue;
           int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
-          for (int j = 0; j < nkv; ++j) {
-            const int kt = win_tile(u, j), key0 = kt * kBN;
-            const bool cut = key0 + kBN > u.hi || (key0 < u.lo && key0 + kBN > p.sinks);
-            if (!cut && lane != 0) continue;
-            const uint32_t vpos = base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u);
-            const uint32_t vslot = vpos % L::kStages;
-            if (lane == 0) ring_wait(vpos);
-            if (cut) {
-              __syncwarp();
-              const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
-              const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
-              const int r_sink = min(max(p.sinks - key0, 0), r_lo);
-              uint8_t* vt = sgen + L::kKV + vslot * L::kTile;
-              for (int ch = 0; ch < L::kChunks; ++ch) {
-                uint4* rows = reinterpret_cast<uint4*>(vt + ch * L::kChunkBytes);
-                for (int i = r_sink * 8 + lane; i < r_lo * 8; i += 32)
-                  rows[i] = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = r_hi * 8 + lane; i < kBN * 8; i += 32)
-                  rows[i] = make_uint4(0u, 0u, 0u, 0u);
+          auto vpos = [&](int j) { return base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u); };
+          bool landed = false;             // tile j has been waited for (and cleared)
+          for (int j = 0;;) {
+            const int jc = win_next_cut(u, landed ? j + 1 : j, p.sinks);
+            if (lane == 0) {
+              for (; j < jc; ++j) {
+                uint32_t vslot = vpos(j) % L::kStages;
+                if (!landed) vslot = ring_wait(vpos(j));
+                landed = false;
+                const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
+                if (win_active(u, 0, j)) issue_pv_own(0, it0++, v_lo);
+                if (win_active(u, 1, j)) issue_pv_own(1, it1++, v_lo);
+                if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
               }
-              ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
-              __syncwarp();
+              issued_any = true;
+              if (jc < nkv) ring_wait(vpos(jc));
             }
-            if (lane != 0) continue;
-            const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
-            if (win_active(u, 0, kt)) issue_pv_own(0, it0++, v_lo);
-            if (win_active(u, 1, kt)) issue_pv_own(1, it1++, v_lo);
-            if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
-            issued_any = true;
+            __syncwarp();
+            if (jc >= nkv) break;
+            j = jc;
+            const int key0 = win_tile(u, j) * kBN;
+            const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
+            const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
+            const int r_sink = min(max(p.sinks - key0, 0), r_lo);
+            uint8_t* vt = sgen + L::kKV + vpos(j) % L::kStages * L::kTile;
+            for (int ch = 0; ch < L::kChunks; ++ch) {
+              uint4* rows = reinterpret_cast<uint4*>(vt + ch * L::kChunkBytes);
+              for (int i = r_sink * 8 + lane; i < r_lo * 8; i += 32)
+                rows[i] = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = r_hi * 8 + lane; i < kBN * 8; i += 32)
+                rows[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
+            landed = true;
+            __syncwarp();
           }
-          __syncwarp();
           if (u.n0 > 0) ++ucnt0;
           if (u.n1 > 0) ++ucnt1;
           base += 2u * nkv;
@@ -1025,7 +1045,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       }
       pf.lap(6);
       const bool pv_thread = (warp == kPvWarp);
-      pf.flush(p, pv_thread ? 3 : 2);
+      if (lane == 0) pf.flush(p, pv_thread ? 3 : 2);
       // Drain: every MMA issued by this thread has completed before TMEM is freed.
       if (issued_any) {
         const uint32_t fb = bar(pv_thread ? L::bFinalPv : L::bFinal);
@@ -1062,12 +1082,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       const int n = w ? u.n1 : u.n0;          // key tiles of this query tile
       const int tile = 2 * u.mblk + w;
       const int row = tile * kBM + t;
-      // kWin: its key tiles are the sink tiles 0 .. win_ns - 1, then j + win_skip;
-      // this row sees keys win_lo .. win_lim - 1 and the sinks before them
-      int win_ns = 0, win_skip = 0, win_lim = 0, win_lo = 0;
+      // kWin: this row sees keys win_lo .. win_lim - 1 and the sinks before them
+      int win_lim = 0, win_lo = 0;
       if constexpr (kWin) {
-        win_ns = min(u.n_sink, w ? u.e1 : u.e0);
-        win_skip = max(w ? u.a1 : u.a0, u.n_sink) - win_ns;
         win_lim = min(u.len, row + u.off + 1);
         win_lo = row + u.off - p.win + 1;
       }
@@ -1107,7 +1124,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         int key0 = 0, lim = 0, lo = 0, sink = 0;
         bool cut = false;
         if constexpr (kWin) {
-          key0 = (j < win_ns ? j : j + win_skip) * kBN;
+          key0 = win_tile(u, win_pos(u, w, j)) * kBN;
           lim = win_lim - key0;
           lo = win_lo - key0;
           sink = min(p.sinks - key0, lim);

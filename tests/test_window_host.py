@@ -54,7 +54,7 @@ static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
     const fa::Unit x = fa::decode_unit<true, true, true>(s, p);
     fa::Piece u{};
     u.mblk = x.mblk; u.n0 = x.n0; u.n1 = x.n1; u.ns = x.ns; u.wa = x.wa; u.nl = x.nl;
-    u.n_sink = x.n_sink; u.a0 = x.a0; u.a1 = x.a1; u.e0 = x.e0; u.e1 = x.e1;
+    u.gap = x.gap; u.lo = x.lo; u.hi = x.hi;
     std::vector<int> pos_in_list((Nk + 127) / 128 + 1, -1);
     int active[2] = {0, 0};
     for (int j = 0; j < u.nl; ++j) {
@@ -62,8 +62,16 @@ static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
       if (kt < 0 || kt * 128 >= len) BAD("fwd tile %d of unit %d", kt, s);
       if (pos_in_list[kt] >= 0) BAD("fwd tile twice %d", kt);
       pos_in_list[kt] = j;
-      for (int w = 0; w < 2; ++w) active[w] += fa::win_active(u, w, kt);
+      if (!fa::win_active(u, 0, j) && !fa::win_active(u, 1, j)) BAD("idle tile %d", kt);
+      for (int w = 0; w < 2; ++w)
+        if (fa::win_active(u, w, j) && fa::win_pos(u, w, active[w]++) != j) BAD("position %d", j);
+      // the tiles with rows to clear come in order, and no other needs it
+      bool unseen = false;
+      for (int key = kt * 128; key < kt * 128 + 128; ++key)
+        unseen |= !(key < sinks && key < x.hi) && !(key >= x.lo && key < x.hi);
+      if (unseen != (fa::win_next_cut(u, j, sinks) == j)) BAD("cut %d of %d", j, u.nl);
     }
+    if (u.nl && fa::win_next_cut(u, u.nl, sinks) != u.nl) BAD("cut after the list");
     if (active[0] != u.n0 || active[1] != u.n1) BAD("fwd active %d %d", active[0], active[1]);
     for (int w = 0; w < 2; ++w)
       for (int r = 0; r < 128; ++r) {
@@ -72,7 +80,7 @@ static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
         for (int key = 0; key < len; ++key)
           if (sees(row + off, key, len, win, sinks)) {
             const int kt = key / 128;
-            if (pos_in_list[kt] < 0 || !fa::win_active(u, w, kt)) BAD("fwd pair %d %d", row, key);
+            if (pos_in_list[kt] < 0 || !fa::win_active(u, w, pos_in_list[kt])) BAD("fwd pair %d %d", row, key);
             if (!(key < sinks && key < x.hi) && !(key >= x.lo && key < x.hi))
               BAD("fwd cleared key %d", key);
           }
