@@ -413,21 +413,19 @@ def fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, window, sinks):
 def fa_decode_window(q, k, v, o, lse, B, H, Hk, Nq, Nk, d, window, sinks, seqlens_k, scale, dtype,
                      workspace, workspace_bytes, stream=None):
     """Raw C call of sliding-window decoding; returns the code."""
-    lib = load_library()
-    return lib.fa_decode_window(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), int(B), int(H),
-                                int(Hk), int(Nq), int(Nk), int(d), int(window), int(sinks),
-                                _addr(seqlens_k), float(scale), int(dtype), _addr(workspace),
-                                int(workspace_bytes), _stream(stream))
+    return load_library().fa_decode_window(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), B, H,
+                                           Hk, Nq, Nk, d, window, sinks, _addr(seqlens_k), scale,
+                                           dtype, _addr(workspace), workspace_bytes,
+                                           _stream(stream))
 
 
 def fa_decode_tree(q, k, v, o, lse, B, H, Hk, Nq, Nk, d, tree, window, sinks, seqlens_k, scale,
                    dtype, workspace, workspace_bytes, stream=None):
     """Raw C call of drafted-tree decoding; returns the code."""
-    lib = load_library()
-    return lib.fa_decode_tree(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), int(B), int(H),
-                              int(Hk), int(Nq), int(Nk), int(d), _addr(tree), int(window),
-                              int(sinks), _addr(seqlens_k), float(scale), int(dtype),
-                              _addr(workspace), int(workspace_bytes), _stream(stream))
+    return load_library().fa_decode_tree(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), B, H,
+                                         Hk, Nq, Nk, d, _addr(tree), window, sinks,
+                                         _addr(seqlens_k), scale, dtype, _addr(workspace),
+                                         workspace_bytes, _stream(stream))
 
 
 def fa_decode_window_workspace_size(B, H, Hk, Nq, Nk, d):
@@ -932,16 +930,17 @@ def attention_decode(q, k, v, causal=False, scale=None, out=None, lse=None, work
 
 def _window_args(q, k, v, window, sinks, seqlens_k, what):
     """Checks shared by the window and tree calls; returns
-    (B, H, Hk, Nq, Nk, d)."""
-    import torch
-    if not (q.dtype == k.dtype == v.dtype):
+    (B, H, Hk, Nq, Nk, d), the dtype's code and the shapes of O and LSE."""
+    dtype, device = q.dtype, q.device
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError(f"dtypes differ: {q.dtype}, {k.dtype}, {v.dtype}")
-    dtype_code(q.dtype)
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+    code = dtype_code(dtype)
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or ks != v.shape:
         raise ValueError(f"{what}: q must be [B, H, Nq, d] and k, v [B, Hk, Nk, d]")
-    B, H, Nq, d = q.shape
-    Hk, Nk = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != d:
+    B, H, Nq, d = qs
+    _, Hk, Nk, _ = ks
+    if ks[0] != B or ks[3] != d:
         raise ValueError(f"{what}: q and k differ in batch or head width")
     if Hk == 0 or H % Hk:
         raise ValueError(f"{what}: {H} query heads are not a multiple of {Hk} key/value heads")
@@ -949,21 +948,30 @@ def _window_args(q, k, v, window, sinks, seqlens_k, what):
         raise ValueError(f"{what}: window must be at least 1")
     if sinks < 0:
         raise ValueError(f"{what}: sinks must not be negative")
-    if not all(t.is_cuda and t.device == q.device for t in (q, k, v)):
+    if not q.is_cuda or k.device != device or v.device != device:
         raise ValueError(f"{what}: q, k, v must be CUDA tensors of one device")
-    if not all(t.is_contiguous() for t in (q, k, v)):
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
         raise ValueError(f"{what}: q, k, v must be contiguous")
     if seqlens_k is not None:
+        import torch
         if (seqlens_k.dtype != torch.int32 or seqlens_k.shape != (B,)
-                or seqlens_k.device != q.device or not seqlens_k.is_contiguous()):
+                or seqlens_k.device != device or not seqlens_k.is_contiguous()):
             raise ValueError(f"{what}: seqlens_k must be a contiguous int32 tensor [B] on q's device")
-    return B, H, Hk, Nq, Nk, d
+    return (B, H, Hk, Nq, Nk, d), code
 
 
 def _check_buffer(t, shape, dtype, device, name):
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device \
-            or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def _workspace_arg(workspace, device):
+    """(address, bytes) of a workspace tensor, (None, 0) without one."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def attention_forward_window(q, k, v, window, sinks=0, causal="bottom_right", seqlens_k=None,
@@ -980,23 +988,21 @@ def attention_forward_window(q, k, v, window, sinks=0, causal="bottom_right", se
     (default: current stream).
     """
     import torch
-    B, H, Hk, Nq, Nk, d = _window_args(q, k, v, window, sinks, seqlens_k,
-                                       "attention_forward_window")
+    dims, code = _window_args(q, k, v, window, sinks, seqlens_k, "attention_forward_window")
+    B, H, Hk, Nq, Nk, d = dims
     if causal not in ("upper_left", "bottom_right"):
         raise ValueError("causal must be 'upper_left' or 'bottom_right'")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with torch.cuda.device(q.device), _on(stream):
+    if out is not None:
+        _check_buffer(out, q.shape, q.dtype, q.device, "out")
+    if lse is not None:
+        _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
+    with _on(stream, q.device):
         if out is None:
             out = torch.empty_like(q)
-        else:
-            _check_buffer(out, (B, H, Nq, d), q.dtype, q.device, "out")
         if lse is None:
             lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        else:
-            _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
-        rc = fa_fwd_window(q, k, v, out, lse, B, H, Hk, Nq, Nk, d, CAUSAL_MODES[causal],
-                           _int32(window), _int32(sinks), seqlens_k, scale, dtype_code(q.dtype),
+        rc = fa_fwd_window(q, k, v, out, lse, *dims, CAUSAL_MODES[causal], _int32(window),
+                           _int32(sinks), seqlens_k, d ** -0.5 if scale is None else scale, code,
                            _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_window")
@@ -1011,28 +1017,24 @@ def attention_backward_window(q, k, v, o, lse, dout, window, sinks=0, causal="bo
     of at least ``fa_bwd_window_workspace_size`` bytes; allocated here when
     None."""
     import torch
-    B, H, Hk, Nq, Nk, d = _window_args(q, k, v, window, sinks, seqlens_k,
-                                       "attention_backward_window")
+    dims, code = _window_args(q, k, v, window, sinks, seqlens_k, "attention_backward_window")
+    B, H, Hk, Nq, Nk, d = dims
     if causal not in ("upper_left", "bottom_right"):
         raise ValueError("causal must be 'upper_left' or 'bottom_right'")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    _check_buffer(o, (B, H, Nq, d), q.dtype, q.device, "o")
-    _check_buffer(dout, (B, H, Nq, d), q.dtype, q.device, "dout")
+    _check_buffer(o, q.shape, q.dtype, q.device, "o")
+    _check_buffer(dout, q.shape, q.dtype, q.device, "dout")
     _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
-    with torch.cuda.device(q.device), _on(stream):
-        if workspace is None:
-            need = fa_bwd_window_workspace_size(B, H, Hk, Nq, Nk, d, _int32(window),
-                                                _int32(sinks))
+    window, sinks = _int32(window), _int32(sinks)
+    with _on(stream, q.device):
+        if workspace is None and sinks > 0:
+            need = fa_bwd_window_workspace_size(*dims, window, sinks)
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        elif workspace.device != q.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on q's device")
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _workspace_arg(workspace, q.device)
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         delta = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        rc = fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, delta, B, H, Hk, Nq, Nk, d,
-                           CAUSAL_MODES[causal], _int32(window), _int32(sinks), seqlens_k, scale,
-                           dtype_code(q.dtype), workspace, ws_bytes, _current(stream, q))
+        rc = fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, delta, *dims, CAUSAL_MODES[causal],
+                           window, sinks, seqlens_k, d ** -0.5 if scale is None else scale, code,
+                           ws, ws_bytes, _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_window")
     return dq, dk, dv
@@ -1051,27 +1053,23 @@ def make_decode_workspace(q, k):
 
 
 def _decode(fn, where, q, k, v, tree, window, sinks, seqlens_k, scale, out, lse, workspace, stream,
-            dims):
+            dims, code):
     import torch
-    B, H, Hk, Nq, Nk, d = dims
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with torch.cuda.device(q.device), _on(stream):
+    B, H, _, Nq, _, d = dims
+    if out is not None:
+        _check_buffer(out, q.shape, q.dtype, q.device, "out")
+    if lse is not None:
+        _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
+    with _on(stream, q.device):
         if out is None:
             out = torch.empty_like(q)
-        else:
-            _check_buffer(out, (B, H, Nq, d), q.dtype, q.device, "out")
         if lse is None:
             lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        else:
-            _check_buffer(lse, (B, H, Nq), torch.float32, q.device, "lse")
         if workspace is None:
             workspace = make_decode_workspace(q, k)
-        elif workspace.device != q.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on q's device")
-        ws_bytes = workspace.numel() * workspace.element_size()
-        rc = fn(q, k, v, out, lse, B, H, Hk, Nq, Nk, d, *tree, _int32(window), _int32(sinks),
-                seqlens_k, scale, dtype_code(q.dtype), workspace, ws_bytes, _current(stream, q))
+        ws, ws_bytes = _workspace_arg(workspace, q.device)
+        rc = fn(q, k, v, out, lse, *dims, *tree, _int32(window), _int32(sinks), seqlens_k,
+                d ** -0.5 if scale is None else scale, code, ws, ws_bytes, _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, where)
     return out, lse
@@ -1086,9 +1084,9 @@ def attention_decode_window(q, k, v, window, sinks=0, seqlens_k=None, scale=None
     Calls ``fa_decode_window``.  ``workspace``: see ``make_decode_workspace``;
     None allocates one.
     """
-    dims = _window_args(q, k, v, window, sinks, seqlens_k, "attention_decode_window")
+    dims, code = _window_args(q, k, v, window, sinks, seqlens_k, "attention_decode_window")
     return _decode(fa_decode_window, "fa_decode_window", q, k, v, (), window, sinks, seqlens_k,
-                   scale, out, lse, workspace, stream, dims)
+                   scale, out, lse, workspace, stream, dims, code)
 
 
 def attention_decode_tree(q, k, v, tree, seqlens_k=None, window=None, sinks=0, scale=None,
@@ -1105,15 +1103,15 @@ def attention_decode_tree(q, k, v, tree, seqlens_k=None, window=None, sinks=0, s
     ``fa_decode_tree``.
     """
     import torch
-    dims = _window_args(q, k, v, 1 if window is None else window, sinks, seqlens_k,
-                        "attention_decode_tree")
-    if tree.dtype != torch.int64 or tree.shape != q.shape[:1] + q.shape[2:3] \
+    dims, code = _window_args(q, k, v, 1 if window is None else window, sinks, seqlens_k,
+                              "attention_decode_tree")
+    if tree.dtype != torch.int64 or tree.shape != (dims[0], dims[3]) \
             or tree.device != q.device or not tree.is_contiguous():
         raise ValueError("attention_decode_tree: tree must be a contiguous int64 tensor [B, Nq] "
                          "on q's device")
     return _decode(fa_decode_tree, "fa_decode_tree", q, k, v, (tree,),
                    0 if window is None else window, sinks, seqlens_k, scale, out, lse, workspace,
-                   stream, dims)
+                   stream, dims, code)
 
 
 def tree_rows(parents):
@@ -1141,12 +1139,25 @@ def _int32(x):
     return min(int(x), 2**31 - 1)
 
 
-def _on(stream):
-    """Context in which a call's results are allocated: the given stream."""
+_NOTHING = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _on_device_and_stream(stream, device):
     import torch
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):   # stream None: unchanged
+        yield
+
+
+def _on(stream, device):
+    """Context of a call: the tensors' device current, and the given stream, on
+    which the call's results are allocated."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _NOTHING
+    return _on_device_and_stream(stream, device)
 
 
 def _current(stream, q):
