@@ -926,7 +926,8 @@ def attention_decode(q, k, v, causal=False, scale=None, out=None, lse=None, work
 # Calls with a sliding window and sinks, or a tree of drafted tokens.  Key/value
 # heads may be shared: q has H heads, k and v Hk, H a multiple of Hk.  They
 # run on the tensors' device and, with ``stream`` given, allocate what they
-# return on that stream.
+# return on that stream; ordering that stream after the inputs' producers, and
+# keeping the inputs alive until it is done, is the caller's part.
 
 def _window_args(q, k, v, window, sinks, seqlens_k, what):
     """Checks shared by the window and tree calls; returns
@@ -1146,7 +1147,8 @@ _NOTHING = contextlib.nullcontext()
 def _on_device_and_stream(stream, device):
     import torch
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
     with torch.cuda.device(device), torch.cuda.stream(stream):   # stream None: unchanged
         yield
 

@@ -307,3 +307,43 @@ def test_long_runs_of_tiles(G, Nq, d):
         val, tol = wc.reference(q[b:b + 1, hq].cpu(), k[b:b + 1, hk:hk + 1].cpu(),
                                 v[b:b + 1, hk:hk + 1].cpu(), masks, wc.scale_of(d), "fp16")
         wc.check(dict(o=o[b:b + 1, hq], lse=lse[b:b + 1, hq]), val, tol, f"batch {b} head {hk}")
+
+
+def test_counts_out_of_range_are_clamped():
+    B, H, Hk, Nk, d = 4, 4, 2, 300, 64
+    lens = [-7, 301, 2**31 - 1, -2**31]
+    q, k, v = inputs(B, H, Hk, 2, Nk, d, "fp16", seed=17)
+    o, lse = fa.attention_decode_window(q.cuda(), k.cuda(), v.cuda(), 60, 3, seqlens_k=counts(lens))
+    rows = fa.tree_rows(torch.tensor([[-1, 0]]).expand(B, 2))
+    o2, lse2 = fa.attention_decode_tree(q.cuda(), k.cuda(), v.cuda(), rows.cuda(),
+                                        seqlens_k=counts(lens), window=60, sinks=3)
+    status_ok()
+    val, tol = wc.reference(q, k, v, window_masks(B, 2, Nk, lens, 60, 3), wc.scale_of(d), "fp16")
+    wc.check(dict(o=o, lse=lse), val, tol, "clamped")
+    ms = [wc.tree_mask(rows[b].tolist(), Nk, lens[b], 60, 3) for b in range(B)]
+    val, tol = wc.reference(q, k, v, ms, wc.scale_of(d), "fp16")
+    wc.check(dict(o=o2, lse=lse2), val, tol, "clamped tree")
+
+
+def test_streams_and_workspaces():
+    """Two calls at once on two streams, each with its workspace and on a
+    stream given as an object and as a handle; a short workspace is refused."""
+    B, H, Hk, Nk, d = 2, 16, 4, 20000, 128
+    k, v = (torch.randn(B, Hk, Nk, d, device="cuda", dtype=torch.float16) for _ in range(2))
+    qs = [torch.randn(B, H, 4, d, device="cuda", dtype=torch.float16) for _ in range(2)]
+    want = [fa.attention_decode_window(q, k, v, 15000, 4) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [fa.attention_decode_window(q, k, v, 15000, 4,
+                                          stream=s if i else s.cuda_stream)
+               for i, (q, s) in enumerate(zip(qs, streams))]
+        status_ok()
+        for (a, b), (c, d2) in zip(want, got):
+            assert torch.equal(a, c) and torch.equal(b, d2)
+    o, lse = fa.attention_decode_window(qs[0], k, v, 15000, 4, stream=0)
+    status_ok()
+    assert torch.equal(o, want[0][0])
+    with pytest.raises(fa.FaError):
+        fa.attention_decode_window(qs[0], k, v, 15000, 4,
+                                   workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))

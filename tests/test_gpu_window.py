@@ -239,3 +239,35 @@ def test_many_tiles_a_unit_and_many_units_a_cta(d):
                                 "bf16", do[:, hq])
         part = {n: got[n][:, hq] if n in ("o", "lse", "dq") else got[n][:, hk:hk + 1] for n in got}
         wc.check(part, val, tol, f"head {hk}")
+
+
+def test_counts_out_of_range_are_clamped():
+    B, H, Hk, Nq, Nk, d = 4, 2, 1, 130, 300, 64
+    q, k, v, do = inputs(B, H, Hk, Nq, Nk, d, "fp16", seed=17)
+    lens = [-7, 301, 2**31 - 1, -2**31]
+    got = run(q, k, v, do, 60, 3, "bottom_right", lens)
+    val, tol = wc.reference(q, k, v, masks(B, Nq, Nk, lens, "bottom_right", 60, 3), wc.scale_of(d),
+                            "fp16", do)
+    wc.check(got, val, tol, "clamped")
+    assert not got["dk"][0].any() and not got["dv"][3].any() and not got["dq"][0].any()
+
+
+def test_given_buffers_are_filled_and_nothing_else():
+    """Outputs given as slices of a larger buffer: the rest stays as it was."""
+    B, H, Hk, N, d = 1, 4, 2, 200, 64
+    q, k, v, _ = (t.cuda() for t in inputs(B, H, Hk, N, N, d, "fp16", seed=19))
+    big = torch.full((3, B, H, N, d), 7.0, dtype=torch.float16, device="cuda")
+    biglse = torch.full((3, B, H, N), 7.0, device="cuda")
+    o, lse = fa.attention_forward_window(q, k, v, 50, 1, out=big[1], lse=biglse[1])
+    o2, lse2 = fa.attention_forward_window(q, k, v, 50, 1)
+    status_ok()
+    assert o.data_ptr() == big[1].data_ptr()
+    assert torch.equal(big[1], o2) and torch.equal(biglse[1], lse2)
+    assert bool((big[0] == 7).all() & (big[2] == 7).all())
+    assert bool((biglse[0] == 7).all() & (biglse[2] == 7).all())
+    with pytest.raises(ValueError):
+        fa.attention_forward_window(q, k, v, 50, 1, out=big[1].transpose(1, 2))
+    with pytest.raises(ValueError):
+        fa.attention_forward_window(q, k, v, 50, 1, lse=biglse[1].half())
+    with pytest.raises(ValueError):
+        fa.attention_forward_window(q.transpose(1, 2), k, v, 50, 1)
