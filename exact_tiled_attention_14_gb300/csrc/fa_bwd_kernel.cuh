@@ -75,6 +75,30 @@ constexpr int kBwdLoadWarp = 9;
 constexpr int kBwdTile = 128;            // rows of a query or key tile = TMEM lanes
 constexpr uint32_t kBwdTmemCols = 512;
 
+// Roles of the tensor-core kernel.  kGroups element-wise warps share a TMEM
+// lane quarter, each on kCols of a tile's 128 columns.
+template <bool kWin>
+struct BwdRoles {
+  static constexpr int kGroups = kWin ? 4 : 2;
+  static constexpr int kCols = kBwdTile / kGroups;
+  static constexpr int kEwThreads = kGroups * 128;
+  static constexpr int kMmaWarp = kEwThreads / 32;
+  static constexpr int kLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = kEwThreads + 64;
+};
+
+// The MMA warp.  kWin: every lane walks the loop and one elected lane issues
+// (elected() is true in it), which keeps descriptors and addresses in uniform
+// registers; a wait's outcome is the warp's.  Otherwise lane 0 walks alone.
+template <bool kWin>
+__device__ __forceinline__ bool bwd_elected() {
+  return !kWin || ptx::elect_one();
+}
+template <bool kWin>
+__device__ __forceinline__ bool bwd_warp_ok(bool ok) {
+  return kWin ? __all_sync(0xffffffffu, ok) : ok;
+}
+
 // Sites recorded in the status word when a wait of a backward kernel runs out.
 enum BwdWaitSite : uint32_t {
   kSiteBwdEmpty = 20, kSiteBwdRes = 21, kSiteBwdFull = 22, kSiteBwdSFull = 23,
@@ -401,15 +425,16 @@ __device__ __forceinline__ void issue_kmajor(uint32_t d_tmem, uint32_t a_lo, uin
 }
 
 // Issue A (16-bit, in TMEM, 128 rows x 128 along K) x B (MN-major tile of 128
-// rows along K, D columns) into d_tmem (N = D).  kSplitA: A's 64 packed
-// columns sit in two blocks of 32 at a_tmem and a_tmem + 64 (a 16-bit tile
-// written over the fp32 columns each half of the warps read).
-template <bool kSplitA>
+// rows along K, D columns) into d_tmem (N = D).  A's 64 packed columns sit
+// in kBlocks equal blocks, 128 / kBlocks columns apart (more than one: a
+// 16-bit tile written over the fp32 columns that each group of warps read).
+template <int kBlocks>
 __device__ __forceinline__ void issue_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                              uint32_t idesc, uint32_t acc) {
 #pragma unroll
   for (int kk = 0; kk < kBwdTile / 16; ++kk) {
-    const uint32_t acol = kSplitA ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 8;
+    constexpr int kPer = 8 / kBlocks;   // K steps of a block
+    const uint32_t acol = kk / kPer * (kBwdTile / kBlocks) + kk % kPer * 8;
     ptx::mma_ts(d_tmem, a_tmem + acol, ptx::desc_sw128(b_lo + kk * (2048 >> 4)), idesc,
                 kk > 0 ? 1u : acc);
   }
@@ -505,12 +530,11 @@ __device__ __forceinline__ void store_acc_cols(uint32_t t_acc, int c0, int nc, i
   }
 }
 
-// One row of a TMEM accumulator (D fp32 columns), times `mul`, to 16-byte
-// aligned fp32.
-template <int D>
-__device__ __forceinline__ void store_acc_f32(uint32_t t_acc, float mul, float* out) {
+// Columns [c0, c0 + nc) (nc a multiple of 32) of one row of a TMEM
+// accumulator, times `mul`, to the fp32 row `out` (16-byte aligned).
+__device__ __forceinline__ void store_acc_f32(uint32_t t_acc, int c0, int nc, float mul, float* out) {
 #pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
+  for (int c = c0; c < c0 + nc; c += 32) {
     uint32_t r[32];
     ptx::tmem_ld32(t_acc + c, r);
     ptx::tmem_wait_ld();
@@ -707,6 +731,7 @@ template <int D, bool kBf16, bool kCausal, bool kDrop, bool kKv, bool kWin = fal
 __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32_t tmem_base) {
   using L = BwdSmem<D, DkdvVec<D>::kBytes>;
   using X = DkdvBars;
+  using W = BwdRoles<kWin>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -789,13 +814,13 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
                                  (kBwdTile * 2 * D);
   }
   if (kWin && nq <= 0 && part_ws != nullptr) {
-    for (int i = threadIdx.x; i < kBwdTile * 2 * D / 4; i += kBwdThreads)
+    for (int i = threadIdx.x; i < kBwdTile * 2 * D / 4; i += W::kThreads)
       reinterpret_cast<float4*>(part_ws)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
   if (kKv && nq <= 0) {
     // no query sees this key tile: its dK and dV rows are zero
-    if (threadIdx.x < kBwdEwThreads) {
+    if (threadIdx.x < 256) {
       const int t = threadIdx.x & 127;
       const long long key = static_cast<long long>(kt) * kBwdTile + t;
       if (key < key_rows) {
@@ -811,13 +836,13 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
   bwd_setup<L>(sbase, sgen, [&](auto b) {
     ptx::mbar_init(b(L::bX + X::kSFull), 1);
     ptx::mbar_init(b(L::bX + X::kDpFull), 1);
-    ptx::mbar_init(b(L::bX + X::kPReady), kBwdEwThreads);
-    ptx::mbar_init(b(L::bX + X::kDsReady), kBwdEwThreads);
+    ptx::mbar_init(b(L::bX + X::kPReady), W::kEwThreads);
+    ptx::mbar_init(b(L::bX + X::kDsReady), W::kEwThreads);
     ptx::mbar_init(b(L::bX + X::kDone), 1);
   });
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
 
-  if (warp == kBwdLoadWarp) {
+  if (warp == W::kLoadWarp) {
     if constexpr (kWin) {
       if (lane == 0) {
         Step at = first_step();
@@ -836,8 +861,8 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
                       tok ? bh % p.H : -1, hd.k0, hd.q0, p.width_qk / 64, p.width_v / 64);
     }
     __syncwarp();
-  } else if (warp == kBwdMmaWarp) {
-    if (lane == 0) {
+  } else if (warp == W::kMmaWarp) {
+    if (kWin || lane == 0) {
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBwdTile, kBwdTile, fmt, 0);
       // dV has width_v columns, dK width_qk
@@ -863,17 +888,19 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       };
       // S^T = K_j Q_i^T and dP^T = V_j dO_i^T (keys on the TMEM lanes)
       auto issue_s = [&](int it) {
+        if (!bwd_elected<kWin>()) return;
         issue_kmajor<D, L::kChunkBytes>(tS, k_lo, q_lo0 + (it % L::kStagesA) * kSlotLo, idesc_s,
                                         steps_s);
         ptx::mma_commit(xbar(X::kSFull));
       };
       auto issue_dp = [&](int it) {
+        if (!bwd_elected<kWin>()) return;
         issue_kmajor<D, L::kChunkBytes>(tDp, v_lo, do_lo0 + (it % L::kStagesB) * kSlotLo, idesc_s,
                                         steps_dp);
         ptx::mma_commit(xbar(X::kDpFull));
       };
-      bool alive = ptx::wait_bounded(bar(L::bRes), 0, wd, kSiteBwdRes);
-      alive = alive && full_a(0) && full_b(0);
+      bool alive = bwd_warp_ok<kWin>(ptx::wait_bounded(bar(L::bRes), 0, wd, kSiteBwdRes) &&
+                                     full_a(0) && full_b(0));
       ptx::tc_fence_after();
       if (alive) {
         issue_s(0);
@@ -881,51 +908,57 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       }
       for (int it = 0; alive && it < nq; ++it) {
         const bool more = it + 1 < nq;
-        alive = ptx::wait_bounded(xbar(X::kPReady), it & 1, wd, kSiteBwdPFull);
+        alive = bwd_warp_ok<kWin>(
+            ptx::wait_bounded(xbar(X::kPReady), it & 1, wd, kSiteBwdPFull));
         ptx::tc_fence_after();
         if (!alive) break;
         // dV_j += P^T dO_i; P^T sits in TMEM columns 0-31 and 64-95
-        issue_tmem_a<true>(tDv, tS, do_mn0 + (it % L::kStagesB) * kSlotLo, idesc_dv,
-                           it > 0 ? 1u : 0u);
-        ptx::mma_commit(bar(L::bEmptyB + it % L::kStagesB));
+        if (bwd_elected<kWin>()) {
+          issue_tmem_a<W::kGroups>(tDv, tS, do_mn0 + (it % L::kStagesB) * kSlotLo, idesc_dv,
+                                   it > 0 ? 1u : 0u);
+          ptx::mma_commit(bar(L::bEmptyB + it % L::kStagesB));
+        }
         if (more) {
-          alive = full_a(it + 1);
+          alive = bwd_warp_ok<kWin>(full_a(it + 1));
           ptx::tc_fence_after();
           if (!alive) break;
           issue_s(it + 1);   // after dV in this thread's order: P^T has been read
         }
-        alive = ptx::wait_bounded(xbar(X::kDsReady), it & 1, wd, kSiteBwdDsReady);
+        alive = bwd_warp_ok<kWin>(
+            ptx::wait_bounded(xbar(X::kDsReady), it & 1, wd, kSiteBwdDsReady));
         ptx::tc_fence_after();
         if (!alive) break;
         // dK_j += dS^T Q_i (scale applied at the end); dS^T in columns 128-159 and 192-223
-        issue_tmem_a<true>(tDk, tDp, q_mn0 + (it % L::kStagesA) * kSlotLo, idesc_dk,
-                           it > 0 ? 1u : 0u);
-        ptx::mma_commit(bar(L::bEmptyA + it % L::kStagesA));
+        if (bwd_elected<kWin>()) {
+          issue_tmem_a<W::kGroups>(tDk, tDp, q_mn0 + (it % L::kStagesA) * kSlotLo, idesc_dk,
+                                   it > 0 ? 1u : 0u);
+          ptx::mma_commit(bar(L::bEmptyA + it % L::kStagesA));
+        }
         if (more) {
-          alive = full_b(it + 1);
+          alive = bwd_warp_ok<kWin>(full_b(it + 1));
           ptx::tc_fence_after();
           if (!alive) break;
           issue_dp(it + 1);  // after dK: dS^T has been read
         }
       }
-      ptx::mma_commit(xbar(X::kDone));
+      if (bwd_elected<kWin>()) ptx::mma_commit(xbar(X::kDone));
       ptx::wait_drain(xbar(X::kDone), 0, 200000000ull);
     }
     __syncwarp();
   } else {
     // ============================================================ element-wise
     ptx::griddep_wait();   // D of the pass launched just before this grid
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, group = warp >> 2;
     const int t = quarter * 32 + lane;                    // key row within the tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // this thread's 64 query columns of S^T and dP^T
-    const uint32_t tS = tmem_base + lane_off + kColS + half * 64;
-    const uint32_t tDp = tmem_base + lane_off + kColDp + half * 64;
+    // this thread's query columns of S^T and dP^T
+    const uint32_t tS = tmem_base + lane_off + kColS + group * W::kCols;
+    const uint32_t tDp = tmem_base + lane_off + kColDp + group * W::kCols;
     const long long key = static_cast<long long>(kt) * kBwdTile + t;
     const uint64_t c2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
 
     // LSE and D of query row t of tile i, fetched one tile ahead by the
-    // first half of the warps.  The loads are unconditional (a row past the
+    // first group of the warps.  The loads are unconditional (a row past the
     // queries reads row 0) and nothing uses their values until the tile is
     // staged, so the warps do not wait for them; a query past N then gets
     // -LSE = -inf, so its P is 0, and D = 0.
@@ -940,9 +973,9 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       dd = p.delta[tok ? bwd_qrow(p, tok, hd, qh, qr) : qi];
     };
     float lse_next = 0.f, d_next = 0.f;
-    if (half == 0) fetch(nxt, lse_next, d_next);
-    int win_lo = 0, win_hi = 64;   // kWin: this key's queries of the thread's 64, phases 1 to 2
-    float pf[64];          // P^T of the current tile, from phase 1 to phase 2
+    if (group == 0) fetch(nxt, lse_next, d_next);
+    int win_lo = 0, win_hi = W::kCols;   // kWin: this key's queries of the thread's, phases 1 to 2
+    float pf[W::kCols];          // P^T of the current tile, from phase 1 to phase 2
     // dropout: keep bits of this key against the thread's 64 queries, from
     // the quad's words (zw[2 k2 + m]: word m of lane k2, blocks 8m + 4h + k2
     // of 4 queries each), from phase 1 to phase 2
@@ -959,31 +992,31 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     auto stage_vec = [&](int it) {
       float* vec = vec_of(it);
       // with one buffer, every thread must be done with the previous tile's
-      if (DkdvVec<D>::kBufs == 1 && it > 0) ptx::named_bar_sync(1, kBwdEwThreads);
-      if (half == 0) {
+      if (DkdvVec<D>::kBufs == 1 && it > 0) ptx::named_bar_sync(1, W::kEwThreads);
+      if (group == 0) {
         vec[t] = in_next ? -lse_next * 1.4426950408889634f : -INFINITY;   // -LSE, log2 units
         vec[128 + t] = in_next ? d_next : 0.f;
       }
       cur = nxt;
       next_step(nxt);
-      if (half == 0 && it + 1 < nq) fetch(nxt, lse_next, d_next);
-      ptx::named_bar_sync(2, kBwdEwThreads);
+      if (group == 0 && it + 1 < nq) fetch(nxt, lse_next, d_next);
+      ptx::named_bar_sync(2, W::kEwThreads);
     };
 
     // ---- phase 1: P^T = 2^(S^T c - LSE) over this thread's 64 queries
     auto phase1 = [&](int it) {
       const int i = cur.tile;
-      const float4* nl4 = reinterpret_cast<const float4*>(vec_of(it)) + half * 16;
+      const float4* nl4 = reinterpret_cast<const float4*>(vec_of(it)) + group * (W::kCols / 4);
       ptx::wait_bounded(xbar(X::kSFull), it & 1, wd, kSiteBwdSFull);
       __syncwarp();
       ptx::tc_fence_after();
       {
-        uint32_t sr[64];
-        ptx::tmem_ld32(tS, sr);
-        ptx::tmem_ld32(tS + 32, sr + 32);
+        uint32_t sr[W::kCols];
+#pragma unroll
+        for (int c = 0; c < W::kCols; c += 32) ptx::tmem_ld32(tS + c, sr + c);
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
+        for (int e = 0; e < W::kCols; e += 4) {
           const float4 nl = nl4[e / 4];
           float x0, x1, x2, x3;
           ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])),
@@ -999,17 +1032,17 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       if constexpr (kWin) {
         // queries q with key <= q + off < key + win (sinks: no upper bound);
         // padding keys see none
-        const int qb = i * kBwdTile + half * 64;
-        win_lo = key >= len ? 64 : static_cast<int>(key) - off - qb;
-        win_hi = key < p.sinks ? 64 : static_cast<int>(key) + p.win - off - qb;
+        const int qb = i * kBwdTile + group * W::kCols;
+        win_lo = key >= len ? W::kCols : static_cast<int>(key) - off - qb;
+        win_hi = key < p.sinks ? W::kCols : static_cast<int>(key) + p.win - off - qb;
         // (one compare and one select a query and end; no short circuits)
         if (win_lo > 0) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) pf[e] = e < win_lo ? 0.f : pf[e];
+          for (int e = 0; e < W::kCols; ++e) pf[e] = e < win_lo ? 0.f : pf[e];
         }
-        if (win_hi < 64) {
+        if (win_hi < W::kCols) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) pf[e] = e >= win_hi ? 0.f : pf[e];
+          for (int e = 0; e < W::kCols; ++e) pf[e] = e >= win_hi ? 0.f : pf[e];
         }
         // Rows at negative positions see no key, nor (without sinks) do rows
         // whose window starts past the batch's keys.  Whatever their Q and dO
@@ -1023,24 +1056,24 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
           __syncwarp();
           uint8_t* qt = sgen + L::kRingA + (it % L::kStagesA) * L::kTile;
           uint8_t* dt = sgen + L::kRingB + (it % L::kStagesB) * L::kTile;
-          zero_rows(qt, L::kChunks, 0, r_lo, threadIdx.x, kBwdEwThreads);
-          zero_rows(qt, L::kChunks, r_hi, kBwdTile, threadIdx.x, kBwdEwThreads);
-          zero_rows(dt, L::kChunks, 0, r_lo, threadIdx.x, kBwdEwThreads);
-          zero_rows(dt, L::kChunks, r_hi, kBwdTile, threadIdx.x, kBwdEwThreads);
+          zero_rows(qt, L::kChunks, 0, r_lo, threadIdx.x, W::kEwThreads);
+          zero_rows(qt, L::kChunks, r_hi, kBwdTile, threadIdx.x, W::kEwThreads);
+          zero_rows(dt, L::kChunks, 0, r_lo, threadIdx.x, W::kEwThreads);
+          zero_rows(dt, L::kChunks, r_hi, kBwdTile, threadIdx.x, W::kEwThreads);
           ptx::fence_proxy_async_smem();
         }
       } else if constexpr (kKv) {
         // padding keys see nothing; with causal masking query q sees this
         // key once q + off >= key
-        const int qb = i * kBwdTile + half * 64;
-        const int lo = key >= len ? 64 : (kCausal ? static_cast<int>(key) - off - qb : 0);
+        const int qb = i * kBwdTile + group * W::kCols;
+        const int lo = key >= len ? W::kCols : (kCausal ? static_cast<int>(key) - off - qb : 0);
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
+        for (int e = 0; e < W::kCols; ++e)
           if (e < lo) pf[e] = 0.f;
       } else if (kCausal && i == kt) {   // diagonal tile: a key after the query is masked
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (i * kBwdTile + half * 64 + e < key) pf[e] = 0.f;
+        for (int e = 0; e < W::kCols; ++e)
+          if (i * kBwdTile + group * W::kCols + e < key) pf[e] = 0.f;
       }
       // dropout: keep bits of this key against the thread's 64 queries, from
       // the quad's words (zw[2 k2 + m]: word m of lane k2, blocks 8m + 4h + k2
@@ -1048,7 +1081,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       // zeroed
       if constexpr (kDrop) {
         const uint2 mine = drop_words16<true>(static_cast<uint32_t>(key >> 2),
-                                              static_cast<uint32_t>(i * kBwdTile + half * 64) >> 2,
+                                              static_cast<uint32_t>(i * kBwdTile + group * W::kCols) >> 2,
                                               static_cast<uint32_t>(lane) & 3u,
                                               static_cast<uint32_t>(bh), p.drop_off, p.drop_k0,
                                               p.drop_k1, p.drop_t);
@@ -1060,14 +1093,15 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
         }
       }
       {
-        uint32_t pk[32];
+        uint32_t pk[W::kCols / 2];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < W::kCols / 2; ++e) {
           pk[e] = ptx::pack2<kBf16>(pf[2 * e], pf[2 * e + 1]);
           if constexpr (kDrop) pk[e] &= prmt(zq(e >> 1), 0u, (e & 1) ? 0xBBAAu : 0x9988u);
         }
-        ptx::tmem_st16(tS, pk);          // over S^T columns this warp has read
-        ptx::tmem_st16(tS + 16, pk + 16);
+#pragma unroll
+        for (int c = 0; c < W::kCols / 2; c += 16)
+          ptx::tmem_st16(tS + c, pk + c);   // over S^T columns this warp has read
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
@@ -1076,13 +1110,13 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
 
     // ---- phase 2: dS^T = P^T * (dP^T - D)
     auto phase2 = [&](int it) {
-      const float4* dl4 = reinterpret_cast<const float4*>(vec_of(it) + 128) + half * 16;
+      const float4* dl4 = reinterpret_cast<const float4*>(vec_of(it) + 128) + group * (W::kCols / 4);
       ptx::wait_bounded(xbar(X::kDpFull), it & 1, wd, kSiteBwdDpFull);
       __syncwarp();
       ptx::tc_fence_after();
-      uint32_t dk[32];
+      uint32_t dk[W::kCols / 2];
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
+      for (int ch = 0; ch < W::kCols / 32; ++ch) {
         uint32_t dpr[32];
         ptx::tmem_ld32(tDp + ch * 32, dpr);
         ptx::tmem_wait_ld();
@@ -1118,17 +1152,18 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
         // its batch's count need not be finite
         if (win_lo > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < W::kCols / 2; ++e)
             dk[e] &= (2 * e < win_lo ? 0u : 0xffffu) | (2 * e + 1 < win_lo ? 0u : 0xffff0000u);
         }
-        if (win_hi < 64) {
+        if (win_hi < W::kCols) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < W::kCols / 2; ++e)
             dk[e] &= (2 * e >= win_hi ? 0u : 0xffffu) | (2 * e + 1 >= win_hi ? 0u : 0xffff0000u);
         }
       }
-      ptx::tmem_st16(tDp, dk);           // over dP^T columns this warp has read
-      ptx::tmem_st16(tDp + 16, dk + 16);
+#pragma unroll
+      for (int c = 0; c < W::kCols / 2; c += 16)
+        ptx::tmem_st16(tDp + c, dk + c);   // over dP^T columns this warp has read
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(xbar(X::kDsReady));
@@ -1139,21 +1174,24 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       phase1(it);
       phase2(it);
     }
-    // dV_j rows (warps 0-3) and dK_j = scale * (dS^T Q) rows (warps 4-7)
+    // dV_j rows (the first half of the groups) and dK_j = scale * (dS^T Q)
+    // rows (the second), each warp a part of the columns
     ptx::wait_bounded(xbar(X::kDone), 0, wd, kSiteBwdDone);
     __syncwarp();
     ptx::tc_fence_after();
     const long long row = bwd_krow(p, tok, hd, bh, key);
+    constexpr int kShare = W::kGroups / 2;
+    const bool is_dk = group >= kShare;
+    const uint32_t acc = tmem_base + lane_off + kColAcc + (is_dk ? D : 0);
+    const int width = is_dk ? p.width_qk : p.width_v;
+    const int c0 = group % kShare * (width / kShare);
+    const float mul = is_dk ? p.scale : (kDrop ? p.drop_scale : 1.f);
     if (part_ws != nullptr)
-      store_acc_f32<D>(tmem_base + lane_off + kColAcc + (half == 0 ? 0 : D),
-                       half == 0 ? 1.f : p.scale,
-                       part_ws + static_cast<size_t>(t) * 2 * D + (half == 0 ? D : 0));
-    else if (half == 0)
-      store_acc_cols<kBf16>(tmem_base + lane_off + kColAcc, 0, p.width_v, p.width_v,
-                            kDrop ? p.drop_scale : 1.f, p.dv, row, key < key_rows);
+      store_acc_f32(acc, c0, width / kShare, mul,
+                    part_ws + static_cast<size_t>(t) * 2 * D + (is_dk ? 0 : D));
     else
-      store_acc_cols<kBf16>(tmem_base + lane_off + kColAcc + D, 0, p.width_qk, p.width_qk,
-                            p.scale, p.dk, row, key < key_rows);
+      store_acc_cols<kBf16>(acc, c0, width / kShare, width, mul, is_dk ? p.dk : p.dv, row,
+                            key < key_rows);
   }
   bwd_teardown<L>(sbase);
 }
@@ -1170,6 +1208,7 @@ template <int D, bool kBf16, bool kCausal, bool kDrop, bool kKv, bool kWin = fal
 __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t tmem_base) {
   using L = BwdSmem<D, 0>;
   using X = DqBars;
+  using W = BwdRoles<kWin>;
   static_assert(kColAcc + D + 128 <= kBwdTmemCols, "dS buffers fit in TMEM");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
@@ -1211,7 +1250,7 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
   const int q_rows = tok ? hd.lenq : p.N;
   if (kKv && nk <= 0) {
     // no query of this tile sees a key: its dQ rows are zero
-    if (threadIdx.x < kBwdEwThreads) {
+    if (threadIdx.x < 256) {
       const int t = threadIdx.x & 127, hf = threadIdx.x >> 7;
       const long long qrow = static_cast<long long>(qt) * kBwdTile + t;
       if (qrow < q_rows) {
@@ -1227,16 +1266,16 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
 
   bwd_setup<L>(sbase, sgen, [&](auto b) {
     ptx::mbar_init(b(L::bX + X::kSFull), 1);
-    ptx::mbar_init(b(L::bX + X::kSFree), kBwdEwThreads);
+    ptx::mbar_init(b(L::bX + X::kSFree), W::kEwThreads);
     for (int k = 0; k < 2; ++k) {
-      ptx::mbar_init(b(L::bX + X::kPFull + k), kBwdEwThreads);
+      ptx::mbar_init(b(L::bX + X::kPFull + k), W::kEwThreads);
       ptx::mbar_init(b(L::bX + X::kDsFree + k), 1);
     }
     ptx::mbar_init(b(L::bX + X::kDone), 1);
   });
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
 
-  if (warp == kBwdLoadWarp) {
+  if (warp == W::kLoadWarp) {
     if constexpr (kWin) {
       if (lane == 0) {
         const int kvh = bh / p.H * p.Hk + bh % p.H / p.G;
@@ -1249,8 +1288,8 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
                       tok ? bh % p.H : -1, hd.q0, hd.k0, p.width_qk / 64, p.width_v / 64);
     }
     __syncwarp();
-  } else if (warp == kBwdMmaWarp) {
-    if (lane == 0) {
+  } else if (warp == W::kMmaWarp) {
+    if (kWin || lane == 0) {
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBwdTile, kBwdTile, fmt, 0);
       const uint32_t idesc_dq = ptx::idesc_f16(kBwdTile, p.width_qk, fmt, 1);   // dQ: width_qk columns
@@ -1265,46 +1304,51 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
       const uint32_t tDq = tmem_base + kColAcc;
       // dQ_i += dS_j K_j for key tile j (scale applied at the end)
       auto issue_dq = [&](int j) -> bool {
-        const bool ok = ptx::wait_bounded(xbar(X::kPFull + (j & 1)), (j >> 1) & 1, wd, kSiteBwdPFull);
+        const bool ok = bwd_warp_ok<kWin>(
+            ptx::wait_bounded(xbar(X::kPFull + (j & 1)), (j >> 1) & 1, wd, kSiteBwdPFull));
         ptx::tc_fence_after();
         if (!ok) return false;
         const int slot = j % L::kStagesA;
-        issue_tmem_a<false>(tDq, tmem_base + dq_ds_col<D>(j & 1), k_mn0 + slot * kSlotLo, idesc_dq,
+        if (!bwd_elected<kWin>()) return true;
+        issue_tmem_a<1>(tDq, tmem_base + dq_ds_col<D>(j & 1), k_mn0 + slot * kSlotLo, idesc_dq,
                             j > 0 ? 1u : 0u);
         ptx::mma_commit(bar(L::bEmptyA + slot));
         ptx::mma_commit(xbar(X::kDsFree + (j & 1)));
         return true;
       };
-      bool alive = ptx::wait_bounded(bar(L::bRes), 0, wd, kSiteBwdRes);
+      bool alive = bwd_warp_ok<kWin>(ptx::wait_bounded(bar(L::bRes), 0, wd, kSiteBwdRes));
       for (int it = 0; alive && it < nk; ++it) {
         const int sa = it % L::kStagesA, sb = it % L::kStagesB;
         alive = ptx::wait_bounded(bar(L::bFullA + sa), (it / L::kStagesA) & 1, wd, kSiteBwdFull);
         alive = alive && ptx::wait_bounded(bar(L::bFullB + sb), (it / L::kStagesB) & 1, wd, kSiteBwdFull);
         // the element-wise warps have read S and dP of the previous key tile
         if (it > 0) alive = alive && ptx::wait_bounded(xbar(X::kSFree), (it - 1) & 1, wd, kSiteBwdSFree);
+        alive = bwd_warp_ok<kWin>(alive);
         ptx::tc_fence_after();
         if (!alive) break;
         // S = Q_i K_j^T and dP = dO_i V_j^T (queries on the TMEM lanes)
-        issue_kmajor<D, L::kChunkBytes>(tS, q_lo, k_lo0 + sa * kSlotLo, idesc_s, steps_s);
-        issue_kmajor<D, L::kChunkBytes>(tDp, do_lo, v_lo0 + sb * kSlotLo, idesc_s, steps_dp);
-        ptx::mma_commit(xbar(X::kSFull));
-        ptx::mma_commit(bar(L::bEmptyB + sb));   // V_j is not read again
+        if (bwd_elected<kWin>()) {
+          issue_kmajor<D, L::kChunkBytes>(tS, q_lo, k_lo0 + sa * kSlotLo, idesc_s, steps_s);
+          issue_kmajor<D, L::kChunkBytes>(tDp, do_lo, v_lo0 + sb * kSlotLo, idesc_s, steps_dp);
+          ptx::mma_commit(xbar(X::kSFull));
+          ptx::mma_commit(bar(L::bEmptyB + sb));   // V_j is not read again
+        }
         if (it > 0) alive = issue_dq(it - 1);
       }
       if (alive) issue_dq(nk - 1);
-      ptx::mma_commit(xbar(X::kDone));
+      if (bwd_elected<kWin>()) ptx::mma_commit(xbar(X::kDone));
       ptx::wait_drain(xbar(X::kDone), 0, 200000000ull);
     }
     __syncwarp();
   } else {
     // ============================================================ element-wise
     ptx::griddep_wait();   // D of the pass launched just before this grid
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, group = warp >> 2;
     const int t = quarter * 32 + lane;                    // query row within the tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // this thread's 64 key columns of S and dP
-    const uint32_t tS = tmem_base + lane_off + kColS + half * 64;
-    const uint32_t tDp = tmem_base + lane_off + kColDp + half * 64;
+    // this thread's key columns of S and dP
+    const uint32_t tS = tmem_base + lane_off + kColS + group * W::kCols;
+    const uint32_t tDp = tmem_base + lane_off + kColDp + group * W::kCols;
     const long long qrow = static_cast<long long>(qt) * kBwdTile + t;
     const bool q_in = qrow < q_rows;
     const long long grow = bwd_qrow(p, tok, hd, bh, qrow);
@@ -1320,12 +1364,12 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
       ptx::tc_fence_after();
       // keys past N, and on the diagonal tile keys after this query, are
       // masked (limits relative to this thread's first key column)
-      int lim = p.N - j * kBwdTile - half * 64;
-      int lo = 0;              // kWin: keys of the thread's 64 before the window, sinks aside
+      int lim = p.N - j * kBwdTile - group * W::kCols;
+      int lo = 0;              // kWin: keys of the thread's before the window, sinks aside
       if constexpr (kWin) {
         const int key0 = k_tile(j) * kBwdTile, pos = static_cast<int>(qrow) + off;
-        lim = min(len, pos + 1) - key0 - half * 64;
-        lo = pos - p.win + 1 - key0 - half * 64;
+        lim = min(len, pos + 1) - key0 - group * W::kCols;
+        lo = pos - p.win + 1 - key0 - group * W::kCols;
         // Keys of this tile that no row sees get dS = 0; their rows of K are
         // cleared so that the product with them is 0 whatever they hold (S
         // and dP have read the tile).
@@ -1334,24 +1378,24 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         const int r_sink = min(max(p.sinks - key0, 0), r_lo);
         if (r_sink < r_lo || r_hi < kBwdTile) {
           uint8_t* kt = sgen + L::kRingA + (j % L::kStagesA) * L::kTile;
-          zero_rows(kt, L::kChunks, r_sink, r_lo, threadIdx.x, kBwdEwThreads);
-          zero_rows(kt, L::kChunks, r_hi, kBwdTile, threadIdx.x, kBwdEwThreads);
+          zero_rows(kt, L::kChunks, r_sink, r_lo, threadIdx.x, W::kEwThreads);
+          zero_rows(kt, L::kChunks, r_hi, kBwdTile, threadIdx.x, W::kEwThreads);
           ptx::fence_proxy_async_smem();
         }
       } else if constexpr (kKv) {
         // keys past this head's count, and with causal masking keys after
         // this query's position
-        lim = len - j * kBwdTile - half * 64;
-        if (kCausal) lim = min(lim, static_cast<int>(qrow) + off + 1 - j * kBwdTile - half * 64);
+        lim = len - j * kBwdTile - group * W::kCols;
+        if (kCausal) lim = min(lim, static_cast<int>(qrow) + off + 1 - j * kBwdTile - group * W::kCols);
       } else if (kCausal && j == qt) {
-        lim = min(lim, t + 1 - half * 64);
+        lim = min(lim, t + 1 - group * W::kCols);
       }
       // all of S and dP into registers first: the next products wait for this
-      uint32_t sr[64], dpr[64];
-      ptx::tmem_ld32(tS, sr);
-      ptx::tmem_ld32(tS + 32, sr + 32);
-      ptx::tmem_ld32(tDp, dpr);
-      ptx::tmem_ld32(tDp + 32, dpr + 32);
+      uint32_t sr[W::kCols], dpr[W::kCols];
+#pragma unroll
+      for (int c = 0; c < W::kCols; c += 32) ptx::tmem_ld32(tS + c, sr + c);
+#pragma unroll
+      for (int c = 0; c < W::kCols; c += 32) ptx::tmem_ld32(tDp + c, dpr + c);
       ptx::tmem_wait_ld();
       ptx::tc_fence_before();
       ptx::mbar_arrive(xbar(X::kSFree));     // S and dP may be overwritten now
@@ -1360,7 +1404,7 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
       // of 4 keys each)
       uint32_t zw[8] = {};
       if constexpr (kDrop) {
-        const uint2 mine = drop_words16<false>(static_cast<uint32_t>(j * kBwdTile + half * 64) >> 2,
+        const uint2 mine = drop_words16<false>(static_cast<uint32_t>(j * kBwdTile + group * W::kCols) >> 2,
                                                static_cast<uint32_t>(qrow >> 2),
                                                static_cast<uint32_t>(lane) & 3u,
                                                static_cast<uint32_t>(bh), p.drop_off, p.drop_k0,
@@ -1372,9 +1416,9 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
           zw[2 * k2 + 1] = __shfl_sync(0xffffffffu, mine.y, src);
         }
       }
-      uint32_t dk[32];
+      uint32_t dk[W::kCols / 2];
 #pragma unroll
-      for (int kc = 0; kc < 64; kc += 2) {
+      for (int kc = 0; kc < W::kCols; kc += 2) {
         float x0, x1;
         ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(__uint_as_float(sr[kc]), __uint_as_float(sr[kc + 1])),
                                   c2, nl2), x0, x1);
@@ -1402,16 +1446,16 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         // masked keys by selection (dP of a key outside its batch's count
         // need not be finite): past the position, or before the window and
         // not a sink
-        const int sink = p.sinks - k_tile(j) * kBwdTile - half * 64;
-        if (lo >= 64) lim = min(lim, sink);
-        if (lim < 64) {
+        const int sink = p.sinks - k_tile(j) * kBwdTile - group * W::kCols;
+        if (lo >= W::kCols) lim = min(lim, sink);
+        if (lim < W::kCols) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < W::kCols / 2; ++e)
             dk[e] &= (2 * e >= lim ? 0u : 0xffffu) | (2 * e + 1 >= lim ? 0u : 0xffff0000u);
         }
-        if (lo > 0 && lo < 64) {
+        if (lo > 0 && lo < W::kCols) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < W::kCols / 2; ++e)
             dk[e] &= ((2 * e < lo) & (2 * e >= sink) ? 0u : 0xffffu) |
                      ((2 * e + 1 < lo) & (2 * e + 1 >= sink) ? 0u : 0xffff0000u);
         }
@@ -1422,19 +1466,22 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
       if (j >= 2) ptx::wait_bounded(xbar(X::kDsFree + b), ((j >> 1) - 1) & 1, wd, kSiteBwdDsFree);
       __syncwarp();
       ptx::tc_fence_after();
-      const uint32_t tDs = tmem_base + lane_off + dq_ds_col<D>(b) + half * 32;
-      ptx::tmem_st16(tDs, dk);
-      ptx::tmem_st16(tDs + 16, dk + 16);
+      const uint32_t tDs = tmem_base + lane_off + dq_ds_col<D>(b) + group * (W::kCols / 2);
+#pragma unroll
+      for (int c = 0; c < W::kCols / 2; c += 16) ptx::tmem_st16(tDs + c, dk + c);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       ptx::mbar_arrive(xbar(X::kPFull + b));
     }
-    // dQ = scale * (dS K): each half of the warps writes half of the columns
+    // dQ = scale * (dS K): each group of the warps writes a part of the
+    // columns, 32 at least
     ptx::wait_bounded(xbar(X::kDone), 0, wd, kSiteBwdDone);
     __syncwarp();
     ptx::tc_fence_after();
-    store_acc_cols<kBf16>(tmem_base + lane_off + kColAcc, half * (p.width_qk / 2), p.width_qk / 2,
-                          p.width_qk, p.scale, p.dq, grow, q_in);
+    const int cols = max(p.width_qk / W::kGroups, 32);
+    if (group * cols < p.width_qk)
+      store_acc_cols<kBf16>(tmem_base + lane_off + kColAcc, group * cols, cols, p.width_qk, p.scale,
+                            p.dq, grow, q_in);
   }
   bwd_teardown<L>(sbase);
 }
@@ -1450,11 +1497,12 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
 // TMEM allocation of every item after its first.  Shared memory is sized
 // for the larger layout.
 template <int D, bool kBf16, bool kCausal, bool kDrop = false, bool kKv = false, bool kWin = false>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(BwdRoles<kWin>::kThreads, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
+  using W = BwdRoles<kWin>;
   __shared__ uint32_t s_tmem_base;
   const int warp = threadIdx.x >> 5;
-  if (warp == kBwdMmaWarp) {
+  if (warp == W::kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&s_tmem_base), kBwdTmemCols);
     ptx::tmem_relinquish();
   }
@@ -1474,7 +1522,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kBwdMmaWarp) {
+  if (warp == W::kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, kBwdTmemCols);
   }

@@ -88,7 +88,7 @@ cudaError_t launch_bwd_variant(const BwdParams& p, const void* o, const void* do
            : static_cast<long long>(p.BH) * p.n_ktiles;
   const long long items = k_items + static_cast<long long>(p.BH) * p.n_tiles;
   e = launch_bwd_grid(fa_bwd_kernel<D, kBf16, kCausal, kDrop, kKv, kWin>, p, items, kAlloc, sms,
-                      stream);
+                      stream, BwdRoles<kWin>::kThreads);
   if (e != cudaSuccess || !kWin || p.split_tiles == 0) return e;
   if constexpr (kWin) {
     const dim3 blocks(static_cast<unsigned>(p.BHk * p.split_tiles), kBwdTile * 2 * D / 4 / 256);
