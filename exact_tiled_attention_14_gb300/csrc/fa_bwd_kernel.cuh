@@ -95,8 +95,12 @@ __device__ __forceinline__ bool bwd_elected() {
   return !kWin || ptx::elect_one();
 }
 template <bool kWin>
+__device__ __forceinline__ int bwd_uniform(int x) {   // x is the same in every lane
+  return kWin ? ptx::warp_same(x) : x;
+}
+template <bool kWin>
 __device__ __forceinline__ bool bwd_warp_ok(bool ok) {
-  return kWin ? __all_sync(0xffffffffu, ok) : ok;
+  return kWin ? ptx::warp_all(ok) : ok;
 }
 
 // Sites recorded in the status word when a wait of a backward kernel runs out.
@@ -736,7 +740,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - raw_base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = bwd_uniform<kWin>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
   auto xbar = [&](int i) -> uint32_t { return bar(L::bX + i); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
@@ -863,12 +867,15 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     __syncwarp();
   } else if (warp == W::kMmaWarp) {
     if (kWin || lane == 0) {
+      const uint32_t tmem = bwd_uniform<kWin>(tmem_base);
+      const int n = bwd_uniform<kWin>(nq);
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBwdTile, kBwdTile, fmt, 0);
       // dV has width_v columns, dK width_qk
-      const uint32_t idesc_dv = ptx::idesc_f16(kBwdTile, p.width_v, fmt, 1);
-      const uint32_t idesc_dk = ptx::idesc_f16(kBwdTile, p.width_qk, fmt, 1);
-      const int steps_s = p.width_qk / 16, steps_dp = p.width_v / 16;
+      const uint32_t idesc_dv = ptx::idesc_f16(kBwdTile, kWin ? D : p.width_v, fmt, 1);
+      const uint32_t idesc_dk = ptx::idesc_f16(kBwdTile, kWin ? D : p.width_qk, fmt, 1);
+      const int steps_s = kWin ? D / 16 : p.width_qk / 16;
+      const int steps_dp = kWin ? D / 16 : p.width_v / 16;
       constexpr uint32_t kSlotLo = L::kTile >> 4;
       const uint32_t k_lo = ptx::desc_lo(sbase + L::kRes, 16);
       const uint32_t v_lo = ptx::desc_lo(sbase + L::kRes + L::kTile, 16);
@@ -876,8 +883,8 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       const uint32_t do_lo0 = ptx::desc_lo(sbase + L::kRingB, 16);
       const uint32_t q_mn0 = ptx::desc_lo(sbase + L::kRingA, L::kChunkBytes);      // MN-major use
       const uint32_t do_mn0 = ptx::desc_lo(sbase + L::kRingB, L::kChunkBytes);
-      const uint32_t tS = tmem_base + kColS, tDp = tmem_base + kColDp;
-      const uint32_t tDv = tmem_base + kColAcc, tDk = tmem_base + kColAcc + D;
+      const uint32_t tS = tmem + kColS, tDp = tmem + kColDp;
+      const uint32_t tDv = tmem + kColAcc, tDk = tmem + kColAcc + D;
       auto full_a = [&](int it) {
         return ptx::wait_bounded(bar(L::bFullA + it % L::kStagesA), (it / L::kStagesA) & 1, wd,
                                  kSiteBwdFull);
@@ -906,8 +913,8 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
         issue_s(0);
         issue_dp(0);
       }
-      for (int it = 0; alive && it < nq; ++it) {
-        const bool more = it + 1 < nq;
+      for (int it = 0; alive && it < n; ++it) {
+        const bool more = it + 1 < n;
         alive = bwd_warp_ok<kWin>(
             ptx::wait_bounded(xbar(X::kPReady), it & 1, wd, kSiteBwdPFull));
         ptx::tc_fence_after();
@@ -1183,7 +1190,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
     constexpr int kShare = W::kGroups / 2;
     const bool is_dk = group >= kShare;
     const uint32_t acc = tmem_base + lane_off + kColAcc + (is_dk ? D : 0);
-    const int width = is_dk ? p.width_qk : p.width_v;
+    const int width = kWin ? D : (is_dk ? p.width_qk : p.width_v);
     const int c0 = group % kShare * (width / kShare);
     const float mul = is_dk ? p.scale : (kDrop ? p.drop_scale : 1.f);
     if (part_ws != nullptr)
@@ -1214,7 +1221,7 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - raw_base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = bwd_uniform<kWin>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
   auto xbar = [&](int i) -> uint32_t { return bar(L::bX + i); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
@@ -1290,18 +1297,21 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
     __syncwarp();
   } else if (warp == W::kMmaWarp) {
     if (kWin || lane == 0) {
+      const uint32_t tmem = bwd_uniform<kWin>(tmem_base);
+      const int n = bwd_uniform<kWin>(nk);
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBwdTile, kBwdTile, fmt, 0);
-      const uint32_t idesc_dq = ptx::idesc_f16(kBwdTile, p.width_qk, fmt, 1);   // dQ: width_qk columns
-      const int steps_s = p.width_qk / 16, steps_dp = p.width_v / 16;
+      const uint32_t idesc_dq = ptx::idesc_f16(kBwdTile, kWin ? D : p.width_qk, fmt, 1);   // dQ: width_qk columns
+      const int steps_s = kWin ? D / 16 : p.width_qk / 16;
+      const int steps_dp = kWin ? D / 16 : p.width_v / 16;
       constexpr uint32_t kSlotLo = L::kTile >> 4;
       const uint32_t q_lo = ptx::desc_lo(sbase + L::kRes, 16);
       const uint32_t do_lo = ptx::desc_lo(sbase + L::kRes + L::kTile, 16);
       const uint32_t k_lo0 = ptx::desc_lo(sbase + L::kRingA, 16);                 // K-major use
       const uint32_t v_lo0 = ptx::desc_lo(sbase + L::kRingB, 16);
       const uint32_t k_mn0 = ptx::desc_lo(sbase + L::kRingA, L::kChunkBytes);     // MN-major use
-      const uint32_t tS = tmem_base + kColS, tDp = tmem_base + kColDp;
-      const uint32_t tDq = tmem_base + kColAcc;
+      const uint32_t tS = tmem + kColS, tDp = tmem + kColDp;
+      const uint32_t tDq = tmem + kColAcc;
       // dQ_i += dS_j K_j for key tile j (scale applied at the end)
       auto issue_dq = [&](int j) -> bool {
         const bool ok = bwd_warp_ok<kWin>(
@@ -1310,14 +1320,14 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         if (!ok) return false;
         const int slot = j % L::kStagesA;
         if (!bwd_elected<kWin>()) return true;
-        issue_tmem_a<1>(tDq, tmem_base + dq_ds_col<D>(j & 1), k_mn0 + slot * kSlotLo, idesc_dq,
+        issue_tmem_a<1>(tDq, tmem + dq_ds_col<D>(j & 1), k_mn0 + slot * kSlotLo, idesc_dq,
                             j > 0 ? 1u : 0u);
         ptx::mma_commit(bar(L::bEmptyA + slot));
         ptx::mma_commit(xbar(X::kDsFree + (j & 1)));
         return true;
       };
       bool alive = bwd_warp_ok<kWin>(ptx::wait_bounded(bar(L::bRes), 0, wd, kSiteBwdRes));
-      for (int it = 0; alive && it < nk; ++it) {
+      for (int it = 0; alive && it < n; ++it) {
         const int sa = it % L::kStagesA, sb = it % L::kStagesB;
         alive = ptx::wait_bounded(bar(L::bFullA + sa), (it / L::kStagesA) & 1, wd, kSiteBwdFull);
         alive = alive && ptx::wait_bounded(bar(L::bFullB + sb), (it / L::kStagesB) & 1, wd, kSiteBwdFull);

@@ -351,6 +351,15 @@ __host__ __device__ __forceinline__ int win_next_cut(const Piece& u, int from, i
   if (from < u.nl && win_cut(u, u.nl - 1, sinks)) return u.nl - 1;
   return u.nl;
 }
+// Marks what the MMA warps' loops read of a piece as the same in every lane.
+__device__ __forceinline__ void win_same(Piece& u) {
+  u.n0 = ptx::warp_same(u.n0);
+  u.n1 = ptx::warp_same(u.n1);
+  u.ns = ptx::warp_same(u.ns);
+  u.wa = ptx::warp_same(u.wa);
+  u.nl = ptx::warp_same(u.nl);
+  u.gap = ptx::warp_same(u.gap);
+}
 // Key/value head of query head bh (kWin: Hk heads shared by groups).
 __host__ __device__ __forceinline__ int kv_head(const FwdParams& p, int bh) {
   return (bh / p.H) * p.Hk + (bh % p.H) / (p.H / p.Hk);
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - raw_base);  // generic pointer to the aligned base
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = kWin ? ptx::warp_same(threadIdx.x >> 5) : threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
   uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
@@ -783,9 +792,12 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     // K16 MMA lasts ~64 cycles), so descriptors are precomputed: per MMA only
     // the 32-bit address word changes, by a compile-time offset.
     // Warp 8 issues the S = Q K^T products, warp 10 the O += P V products,
-    // each from its first lane.  In the kWin variants all of warp 10 walks
-    // the tiles, since it also clears rows of V (below).
-    if (lane == 0 || (kWin && warp == kPvWarp)) {
+    // each from its first lane.  In the kWin variants the whole warp walks
+    // the tiles and one elected lane issues: conditions, descriptors and
+    // addresses then stay in uniform registers.
+    auto warp_ok = [](bool ok) { return kWin ? ptx::warp_all(ok) : ok; };
+    auto elected = [] { return !kWin || ptx::elect_one(); };
+    if (kWin || lane == 0) {
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBM, kBN, fmt, 0);  // Q (K-major) x K (K-major)
       constexpr uint32_t idesc_o_full = ptx::idesc_f16(kBM, D, fmt, 1);  // P x V (MN-major)
@@ -798,8 +810,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       const uint32_t k_lo0 = ptx::desc_lo(sbase + L::kKV, 16);
       const uint32_t v_lo0 = ptx::desc_lo(sbase + L::kKV, L::kChunkBytes);
       constexpr uint32_t kSlotLo = L::kTile >> 4;
-      const uint32_t tS0 = tmem_base + s_col<D>(0), tS1 = tmem_base + s_col<D>(1);
-      const uint32_t tO0 = tmem_base + o_col<D>(0), tO1 = tmem_base + o_col<D>(1);
+      const uint32_t tmem = kWin ? ptx::warp_same(tmem_base) : tmem_base;
+      const uint32_t tS0 = tmem + s_col<D>(0), tS1 = tmem + s_col<D>(1);
+      const uint32_t tO0 = tmem + o_col<D>(0), tO1 = tmem + o_col<D>(1);
 
       // S = Q_w K^T over the head width: K-major operands, 128-byte swizzle;
       // a K step of 16 columns moves 32 bytes inside a swizzle row, and every
@@ -848,22 +861,22 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       // With a P buffer per query tile, S_w_{j+1} waits only until the
       // softmax has read S_w_j, and P_w_j V_j only for P_w_j.
       // P_w: TMEM column address, or the address word of its shared-memory descriptor
-      const uint32_t tP0 = OwnP<D>::kSmem ? ptx::desc_lo(sbase + L::kP, 16) : tmem_base + p_col<D>(0);
+      const uint32_t tP0 = OwnP<D>::kSmem ? ptx::desc_lo(sbase + L::kP, 16) : tmem + p_col<D>(0);
       const uint32_t tP1 = OwnP<D>::kSmem ? ptx::desc_lo(sbase + L::kP + kBM * kBN * 2, 16)
-                                          : tmem_base + p_col<D>(1);
+                                          : tmem + p_col<D>(1);
       uint32_t sc0 = 0, sc1 = 0;     // S issued into S0 / S1 so far
       uint32_t q_add = 0;            // address-word offset of the current unit's Q buffer
       auto wait_s_own = [&](int w) {
         const uint32_t sc = w ? sc1 : sc0;
         pf.lap(6);
         if (sc > 0)   // the softmax has read the previous S of this tile
-          alive = ptx::wait_bounded(bar(L::bSFree + w), (sc - 1) & 1, wd, kSiteSFree) && alive;
+          alive = warp_ok(ptx::wait_bounded(bar(L::bSFree + w), (sc - 1) & 1, wd, kSiteSFree)) && alive;
         pf.lap(16);
       };
       auto do_s_own = [&](int w, uint32_t kslot_) {
         uint32_t& sc = w ? sc1 : sc0;
         ptx::tc_fence_after();
-        if (alive) {
+        if (alive && elected()) {
           issue_s(w ? tS1 : tS0, (w ? q_lo1 : q_lo0) + q_add, k_lo0 + kslot_ * kSlotLo);
           ptx::mma_commit(bar(L::bSFull + w));
         }
@@ -880,15 +893,15 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         const uint32_t ucnt = w ? ucnt1 : ucnt0;
         pf.lap(6);
         if (j == 0 && ucnt > 0)   // O_w of the previous piece must have been read out
-          alive = ptx::wait_bounded(bar(L::bOFree + w), (ucnt - 1) & 1, wd, kSiteOFree) && alive;
+          alive = warp_ok(ptx::wait_bounded(bar(L::bOFree + w), (ucnt - 1) & 1, wd, kSiteOFree)) && alive;
         pf.lap(3);
-        alive = ptx::wait_bounded(bar(L::bPFull + w), pph, wd, kSitePFull) && alive;
+        alive = warp_ok(ptx::wait_bounded(bar(L::bPFull + w), pph, wd, kSitePFull)) && alive;
         pf.lap(1);
         pph ^= 1u;
       };
       auto do_pv_own = [&](int w, int j, uint32_t v_lo) {
         ptx::tc_fence_after();
-        if (alive) {
+        if (alive && elected()) {
           issue_pv(w ? tO1 : tO0, w ? tP1 : tP0, v_lo, j > 0 ? 1u : 0u);
           ptx::mma_commit(bar(L::bPvDone + w));
         }
@@ -912,9 +925,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       auto ring_wait = [&](uint32_t pos) -> uint32_t {
         const uint32_t sl = pos % L::kStages;
         pf.lap(6);
-        alive = ptx::wait_bounded(full0 + 8u * sl,
+        alive = warp_ok(ptx::wait_bounded(full0 + 8u * sl,
                                   L::kTwoFull ? (odd >> sl) & 1u : (pos / L::kStages) & 1u, wd,
-                                  kSiteKvFull) && alive;
+                                  kSiteKvFull)) && alive;
         if (L::kTwoFull) odd ^= 1u << sl;
         pf.lap(0);
         ptx::tc_fence_after();
@@ -924,12 +937,12 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       if (warp == kMmaWarp) {
         // S = Q K^T for both query tiles, one key tile ahead of the softmax
         while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
+          if constexpr (kWin) win_same(u);
           const int nkv = kWin ? u.nl : max(u.n0, u.n1);
           if (kKv && nkv == 0) continue;
           pf.lap(6);
           const uint32_t qb = k_units % L::kQBufs;
-          alive = ptx::wait_bounded(bar(L::bQFull + qb), (k_units / L::kQBufs) & 1, wd, kSiteQFull) &&
-                  alive;
+          alive = warp_ok(ptx::wait_bounded(bar(L::bQFull + qb), (k_units / L::kQBufs) & 1, wd, kSiteQFull)) && alive;
           q_add = qb * static_cast<uint32_t>((2 * L::kTile) >> 4);
           pf.lap(2);
           ptx::tc_fence_after();
@@ -951,7 +964,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
               if (j < u.n0) issue_s_own(0, kslot);
               if (j < u.n1) issue_s_own(1, kslot);
             }
-            if (alive) {
+            if (alive && elected()) {
               ptx::mma_commit(bar(L::bKvEmpty + kslot));
               if (j + 1 == nkv) ptx::mma_commit(bar(L::bQEmpty + qb));  // last use of Q
             }
@@ -995,48 +1008,36 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         // of such keys in the loaded V tile are overwritten with zeros first.
         // These are the first and last tiles of the list and the last sink
         // tile; the tensor core meanwhile works on S and the softmax on P.
-        // Lane 0 alone waits on barriers, and the other lanes join it only at
-        // such tiles: a lane that polled on its own could miss a phase that
-        // lane 0's progress lets pass twice.
         while (next_piece<kCausal, kSplit, kKv, kWin>(p, cta, grid, cu, u)) {
+          win_same(u);
           const int nkv = u.nl;
           if (nkv == 0) continue;
           int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
-          auto vpos = [&](int j) { return base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u); };
-          bool landed = false;             // tile j has been waited for (and cleared)
-          for (int j = 0;;) {
-            const int jc = win_next_cut(u, landed ? j + 1 : j, p.sinks);
-            if (lane == 0) {
-              for (; j < jc; ++j) {
-                uint32_t vslot = vpos(j) % L::kStages;
-                if (!landed) vslot = ring_wait(vpos(j));
-                landed = false;
-                const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
-                if (win_active(u, 0, j)) issue_pv_own(0, it0++, v_lo);
-                if (win_active(u, 1, j)) issue_pv_own(1, it1++, v_lo);
-                if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
+          int cut = ptx::warp_same(win_next_cut(u, 0, p.sinks));
+          for (int j = 0; j < nkv; ++j) {
+            const uint32_t vslot = ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u));
+            if (j == cut) {
+              const int key0 = win_tile(u, j) * kBN;
+              const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
+              const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
+              const int r_sink = min(max(p.sinks - key0, 0), r_lo);
+              uint8_t* vt = sgen + L::kKV + vslot * L::kTile;
+              for (int ch = 0; ch < L::kChunks; ++ch) {
+                uint4* rows = reinterpret_cast<uint4*>(vt + ch * L::kChunkBytes);
+                for (int i = r_sink * 8 + lane; i < r_lo * 8; i += 32)
+                  rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = r_hi * 8 + lane; i < kBN * 8; i += 32)
+                  rows[i] = make_uint4(0u, 0u, 0u, 0u);
               }
-              issued_any = true;
-              if (jc < nkv) ring_wait(vpos(jc));
+              ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
+              __syncwarp();
+              cut = ptx::warp_same(win_next_cut(u, j + 1, p.sinks));
             }
-            __syncwarp();
-            if (jc >= nkv) break;
-            j = jc;
-            const int key0 = win_tile(u, j) * kBN;
-            const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
-            const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
-            const int r_sink = min(max(p.sinks - key0, 0), r_lo);
-            uint8_t* vt = sgen + L::kKV + vpos(j) % L::kStages * L::kTile;
-            for (int ch = 0; ch < L::kChunks; ++ch) {
-              uint4* rows = reinterpret_cast<uint4*>(vt + ch * L::kChunkBytes);
-              for (int i = r_sink * 8 + lane; i < r_lo * 8; i += 32)
-                rows[i] = make_uint4(0u, 0u, 0u, 0u);
-              for (int i = r_hi * 8 + lane; i < kBN * 8; i += 32)
-                rows[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
-            landed = true;
-            __syncwarp();
+            const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
+            if (win_active(u, 0, j)) issue_pv_own(0, it0++, v_lo);
+            if (win_active(u, 1, j)) issue_pv_own(1, it1++, v_lo);
+            if (alive && elected()) ptx::mma_commit(bar(L::bKvEmpty + vslot));
+            issued_any = true;
           }
           if (u.n0 > 0) ++ucnt0;
           if (u.n1 > 0) ++ucnt1;
@@ -1049,7 +1050,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       // Drain: every MMA issued by this thread has completed before TMEM is freed.
       if (issued_any) {
         const uint32_t fb = bar(pv_thread ? L::bFinalPv : L::bFinal);
-        ptx::mma_commit(fb);
+        if (elected()) ptx::mma_commit(fb);
         ptx::wait_drain(fb, 0, 200000000ull);
       }
     }
