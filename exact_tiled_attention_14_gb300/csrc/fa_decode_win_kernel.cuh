@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - raw_base);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = ptx::warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
   uint32_t* tmem_base_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
@@ -554,7 +554,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       __syncwarp();
     } else if (warp == kDwSWarp) {
       // ============================================================ S = Q K^T
-      if (lane == 0) {
+      // The whole warp walks the tiles and one elected lane issues: conditions,
+      // descriptors and addresses then stay in uniform registers.
+      {
+        const uint32_t tmem = ptx::warp_same(tmem_base);
         constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, kDwTile, kBf16 ? 1 : 0, 0);
         const uint32_t q_lo = ptx::desc_lo(sbase + L::kQ, 16);
         const uint32_t k_lo = ptx::desc_lo(sbase + L::kKV, 16);
@@ -562,68 +565,72 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         DwRing<L::kStages> ring;
         uint32_t pieces = 0, sc[2] = {0, 0}, odd = 0;
         bool alive = true, issued = false;
-        while (dec_next(p, cu, pc)) {
+        while (ptx::warp_all(dec_next(p, cu, pc))) {
           const uint32_t qb = pieces % L::kQBufs;
-          alive = alive && ptx::wait_bounded(bar(L::bQFull + qb), (pieces / L::kQBufs) & 1, wd,
-                                             kSiteDwQFull);
-          const bool second = kTiles == 2 && rows_of(pc, 1) > 0;
-          for (int j = 0; j < pc.n; ++j) {
+          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bQFull + qb),
+                                                           (pieces / L::kQBufs) & 1, wd,
+                                                           kSiteDwQFull));
+          const bool second = kTiles == 2 && ptx::warp_all(rows_of(pc, 1) > 0);
+          const int n = ptx::warp_same(pc.n);
+          for (int j = 0; j < n; ++j) {
             const uint32_t slot = ring.slot;
-            alive = alive && ptx::wait_bounded(bar(L::bKFull + slot), (odd >> slot) & 1u, wd,
-                                               kSiteDwKvFull);
+            alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bKFull + slot),
+                                                             (odd >> slot) & 1u, wd,
+                                                             kSiteDwKvFull));
             odd ^= 1u << slot;   // per slot: parity of its K tiles so far
-            ring.step(j == 0 ? (pc.n == 1 ? 2 : 1) : (j + 1 == pc.n ? 3 : 2));
+            ring.step(j == 0 ? (n == 1 ? 2 : 1) : (j + 1 == n ? 3 : 2));
             ptx::tc_fence_after();
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               if (kTiles == 1 ? (j & 1) != w : w == 1 && !second) continue;
               if (sc[w] > 0)   // the softmax has read this group's previous S (over
                                // which, at d = 128, P was written and must be read too)
-                alive = alive && ptx::wait_bounded(bar((L::kOwnP ? L::bSFree : L::bPvDone) + w),
-                                                   (sc[w] - 1) & 1, wd, kSiteDwSFree);
+                alive = ptx::warp_all(
+                    alive && ptx::wait_bounded(bar((L::kOwnP ? L::bSFree : L::bPvDone) + w),
+                                               (sc[w] - 1) & 1, wd, kSiteDwSFree));
               ++sc[w];
               ptx::tc_fence_after();
               if (!alive) continue;
+              issued = true;
+              if (!ptx::elect_one()) continue;
               const uint32_t a = q_lo + (qb * kTiles + (kTiles == 2 ? w : 0)) * (L::kTile >> 4);
               const uint32_t b = k_lo + slot * (L::kTile >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off =
                     static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-                ptx::mma_ss(tmem_base + L::s_col(w), ptx::desc_sw128(a + off), ptx::desc_sw128(b + off), idesc,
-                            kk > 0);
+                ptx::mma_ss(tmem + L::s_col(w), ptx::desc_sw128(a + off), ptx::desc_sw128(b + off),
+                            idesc, kk > 0);
               }
               ptx::mma_commit(bar(L::bSFull + w));
-              issued = true;
             }
-            if (alive) {
+            if (alive && ptx::elect_one()) {
               ptx::mma_commit(bar(L::bKvEmpty + slot));
-              if (j + 1 == pc.n) ptx::mma_commit(bar(L::bQEmpty + qb));
+              if (j + 1 == n) ptx::mma_commit(bar(L::bQEmpty + qb));
             }
           }
           ++pieces;
         }
         if (issued) {
-          ptx::mma_commit(bar(L::bFinalS));
+          if (ptx::elect_one()) ptx::mma_commit(bar(L::bFinalS));
           ptx::wait_drain(bar(L::bFinalS), 0, 200000000ull);
         }
       }
       __syncwarp();
     } else if (warp == kDwPvWarp) {
       // ============================================================ O += P V
-      // The whole warp walks the tiles.  Rows of V that are no key some row
-      // sees (box padding, past the keys, drafted slots that no row marks)
-      // meet weights 0, but 0 times a value that is not finite is not 0, so
-      // they are overwritten with zeros.  Lane 0 alone waits on barriers and
-      // the warp joins it afterwards: a lane that polled on its own could miss
-      // a phase that lane 0's progress lets pass twice.
+      // The whole warp walks the tiles, as above.  Rows of V that are no key
+      // some row sees (box padding, past the keys, drafted slots that no row
+      // marks) meet weights 0, but 0 times a value that is not finite is not
+      // 0, so they are overwritten with zeros.
+      const uint32_t tmem = ptx::warp_same(tmem_base);
       constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, D, kBf16 ? 1 : 0, 1);
       const uint32_t v_lo = ptx::desc_lo(sbase + L::kKV, L::kChunkBytes);
       const uint32_t p_lo = ptx::desc_lo(sbase + L::kP, 16);   // where P is in shared memory
       DwRing<L::kStages> ring;
       uint32_t pcn[2] = {0, 0}, units[2] = {0, 0}, odd = 0;
       bool alive = true, issued = false, cut_here = false;
-      while (dec_next(p, cu, pc)) {
+      while (ptx::warp_all(dec_next(p, cu, pc))) {
         // a tree's keys below `from` are before the window of its shallowest
         // token; `holes` are the drafted tokens that no row marks
         int from = 0;
@@ -642,11 +649,13 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         }
         const int lead = min(from, pc.s.len);          // keys before every window end here
         const DecRange plain = dec_plain(pc.s, lead, holes ? pc.s.len : pc.s.hi);
-        const bool second = kTiles == 2 && rows_of(pc, 1) > 0;
-        // tile j's product for the groups that take it, by lane 0
+        const bool second = kTiles == 2 && ptx::warp_all(rows_of(pc, 1) > 0);
+        const int n = ptx::warp_same(pc.n);
+        const int keep0 = ptx::warp_same(plain.from - pc.t0), keep1 = ptx::warp_same(plain.to - pc.t0);
+        // tile j's product for the groups that take it
         auto wait_v = [&](uint32_t slot) {
-          alive = alive && ptx::wait_bounded(bar(L::bVFull + slot), (odd >> slot) & 1u, wd,
-                                             kSiteDwKvFull);
+          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bVFull + slot),
+                                                           (odd >> slot) & 1u, wd, kSiteDwKvFull));
           odd ^= 1u << slot;   // per slot: parity of its V tiles so far
         };
         auto issue = [&](int j, uint32_t slot) {
@@ -655,12 +664,15 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             if (kTiles == 1 ? (j & 1) != w : w == 1 && !second) continue;
             const bool first = kTiles == 1 ? j == w : j == 0;
             if (first && units[w] > 0)   // the previous unit's O has been read
-              alive = alive && ptx::wait_bounded(bar(L::bOFree + w), (units[w] - 1) & 1, wd,
-                                                 kSiteDwOFree);
-            alive = alive && ptx::wait_bounded(bar(L::bPFull + w), pcn[w] & 1, wd, kSiteDwPFull);
+              alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bOFree + w),
+                                                               (units[w] - 1) & 1, wd,
+                                                               kSiteDwOFree));
+            alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bPFull + w), pcn[w] & 1, wd,
+                                                             kSiteDwPFull));
             ++pcn[w];
             ptx::tc_fence_after();
-            if (alive) {
+            if (alive) issued = true;
+            if (alive && ptx::elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kDwTile / 16; ++kk) {
                 const uint64_t vd =
@@ -668,30 +680,25 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                 const uint32_t acc = (kk > 0 || !first) ? 1u : 0u;
                 if constexpr (L::kSmemP) {   // K-major, 64 keys to a chunk
                   const uint32_t off = (kk >> 2) * L::kChunkBytes + (kk & 3) * 32;
-                  ptx::mma_ss(tmem_base + L::o_col(w),
+                  ptx::mma_ss(tmem + L::o_col(w),
                               ptx::desc_sw128(p_lo + ((w * L::kPTile + off) >> 4)), vd, idesc, acc);
                 } else {
-                  ptx::mma_ts(tmem_base + L::o_col(w), tmem_base + L::p_col(w) + kk * 8, vd, idesc,
+                  ptx::mma_ts(tmem + L::o_col(w), tmem + L::p_col(w) + kk * 8, vd, idesc,
                               acc);
                 }
               }
               ptx::mma_commit(bar(L::bPvDone + w));
-              issued = true;
             }
           }
-          if (alive) ptx::mma_commit(bar(L::bKvEmpty + slot));
+          if (alive && ptx::elect_one()) ptx::mma_commit(bar(L::bKvEmpty + slot));
         };
         // V tiles sit at ring positions 2, 4, ..., 2 n - 2 and 2 n - 1 of the
-        // piece's 2 n.  The other lanes join lane 0 only at tiles with rows to
-        // clear: sinks' padding, past the keys, before every window, drafted
-        // slots.
-        for (int j = 0; j < pc.n; ++j) {
-          ring.step(j + 1 < pc.n ? 2 : 1);
-          const bool keep = pc.t0 + j >= plain.from && pc.t0 + j < plain.to;
-          if (keep && lane != 0) continue;
-          if (lane == 0) wait_v(ring.slot);
-          if (!keep) {
-            __syncwarp();
+        // piece's 2 n.  Tiles with rows to clear: sinks' padding, past the keys,
+        // before every window, drafted slots.
+        for (int j = 0; j < n; ++j) {
+          ring.step(j + 1 < n ? 2 : 1);
+          wait_v(ring.slot);
+          if (j < keep0 || j >= keep1) {
             const DecTile t = dec_tile(pc.s, pc.t0 + j);
             auto clear = [&](int r0, int r1) {
               for (int c = 0; c < L::kChunks; ++c) {
@@ -709,10 +716,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             ptx::fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) issue(j, ring.slot);
+          issue(j, ring.slot);
         }
         ring.step();
-        __syncwarp();
         // kTiles == 1: both groups read both outputs, and arrive for a group
         // that had no tile too
         ++units[0];
@@ -728,8 +734,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         }
       }
       if (lane == 0 && !cut_here) p.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
-      if (issued) {   // lane 0 only
-        ptx::mma_commit(bar(L::bFinalPv));
+      if (issued) {
+        if (ptx::elect_one()) ptx::mma_commit(bar(L::bFinalPv));
         ptx::wait_drain(bar(L::bFinalPv), 0, 200000000ull);
       }
       __syncwarp();
