@@ -137,8 +137,10 @@ int decode(const void* q, const void* k, const void* v, void* o, float* lse, int
   const void* vp = has_k ? v : q;
   const int kh = has_k ? bhk : 1, kn = has_k ? Nk : 1;
   const int q_box = R <= kDwTile ? kDwTile / copies_of(R) : kDwTile;
-  if (!make_tmap(&p.tm_q, q, bhk, R, d, bf16, q_box) || !make_tmap(&p.tm_k, kp, kh, kn, d, bf16) ||
-      !make_tmap(&p.tm_v, vp, kh, kn, d, bf16) ||
+  const int kv_box = dec_big_box(R > kDwTile ? 2 : 1);
+  if (!make_tmap(&p.tm_q, q, bhk, R, d, bf16, q_box) ||
+      !make_tmap(&p.tm_k, kp, kh, kn, d, bf16, kv_box) ||
+      !make_tmap(&p.tm_v, vp, kh, kn, d, bf16, kv_box) ||
       !make_tmap(&p.tm_k16, kp, kh, kn, d, bf16, kDwBox) ||
       !make_tmap(&p.tm_v16, vp, kh, kn, d, bf16, kDwBox))
     return FA_ERR_TENSORMAP;

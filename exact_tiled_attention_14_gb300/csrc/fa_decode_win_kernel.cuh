@@ -53,6 +53,11 @@ namespace fa {
 constexpr int kDwThreads = 384;
 constexpr int kDwTile = 128;          // keys per tile, rows per row tile
 constexpr int kDwBox = 16;            // rows of the small load box
+// Rows of the other.  With one row tile 64, in which sink tiles and spans'
+// last tiles take fewer copies (16 caches of 2000 keys and 5 sinks, d = 64:
+// 41.4 -> 38.9 us); with two, which wait less for copies than for products,
+// 128 (8 caches of 131k keys, d = 128: 772 us against 891 with 64).
+constexpr int dec_big_box(int tiles) { return tiles == 2 ? 128 : 64; }
 constexpr int kDwSWarp = 8, kDwLoadWarp = 9, kDwPvWarp = 10;
 constexpr uint32_t kDwSoftmaxRegs = 208, kDwIssueRegs = 88;
 static_assert(2 * 128 * kDwSoftmaxRegs + 128 * kDwIssueRegs <= 168 * kDwThreads, "register split");
@@ -68,7 +73,7 @@ enum DwWaitSite : uint32_t {
 
 struct DecWinParams {
   CUtensorMap tm_q;        // [B * Hk, R, d], boxes of 128 / kCopies rows x 64 columns, 128-byte swizzle
-  CUtensorMap tm_k;        // [B * Hk, Nk, d], boxes of 128 rows
+  CUtensorMap tm_k;        // [B * Hk, Nk, d], boxes of dec_big_box rows
   CUtensorMap tm_v;
   CUtensorMap tm_k16;      // the same tensors in boxes of 16 rows
   CUtensorMap tm_v16;
@@ -488,12 +493,16 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             const uint32_t dst = sbase + L::kKV + slot * L::kTile, full = bar((v ? L::bVFull : L::bKFull) + slot);
             (v ? v_odd : k_odd) ^= 1u << slot;
             (v ? v_used : k_used) |= 1u << slot;
-            if (pc.t0 + j >= plain.from && pc.t0 + j < plain.to) {   // one box of 128 rows
+            constexpr int kBig = dec_big_box(kTiles);
+            const CUtensorMap* big = v ? &p.tm_v : &p.tm_k;
+            if (pc.t0 + j >= plain.from && pc.t0 + j < plain.to) {   // 128 rows of the cache
               ptx::mbar_arrive_expect_tx(full, L::kTile);
 #pragma unroll
               for (int c = 0; c < L::kChunks; ++c)
-                ptx::tma_load_3d(dst + c * L::kChunkBytes, v ? &p.tm_v : &p.tm_k, full, c * 64,
-                                 plain.base + (pc.t0 + j) * kDwTile, head);
+#pragma unroll
+                for (int i = 0; i < kDwTile; i += kBig)
+                  ptx::tma_load_3d(dst + c * L::kChunkBytes + i * 128, big, full, c * 64,
+                                   plain.base + (pc.t0 + j) * kDwTile + i, head);
             } else {
               const DecTile t = dec_tile(pc.s, pc.t0 + j);
               // boxes of 16 rows; a tile without keys still loads one box,
@@ -506,9 +515,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                 for (int i = 0; i < bs; ++i)
                   ptx::tma_load_3d(dst + c * L::kChunkBytes + i * kDwBox * 128, tm, full, c * 64,
                                    t.sink0 + i * kDwBox, head);
-                for (int i = 0; i < bw; ++i)
-                  ptx::tma_load_3d(dst + c * L::kChunkBytes + (bs + i) * kDwBox * 128, tm, full,
-                                   c * 64, t.key0 + i * kDwBox, head);
+                for (int i = 0; i < bw;) {
+                  const bool wide = bw - i >= kBig / kDwBox;
+                  ptx::tma_load_3d(dst + c * L::kChunkBytes + (bs + i) * kDwBox * 128,
+                                   wide ? big : tm, full, c * 64, t.key0 + i * kDwBox, head);
+                  i += wide ? kBig / kDwBox : 1;
+                }
               }
             }
             ++loads;
