@@ -41,20 +41,27 @@ int check_window_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int causal, 
 // Cut of the sink tiles of the backward pass: every query tile after a sink
 // tile visits it, where a window's tile is visited by about window / 128 + 2,
 // and the CTAs' work is dealt by items.  So a sink tile is cut into as many
-// parts as give each the steps of a window's tile (measured on B1 H32/8 N16384
-// window 2048, 64 sinks: uncut, 8 of 152 CTAs hold one item with half of a
-// CTA's whole share, figures in fa_bwd_win.cu).
+// parts as give each the steps of a window's tile (a training step of B1
+// H32/8 N16384 d128 window 2048 with 64 sinks: 2150 us, against 3015 with
+// whole tiles, of which 8 of 152 CTAs hold one with half of a CTA's whole
+// share each).  kMaxParts parts in all, four for each of 152 SMs, even the
+// work out and bound the workspace (80 MB at d = 128); more sink tiles than
+// that are dealt whole.
+constexpr long long kMaxParts = 608;
 struct SinkSplit {
   int tiles = 0, parts = 1;
 };
-SinkSplit sink_split(int Nq, int Nk, int window, int sinks) {
+SinkSplit sink_split(int BHk, int Nq, int Nk, int window, int sinks) {
   SinkSplit s;
+  const int used = std::min(sinks, Nk);
+  if (used == 0 || BHk == 0) return s;
+  const int tiles = (used + fa::kBwdTile - 1) / fa::kBwdTile;
   const long long q_tiles = (static_cast<long long>(Nq) + fa::kBwdTile - 1) / fa::kBwdTile;
   const long long per = static_cast<long long>(window) / fa::kBwdTile + 2;
-  const long long parts = std::min<long long>((q_tiles + per - 1) / per, 64);
-  const int used = std::min(sinks, Nk);
-  if (used == 0 || parts < 2) return s;
-  s.tiles = (used + fa::kBwdTile - 1) / fa::kBwdTile;
+  const long long parts = std::min<long long>((q_tiles + per - 1) / per,
+                                              kMaxParts / (static_cast<long long>(BHk) * tiles));
+  if (parts < 2) return s;
+  s.tiles = tiles;
   s.parts = static_cast<int>(parts);
   return s;
 }
@@ -136,7 +143,7 @@ int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, in
   if (!bytes) return FA_ERR_NULLPTR;
   const int rc = check_window_sizes(B, H, Hk, Nq, Nk, d, 1, window, sinks, 1.0f, FA_BF16);
   if (rc != FA_OK) return rc;
-  const SinkSplit sp = sink_split(Nq, Nk, window, sinks);
+  const SinkSplit sp = sink_split(B * Hk, Nq, Nk, window, sinks);
   *bytes = static_cast<size_t>(B) * Hk * sp.tiles * sp.parts * fa::kBwdTile * 2 * d * sizeof(float);
   return FA_OK;
 }
@@ -204,7 +211,7 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
   p.Hk = Hk;
   p.G = H / Hk;
   p.BHk = bhk;
-  const SinkSplit sp = sink_split(Nq, Nk, window, sinks);
+  const SinkSplit sp = sink_split(B * Hk, Nq, Nk, window, sinks);
   p.split_tiles = sp.tiles;
   p.split_parts = sp.parts;
   p.split_ws = static_cast<float*>(workspace);

@@ -73,6 +73,16 @@ def test_backward_workspace_size(lib):
     assert lib.fa_bwd_window_workspace_size(2, 6, 3, 3000, 3000, 64, 100, 4, None) == fa.FA_ERR_NULLPTR
 
 
+@pytest.mark.parametrize("B,Hk,N,window,sinks", [(1, 8, 16384, 2048, 64), (8, 8, 131072, 1, 131072),
+                                                 (1, 1, 1 << 20, 1, 70000), (64, 32, 65536, 100, 4)])
+def test_backward_workspace_is_bounded(lib, B, Hk, N, window, sinks):
+    """However many sink tiles there are, at most 608 parts of 128 x 2 d floats."""
+    n = ctypes.c_size_t(1)
+    assert lib.fa_bwd_window_workspace_size(B, Hk, Hk, N, N, 128, window, sinks, ctypes.byref(n)) == fa.FA_OK
+    assert n.value <= 608 * 128 * 256 * 4
+    assert (n.value > 0) == (B * Hk * -(-sinks // 128) <= 304)
+
+
 DEC = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=FAKE, B=2, H=6, Hk=3, Nq=4, Nk=500, d=128, window=100,
            sinks=4, seqlens_k=FAKE, scale=0.1, dtype=fa.FA_FP16, workspace=FAKE,
            workspace_bytes=1 << 40)
