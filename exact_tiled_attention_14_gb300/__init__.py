@@ -1002,9 +1002,10 @@ def attention_forward_window(q, k, v, window, sinks=0, causal="bottom_right", se
             out = torch.empty_like(q)
         if lse is None:
             lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        rc = fa_fwd_window(q, k, v, out, lse, *dims, CAUSAL_MODES[causal], _int32(window),
-                           _int32(sinks), seqlens_k, d ** -0.5 if scale is None else scale, code,
-                           _current(stream, q))
+        rc = load_library().fa_fwd_window(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *dims,
+            CAUSAL_MODES[causal], _int32(window), _int32(sinks), _addr(seqlens_k),
+            d ** -0.5 if scale is None else float(scale), code, _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_window")
     return out, lse
@@ -1033,9 +1034,11 @@ def attention_backward_window(q, k, v, o, lse, dout, window, sinks=0, causal="bo
         ws, ws_bytes = _workspace_arg(workspace, q.device)
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         delta = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        rc = fa_bwd_window(q, k, v, o, lse, dout, dq, dk, dv, delta, *dims, CAUSAL_MODES[causal],
-                           window, sinks, seqlens_k, d ** -0.5 if scale is None else scale, code,
-                           ws, ws_bytes, _current(stream, q))
+        rc = load_library().fa_bwd_window(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), delta.data_ptr(), *dims,
+            CAUSAL_MODES[causal], window, sinks, _addr(seqlens_k),
+            d ** -0.5 if scale is None else float(scale), code, ws, ws_bytes, _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_window")
     return dq, dk, dv
@@ -1053,7 +1056,7 @@ def make_decode_workspace(q, k):
         return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
 
 
-def _decode(fn, where, q, k, v, tree, window, sinks, seqlens_k, scale, out, lse, workspace, stream,
+def _decode(where, q, k, v, tree, window, sinks, seqlens_k, scale, out, lse, workspace, stream,
             dims, code):
     import torch
     B, H, _, Nq, _, d = dims
@@ -1069,8 +1072,10 @@ def _decode(fn, where, q, k, v, tree, window, sinks, seqlens_k, scale, out, lse,
         if workspace is None:
             workspace = make_decode_workspace(q, k)
         ws, ws_bytes = _workspace_arg(workspace, q.device)
-        rc = fn(q, k, v, out, lse, *dims, *tree, _int32(window), _int32(sinks), seqlens_k,
-                d ** -0.5 if scale is None else scale, code, ws, ws_bytes, _current(stream, q))
+        rc = getattr(load_library(), where)(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *dims, *tree,
+            _int32(window), _int32(sinks), _addr(seqlens_k),
+            d ** -0.5 if scale is None else float(scale), code, ws, ws_bytes, _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, where)
     return out, lse
@@ -1086,7 +1091,7 @@ def attention_decode_window(q, k, v, window, sinks=0, seqlens_k=None, scale=None
     None allocates one.
     """
     dims, code = _window_args(q, k, v, window, sinks, seqlens_k, "attention_decode_window")
-    return _decode(fa_decode_window, "fa_decode_window", q, k, v, (), window, sinks, seqlens_k,
+    return _decode("fa_decode_window", q, k, v, (), window, sinks, seqlens_k,
                    scale, out, lse, workspace, stream, dims, code)
 
 
@@ -1110,7 +1115,7 @@ def attention_decode_tree(q, k, v, tree, seqlens_k=None, window=None, sinks=0, s
             or tree.device != q.device or not tree.is_contiguous():
         raise ValueError("attention_decode_tree: tree must be a contiguous int64 tensor [B, Nq] "
                          "on q's device")
-    return _decode(fa_decode_tree, "fa_decode_tree", q, k, v, (tree,),
+    return _decode("fa_decode_tree", q, k, v, (tree.data_ptr(),),
                    0 if window is None else window, sinks, seqlens_k, scale, out, lse, workspace,
                    stream, dims, code)
 
@@ -1137,7 +1142,8 @@ def tree_rows(parents):
 
 def _int32(x):
     """A count clamped to int32 (larger windows and sinks hide nothing more)."""
-    return min(int(x), 2**31 - 1)
+    x = int(x)
+    return x if x < 2**31 else 2**31 - 1
 
 
 _NOTHING = contextlib.nullcontext()
@@ -1163,8 +1169,12 @@ def _on(stream, device):
 
 
 def _current(stream, q):
+    """Address of the given stream, or of the current one of q's device (read
+    without building a Stream object, which takes as long as a launch)."""
+    if stream is not None:
+        return _stream(stream)
     import torch
-    return torch.cuda.current_stream(q.device) if stream is None else stream
+    return torch._C._cuda_getCurrentRawStream(q.get_device())
 
 
 # ---------------------------------------------------------------- autograd

@@ -57,7 +57,20 @@
 // with j > p - win or j < sinks; H query heads share Hk key/value heads)
 // walk only the tile pairs that hold a visible (query, key): a dQ item the
 // sink tiles and the tiles of its rows' windows, a dK/dV item the query
-// tiles of every head of its group that see the key tile.
+// tiles of every head of its group that see the key tile.  Sixteen warps do
+// the element-wise work there (four column groups of 32; 8 warps measured 353
+// us where 16 take 339, B4 H16/4 N4096 d64 window 1024, and the same at
+// d = 128), and the whole MMA warp walks the steps with one elected lane
+// issuing, so that descriptors and conditions stay in uniform registers: with
+// lane 0 walking alone the issue of a step's 16 to 32 products outlasted
+// them (400 us; d = 128, B1 H32/8 N16384 window 2048 64 sinks: 1520, now 1400,
+// 947 TFLOP/s of the visible pairs).  What bounds it: at d = 128 the chain S,
+// dP, element-wise work of a tile beside 3 or 4 products of about 550 cycles
+// (2400 and 2670 cycles a step), at d = 64 the element-wise work (about 2000
+// of 2300 cycles).  Measured and not kept: an issuing warp for each of S and
+// dP (1466, 346: dV and dQ get ahead of the S that the warps wait for), LSE
+// and D staged through a barrier in shared memory (1419, 363), the two halves
+// of a tile on barriers of their own (d = 64: 389).
 #pragma once
 
 #include <cuda.h>
@@ -68,6 +81,7 @@
 
 namespace fa {
 
+// (of the variants without a window; see BwdRoles for theirs)
 constexpr int kBwdThreads = 320;
 constexpr int kBwdEwThreads = 256;       // element-wise warps 0-7
 constexpr int kBwdMmaWarp = 8;
@@ -578,8 +592,8 @@ __global__ void __launch_bounds__(256) fa_bwd_win_parts_kernel(const __grid_cons
 }
 
 // Shared setup of one work item of the tensor-core grid: the ring barriers
-// and, through `init_x(bar)`, the item's own barriers, initialised by the
-// load thread.  The CTA's TMEM is allocated once for all its items.
+// and, through `init_x(bar)`, the item's own barriers, initialised by one
+// thread (the load thread without a window).  The CTA's TMEM is allocated once for all its items.
 template <class L, class InitX>
 __device__ __forceinline__ void bwd_setup(uint32_t sbase, uint8_t* sgen, InitX init_x) {
   if (threadIdx.x == kBwdLoadWarp * 32) {
@@ -604,7 +618,7 @@ __device__ __forceinline__ void bwd_setup(uint32_t sbase, uint8_t* sgen, InitX i
 }
 
 // End of one work item: every role is done (the MMA thread has seen its
-// last commit, the load thread its last copy), so the load thread
+// last commit, the load thread its last copy), so the thread that set them up
 // invalidates the item's barriers; the next item, whose layout may put
 // other data there, initialises its own.
 template <class L>
@@ -1100,6 +1114,8 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
         }
       }
       {
+        // P and dS are rounded to the storage dtype, the tensor core's operand
+        // type; what they sum up to (dV, dK, dQ) is fp32
         uint32_t pk[W::kCols / 2];
 #pragma unroll
         for (int e = 0; e < W::kCols / 2; ++e) {

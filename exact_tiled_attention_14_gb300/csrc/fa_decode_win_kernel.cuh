@@ -34,13 +34,22 @@
 // each group owns a row tile and both take every key tile.
 //
 // Copies.  A thread works on the lane its warp owns, and one row's 128 scores
-// of a tile take a thread about 2000 cycles from S to P, which two groups
-// cannot hide behind the loads at d = 64 (0.9 us a tile of 32 KB against 0.73
-// at the HBM rate, with 1 row or 128).  So with few rows the query tile holds
-// kCopies copies of them (4 up to 32 rows, 2 up to 64), S comes out once per
-// copy, and copy g weighs only keys g * 128 / kCopies ...: its rows of P are
-// zero elsewhere, and its O is the part of those keys.  The copies are parts
-// like the groups' and are merged with them.
+// of a tile take a thread about 2000 cycles from S to P: latency at the start
+// and end of each unit.  So with few rows the query tile holds kCopies copies
+// of them (4 up to 32 rows, 2 up to 64), S comes out once per copy, and copy
+// g weighs only keys g * 128 / kCopies ...: its rows of P are zero elsewhere,
+// and its O is the part of those keys.  The copies are parts like the groups'
+// and are merged with them.  Measured with 4 rows against one copy: one tile
+// 7.2 and 7.9 us, 16 caches of 2005 keys (256 units, d = 64) 37.8 and 44.6;
+// in a long unit a tile takes 0.73 us instead of 0.68, so that units of more
+// than about 40 tiles would gain a little from one copy.
+//
+// Measured (key tiles of one unit a CTA, 152 CTAs, inputs larger than L2):
+// d = 128 1.34 us a tile of 64 KB, 7.4 TB/s with what L2 keeps, up to 128
+// rows, and 1.68 at 256 rows; d = 64 0.73 us a tile of 32 KB (6.8 TB/s), and
+// 1.16 at 256 rows.  A unit costs about 2 us more than its tiles and a call
+// about 7 us.  Up to 128 rows the loads bound the time; at 256 rows the
+// softmax of two row tiles a key tile does, with the two products' chain.
 #pragma once
 
 #include <cuda.h>
@@ -240,9 +249,9 @@ __device__ __forceinline__ bool dec_next(const DecWinParams& p, DecCursor& c, De
 // the S it was formed from, and the group's next S waits for the product that
 // reads P (the loads bound these calls, not that chain); with two row tiles
 // P goes to shared memory, which costs two ring stages but lets the next S
-// be formed during the softmax (measured for 256 rows: 2.07 us a tile with P
-// over S, the chain of softmax and both products, against the figure in
-// the header of fa_decode_win_kernel).
+// be formed during the softmax (measured for 256 rows: 1.80 us a tile against
+// 2.07 with P over S, the chain of softmax and both products; 1.68 since the
+// issuing warps keep their descriptors in uniform registers).
 //
 // Shared memory: query tiles (two buffers, so a unit's queries load while the
 // previous unit runs; one at d = 128 with two row tiles, where there is no
@@ -567,7 +576,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     } else if (warp == kDwSWarp) {
       // ============================================================ S = Q K^T
       // The whole warp walks the tiles and one elected lane issues: conditions,
-      // descriptors and addresses then stay in uniform registers.
+      // descriptors and addresses then stay in uniform registers (64 rows of
+      // 8 caches of 131k keys, d = 128: 772 us, 836 with lane 0 walking alone).
       {
         const uint32_t tmem = ptx::warp_same(tmem_base);
         constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, kDwTile, kBf16 ? 1 : 0, 0);
