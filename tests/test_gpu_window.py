@@ -271,3 +271,38 @@ def test_given_buffers_are_filled_and_nothing_else():
         fa.attention_forward_window(q, k, v, 50, 1, lse=biglse[1].half())
     with pytest.raises(ValueError):
         fa.attention_forward_window(q.transpose(1, 2), k, v, 50, 1)
+
+
+@pytest.mark.parametrize("causal,lens", [("bottom_right", [1000, 100, 0]), ("upper_left", [1000, 128, 3])])
+def test_parts_of_sink_tiles_without_steps(causal, lens):
+    """Sink tiles cut into parts, of which a short batch fills few or none."""
+    B, H, Hk, N, d, win, sinks = 3, 4, 2, 1000, 64, 100, 200
+    assert fa.fa_bwd_window_workspace_size(B, H, Hk, N, N, d, win, sinks) > 0
+    q, k, v, do = inputs(B, H, Hk, N, N, d, "bf16", seed=23)
+    got = run(q, k, v, do, win, sinks, causal, lens)
+    val, tol = wc.reference(q, k, v, masks(B, N, N, lens, causal, win, sinks), wc.scale_of(d),
+                            "bf16", do)
+    wc.check(got, val, tol, f"{causal} {lens}")
+
+
+def test_rows_past_two_to_the_31_elements():
+    """Q, O, dO and dQ of more than 2^31 elements: the last rows of the last
+    head, and the last keys, against the definition of the last 300 tokens."""
+    B, H, Hk, N, d, win, m = 1, 2, 1, 2**24 + 300, 64, 40, 300
+    gen = torch.Generator(device="cuda").manual_seed(29)
+    q, do = (torch.randn(B, H, N, d, dtype=torch.bfloat16, device="cuda", generator=gen)
+             for _ in range(2))
+    k, v = (torch.randn(B, Hk, N, d, dtype=torch.bfloat16, device="cuda", generator=gen)
+            for _ in range(2))
+    o, lse = fa.attention_forward_window(q, k, v, win, causal="upper_left")
+    dq, dk, dv = fa.attention_backward_window(q, k, v, o, lse, do, win, causal="upper_left")
+    status_ok()
+    last = [t[:, :, -m:].contiguous() for t in (q, k, v, do, o, lse, dq, dk, dv)]
+    del q, k, v, do, o, lse, dq, dk, dv
+    torch.cuda.empty_cache()
+    val, tol = wc.reference(*(t.cpu() for t in last[:3]), masks(B, m, m, None, "upper_left", win, 0),
+                            wc.scale_of(d), "bf16", last[3].cpu())
+    # the first `win` rows and keys of the cut lack what lies before it
+    cut = lambda t: t[:, :, win:]
+    got = dict(zip(("o", "lse", "dq", "dk", "dv"), map(cut, last[4:])))
+    wc.check(got, {n: cut(x) for n, x in val.items()}, {n: cut(x) for n, x in tol.items()}, "last rows")
