@@ -50,8 +50,9 @@ cudaError_t launch_variant(const DecWinParams& p, cudaStream_t stream) {
   // Programmatic dependent launch: the combine grid is set up while the main
   // kernel runs its last CTAs, and waits on the device for the parts.
   cudaLaunchConfig_t cfg = {};
-  const int rows = kDwCombineThreads / (D / 4);   // rows a block
-  cfg.gridDim = dim3(p.grid, (p.slot_rows + rows - 1) / rows);
+  const int rows = 1 << p.combine_rows;
+  const int groups = std::max(D / 4 * rows / kDwCombineThreads, 1);
+  cfg.gridDim = dim3(p.grid, (p.slot_rows + rows - 1) / rows * groups);
   cfg.blockDim = dim3(kDwCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -59,7 +60,13 @@ cudaError_t launch_variant(const DecWinParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_decode_win_combine_kernel<D, kBf16>, p);
+  // Where units are cut into two or three parts, a thread with registers for
+  // three lets more of them run at a time (44 against 72 registers; 128 rows
+  // of 16 caches, 128 units: the call 72.5 us, 77.5 with eight); many parts
+  // are loaded eight at a time, one wait for each eight.
+  const bool few = p.grid <= 2ll * p.B * p.Hk * p.row_blocks;
+  return few ? cudaLaunchKernelEx(&cfg, fa_decode_win_combine_kernel<D, kBf16, 3>, p)
+             : cudaLaunchKernelEx(&cfg, fa_decode_win_combine_kernel<D, kBf16, 8>, p);
 }
 
 constexpr long long kMaxCount = 1ll << 30;
@@ -146,7 +153,7 @@ int decode(const void* q, const void* k, const void* v, void* o, float* lse, int
     return FA_ERR_TENSORMAP;
   p.o = o;
   p.lse = lse;
-  p.part_o = static_cast<float*>(workspace);
+  p.part_o = static_cast<float4*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + pl.o_bytes);
   p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + pl.o_bytes + pl.ml_bytes);
   p.status = info->status;
@@ -163,6 +170,7 @@ int decode(const void* q, const void* k, const void* v, void* o, float* lse, int
   p.row_span = pl.row_span;
   p.row_blocks = pl.row_blocks;
   p.slot_rows = pl.slot_rows;
+  while (p.combine_rows < 5 && (1 << p.combine_rows) < pl.slot_rows) ++p.combine_rows;
   p.grid = pl.grid;
   // a window past every position hides nothing, as none (0, tree) does
   const int all = Nk + Nq + 1;

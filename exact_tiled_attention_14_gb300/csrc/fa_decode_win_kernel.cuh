@@ -71,7 +71,6 @@ constexpr int kDwSWarp = 8, kDwLoadWarp = 9, kDwPvWarp = 10;
 constexpr uint32_t kDwSoftmaxRegs = 208, kDwIssueRegs = 88;
 static_assert(2 * 128 * kDwSoftmaxRegs + 128 * kDwIssueRegs <= 168 * kDwThreads, "register split");
 constexpr float kDwTau = 8.0f;        // lazy-rescale threshold, log2 units
-constexpr int kDwCombine = 8;         // parts of a row that are loaded together
 constexpr int kDwMaxTree = 64;        // drafted tokens (bits of a row's mask)
 constexpr int kDwMaxTokens = 16;      // new tokens of a window call
 
@@ -88,7 +87,8 @@ struct DecWinParams {
   CUtensorMap tm_v16;
   void* o;                 // [B * Hk, R, d]
   float* lse;              // [B * Hk, R]
-  float* part_o;           // [2 * grid, slot_rows, d] unnormalised parts
+  float4* part_o;          // [2 * grid, d / 4, slot_rows] unnormalised parts, 4 columns each
+                           // ([2 * grid, slot_rows, d / 4] where rows have copies)
   float2* part_ml;         // [2 * grid, slot_rows] (-m in log2 units, l)
   int4* cut;               // [grid] the cut unit that starts in the run: (head, row block,
                            // slot of its first part, run of its last part), run -1: none
@@ -102,6 +102,7 @@ struct DecWinParams {
   int row_span;            // rows of a unit: 128 * kTiles
   int row_blocks;          // units per head: ceil(R / row_span)
   int slot_rows;
+  int combine_rows;        // log2 of a combine block's rows
   int grid;
   int win;                 // >= 1; larger than every position: no window
   int sinks;
@@ -241,6 +242,15 @@ __device__ __forceinline__ bool dec_next(const DecWinParams& p, DecCursor& c, De
     ++c.b;
   }
   return true;
+}
+
+// Columns 4 c .. 4 c + 3 of row r of a part: next to each other for the rows of
+// a warp that holds a row a lane, which so writes 512 bytes at a time, and
+// row by row where neighbouring threads hold a row's columns (copies).
+template <int D>
+__device__ __forceinline__ float4* dec_part(const DecWinParams& p, size_t slot, int r, int c) {
+  const bool by_row = p.slot_rows <= kDwTile / 2;
+  return p.part_o + slot * (D / 4) * p.slot_rows + (by_row ? r * (D / 4) + c : c * p.slot_rows + r);
 }
 
 // Where P is.  S of the two groups fills TMEM columns 0-255, their O the
@@ -1001,10 +1011,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                                         ptx::pack2<kBf16>(x[8 * v + 4], x[8 * v + 5]),
                                         ptx::pack2<kBf16>(x[8 * v + 6], x[8 * v + 7]));
                 } else {
-                  float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * p.slot_rows + r) * D + col);
 #pragma unroll
                   for (int v = 0; v < 4; ++v)
-                    dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+                    *dec_part<D>(p, slot, r, col / 4 + v) =
+                        make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
                 }
               }
             }
@@ -1049,7 +1059,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                                                       (head * p.R + rr) * D + col);
                 *dst = make_uint2(ptx::pack2<kBf16>(sum.x, sum.y), ptx::pack2<kBf16>(sum.z, sum.w));
               } else {
-                *reinterpret_cast<float4*>(p.part_o + (slot * p.slot_rows + rr) * D + col) = sum;
+                *dec_part<D>(p, slot, rr, col / 4) = sum;
               }
             }
           }
@@ -1081,11 +1091,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                                       ptx::pack2<kBf16>(x[8 * v + 4] * inv, x[8 * v + 5] * inv),
                                       ptx::pack2<kBf16>(x[8 * v + 6] * inv, x[8 * v + 7] * inv));
               } else {
-                float4* dst = reinterpret_cast<float4*>(
-                    p.part_o + (slot * p.slot_rows + w * kDwTile + r) * D + col);
 #pragma unroll
                 for (int v = 0; v < 8; ++v)
-                  dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+                  *dec_part<D>(p, slot, w * kDwTile + r, col / 4 + v) =
+                      make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
               }
             }
           }
@@ -1113,53 +1122,56 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 
 // The cut units: block (run, y) adds up the parts of rows of the unit that
 // starts in that run and ends in a later one (most runs have one, the run
-// table says which), D / 4 threads a row with 4 columns each: every part is
-// scaled to the largest maximum, added in the order of the runs, and the sum
-// divided once.  A row without a visible key has no live part: O = 0 and
-// LSE = -inf.
+// table says which), 4 columns a thread: every part is scaled to the largest
+// maximum, added in the order of the runs, and the sum divided once.  A row
+// without a visible key has no live part: O = 0 and LSE = -inf.  A block takes
+// 2^combine_rows rows (up to 32) and as many columns as its threads reach;
+// four neighbours share a row, so that a warp reads 128 bytes of each of four
+// columns' parts and writes 32 of each row.  kBatch parts are loaded together.
 constexpr int kDwCombineThreads = 128;
-template <int D, bool kBf16>
+template <int D, bool kBf16, int kBatch>
 __global__ void __launch_bounds__(kDwCombineThreads)
     fa_decode_win_combine_kernel(const __grid_constant__ DecWinParams p) {
   constexpr int kPer = D / 4;
+  const int lr = p.combine_rows, pieces = kDwCombineThreads >> lr;
+  const int groups = max(kPer / pieces, 1);      // blocks that share rows
+  const int srow = ((threadIdx.x >> 2) & ((1 << lr) - 1)) + (blockIdx.y / groups << lr);
+  const int c = (threadIdx.x & 3) + (threadIdx.x >> (2 + lr)) * 4 + blockIdx.y % groups * pieces;
   ptx::griddep_wait();   // the parts are complete, and this grid ends after the main one
   const int run0 = blockIdx.x;
   const int4 cut = p.cut[run0];
   if (cut.w < 0) return;
-  const int srow = blockIdx.y * (kDwCombineThreads / kPer) + threadIdx.x / kPer;
-  const int row = cut.y * p.row_span + srow, c = threadIdx.x % kPer;
-  if (srow >= p.slot_rows || row >= p.R) return;
+  const int row = cut.y * p.row_span + srow;
+  if (srow >= p.slot_rows || row >= p.R || c >= kPer) return;
   // the unit's first part is the last piece of its run, the others are the
   // first of theirs
-  auto part_of = [&](int run) {
-    return static_cast<size_t>(run == run0 ? cut.z : 2 * run) * p.slot_rows + srow;
-  };
+  auto slot_of = [&](int run) { return static_cast<size_t>(run == run0 ? cut.z : 2 * run); };
   float nm = INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int run = run0; run <= cut.w; run += kDwCombine) {
+  for (int run = run0; run <= cut.w; run += kBatch) {
     // a batch of parts, their loads in flight together
-    float2 ml[kDwCombine];
-    float4 x[kDwCombine];
+    float2 ml[kBatch];
+    float4 x[kBatch];
 #pragma unroll
-    for (int i = 0; i < kDwCombine; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       if (run + i <= cut.w) {
-        const size_t part = part_of(run + i);
-        ml[i] = p.part_ml[part];
-        x[i] = reinterpret_cast<const float4*>(p.part_o + part * D)[c];
+        const size_t slot = slot_of(run + i);
+        ml[i] = p.part_ml[slot * p.slot_rows + srow];
+        x[i] = *dec_part<D>(p, slot, srow, c);
       } else {
         ml[i] = make_float2(0.f, 0.f);
       }
     }
     float m = nm;
 #pragma unroll
-    for (int i = 0; i < kDwCombine; ++i)
+    for (int i = 0; i < kBatch; ++i)
       if (ml[i].y > 0.f) m = fminf(m, ml[i].x);
     const float fo = nm == INFINITY ? 0.f : ptx::ex2(m - nm);
     acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
     l *= fo;
     nm = m;
 #pragma unroll
-    for (int i = 0; i < kDwCombine; ++i)
+    for (int i = 0; i < kBatch; ++i)
       if (ml[i].y > 0.f) {
         const float f = ptx::ex2(m - ml[i].x);
         acc.x = fmaf(f, x[i].x, acc.x);
