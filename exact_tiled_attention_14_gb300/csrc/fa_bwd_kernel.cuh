@@ -88,6 +88,7 @@ constexpr int kBwdMmaWarp = 8;
 constexpr int kBwdLoadWarp = 9;
 constexpr int kBwdTile = 128;            // rows of a query or key tile = TMEM lanes
 constexpr uint32_t kBwdTmemCols = 512;
+constexpr int kBwdNarrow = 32;           // keys of a sink tile worked on at that width
 
 // Roles of the tensor-core kernel.  kGroups element-wise warps share a TMEM
 // lane quarter, each on kCols of a tile's 128 columns.
@@ -446,11 +447,13 @@ __device__ __forceinline__ void issue_kmajor(uint32_t d_tmem, uint32_t a_lo, uin
 // rows along K, D columns) into d_tmem (N = D).  A's 64 packed columns sit
 // in kBlocks equal blocks, 128 / kBlocks columns apart (more than one: a
 // 16-bit tile written over the fp32 columns that each group of warps read).
+// `narrow`: the first kBwdNarrow along K only.
 template <int kBlocks>
 __device__ __forceinline__ void issue_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                             uint32_t idesc, uint32_t acc) {
+                                             uint32_t idesc, uint32_t acc, bool narrow = false) {
 #pragma unroll
   for (int kk = 0; kk < kBwdTile / 16; ++kk) {
+    if (kk == kBwdNarrow / 16 && narrow) break;
     constexpr int kPer = 8 / kBlocks;   // K steps of a block
     const uint32_t acol = kk / kPer * (kBwdTile / kBlocks) + kk % kPer * 8;
     ptx::mma_ts(d_tmem, a_tmem + acol, ptx::desc_sw128(b_lo + kk * (2048 >> 4)), idesc,
@@ -1269,6 +1272,10 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
                       p.sinks);
     nk = wk.count;
   }
+  // kWin: of the first tile's keys any row sees only the sinks, in the first
+  // column group; the products take that many keys, the other groups nothing
+  const bool narrow0 = kWin && wk.ns == 1 && p.sinks <= kBwdNarrow && wk.lo >= kBwdTile;
+  static_assert(!kWin || W::kCols == kBwdNarrow, "the first column group");
   auto k_tile = [&](int j) { return kWin && j >= wk.ns ? wk.wa + (j - wk.ns) : j; };
   const int q_rows = tok ? hd.lenq : p.N;
   if (kKv && nk <= 0) {
@@ -1315,6 +1322,7 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
     if (kWin || lane == 0) {
       const uint32_t tmem = bwd_uniform<kWin>(tmem_base);
       const int n = bwd_uniform<kWin>(nk);
+      const bool narrow = kWin && ptx::warp_all(narrow0);
       constexpr int fmt = kBf16 ? 1 : 0;
       constexpr uint32_t idesc_s = ptx::idesc_f16(kBwdTile, kBwdTile, fmt, 0);
       const uint32_t idesc_dq = ptx::idesc_f16(kBwdTile, kWin ? D : p.width_qk, fmt, 1);   // dQ: width_qk columns
@@ -1337,7 +1345,7 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         const int slot = j % L::kStagesA;
         if (!bwd_elected<kWin>()) return true;
         issue_tmem_a<1>(tDq, tmem + dq_ds_col<D>(j & 1), k_mn0 + slot * kSlotLo, idesc_dq,
-                            j > 0 ? 1u : 0u);
+                        j > 0 ? 1u : 0u, kWin && narrow && j == 0);
         ptx::mma_commit(bar(L::bEmptyA + slot));
         ptx::mma_commit(xbar(X::kDsFree + (j & 1)));
         return true;
@@ -1354,8 +1362,10 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         if (!alive) break;
         // S = Q_i K_j^T and dP = dO_i V_j^T (queries on the TMEM lanes)
         if (bwd_elected<kWin>()) {
-          issue_kmajor<D, L::kChunkBytes>(tS, q_lo, k_lo0 + sa * kSlotLo, idesc_s, steps_s);
-          issue_kmajor<D, L::kChunkBytes>(tDp, do_lo, v_lo0 + sb * kSlotLo, idesc_s, steps_dp);
+          constexpr uint32_t idesc_narrow = ptx::idesc_f16(kBwdTile, kBwdNarrow, fmt, 0);
+          const uint32_t idesc = kWin && narrow && it == 0 ? idesc_narrow : idesc_s;
+          issue_kmajor<D, L::kChunkBytes>(tS, q_lo, k_lo0 + sa * kSlotLo, idesc, steps_s);
+          issue_kmajor<D, L::kChunkBytes>(tDp, do_lo, v_lo0 + sb * kSlotLo, idesc, steps_dp);
           ptx::mma_commit(xbar(X::kSFull));
           ptx::mma_commit(bar(L::bEmptyB + sb));   // V_j is not read again
         }
@@ -1399,14 +1409,20 @@ __device__ __forceinline__ void bwd_dq_cta(const BwdParams& p, int blk, uint32_t
         // Keys of this tile that no row sees get dS = 0; their rows of K are
         // cleared so that the product with them is 0 whatever they hold (S
         // and dP have read the tile).
-        const int r_hi = min(max(wk.hi - key0, 0), kBwdTile);
+        const int rows_k = narrow0 && j == 0 ? kBwdNarrow : kBwdTile;   // rows that are read
+        const int r_hi = min(max(wk.hi - key0, 0), rows_k);
         const int r_lo = min(max(wk.lo - key0, 0), r_hi);
         const int r_sink = min(max(p.sinks - key0, 0), r_lo);
-        if (r_sink < r_lo || r_hi < kBwdTile) {
+        if (r_sink < r_lo || r_hi < rows_k) {
           uint8_t* kt = sgen + L::kRingA + (j % L::kStagesA) * L::kTile;
           zero_rows(kt, L::kChunks, r_sink, r_lo, threadIdx.x, W::kEwThreads);
-          zero_rows(kt, L::kChunks, r_hi, kBwdTile, threadIdx.x, W::kEwThreads);
+          zero_rows(kt, L::kChunks, r_hi, rows_k, threadIdx.x, W::kEwThreads);
           ptx::fence_proxy_async_smem();
+        }
+        if (narrow0 && j == 0 && group > 0) {
+          ptx::mbar_arrive(xbar(X::kSFree));
+          ptx::mbar_arrive(xbar(X::kPFull));   // of buffer 0
+          continue;
         }
       } else if constexpr (kKv) {
         // keys past this head's count, and with causal masking keys after

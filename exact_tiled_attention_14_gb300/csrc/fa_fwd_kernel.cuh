@@ -49,10 +49,11 @@
 // (win_active), so a unit of 256 rows costs about (win + 128) / 128 + the
 // sink tiles per query tile whatever the length.  H query heads may share
 // Hk key/value heads.  Measured (bf16; TFLOP/s of the visible pairs): B1 H32/8
-// N32768 d128 window 4096 16 sinks 1375 us (1505), bound by the tensor core
+// N32768 d128 window 4096 16 sinks 1365 us (1515), bound by the tensor core
 // and, in tiles cut by a window's ends, by products with masked pairs (33.1
 // tiles for 32 tiles' worth of pairs, and one of sinks); B4 H16/4 N4096 d64
-// window 1024 4 sinks 87 us (692), bound by the softmax, 10 tiles for 7.6.
+// window 1024 4 sinks 85 us (705), bound by the softmax, 9 tiles and a narrow
+// one for 7.6.
 #pragma once
 
 #include <cuda.h>
@@ -168,6 +169,11 @@ struct FwdParams {
   int win;
   int sinks;
   int Hk;
+  // Order of a unit's tiles (see Unit): the first window's tile before the
+  // sinks at d = 128 (B1 H32/8 N16384 window 2048, 64 sinks: 383 us against 404
+  // with the sinks first), after them at d = 64 (B4 H16/4 N4096 window 1024, 33
+  // sinks: 90 us against 95 with them second).
+  int gap_first;
 };
 
 // ---------------------------------------------------------------- tracing
@@ -313,11 +319,14 @@ struct Unit {
   int bh, mblk, n0, n1;
   int len, off;   // keys of this head; position of query row r is r + off (kKv)
   int lenq, q0, k0;   // queries of this head; first query and key token (varlen)
-  // kWin: the list of key tiles the unit streams is the sink tiles 0 .. ns - 1,
-  // then wa, wa + 1, ... (nl tiles in all).  Query tile 0 computes the first
-  // n0 of them, query tile 1 (when n1 > 0) all but the one at position gap
-  // (-1: all): its window may start a tile later.  Of the keys in them some
-  // row of the unit sees those below min(sinks, hi) and lo .. hi - 1.
+  // kWin: the unit streams a list of nl key tiles, the sink tiles 0 .. ns - 1
+  // and wa, wa + 1, ...  Query tile 0 computes the first n0 of the list, query
+  // tile 1 (when n1 > 0) all but the one at position gap (-1: all), since
+  // its window may start a tile later.  With gap_first that tile, wa, comes
+  // first then, and the sinks after it, so that query tile 1 starts a tile
+  // after query tile 0 as it ends one after it; otherwise the sinks come first.
+  // Of the keys in the list some row of the unit sees those below
+  // min(sinks, hi) and lo .. hi - 1.
   int ns, wa, nl, gap, lo, hi;
 };
 
@@ -332,8 +341,11 @@ struct Piece {
 
 // Key tile at position j of a piece's list (kWin), whether query tile w
 // computes it, and the list position of query tile w's j-th tile.
-__host__ __device__ __forceinline__ int win_tile(const Piece& u, int j) {
-  return j < u.ns ? j : u.wa + (j - u.ns);
+// gap_first as in FwdParams.
+__host__ __device__ __forceinline__ int win_tile(const Piece& u, int j, bool gap_first) {
+  const int i = gap_first && u.gap == 0 ? j - 1 : j;   // from the first sink tile on
+  if (gap_first && i < 0) return u.wa;
+  return i < u.ns ? i : u.wa + (j - u.ns);
 }
 __host__ __device__ __forceinline__ bool win_active(const Piece& u, int w, int j) {
   return w ? u.n1 > 0 && j != u.gap : j < u.n0;
@@ -344,16 +356,30 @@ __host__ __device__ __forceinline__ int win_pos(const Piece& u, int w, int j) {
 // Whether the tile at list position j holds keys that no row of the unit
 // sees: only the last sink tile, the first tile of the windows and the last
 // tile can.
-__host__ __device__ __forceinline__ bool win_cut(const Piece& u, int j, int sinks) {
-  const int key0 = win_tile(u, j) * kBN;
+__host__ __device__ __forceinline__ bool win_cut(const Piece& u, int j, int sinks, bool gap_first) {
+  const int key0 = win_tile(u, j, gap_first) * kBN;
   return key0 + kBN > u.hi || imax(key0, sinks) < imin(u.lo, key0 + kBN);
 }
 // First list position >= from of a tile with such keys, nl if there is none.
-__host__ __device__ __forceinline__ int win_next_cut(const Piece& u, int from, int sinks) {
-  if (from < u.ns && win_cut(u, u.ns - 1, sinks)) return u.ns - 1;
-  if (from <= u.ns && u.ns < u.nl && win_cut(u, u.ns, sinks)) return u.ns;
-  if (from < u.nl && win_cut(u, u.nl - 1, sinks)) return u.nl - 1;
+__host__ __device__ __forceinline__ int win_next_cut(const Piece& u, int from, int sinks,
+                                                            bool gap_first) {
+  const bool second = gap_first && u.gap == 0;   // the sinks come after the first window tile
+  const int sink = second ? u.ns : u.ns - 1, first = second ? 0 : u.ns;
+  const int p0 = imin(sink, first), p1 = imax(sink, first);
+  if (from <= p0 && win_cut(u, p0, sinks, gap_first)) return p0;
+  if (from <= p1 && p1 < u.nl && win_cut(u, p1, sinks, gap_first)) return p1;
+  if (from < u.nl && win_cut(u, u.nl - 1, sinks, gap_first)) return u.nl - 1;
   return u.nl;
+}
+// List position of the only sink tile if, of its keys that any row sees, there
+// are only sinks, in its first kNarrow keys; -1 otherwise.  Such a tile is
+// worked on at that width: products with kNarrow keys, and a fourth of the
+// exponentials (16 sinks instead of 64 at d = 128, sizes as at gap_first: 370
+// us against 383; 4 instead of 33 at d = 64: 84 against 90).
+constexpr int kNarrow = 32;
+__host__ __device__ __forceinline__ int win_narrow(const Piece& u, int sinks, bool gap_first) {
+  if (u.ns != 1 || sinks > kNarrow || u.lo < kBN) return -1;
+  return gap_first && u.gap == 0 ? 1 : 0;
 }
 // Marks what the MMA warps' loops read of a piece as the same in every lane.
 __device__ __forceinline__ void win_same(Piece& u) {
@@ -363,6 +389,7 @@ __device__ __forceinline__ void win_same(Piece& u) {
   u.wa = ptx::warp_same(u.wa);
   u.nl = ptx::warp_same(u.nl);
   u.gap = ptx::warp_same(u.gap);
+  u.lo = ptx::warp_same(u.lo);
 }
 // Key/value head of query head bh (kWin: Hk heads shared by groups).
 __host__ __device__ __forceinline__ int kv_head(const FwdParams& p, int bh) {
@@ -453,7 +480,7 @@ __host__ __device__ __forceinline__ Unit decode_unit(int s, const FwdParams& p) 
       u.ns = imin(n_sink, end);
       u.wa = imax(e[0] == 0 ? a[1] : (e[1] == 0 ? a[0] : imin(a[0], a[1])), n_sink);
       u.nl = u.ns + imax(0, end - u.wa);
-      u.gap = e[1] > 0 && imax(a[1], n_sink) > u.wa ? u.ns : -1;
+      u.gap = e[1] > 0 && imax(a[1], n_sink) > u.wa ? (p.gap_first ? 0 : u.ns) : -1;
       u.lo = imax(t0 * kBM + u.off - p.win + 1, 0);
       u.hi = imin(len, imax(imin((t0 + 2) * kBM, lenq) + u.off, 0));
     }
@@ -594,6 +621,7 @@ template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool k
 __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using L = Smem<D, kDrop, kWin>;
+  constexpr bool kGapFirst = D == 128;         // kWin: as in the parameters
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;
@@ -756,7 +784,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             ptx::mbar_arrive_expect_tx(full, nc * L::kChunkBytes);
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
-            if constexpr (kWin) { y = win_tile(u, j) * kBN; z = kvh; }
+            if constexpr (kWin) { y = win_tile(u, j, kGapFirst) * kBN; z = kvh; }
             if (kKv && !kWin && p.varlen) { z = u.k0 + y; y = u.bh % p.H; }   // head, token
             for (int c = 0; c < nc; ++c)
               ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm, full,
@@ -824,12 +852,14 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       // a K step of 16 columns moves 32 bytes inside a swizzle row, and every
       // 64 columns start a new chunk.
       const int s_steps = kKv && !kWin ? p.dqk / 16 : D / 16;   // K steps of S (columns of Q, K / 16)
-      auto issue_s = [&](uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo) {
+      auto issue_s = [&](uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo, bool narrow) {
+        constexpr uint32_t idesc_narrow = ptx::idesc_f16(kBM, kNarrow, fmt, 0);
+        const uint32_t idesc = kWin && narrow ? idesc_narrow : idesc_s;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if (kKv && !kWin && kk >= s_steps) break;
           const uint32_t off = static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-          ptx::mma_ss(d_tmem, ptx::desc_sw128(q_lo + off), ptx::desc_sw128(k_lo + off), idesc_s,
+          ptx::mma_ss(d_tmem, ptx::desc_sw128(q_lo + off), ptx::desc_sw128(k_lo + off), idesc,
                       kk > 0);
         }
       };
@@ -839,9 +869,11 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       // P in shared memory: the A operand is a K-major tile laid out like Q
       // (128 keys along K in two 64-column chunks), so its K steps advance as
       // in issue_s.
-      auto issue_pv = [&](uint32_t o_tmem, uint32_t p_addr, uint32_t v_lo, uint32_t acc) {
+      auto issue_pv = [&](uint32_t o_tmem, uint32_t p_addr, uint32_t v_lo, uint32_t acc,
+                          bool narrow) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk) {
+          if (kWin && kk == kNarrow / 16 && narrow) break;
           if constexpr (OwnP<D>::kSmem) {
             const uint32_t off = static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
             ptx::mma_ss(o_tmem, ptx::desc_sw128(p_addr + off),
@@ -879,20 +911,21 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           alive = warp_ok(ptx::wait_bounded(bar(L::bSFree + w), (sc - 1) & 1, wd, kSiteSFree)) && alive;
         pf.lap(16);
       };
-      auto do_s_own = [&](int w, uint32_t kslot_) {
+      auto do_s_own = [&](int w, uint32_t kslot_, bool narrow = false) {
         uint32_t& sc = w ? sc1 : sc0;
         ptx::tc_fence_after();
         if (alive && elected()) {
-          issue_s(w ? tS1 : tS0, (w ? q_lo1 : q_lo0) + q_add, k_lo0 + kslot_ * kSlotLo);
+          issue_s(w ? tS1 : tS0, (w ? q_lo1 : q_lo0) + q_add, k_lo0 + kslot_ * kSlotLo,
+                  narrow);
           ptx::mma_commit(bar(L::bSFull + w));
         }
         ++sc;
         pf.lap(4);
         pf.count(7);
       };
-      auto issue_s_own = [&](int w, uint32_t kslot_) {
+      auto issue_s_own = [&](int w, uint32_t kslot_, bool narrow = false) {
         wait_s_own(w);
-        do_s_own(w, kslot_);
+        do_s_own(w, kslot_, narrow);
       };
       auto wait_p_own = [&](int w, int j) {
         uint32_t& pph = w ? pph1 : pph0;
@@ -905,18 +938,18 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         pf.lap(1);
         pph ^= 1u;
       };
-      auto do_pv_own = [&](int w, int j, uint32_t v_lo) {
+      auto do_pv_own = [&](int w, int j, uint32_t v_lo, bool narrow = false) {
         ptx::tc_fence_after();
         if (alive && elected()) {
-          issue_pv(w ? tO1 : tO0, w ? tP1 : tP0, v_lo, j > 0 ? 1u : 0u);
+          issue_pv(w ? tO1 : tO0, w ? tP1 : tP0, v_lo, j > 0 ? 1u : 0u, narrow);
           ptx::mma_commit(bar(L::bPvDone + w));
         }
         pf.lap(5);
         pf.count(7);
       };
-      auto issue_pv_own = [&](int w, int j, uint32_t v_lo) {
+      auto issue_pv_own = [&](int w, int j, uint32_t v_lo, bool narrow = false) {
         wait_p_own(w, j);
-        do_pv_own(w, j, v_lo);
+        do_pv_own(w, j, v_lo, narrow);
       };
       // The producer fills the ring with K0 K1 V0 K2 V1 ... K_{n-1} V_{n-2}
       // V_{n-1} for a piece of n key tiles: 2n loads from ring position
@@ -963,8 +996,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
               if (w == 0 && j < u.n1) issue_s_own(1, kslot);
             } else if constexpr (kWin) {
               kslot = ring_wait(kpos);
-              if (win_active(u, 0, j)) issue_s_own(0, kslot);
-              if (win_active(u, 1, j)) issue_s_own(1, kslot);
+              const bool narrow = j == win_narrow(u, p.sinks, kGapFirst);
+              if (win_active(u, 0, j)) issue_s_own(0, kslot, narrow);
+              if (win_active(u, 1, j)) issue_s_own(1, kslot, narrow);
             } else {
               kslot = ring_wait(kpos);
               if (j < u.n0) issue_s_own(0, kslot);
@@ -1019,12 +1053,14 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           const int nkv = u.nl;
           if (nkv == 0) continue;
           int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
-          int cut = ptx::warp_same(win_next_cut(u, 0, p.sinks));
+          int cut = ptx::warp_same(win_next_cut(u, 0, p.sinks, kGapFirst));
           for (int j = 0; j < nkv; ++j) {
             const uint32_t vslot = ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u));
+            const bool narrow = j == win_narrow(u, p.sinks, kGapFirst);
             if (j == cut) {
-              const int key0 = win_tile(u, j) * kBN;
-              const int r_hi = min(max(u.hi - key0, 0), kBN);            // rows from here on
+              const int key0 = win_tile(u, j, kGapFirst) * kBN;
+              const int rows_v = narrow ? kNarrow : kBN;                 // rows that are read
+              const int r_hi = min(max(u.hi - key0, 0), rows_v);         // rows from here on
               const int r_lo = min(max(u.lo - key0, 0), r_hi);           // rows r_sink .. r_lo - 1
               const int r_sink = min(max(p.sinks - key0, 0), r_lo);
               uint8_t* vt = sgen + L::kKV + vslot * L::kTile;
@@ -1032,16 +1068,16 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
                 uint4* rows = reinterpret_cast<uint4*>(vt + ch * L::kChunkBytes);
                 for (int i = r_sink * 8 + lane; i < r_lo * 8; i += 32)
                   rows[i] = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = r_hi * 8 + lane; i < kBN * 8; i += 32)
+                for (int i = r_hi * 8 + lane; i < rows_v * 8; i += 32)
                   rows[i] = make_uint4(0u, 0u, 0u, 0u);
               }
               ptx::fence_proxy_async_smem();   // visible to the tensor core's reads
               __syncwarp();
-              cut = ptx::warp_same(win_next_cut(u, j + 1, p.sinks));
+              cut = ptx::warp_same(win_next_cut(u, j + 1, p.sinks, kGapFirst));
             }
             const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
-            if (win_active(u, 0, j)) issue_pv_own(0, it0++, v_lo);
-            if (win_active(u, 1, j)) issue_pv_own(1, it1++, v_lo);
+            if (win_active(u, 0, j)) issue_pv_own(0, it0++, v_lo, narrow);
+            if (win_active(u, 1, j)) issue_pv_own(1, it1++, v_lo, narrow);
             if (alive && elected()) ptx::mma_commit(bar(L::bKvEmpty + vslot));
             issued_any = true;
           }
@@ -1113,7 +1149,82 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       float m_ref = -INFINITY;  // reference maximum of the raw scores q.k
       float neg_m = 0.f;        // -m_ref * c (0 while m_ref is -inf)
       float l = 0.f;            // running sum of 2^(s*c + neg_m)
-      for (int j = 0; j < n; ++j) {
+      // kWin: which of this query tile's tiles is a narrow sink tile
+      int j_sink = kWin ? win_narrow(u, p.sinks, kGapFirst) : -1;
+      if (w == 1) j_sink = min(j_sink, 0);
+      // The narrow sink tile, j-th of this query tile: 32 scores, otherwise as below.
+      auto narrow_step = [&](int j) {
+        ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteSFull);
+        ++scnt;
+        __syncwarp();
+        ptx::tc_fence_after();
+        uint32_t sr[kNarrow];
+        ptx::tmem_ld32(tS, sr);
+        ptx::tmem_wait_ld();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(L::bSFree + w));
+        const int lim = min(p.sinks, win_lim);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kNarrow; ++i) {
+          sr[i] = i < lim ? sr[i] : __float_as_uint(-INFINITY);
+          mx = fmaxf(mx, __uint_as_float(sr[i]));
+        }
+        const bool grow = (mx - m_ref) * c > kTau;
+        float alpha = 1.f;
+        if (grow) {
+          const float nm = -mx * c;
+          alpha = (m_ref == -INFINITY) ? 0.f : ptx::ex2(nm - neg_m);
+          l *= alpha;
+          m_ref = mx;
+          neg_m = nm;
+        }
+        uint32_t pk[kNarrow / 2];
+#pragma unroll
+        for (int i = 0; i < kNarrow / 2; ++i) {
+          const float p0 = ptx::ex2(fmaf(__uint_as_float(sr[2 * i]), c, neg_m));
+          const float p1 = ptx::ex2(fmaf(__uint_as_float(sr[2 * i + 1]), c, neg_m));
+          l += p0 + p1;
+          pk[i] = ptx::pack2<kBf16>(p0, p1);
+        }
+        if (j > 0) {
+          ptx::wait_bounded(bar(L::bPvDone + w), pvcnt & 1, wd, kSitePvDone);
+          ++pvcnt;
+          __syncwarp();
+          ptx::tc_fence_after();
+          if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              ptx::tmem_ld32(tO + q4 * 32, sr);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sr[i] = __float_as_uint(__uint_as_float(sr[i]) * alpha);
+              ptx::tmem_st32(tO + q4 * 32, sr);
+            }
+          }
+        }
+        if constexpr (OwnP<D>::kSmem) {
+          uint8_t* prow = sgen + L::kP + w * (kBM * kBN * 2) + t * 128;
+#pragma unroll
+          for (int k = 0; k < kNarrow / 8; ++k)
+            *reinterpret_cast<uint4*>(prow + ((k ^ (t & 7)) << 4)) =
+                make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+          ptx::fence_proxy_async_smem();
+        } else {
+          ptx::tmem_st16(tP, pk);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(L::bPFull + w));
+      };
+      // It stays out of the loop over the others (a branch in the loop cost 5 to
+      // 10 %): at d = 64 it is the first, at d = 128 it may be the second.
+      if constexpr (kWin && D == 64) {
+        if (j_sink == 0) narrow_step(0);
+      }
+      for (int j = kWin && D == 64 ? j_sink + 1 : 0;;) {
+      for (const int end = D == 128 && j == 0 && j_sink >= 0 ? j_sink : n; j < end; ++j) {
         pf.lap(7);
         ptx::wait_bounded(bar(L::bSFull + w), scnt & 1, wd, kSiteSFull);
         pf.lap(0);
@@ -1131,7 +1242,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         int key0 = 0, lim = 0, lo = 0, sink = 0;
         bool cut = false;
         if constexpr (kWin) {
-          key0 = win_tile(u, win_pos(u, w, j)) * kBN;
+          key0 = win_tile(u, win_pos(u, w, j), kGapFirst) * kBN;
           lim = win_lim - key0;
           lo = win_lo - key0;
           sink = min(p.sinks - key0, lim);
@@ -1362,6 +1473,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         ptx::mbar_arrive(bar(L::bPFull + w));
         pf.lap(4);
         if (tracer) trace_event(p, w, tr, kEvPArrive, j);
+      }
+      if (!kWin || D == 64 || j >= n) break;
+      if constexpr (kWin) narrow_step(j++);
       }
 
       // ---- epilogue: O / l in the storage dtype, and LSE = m + ln l per row

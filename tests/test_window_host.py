@@ -36,8 +36,9 @@ static bool sees(long long pos, long long key, int len, int win, int sinks) {
 }
 
 // one head: Nq queries, Nk keys of which len count, window, sinks, alignment
-static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
+static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br, int gap_first = 0) {
   fa::FwdParams p{};
+  p.gap_first = gap_first;
   p.BH = p.H = p.Hk = 1;
   p.N = Nq;
   p.Nk = Nk;
@@ -58,7 +59,7 @@ static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
     std::vector<int> pos_in_list((Nk + 127) / 128 + 1, -1);
     int active[2] = {0, 0};
     for (int j = 0; j < u.nl; ++j) {
-      const int kt = fa::win_tile(u, j);
+      const int kt = fa::win_tile(u, j, gap_first);
       if (kt < 0 || kt * 128 >= len) BAD("fwd tile %d of unit %d", kt, s);
       if (pos_in_list[kt] >= 0) BAD("fwd tile twice %d", kt);
       pos_in_list[kt] = j;
@@ -69,9 +70,9 @@ static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
       bool unseen = false;
       for (int key = kt * 128; key < kt * 128 + 128; ++key)
         unseen |= !(key < sinks && key < x.hi) && !(key >= x.lo && key < x.hi);
-      if (unseen != (fa::win_next_cut(u, j, sinks) == j)) BAD("cut %d of %d", j, u.nl);
+      if (unseen != (fa::win_next_cut(u, j, sinks, gap_first) == j)) BAD("cut %d of %d", j, u.nl);
     }
-    if (u.nl && fa::win_next_cut(u, u.nl, sinks) != u.nl) BAD("cut after the list");
+    if (u.nl && fa::win_next_cut(u, u.nl, sinks, gap_first) != u.nl) BAD("cut after the list");
     if (active[0] != u.n0 || active[1] != u.n1) BAD("fwd active %d %d", active[0], active[1]);
     for (int w = 0; w < 2; ++w)
       for (int r = 0; r < 128; ++r) {
@@ -85,6 +86,12 @@ static int check_prompt(int Nq, int Nk, int len, int win, int sinks, int br) {
               BAD("fwd cleared key %d", key);
           }
       }
+  }
+  if (!gap_first) {
+    const int rc = check_prompt(Nq, Nk, len, win, sinks, br, 1);
+    if (rc) return rc;
+  } else {
+    return 0;
   }
   const int n_tiles = (Nq + 127) / 128, n_ktiles = (Nk + 127) / 128;
   const int nkv = (len + 127) / 128;
