@@ -306,3 +306,38 @@ def test_rows_past_two_to_the_31_elements():
     cut = lambda t: t[:, :, win:]
     got = dict(zip(("o", "lse", "dq", "dk", "dv"), map(cut, last[4:])))
     wc.check(got, {n: cut(x) for n, x in val.items()}, {n: cut(x) for n, x in tol.items()}, "last rows")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sinks", [1, 16, 31, 32, 33, 128, 129, 300])
+def test_sinks_far_behind_the_window(d, sinks):
+    """Units whose windows lie past the sinks, whole and ragged lengths: a sink
+    tile of its own, narrow up to 32 sinks, before or behind the first tile of
+    the windows."""
+    B, H, Hk, Nq, Nk, win = 2, 4, 2, 700, 1300, 200
+    lens = [1300, 911]
+    q, k, v, do = inputs(B, H, Hk, Nq, Nk, d, "bf16", seed=100 + sinks)
+    ms = masks(B, Nq, Nk, lens, "bottom_right", win, sinks)
+    for b in range(B):      # what nobody sees must not matter here either
+        unseen = ~torch.from_numpy(ms[b].any(0))
+        k[b, :, unseen] = float("nan")
+        v[b, :, unseen] = float("nan")
+    got = run(q, k, v, do, win, sinks, "bottom_right", lens)
+    val, tol = wc.reference(q, k, v, ms, wc.scale_of(d), "bf16", do)
+    wc.check(got, val, tol, f"{sinks} sinks")
+
+
+def test_large_scores_move_the_reference_at_every_tile():
+    """Scores that grow along the keys, and largest at the sinks: the running
+    maximum moves at each tile, also at a narrow sink tile behind the first."""
+    B, H, Hk, N, win = 1, 2, 1, 900, 300
+    for d in (64, 128):
+        for sign in (1, -1):
+            q, k, v, do = inputs(B, H, Hk, N, N, d, "bf16", seed=55)
+            ramp = torch.linspace(0.2, 3, N) if sign > 0 else torch.linspace(3, 0.2, N)
+            k = (k.float() * ramp[None, None, :, None]).to(k.dtype)
+            k[:, :, :4] *= 6
+            got = run(q, k, v, do, win, 4, "upper_left", None)
+            val, tol = wc.reference(q, k, v, masks(B, N, N, None, "upper_left", win, 4),
+                                    wc.scale_of(d), "bf16", do)
+            wc.check(got, val, tol, f"d {d} sign {sign}")
