@@ -44,8 +44,8 @@
 //
 // Sliding-window calls (kWin) keep for the query at position p the keys
 // j <= p with j > p - win or j < sinks.  A unit streams only the key tiles
-// that one of its rows can see: the tiles of the sinks, then the tiles of
-// the union of its rows' windows; of these each query tile computes its own
+// that one of its rows can see: the tiles of the sinks and those of the
+// union of its rows' windows; of these each query tile computes its own
 // (win_active), so a unit of 256 rows costs about (win + 128) / 128 + the
 // sink tiles per query tile whatever the length.  H query heads may share
 // Hk key/value heads.  Measured (bf16; TFLOP/s of the visible pairs): B1 H32/8
@@ -908,7 +908,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         const uint32_t sc = w ? sc1 : sc0;
         pf.lap(6);
         if (sc > 0)   // the softmax has read the previous S of this tile
-          alive = warp_ok(ptx::wait_bounded(bar(L::bSFree + w), (sc - 1) & 1, wd, kSiteSFree)) && alive;
+          alive = warp_ok(ptx::wait_bounded(bar(L::bSFree + w), (sc - 1) & 1, wd, kSiteSFree)) &&
+                  alive;
         pf.lap(16);
       };
       auto do_s_own = [&](int w, uint32_t kslot_, bool narrow = false) {
@@ -932,7 +933,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         const uint32_t ucnt = w ? ucnt1 : ucnt0;
         pf.lap(6);
         if (j == 0 && ucnt > 0)   // O_w of the previous piece must have been read out
-          alive = warp_ok(ptx::wait_bounded(bar(L::bOFree + w), (ucnt - 1) & 1, wd, kSiteOFree)) && alive;
+          alive = warp_ok(ptx::wait_bounded(bar(L::bOFree + w), (ucnt - 1) & 1, wd, kSiteOFree)) &&
+                  alive;
         pf.lap(3);
         alive = warp_ok(ptx::wait_bounded(bar(L::bPFull + w), pph, wd, kSitePFull)) && alive;
         pf.lap(1);
@@ -964,9 +966,10 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       auto ring_wait = [&](uint32_t pos) -> uint32_t {
         const uint32_t sl = pos % L::kStages;
         pf.lap(6);
-        alive = warp_ok(ptx::wait_bounded(full0 + 8u * sl,
-                                  L::kTwoFull ? (odd >> sl) & 1u : (pos / L::kStages) & 1u, wd,
-                                  kSiteKvFull)) && alive;
+        alive = warp_ok(ptx::wait_bounded(
+                    full0 + 8u * sl, L::kTwoFull ? (odd >> sl) & 1u : (pos / L::kStages) & 1u, wd,
+                    kSiteKvFull)) &&
+                alive;
         if (L::kTwoFull) odd ^= 1u << sl;
         pf.lap(0);
         ptx::tc_fence_after();
@@ -981,7 +984,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           if (kKv && nkv == 0) continue;
           pf.lap(6);
           const uint32_t qb = k_units % L::kQBufs;
-          alive = warp_ok(ptx::wait_bounded(bar(L::bQFull + qb), (k_units / L::kQBufs) & 1, wd, kSiteQFull)) && alive;
+          alive = warp_ok(ptx::wait_bounded(bar(L::bQFull + qb), (k_units / L::kQBufs) & 1, wd,
+                                            kSiteQFull)) &&
+                  alive;
           q_add = qb * static_cast<uint32_t>((2 * L::kTile) >> 4);
           pf.lap(2);
           ptx::tc_fence_after();
@@ -1223,6 +1228,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       if constexpr (kWin && D == 64) {
         if (j_sink == 0) narrow_step(0);
       }
+      // The outer loop, around it, runs once where there is none, else twice.
       for (int j = kWin && D == 64 ? j_sink + 1 : 0;;) {
       for (const int end = D == 128 && j == 0 && j_sink >= 0 ? j_sink : n; j < end; ++j) {
         pf.lap(7);
