@@ -1055,10 +1055,11 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
       }
       if constexpr (kWin) {
         // queries q with key <= q + off < key + win (sinks: no upper bound);
-        // padding keys see none
+        // padding keys see none, and rows past the queries are none (their
+        // weights are 0, unless the score with a key that nobody sees is NaN)
         const int qb = i * kBwdTile + group * W::kCols;
         win_lo = key >= len ? W::kCols : static_cast<int>(key) - off - qb;
-        win_hi = key < p.sinks ? W::kCols : static_cast<int>(key) + p.win - off - qb;
+        win_hi = min(key < p.sinks ? q_rows : static_cast<int>(key) + p.win - off, q_rows) - qb;
         // (one compare and one select a query and end; no short circuits)
         if (win_lo > 0) {
 #pragma unroll

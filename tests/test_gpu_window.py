@@ -341,3 +341,18 @@ def test_large_scores_move_the_reference_at_every_tile():
             val, tol = wc.reference(q, k, v, masks(B, N, N, None, "upper_left", win, 4),
                                     wc.scale_of(d), "bf16", do)
             wc.check(got, val, tol, f"d {d} sign {sign}")
+
+
+@pytest.mark.parametrize("junk", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Nq,Nk,sinks", [(1, 506, 1), (5, 9, 4), (254, 395, 0), (130, 200, 180)])
+def test_keys_after_the_last_query_may_hold_anything(Nq, Nk, sinks, junk):
+    """Keys of a query tile's key tile that come after its last query."""
+    B, H, Hk, win = 2, 4, 2, 35
+    for d in (64, 128):
+        q, k, v, do = inputs(B, H, Hk, Nq, Nk, d, "bf16", seed=61)
+        k[:, :, Nq:] = junk
+        v[:, :, Nq:] = junk
+        got = run(q, k, v, do, win, sinks, "upper_left", None)
+        val, tol = wc.reference(q, k, v, masks(B, Nq, Nk, None, "upper_left", win, sinks),
+                                wc.scale_of(d), "bf16", do)
+        wc.check(got, val, tol, f"{Nq} of {Nk}, {junk}")
