@@ -61,7 +61,7 @@ cudaError_t launch_variant(const DecWinParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Where units are cut into two or three parts, a thread with registers for
-  // three lets more of them run at a time (44 against 72 registers; 128 rows
+  // three lets more of them run at a time (40 against 72 registers; 128 rows
   // of 16 caches, 128 units: the call 72.5 us, 77.5 with eight); many parts
   // are loaded eight at a time, one wait for each eight.
   const bool few = p.grid <= 2ll * p.B * p.Hk * p.row_blocks;

@@ -1146,6 +1146,8 @@ __global__ void __launch_bounds__(kDwCombineThreads)
   // the unit's first part is the last piece of its run, the others are the
   // first of theirs
   auto slot_of = [&](int run) { return static_cast<size_t>(run == run0 ? cut.z : 2 * run); };
+  const float4* const part = dec_part<D>(p, 0, srow, c);
+  const size_t part_step = static_cast<size_t>(D / 4) * p.slot_rows;
   float nm = INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int run = run0; run <= cut.w; run += kBatch) {
@@ -1157,7 +1159,7 @@ __global__ void __launch_bounds__(kDwCombineThreads)
       if (run + i <= cut.w) {
         const size_t slot = slot_of(run + i);
         ml[i] = p.part_ml[slot * p.slot_rows + srow];
-        x[i] = *dec_part<D>(p, slot, srow, c);
+        x[i] = part[slot * part_step];
       } else {
         ml[i] = make_float2(0.f, 0.f);
       }
