@@ -279,19 +279,18 @@ struct Smem {
   static constexpr int kMask = kP + (OwnP<D>::kSmem ? 2 * kBM * kBN * 2 : 0);  // mask rings
   static constexpr int kBar = kMask + (kGen ? 2 * kMaskStages * kMaskBytes : 0);
   // barrier indices (the mask barriers, [query tile][stage], only with the generator)
-  // Full barriers of a ring slot.  K tiles are waited for by the S issuer, V
-  // tiles by the P V issuer, and a wait by parity is only sound while the
-  // barrier is at most one phase behind the waiting thread: polling use u of
-  // a slot while the other issuer's use u - 1 is still in flight would pass
-  // on the parity of use u - 2.  With eight stages a slot's previous use is a
-  // tile of the same issuer, or (across a unit's end) one that products already
-  // issued depend on.  With three, V_j follows K_j in its slot and K_j follows
-  // V_{j-3}: there the issuers order their waits so that the previous use is
-  // known to be over (ring_order below), or (kWin, whose query tiles skip some
-  // of the listed tiles) a slot has a barrier for K and one for V.
-  static constexpr bool kTwoFull = kWin && kStages == 3;
+  // A ring slot has a full barrier for its K tiles, which the S issuer waits
+  // for, and one for its V tiles, which the P V issuer waits for.  A wait by
+  // parity is only sound while the barrier is at most one phase behind the
+  // waiting thread: on a barrier of both, polling use u of a slot while the
+  // other issuer's use u - 1 is still in flight would pass on the parity of
+  // use u - 2, and the product would read a slot that a copy is being written
+  // to.  A slot's previous use can be the other issuer's in a ring of any depth
+  // (two stages: V_0 after K_0; three: V_j after K_j; two to eight: the K
+  // tiles at a unit's start after the V tiles at the previous one's end), and
+  // no order of the issuers' waits covers them all.
   static constexpr int bQFull = 0, bQEmpty = kQBufs, bKFull = 2 * kQBufs,
-                       bVFull = bKFull + (kTwoFull ? kStages : 0), bKvEmpty = bVFull + kStages,
+                       bVFull = bKFull + kStages, bKvEmpty = bVFull + kStages,
                        bSFull = bKvEmpty + kStages, bPFull = bSFull + 2,
                        bOFree = bPFull + 2, bSFree = bOFree + 2, bPvDone = bSFree + 2,
                        bFinal = bPvDone + 2, bFinalPv = bFinal + 1, bMaskFull = bFinalPv + 1,
@@ -647,7 +646,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     }
     for (int s = 0; s < L::kStages; ++s) {
       ptx::mbar_init(bar(L::bKFull + s), 1);
-      if (L::kTwoFull) ptx::mbar_init(bar(L::bVFull + s), 1);
+      ptx::mbar_init(bar(L::bVFull + s), 1);
       ptx::mbar_init(bar(L::bKvEmpty + s), 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -777,10 +776,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             // kKv: only the chunks of the tensor's own width (d for K, dv for V)
             const int nc = kKv && !kWin ? (kv ? p.dv : p.dqk) / 64 : L::kChunks;
             const uint32_t full = bar((kv ? L::bVFull : L::bKFull) + slot);
-            if constexpr (L::kTwoFull) {
-              (kv ? v_odd : k_odd) ^= 1u << slot;
-              (kv ? v_used : k_used) |= 1u << slot;
-            }
+            (kv ? v_odd : k_odd) ^= 1u << slot;
+            (kv ? v_used : k_used) |= 1u << slot;
             ptx::mbar_arrive_expect_tx(full, nc * L::kChunkBytes);
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
@@ -805,10 +802,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       }
       // Drain: make sure every issued copy has landed before the CTA can exit.
       const unsigned long long drain = 200000000ull;   // cycles (~0.1 s)
-      const uint32_t first = loads > (uint32_t)L::kStages ? loads - L::kStages : 0;
-      for (uint32_t l = first; !L::kTwoFull && l < loads; ++l)
-        ptx::wait_drain(bar(L::bKFull + l % L::kStages), (l / L::kStages) & 1, drain);
-      for (int s = 0; L::kTwoFull && s < L::kStages; ++s) {
+      for (int s = 0; s < L::kStages; ++s) {
         if ((k_used >> s) & 1u)
           ptx::wait_drain(bar(L::bKFull + s), ((k_odd >> s) & 1u) ^ 1u, drain);
         if ((v_used >> s) & 1u)
@@ -904,16 +898,13 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
                                           : tmem + p_col<D>(1);
       uint32_t sc0 = 0, sc1 = 0;     // S issued into S0 / S1 so far
       uint32_t q_add = 0;            // address-word offset of the current unit's Q buffer
-      auto wait_s_own = [&](int w) {
-        const uint32_t sc = w ? sc1 : sc0;
+      auto issue_s_own = [&](int w, uint32_t kslot_, bool narrow = false) {
+        uint32_t& sc = w ? sc1 : sc0;
         pf.lap(6);
         if (sc > 0)   // the softmax has read the previous S of this tile
           alive = warp_ok(ptx::wait_bounded(bar(L::bSFree + w), (sc - 1) & 1, wd, kSiteSFree)) &&
                   alive;
         pf.lap(16);
-      };
-      auto do_s_own = [&](int w, uint32_t kslot_, bool narrow = false) {
-        uint32_t& sc = w ? sc1 : sc0;
         ptx::tc_fence_after();
         if (alive && elected()) {
           issue_s(w ? tS1 : tS0, (w ? q_lo1 : q_lo0) + q_add, k_lo0 + kslot_ * kSlotLo,
@@ -924,11 +915,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         pf.lap(4);
         pf.count(7);
       };
-      auto issue_s_own = [&](int w, uint32_t kslot_, bool narrow = false) {
-        wait_s_own(w);
-        do_s_own(w, kslot_, narrow);
-      };
-      auto wait_p_own = [&](int w, int j) {
+      auto issue_pv_own = [&](int w, int j, uint32_t v_lo, bool narrow = false) {
         uint32_t& pph = w ? pph1 : pph0;
         const uint32_t ucnt = w ? ucnt1 : ucnt0;
         pf.lap(6);
@@ -939,8 +926,6 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         alive = warp_ok(ptx::wait_bounded(bar(L::bPFull + w), pph, wd, kSitePFull)) && alive;
         pf.lap(1);
         pph ^= 1u;
-      };
-      auto do_pv_own = [&](int w, int j, uint32_t v_lo, bool narrow = false) {
         ptx::tc_fence_after();
         if (alive && elected()) {
           issue_pv(w ? tO1 : tO0, w ? tP1 : tP0, v_lo, j > 0 ? 1u : 0u, narrow);
@@ -949,28 +934,19 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         pf.lap(5);
         pf.count(7);
       };
-      auto issue_pv_own = [&](int w, int j, uint32_t v_lo, bool narrow = false) {
-        wait_p_own(w, j);
-        do_pv_own(w, j, v_lo, narrow);
-      };
       // The producer fills the ring with K0 K1 V0 K2 V1 ... K_{n-1} V_{n-2}
       // V_{n-1} for a piece of n key tiles: 2n loads from ring position
-      // `base`; each issuer waits only for the tiles it reads (kTwoFull: on its
-      // own full barrier of the slot; odd: per slot, parity of its tiles so far).
-      // One barrier a slot and three stages: the P V issuer first waits for P_j
-      // (formed from K_j) and the S issuer for the softmax to have read S_{j-1}
-      // (after writing P_{j-2}, which follows P V_{j-3}).
-      constexpr bool ring_order = !kWin && L::kStages == 3;
-      const uint32_t full0 = bar(warp == kMmaWarp ? L::bKFull : L::bVFull);
+      // `base`; each issuer waits only for the tiles it reads, on its own full
+      // barrier of the slot (odd: per slot, parity of its tiles so far).
+      // (`full` is a constant in each role's loop: picked by the warp's index
+      // instead, it cost 10 % at d = 64, B16 H16 N1024 80.0 us against 72.7.)
       uint32_t odd = 0;
-      auto ring_wait = [&](uint32_t pos) -> uint32_t {
+      auto ring_wait = [&](uint32_t pos, int full) -> uint32_t {
         const uint32_t sl = pos % L::kStages;
         pf.lap(6);
-        alive = warp_ok(ptx::wait_bounded(
-                    full0 + 8u * sl, L::kTwoFull ? (odd >> sl) & 1u : (pos / L::kStages) & 1u, wd,
-                    kSiteKvFull)) &&
+        alive = warp_ok(ptx::wait_bounded(bar(full + sl), (odd >> sl) & 1u, wd, kSiteKvFull)) &&
                 alive;
-        if (L::kTwoFull) odd ^= 1u << sl;
+        odd ^= 1u << sl;
         pf.lap(0);
         ptx::tc_fence_after();
         return sl;
@@ -991,21 +967,12 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           pf.lap(2);
           ptx::tc_fence_after();
           for (int j = 0; j < nkv; ++j) {
-            const uint32_t kpos = base + (j == 0 ? 0u : 2u * j - 1u);
-            uint32_t kslot;
-            if constexpr (ring_order) {
-              const int w = j < u.n0 ? 0 : 1;
-              wait_s_own(w);
-              kslot = ring_wait(kpos);
-              do_s_own(w, kslot);
-              if (w == 0 && j < u.n1) issue_s_own(1, kslot);
-            } else if constexpr (kWin) {
-              kslot = ring_wait(kpos);
+            const uint32_t kslot = ring_wait(base + (j == 0 ? 0u : 2u * j - 1u), L::bKFull);
+            if constexpr (kWin) {
               const bool narrow = j == win_narrow(u, p.sinks, kGapFirst);
               if (win_active(u, 0, j)) issue_s_own(0, kslot, narrow);
               if (win_active(u, 1, j)) issue_s_own(1, kslot, narrow);
             } else {
-              kslot = ring_wait(kpos);
               if (j < u.n0) issue_s_own(0, kslot);
               if (j < u.n1) issue_s_own(1, kslot);
             }
@@ -1024,20 +991,11 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           const int nkv = max(u.n0, u.n1);
           if (kKv && nkv == 0) continue;
           for (int j = 0; j < nkv; ++j) {
-            const uint32_t vpos = base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u);
-            uint32_t vslot;
-            if constexpr (ring_order) {
-              const int w = j < u.n0 ? 0 : 1;
-              wait_p_own(w, j);
-              vslot = ring_wait(vpos);
-              do_pv_own(w, j, v_lo0 + vslot * kSlotLo);
-              if (w == 0 && j < u.n1) issue_pv_own(1, j, v_lo0 + vslot * kSlotLo);
-            } else {
-              vslot = ring_wait(vpos);
-              const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
-              if (j < u.n0) issue_pv_own(0, j, v_lo);
-              if (j < u.n1) issue_pv_own(1, j, v_lo);
-            }
+            const uint32_t vslot =
+                ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u), L::bVFull);
+            const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
+            if (j < u.n0) issue_pv_own(0, j, v_lo);
+            if (j < u.n1) issue_pv_own(1, j, v_lo);
             if (alive) ptx::mma_commit(bar(L::bKvEmpty + vslot));
             issued_any = true;
           }
@@ -1060,7 +1018,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
           int cut = ptx::warp_same(win_next_cut(u, 0, p.sinks, kGapFirst));
           for (int j = 0; j < nkv; ++j) {
-            const uint32_t vslot = ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u));
+            const uint32_t vslot =
+                ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u), L::bVFull);
             const bool narrow = j == win_narrow(u, p.sinks, kGapFirst);
             if (j == cut) {
               const int key0 = win_tile(u, j, kGapFirst) * kBN;
