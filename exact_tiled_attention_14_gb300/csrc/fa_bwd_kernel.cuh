@@ -1563,6 +1563,11 @@ __global__ void __launch_bounds__(BwdRoles<kWin>::kThreads, 1)
     else
       bwd_dq_cta<D, kBf16, kCausal, kDrop, kKv, kWin>(p, item - per_pass, tmem_base);
   }
+  // A call in which no query sees a key (all counts 0, no keys, every position
+  // negative) has only items without steps, none of which waits for the D
+  // pass: without this wait the grid, and with it the call, could end while
+  // that pass still writes `delta`.
+  if constexpr (kKv) ptx::griddep_wait();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == W::kMmaWarp) {
