@@ -948,6 +948,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         // maximum.  The statistics go through the unit's query buffer, which
         // S no longer reads; group w then handles half w of the columns of
         // both groups' O (both groups' warps reach the same TMEM lanes).
+        // A part takes no part only where its sum is exactly 0 (nothing seen):
+        // a sum of NaN, from a key that is not finite, makes the row NaN.
         uint8_t* scratch = sgen + L::kQ + qb * L::kTile;
         float2* ml_s = reinterpret_cast<float2*>(scratch);
         ptx::named_bar_sync(1, 256);             // both groups have their last S
@@ -959,19 +961,19 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 #pragma unroll
         for (int g = 0; g < 2 * kCopies; ++g) {
           const float2 x = ml_s[g * kRows + r];
-          if (x.y > 0.f) nm = fminf(nm, x.x);
+          if (x.y != 0.f) nm = fminf(nm, x.x);
         }
 #pragma unroll
         for (int g = 0; g < 2 * kCopies; ++g) {
           const float2 x = ml_s[g * kRows + r];
-          if (x.y > 0.f) lt = fmaf(ptx::ex2(nm - x.x), x.y, lt);
+          if (x.y != 0.f) lt = fmaf(ptx::ex2(nm - x.x), x.y, lt);
         }
         // this lane's parts
         const float2 y0 = ml_s[t], y1 = ml_s[kDwTile + t];
         // (a finished unit's are divided by l here)
-        const float inv = pc.whole && lt > 0.f ? 1.0f / lt : 1.f;
-        const float f0 = y0.y > 0.f ? ptx::ex2(nm - y0.x) * inv : 0.f;
-        const float f1 = y1.y > 0.f ? ptx::ex2(nm - y1.x) * inv : 0.f;
+        const float inv = pc.whole && lt != 0.f ? 1.0f / lt : 1.f;
+        const bool live0 = y0.y != 0.f, live1 = y1.y != 0.f;
+        const float f0 = ptx::ex2(nm - y0.x) * inv, f1 = ptx::ex2(nm - y1.x) * inv;
         const size_t out_row = head * p.R + row;
         const bool two = pc.n > 1;               // the second group had a tile
         // 16 columns of this lane, both groups' parts added
@@ -980,20 +982,20 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           ptx::tmem_ld16(tmem_base + lane_off + L::o_col(0) + col, a);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = f0 > 0.f ? __uint_as_float(a[e]) * f0 : 0.f;
+          for (int e = 0; e < 16; ++e) x[e] = live0 ? __uint_as_float(a[e]) * f0 : 0.f;
           if (two) {
             ptx::tmem_ld16(tmem_base + lane_off + L::o_col(1) + col, a);
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              x[e] = f1 > 0.f ? fmaf(__uint_as_float(a[e]), f1, x[e]) : x[e];
+              x[e] = live1 ? fmaf(__uint_as_float(a[e]), f1, x[e]) : x[e];
           }
         };
         if (r < nrows && seg == 0 && w == 0) {
           if (pc.whole)
-            p.lse[out_row] = lt > 0.f ? (ptx::lg2(lt) - nm) * 0.693147180559945309f : -INFINITY;
+            p.lse[out_row] = lt != 0.f ? (ptx::lg2(lt) - nm) * 0.693147180559945309f : -INFINITY;
           else
-            p.part_ml[slot * p.slot_rows + r] = make_float2(lt > 0.f ? nm : 0.f, lt);
+            p.part_ml[slot * p.slot_rows + r] = make_float2(lt != 0.f ? nm : 0.f, lt);
         }
         if constexpr (kCopies == 1) {
           if (has) {
@@ -1071,7 +1073,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         ptx::mbar_arrive(bar(L::bOFree + 1));
       } else {
         const size_t out_row = head * p.R + row;
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        const float inv = l != 0.f ? 1.0f / l : 0.f;
         if (has) {
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
@@ -1080,7 +1082,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             ptx::tmem_wait_ld();
             float x[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = l > 0.f ? __uint_as_float(a[e]) : 0.f;
+            for (int e = 0; e < 32; ++e) x[e] = l != 0.f ? __uint_as_float(a[e]) : 0.f;
             if (r < nrows) {
               if (pc.whole) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + out_row * D + col);
@@ -1100,7 +1102,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           }
           if (r < nrows) {
             if (pc.whole)
-              p.lse[out_row] = l > 0.f ? (ptx::lg2(l) - neg_m) * 0.693147180559945309f : -INFINITY;
+              p.lse[out_row] = l != 0.f ? (ptx::lg2(l) - neg_m) * 0.693147180559945309f : -INFINITY;
             else
               p.part_ml[slot * p.slot_rows + w * kDwTile + r] = make_float2(neg_m, l);
           }
@@ -1124,10 +1126,11 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 // starts in that run and ends in a later one (most runs have one, the run
 // table says which), 4 columns a thread: every part is scaled to the largest
 // maximum, added in the order of the runs, and the sum divided once.  A row
-// without a visible key has no live part: O = 0 and LSE = -inf.  A block takes
-// 2^combine_rows rows (up to 32) and as many columns as its threads reach;
-// four neighbours share a row, so that a warp reads 128 bytes of each of four
-// columns' parts and writes 32 of each row.  kBatch parts are loaded together.
+// without a visible key has no live part (all sums are 0; a sum of NaN is live):
+// O = 0 and LSE = -inf.  A block takes 2^combine_rows rows (up to 32) and as
+// many columns as its threads reach; four neighbours share a row, so that a
+// warp reads 128 bytes of each of four columns' parts and writes 32 of each
+// row.  kBatch parts are loaded together.
 constexpr int kDwCombineThreads = 128;
 template <int D, bool kBf16, int kBatch>
 __global__ void __launch_bounds__(kDwCombineThreads)
@@ -1167,14 +1170,14 @@ __global__ void __launch_bounds__(kDwCombineThreads)
     float m = nm;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (ml[i].y > 0.f) m = fminf(m, ml[i].x);
+      if (ml[i].y != 0.f) m = fminf(m, ml[i].x);
     const float fo = nm == INFINITY ? 0.f : ptx::ex2(m - nm);
     acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
     l *= fo;
     nm = m;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (ml[i].y > 0.f) {
+      if (ml[i].y != 0.f) {
         const float f = ptx::ex2(m - ml[i].x);
         acc.x = fmaf(f, x[i].x, acc.x);
         acc.y = fmaf(f, x[i].y, acc.y);
@@ -1184,11 +1187,11 @@ __global__ void __launch_bounds__(kDwCombineThreads)
       }
   }
   const size_t out = static_cast<size_t>(cut.x) * p.R + row;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = l != 0.f ? 1.0f / l : 0.f;
   reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D)[c] =
       make_uint2(ptx::pack2<kBf16>(acc.x * inv, acc.y * inv),
                  ptx::pack2<kBf16>(acc.z * inv, acc.w * inv));
-  if (c == 0) p.lse[out] = l > 0.f ? (ptx::lg2(l) - nm) * 0.693147180559945309f : -INFINITY;
+  if (c == 0) p.lse[out] = l != 0.f ? (ptx::lg2(l) - nm) * 0.693147180559945309f : -INFINITY;
 }
 
 }  // namespace fa
