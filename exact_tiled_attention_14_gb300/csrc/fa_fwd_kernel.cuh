@@ -1452,8 +1452,9 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       if (tracer) trace_event(p, w, tr, kEvEpiStart, ucnt - 1);
       __syncwarp();
       ptx::tc_fence_after();
-      // a row that saw no key (kKv masks) keeps l = 0: O = 0, LSE = -inf
-      const float inv_l = (l > 0.f ? 1.0f / l : 0.f) * (kDrop ? p.drop_scale : 1.f);
+      // a row that saw no key (kKv masks) keeps l = 0: O = 0, LSE = -inf.  A
+      // key that is not finite makes l NaN, and O and LSE with it.
+      const float inv_l = (l != 0.f ? 1.0f / l : 0.f) * (kDrop ? p.drop_scale : 1.f);
       if (kSplit && u.tail >= 0) {
         // Partial piece of a split unit: unnormalised O rows and (-m*c, l)
         // go to this piece's workspace slot; the piece that finishes last
@@ -1513,7 +1514,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
             const float* sp = p.ws_part +
                               static_cast<size_t>(2 * tw.c + (u.tail == first_t ? 0 : 1)) * kSlotFloats<D>();
             const float2 ml = reinterpret_cast<const float2*>(sp + 2 * kBM * D)[w * kBM + t];
-            if (!(ml.y > 0.f)) continue;
+            if (ml.y == 0.f) continue;
             float f = 1.f;
             if (ml.x < nm_run) {                              // larger maximum: move the reference
               const float a = (nm_run == INFINITY) ? 0.f : ptx::ex2(ml.x - nm_run);
@@ -1612,7 +1613,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         ptx::mbar_arrive(bar(L::bOFree + w));        // O_w may be overwritten now
       }
       if ((!kSplit || u.tail < 0) && row < (kKv ? rows_q : p.N))
-        p.lse[lse_at<kKv, kWin>(p, u, row)] = l > 0.f ? (ptx::lg2(l) - neg_m) * kLn2 : -INFINITY;
+        p.lse[lse_at<kKv, kWin>(p, u, row)] = l != 0.f ? (ptx::lg2(l) - neg_m) * kLn2 : -INFINITY;
       if (tracer) trace_event(p, w, tr, kEvEpiEnd, ucnt - 1);
       pf.lap(6);
     }

@@ -93,3 +93,34 @@ def test_decode_tree(T, G, Nk, junk):
     run = lambda kk: fa.attention_decode_tree(q, kk, v, rows, seqlens_k=n)
     check(run, k, [(0, 0, hist[0] // 2)], ms, junk)
     check(run, k, [(0, 0, hist[0] + 1), (1, 0, 150 + T - 1)], ms, junk)
+
+
+@ONE_KIND
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_window(d, junk):
+    lens = [700, 650]
+    q, k, v = inputs(2, 4, 2, 600, 700, d)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for win, sinks in ((300, 5), (100, 40)):
+        ms = masks_of(600, 700, lens, win, sinks)
+        run = lambda kk: fa.attention_forward_window(q, kk, v, win, sinks, seqlens_k=n)
+        check(run, k, [(0, 0, 400)], ms, junk)
+        check(run, k, [(1, 1, 649), (0, 1, 699)], ms, junk)
+
+
+@ONE_KIND
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", ["plain", "causal", "split", "split causal", "dropout"])
+def test_square_forward(form, d, junk):
+    """Heads with one bad key; with dropout a row that dropped it has a sum of NaN too."""
+    B, H, N = 2, 40, 600
+    q, k, v = inputs(B, H, H, N, N, d, "bf16")
+    causal = "causal" in form
+    ms = [np.tril(np.ones((N, N), dtype=bool)) if causal else np.ones((N, N), dtype=bool)] * B
+    if form == "dropout":
+        run = lambda kk: fa.flash_attention(q, kk, v, dropout_p=0.5, seed=3)
+    else:
+        ws = "auto" if "split" in form else None
+        run = lambda kk: fa.attention_forward(q, kk, v, causal=causal, workspace=ws)
+    places = [(b, h, (37 * h) % N) for b in range(B) for h in range(0, H, 3)]
+    check(run, k, places, ms, junk)
