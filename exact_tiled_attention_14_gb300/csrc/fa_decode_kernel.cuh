@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 }
 
 // One block of D threads per (batch*head, query): combine the parts, thread
-// c owning output column c.  Parts with no visible key (l = 0) are skipped;
-// a query with none at all gets O = 0 and LSE = -inf.
+// c owning output column c.  Parts with no visible key (l = 0 exactly: a sum of
+// NaN, from a key that is not finite, makes the row NaN) are skipped; a query
+// with none at all gets O = 0 and LSE = -inf.
 constexpr int kCombineFast = 32;   // parts merged from registers in one pass
 
 template <int D, bool kBf16>
@@ -322,10 +323,10 @@ __global__ void __launch_bounds__(D, 1) fa_decode_combine_kernel(const float* __
     }
 #pragma unroll
     for (int i = 0; i < kCombineFast; ++i)
-      if (ml[i].y > 0.f) m = fmaxf(m, ml[i].x);
+      if (ml[i].y != 0.f) m = fmaxf(m, ml[i].x);
 #pragma unroll
     for (int i = 0; i < kCombineFast; ++i) {
-      const bool live = ml[i].y > 0.f;
+      const bool live = ml[i].y != 0.f;
       const float f = live ? ptx::ex2(ml[i].x - m) : 0.f;
       acc = live ? fmaf(f, ov[i], acc) : acc;
       lt = live ? fmaf(f, ml[i].y, lt) : lt;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(D, 1) fa_decode_combine_kernel(const float* __
   } else {
     for (int s = c; s < splits; s += D) {
       const float2 ml = part_ml[base + static_cast<size_t>(s) * Nq];
-      if (ml.y > 0.f) m = fmaxf(m, ml.x);
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(D, 1) fa_decode_combine_kernel(const float* __
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool live = ml[i].y > 0.f;
+        const bool live = ml[i].y != 0.f;
         const float f = live ? ptx::ex2(ml[i].x - m) : 0.f;
         acc = live ? fmaf(f, ov[i], acc) : acc;
         lt = live ? fmaf(f, ml[i].y, lt) : lt;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(D, 1) fa_decode_combine_kernel(const float* __
     for (; s < splits; ++s) {
       const size_t part = base + static_cast<size_t>(s) * Nq;
       const float2 ml = part_ml[part];
-      if (ml.y > 0.f) {
+      if (ml.y != 0.f) {
         const float f = ptx::ex2(ml.x - m);
         acc = fmaf(f, part_o[part * D + c], acc);
         lt = fmaf(f, ml.y, lt);
@@ -371,10 +372,10 @@ __global__ void __launch_bounds__(D, 1) fa_decode_combine_kernel(const float* __
     }
   }
   const size_t row = static_cast<size_t>(bh) * Nq + q;
-  const float out = lt > 0.f ? acc / lt : 0.f;
+  const float out = lt != 0.f ? acc / lt : 0.f;
   const uint32_t pk = ptx::pack2<kBf16>(out, 0.f);   // the value in the low half
   static_cast<uint16_t*>(o)[row * D + c] = static_cast<uint16_t>(pk & 0xffffu);
-  if (c == 0) lse[row] = lt > 0.f ? (m + ptx::lg2(lt)) * 0.693147180559945309f : -INFINITY;
+  if (c == 0) lse[row] = lt != 0.f ? (m + ptx::lg2(lt)) * 0.693147180559945309f : -INFINITY;
 }
 
 }  // namespace fa

@@ -124,3 +124,14 @@ def test_square_forward(form, d, junk):
         run = lambda kk: fa.attention_forward(q, kk, v, causal=causal, workspace=ws)
     places = [(b, h, (37 * h) % N) for b in range(B) for h in range(0, H, 3)]
     check(run, k, places, ms, junk)
+
+
+@ONE_KIND
+@pytest.mark.parametrize("Nk", [700, 20000])
+def test_decode(Nk, junk):
+    B, H, Nq, d = 1, 2, 3, 128
+    q, k, v = inputs(B, H, H, Nq, Nk, d, "bf16")
+    ms = masks_of(Nq, Nk, [Nk], 1 << 30, 0)
+    run = lambda kk: fa.attention_decode(q, kk, v, causal=True)
+    for key in (0, Nk // 2, Nk - 1):
+        check(run, k, [(0, 1, key)], ms, junk)
