@@ -335,7 +335,7 @@ __host__ __device__ __forceinline__ DecRow dec_row(const unsigned long long* row
   const unsigned long long used = Nq == 64 ? ~0ull : (1ull << Nq) - 1ull;   // later bits: nothing
   r.bits = rows[i] & used;
   r.pos = len + dec_popc(r.bits) - 1;
-  if (win < kDwMaxTree) {
+  if (win <= kDwMaxTree) {   // positions lie up to 64 apart (a row of 0, one of 64 marks)
     // drop drafted tokens that lie before the row's window and are no sinks
     unsigned long long in = 0;
     for (int j = 0; j < Nq; ++j) {
