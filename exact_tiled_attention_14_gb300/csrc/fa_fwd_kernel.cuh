@@ -169,12 +169,16 @@ struct FwdParams {
   int win;
   int sinks;
   int Hk;
-  // Order of a unit's tiles (see Unit): the first window's tile before the
-  // sinks at d = 128 (B1 H32/8 N16384 window 2048, 64 sinks: 383 us against 404
-  // with the sinks first), after them at d = 64 (B4 H16/4 N4096 window 1024, 33
-  // sinks: 90 us against 95 with them second).
+  // Order of a unit's tiles (see Unit), win_gap_first(D) of the variant; the
+  // launch writes it (win_launch_params), no caller does.
   int gap_first;
 };
+
+// Order of a windowed unit's tiles at head width d: the first window's tile
+// before the sinks at d = 128 (B1 H32/8 N16384 window 2048, 64 sinks: 383 us
+// against 404 with the sinks first), after them at d = 64 (B4 H16/4 N4096 window
+// 1024, 33 sinks: 90 us against 95 with them second).
+__host__ __device__ constexpr bool win_gap_first(int d) { return d == 128; }
 
 // ---------------------------------------------------------------- tracing
 // Builds compiled with -DFA_TRACE record timestamped events of each role of
@@ -340,7 +344,7 @@ struct Piece {
 
 // Key tile at position j of a piece's list (kWin), whether query tile w
 // computes it, and the list position of query tile w's j-th tile.
-// gap_first as in FwdParams.
+// gap_first: win_gap_first of the head width.
 __host__ __device__ __forceinline__ int win_tile(const Piece& u, int j, bool gap_first) {
   const int i = gap_first && u.gap == 0 ? j - 1 : j;   // from the first sink tile on
   if (gap_first && i < 0) return u.wa;
@@ -373,7 +377,7 @@ __host__ __device__ __forceinline__ int win_next_cut(const Piece& u, int from, i
 // List position of the only sink tile if, of its keys that any row sees, there
 // are only sinks, in its first kNarrow keys; -1 otherwise.  Such a tile is
 // worked on at that width: products with kNarrow keys, and a fourth of the
-// exponentials (16 sinks instead of 64 at d = 128, sizes as at gap_first: 370
+// exponentials (16 sinks instead of 64 at d = 128, sizes as at win_gap_first: 370
 // us against 383; 4 instead of 33 at d = 64: 84 against 90).
 constexpr int kNarrow = 32;
 __host__ __device__ __forceinline__ int win_narrow(const Piece& u, int sinks, bool gap_first) {
@@ -620,7 +624,7 @@ template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool k
 __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using L = Smem<D, kDrop, kWin>;
-  constexpr bool kGapFirst = D == 128;         // kWin: as in the parameters
+  constexpr bool kGapFirst = win_gap_first(D);   // kWin
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw_base + 1023u) & ~1023u;

@@ -10,6 +10,14 @@
 
 namespace fa {
 
+// The parameters of a windowed launch at width D: the order of its units'
+// tiles, which decode_unit reads from them, is the kernel's own.
+template <int D>
+FwdParams win_launch_params(FwdParams p) {
+  p.gap_first = win_gap_first(D);
+  return p;
+}
+
 // Launch fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin> with `grid` persistent CTAs.
 template <int D, bool kBf16, bool kCausal, bool kSplit, bool kKv = false, bool kDrop = false,
           bool kWin = false>
@@ -25,8 +33,12 @@ cudaError_t launch_variant(const FwdParams& p, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
-  fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin>
-      <<<grid, threads_of<D, kDrop>(), Smem<D, kDrop, kWin>::kAlloc, stream>>>(p);
+  auto kernel = fa_fwd_kernel<D, kBf16, kCausal, kSplit, kKv, kDrop, kWin>;
+  constexpr int kThreads = threads_of<D, kDrop>(), kAlloc = Smem<D, kDrop, kWin>::kAlloc;
+  if constexpr (kWin)
+    kernel<<<grid, kThreads, kAlloc, stream>>>(win_launch_params<D>(p));
+  else
+    kernel<<<grid, kThreads, kAlloc, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -132,7 +132,6 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
   set_dropout(&p, 256, 0, 0);
   // a window or sink count past every length hides nothing more
   p.win = std::min(window, std::max(Nq, Nk) + 1);
-  p.gap_first = d == 128;
   p.sinks = std::min(sinks, Nk);
   p.Hk = Hk;
   const int grid = p.num_units < info->sms ? p.num_units : info->sms;
