@@ -70,7 +70,7 @@ cudaError_t launch_variant(const DecWinParams& p, cudaStream_t stream) {
 }
 
 constexpr long long kMaxCount = 1ll << 30;
-constexpr long long kMaxRowTiles = 1ll << 31;
+constexpr long long kMaxRowTiles = (1ll << 31) - 1;
 
 // Sizes and widths, in the documented order.
 int check_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int max_q) {

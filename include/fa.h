@@ -643,9 +643,9 @@ int fa_bwd_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, in
  * A token that sees no key (Nq > len_b) gets O = 0 and LSE = -inf.  Results
  * do not depend on the order CTAs run in.
  * Errors: FA_ERR_SHAPE (also for H not a multiple of Hk, Nq outside 1 .. 16,
- * Nk or B * H * Nq over 2^30, B * H * Nq * (Nk / 128 + 2) over 2^31), FA_ERR_UNSUPPORTED_D, FA_ERR_SHAPE for
- * window < 1 or sinks < 0, FA_ERR_DTYPE, FA_ERR_SCALE, then B * H == 0
- * returns FA_OK, then FA_ERR_NULLPTR, FA_ERR_ALIGN, FA_ERR_DEVICE,
+ * Nk or B * H * Nq over 2^30, B * H * Nq * (ceil(Nk / 128) + 1) not below
+ * 2^31), FA_ERR_UNSUPPORTED_D, FA_ERR_SHAPE for window < 1 or sinks < 0,
+ * FA_ERR_DTYPE, FA_ERR_SCALE, then B * H == 0 returns FA_OK, then FA_ERR_NULLPTR, FA_ERR_ALIGN, FA_ERR_DEVICE,
  * FA_ERR_WORKSPACE, FA_ERR_TENSORMAP, FA_ERR_LAUNCH.
  */
 int fa_decode_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
