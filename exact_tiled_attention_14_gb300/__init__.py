@@ -1183,9 +1183,12 @@ def _current(stream, q):
 # the library directly.  They only route tensors to the C ABI; what is saved
 # for backward is what the pages say a backward pass keeps (Q, K, V, O and
 # the row statistics LSE, plus the dropout generator's seed and offset).
+# LSE carries no gradient, and gradients are of first order only: a second
+# differentiation through them raises.
 
 def _autograd():
     import torch
+    from torch.autograd.function import once_differentiable
 
     class _FlashAttention(torch.autograd.Function):
         @staticmethod
@@ -1202,6 +1205,7 @@ def _autograd():
             return o, lse
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, do, _dlse):
             q, k, v, o, lse = ctx.saved_tensors
             causal, scale, dropout_p, seed, offset = ctx.args
@@ -1225,6 +1229,7 @@ def _autograd():
             return o, lse
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, do, _dlse):
             q, k, v, o, lse = ctx.saved_tensors
             causal, seqlens_k, scale, dropout_p, seed, offset = ctx.args
@@ -1247,6 +1252,7 @@ def _autograd():
             return o, lse
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, do, _dlse):
             q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
             max_q, max_k, causal, scale, dropout_p, seed, offset = ctx.args
@@ -1267,6 +1273,7 @@ def _autograd():
             return o, lse
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, do, _dlse):
             q, k, v, o, lse, seqlens_k = ctx.saved_tensors
             window, sinks, causal, scale = ctx.args
