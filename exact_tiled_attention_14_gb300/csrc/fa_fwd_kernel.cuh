@@ -283,18 +283,23 @@ struct Smem {
   static constexpr int kMask = kP + (OwnP<D>::kSmem ? 2 * kBM * kBN * 2 : 0);  // mask rings
   static constexpr int kBar = kMask + (kGen ? 2 * kMaskStages * kMaskBytes : 0);
   // barrier indices (the mask barriers, [query tile][stage], only with the generator)
-  // A ring slot has a full barrier for its K tiles, which the S issuer waits
-  // for, and one for its V tiles, which the P V issuer waits for.  A wait by
+  // Full barriers.  K tiles are waited for by the S issuer, V tiles by the P V
+  // issuer, and each barrier has one of them as its only consumer: a wait by
   // parity is only sound while the barrier is at most one phase behind the
-  // waiting thread: on a barrier of both, polling use u of a slot while the
+  // waiting thread.  On a barrier of both, polling use u of a slot while the
   // other issuer's use u - 1 is still in flight would pass on the parity of
   // use u - 2, and the product would read a slot that a copy is being written
-  // to.  A slot's previous use can be the other issuer's in a ring of any depth
-  // (two stages: V_0 after K_0; three: V_j after K_j; two to eight: the K
-  // tiles at a unit's start after the V tiles at the previous one's end), and
-  // no order of the issuers' waits covers them all.
+  // to (in one ring a slot's previous use can be the other issuer's at any
+  // depth: the K tiles at a unit's start after the V tiles at the previous
+  // one's end, with two and three stages V_j after K_j, and no order of the
+  // issuers' waits covers them all).  An even number of stages is two rings,
+  // the first half of the slots for K and the second for V; with three a slot
+  // takes both and has a full barrier for each.
+  static constexpr bool kTwoRings = kStages % 2 == 0;
+  static constexpr int kHalf = kStages / 2;          // slots of each of two rings
   static constexpr int bQFull = 0, bQEmpty = kQBufs, bKFull = 2 * kQBufs,
-                       bVFull = bKFull + kStages, bKvEmpty = bVFull + kStages,
+                       bVFull = bKFull + (kTwoRings ? kHalf : kStages),
+                       bKvEmpty = bVFull + (kTwoRings ? kHalf : kStages),
                        bSFull = bKvEmpty + kStages, bPFull = bSFull + 2,
                        bOFree = bPFull + 2, bSFree = bOFree + 2, bPvDone = bSFree + 2,
                        bFinal = bPvDone + 2, bFinalPv = bFinal + 1, bMaskFull = bFinalPv + 1,
@@ -648,11 +653,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       ptx::mbar_init(bar(L::bQFull + qb), 1);
       ptx::mbar_init(bar(L::bQEmpty + qb), 1);
     }
-    for (int s = 0; s < L::kStages; ++s) {
-      ptx::mbar_init(bar(L::bKFull + s), 1);
-      ptx::mbar_init(bar(L::bVFull + s), 1);
-      ptx::mbar_init(bar(L::bKvEmpty + s), 1);
-    }
+    for (int i = L::bKFull; i < L::bKvEmpty + L::kStages; ++i) ptx::mbar_init(bar(i), 1);
     for (int w = 0; w < 2; ++w) {
       ptx::mbar_init(bar(L::bSFull + w), 1);
       ptx::mbar_init(bar(L::bPFull + w), 128);
@@ -733,9 +734,8 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
     // ============================================================ TMA producer
     if (lane == 0) {
       uint32_t tr = 0;          // trace events recorded
-      uint32_t loads = 0;       // K/V tiles issued (ring position)
-      uint32_t k_odd = 0, v_odd = 0;     // per slot: parity of the K / V tiles issued into it
-      uint32_t k_used = 0, v_used = 0;   // per slot: any K / V tile issued
+      uint32_t kv_loads[2] = {0, 0};     // K and V tiles issued
+      uint32_t kv_odd[2] = {0, 0};       // three stages, per slot: parity of the K / V tiles issued
       uint32_t q_issued = 0;    // units whose Q load was issued
       uint32_t k_units = 0;     // pieces walked
       bool alive = true;
@@ -772,16 +772,18 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
         };
         const int kvh = kWin ? kv_head(p, u.bh) : 0;   // divisions once a unit
         auto load_kv = [&](int kv, int j) {
-          const uint32_t slot = loads % L::kStages, use = loads / L::kStages;
+          const uint32_t n = L::kTwoRings ? kv_loads[kv] : kv_loads[0] + kv_loads[1];
+          constexpr uint32_t kSlots = L::kTwoRings ? L::kHalf : L::kStages;
+          const uint32_t at = n % kSlots, use = n / kSlots;   // place in its ring
+          const uint32_t slot = L::kTwoRings && kv ? L::kHalf + at : at;
           if (use > 0)
             alive = ptx::wait_bounded(bar(L::bKvEmpty + slot), (use - 1) & 1, wd, kSiteKvEmpty) &&
                     alive;
           if (alive) {
             // kKv: only the chunks of the tensor's own width (d for K, dv for V)
             const int nc = kKv && !kWin ? (kv ? p.dv : p.dqk) / 64 : L::kChunks;
-            const uint32_t full = bar((kv ? L::bVFull : L::bKFull) + slot);
-            (kv ? v_odd : k_odd) ^= 1u << slot;
-            (kv ? v_used : k_used) |= 1u << slot;
+            const uint32_t full = bar((kv ? L::bVFull : L::bKFull) + at);
+            if (!L::kTwoRings) kv_odd[kv] ^= 1u << at;
             ptx::mbar_arrive_expect_tx(full, nc * L::kChunkBytes);
             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
             int y = (u.kb + j) * kBN, z = u.bh;              // row, batch*head
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
               ptx::tma_load_3d(sbase + L::kKV + slot * L::kTile + c * L::kChunkBytes, tm, full,
                                c * 64, y, z);
             trace_event(p, 3, tr, kv ? kEvLoadV : kEvLoadK, j);
-            ++loads;
+            ++kv_loads[kv];
           }
         };
         // The ring is filled in the order the two MMA issuers need the tiles:
@@ -806,11 +808,17 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       }
       // Drain: make sure every issued copy has landed before the CTA can exit.
       const unsigned long long drain = 200000000ull;   // cycles (~0.1 s)
-      for (int s = 0; s < L::kStages; ++s) {
-        if ((k_used >> s) & 1u)
-          ptx::wait_drain(bar(L::bKFull + s), ((k_odd >> s) & 1u) ^ 1u, drain);
-        if ((v_used >> s) & 1u)
-          ptx::wait_drain(bar(L::bVFull + s), ((v_odd >> s) & 1u) ^ 1u, drain);
+      for (int kv = 0; kv < 2; ++kv) {
+        const int full = kv ? L::bVFull : L::bKFull;
+        if constexpr (L::kTwoRings) {
+          const uint32_t n = kv_loads[kv];
+          for (uint32_t l = n > (uint32_t)L::kHalf ? n - L::kHalf : 0; l < n; ++l)
+            ptx::wait_drain(bar(full + l % L::kHalf), (l / L::kHalf) & 1, drain);
+        } else {
+          // the last use of each slot's barrier (one without any passes)
+          for (int s = 0; s < L::kStages; ++s)
+            ptx::wait_drain(bar(full + s), ((kv_odd[kv] >> s) & 1u) ^ 1u, drain);
+        }
       }
       for (uint32_t q = q_issued > (uint32_t)L::kQBufs ? q_issued - L::kQBufs : 0; q < q_issued; ++q)
         ptx::wait_drain(bar(L::bQFull + q % L::kQBufs), (q / L::kQBufs) & 1, drain);
@@ -940,20 +948,30 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
       };
       // The producer fills the ring with K0 K1 V0 K2 V1 ... K_{n-1} V_{n-2}
       // V_{n-1} for a piece of n key tiles: 2n loads from ring position
-      // `base`; each issuer waits only for the tiles it reads, on its own full
-      // barrier of the slot (odd: per slot, parity of its tiles so far).
-      // (`full` is a constant in each role's loop: picked by the warp's index
-      // instead, it cost 10 % at d = 64, B16 H16 N1024 80.0 us against 72.7.)
-      uint32_t odd = 0;
-      auto ring_wait = [&](uint32_t pos, int full) -> uint32_t {
-        const uint32_t sl = pos % L::kStages;
+      // `base` (two rings: n K tiles and n V tiles); each issuer waits only for
+      // the tiles it reads, tile j of its kind here.  `kv` is a constant in
+      // each role's loop: barriers picked by the warp's index instead cost 10 %
+      // at d = 64 (B16 H16 N1024 80.0 us against 72.7).
+      uint32_t odd = 0;   // three stages, per slot: parity of this issuer's tiles so far
+      auto ring_wait = [&](int kv, uint32_t base, int j, int nkv) -> uint32_t {
+        uint32_t at, parity;
+        if constexpr (L::kTwoRings) {
+          const uint32_t n = base / 2u + j;
+          at = n % L::kHalf;
+          parity = (n / L::kHalf) & 1u;
+        } else {
+          at = (base + (kv ? (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u) : (j == 0 ? 0u : 2u * j - 1u))) %
+               L::kStages;
+          parity = (odd >> at) & 1u;
+          odd ^= 1u << at;
+        }
         pf.lap(6);
-        alive = warp_ok(ptx::wait_bounded(bar(full + sl), (odd >> sl) & 1u, wd, kSiteKvFull)) &&
+        alive = warp_ok(ptx::wait_bounded(bar((kv ? L::bVFull : L::bKFull) + at), parity, wd,
+                                          kSiteKvFull)) &&
                 alive;
-        odd ^= 1u << sl;
         pf.lap(0);
         ptx::tc_fence_after();
-        return sl;
+        return L::kTwoRings && kv ? L::kHalf + at : at;
       };
       uint32_t base = 0;
       if (warp == kMmaWarp) {
@@ -971,7 +989,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           pf.lap(2);
           ptx::tc_fence_after();
           for (int j = 0; j < nkv; ++j) {
-            const uint32_t kslot = ring_wait(base + (j == 0 ? 0u : 2u * j - 1u), L::bKFull);
+            const uint32_t kslot = ring_wait(0, base, j, nkv);
             if constexpr (kWin) {
               const bool narrow = j == win_narrow(u, p.sinks, kGapFirst);
               if (win_active(u, 0, j)) issue_s_own(0, kslot, narrow);
@@ -995,8 +1013,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           const int nkv = max(u.n0, u.n1);
           if (kKv && nkv == 0) continue;
           for (int j = 0; j < nkv; ++j) {
-            const uint32_t vslot =
-                ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u), L::bVFull);
+            const uint32_t vslot = ring_wait(1, base, j, nkv);
             const uint32_t v_lo = v_lo0 + vslot * kSlotLo;
             if (j < u.n0) issue_pv_own(0, j, v_lo);
             if (j < u.n1) issue_pv_own(1, j, v_lo);
@@ -1022,8 +1039,7 @@ __global__ void __launch_bounds__(threads_of<D, kDrop>(), 1)
           int it0 = 0, it1 = 0;            // key tiles of query tile 0 / 1 issued
           int cut = ptx::warp_same(win_next_cut(u, 0, p.sinks, kGapFirst));
           for (int j = 0; j < nkv; ++j) {
-            const uint32_t vslot =
-                ring_wait(base + (j + 1 < nkv ? 2u * j + 2u : 2u * nkv - 1u), L::bVFull);
+            const uint32_t vslot = ring_wait(1, base, j, nkv);
             const bool narrow = j == win_narrow(u, p.sinks, kGapFirst);
             if (j == cut) {
               const int key0 = win_tile(u, j, kGapFirst) * kBN;

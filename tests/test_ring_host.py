@@ -5,7 +5,7 @@ use u - 1 on the same barrier is still in flight (its parity is that of use
 u - 2).  It is sound only if use u - 1 is known to be over when the wait
 begins, whatever time each load, product and softmax step takes.  The test
 reads each variant's ring from the header (stages, query buffers, whether K
-and V tiles of a slot share a full barrier), writes the kernel's roles down
+and V tiles take rings of their own or share slots), writes the kernel's roles down
 as a graph of what must come before what, and asks of every ring wait
 whether the landing of the barrier's previous use comes before it.
 """
@@ -26,8 +26,8 @@ PROGRAM = r'''
 template <int D, bool kDrop, bool kWin>
 void show() {
   using L = fa::Smem<D, kDrop, kWin>;
-  std::printf("%d %d %d %d %d %d\n", D, kDrop, kWin, L::kStages, L::kQBufs,
-              L::bVFull - L::bKFull);
+  std::printf("%d %d %d %d %d %d %d %d\n", D, kDrop, kWin, L::kStages, L::kQBufs, L::kTwoRings,
+              L::bVFull - L::bKFull, L::bKvEmpty - L::bVFull);
 }
 int main() {
   show<64, false, false>(); show<64, true, false>(); show<64, false, true>();
@@ -55,10 +55,12 @@ def rings(tmp_path_factory):
     return {r[:3]: r[3:] for r in rows}
 
 
-def unsound_waits(pieces, stages, q_bufs, apart):
+def unsound_waits(pieces, stages, q_bufs, form):
     """Ring waits of one CTA that may pass early, as (kind, piece, key tile).
-    pieces: the two query tiles' numbers of key tiles, piece by piece;
-    apart: whether K and V tiles of a slot have a full barrier each."""
+    pieces: the two query tiles' numbers of key tiles, piece by piece; form:
+    "shared" (one ring, one full barrier a slot), "apart" (one ring, a full
+    barrier a slot for K and one for V) or "two" (half of the slots a ring for
+    K, half for V)."""
     before, last = {}, {}
 
     def after(node, *earlier):
@@ -76,9 +78,19 @@ def unsound_waits(pieces, stages, q_bufs, apart):
             if j + 1 < max(nn):
                 tiles.append(("K", k, j + 1))
             tiles.append(("V", k, j))
-    slot_use = {t: i for i, t in enumerate(tiles)}
-    for i, t in enumerate(tiles):
-        step("load", ("issue", t), ("free", tiles[i - stages]) if i >= stages else None)
+    rings = ([[t for t in tiles if t[0] == kind] for kind in "KV"] if form == "two" else [tiles])
+    depth = stages // len(rings)
+    ring_of = {t: ring for ring in rings for t in ring}
+    slot_use = {t: i for ring in rings for i, t in enumerate(ring)}
+
+    def previous(t, same_kind=False):    # the tile that had t's slot (and barrier) before it
+        i = slot_use[t] - depth
+        while same_kind and i >= 0 and ring_of[t][i][0] != t[0]:
+            i -= depth
+        return ring_of[t][i] if i >= 0 else None
+
+    for t in tiles:
+        step("load", ("issue", t), ("free", previous(t)) if previous(t) else None)
         after(("landed", t), ("issue", t))
         if t[0] == "K" and t[2] == 0:
             step("load", ("issue q", t[1]), ("free q", t[1] - q_bufs) if t[1] >= q_bufs else None)
@@ -135,10 +147,8 @@ def unsound_waits(pieces, stages, q_bufs, apart):
 
     bad = []
     for t in waits:
-        i = slot_use[t] - stages
-        while apart and i >= 0 and tiles[i][0] != t[0]:
-            i -= stages                  # the previous use of this barrier
-        if i >= 0 and not comes_before(("landed", tiles[i]), ("wait", t)):
+        use = previous(t, same_kind=form == "apart")
+        if use and not comes_before(("landed", use), ("wait", t)):
             bad.append(t)
     return bad
 
@@ -147,15 +157,17 @@ def test_the_model_finds_shared_barriers_unsound():
     # V_0 is the second use of slot 0 in a ring of two; with three stages V_1
     # follows K_1, with eight K_3 may follow a V that only the other query
     # tile's products wait for
-    assert ("V", 0, 0) in unsound_waits([(2, 2)], 2, 1, False)
-    assert ("V", 0, 1) in unsound_waits([(4, 4)], 3, 1, False)
-    assert unsound_waits([(2, 0), (1, 0), (0, 4)], 8, 2, False) == [("K", 2, 3)]
+    assert ("V", 0, 0) in unsound_waits([(2, 2)], 2, 1, "shared")
+    assert ("V", 0, 1) in unsound_waits([(4, 4)], 3, 1, "shared")
+    assert unsound_waits([(2, 0), (1, 0), (0, 4)], 8, 2, "shared") == [("K", 2, 3)]
 
 
 @pytest.mark.parametrize("variant", VARIANTS)
 def test_no_ring_wait_passes_early(rings, variant):
-    stages, q_bufs, gap = rings[variant]
-    assert gap in (0, stages)
+    stages, q_bufs, two, k_bars, v_bars = rings[variant]
+    form = "two" if two else ("apart" if k_bars else "shared")
+    # a barrier a slot of each ring, or two a slot
+    assert (k_bars, v_bars) == ((stages // 2, stages // 2) if two else (stages, stages))
     rng = random.Random(5)
     lengths = (1, 1, 2, 3, 4, 5, 6, 9)
     for _ in range(400):
@@ -163,4 +175,4 @@ def test_no_ring_wait_passes_early(rings, variant):
         for _ in range(rng.randint(1, 5)):
             n, m = rng.choice(lengths), rng.choice(lengths)
             pieces.append(rng.choice(((n, n), (n, n + 1), (n, 0), (0, n), (n + 1, n), (n, m))))
-        assert unsound_waits(pieces, stages, q_bufs, gap > 0) == [], pieces
+        assert unsound_waits(pieces, stages, q_bufs, form) == [], pieces
