@@ -29,21 +29,23 @@
 // holds the other trade: five tile GEMMs per pair, dQ summed in fp32 by the
 // TMA engine in no fixed order.
 //
-// CTA layout (both tensor-core kernels): warps 0-7 do the element-wise
-// work, warp w on TMEM lanes 32*(w%4) .. +31 (key rows in dkdv, query rows
-// in dq) and on column half w/4 of each 128-column tile, so a row's 128
-// scores are shared by two threads; warp 8 issues the tcgen05 MMAs from one
-// thread; warp 9 issues the TMA loads from one thread.  TMEM: S (or S^T) in
-// columns 0-127, dP (dP^T) in 128-255, the fp32 accumulators from 256.  The
-// streamed operands come through two rings: ring A holds the operand the
-// last product of a tile still reads (Q_i in dkdv, K_j in dq), ring B the
-// other one (dO_i, V_j), so B's slots free up earlier.
+// CTA layout (both tensor-core passes; the sliding-window variants' is
+// below): warps 0-7 do the element-wise work, warp w on TMEM lanes 32*(w%4)
+// .. +31 (key rows in dkdv, query rows in dq) and on column half w/4 of each
+// 128-column tile, so a row's 128 scores are shared by two threads; warp 8
+// issues the tcgen05 MMAs from one thread; warp 9 issues the TMA loads from
+// one thread.  TMEM: S (or S^T) in columns 0-127, dP (dP^T) in 128-255, the
+// fp32 accumulators from 256.  The streamed operands come through two rings:
+// ring A holds the operand the last product of a tile still reads (Q_i in
+// dkdv, K_j in dq), ring B the other one (dO_i, V_j), so B's slots free up
+// earlier.
 //
 // Overlap.  The tensor core is kept busy while the element-wise warps work:
 //   dkdv  the element-wise pass runs in two phases.  Phase 1 turns S^T_i into
 //         P^T_i and writes it, 16-bit, over the S^T columns the same warp has
-//         just read (columns 0-31 and 64-95); phase 2 does the same with
-//         dP^T_i and dS^T_i (columns 128-159 and 192-223).  The MMA thread
+//         just read (the first half of each group's columns: 0-31 and
+//         64-95); phase 2 does the same with dP^T_i and dS^T_i (columns
+//         128-159 and 192-223).  The MMA thread
 //         issues dV_j += P^T_i dO_i as soon as phase 1 is done, then S^T_{i+1},
 //         then dK_j += dS^T_i Q_i once phase 2 is done, then dP^T_{i+1}: each
 //         product that overwrites a 16-bit operand follows the one that reads
@@ -57,14 +59,16 @@
 // with j > p - win or j < sinks; H query heads share Hk key/value heads)
 // walk only the tile pairs that hold a visible (query, key): a dQ item the
 // sink tiles and the tiles of its rows' windows, a dK/dV item the query
-// tiles of every head of its group that see the key tile.  Sixteen warps do
-// the element-wise work there (four column groups of 32; 8 warps measured 353
-// us where 16 take 339, B4 H16/4 N4096 d64 window 1024, and the same at
-// d = 128), and the whole MMA warp walks the steps with one elected lane
+// tiles of every head of its group that see the key tile.  There warps 0-15 do
+// the element-wise work (four column groups of 32, so P^T and dS^T sit in four
+// blocks of 16 columns, 32 apart; 8 warps measured 353 us where 16 take 339,
+// B4 H16/4 N4096 d64 window 1024, and the same at d = 128), warp 16 issues and
+// warp 17 loads.  The whole MMA warp walks the steps with one elected lane
 // issuing, so that descriptors and conditions stay in uniform registers: with
-// lane 0 walking alone the issue of a step's 16 to 32 products outlasted
-// them (400 us; d = 128, B1 H32/8 N16384 window 2048 64 sinks: 1520, now 1400,
-// 947 TFLOP/s of the visible pairs).  What bounds it: at d = 128 the chain S,
+// lane 0 walking alone the issue of a step's 16 to 32 products outlasted them
+// (400 us against 343; d = 128, B1 H32/8 N16384 window 2048 64 sinks: 1520
+// against 1400).  Measured on the present sources: 342 us (441 TFLOP/s of the
+// visible pairs) and 1450 to 1460 us (910).  What bounds it: at d = 128 the chain S,
 // dP, element-wise work of a tile beside 3 or 4 products of about 550 cycles
 // (2400 and 2670 cycles a step), at d = 64 the element-wise work (about 2000
 // of 2300 cycles).  Measured and not kept: an issuing warp for each of S and
@@ -936,7 +940,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
             ptx::wait_bounded(xbar(X::kPReady), it & 1, wd, kSiteBwdPFull));
         ptx::tc_fence_after();
         if (!alive) break;
-        // dV_j += P^T dO_i; P^T sits in TMEM columns 0-31 and 64-95
+        // dV_j += P^T dO_i; P^T sits in the first half of each group's columns of S^T
         if (bwd_elected<kWin>()) {
           issue_tmem_a<W::kGroups>(tDv, tS, do_mn0 + (it % L::kStagesB) * kSlotLo, idesc_dv,
                                    it > 0 ? 1u : 0u);
@@ -952,7 +956,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const BwdParams& p, int blk, uint32
             ptx::wait_bounded(xbar(X::kDsReady), it & 1, wd, kSiteBwdDsReady));
         ptx::tc_fence_after();
         if (!alive) break;
-        // dK_j += dS^T Q_i (scale applied at the end); dS^T in columns 128-159 and 192-223
+        // dK_j += dS^T Q_i (scale applied at the end); dS^T likewise over dP^T
         if (bwd_elected<kWin>()) {
           issue_tmem_a<W::kGroups>(tDk, tDp, q_mn0 + (it % L::kStagesA) * kSlotLo, idesc_dk,
                                    it > 0 ? 1u : 0u);

@@ -46,7 +46,9 @@
 //
 // Measured (key tiles of one unit a CTA, 152 CTAs, inputs larger than L2):
 // d = 128 1.34 us a tile of 64 KB, 7.4 TB/s with what L2 keeps, up to 128
-// rows, and 1.68 at 256 rows; d = 64 0.73 us a tile of 32 KB (6.8 TB/s), and
+// rows, and 1.68 at 256 rows (in short runs; a call of 8 caches of 131k keys
+// repeated for seconds runs into the power cap, 1670 MHz, and takes 1.97 us a
+// tile, 850 us); d = 64 0.73 us a tile of 32 KB (6.8 TB/s), and
 // 1.16 at 256 rows.  A unit costs about 2 us more than its tiles and a call
 // about 7 us.  Up to 128 rows the loads bound the time; at 256 rows the
 // softmax of two row tiles a key tile does, with the two products' chain.
@@ -65,7 +67,7 @@ constexpr int kDwBox = 16;            // rows of the small load box
 // Rows of the other.  With one row tile 64, in which sink tiles and spans'
 // last tiles take fewer copies (16 caches of 2000 keys and 5 sinks, d = 64:
 // 41.4 -> 38.9 us); with two, which wait less for copies than for products,
-// 128 (8 caches of 131k keys, d = 128: 772 us against 891 with 64).
+// 128 (8 caches of 131k keys, d = 128: 13 % less time than with 64 in one run).
 constexpr int dec_big_box(int tiles) { return tiles == 2 ? 128 : 64; }
 constexpr int kDwSWarp = 8, kDwLoadWarp = 9, kDwPvWarp = 10;
 constexpr uint32_t kDwSoftmaxRegs = 208, kDwIssueRegs = 88;
@@ -587,7 +589,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       // ============================================================ S = Q K^T
       // The whole warp walks the tiles and one elected lane issues: conditions,
       // descriptors and addresses then stay in uniform registers (64 rows of
-      // 8 caches of 131k keys, d = 128: 772 us, 836 with lane 0 walking alone).
+      // 8 caches of 131k keys, d = 128: 8 % less time than with lane 0 walking
+      // alone, in one run).
       {
         const uint32_t tmem = ptx::warp_same(tmem_base);
         constexpr uint32_t idesc = ptx::idesc_f16(kDwTile, kDwTile, kBf16 ? 1 : 0, 0);

@@ -23,7 +23,7 @@
 //   warps 0-3  softmax warpgroup 0  -> query tile 0 of the unit (TMEM lanes 0-127)
 //   warps 4-7  softmax warpgroup 1  -> query tile 1 of the unit
 //   warp  8    MMA issuer (one thread): S = Q K^T
-//   warp  9    TMA producer (one thread): Q tiles and a ring of K/V tiles
+//   warp  9    TMA producer (one thread): Q tiles and the rings of K and V tiles
 //   warp  10   MMA issuer (one thread): O += P V
 //   warp  11   idle (it completes the third warpgroup, which lets the issue
 //              warps give their registers to the softmax warpgroups)
@@ -49,10 +49,10 @@
 // (win_active), so a unit of 256 rows costs about (win + 128) / 128 + the
 // sink tiles per query tile whatever the length.  H query heads may share
 // Hk key/value heads.  Measured (bf16; TFLOP/s of the visible pairs): B1 H32/8
-// N32768 d128 window 4096 16 sinks 1365 us (1515), bound by the tensor core
-// and, in tiles cut by a window's ends, by products with masked pairs (33.1
+// N32768 d128 window 4096 16 sinks 1374 to 1403 us (1505 to 1474, at the power
+// cap), bound by the tensor core and, in tiles cut by a window's ends, by products with masked pairs (33.1
 // tiles for 32 tiles' worth of pairs, and one of sinks); B4 H16/4 N4096 d64
-// window 1024 4 sinks 85 us (705), bound by the softmax, 9 tiles and a narrow
+// window 1024 4 sinks 87 us (690), bound by the softmax, 9 tiles and a narrow
 // one for 7.6.
 #pragma once
 

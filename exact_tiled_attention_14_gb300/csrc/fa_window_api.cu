@@ -46,7 +46,8 @@ int check_window_sizes(int B, int H, int Hk, int Nq, int Nk, int d, int causal, 
 // whole tiles, of which 8 of 152 CTAs hold one with half of a CTA's whole
 // share each).  kMaxParts parts in all, four for each of 152 SMs, even the
 // work out and bound the workspace (80 MB at d = 128); more sink tiles than
-// that are dealt whole.
+// that are dealt whole.  (A constant of GB300's 152 SMs, not the device's count:
+// the size call is host-only and answers the same on every machine.)
 constexpr long long kMaxParts = 608;
 struct SinkSplit {
   int tiles = 0, parts = 1;
