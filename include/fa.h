@@ -579,7 +579,10 @@ int fa_decode_workspace_size(int B, int H, int Nq, int Nk, int d, size_t *bytes)
  *   seqlens_k : NULL (len_b = Nk) or B int32 key counts on the device, 4-byte
  *               aligned, clamped to [0, Nk].
  *   d, scale, dtype, stream : as fa_fwd.
- * A row that sees no key gets O = 0 and LSE = -inf.  Keys and values past a
+ * A row that sees no key gets O = 0 and LSE = -inf.  A row that sees a key
+ * whose score is NaN or +inf gets O and LSE = NaN (as in every forward and
+ * decoding entry point here); a score of -inf weighs 0, and a row whose scores
+ * are all -inf counts as one that sees no key.  Keys and values past a
  * batch's count, and those no query of a 256-row block sees, may hold
  * anything (NaN included).  A value that some row of the block sees must be
  * finite for the block's other rows to be, as in every entry point here.
