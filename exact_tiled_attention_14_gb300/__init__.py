@@ -1295,7 +1295,7 @@ def _fns():
 
 
 def flash_attention(q, k, v, causal=False, scale=None, dropout_p=0.0, seed=0, offset=0):
-    """Differentiable O, LSE of exact attention over [B, H, N, d] (fa_fwd, or
+    """O (differentiable, first order) and LSE (no gradient) of exact attention over [B, H, N, d] (fa_fwd, or
     fa_fwd_dropout when dropout_p > 0; the backward through fa_bwd /
     fa_bwd_dropout with the same seed and offset)."""
     if scale is None:
@@ -1306,7 +1306,8 @@ def flash_attention(q, k, v, causal=False, scale=None, dropout_p=0.0, seed=0, of
 
 def flash_attention_kv(q, k, v, causal=None, seqlens_k=None, scale=None, dropout_p=0.0, seed=0,
                        offset=0):
-    """Differentiable O, LSE of queries [B, H, Nq, d] against keys [B, H, Nk, d]
+    """O (differentiable, first order) and LSE (no gradient) of queries
+    [B, H, Nq, d] against keys [B, H, Nk, d]
     and values [B, H, Nk, dv] (fa_fwd_kv / fa_bwd_kv, or their dropout forms
     when dropout_p > 0)."""
     if scale is None:
@@ -1317,7 +1318,8 @@ def flash_attention_kv(q, k, v, causal=None, seqlens_k=None, scale=None, dropout
 
 def flash_attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                            causal=None, scale=None, dropout_p=0.0, seed=0, offset=0):
-    """Differentiable O [total_q, H, dv], LSE [H, total_q] of a packed batch
+    """O [total_q, H, dv] (differentiable, first order) and LSE [H, total_q] (no
+    gradient) of a packed batch
     (fa_fwd_varlen / fa_bwd_varlen, or their dropout forms when dropout_p > 0)."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
@@ -1328,7 +1330,8 @@ def flash_attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, ma
 
 def flash_attention_window(q, k, v, window, sinks=0, causal="bottom_right", seqlens_k=None,
                            scale=None):
-    """Differentiable O, LSE of attention_forward_window (fa_fwd_window /
+    """O (differentiable, first order) and LSE (no gradient) of
+    attention_forward_window (fa_fwd_window /
     fa_bwd_window): q [B, H, Nq, d] on k, v [B, Hk, Nk, d].
 
     To capture forward and backward in a CUDA graph, use leaves that no eager
