@@ -27,6 +27,7 @@ current CUDA stream.  ``attention_backward`` does the same for ``fa_bwd``
 ``flash_attention_window`` wrap the forward and backward entry points in
 torch.autograd functions.
 """
+import collections
 import contextlib
 import ctypes
 import math
@@ -36,6 +37,9 @@ from .build import LIB_PATH, build  # noqa: F401
 
 FA_BF16 = 0
 FA_FP16 = 1
+
+FA_E4M3 = 0
+FA_INT8 = 1
 
 FA_OK = 0
 FA_ERR_NULLPTR = 1
@@ -61,6 +65,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_kv", "fa_fwd_varlen", "fa_fwd_dropout", "fa_bwd_dro
            "fa_decode", "fa_decode_workspace_size",
            "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_workspace_size",
            "fa_decode_window", "fa_decode_tree", "fa_decode_window_workspace_size",
+           "fa_rotary", "fa_cache_append", "fa_cache_read", "fa_decode_paged",
+           "fa_decode_paged_workspace_size",
            "fa_strerror", "fa_status",
            "fa_set_watchdog_ns", "fa_set_unit_group", "fa_watchdog_selftest", "fa_work_tiles",
            "fa_version")
@@ -143,6 +149,18 @@ def load_library(path=None):
     lib.fa_decode_tree.restype = i
     lib.fa_decode_window_workspace_size.argtypes = [i] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.fa_decode_window_workspace_size.restype = i
+    longs, size = ctypes.POINTER(ctypes.c_longlong), ctypes.c_size_t
+    lib.fa_rotary.argtypes = [vp] * 4 + [i] * 5 + [longs, vp, i, f, i, i, vp, vp, i, vp]
+    lib.fa_rotary.restype = i
+    lib.fa_cache_append.argtypes = ([vp] * 2 + [i] * 4 + [longs] + [vp] * 4 + [i, i, vp, i]
+                                    + [vp] * 3 + [i, f, i, vp, i, i, vp])
+    lib.fa_cache_append.restype = i
+    lib.fa_cache_read.argtypes = [vp] * 6 + [i] * 6 + [vp, i, vp, i, i, vp]
+    lib.fa_cache_read.restype = i
+    lib.fa_decode_paged.argtypes = ([vp] * 7 + [i] * 7 + [vp, i, vp, i, i, f, i, i, vp, size, vp])
+    lib.fa_decode_paged.restype = i
+    lib.fa_decode_paged_workspace_size.argtypes = [i] * 7 + [ctypes.POINTER(size)]
+    lib.fa_decode_paged_workspace_size.restype = i
     lib.fa_strerror.argtypes = [i]
     lib.fa_strerror.restype = ctypes.c_char_p
     lib.fa_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
@@ -436,6 +454,66 @@ def fa_decode_window_workspace_size(B, H, Hk, Nq, Nk, d):
                                                           int(Nk), int(d), ctypes.byref(out))
     if code:
         raise FaError(code, "fa_decode_window_workspace_size")
+    return out.value
+
+
+def _longs(values):
+    return (ctypes.c_longlong * len(values))(*values)
+
+
+def fa_rotary(q, k, q_out, k_out, B, H, Hk, N, d, strides, freqs, rot, mscale, interleaved, inverse,
+              positions, seqlens, dtype, stream=None):
+    """Raw C call of the rotation by positions (strides: 12 ints, in elements, or
+    None); returns the code."""
+    return load_library().fa_rotary(
+        _addr(q), _addr(k), _addr(q_out), _addr(k_out), int(B), int(H), int(Hk), int(N), int(d),
+        None if strides is None else _longs(strides), _addr(freqs), int(rot), float(mscale),
+        int(interleaved), int(inverse), _addr(positions), _addr(seqlens), int(dtype),
+        _stream(stream))
+
+
+def fa_cache_append(k, v, B, Hk, T, d, strides, k_cache, v_cache, k_scale, v_scale, pages, page_size,
+                    page_table, pages_per_seq, seqlens, counts, freqs, rot, mscale, interleaved,
+                    positions, dtype, cache_dtype, stream=None):
+    """Raw C call of the append to a paged 8-bit cache (strides: 6 ints, in
+    elements, or None); returns the code."""
+    return load_library().fa_cache_append(
+        _addr(k), _addr(v), int(B), int(Hk), int(T), int(d),
+        None if strides is None else _longs(strides), _addr(k_cache), _addr(v_cache),
+        _addr(k_scale), _addr(v_scale), int(pages), int(page_size), _addr(page_table),
+        int(pages_per_seq), _addr(seqlens), _addr(counts), _addr(freqs), int(rot), float(mscale),
+        int(interleaved), _addr(positions), int(dtype), int(cache_dtype), _stream(stream))
+
+
+def fa_cache_read(k_cache, v_cache, k_scale, v_scale, k, v, B, Hk, N, d, pages, page_size, page_table,
+                  pages_per_seq, seqlens, dtype, cache_dtype, stream=None):
+    """Raw C call that reads a paged 8-bit cache back in 16 bits; returns the code."""
+    return load_library().fa_cache_read(
+        _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(k), _addr(v), int(B),
+        int(Hk), int(N), int(d), int(pages), int(page_size), _addr(page_table), int(pages_per_seq),
+        _addr(seqlens), int(dtype), int(cache_dtype), _stream(stream))
+
+
+def fa_decode_paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, B, H, Hk, Nq, d, pages, page_size,
+                    page_table, pages_per_seq, seqlens, window, sinks, scale, dtype, cache_dtype,
+                    workspace, workspace_bytes, stream=None):
+    """Raw C call of decoding over a paged 8-bit cache; returns the code."""
+    return load_library().fa_decode_paged(
+        _addr(q), _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(o),
+        _addr(lse), int(B), int(H), int(Hk), int(Nq), int(d), int(pages), int(page_size),
+        _addr(page_table), int(pages_per_seq), _addr(seqlens), int(window), int(sinks),
+        float(scale), int(dtype), int(cache_dtype), _addr(workspace), int(workspace_bytes),
+        _stream(stream))
+
+
+def fa_decode_paged_workspace_size(B, H, Hk, Nq, d, page_size, pages_per_seq):
+    """Bytes of the workspace fa_decode_paged needs for this shape."""
+    out = ctypes.c_size_t(0)
+    rc = load_library().fa_decode_paged_workspace_size(
+        int(B), int(H), int(Hk), int(Nq), int(d), int(page_size), int(pages_per_seq),
+        ctypes.byref(out))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_decode_paged_workspace_size")
     return out.value
 
 
@@ -1140,6 +1218,371 @@ def tree_rows(parents):
     return rows[:, :Nq].contiguous()
 
 
+# ---------------------------------------------------------------- rotary positions
+# Rotation of q and k by their positions, between a model's projections and the
+# attention calls.  Inputs may be strided views with whole rows (the slices of a
+# fused projection's output); outputs come in the layout attention reads.
+
+def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_length=None, low=1.0,
+                       high=32.0, device=None):
+    """The frequencies of ``rot // 2`` pairs for the rotary and cache calls: an
+    int64 tensor of turns per position in units of 2^-64, from the angle per
+    position w_j = base ** (-2 j / rot).
+
+    ``scaling`` for contexts longer than the trained ``original_length``:
+    "linear" divides w_j by ``factor`` (positions interpolated), "base" raises
+    the base by factor ** (rot / (rot - 2)) (the slowest pair slows down by the
+    factor, the fastest not at all), "parts" divides the pairs that turn less
+    than ``low`` times over the original length, leaves alone those that turn
+    more than ``high`` times, and blends in between.
+    """
+    import torch
+    if rot < 16 or rot % 16:
+        raise ValueError("rot must be a positive multiple of 16")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    if not (base > 0 and factor > 0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError("base and factor must be finite and positive")
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    w = [base ** (-2.0 * j / rot) for j in range(rot // 2)]
+    if scaling == "linear":
+        w = [x / factor for x in w]
+    if scaling == "parts":
+        if not original_length or not high > low:
+            raise ValueError("scaling 'parts' needs original_length, and low < high")
+        for j, x in enumerate(w):
+            keep = (original_length * x / (2 * math.pi) - low) / (high - low)
+            keep = min(max(keep, 0.0), 1.0)
+            w[j] = x * keep + x / factor * (1.0 - keep)
+    turns = [round(x / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for x in w]
+    return torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64,
+                        device=device)
+
+
+def _check_int32(t, shape, device, name, what):
+    import torch
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous int32 tensor {list(shape)} on the "
+                         "inputs' device")
+
+
+def _check_freqs(freqs, d, device, what):
+    import torch
+    if freqs.dtype != torch.int64 or freqs.dim() != 1 or freqs.device != device \
+            or not freqs.is_contiguous():
+        raise ValueError(f"{what}: freqs must be a contiguous int64 tensor [rot / 2] on the "
+                         "inputs' device (see rotary_frequencies)")
+    rot = 2 * freqs.shape[0]
+    if rot < 16 or rot > d or rot % 16:
+        raise ValueError(f"{what}: {rot} rotated elements are not a multiple of 16 up to {d}")
+    return rot
+
+
+def _rows_differ(t):
+    """Whether no two indices of t name the same element (dense, whole rows)."""
+    need = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride < need:
+            return False
+        need = stride * size
+    return True
+
+
+def _rotary(what, q, k, freqs, positions, seqlens, mscale, interleaved, inverse, out, stream):
+    import torch
+    dtype, device = q.dtype, q.device
+    code = dtype_code(dtype)
+    tensors = [q] if k is None else [q, k]
+    if any(x.dim() != 4 for x in tensors):
+        raise ValueError(f"{what}: q must be [B, H, N, d] and k [B, Hk, N, d]")
+    B, H, N, d = q.shape
+    if k is not None:
+        if k.dtype != dtype:
+            raise TypeError(f"dtypes differ: {dtype}, {k.dtype}")
+        if k.shape[0] != B or k.shape[2:] != q.shape[2:]:
+            raise ValueError(f"{what}: q and k differ in batch, tokens or head width")
+    if not all(x.is_cuda and x.device == device for x in tensors):
+        raise ValueError(f"{what}: q and k must be CUDA tensors of one device")
+    for x in tensors:
+        if x.stride(3) != 1 and x.numel():
+            raise ValueError(f"{what}: a head's elements must be contiguous")
+    if positions is not None and seqlens is not None:
+        raise ValueError(f"{what}: give positions or seqlens, not both")
+    if positions is not None:
+        _check_int32(positions, (B, N), device, "positions", what)
+    if seqlens is not None:
+        _check_int32(seqlens, (B,), device, "seqlens", what)
+    rot = _check_freqs(freqs, d, device, what)
+    if out is not None:
+        out = tuple(out)
+        if len(out) != 2 or (out[1] is None) != (k is None):
+            raise ValueError(f"{what}: out must be a pair like (q, k)")
+        for x, y in zip(tensors, out):
+            if y.shape != x.shape or y.dtype != dtype or y.device != device \
+                    or (y.stride(3) != 1 and y.numel()) or not _rows_differ(y):
+                raise ValueError(f"{what}: out must be like q and k, with rows of its own")
+    with _on(stream, device):
+        if out is None:
+            out = tuple(torch.empty(x.shape, dtype=dtype, device=device) for x in tensors)
+        strides = [0] * 12
+        for i, (x, y) in enumerate(zip(tensors, out)):
+            strides[6 * i:6 * i + 6] = [n if x.shape[j % 3] > 1 else 0 for j, n in
+                                        enumerate(x.stride()[:3] + y.stride()[:3])]
+        rc = load_library().fa_rotary(
+            q.data_ptr(), None if k is None else k.data_ptr(), out[0].data_ptr(),
+            None if k is None else out[1].data_ptr(), B, H, 0 if k is None else k.shape[1], N, d,
+            _longs(strides), freqs.data_ptr(), rot, float(mscale), int(bool(interleaved)), inverse,
+            _addr(positions), _addr(seqlens), code, _current(stream, q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rotary")
+    return out[0], None if k is None else out[1]
+
+
+def rotary_forward(q, k, freqs, positions=None, seqlens=None, mscale=1.0, interleaved=False, out=None,
+                   stream=None):
+    """q [B, H, N, d] and k [B, Hk, N, d] (or None) with the first
+    ``2 * len(freqs)`` elements of each head rotated by their token's position:
+    pair j of a token at position p turns by p times its frequency, times
+    ``mscale``; the other elements are copied.
+
+    q, k: CUDA, one 16-bit dtype, d 64 or 128, rows of d contiguous elements
+    that start at multiples of 16 bytes, any other strides (a packed batch
+    [total, H, d] is ``x.transpose(0, 1)[None]`` with positions [1, total]).
+    ``freqs``: see ``rotary_frequencies``.  Pairs are (j, j + rot / 2), or
+    (2 j, 2 j + 1) when ``interleaved``.  Positions: int32 ``positions``
+    [B, N]; or ``seqlens`` int32 [B], token i sitting at seqlens[b] - N + i
+    (the last tokens of each sequence, as the decoding calls place them); or
+    neither, token i sitting at i.  Returns contiguous tensors, or ``out``, a
+    pair of tensors that may be (q, k) themselves.  Calls ``fa_rotary``.
+    """
+    return _rotary("rotary_forward", q, k, freqs, positions, seqlens, mscale, interleaved, 0, out,
+                   stream)
+
+
+def rotary_backward(dq, dk, freqs, positions=None, seqlens=None, mscale=1.0, interleaved=False,
+                    out=None, stream=None):
+    """The gradients with respect to rotary_forward's q and k, from those with
+    respect to its results: the transposed rotation, by the same arguments."""
+    return _rotary("rotary_backward", dq, dk, freqs, positions, seqlens, mscale, interleaved, 1, out,
+                   stream)
+
+
+# ---------------------------------------------------------------- paged 8-bit cache
+
+class PagedCache(collections.namedtuple("PagedCache", "k v k_scale v_scale")):
+    """One layer's pool of key/value pages: ``k`` and ``v`` [pages, Hk,
+    page_size, d] of 8-bit codes (torch.float8_e4m3fn or torch.int8) and
+    ``k_scale`` and ``v_scale`` [pages, Hk] float32; an element's value is
+    code * scale.  A page table (int32 [B, pages_per_seq]) names the pages of
+    each sequence in order; see ``make_paged_cache``."""
+    __slots__ = ()
+
+
+def make_paged_cache(pages, Hk, page_size, d, dtype=None, device="cuda"):
+    """An empty PagedCache (codes and scales 0).  ``dtype``: torch.float8_e4m3fn
+    (None) or torch.int8; ``page_size`` a multiple of 16 up to 128."""
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    _cache_code(dtype)
+    if page_size < 16 or page_size > 128 or page_size % 16:
+        raise ValueError("page_size must be a multiple of 16 up to 128")
+
+    def codes():
+        return torch.zeros((pages, Hk, page_size, d), dtype=torch.uint8, device=device).view(dtype)
+
+    def scales():
+        return torch.zeros((pages, Hk), dtype=torch.float32, device=device)
+    return PagedCache(codes(), codes(), scales(), scales())
+
+
+def _cache_code(dtype):
+    import torch
+    if dtype == torch.float8_e4m3fn:
+        return FA_E4M3
+    if dtype == torch.int8:
+        return FA_INT8
+    raise TypeError(f"unsupported cache dtype {dtype} (float8_e4m3fn or int8)")
+
+
+def _paged_args(cache, page_table, seqlens, what):
+    """Checks shared by the cache calls; returns (pages, Hk, page_size, d), B,
+    pages_per_seq and the codes' dtype."""
+    import torch
+    k, v, k_scale, v_scale = cache
+    device = k.device
+    code = _cache_code(k.dtype)
+    if v.dtype != k.dtype:
+        raise TypeError(f"dtypes differ: {k.dtype}, {v.dtype}")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError(f"{what}: the cache's k and v must be [pages, Hk, page_size, d]")
+    if not k.is_cuda or v.device != device:
+        raise ValueError(f"{what}: the cache must be CUDA tensors of one device")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError(f"{what}: the cache's k and v must be contiguous")
+    for s in (k_scale, v_scale):
+        if s.dtype != torch.float32 or s.shape != k.shape[:2] or s.device != device \
+                or not s.is_contiguous():
+            raise ValueError(f"{what}: the cache's scales must be contiguous float32 [pages, Hk] on "
+                             "its device")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != device \
+            or not page_table.is_contiguous():
+        raise ValueError(f"{what}: page_table must be a contiguous int32 tensor [B, pages_per_seq] "
+                         "on the cache's device")
+    B, per_seq = page_table.shape
+    _check_int32(seqlens, (B,), device, "seqlens", what)
+    return k.shape, B, per_seq, code
+
+
+def cache_append(k, v, cache, page_table, seqlens, counts=None, freqs=None, positions=None, mscale=1.0,
+                 interleaved=False, stream=None):
+    """Append k, v [B, Hk, T, d] (16-bit, rows of d contiguous elements at
+    multiples of 16 bytes, other strides free) to the sequences of a PagedCache
+    in place, keys rotated first when ``freqs`` is given (see
+    ``rotary_forward``).
+
+    ``seqlens`` (int32 [B]) counts the tokens of each sequence after the call,
+    the last ``counts[b]`` of them (int32 [B]; None: T) new: token i goes to
+    slot seqlens[b] - counts[b] + i, and turns by ``positions[b, i]`` (int32
+    [B, T]) or by its slot.  Slots past the page table's, before 0, or in a page
+    number outside the pool are dropped.  A page and head's scale is set by its
+    largest new element and only grows while it fills; when it does, the codes
+    that the page holds are quantised again (see ``fa_cache_append`` in
+    include/fa.h for the exact rules, NaN and infinities among them).  Pages
+    that the call writes must belong to one sequence each.
+    """
+    what = "cache_append"
+    dtype, device = k.dtype, cache.k.device
+    code = dtype_code(dtype)
+    if v.dtype != dtype:
+        raise TypeError(f"dtypes differ: {dtype}, {v.dtype}")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError(f"{what}: k and v must be [B, Hk, T, d]")
+    (pages, Hk, page_size, d), B, per_seq, cache_code = _paged_args(cache, page_table, seqlens, what)
+    T = k.shape[2]
+    if k.shape != (B, Hk, T, d):
+        raise ValueError(f"{what}: k and v differ from the cache or its table in batch, heads or width")
+    if k.device != device or v.device != device:
+        raise ValueError(f"{what}: k and v must be on the cache's device")
+    if k.numel() and (k.stride(3) != 1 or v.stride(3) != 1):
+        raise ValueError(f"{what}: a head's elements must be contiguous")
+    if counts is not None:
+        _check_int32(counts, (B,), device, "counts", what)
+    if positions is not None:
+        _check_int32(positions, (B, T), device, "positions", what)
+    rot = 0 if freqs is None else _check_freqs(freqs, d, device, what)
+    strides = [n if k.shape[j % 3] > 1 else 0 for j, n in
+               enumerate(k.stride()[:3] + v.stride()[:3])]
+    with _on(stream, device):
+        rc = load_library().fa_cache_append(
+            k.data_ptr(), v.data_ptr(), B, Hk, T, d, _longs(strides), cache.k.data_ptr(),
+            cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), pages, page_size,
+            page_table.data_ptr(), per_seq, seqlens.data_ptr(), _addr(counts), _addr(freqs), rot,
+            float(mscale), int(bool(interleaved)), _addr(positions), code, cache_code,
+            _current(stream, k))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_cache_append")
+
+
+def cache_read(cache, page_table, seqlens, length=None, dtype=None, out=None, stream=None):
+    """k, v [B, Hk, length, d] of the first ``length`` slots (None: the page
+    table's capacity) of each sequence in 16 bits (``dtype``: torch.bfloat16,
+    None, or torch.float16), for ``attention_forward_kv`` or
+    ``attention_forward_window`` over the cache.  Rows from ``seqlens[b]`` on
+    are zeros.  ``out``: a pair of such tensors.  Calls ``fa_cache_read``."""
+    import torch
+    what = "cache_read"
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = dtype_code(dtype)
+    (pages, Hk, page_size, d), B, per_seq, cache_code = _paged_args(cache, page_table, seqlens, what)
+    N = per_seq * page_size if length is None else int(length)
+    if N < 0:
+        raise ValueError(f"{what}: length must not be negative")
+    device = cache.k.device
+    if out is not None:
+        out = tuple(out)
+        if len(out) != 2:
+            raise ValueError(f"{what}: out must be a pair (k, v)")
+        for x in out:
+            _check_buffer(x, (B, Hk, N, d), dtype, device, "out")
+    with _on(stream, device):
+        if out is None:
+            out = tuple(torch.empty((B, Hk, N, d), dtype=dtype, device=device) for _ in range(2))
+        rc = load_library().fa_cache_read(
+            cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+            cache.v_scale.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), B, Hk, N, d, pages,
+            page_size, page_table.data_ptr(), per_seq, seqlens.data_ptr(), code, cache_code,
+            _current(stream, cache.k))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_cache_read")
+    return out
+
+
+def make_paged_workspace(q, cache, page_table):
+    """A workspace (uint8 tensor on q's device) for attention_decode_paged calls
+    with q [B, H, Nq, d].  Calls that may run at the same time, on two streams
+    or in two captured graphs, need one each."""
+    import torch
+    B, H, Nq, d = q.shape
+    with torch.cuda.device(q.device):
+        n = fa_decode_paged_workspace_size(B, H, cache.k.shape[1], Nq, d, cache.k.shape[2],
+                                           page_table.shape[1])
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def attention_decode_paged(q, cache, page_table, seqlens, window=None, sinks=0, scale=None, out=None,
+                           lse=None, workspace=None, stream=None):
+    """O, LSE of the last Nq (1 .. 16) tokens of each sequence, q [B, H, Nq, d]
+    (16-bit, contiguous), against its pages of a PagedCache with Hk heads, H a
+    multiple of Hk, under attention_forward_window's mask (``window`` None: no
+    limit).
+
+    ``seqlens`` (int32 [B]) counts each sequence's tokens, the new ones (whose
+    keys and values ``cache_append`` has put there) among them: token i sits at
+    position seqlens[b] - Nq + i.  A token that sees no key gets O = 0 and
+    LSE = -inf.  ``workspace``: see ``make_paged_workspace``; None allocates
+    one.  Calls ``fa_decode_paged``.
+    """
+    import torch
+    what = "attention_decode_paged"
+    dtype, device = q.dtype, q.device
+    code = dtype_code(dtype)
+    (pages, Hk, page_size, d), B, per_seq, cache_code = _paged_args(cache, page_table, seqlens, what)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
+        raise ValueError(f"{what}: q must be [B, H, Nq, d] with the page table's B and the cache's d")
+    _, H, Nq, _ = q.shape
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"{what}: {H} query heads are not a multiple of {Hk} key/value heads")
+    if window is not None and window < 1:
+        raise ValueError(f"{what}: window must be at least 1")
+    if sinks < 0:
+        raise ValueError(f"{what}: sinks must not be negative")
+    if device != cache.k.device or not q.is_contiguous():
+        raise ValueError(f"{what}: q must be contiguous, on the cache's device")
+    if out is not None:
+        _check_buffer(out, q.shape, dtype, device, "out")
+    if lse is not None:
+        _check_buffer(lse, (B, H, Nq), torch.float32, device, "lse")
+    with _on(stream, device):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=device)
+        if workspace is None:
+            workspace = make_paged_workspace(q, cache, page_table)
+        ws, ws_bytes = _workspace_arg(workspace, device)
+        rc = load_library().fa_decode_paged(
+            q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+            cache.v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hk, Nq, d, pages,
+            page_size, page_table.data_ptr(), per_seq, seqlens.data_ptr(),
+            0 if window is None else _int32(window), _int32(sinks),
+            d ** -0.5 if scale is None else float(scale), code, cache_code, ws, ws_bytes,
+            _current(stream, q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_decode_paged")
+    return out, lse
+
+
 def _int32(x):
     """A count clamped to int32 (larger windows and sinks hide nothing more)."""
     x = int(x)
@@ -1281,7 +1724,30 @@ def _autograd():
                                           causal=causal, seqlens_k=seqlens_k, scale=scale)
             return g[0], g[1], g[2], None, None, None, None, None
 
-    return _FlashAttention, _FlashAttentionKv, _FlashAttentionVarlen, _FlashAttentionWindow
+    class _Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, freqs, positions, seqlens, mscale, interleaved):
+            ctx.save_for_backward(freqs, positions, seqlens)
+            ctx.args = (mscale, interleaved)
+            return rotary_forward(q, k, freqs, positions, seqlens, mscale, interleaved)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dq, dk):
+            freqs, positions, seqlens = ctx.saved_tensors
+            dq = _whole_rows(dq)
+            dk = None if dk is None else _whole_rows(dk)
+            return (*rotary_backward(dq, dk, freqs, positions, seqlens, *ctx.args), None, None, None,
+                    None, None)
+
+    return (_FlashAttention, _FlashAttentionKv, _FlashAttentionVarlen, _FlashAttentionWindow,
+            _Rotary)
+
+
+def _whole_rows(t):
+    """t, or a contiguous copy where its rows are not contiguous or aligned."""
+    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in t.stride()[:3])
+    return t if ok else t.contiguous()
 
 
 _AUTOGRAD = None
@@ -1342,3 +1808,9 @@ def flash_attention_window(q, k, v, window, sinks=0, causal="bottom_right", seql
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     return _fns()[3].apply(q, k, v, int(window), int(sinks), causal, seqlens_k, float(scale))
+
+
+def rotary_embedding(q, k, freqs, positions=None, seqlens=None, mscale=1.0, interleaved=False):
+    """rotary_forward(q, k, ...), differentiable (first order) in q and k (k may
+    be None); the gradients are rotary_backward's."""
+    return _fns()[4].apply(q, k, freqs, positions, seqlens, float(mscale), bool(interleaved))

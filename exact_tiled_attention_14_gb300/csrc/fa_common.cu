@@ -13,6 +13,7 @@
 #include "fa.h"
 #include "fa_host.cuh"
 #include "fa_launch.cuh"
+#include "fa_paged.cuh"
 
 using namespace fa::host;
 
@@ -168,6 +169,36 @@ bool make_tmap_tokens(CUtensorMap* m, const void* ptr, int H, int tokens, int wi
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_codes(CUtensorMap* m, const void* ptr, long long rows, int width, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t elem_strides[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides,
+                        box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+int check_paged(int B, int Hk, int d, int pages, int page_size, int pages_per_seq,
+                int cache_dtype) {
+  if (B < 0 || Hk < 0 || d <= 0 || pages < 1 || pages_per_seq < 1) return FA_ERR_SHAPE;
+  if (page_size < fa::kPageRows || page_size > fa::kMaxPage || page_size % fa::kPageRows != 0)
+    return FA_ERR_SHAPE;
+  const long long cap = 1ll << 30;
+  if (static_cast<long long>(B) * Hk > cap || static_cast<long long>(B) * pages_per_seq > cap ||
+      static_cast<long long>(pages_per_seq) * page_size > cap ||
+      static_cast<long long>(pages) * page_size > cap ||
+      static_cast<long long>(pages) * page_size * Hk > 2 * cap - 1)   // rows of the pool
+    return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
+  if (cache_dtype != FA_E4M3 && cache_dtype != FA_INT8) return FA_ERR_DTYPE;
+  return FA_OK;
+}
+
 int drop_threshold(float p) {
   if (!(p >= 0.0f) || !(p < 1.0f)) return -1;
   const int t = static_cast<int>(std::floor((1.0 - static_cast<double>(p)) * 256.0 + 0.5));
@@ -179,7 +210,7 @@ int drop_threshold(float p) {
 
 extern "C" {
 
-int fa_version(void) { return 105; }
+int fa_version(void) { return 106; }
 
 const char* fa_strerror(int code) {
   switch (code) {
@@ -187,7 +218,7 @@ const char* fa_strerror(int code) {
     case FA_ERR_NULLPTR: return "a required pointer is NULL";
     case FA_ERR_SHAPE: return "bad shape (negative size, d <= 0, or sizes overflow)";
     case FA_ERR_UNSUPPORTED_D: return "head width d must be 64 or 128";
-    case FA_ERR_DTYPE: return "dtype must be FA_BF16 or FA_FP16";
+    case FA_ERR_DTYPE: return "dtype must be FA_BF16 or FA_FP16 (a cache's FA_E4M3 or FA_INT8)";
     case FA_ERR_ALIGN: return "q/k/v/o must be 16-byte aligned and lse 4-byte aligned";
     case FA_ERR_SCALE: return "scale must be finite and > 0";
     case FA_ERR_DEVICE: return "current device is not a compute capability 10.3 GPU";

@@ -1,0 +1,678 @@
+// fa_decode_paged_kernel.cuh — the last tokens of each sequence against its
+// pages of 8-bit keys and values (see fa_paged.cuh), under a sliding window
+// with sinks or none.
+//
+// For one (batch, key/value head) the G query heads that share it and their
+// Nq tokens are R = G * Nq rows of one problem.  With k_j = ks * a_j and
+// v_j = vs * b_j (codes a, b, scales of the key's page),
+//     s_rj = scale * ks * (q_r . a_j),   O_r = sum_j softmax_j(s_r) vs b_j.
+// Codes are exact in half precision, and so are the queries once each row is
+// multiplied by a power of two that brings its largest element to 2^12 (what
+// falls below 2^-24 then is 2^-36 of the row's largest): the products
+// accumulate exactly what float32 sums of the codes' values do.  The scales
+// stay in float32, that of K on the scores, that of V on each page's product
+// before it joins the output; so weights p in [0, 2^8] are all that is rounded
+// (to 11 bits).
+//
+// Bound.  A key costs 2 d bytes and 4 d R operations: HBM bounds it, an SM's
+// share is 23 bytes a cycle.  The codes have to be turned into 16-bit
+// registers before any tensor-core product, which is most of the issue slots
+// (about 230 instructions for 16 keys of 8 rows at d = 128, which arrive
+// every 174 cycles), and mma.sync takes registers as they are.  tcgen05 would
+// need them written to shared memory or TMEM first, and its 8-bit kinds would
+// need the queries and weights in 8 bits too.
+//
+// Layout.  S^T = K Q^T and O^T += V^T P^T: the 16-row side of m16n8k16 goes
+// to keys (head elements for O), the 8-row side to the query rows, since few
+// rows are the usual case.  The order of a product's contraction is free, so
+// a thread takes 16 bytes of a row at a time (below) without ldmatrix.
+//
+// Split.  A unit is (batch, K/V head, block of 8 kTiles rows); its keys are
+// tiles of kKeys (4 KB of K and of V).  The tiles of all units are laid end to
+// end and cut into equal runs, one per CTA; the warps of a CTA take its tiles
+// in turn, each with a ring of its own that its lanes fill by TMA, and are
+// merged at the end of each unit.  A unit cut by a run's end leaves its parts
+// in the workspace; fa_decode_win_combine_kernel adds them up in the order of
+// the runs.
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "fa_decode_win_kernel.cuh"
+#include "fa_paged.cuh"
+#include "ptx_sm103.cuh"
+
+namespace fa {
+
+constexpr int kDpWarps = 8;
+constexpr int kDpThreads = 32 * kDpWarps;
+constexpr int kDpTileBytes = 4096;       // of K, and of V
+constexpr float kDpTau = 8.0f;           // lazy-rescale threshold, log2 units
+constexpr uint32_t kSiteDpFull = 50;
+__host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
+
+struct DecPagedParams {
+  CUtensorMap tm_k;        // [pages * Hk * page, d] bytes, boxes of box_rows rows
+  CUtensorMap tm_v;
+  DecWinParams out;        // o, lse, parts, run table and sizes, as the combine reads them
+  const void* q;           // [B * Hk, R, d]
+  const float* k_scale;    // [pages, Hk]
+  const float* v_scale;
+  const int* table;        // [B, per_seq]
+  int per_seq, pages, page;
+  int boxes;               // boxes of a tile: 1, or one per 16 keys where pages are no multiples
+                           // of a tile
+};
+
+// Keys that the rows of a batch see, as tiles: the sinks' tiles before the
+// window's first, then tiles from `first` on.  A batch has one tile at least,
+// so that each unit has a writer.
+struct PagedSpan {
+  int len, lo, sink_tiles, first, tiles;
+};
+__host__ __device__ __forceinline__ PagedSpan paged_span(int count, int capacity, int Nq, int win,
+                                                         int sinks, int keys) {
+  PagedSpan s;
+  s.len = count < 0 ? 0 : (count > capacity ? capacity : count);
+  s.lo = s.len - Nq - win + 1;                  // the first token's window
+  if (s.lo < 0) s.lo = 0;
+  s.first = s.lo / keys;
+  const int st = (sinks < s.lo ? sinks : s.lo) + keys - 1;
+  s.sink_tiles = st / keys < s.first ? st / keys : s.first;
+  const int last = (s.len + keys - 1) / keys;
+  s.tiles = s.sink_tiles + (last > s.first ? last - s.first : 0);
+  if (s.tiles < 1) s.tiles = 1;
+  return s;
+}
+// First key of tile t of the list.
+__host__ __device__ __forceinline__ int paged_key0(const PagedSpan& s, int t, int keys) {
+  return (t < s.sink_tiles ? t : s.first + t - s.sink_tiles) * keys;
+}
+// Whether the row at position pos sees some key of [key0, key0 + n).
+__host__ __device__ __forceinline__ bool paged_sees(int key0, int n, int pos, int win, int sinks) {
+  return key0 <= pos && (key0 + n - 1 > pos - win || key0 < sinks);
+}
+
+// Key rows of the 16 of a product.  At d = 128 a row is 128 bytes, its 16-byte
+// chunks permuted by its number (128-byte swizzle); at d = 64 two rows share
+// 128 bytes (64-byte swizzle).  A quarter warp reads K as two rows of four
+// chunks and V as four rows of two chunks; slot order dp_row makes both touch
+// all banks once: at d = 64 slots 2 t and 2 t + 1 are rows of different parity,
+// and slots 0, 2, 4, 6 (1, 3, 5, 7) differ in parity or in the row's bit 2.
+template <int D>
+__host__ __device__ constexpr int dp_row(int slot) {
+  return D == 128 ? slot
+                  : ((slot >> 1 & 1) + (slot >> 2 & 1) * 4) ^ (slot & 1 ? 3 : 0);
+}
+// Byte offset of 16-byte chunk c of row r.
+template <int D>
+__host__ __device__ constexpr uint32_t dp_chunk(int r, int c) {
+  return D == 128 ? r * 128u + ((c ^ (r & 7)) << 4) : r * 64u + ((c ^ (r >> 1 & 3)) << 4);
+}
+
+template <int D, int kTiles>
+struct DpLayout {
+  static constexpr int kRows = 8 * kTiles;
+  static constexpr int kStages = kTiles == 1 ? 3 : 2;
+  static constexpr int kRing = 0;
+  static constexpr int kQ = kRing + kDpWarps * kStages * 2 * kDpTileBytes;
+  static constexpr int kSum = kQ + kRows * D * 2;             // 4 warps' O
+  static constexpr int kMl = kSum + 4 * kRows * D * 4;        // (m, l) [warp][row]
+  static constexpr int kQmul = kMl + kDpWarps * kRows * 8;    // [row]
+  static constexpr int kMeta = kQmul + kRows * 4;             // [warp][stage]: 4 K, 4 V scales
+  static constexpr int kBar = kMeta + kDpWarps * kStages * 32;
+  static constexpr int kMisc = kBar + 8 * kDpWarps * kStages;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* tm, uint32_t bar,
+                                              int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A place in the list of all tiles: batch, unit of the batch, tile of the unit.
+struct DpPlace {
+  int b, unit, tile;
+  PagedSpan s;
+};
+
+template <int D, bool kBf16, bool kInt8, int kTiles>
+__global__ void __launch_bounds__(kDpThreads, 1)
+    fa_decode_paged_kernel(const __grid_constant__ DecPagedParams p) {
+  using L = DpLayout<D, kTiles>;
+  constexpr int kKeys = dp_keys(D);          // of a tile
+  constexpr int kMt = kKeys / 16;            // products' key blocks of a tile
+  constexpr int kJ = D / 16;
+  constexpr int kWords = D / 16;             // 4-byte words of a thread's part of a K row
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = ptx::smem_u32(smem_raw);
+  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+  uint8_t* const sgen = smem_raw + (sbase - raw_base);
+  const int warp = ptx::warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const DecWinParams& po = p.out;
+  const int units = po.Hk * po.row_blocks;   // of a batch
+  const int capacity = p.per_seq * p.page;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc);
+  const ptx::Watchdog wd{po.watchdog_cycles, abort_flag, po.status};
+
+  ptx::griddep_launch_dependents();
+  auto bar = [&](int stage) -> uint32_t { return sbase + L::kBar + 8u * (warp * kStages + stage); };
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(bar(i), 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+
+  auto span_of = [&](int b) {
+    return paged_span(po.seqlens[b], capacity, po.Nq, po.win, po.sinks, kKeys);
+  };
+  // ---- the CTA's run and its first place (each warp for itself)
+  int total = 0;
+  for (int b = lane; b < po.B; b += 32) total += span_of(b).tiles * units;
+  total = __reduce_add_sync(0xffffffffu, total);
+  const DecDeal deal = dec_deal(total, po.grid);
+  const int run = blockIdx.x;
+  int left = 0;
+  DpPlace at{};
+  if (run < deal.runs) {
+    const int start = dec_run_start(deal, run);
+    left = dec_run_start(deal, run + 1) - start;
+    int before = 0;
+    for (int b0 = 0; b0 < po.B; b0 += 32) {
+      const int mine = b0 + lane < po.B ? span_of(b0 + lane).tiles * units : 0;
+      int upto = mine;
+#pragma unroll
+      for (int i = 1; i < 32; i *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane >= i) upto += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > start);
+      if (past != 0) {
+        const int k = __ffs(past) - 1;
+        at.b = b0 + k;
+        at.s = span_of(at.b);
+        const int skip = start - (before + __shfl_sync(0xffffffffu, upto - mine, k));
+        at.unit = skip / at.s.tiles;
+        at.tile = skip - at.unit * at.s.tiles;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  const int n_tiles = left;                  // of the run
+  auto advance = [&](DpPlace& x, int n) {
+    x.tile += n;
+    while (x.tile >= x.s.tiles) {
+      x.tile -= x.s.tiles;
+      if (++x.unit == units) {
+        x.unit = 0;
+        if (++x.b == po.B) {                 // past the last tile
+          x.b = po.B - 1;
+          x.tile = 0;
+          return;
+        }
+        x.s = span_of(x.b);
+      }
+    }
+  };
+
+  // ---- the warp's loads: tile i of the run goes to warp i % kDpWarps
+  const uint32_t ring = sbase + L::kRing + warp * (kStages * 2 * kDpTileBytes);
+  uint8_t* const ring_gen = sgen + L::kRing + warp * (kStages * 2 * kDpTileBytes);
+  const uint32_t meta = sbase + L::kMeta + warp * (kStages * 32);
+  const float* const meta_gen =
+      reinterpret_cast<const float*>(sgen + L::kMeta + warp * (kStages * 32));
+  const int box_rows = kKeys / p.boxes;
+  DpPlace nx = at;                           // the next tile to load
+  int nx_i = warp;                           // its number in the run
+  int nx_page = -1, nx_row = 0;              // page of the lane's box, its first row in the page
+  uint32_t valid = 0;                        // 4 bits per stage: boxes that name a page
+  int loaded = 0;                            // tiles that the warp has asked for
+  auto look = [&]() {                        // the page of the lane's box of tile nx
+    nx_page = -1;
+    if (nx_i < n_tiles && lane < p.boxes) {
+      const int key = paged_key0(nx.s, nx.tile, kKeys) + lane * box_rows;
+      const int nth = key / p.page;
+      nx_row = key - nth * p.page;
+      if (key < nx.s.len) nx_page = p.table[static_cast<size_t>(nx.b) * p.per_seq + nth];
+    }
+  };
+  auto load = [&](int stage) {               // into the stage; then look at the one after
+    if (nx_i < n_tiles) {
+      const int hk = nx.unit / po.row_blocks;
+      const bool ok = nx_page >= 0 && nx_page < p.pages;
+      const uint32_t have = __ballot_sync(0xffffffffu, ok);
+      valid = (valid & ~(15u << (4 * stage))) | have << (4 * stage);
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(bar(stage), __popc(have) * 2 * box_rows * D);
+      __syncwarp();
+      if (ok) {
+        const int head = nx_page * po.Hk + hk;
+        const int row = head * p.page + nx_row;
+        const uint32_t dst = ring + stage * (2 * kDpTileBytes) + lane * box_rows * D;
+        tma_load_rows(dst, &p.tm_k, bar(stage), row);
+        tma_load_rows(dst + kDpTileBytes, &p.tm_v, bar(stage), row);
+        cp_async4(meta + stage * 32 + lane * 4, p.k_scale + head);
+        cp_async4(meta + stage * 32 + 16 + lane * 4, p.v_scale + head);
+      }
+      ++loaded;
+      nx_i += kDpWarps;
+      if (nx_i < n_tiles) advance(nx, kDpWarps);
+      look();
+    }
+    cp_async_commit();                       // one group per tile, empty ones too
+  };
+  if (nx_i < n_tiles) advance(nx, warp);
+  look();
+  for (int i = 0; i < kStages; ++i) load(i);
+
+  // ---- pieces of units, in the order of the run
+  bool alive = true, cut_here = false;
+  int done = 0;                              // tiles of the run before the piece
+  int stage = 0, parity = 0, pieces = 0;
+  int waited = 0;                            // the warp's loads that have arrived
+  int mine = warp;                           // the warp's next tile in the run
+  uint2* const q_s = reinterpret_cast<uint2*>(sgen + L::kQ);
+  float* const qmul_s = reinterpret_cast<float*>(sgen + L::kQmul);
+  float4* const sum_s = reinterpret_cast<float4*>(sgen + L::kSum);
+  float2* const ml_s = reinterpret_cast<float2*>(sgen + L::kMl);
+
+  while (done < n_tiles) {
+    const int tile0 = at.tile;
+    const int n = min(at.s.tiles - tile0, n_tiles - done);
+    const bool whole = tile0 == 0 && n == at.s.tiles;
+    const int hk = at.unit / po.row_blocks, block = at.unit - hk * po.row_blocks;
+    const size_t head = static_cast<size_t>(at.b) * po.Hk + hk;
+    const int row0 = block * po.row_span, rows = min(po.R - row0, po.row_span);
+    const PagedSpan s = at.s;
+
+    // queries of the unit: row r, elements 4 c .. 4 c + 3 as the B operand's
+    // registers of lane (r % 8, 4 c / (D / 4)), in half precision
+    for (int r = warp; r < L::kRows; r += kDpWarps) {
+      uint2 raw = make_uint2(0, 0);
+      if (r < rows && lane * 4 < D)
+        raw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
+                                              (head * po.R + row0 + r) * D + lane * 4);
+      float x[4];
+      ptx::unpack2<kBf16>(raw.x, x[0], x[1]);
+      ptx::unpack2<kBf16>(raw.y, x[2], x[3]);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      top = __reduce_max_sync(0xffffffffu, top);
+      int shift = 0;                         // the row times 2^shift
+      if (top != 0 && top < kInfBits) shift = min(12 - (static_cast<int>(top >> 23) - 127), 120);
+      const float mul = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+      if (lane * 4 < D)
+        q_s[(lane % (D / 16) * kTiles + (r >> 3)) * 32 + (r & 7) * 4 + lane / (D / 16)] =
+            make_uint2(ptx::pack2<false>(x[0] * mul, x[1] * mul),
+                       ptx::pack2<false>(x[2] * mul, x[3] * mul));
+      if (lane == 0)
+        qmul_s[r] = po.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+    }
+    __syncthreads();
+
+    uint2 qf[kTiles <= 2 ? kJ * kTiles : 1];
+    if constexpr (kTiles <= 2) {
+#pragma unroll
+      for (int i = 0; i < kJ * kTiles; ++i) qf[i] = q_s[i * 32 + lane];
+    }
+    float qmul[kTiles][2];
+    int pos[kTiles][2];
+    float m[kTiles][2], l[kTiles][2];
+#pragma unroll
+    for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
+        qmul[nt][e] = qmul_s[r];
+        pos[nt][e] = s.len - po.Nq + (row0 + r) % po.Nq;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+    float o[kJ][kTiles][4] = {};
+    const int pos_lo = s.len - po.Nq, pos_hi = s.len - 1;
+
+    for (; mine < done + n; mine += kDpWarps) {
+      const int key0 = paged_key0(s, tile0 + mine - done, kKeys);
+      alive = ptx::warp_all(alive && ptx::wait_bounded(bar(stage), parity, wd, kSiteDpFull));
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      waited += alive;
+      const uint8_t* const kt = ring_gen + stage * (2 * kDpTileBytes);
+      uint8_t* const vt = ring_gen + stage * (2 * kDpTileBytes) + kDpTileBytes;
+      const float* const sc = meta_gen + stage * 8;
+      const uint32_t have = valid >> (4 * stage) & 15u;
+      // every row sees every key of the tile
+      const bool full = have == (1u << p.boxes) - 1u && key0 + kKeys - 1 <= pos_lo &&
+                        (key0 > pos_hi - po.win || key0 + kKeys <= po.sinks);
+      auto box_of = [&](int mt) { return p.boxes == 1 ? 0 : mt; };
+      if (!full) {
+        // values that no row sees weigh 0, and 0 times what they hold must be 0
+        for (int i = lane; i < kKeys; i += 32) {
+          const int key = key0 + i;
+          const bool seen = (have >> box_of(i >> 4) & 1u) && key <= pos_hi &&
+                            (key > pos_lo - po.win || key < po.sinks);
+          if (!seen)
+            for (int c = 0; c < D / 16; ++c)
+              *reinterpret_cast<uint4*>(vt + i * D + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      }
+
+      // ---- S^T
+      float sv[kMt][kTiles][4] = {};
+      {
+        uint32_t w[kMt][2][kWords];          // rows dp_row(g) and + 8 of each 16
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = mt * 16 + h * 8 + dp_row<D>(g);
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4*>(
+                  kt + dp_chunk<D>(r, t * (kWords / 4) + i));
+              w[mt][h][4 * i] = x.x;
+              w[mt][h][4 * i + 1] = x.y;
+              w[mt][h][4 * i + 2] = x.z;
+              w[mt][h][4 * i + 3] = x.w;
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          uint2 qb[kTiles];
+#pragma unroll
+          for (int nt = 0; nt < kTiles; ++nt) {
+            if constexpr (kTiles <= 2)
+              qb[nt] = qf[j * kTiles + nt];
+            else
+              qb[nt] = q_s[(j * kTiles + nt) * 32 + lane];
+          }
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) {
+            uint32_t a0, a1, a2, a3;
+            codes4<kInt8>(w[mt][0][j], a0, a2);
+            codes4<kInt8>(w[mt][1][j], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
+              mma16816(sv[mt][nt], a0, a1, a2, a3, qb[nt].x, qb[nt].y);
+          }
+        }
+      }
+
+      // ---- scores, weights
+      float mx[kTiles][2];
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt) {
+        mx[nt][0] = mx[nt][1] = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          const float ks = sc[box_of(mt)];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = sv[mt][nt][e] * qmul[nt][e & 1] * ks;
+            if (!full) {
+              const int i = mt * 16 + (e >> 1) * 8 + dp_row<D>(g), key = key0 + i;
+              const int ps = pos[nt][e & 1];
+              const bool see = (have >> box_of(mt) & 1u) && key <= ps &&
+                               (key > ps - po.win || key < po.sinks);
+              x = see ? x : -INFINITY;
+            }
+            sv[mt][nt][e] = x;
+            mx[nt][e & 1] = fmaxf(mx[nt][e & 1], x);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int i = 4; i < 32; i *= 2)
+            mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], i));
+          // a row keeps its reference until a score passes it by the threshold
+          if (!(mx[nt][e] > m[nt][e] + kDpTau)) mx[nt][e] = m[nt][e];
+          raise |= mx[nt][e] != m[nt][e];
+        }
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // a row without a reference so far holds zeros (or NaN, which stays)
+            f[e] = m[nt][e] == -INFINITY || mx[nt][e] == m[nt][e] ? 1.f
+                                                                  : ptx::ex2(m[nt][e] - mx[nt][e]);
+            m[nt][e] = mx[nt][e];
+            l[nt][e] *= f[e];
+          }
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[e & 1];
+        }
+      }
+      uint32_t pb[kMt][kTiles][2];           // P^T as the B operand
+#pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          const float a = ptx::ex2(sv[mt][nt][0] - m0), b = ptx::ex2(sv[mt][nt][1] - m1);
+          const float c = ptx::ex2(sv[mt][nt][2] - m0), d = ptx::ex2(sv[mt][nt][3] - m1);
+          l[nt][0] += a + c;
+          l[nt][1] += b + d;
+          pb[mt][nt][0] = transpose8x8(ptx::pack2<false>(a, b));
+          pb[mt][nt][1] = transpose8x8(ptx::pack2<false>(c, d));
+        }
+      }
+
+      // ---- O^T: element 2 j (+ 1) of the thread's kBytes = D / 8 of a row
+      {
+        constexpr int kVw = D / 32;          // 4-byte words
+        uint32_t v[kMt][4][kVw];             // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = mt * 16 + (i >> 1) * 8 + dp_row<D>(2 * t + (i & 1));
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vt + dp_chunk<D>(r, g));
+              v[mt][i][0] = x.x;
+              v[mt][i][1] = x.y;
+              v[mt][i][2] = x.z;
+              v[mt][i][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(vt + dp_chunk<D>(r, g >> 1) +
+                                                              (g & 1) * 8);
+              v[mt][i][0] = x.x;
+              v[mt][i][1] = x.y;
+            }
+          }
+        float vs[kMt];
+        bool odd = false;                    // a scale that is not finite
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
+          odd |= !(fabsf(vs[mt]) < INFINITY);
+        }
+        odd &= !full;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          float part[kTiles][4] = {};
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) {
+            uint32_t a0, a1, a2, a3;
+            constexpr uint32_t kSel[2] = {0x5140, 0x7362};
+            codes4<kInt8>(__byte_perm(v[mt][0][j >> 1], v[mt][1][j >> 1], kSel[j & 1]), a0, a1);
+            codes4<kInt8>(__byte_perm(v[mt][2][j >> 1], v[mt][3][j >> 1], kSel[j & 1]), a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
+              mma16816(part[nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
+            if (mt == kMt - 1 || p.boxes > 1) {
+#pragma unroll
+              for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float f = vs[mt];
+                  // rows that see nothing of the box take nothing from it
+                  if (odd && !paged_sees(key0 + box_of(mt) * box_rows, box_rows, pos[nt][e & 1],
+                                         po.win, po.sinks))
+                    f = 0.f;
+                  o[j][nt][e] = fmaf(part[nt][e], f, o[j][nt][e]);
+                  part[nt][e] = 0.f;
+                }
+            }
+          }
+        }
+      }
+      __syncwarp();                          // the stage has been read
+      if (alive) load(stage);
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
+
+    // ---- merge of the warps, and the unit's result or its part
+#pragma unroll
+    for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int i = 4; i < 32; i *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], i);
+        if (m[nt][e] == -INFINITY) m[nt][e] = 0.f;
+        if (g == 0) ml_s[warp * L::kRows + nt * 8 + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < kTiles; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kDpWarps; ++w) {
+          const float2 x = ml_s[w * L::kRows + nt * 8 + 2 * t + e];
+          if (x.y != 0.f) top = fmaxf(top, x.x);
+        }
+        f[e] = l[nt][e] != 0.f ? ptx::ex2(m[nt][e] - top) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[e & 1];
+    }
+    // a row's D floats as D / 4 pieces, permuted by the row so that the rows of
+    // a quarter warp use other banks
+    constexpr int kPieces = D / 4;
+    auto place = [&](int w, int r, int c) { return (w * L::kRows + r) * kPieces + (c ^ (r >> 1 & 3)); };
+    auto each = [&](auto&& f) {              // f(row, piece, its four values)
+#pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < kJ / 2; ++i)
+            f(nt * 8 + 2 * t + e, g * (kJ / 2) + i, o[2 * i][nt][e], o[2 * i][nt][e + 2],
+              o[2 * i + 1][nt][e], o[2 * i + 1][nt][e + 2]);
+    };
+    if (warp >= 4)
+      each([&](int r, int c, float& x, float& y, float& z, float& w) {
+        sum_s[place(warp - 4, r, c)] = make_float4(x, y, z, w);
+      });
+    __syncthreads();
+    if (warp < 4)
+      each([&](int r, int c, float& x, float& y, float& z, float& w) {
+        float4& a = sum_s[place(warp, r, c)];
+        a = make_float4(x + a.x, y + a.y, z + a.z, w + a.w);
+      });
+    __syncthreads();
+    const size_t slot = 2 * static_cast<size_t>(run) + (pieces == 0 ? 0 : 1);
+    for (int i = threadIdx.x; i < rows * kPieces; i += kDpThreads) {
+      const int r = i / kPieces, c = i - r * kPieces;
+      float4 a = sum_s[place(0, r, c)];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float4 x = sum_s[place(w, r, c)];
+        a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      }
+      float top = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDpWarps; ++w) {
+        const float2 x = ml_s[w * L::kRows + r];
+        if (x.y != 0.f) top = fmaxf(top, x.x);
+      }
+#pragma unroll
+      for (int w = 0; w < kDpWarps; ++w) {
+        const float2 x = ml_s[w * L::kRows + r];
+        if (x.y != 0.f) lt = fmaf(x.y, ptx::ex2(x.x - top), lt);
+      }
+      if (whole) {
+        const float inv = lt != 0.f ? 1.0f / lt : 0.f;
+        const size_t out = head * po.R + row0 + r;
+        if (!(lt != 0.f)) a = make_float4(0.f, 0.f, 0.f, 0.f);
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(po.o) + out * D)[c] =
+            make_uint2(ptx::pack2<kBf16>(a.x * inv, a.y * inv),
+                       ptx::pack2<kBf16>(a.z * inv, a.w * inv));
+        if (c == 0)
+          po.lse[out] = lt != 0.f ? (ptx::lg2(lt) + top) * 0.693147180559945309f : -INFINITY;
+      } else {
+        *dec_part<D>(po, slot, r, c) = a;
+        if (c == 0) po.part_ml[slot * po.slot_rows + r] = make_float2(lt != 0.f ? -top : 0.f, lt);
+      }
+    }
+    if (tile0 == 0 && !whole && threadIdx.x == 0) {
+      // a unit that starts here and ends in a later run: its parts' place
+      const int last = dec_run_start(deal, run) + done + at.s.tiles - 1;
+      po.cut[run] = make_int4(static_cast<int>(head), block, static_cast<int>(slot),
+                              dec_run_of(deal, last));
+    }
+    cut_here |= tile0 == 0 && !whole;
+    ++pieces;
+    done += n;
+    if (done < n_tiles) advance(at, n);
+    __syncthreads();                         // sums and queries have been read
+  }
+  if (threadIdx.x == 0 && !cut_here) po.cut[run] = make_int4(0, 0, 0, -1);
+  // after a wait that ran out: the loads in flight land before the block ends
+  cp_async_wait<0>();
+  for (; waited < loaded; ++waited)
+    ptx::wait_drain(bar(waited % kStages), waited / kStages & 1, 200000000ull);
+}
+
+}  // namespace fa

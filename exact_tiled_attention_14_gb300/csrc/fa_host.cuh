@@ -49,6 +49,14 @@ bool make_tmap(CUtensorMap* m, const void* ptr, int BH, int N, int d, bool bf16,
 // like a 128 x 64 tile of the [B, H, N, d] layout.
 bool make_tmap_tokens(CUtensorMap* m, const void* ptr, int H, int tokens, int width, bool bf16);
 
+// Rows of `width` bytes (64 or 128), boxes of box_rows whole rows, swizzled by
+// the row's width: the codes of a paged cache.
+bool make_tmap_codes(CUtensorMap* m, const void* ptr, long long rows, int width, int box_rows);
+
+// Sizes of a paged cache, in the documented order.
+int check_paged(int B, int Hk, int d, int pages, int page_size, int pages_per_seq,
+                int cache_dtype);
+
 // Budget of the kernels' bounded waits in ns (fa_set_watchdog_ns; 0 means
 // kDefaultWatchdogNs), and the event-trace buffer of FA_TRACE builds.
 extern std::atomic<unsigned long long> g_watchdog_ns;

@@ -1,0 +1,81 @@
+// fa_rotary.cuh — rotation of query and key elements by their token's
+// position, shared by the rotary kernels and the cache's append.
+//
+// A head's first `rot` elements are rot / 2 pairs; pair j of the token at
+// position p is turned by the angle p * w_j:
+//     (a, b) -> mscale * (a cos - b sin, b cos + a sin),
+// and back (the gradient) by the negative angle.  Pairs are (2 j, 2 j + 1)
+// (interleaved) or (j, j + rot / 2) (halves); elements from `rot` on stay.
+//
+// Angles.  w_j arrives as turns per position in units of 2^-64, so the
+// product with the position, wrapped at 64 bits as integers wrap, is the
+// angle's fraction of a turn with an error of p * 2^-65 turns whatever its
+// whole turns: 2^-44 at position 2^20, where a float32 angle is off by whole
+// radians.  The fraction is cut to the nearest quarter turn, and the rest,
+// at most an eighth, goes through sincospif in float32.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx_sm103.cuh"
+
+namespace fa {
+
+__device__ __forceinline__ void rotary_cos_sin(int pos, unsigned long long freq, float mscale,
+                                               float& c, float& s) {
+  const unsigned long long turn =
+      static_cast<unsigned long long>(static_cast<long long>(pos)) * freq;
+  const unsigned long long near = turn + (1ull << 61);
+  const int quarter = static_cast<int>(near >> 62);
+  const long long rest = static_cast<long long>(turn - (near & (3ull << 62)));
+  float sn, cs;
+  sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &sn, &cs);   // half turns: 2^-63
+  const float x = (quarter & 1) ? sn : cs, y = (quarter & 1) ? cs : sn;
+  c = (quarter == 1 || quarter == 2) ? -x : x;
+  s = quarter >= 2 ? -y : y;
+  c *= mscale;
+  s *= mscale;
+}
+
+// Sixteen elements of a row that are turned together: eight pairs, or sixteen
+// elements behind the rotated ones.  Unit u of a row covers vectors of eight
+// elements that start at columns first(u) and second(u).
+struct RotaryUnit {
+  int first, second;
+  bool turned;
+};
+__host__ __device__ __forceinline__ RotaryUnit rotary_unit(int u, int rot, bool interleaved) {
+  RotaryUnit r;
+  r.turned = u * 16 < rot;
+  r.first = r.turned && !interleaved ? u * 8 : u * 16;
+  r.second = r.turned && !interleaved ? u * 8 + rot / 2 : u * 16 + 8;
+  return r;
+}
+
+// Turn a unit's values x[0..7] (first vector), x[8..15] (second).
+template <bool kInterleaved>
+__device__ __forceinline__ void rotary_turn(float* x, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int ia = kInterleaved ? 2 * i : i, ib = kInterleaved ? 2 * i + 1 : i + 8;
+    const float a = x[ia], b = x[ib];
+    x[ia] = fmaf(a, c[i], -(b * s[i]));
+    x[ib] = fmaf(b, c[i], a * s[i]);
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const uint4 v, float* x) {
+  ptx::unpack2<kBf16>(v.x, x[0], x[1]);
+  ptx::unpack2<kBf16>(v.y, x[2], x[3]);
+  ptx::unpack2<kBf16>(v.z, x[4], x[5]);
+  ptx::unpack2<kBf16>(v.w, x[6], x[7]);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(ptx::pack2<kBf16>(x[0], x[1]), ptx::pack2<kBf16>(x[2], x[3]),
+                    ptx::pack2<kBf16>(x[4], x[5]), ptx::pack2<kBf16>(x[6], x[7]));
+}
+
+}  // namespace fa

@@ -29,6 +29,12 @@
  *    heads: fa_fwd_window, fa_bwd_window (prompts, chunks after a cache,
  *    training), fa_decode_window (the last tokens of each cache),
  *    fa_decode_tree (the tokens of a drafted tree behind each cache);
+ *  - rotation of queries and keys by their positions, and its gradient:
+ *    fa_rotary;
+ *  - a key/value cache in pages of 8-bit codes: fa_cache_append (new tokens,
+ *    keys rotated on the way), fa_cache_read (its tokens in 16 bits, for the
+ *    attention of prompt chunks), fa_decode_paged (the last tokens of each
+ *    sequence over it);
  *  - status and settings: fa_strerror, fa_status, fa_set_watchdog_ns,
  *    fa_set_unit_group, fa_watchdog_selftest, fa_work_tiles, fa_version.
  *
@@ -62,6 +68,10 @@ extern "C" {
 /* Storage dtype of q, k, v and o. */
 typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
 
+/* Codes of a paged cache: 8-bit floats (4 exponent bits, 3 of significand, no
+ * infinities, largest 448), or integers from -127 to 127. */
+typedef enum { FA_E4M3 = 0, FA_INT8 = 1 } fa_cache_dtype;
+
 /* Return codes.  They mirror the pages' raise-on-bad-input contract (section
  * "Build it", the input checks; section "Check it", the failing cases). */
 enum {
@@ -69,7 +79,7 @@ enum {
   FA_ERR_NULLPTR = 1,        /* a required pointer is NULL                     */
   FA_ERR_SHAPE = 2,          /* B, H or N negative, d <= 0, or sizes overflow  */
   FA_ERR_UNSUPPORTED_D = 3,  /* d is not 64 or 128                             */
-  FA_ERR_DTYPE = 4,          /* dtype is not FA_BF16 / FA_FP16                 */
+  FA_ERR_DTYPE = 4,          /* dtype is not FA_BF16 / FA_FP16 (cache: fa_cache_dtype) */
   FA_ERR_ALIGN = 5,          /* q/k/v/o not 16-byte aligned, lse not 4-byte    */
   FA_ERR_SCALE = 6,          /* scale not finite and > 0                       */
   FA_ERR_DEVICE = 7,         /* current device is not a compute 10.3 GPU       */
@@ -693,6 +703,152 @@ int fa_decode_tree(const void *q, const void *k, const void *v, void *o, float *
  * FA_ERR_UNSUPPORTED_D or FA_ERR_DEVICE.
  */
 int fa_decode_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d, size_t *bytes);
+
+/*
+ * fa_rotary — rotation of queries and keys by their positions (rotary
+ * positions), in one pass over both.
+ *
+ * The first `rot` elements of a head are rot / 2 pairs; pair j of the token at
+ * position p turns by the angle p * w_j:
+ *     (a, b)  ->  mscale * (a cos - b sin,  b cos + a sin),
+ * or with `inverse` by the negative angle, which is the gradient of the same
+ * call without it.  The other elements are copied.  The pages feed attention
+ * with queries and keys as they are and have no counterpart.
+ *
+ *   q, q_out  : H heads, k, k_out: Hk heads, of N tokens of B sequences, dtype
+ *               `dtype`, rows of d contiguous elements, 16-byte aligned.  Hk = 0
+ *               (or H = 0) leaves that tensor out.  An output may be its own
+ *               input (the same pointer and strides); it must not overlap an
+ *               input otherwise.
+ *   strides   : 12 numbers (host memory), in elements: batch, head and token
+ *               strides of q, q_out, k, k_out, in this order; multiples of 8.
+ *               An input's may be 0 (a broadcast); an output's rows must differ.
+ *   d         : 64 or 128.   rot : 16 .. d, a multiple of 16.
+ *   freqs     : [rot / 2] w_j as turns per position in units of 2^-64 (device,
+ *               16-byte aligned): w_j * 2^64 / (2 pi), rounded.  The angle is
+ *               exact to p * 2^-65 turns at any position.
+ *   mscale    : finite and > 0 (1; another for some long-context scalings).
+ *   interleaved : 0: pair j is elements j and j + rot / 2; else 2 j and 2 j + 1.
+ *   positions : NULL or [B, N] int32 (device).
+ *   seqlens   : NULL or B int32 (device): token i of sequence b sits at
+ *               position seqlens[b] - N + i.  Not both; with neither, token i
+ *               sits at position i.
+ * Errors: FA_ERR_SHAPE (negative sizes, B * N or H + Hk over 2^30),
+ * FA_ERR_UNSUPPORTED_D, FA_ERR_SHAPE (rot; both positions and seqlens),
+ * FA_ERR_DTYPE, FA_ERR_SCALE, then B * N * (H + Hk) == 0 returns FA_OK, then
+ * FA_ERR_NULLPTR, FA_ERR_ALIGN, FA_ERR_DEVICE, FA_ERR_LAUNCH.
+ */
+int fa_rotary(const void *q, const void *k, void *q_out, void *k_out, int B, int H, int Hk, int N,
+              int d, const long long *strides, const unsigned long long *freqs, int rot,
+              float mscale, int interleaved, int inverse, const int *positions,
+              const int *seqlens, int dtype, cudaStream_t stream);
+
+/*
+ * fa_cache_append — new keys and values into a cache of pages of 8-bit codes.
+ *
+ * The cache of one layer is a pool: k_cache, v_cache [pages, Hk, page_size, d]
+ * codes with scales k_scale, v_scale [pages, Hk] float32; an element's value
+ * is code * scale.  page_table [B, pages_per_seq] names the pages of each
+ * sequence in order: slot n of sequence b is row n % page_size of page
+ * page_table[b][n / page_size].
+ *
+ * After the call sequence b has seqlens[b] tokens, the last counts[b] of them
+ * (NULL: T) new: token i goes to slot seqlens[b] - counts[b] + i.  Keys are
+ * rotated as by fa_rotary when `freqs` is given, by positions[b][i], or NULL:
+ * by their slot.  Each page and head that gets tokens gets a scale from the
+ * magnitudes (after rotation, in float32) of its new elements, the largest
+ * being `top`:
+ *     FA_E4M3: the smallest power of two s with top <= 448 s,
+ *     FA_INT8: s = top / 127,       both at least 2^-100,
+ * and codes round(x * (1 / s)), to nearest even.  A page that holds earlier
+ * tokens of the sequence keeps its scale s0 where s <= s0; otherwise those
+ * tokens' codes become round(code * (s0 * (1 / s))).  (For FA_E4M3 that shifts
+ * exponents; it rounds only below 2^-6 s.)  A NaN or infinite element makes
+ * the scale of its page and head NaN, and everything read of it NaN, until the
+ * page is filled from its first slot again.
+ *
+ *   k, v      : T tokens of Hk heads of B sequences, dtype `dtype`, rows of d
+ *               contiguous elements, 16-byte aligned.  Tokens from counts[b]
+ *               on are padding and not read.
+ *   strides   : 6 numbers (host memory), in elements: batch, head and token
+ *               strides of k and of v; multiples of 8.
+ *   pages, page_size, pages_per_seq : page_size a multiple of 16, up to 128.
+ *   seqlens   : B int32; counts: NULL or B int32 (clamped to 0 .. T).  Tokens
+ *               whose slot is negative, past the sequence's pages, or in a page
+ *               whose number is outside 0 .. pages - 1 are not written.
+ *   A page that a call writes belongs to one sequence of the call.  Slots from
+ *   seqlens[b] on, and pages without new tokens, stay as they are.
+ *   d, freqs, rot, mscale, interleaved : as fa_rotary.
+ * Errors: FA_ERR_SHAPE (negative sizes; no pages; page_size; B * Hk, B * T,
+ * B * pages_per_seq, or pages or pages_per_seq times page_size over 2^30, the
+ * pool's rows 2^31 or more), FA_ERR_UNSUPPORTED_D, FA_ERR_DTYPE (cache_dtype),
+ * FA_ERR_SHAPE (T, rot), FA_ERR_DTYPE, FA_ERR_SCALE, then B * Hk * T == 0
+ * returns FA_OK, then FA_ERR_NULLPTR, FA_ERR_ALIGN, FA_ERR_DEVICE,
+ * FA_ERR_LAUNCH.
+ */
+int fa_cache_append(const void *k, const void *v, int B, int Hk, int T, int d,
+                    const long long *strides, void *k_cache, void *v_cache, float *k_scale,
+                    float *v_scale, int pages, int page_size, const int *page_table,
+                    int pages_per_seq, const int *seqlens, const int *counts,
+                    const unsigned long long *freqs, int rot, float mscale, int interleaved,
+                    const int *positions, int dtype, int cache_dtype, cudaStream_t stream);
+
+/*
+ * fa_cache_read — the first N slots of each sequence of a paged cache as
+ * 16-bit keys and values, the layout that fa_fwd_kv and fa_fwd_window read (a
+ * prompt chunk's attention over its cache).
+ *
+ *   k, v      : [B, Hk, N, d], dtype `dtype`, 16-byte aligned (written):
+ *               code * scale, rounded to nearest even.  Rows from seqlens[b]
+ *               on, and rows whose page's number is outside 0 .. pages - 1, are
+ *               zeros.
+ *   other arguments as fa_cache_append; B at most 32767.
+ * Errors as fa_cache_append; B * Hk * N == 0 writes nothing.
+ */
+int fa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale,
+                  const float *v_scale, void *k, void *v, int B, int Hk, int N, int d, int pages,
+                  int page_size, const int *page_table, int pages_per_seq, const int *seqlens,
+                  int dtype, int cache_dtype, cudaStream_t stream);
+
+/*
+ * fa_decode_paged — the last Nq tokens of each sequence against its pages of
+ * 8-bit keys and values (the cache of fa_cache_append, which has appended the
+ * new tokens' own): fa_decode_window's function with k and v read as
+ * code * scale, the keys of all sequences split evenly across the GPU.
+ *
+ *   q, o      : [B, H, Nq, d], 1 <= Nq <= 16, 16-byte aligned (o written).
+ *   lse       : [B, H, Nq] float32.
+ *   H, Hk     : H a multiple of Hk; query head h reads head h / (H / Hk).
+ *   seqlens   : B int32 token counts, the new tokens among them, clamped to
+ *               0 .. pages_per_seq * page_size; token i of sequence b sits at
+ *               position seqlens[b] - Nq + i (by slot, whatever its rotation).
+ *   window    : >= 1, or 0 for none.   sinks : >= 0.
+ *   workspace, workspace_bytes : as fa_decode_window, at least
+ *               fa_decode_paged_workspace_size bytes.
+ *   other arguments as fa_cache_append.  Any finite scales do, not only
+ *   those that fa_cache_append writes.
+ * A token that sees no key gets O = 0 and LSE = -inf; keys in a page whose
+ * number is outside 0 .. pages - 1 are not seen.  Slots that no token of a
+ * sequence sees may hold anything; a page's scale that is not finite reaches
+ * the tokens that see one of its slots.  Results do not depend on the order
+ * CTAs run in.
+ * Errors as fa_cache_append and fa_decode_window (FA_ERR_SHAPE also for
+ * B * H * Nq over 2^30 and B * Hk * ceil(H / Hk * Nq / 32) * (ceil(capacity /
+ * 32) + 1) of 2^31 or more, at d = 64 with 64 in the place of the last 32).
+ */
+int fa_decode_paged(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                    const float *v_scale, void *o, float *lse, int B, int H, int Hk, int Nq, int d,
+                    int pages, int page_size, const int *page_table, int pages_per_seq,
+                    const int *seqlens, int window, int sinks, float scale, int dtype,
+                    int cache_dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_decode_paged_workspace_size — bytes of workspace that fa_decode_paged
+ * needs for this shape on the current device (0 when B * H == 0).  Returns
+ * FA_ERR_NULLPTR, FA_ERR_SHAPE, FA_ERR_UNSUPPORTED_D or FA_ERR_DEVICE.
+ */
+int fa_decode_paged_workspace_size(int B, int H, int Hk, int Nq, int d, int page_size,
+                                   int pages_per_seq, size_t *bytes);
 
 /*
  * fa_strerror — human-readable name of a return code (a static string, never
