@@ -32,7 +32,7 @@ cudaError_t launch_main(const DecPagedParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
-  kernel<<<p.out.grid, kDpThreads, kAlloc, stream>>>(p);
+  kernel<<<p.out.grid, DpLayout<D, kTiles>::kThreads, kAlloc, stream>>>(p);
   return cudaGetLastError();
 }
 

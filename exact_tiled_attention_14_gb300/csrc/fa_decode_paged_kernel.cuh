@@ -45,8 +45,8 @@
 
 namespace fa {
 
-constexpr int kDpWarps = 8;
-constexpr int kDpThreads = 32 * kDpWarps;
+// Warps of a CTA by its row tiles (8 rows each).
+__host__ __device__ constexpr int dp_warps(int tiles) { return tiles == 1 ? 12 : 8; }
 constexpr int kDpTileBytes = 4096;       // of K, and of V
 constexpr float kDpTau = 8.0f;           // lazy-rescale threshold, log2 units
 constexpr uint32_t kSiteDpFull = 50;
@@ -114,15 +114,17 @@ __host__ __device__ constexpr uint32_t dp_chunk(int r, int c) {
 template <int D, int kTiles>
 struct DpLayout {
   static constexpr int kRows = 8 * kTiles;
-  static constexpr int kStages = kTiles == 1 ? 3 : 2;
+  static constexpr int kWarps = dp_warps(kTiles), kThreads = 32 * kWarps, kHalf = kWarps / 2;
+  static constexpr int kStages = 2;
   static constexpr int kRing = 0;
-  static constexpr int kQ = kRing + kDpWarps * kStages * 2 * kDpTileBytes;
-  static constexpr int kSum = kQ + kRows * D * 2;             // 4 warps' O
-  static constexpr int kMl = kSum + 4 * kRows * D * 4;        // (m, l) [warp][row]
-  static constexpr int kQmul = kMl + kDpWarps * kRows * 8;    // [row]
+  static constexpr int kQ = kRing + kWarps * kStages * 2 * kDpTileBytes;
+  static constexpr int kSum = kQ + kRows * D * 2;             // half the warps' O
+  static constexpr int kP = kSum + kHalf * kRows * D * 4;     // the warps' weights
+  static constexpr int kMl = kP + kWarps * (kDpTileBytes / D / 16) * kTiles * 256;   // (m, l) [warp][row]
+  static constexpr int kQmul = kMl + kWarps * kRows * 8;    // [row]
   static constexpr int kMeta = kQmul + kRows * 4;             // [warp][stage]: 4 K, 4 V scales
-  static constexpr int kBar = kMeta + kDpWarps * kStages * 32;
-  static constexpr int kMisc = kBar + 8 * kDpWarps * kStages;
+  static constexpr int kBar = kMeta + kWarps * kStages * 32;
+  static constexpr int kMisc = kBar + 8 * kWarps * kStages;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
@@ -166,7 +168,7 @@ struct DpPlace {
 };
 
 template <int D, bool kBf16, bool kInt8, int kTiles>
-__global__ void __launch_bounds__(kDpThreads, 1)
+__global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
     fa_decode_paged_kernel(const __grid_constant__ DecPagedParams p) {
   using L = DpLayout<D, kTiles>;
   constexpr int kKeys = dp_keys(D);          // of a tile
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kDpThreads, 1)
     }
   };
 
-  // ---- the warp's loads: tile i of the run goes to warp i % kDpWarps
+  // ---- the warp's loads: tile i of the run goes to warp i % L::kWarps
   const uint32_t ring = sbase + L::kRing + warp * (kStages * 2 * kDpTileBytes);
   uint8_t* const ring_gen = sgen + L::kRing + warp * (kStages * 2 * kDpTileBytes);
   const uint32_t meta = sbase + L::kMeta + warp * (kStages * 32);
@@ -288,8 +290,8 @@ __global__ void __launch_bounds__(kDpThreads, 1)
         cp_async4(meta + stage * 32 + 16 + lane * 4, p.v_scale + head);
       }
       ++loaded;
-      nx_i += kDpWarps;
-      if (nx_i < n_tiles) advance(nx, kDpWarps);
+      nx_i += L::kWarps;
+      if (nx_i < n_tiles) advance(nx, L::kWarps);
       look();
     }
     cp_async_commit();                       // one group per tile, empty ones too
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kDpThreads, 1)
   int stage = 0, parity = 0, pieces = 0;
   int waited = 0;                            // the warp's loads that have arrived
   int mine = warp;                           // the warp's next tile in the run
+  uint2* const p_s = reinterpret_cast<uint2*>(sgen + L::kP) + warp * (kMt * kTiles * 32);
   uint2* const q_s = reinterpret_cast<uint2*>(sgen + L::kQ);
   float* const qmul_s = reinterpret_cast<float*>(sgen + L::kQmul);
   float4* const sum_s = reinterpret_cast<float4*>(sgen + L::kSum);
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kDpThreads, 1)
 
     // queries of the unit: row r, elements 4 c .. 4 c + 3 as the B operand's
     // registers of lane (r % 8, 4 c / (D / 4)), in half precision
-    for (int r = warp; r < L::kRows; r += kDpWarps) {
+    for (int r = warp; r < L::kRows; r += L::kWarps) {
       uint2 raw = make_uint2(0, 0);
       if (r < rows && lane * 4 < D)
         raw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
@@ -344,11 +347,6 @@ __global__ void __launch_bounds__(kDpThreads, 1)
     }
     __syncthreads();
 
-    uint2 qf[kTiles <= 2 ? kJ * kTiles : 1];
-    if constexpr (kTiles <= 2) {
-#pragma unroll
-      for (int i = 0; i < kJ * kTiles; ++i) qf[i] = q_s[i * 32 + lane];
-    }
     float qmul[kTiles][2];
     int pos[kTiles][2];
     float m[kTiles][2], l[kTiles][2];
@@ -363,9 +361,10 @@ __global__ void __launch_bounds__(kDpThreads, 1)
         l[nt][e] = 0.f;
       }
     float o[kJ][kTiles][4] = {};
+    float vref = 0.f;                        // unit of O (0: nothing summed yet)
     const int pos_lo = s.len - po.Nq, pos_hi = s.len - 1;
 
-    for (; mine < done + n; mine += kDpWarps) {
+    for (; mine < done + n; mine += L::kWarps) {
       const int key0 = paged_key0(s, tile0 + mine - done, kKeys);
       alive = ptx::warp_all(alive && ptx::wait_bounded(bar(stage), parity, wd, kSiteDpFull));
       cp_async_wait<kStages - 1>();
@@ -393,35 +392,27 @@ __global__ void __launch_bounds__(kDpThreads, 1)
         __syncwarp();
       }
 
-      // ---- S^T
+      // ---- S^T, 16 bytes of each key row at a time
       float sv[kMt][kTiles][4] = {};
-      {
-        uint32_t w[kMt][2][kWords];          // rows dp_row(g) and + 8 of each 16
+#pragma unroll 1
+      for (int i = 0; i < kWords / 4; ++i) {
+        uint32_t w[kMt][2][4];               // rows dp_row(g) and + 8 of each 16
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int r = mt * 16 + h * 8 + dp_row<D>(g);
-#pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-              const uint4 x = *reinterpret_cast<const uint4*>(
-                  kt + dp_chunk<D>(r, t * (kWords / 4) + i));
-              w[mt][h][4 * i] = x.x;
-              w[mt][h][4 * i + 1] = x.y;
-              w[mt][h][4 * i + 2] = x.z;
-              w[mt][h][4 * i + 3] = x.w;
-            }
+            const uint4 x = *reinterpret_cast<const uint4*>(
+                kt + dp_chunk<D>(mt * 16 + h * 8 + dp_row<D>(g), t * (kWords / 4) + i));
+            w[mt][h][0] = x.x;
+            w[mt][h][1] = x.y;
+            w[mt][h][2] = x.z;
+            w[mt][h][3] = x.w;
           }
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
+        for (int j = 0; j < 4; ++j) {
           uint2 qb[kTiles];
 #pragma unroll
-          for (int nt = 0; nt < kTiles; ++nt) {
-            if constexpr (kTiles <= 2)
-              qb[nt] = qf[j * kTiles + nt];
-            else
-              qb[nt] = q_s[(j * kTiles + nt) * 32 + lane];
-          }
+          for (int nt = 0; nt < kTiles; ++nt) qb[nt] = q_s[((i * 4 + j) * kTiles + nt) * 32 + lane];
 #pragma unroll
           for (int mt = 0; mt < kMt; ++mt) {
             uint32_t a0, a1, a2, a3;
@@ -435,30 +426,62 @@ __global__ void __launch_bounds__(kDpThreads, 1)
       }
 
       // ---- scores, weights
-      float mx[kTiles][2];
-      bool raise = false;
+      float vs[kMt], vs_top = 0.f;
+      bool odd = false;                      // a scale of values that is not finite
 #pragma unroll
-      for (int nt = 0; nt < kTiles; ++nt) {
-        mx[nt][0] = mx[nt][1] = -INFINITY;
+      for (int mt = 0; mt < kMt; ++mt) {
+        const float ks = sc[box_of(mt)];
+        vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
+        if (!(fabsf(vs[mt]) < INFINITY)) {
+          vs[mt] = 0.f;
+          odd = true;
+        }
+        vs_top = fmaxf(vs_top, fabsf(vs[mt]));
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
-          const float ks = sc[box_of(mt)];
+        for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = sv[mt][nt][e] * qmul[nt][e & 1] * ks;
-            if (!full) {
-              const int i = mt * 16 + (e >> 1) * 8 + dp_row<D>(g), key = key0 + i;
-              const int ps = pos[nt][e & 1];
+          for (int e = 0; e < 4; ++e) sv[mt][nt][e] = sv[mt][nt][e] * qmul[nt][e & 1] * ks;
+      }
+      if (!full) {
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + mt * 16 + (e >> 1) * 8 + dp_row<D>(g), ps = pos[nt][e & 1];
               const bool see = (have >> box_of(mt) & 1u) && key <= ps &&
                                (key > ps - po.win || key < po.sinks);
-              x = see ? x : -INFINITY;
+              if (!see) sv[mt][nt][e] = -INFINITY;
             }
-            sv[mt][nt][e] = x;
-            mx[nt][e & 1] = fmaxf(mx[nt][e & 1], x);
-          }
+      }
+      // O is held in units of vref, a power of two next to the scales of the
+      // last pages: weights times their page's scale / vref round like weights
+      if (vs_top > vref || vs_top < vref * (1.f / 64.f)) {
+        if (vs_top > 0.f) {
+          const float unit = __uint_as_float((__float_as_uint(vs_top) + 0x7fffffu) & 0x7f800000u);
+          const float now = fminf(fmaxf(unit, 0x1p-120f), 0x1p120f);
+          const float f = vref > 0.f ? fminf(vref / now, 0x1p120f) : 1.f;
+          vref = now;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[j][nt][e] *= f;
         }
+      }
+      const float inv_vref = vref > 0.f ? 1.f / vref : 0.f;
+      bool raise = false;
+      float mx[kTiles][2];
+#pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt)
+            mx[nt][e] = ptx::max3(mx[nt][e], sv[mt][nt][e], sv[mt][nt][e + 2]);
 #pragma unroll
           for (int i = 4; i < 32; i *= 2)
             mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], i));
@@ -466,7 +489,6 @@ __global__ void __launch_bounds__(kDpThreads, 1)
           if (!(mx[nt][e] > m[nt][e] + kDpTau)) mx[nt][e] = m[nt][e];
           raise |= mx[nt][e] != m[nt][e];
         }
-      }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
@@ -485,79 +507,73 @@ __global__ void __launch_bounds__(kDpThreads, 1)
             for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[e & 1];
         }
       }
-      uint32_t pb[kMt][kTiles][2];           // P^T as the B operand
 #pragma unroll
-      for (int nt = 0; nt < kTiles; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      for (int mt = 0; mt < kMt; ++mt) {
+        const float r = vs[mt] * inv_vref;
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
+        for (int nt = 0; nt < kTiles; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+          const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
           const float a = ptx::ex2(sv[mt][nt][0] - m0), b = ptx::ex2(sv[mt][nt][1] - m1);
           const float c = ptx::ex2(sv[mt][nt][2] - m0), d = ptx::ex2(sv[mt][nt][3] - m1);
           l[nt][0] += a + c;
           l[nt][1] += b + d;
-          pb[mt][nt][0] = transpose8x8(ptx::pack2<false>(a, b));
-          pb[mt][nt][1] = transpose8x8(ptx::pack2<false>(c, d));
+          // P^T as the B operand
+          p_s[(mt * kTiles + nt) * 32 + lane] =
+              make_uint2(transpose8x8(ptx::pack2<false>(a * r, b * r)),
+                         transpose8x8(ptx::pack2<false>(c * r, d * r)));
+        }
+      }
+      if (odd) {                             // rows that see such a page: NaN
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          if (!(have >> box_of(mt) & 1u) || fabsf(sc[4 + box_of(mt)]) < INFINITY) continue;
+#pragma unroll
+          for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (paged_sees(key0 + box_of(mt) * box_rows, box_rows, pos[nt][e & 1], po.win,
+                             po.sinks))
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) o[j][nt][e] = NAN;
         }
       }
 
-      // ---- O^T: element 2 j (+ 1) of the thread's kBytes = D / 8 of a row
-      {
+      // ---- O^T: element 2 j (+ 1) of the thread's D / 8 of a row, 16 keys at a time
+#pragma unroll 1
+      for (int mt = 0; mt < kMt; ++mt) {
         constexpr int kVw = D / 32;          // 4-byte words
-        uint32_t v[kMt][4][kVw];             // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        uint32_t v[4][kVw];                  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = mt * 16 + (i >> 1) * 8 + dp_row<D>(2 * t + (i & 1));
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vt + dp_chunk<D>(r, g));
-              v[mt][i][0] = x.x;
-              v[mt][i][1] = x.y;
-              v[mt][i][2] = x.z;
-              v[mt][i][3] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(vt + dp_chunk<D>(r, g >> 1) +
-                                                              (g & 1) * 8);
-              v[mt][i][0] = x.x;
-              v[mt][i][1] = x.y;
-            }
+        for (int i = 0; i < 4; ++i) {
+          // (the 16 rows of a block do not change a row's chunk order)
+          const uint8_t* const row = vt + mt * 16 * D;
+          const int r = (i >> 1) * 8 + dp_row<D>(2 * t + (i & 1));
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + dp_chunk<D>(r, g));
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+            v[i][2] = x.z;
+            v[i][3] = x.w;
+          } else {
+            const uint2 x =
+                *reinterpret_cast<const uint2*>(row + dp_chunk<D>(r, g >> 1) + (g & 1) * 8);
+            v[i][0] = x.x;
+            v[i][1] = x.y;
           }
-        float vs[kMt];
-        bool odd = false;                    // a scale that is not finite
-#pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
-          vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
-          odd |= !(fabsf(vs[mt]) < INFINITY);
         }
-        odd &= !full;
+        uint2 pb[kTiles];
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) pb[nt] = p_s[(mt * kTiles + nt) * 32 + lane];
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
-          float part[kTiles][4] = {};
+          uint32_t a0, a1, a2, a3;
+          constexpr uint32_t kSel[2] = {0x5140, 0x7362};
+          codes4<kInt8>(__byte_perm(v[0][j >> 1], v[1][j >> 1], kSel[j & 1]), a0, a1);
+          codes4<kInt8>(__byte_perm(v[2][j >> 1], v[3][j >> 1], kSel[j & 1]), a2, a3);
 #pragma unroll
-          for (int mt = 0; mt < kMt; ++mt) {
-            uint32_t a0, a1, a2, a3;
-            constexpr uint32_t kSel[2] = {0x5140, 0x7362};
-            codes4<kInt8>(__byte_perm(v[mt][0][j >> 1], v[mt][1][j >> 1], kSel[j & 1]), a0, a1);
-            codes4<kInt8>(__byte_perm(v[mt][2][j >> 1], v[mt][3][j >> 1], kSel[j & 1]), a2, a3);
-#pragma unroll
-            for (int nt = 0; nt < kTiles; ++nt)
-              mma16816(part[nt], a0, a1, a2, a3, pb[mt][nt][0], pb[mt][nt][1]);
-            if (mt == kMt - 1 || p.boxes > 1) {
-#pragma unroll
-              for (int nt = 0; nt < kTiles; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float f = vs[mt];
-                  // rows that see nothing of the box take nothing from it
-                  if (odd && !paged_sees(key0 + box_of(mt) * box_rows, box_rows, pos[nt][e & 1],
-                                         po.win, po.sinks))
-                    f = 0.f;
-                  o[j][nt][e] = fmaf(part[nt][e], f, o[j][nt][e]);
-                  part[nt][e] = 0.f;
-                }
-            }
-          }
+          for (int nt = 0; nt < kTiles; ++nt)
+            mma16816(o[j][nt], a0, a1, a2, a3, pb[nt].x, pb[nt].y);
         }
       }
       __syncwarp();                          // the stage has been read
@@ -586,11 +602,11 @@ __global__ void __launch_bounds__(kDpThreads, 1)
       for (int e = 0; e < 2; ++e) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kDpWarps; ++w) {
+        for (int w = 0; w < L::kWarps; ++w) {
           const float2 x = ml_s[w * L::kRows + nt * 8 + 2 * t + e];
           if (x.y != 0.f) top = fmaxf(top, x.x);
         }
-        f[e] = l[nt][e] != 0.f ? ptx::ex2(m[nt][e] - top) : 0.f;
+        f[e] = l[nt][e] != 0.f ? ptx::ex2(m[nt][e] - top) * vref : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
@@ -611,34 +627,34 @@ __global__ void __launch_bounds__(kDpThreads, 1)
             f(nt * 8 + 2 * t + e, g * (kJ / 2) + i, o[2 * i][nt][e], o[2 * i][nt][e + 2],
               o[2 * i + 1][nt][e], o[2 * i + 1][nt][e + 2]);
     };
-    if (warp >= 4)
+    if (warp >= L::kHalf)
       each([&](int r, int c, float& x, float& y, float& z, float& w) {
-        sum_s[place(warp - 4, r, c)] = make_float4(x, y, z, w);
+        sum_s[place(warp - L::kHalf, r, c)] = make_float4(x, y, z, w);
       });
     __syncthreads();
-    if (warp < 4)
+    if (warp < L::kHalf)
       each([&](int r, int c, float& x, float& y, float& z, float& w) {
         float4& a = sum_s[place(warp, r, c)];
         a = make_float4(x + a.x, y + a.y, z + a.z, w + a.w);
       });
     __syncthreads();
     const size_t slot = 2 * static_cast<size_t>(run) + (pieces == 0 ? 0 : 1);
-    for (int i = threadIdx.x; i < rows * kPieces; i += kDpThreads) {
+    for (int i = threadIdx.x; i < rows * kPieces; i += L::kThreads) {
       const int r = i / kPieces, c = i - r * kPieces;
       float4 a = sum_s[place(0, r, c)];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
+      for (int w = 1; w < L::kHalf; ++w) {
         const float4 x = sum_s[place(w, r, c)];
         a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
       }
       float top = -INFINITY, lt = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDpWarps; ++w) {
+      for (int w = 0; w < L::kWarps; ++w) {
         const float2 x = ml_s[w * L::kRows + r];
         if (x.y != 0.f) top = fmaxf(top, x.x);
       }
 #pragma unroll
-      for (int w = 0; w < kDpWarps; ++w) {
+      for (int w = 0; w < L::kWarps; ++w) {
         const float2 x = ml_s[w * L::kRows + r];
         if (x.y != 0.f) lt = fmaf(x.y, ptx::ex2(x.x - top), lt);
       }
