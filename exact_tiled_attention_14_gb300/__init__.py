@@ -32,6 +32,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 
 from .build import LIB_PATH, build  # noqa: F401
 
@@ -149,10 +150,10 @@ def load_library(path=None):
     lib.fa_decode_tree.restype = i
     lib.fa_decode_window_workspace_size.argtypes = [i] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.fa_decode_window_workspace_size.restype = i
-    longs, size = ctypes.POINTER(ctypes.c_longlong), ctypes.c_size_t
-    lib.fa_rotary.argtypes = [vp] * 4 + [i] * 5 + [longs, vp, i, f, i, i, vp, vp, i, vp]
+    size = ctypes.c_size_t
+    lib.fa_rotary.argtypes = [vp] * 4 + [i] * 5 + [vp, vp, i, f, i, i, vp, vp, i, vp]
     lib.fa_rotary.restype = i
-    lib.fa_cache_append.argtypes = ([vp] * 2 + [i] * 4 + [longs] + [vp] * 4 + [i, i, vp, i]
+    lib.fa_cache_append.argtypes = ([vp] * 2 + [i] * 4 + [vp] * 5 + [i, i, vp, i]
                                     + [vp] * 3 + [i, f, i, vp, i, i, vp])
     lib.fa_cache_append.restype = i
     lib.fa_cache_read.argtypes = [vp] * 6 + [i] * 6 + [vp, i, vp, i, i, vp]
@@ -457,8 +458,8 @@ def fa_decode_window_workspace_size(B, H, Hk, Nq, Nk, d):
     return out.value
 
 
-def _longs(values):
-    return (ctypes.c_longlong * len(values))(*values)
+# Strides as the C ABI's arrays of long long (bytes pass as their address).
+_PACK6, _PACK12 = struct.Struct("6q").pack, struct.Struct("12q").pack
 
 
 def fa_rotary(q, k, q_out, k_out, B, H, Hk, N, d, strides, freqs, rot, mscale, interleaved, inverse,
@@ -467,7 +468,7 @@ def fa_rotary(q, k, q_out, k_out, B, H, Hk, N, d, strides, freqs, rot, mscale, i
     None); returns the code."""
     return load_library().fa_rotary(
         _addr(q), _addr(k), _addr(q_out), _addr(k_out), int(B), int(H), int(Hk), int(N), int(d),
-        None if strides is None else _longs(strides), _addr(freqs), int(rot), float(mscale),
+        None if strides is None else _PACK12(*strides), _addr(freqs), int(rot), float(mscale),
         int(interleaved), int(inverse), _addr(positions), _addr(seqlens), int(dtype),
         _stream(stream))
 
@@ -479,7 +480,7 @@ def fa_cache_append(k, v, B, Hk, T, d, strides, k_cache, v_cache, k_scale, v_sca
     elements, or None); returns the code."""
     return load_library().fa_cache_append(
         _addr(k), _addr(v), int(B), int(Hk), int(T), int(d),
-        None if strides is None else _longs(strides), _addr(k_cache), _addr(v_cache),
+        None if strides is None else _PACK6(*strides), _addr(k_cache), _addr(v_cache),
         _addr(k_scale), _addr(v_scale), int(pages), int(page_size), _addr(page_table),
         int(pages_per_seq), _addr(seqlens), _addr(counts), _addr(freqs), int(rot), float(mscale),
         int(interleaved), _addr(positions), int(dtype), int(cache_dtype), _stream(stream))
@@ -1262,21 +1263,33 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_len
 
 def _check_int32(t, shape, device, name, what):
     import torch
-    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+    if (t.dtype is not torch.int32 or t.shape != shape or t.device != device
+            or not t.is_contiguous()):
         raise ValueError(f"{what}: {name} must be a contiguous int32 tensor {list(shape)} on the "
                          "inputs' device")
 
 
 def _check_freqs(freqs, d, device, what):
     import torch
-    if freqs.dtype != torch.int64 or freqs.dim() != 1 or freqs.device != device \
-            or not freqs.is_contiguous():
+    if (freqs.dtype is not torch.int64 or freqs.dim() != 1 or freqs.device != device
+            or not freqs.is_contiguous()):
         raise ValueError(f"{what}: freqs must be a contiguous int64 tensor [rot / 2] on the "
                          "inputs' device (see rotary_frequencies)")
     rot = 2 * freqs.shape[0]
-    if rot < 16 or rot > d or rot % 16:
+    if rot < 16 or rot > d or rot & 15:
         raise ValueError(f"{what}: {rot} rotated elements are not a multiple of 16 up to {d}")
     return rot
+
+
+def _row_strides(t, what):
+    """Batch, head and token strides of t [B, H, N, d] with whole rows (those of
+    dimensions of size 1, where torch leaves any number, as 0 if they are odd)."""
+    b, h, n, one = t.stride()
+    if one != 1 and t.numel():
+        raise ValueError(f"{what}: a head's elements must be contiguous")
+    if (b | h | n) & 7:
+        b, h, n = (s if size > 1 else 0 for s, size in zip((b, h, n), t.shape))
+    return b, h, n
 
 
 def _rows_differ(t):
@@ -1289,54 +1302,65 @@ def _rows_differ(t):
     return True
 
 
+_NO_STRIDES = (0, 0, 0)
+
+
 def _rotary(what, q, k, freqs, positions, seqlens, mscale, interleaved, inverse, out, stream):
-    import torch
     dtype, device = q.dtype, q.device
     code = dtype_code(dtype)
-    tensors = [q] if k is None else [q, k]
-    if any(x.dim() != 4 for x in tensors):
-        raise ValueError(f"{what}: q must be [B, H, N, d] and k [B, Hk, N, d]")
+    if q.dim() != 4:
+        raise ValueError(f"{what}: q must be [B, H, N, d]")
     B, H, N, d = q.shape
+    si, so = _row_strides(q, what), _NO_STRIDES
+    Hk, ki, ko, k_at, ko_at = 0, _NO_STRIDES, _NO_STRIDES, None, None
     if k is not None:
-        if k.dtype != dtype:
+        if k.dtype is not dtype:
             raise TypeError(f"dtypes differ: {dtype}, {k.dtype}")
-        if k.shape[0] != B or k.shape[2:] != q.shape[2:]:
+        if k.dim() != 4:
+            raise ValueError(f"{what}: k must be [B, Hk, N, d]")
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
             raise ValueError(f"{what}: q and k differ in batch, tokens or head width")
-    if not all(x.is_cuda and x.device == device for x in tensors):
+        ki, k_at = _row_strides(k, what), k.data_ptr()
+    if not q.is_cuda or (k is not None and k.device != device):
         raise ValueError(f"{what}: q and k must be CUDA tensors of one device")
-    for x in tensors:
-        if x.stride(3) != 1 and x.numel():
-            raise ValueError(f"{what}: a head's elements must be contiguous")
-    if positions is not None and seqlens is not None:
-        raise ValueError(f"{what}: give positions or seqlens, not both")
     if positions is not None:
+        if seqlens is not None:
+            raise ValueError(f"{what}: give positions or seqlens, not both")
         _check_int32(positions, (B, N), device, "positions", what)
     if seqlens is not None:
         _check_int32(seqlens, (B,), device, "seqlens", what)
     rot = _check_freqs(freqs, d, device, what)
     if out is not None:
-        out = tuple(out)
-        if len(out) != 2 or (out[1] is None) != (k is None):
+        qo, ko_t = out
+        if (ko_t is None) != (k is None):
             raise ValueError(f"{what}: out must be a pair like (q, k)")
-        for x, y in zip(tensors, out):
-            if y.shape != x.shape or y.dtype != dtype or y.device != device \
-                    or (y.stride(3) != 1 and y.numel()) or not _rows_differ(y):
+        for x, y in ((q, qo), (k, ko_t)):
+            if x is not None and (y.shape != x.shape or y.dtype is not dtype or y.device != device
+                                  or not _rows_differ(y)):
                 raise ValueError(f"{what}: out must be like q and k, with rows of its own")
+        so = _row_strides(qo, what)
+        if k is not None:
+            ko = _row_strides(ko_t, what)
     with _on(stream, device):
         if out is None:
-            out = tuple(torch.empty(x.shape, dtype=dtype, device=device) for x in tensors)
-        strides = [0] * 12
-        for i, (x, y) in enumerate(zip(tensors, out)):
-            strides[6 * i:6 * i + 6] = [n if x.shape[j % 3] > 1 else 0 for j, n in
-                                        enumerate(x.stride()[:3] + y.stride()[:3])]
+            import torch
+            rows = N * d
+            qo, so = torch.empty((B, H, N, d), dtype=dtype, device=device), (H * rows, rows, d)
+            ko_t = None
+            if k is not None:
+                ko_t = torch.empty((B, Hk, N, d), dtype=dtype, device=device)
+                ko = (Hk * rows, rows, d)
+        if k is not None:
+            ko_at = ko_t.data_ptr()
         rc = load_library().fa_rotary(
-            q.data_ptr(), None if k is None else k.data_ptr(), out[0].data_ptr(),
-            None if k is None else out[1].data_ptr(), B, H, 0 if k is None else k.shape[1], N, d,
-            _longs(strides), freqs.data_ptr(), rot, float(mscale), int(bool(interleaved)), inverse,
-            _addr(positions), _addr(seqlens), code, _current(stream, q))
+            q.data_ptr(), k_at, qo.data_ptr(), ko_at, B, H, Hk, N, d,
+            _PACK12(*si, *so, *ki, *ko), freqs.data_ptr(), rot, mscale, bool(interleaved), inverse,
+            None if positions is None else positions.data_ptr(),
+            None if seqlens is None else seqlens.data_ptr(), code, _current(stream, q))
     if rc != FA_OK:
         raise FaError(rc, "fa_rotary")
-    return out[0], None if k is None else out[1]
+    return qo, ko_t
 
 
 def rotary_forward(q, k, freqs, positions=None, seqlens=None, mscale=1.0, interleaved=False, out=None,
@@ -1407,31 +1431,34 @@ def _cache_code(dtype):
 
 def _paged_args(cache, page_table, seqlens, what):
     """Checks shared by the cache calls; returns (pages, Hk, page_size, d), B,
-    pages_per_seq and the codes' dtype."""
+    pages_per_seq, the codes' dtype and the device."""
     import torch
     k, v, k_scale, v_scale = cache
-    device = k.device
+    device, shape = k.device, k.shape
     code = _cache_code(k.dtype)
-    if v.dtype != k.dtype:
+    if v.dtype is not k.dtype:
         raise TypeError(f"dtypes differ: {k.dtype}, {v.dtype}")
-    if k.dim() != 4 or v.shape != k.shape:
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError(f"{what}: the cache's k and v must be [pages, Hk, page_size, d]")
     if not k.is_cuda or v.device != device:
         raise ValueError(f"{what}: the cache must be CUDA tensors of one device")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError(f"{what}: the cache's k and v must be contiguous")
+    per_head = shape[:2]
     for s in (k_scale, v_scale):
-        if s.dtype != torch.float32 or s.shape != k.shape[:2] or s.device != device \
-                or not s.is_contiguous():
+        if (s.dtype is not torch.float32 or s.shape != per_head or s.device != device
+                or not s.is_contiguous()):
             raise ValueError(f"{what}: the cache's scales must be contiguous float32 [pages, Hk] on "
                              "its device")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != device \
-            or not page_table.is_contiguous():
+    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != device
+            or not page_table.is_contiguous()):
         raise ValueError(f"{what}: page_table must be a contiguous int32 tensor [B, pages_per_seq] "
                          "on the cache's device")
     B, per_seq = page_table.shape
-    _check_int32(seqlens, (B,), device, "seqlens", what)
-    return k.shape, B, per_seq, code
+    if (seqlens.dtype is not torch.int32 or seqlens.shape != (B,) or seqlens.device != device
+            or not seqlens.is_contiguous()):
+        raise ValueError(f"{what}: seqlens must be a contiguous int32 tensor [B] on the cache's device")
+    return shape, B, per_seq, code, device
 
 
 def cache_append(k, v, cache, page_table, seqlens, counts=None, freqs=None, positions=None, mscale=1.0,
@@ -1452,34 +1479,32 @@ def cache_append(k, v, cache, page_table, seqlens, counts=None, freqs=None, posi
     that the call writes must belong to one sequence each.
     """
     what = "cache_append"
-    dtype, device = k.dtype, cache.k.device
+    dtype = k.dtype
     code = dtype_code(dtype)
-    if v.dtype != dtype:
+    if v.dtype is not dtype:
         raise TypeError(f"dtypes differ: {dtype}, {v.dtype}")
-    if k.dim() != 4 or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError(f"{what}: k and v must be [B, Hk, T, d]")
-    (pages, Hk, page_size, d), B, per_seq, cache_code = _paged_args(cache, page_table, seqlens, what)
-    T = k.shape[2]
-    if k.shape != (B, Hk, T, d):
+    (pages, Hk, page_size, d), B, per_seq, cache_code, device = _paged_args(cache, page_table,
+                                                                            seqlens, what)
+    T = shape[2]
+    if shape != (B, Hk, T, d):
         raise ValueError(f"{what}: k and v differ from the cache or its table in batch, heads or width")
     if k.device != device or v.device != device:
         raise ValueError(f"{what}: k and v must be on the cache's device")
-    if k.numel() and (k.stride(3) != 1 or v.stride(3) != 1):
-        raise ValueError(f"{what}: a head's elements must be contiguous")
     if counts is not None:
         _check_int32(counts, (B,), device, "counts", what)
     if positions is not None:
         _check_int32(positions, (B, T), device, "positions", what)
     rot = 0 if freqs is None else _check_freqs(freqs, d, device, what)
-    strides = [n if k.shape[j % 3] > 1 else 0 for j, n in
-               enumerate(k.stride()[:3] + v.stride()[:3])]
+    strides = _PACK6(*_row_strides(k, what), *_row_strides(v, what))
     with _on(stream, device):
         rc = load_library().fa_cache_append(
-            k.data_ptr(), v.data_ptr(), B, Hk, T, d, _longs(strides), cache.k.data_ptr(),
+            k.data_ptr(), v.data_ptr(), B, Hk, T, d, strides, cache.k.data_ptr(),
             cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), pages, page_size,
             page_table.data_ptr(), per_seq, seqlens.data_ptr(), _addr(counts), _addr(freqs), rot,
-            float(mscale), int(bool(interleaved)), _addr(positions), code, cache_code,
-            _current(stream, k))
+            mscale, bool(interleaved), _addr(positions), code, cache_code, _current(stream, k))
     if rc != FA_OK:
         raise FaError(rc, "fa_cache_append")
 
@@ -1494,11 +1519,11 @@ def cache_read(cache, page_table, seqlens, length=None, dtype=None, out=None, st
     what = "cache_read"
     dtype = torch.bfloat16 if dtype is None else dtype
     code = dtype_code(dtype)
-    (pages, Hk, page_size, d), B, per_seq, cache_code = _paged_args(cache, page_table, seqlens, what)
+    (pages, Hk, page_size, d), B, per_seq, cache_code, device = _paged_args(cache, page_table,
+                                                                            seqlens, what)
     N = per_seq * page_size if length is None else int(length)
     if N < 0:
         raise ValueError(f"{what}: length must not be negative")
-    device = cache.k.device
     if out is not None:
         out = tuple(out)
         if len(out) != 2:
@@ -1545,22 +1570,23 @@ def attention_decode_paged(q, cache, page_table, seqlens, window=None, sinks=0, 
     """
     import torch
     what = "attention_decode_paged"
-    dtype, device = q.dtype, q.device
+    dtype, shape = q.dtype, q.shape
     code = dtype_code(dtype)
-    (pages, Hk, page_size, d), B, per_seq, cache_code = _paged_args(cache, page_table, seqlens, what)
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
+    (pages, Hk, page_size, d), B, per_seq, cache_code, device = _paged_args(cache, page_table,
+                                                                            seqlens, what)
+    if len(shape) != 4 or shape[0] != B or shape[3] != d:
         raise ValueError(f"{what}: q must be [B, H, Nq, d] with the page table's B and the cache's d")
-    _, H, Nq, _ = q.shape
+    _, H, Nq, _ = shape
     if Hk == 0 or H % Hk:
         raise ValueError(f"{what}: {H} query heads are not a multiple of {Hk} key/value heads")
     if window is not None and window < 1:
         raise ValueError(f"{what}: window must be at least 1")
     if sinks < 0:
         raise ValueError(f"{what}: sinks must not be negative")
-    if device != cache.k.device or not q.is_contiguous():
+    if q.device != device or not q.is_contiguous():
         raise ValueError(f"{what}: q must be contiguous, on the cache's device")
     if out is not None:
-        _check_buffer(out, q.shape, dtype, device, "out")
+        _check_buffer(out, shape, dtype, device, "out")
     if lse is not None:
         _check_buffer(lse, (B, H, Nq), torch.float32, device, "lse")
     with _on(stream, device):
