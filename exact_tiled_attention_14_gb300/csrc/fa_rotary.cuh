@@ -11,8 +11,10 @@
 // product with the position, wrapped at 64 bits as integers wrap, is the
 // angle's fraction of a turn with an error of p * 2^-65 turns whatever its
 // whole turns: 2^-44 at position 2^20, where a float32 angle is off by whole
-// radians.  The fraction is cut to the nearest quarter turn, and the rest,
-// at most an eighth, goes through sincospif in float32.
+// radians.  The fraction is cut to the nearest quarter turn; the rest, at most
+// an eighth, goes in 32 bits (to 2^-34 turns) through the Taylor polynomials of
+// sine and cosine, of which the first terms left out are 2e-9 and 2.5e-8 there
+// (about 30 instructions a pair; sincospif with its own reduction took 70).
 #pragma once
 
 #include <cstdint>
@@ -25,16 +27,26 @@ __device__ __forceinline__ void rotary_cos_sin(int pos, unsigned long long freq,
                                                float& c, float& s) {
   const unsigned long long turn =
       static_cast<unsigned long long>(static_cast<long long>(pos)) * freq;
-  const unsigned long long near = turn + (1ull << 61);
-  const int quarter = static_cast<int>(near >> 62);
-  const long long rest = static_cast<long long>(turn - (near & (3ull << 62)));
-  float sn, cs;
-  sincospif(__ll2float_rn(rest) * 1.0842021724855044e-19f, &sn, &cs);   // half turns: 2^-63
-  const float x = (quarter & 1) ? sn : cs, y = (quarter & 1) ? cs : sn;
-  c = (quarter == 1 || quarter == 2) ? -x : x;
-  s = quarter >= 2 ? -y : y;
-  c *= mscale;
-  s *= mscale;
+  const uint32_t quarter = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
+  // the rest in units of 2^-34 turns: the two top bits leave by themselves
+  const int rest = static_cast<int>(static_cast<uint32_t>(turn >> 30));
+  const float x = static_cast<float>(rest) * 3.6572954e-10f;      // 2 pi 2^-34
+  const float y = x * x;
+  // x - x^3 / 3! + x^5 / 5! - x^7 / 7! + x^9 / 9!
+  float sn = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  sn = fmaf(y, sn, 1.f / 120.f);
+  sn = fmaf(y, sn, -1.f / 6.f);
+  sn = fmaf(x * y, sn, x);
+  // 1 - x^2 / 2! + x^4 / 4! - x^6 / 6! + x^8 / 8!
+  float cs = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
+  cs = fmaf(y, cs, 1.f / 24.f);
+  cs = fmaf(y, cs, -0.5f);
+  cs = fmaf(y, cs, 1.f);
+  // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
+  const bool odd = quarter & 1u;
+  const float u = (odd ? sn : cs) * mscale, v = (odd ? cs : sn) * mscale;
+  c = __uint_as_float(__float_as_uint(u) ^ ((quarter + 1u & 2u) << 30));
+  s = __uint_as_float(__float_as_uint(v) ^ ((quarter & 2u) << 30));
 }
 
 // Sixteen elements of a row that are turned together: eight pairs, or sixteen

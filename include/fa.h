@@ -782,7 +782,7 @@ int fa_rotary(const void *q, const void *k, void *q_out, void *k_out, int B, int
  * Errors: FA_ERR_SHAPE (negative sizes; no pages; page_size; B * Hk, B * T,
  * B * pages_per_seq, or pages or pages_per_seq times page_size over 2^30, the
  * pool's rows 2^31 or more), FA_ERR_UNSUPPORTED_D, FA_ERR_DTYPE (cache_dtype),
- * FA_ERR_SHAPE (T, rot), FA_ERR_DTYPE, FA_ERR_SCALE, then B * Hk * T == 0
+ * FA_ERR_SHAPE (T, Hk over 65535, rot), FA_ERR_DTYPE, FA_ERR_SCALE, then B * Hk * T == 0
  * returns FA_OK, then FA_ERR_NULLPTR, FA_ERR_ALIGN, FA_ERR_DEVICE,
  * FA_ERR_LAUNCH.
  */
