@@ -32,50 +32,58 @@ cudaError_t launch_main(const DecPagedParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
-  kernel<<<p.out.grid, DpLayout<D, kTiles>::kThreads, kAlloc, stream>>>(p);
+  kernel<<<p.grid, DpLayout<D, kTiles>::kThreads, kAlloc, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool kBf16, bool kInt8>
-cudaError_t launch_variant(const DecPagedParams& p, cudaStream_t stream) {
-  cudaError_t e = p.out.row_span == 8    ? launch_main<D, kBf16, kInt8, 1>(p, stream)
-                  : p.out.row_span == 16 ? launch_main<D, kBf16, kInt8, 2>(p, stream)
-                                         : launch_main<D, kBf16, kInt8, 4>(p, stream);
+cudaError_t launch_variant(const DecPagedParams& p, int tiles, int sms, cudaStream_t stream) {
+  cudaError_t e = tiles == 1   ? launch_main<D, kBf16, kInt8, 1>(p, stream)
+                  : tiles == 2 ? launch_main<D, kBf16, kInt8, 2>(p, stream)
+                               : launch_main<D, kBf16, kInt8, 4>(p, stream);
   if (e != cudaSuccess) return e;
+  // Programmatic dependent launch: the combine grid is set up while the main
+  // kernel runs its last CTAs, and waits on the device for the parts.  Blocks
+  // take several units where those are many, since most are whole then, and
+  // more threads where a unit may have many parts.
+  const int units = p.B * p.Hk * p.row_blocks, per_block = (units + 4 * sms - 1) / (4 * sms);
+  constexpr int kFew = 512 / D, kMany = 2048 / D;     // groups of D / 4 threads
+  const bool many = p.runs > 8 * kFew * units;
   cudaLaunchConfig_t cfg = {};
-  const int rows = 1 << p.out.combine_rows;
-  const int groups = std::max(D / 4 * rows / kDwCombineThreads, 1);
-  cfg.gridDim = dim3(p.out.grid, (p.out.slot_rows + rows - 1) / rows * groups);
-  cfg.blockDim = dim3(kDwCombineThreads);
+  cfg.gridDim = dim3((units + per_block - 1) / per_block, p.slot_rows);
+  cfg.blockDim = dim3((many ? kMany : kFew) * (D / 4));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_decode_win_combine_kernel<D, kBf16, 8>, p.out);
+  return many ? cudaLaunchKernelEx(&cfg, fa_decode_paged_combine_kernel<D, kBf16, kMany>, p, units,
+                                   per_block)
+              : cudaLaunchKernelEx(&cfg, fa_decode_paged_combine_kernel<D, kBf16, kFew>, p, units,
+                                   per_block);
 }
 
 constexpr int kMaxTokens = 16;
 
-// Rows of a unit (8, 16 or 32), grid (one CTA per SM, or one per key tile where
-// there are fewer) and the workspace: two parts per CTA, and the run table.
+// Row tiles of a unit (1, 2 or 4 of 8 rows), runs (one per warp of a CTA per SM,
+// or fewer) and the workspace: two parts per run, and the units' table.
 struct Plan {
-  int row_span, row_blocks, slot_rows, grid;
+  int tiles, row_blocks, slot_rows, grid, runs;
   size_t o_bytes, ml_bytes, bytes;
 };
+int row_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : 4; }
 // Tiles of all units at most: whole capacities, and one of each sequence's own.
 long long max_tiles(int B, int Hk, int row_blocks, int d, int capacity) {
   const long long tiles = (static_cast<long long>(capacity) + dp_keys(d) - 1) / dp_keys(d) + 1;
   return static_cast<long long>(B) * Hk * row_blocks * tiles;
 }
-int row_span_of(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 int check_sizes(int B, int H, int Hk, int Nq, int d, int page_size, int pages_per_seq) {
   if (H < 0 || (H > 0 ? (Hk <= 0 || H % Hk != 0) : Hk != 0)) return FA_ERR_SHAPE;
   if (Nq < 1 || Nq > kMaxTokens) return FA_ERR_SHAPE;
   if (static_cast<long long>(B) * H * Nq > (1 << 30)) return FA_ERR_SHAPE;
   if (B == 0 || H == 0) return FA_OK;
-  const int R = H / Hk * Nq, span = row_span_of(R);
+  const int R = H / Hk * Nq, span = 8 * row_tiles(R);
   // the numbers of all tiles fit in int
   if (max_tiles(B, Hk, (R + span - 1) / span, d, pages_per_seq * page_size) >= (1ll << 31))
     return FA_ERR_SHAPE;
@@ -84,15 +92,18 @@ int check_sizes(int B, int H, int Hk, int Nq, int d, int page_size, int pages_pe
 Plan make_plan(int B, int H, int Hk, int Nq, int d, int capacity, int sms) {
   Plan pl{};
   const int R = H / Hk * Nq;
-  pl.row_span = row_span_of(R);
-  pl.row_blocks = (R + pl.row_span - 1) / pl.row_span;
-  pl.slot_rows = std::min(R, pl.row_span);
-  pl.grid = static_cast<int>(
-      std::min<long long>(max_tiles(B, Hk, pl.row_blocks, d, capacity), sms));
-  const size_t rows = 2 * static_cast<size_t>(pl.grid) * pl.slot_rows;
+  pl.tiles = row_tiles(R);
+  pl.row_blocks = (R + 8 * pl.tiles - 1) / (8 * pl.tiles);
+  pl.slot_rows = std::min(R, 8 * pl.tiles);
+  const long long min_tiles = dp_min_tiles(pl.tiles), warps = dp_warps(pl.tiles);
+  const long long all = (max_tiles(B, Hk, pl.row_blocks, d, capacity) + min_tiles - 1) / min_tiles;
+  pl.runs = static_cast<int>(std::min(all, sms * warps));
+  pl.grid = std::min(pl.runs, sms);
+  const size_t rows = 2 * static_cast<size_t>(pl.runs) * pl.slot_rows;
   pl.o_bytes = (rows * d * sizeof(float) + 255) / 256 * 256;
   pl.ml_bytes = (rows * sizeof(float2) + 255) / 256 * 256;
-  pl.bytes = pl.o_bytes + pl.ml_bytes + (pl.grid * sizeof(int4) + 255) / 256 * 256;
+  const size_t units = static_cast<size_t>(B) * Hk * pl.row_blocks;
+  pl.bytes = pl.o_bytes + pl.ml_bytes + (units * sizeof(int2) + 255) / 256 * 256;
   return pl;
 }
 
@@ -162,45 +173,47 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, con
   p.per_seq = pages_per_seq;
   p.pages = pages;
   p.page = page_size;
-  fa::DecWinParams& out = p.out;
-  out.o = o;
-  out.lse = lse;
-  out.part_o = static_cast<float4*>(workspace);
-  out.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + pl.o_bytes);
-  out.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + pl.o_bytes + pl.ml_bytes);
-  out.status = info->status;
+  p.page_magic = page_size == fa::kPageRows
+                     ? 0
+                     : static_cast<uint32_t>(((1ull << 32) + page_size / fa::kPageRows - 1) /
+                                             (page_size / fa::kPageRows));
+  p.o = o;
+  p.lse = lse;
+  p.part_o = static_cast<float4*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + pl.o_bytes);
+  p.cut = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + pl.o_bytes + pl.ml_bytes);
+  p.status = info->status;
   const unsigned long long wd = g_watchdog_ns.load();
-  out.watchdog_cycles = (wd ? wd : kDefaultWatchdogNs) * 21ull / 10ull;
-  out.seqlens = seqlens;
-  out.B = B;
-  out.Hk = Hk;
-  out.Nq = Nq;
-  out.R = H / Hk * Nq;
-  out.row_span = pl.row_span;
-  out.row_blocks = pl.row_blocks;
-  out.slot_rows = pl.slot_rows;
-  while (out.combine_rows < 5 && (1 << out.combine_rows) < pl.slot_rows) ++out.combine_rows;
-  out.grid = pl.grid;
+  p.watchdog_cycles = (wd ? wd : kDefaultWatchdogNs) * 21ull / 10ull;
+  p.seqlens = seqlens;
+  p.B = B;
+  p.Hk = Hk;
+  p.Nq = Nq;
+  p.R = H / Hk * Nq;
+  p.row_blocks = pl.row_blocks;
+  p.slot_rows = pl.slot_rows;
+  p.runs = pl.runs;
+  p.grid = pl.grid;
   const int all = capacity + Nq + 1;
-  out.win = window == 0 ? all : std::min(window, all);
-  out.sinks = std::min(sinks, capacity);
-  out.scale_log2 = scale * 1.4426950408889634f;
+  p.win = window == 0 ? all : std::min(window, all);
+  p.sinks = std::min(sinks, capacity);
+  p.scale_log2 = scale * 1.4426950408889634f;
   const bool bf16 = dtype == FA_BF16;
   cudaError_t e;
   if (cache_dtype == FA_INT8) {
     if (d == 64)
-      e = bf16 ? fa::launch_variant<64, true, true>(p, stream)
-               : fa::launch_variant<64, false, true>(p, stream);
+      e = bf16 ? fa::launch_variant<64, true, true>(p, pl.tiles, info->sms, stream)
+               : fa::launch_variant<64, false, true>(p, pl.tiles, info->sms, stream);
     else
-      e = bf16 ? fa::launch_variant<128, true, true>(p, stream)
-               : fa::launch_variant<128, false, true>(p, stream);
+      e = bf16 ? fa::launch_variant<128, true, true>(p, pl.tiles, info->sms, stream)
+               : fa::launch_variant<128, false, true>(p, pl.tiles, info->sms, stream);
   } else {
     if (d == 64)
-      e = bf16 ? fa::launch_variant<64, true, false>(p, stream)
-               : fa::launch_variant<64, false, false>(p, stream);
+      e = bf16 ? fa::launch_variant<64, true, false>(p, pl.tiles, info->sms, stream)
+               : fa::launch_variant<64, false, false>(p, pl.tiles, info->sms, stream);
     else
-      e = bf16 ? fa::launch_variant<128, true, false>(p, stream)
-               : fa::launch_variant<128, false, false>(p, stream);
+      e = bf16 ? fa::launch_variant<128, true, false>(p, pl.tiles, info->sms, stream)
+               : fa::launch_variant<128, false, false>(p, pl.tiles, info->sms, stream);
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }

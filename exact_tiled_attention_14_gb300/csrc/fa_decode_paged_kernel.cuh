@@ -29,11 +29,13 @@
 //
 // Split.  A unit is (batch, K/V head, block of 8 kTiles rows); its keys are
 // tiles of kKeys (4 KB of K and of V).  The tiles of all units are laid end to
-// end and cut into equal runs, one per CTA; the warps of a CTA take its tiles
-// in turn, each with a ring of its own that its lanes fill by TMA, and are
-// merged at the end of each unit.  A unit cut by a run's end leaves its parts
-// in the workspace; fa_decode_win_combine_kernel adds them up in the order of
-// the runs.
+// end and cut into equal runs, one per warp, whatever the sequences' lengths,
+// which only the device knows.  Warps share nothing: each has its ring, which
+// its lanes fill by TMA, and its queries, so none ever waits for another.  A
+// unit that lies in one run is finished there; of a cut unit each warp leaves
+// its part in the workspace, and a second kernel adds the parts up in the order
+// of the runs: no atomics.  (Warps of a CTA sharing its tiles, merged at the
+// end of each unit, cost 3.6 us a unit: 4096 units of one tile took 98 us.)
 #pragma once
 
 #include <cuda.h>
@@ -46,8 +48,13 @@
 namespace fa {
 
 // Warps of a CTA by its row tiles (8 rows each).
-__host__ __device__ constexpr int dp_warps(int tiles) { return tiles == 1 ? 12 : 8; }
+__host__ __device__ constexpr int dp_warps(int tiles) {
+  return tiles == 1 ? 12 : tiles == 2 ? 10 : 8;
+}
 constexpr int kDpTileBytes = 4096;       // of K, and of V
+// A run takes this many tiles at least (2, 3, 4 by its row tiles): a part is 4 KB
+// for each row tile at d = 128, a tile 8 KB.
+__host__ __device__ constexpr int dp_min_tiles(int tiles) { return tiles < 3 ? tiles + 1 : 4; }
 constexpr float kDpTau = 8.0f;           // lazy-rescale threshold, log2 units
 constexpr uint32_t kSiteDpFull = 50;
 __host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
@@ -55,14 +62,31 @@ __host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
 struct DecPagedParams {
   CUtensorMap tm_k;        // [pages * Hk * page, d] bytes, boxes of box_rows rows
   CUtensorMap tm_v;
-  DecWinParams out;        // o, lse, parts, run table and sizes, as the combine reads them
   const void* q;           // [B * Hk, R, d]
+  void* o;                 // [B * Hk, R, d]
+  float* lse;              // [B * Hk, R]
+  float4* part_o;          // [2 * runs, slot_rows, d / 4] unnormalised parts
+  float2* part_ml;         // [2 * runs, slot_rows] (m in log2 units, l)
+  int2* cut;               // [units] (slot of the unit's first part, run of its last), (-1, 0): whole
   const float* k_scale;    // [pages, Hk]
   const float* v_scale;
   const int* table;        // [B, per_seq]
+  const int* seqlens;      // [B]
+  unsigned int* status;
+  unsigned long long watchdog_cycles;
+  int B, Hk, Nq;
+  int R;                   // rows of a head: G * Nq, row g * Nq + i
+  int row_blocks;          // units per head
+  int slot_rows;           // rows of a unit's part
   int per_seq, pages, page;
+  uint32_t page_magic;     // ceil(2^32 / (page / 16)), 0 for pages of 16
   int boxes;               // boxes of a tile: 1, or one per 16 keys where pages are no multiples
                            // of a tile
+  int runs;                // at most
+  int grid;
+  int win;                 // >= 1; larger than every position: no window
+  int sinks;
+  float scale_log2;
 };
 
 // Keys that the rows of a batch see, as tiles: the sinks' tiles before the
@@ -111,22 +135,22 @@ __host__ __device__ constexpr uint32_t dp_chunk(int r, int c) {
   return D == 128 ? r * 128u + ((c ^ (r & 7)) << 4) : r * 64u + ((c ^ (r >> 1 & 3)) << 4);
 }
 
+// Shared memory: the warps' rings, then each warp's queries, weights and scales.
 template <int D, int kTiles>
 struct DpLayout {
   static constexpr int kRows = 8 * kTiles;
-  static constexpr int kWarps = dp_warps(kTiles), kThreads = 32 * kWarps, kHalf = kWarps / 2;
+  static constexpr int kWarps = dp_warps(kTiles), kThreads = 32 * kWarps;
   static constexpr int kStages = 2;
-  static constexpr int kRing = 0;
-  static constexpr int kQ = kRing + kWarps * kStages * 2 * kDpTileBytes;
-  static constexpr int kSum = kQ + kRows * D * 2;             // half the warps' O
-  static constexpr int kP = kSum + kHalf * kRows * D * 4;     // the warps' weights
-  static constexpr int kMl = kP + kWarps * (kDpTileBytes / D / 16) * kTiles * 256;   // (m, l) [warp][row]
-  static constexpr int kQmul = kMl + kWarps * kRows * 8;    // [row]
-  static constexpr int kMeta = kQmul + kRows * 4;             // [warp][stage]: 4 K, 4 V scales
-  static constexpr int kBar = kMeta + kWarps * kStages * 32;
-  static constexpr int kMisc = kBar + 8 * kWarps * kStages;
+  static constexpr int kRing = kStages * 2 * kDpTileBytes;    // of a warp
+  static constexpr int kQ = 0;                                // within a warp's own
+  static constexpr int kP = kQ + kRows * D * 2;
+  static constexpr int kQmul = kP + dp_keys(D) / 16 * kTiles * 256;
+  static constexpr int kMeta = kQmul + kRows * 4;             // [stage]: 4 K, 4 V scales
+  static constexpr int kBar = kMeta + kStages * 32;
+  static constexpr int kOwn = kBar + kStages * 8;
+  static constexpr int kMisc = kWarps * (kRing + kOwn);
   static constexpr int kAlloc = kMisc + 16 + 1024;
-  static_assert(kAlloc <= 232448, "shared memory budget");
+  static_assert(kOwn % 16 == 0 && kAlloc <= 232448, "shared memory budget");
 };
 
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* tm, uint32_t bar,
@@ -161,9 +185,9 @@ __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A place in the list of all tiles: batch, unit of the batch, tile of the unit.
+// A place in the list of all tiles.
 struct DpPlace {
-  int b, unit, tile;
+  int b, hk, block, tile;
   PagedSpan s;
 };
 
@@ -182,38 +206,50 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
   uint8_t* const sgen = smem_raw + (sbase - raw_base);
   const int warp = ptx::warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const DecWinParams& po = p.out;
-  const int units = po.Hk * po.row_blocks;   // of a batch
   const int capacity = p.per_seq * p.page;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc);
-  const ptx::Watchdog wd{po.watchdog_cycles, abort_flag, po.status};
+  const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
+  const uint32_t ring = sbase + warp * L::kRing;
+  uint8_t* const ring_gen = sgen + warp * L::kRing;
+  const uint32_t own = sbase + L::kWarps * L::kRing + warp * L::kOwn;
+  uint8_t* const own_gen = sgen + L::kWarps * L::kRing + warp * L::kOwn;
+  uint2* const q_s = reinterpret_cast<uint2*>(own_gen + L::kQ);
+  uint2* const p_s = reinterpret_cast<uint2*>(own_gen + L::kP);
+  float* const qmul_s = reinterpret_cast<float*>(own_gen + L::kQmul);
+  const float* const meta_gen = reinterpret_cast<const float*>(own_gen + L::kMeta);
+  auto bar = [&](int stage) -> uint32_t { return own + L::kBar + 8u * stage; };
 
   ptx::griddep_launch_dependents();
-  auto bar = [&](int stage) -> uint32_t { return sbase + L::kBar + 8u * (warp * kStages + stage); };
-  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    ptx::prefetch_tmap(&p.tm_k);
+    ptx::prefetch_tmap(&p.tm_v);
+  }
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) ptx::mbar_init(bar(i), 1);
     ptx::fence_mbar_init();
   }
-  __syncthreads();
+  __syncthreads();                           // (the abort flag; the only one)
 
+  // ---- the warp's run and its first place
+  const int units = p.Hk * p.row_blocks;     // of a batch
   auto span_of = [&](int b) {
-    return paged_span(po.seqlens[b], capacity, po.Nq, po.win, po.sinks, kKeys);
+    return paged_span(p.seqlens[b], capacity, p.Nq, p.win, p.sinks, kKeys);
   };
-  // ---- the CTA's run and its first place (each warp for itself)
   int total = 0;
-  for (int b = lane; b < po.B; b += 32) total += span_of(b).tiles * units;
+  for (int b = lane; b < p.B; b += 32) total += span_of(b).tiles * units;
   total = __reduce_add_sync(0xffffffffu, total);
-  const DecDeal deal = dec_deal(total, po.grid);
-  const int run = blockIdx.x;
-  int left = 0;
+  constexpr int kMin = dp_min_tiles(kTiles);
+  const DecDeal deal = dec_deal(total, min(p.runs, (total + kMin - 1) / kMin));
+  const int run = warp * p.grid + blockIdx.x;    // few runs spread over the SMs
+  if (run >= deal.runs) return;
+  const int start = dec_run_start(deal, run);
+  int left = dec_run_start(deal, run + 1) - start;   // tiles not begun
   DpPlace at{};
-  if (run < deal.runs) {
-    const int start = dec_run_start(deal, run);
-    left = dec_run_start(deal, run + 1) - start;
+  {
     int before = 0;
-    for (int b0 = 0; b0 < po.B; b0 += 32) {
-      const int mine = b0 + lane < po.B ? span_of(b0 + lane).tiles * units : 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int mine = b0 + lane < p.B ? span_of(b0 + lane).tiles * units : 0;
       int upto = mine;
 #pragma unroll
       for (int i = 1; i < 32; i *= 2) {
@@ -226,54 +262,42 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         at.b = b0 + k;
         at.s = span_of(at.b);
         const int skip = start - (before + __shfl_sync(0xffffffffu, upto - mine, k));
-        at.unit = skip / at.s.tiles;
-        at.tile = skip - at.unit * at.s.tiles;
+        const int unit = skip / at.s.tiles;
+        at.tile = skip - unit * at.s.tiles;
+        at.hk = unit / p.row_blocks;
+        at.block = unit - at.hk * p.row_blocks;
         break;
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  const int n_tiles = left;                  // of the run
-  auto advance = [&](DpPlace& x, int n) {
-    x.tile += n;
-    while (x.tile >= x.s.tiles) {
-      x.tile -= x.s.tiles;
-      if (++x.unit == units) {
-        x.unit = 0;
-        if (++x.b == po.B) {                 // past the last tile
-          x.b = po.B - 1;
-          x.tile = 0;
-          return;
-        }
-        x.s = span_of(x.b);
-      }
-    }
+  auto next_unit = [&](DpPlace& x) {         // (past the last unit: a place never used)
+    x.tile = 0;
+    if (++x.block < p.row_blocks) return;
+    x.block = 0;
+    if (++x.hk < p.Hk) return;
+    x.hk = 0;
+    if (++x.b < p.B) x.s = span_of(x.b);
   };
 
-  // ---- the warp's loads: tile i of the run goes to warp i % L::kWarps
-  const uint32_t ring = sbase + L::kRing + warp * (kStages * 2 * kDpTileBytes);
-  uint8_t* const ring_gen = sgen + L::kRing + warp * (kStages * 2 * kDpTileBytes);
-  const uint32_t meta = sbase + L::kMeta + warp * (kStages * 32);
-  const float* const meta_gen =
-      reinterpret_cast<const float*>(sgen + L::kMeta + warp * (kStages * 32));
+  // ---- the warp's loads
   const int box_rows = kKeys / p.boxes;
   DpPlace nx = at;                           // the next tile to load
-  int nx_i = warp;                           // its number in the run
+  int nx_left = left;                        // tiles from it on
   int nx_page = -1, nx_row = 0;              // page of the lane's box, its first row in the page
   uint32_t valid = 0;                        // 4 bits per stage: boxes that name a page
-  int loaded = 0;                            // tiles that the warp has asked for
+  int loaded = 0, waited = 0;                // tiles asked for, tiles that have arrived
   auto look = [&]() {                        // the page of the lane's box of tile nx
     nx_page = -1;
-    if (nx_i < n_tiles && lane < p.boxes) {
+    if (nx_left > 0 && lane < p.boxes) {
       const int key = paged_key0(nx.s, nx.tile, kKeys) + lane * box_rows;
-      const int nth = key / p.page;
+      const int nth = p.page_magic ? __umulhi(key >> 4, p.page_magic) : key >> 4;
       nx_row = key - nth * p.page;
       if (key < nx.s.len) nx_page = p.table[static_cast<size_t>(nx.b) * p.per_seq + nth];
     }
   };
   auto load = [&](int stage) {               // into the stage; then look at the one after
-    if (nx_i < n_tiles) {
-      const int hk = nx.unit / po.row_blocks;
+    if (nx_left > 0) {
       const bool ok = nx_page >= 0 && nx_page < p.pages;
       const uint32_t have = __ballot_sync(0xffffffffu, ok);
       valid = (valid & ~(15u << (4 * stage))) | have << (4 * stage);
@@ -281,71 +305,71 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         ptx::mbar_arrive_expect_tx(bar(stage), __popc(have) * 2 * box_rows * D);
       __syncwarp();
       if (ok) {
-        const int head = nx_page * po.Hk + hk;
+        const int head = nx_page * p.Hk + nx.hk;
         const int row = head * p.page + nx_row;
         const uint32_t dst = ring + stage * (2 * kDpTileBytes) + lane * box_rows * D;
         tma_load_rows(dst, &p.tm_k, bar(stage), row);
         tma_load_rows(dst + kDpTileBytes, &p.tm_v, bar(stage), row);
-        cp_async4(meta + stage * 32 + lane * 4, p.k_scale + head);
-        cp_async4(meta + stage * 32 + 16 + lane * 4, p.v_scale + head);
+        const uint32_t meta = own + L::kMeta + stage * 32 + lane * 4;
+        cp_async4(meta, p.k_scale + head);
+        cp_async4(meta + 16, p.v_scale + head);
       }
       ++loaded;
-      nx_i += L::kWarps;
-      if (nx_i < n_tiles) advance(nx, L::kWarps);
+      --nx_left;
+      if (++nx.tile == nx.s.tiles) next_unit(nx);
       look();
     }
     cp_async_commit();                       // one group per tile, empty ones too
   };
-  if (nx_i < n_tiles) advance(nx, warp);
   look();
   for (int i = 0; i < kStages; ++i) load(i);
 
   // ---- pieces of units, in the order of the run
-  bool alive = true, cut_here = false;
-  int done = 0;                              // tiles of the run before the piece
-  int stage = 0, parity = 0, pieces = 0;
-  int waited = 0;                            // the warp's loads that have arrived
-  int mine = warp;                           // the warp's next tile in the run
-  uint2* const p_s = reinterpret_cast<uint2*>(sgen + L::kP) + warp * (kMt * kTiles * 32);
-  uint2* const q_s = reinterpret_cast<uint2*>(sgen + L::kQ);
-  float* const qmul_s = reinterpret_cast<float*>(sgen + L::kQmul);
-  float4* const sum_s = reinterpret_cast<float4*>(sgen + L::kSum);
-  float2* const ml_s = reinterpret_cast<float2*>(sgen + L::kMl);
-
-  while (done < n_tiles) {
+  bool alive = true;
+  int stage = 0, parity = 0, pieces = 0, done = 0;
+  for (; left > 0; next_unit(at), ++pieces) {
     const int tile0 = at.tile;
-    const int n = min(at.s.tiles - tile0, n_tiles - done);
+    const int n = min(at.s.tiles - tile0, left);
     const bool whole = tile0 == 0 && n == at.s.tiles;
-    const int hk = at.unit / po.row_blocks, block = at.unit - hk * po.row_blocks;
-    const size_t head = static_cast<size_t>(at.b) * po.Hk + hk;
-    const int row0 = block * po.row_span, rows = min(po.R - row0, po.row_span);
+    const size_t head = static_cast<size_t>(at.b) * p.Hk + at.hk;
+    const int row0 = at.block * L::kRows, rows = min(p.R - row0, L::kRows);
     const PagedSpan s = at.s;
+    left -= n;
 
     // queries of the unit: row r, elements 4 c .. 4 c + 3 as the B operand's
     // registers of lane (r % 8, 4 c / (D / 4)), in half precision
-    for (int r = warp; r < L::kRows; r += L::kWarps) {
-      uint2 raw = make_uint2(0, 0);
-      if (r < rows && lane * 4 < D)
-        raw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
-                                              (head * po.R + row0 + r) * D + lane * 4);
-      float x[4];
-      ptx::unpack2<kBf16>(raw.x, x[0], x[1]);
-      ptx::unpack2<kBf16>(raw.y, x[2], x[3]);
-      uint32_t top = 0;
+#pragma unroll 1
+    for (int nt = 0; nt < kTiles; ++nt) {
+      uint2 raw[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-      top = __reduce_max_sync(0xffffffffu, top);
-      int shift = 0;                         // the row times 2^shift
-      if (top != 0 && top < kInfBits) shift = min(12 - (static_cast<int>(top >> 23) - 127), 120);
-      const float mul = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
-      if (lane * 4 < D)
-        q_s[(lane % (D / 16) * kTiles + (r >> 3)) * 32 + (r & 7) * 4 + lane / (D / 16)] =
-            make_uint2(ptx::pack2<false>(x[0] * mul, x[1] * mul),
-                       ptx::pack2<false>(x[2] * mul, x[3] * mul));
-      if (lane == 0)
-        qmul_s[r] = po.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      for (int i = 0; i < 8; ++i) {
+        raw[i] = make_uint2(0, 0);
+        if (nt * 8 + i < rows && lane * 4 < D)
+          raw[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
+                                                   (head * p.R + row0 + nt * 8 + i) * D + lane * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[4];
+        ptx::unpack2<kBf16>(raw[i].x, x[0], x[1]);
+        ptx::unpack2<kBf16>(raw[i].y, x[2], x[3]);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        int shift = 0;                       // the row times 2^shift
+        if (top != 0 && top < kInfBits) shift = min(12 - (static_cast<int>(top >> 23) - 127), 120);
+        const float mul = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+        if (lane * 4 < D)
+          q_s[(lane % (D / 16) * kTiles + nt) * 32 + i * 4 + lane / (D / 16)] =
+              make_uint2(ptx::pack2<false>(x[0] * mul, x[1] * mul),
+                         ptx::pack2<false>(x[2] * mul, x[3] * mul));
+        if (lane == 0)
+          qmul_s[nt * 8 + i] =
+              p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+      }
     }
-    __syncthreads();
+    __syncwarp();
 
     float qmul[kTiles][2];
     int pos[kTiles][2];
@@ -356,16 +380,17 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * t + e;
         qmul[nt][e] = qmul_s[r];
-        pos[nt][e] = s.len - po.Nq + (row0 + r) % po.Nq;
+        pos[nt][e] = s.len - p.Nq + (row0 + r) % p.Nq;
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
       }
     float o[kJ][kTiles][4] = {};
     float vref = 0.f;                        // unit of O (0: nothing summed yet)
-    const int pos_lo = s.len - po.Nq, pos_hi = s.len - 1;
+    const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
 
-    for (; mine < done + n; mine += L::kWarps) {
-      const int key0 = paged_key0(s, tile0 + mine - done, kKeys);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int key0 = paged_key0(s, tile0 + i, kKeys);
       alive = ptx::warp_all(alive && ptx::wait_bounded(bar(stage), parity, wd, kSiteDpFull));
       cp_async_wait<kStages - 1>();
       __syncwarp();
@@ -376,14 +401,14 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       const uint32_t have = valid >> (4 * stage) & 15u;
       // every row sees every key of the tile
       const bool full = have == (1u << p.boxes) - 1u && key0 + kKeys - 1 <= pos_lo &&
-                        (key0 > pos_hi - po.win || key0 + kKeys <= po.sinks);
+                        (key0 > pos_hi - p.win || key0 + kKeys <= p.sinks);
       auto box_of = [&](int mt) { return p.boxes == 1 ? 0 : mt; };
       if (!full) {
         // values that no row sees weigh 0, and 0 times what they hold must be 0
         for (int i = lane; i < kKeys; i += 32) {
           const int key = key0 + i;
           const bool seen = (have >> box_of(i >> 4) & 1u) && key <= pos_hi &&
-                            (key > pos_lo - po.win || key < po.sinks);
+                            (key > pos_lo - p.win || key < p.sinks);
           if (!seen)
             for (int c = 0; c < D / 16; ++c)
               *reinterpret_cast<uint4*>(vt + i * D + c * 16) = make_uint4(0, 0, 0, 0);
@@ -395,14 +420,14 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       // ---- S^T, 16 bytes of each key row at a time
       float sv[kMt][kTiles][4] = {};
 #pragma unroll 1
-      for (int i = 0; i < kWords / 4; ++i) {
+      for (int c = 0; c < kWords / 4; ++c) {
         uint32_t w[kMt][2][4];               // rows dp_row(g) and + 8 of each 16
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint4 x = *reinterpret_cast<const uint4*>(
-                kt + dp_chunk<D>(mt * 16 + h * 8 + dp_row<D>(g), t * (kWords / 4) + i));
+                kt + dp_chunk<D>(mt * 16 + h * 8 + dp_row<D>(g), t * (kWords / 4) + c));
             w[mt][h][0] = x.x;
             w[mt][h][1] = x.y;
             w[mt][h][2] = x.z;
@@ -412,7 +437,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         for (int j = 0; j < 4; ++j) {
           uint2 qb[kTiles];
 #pragma unroll
-          for (int nt = 0; nt < kTiles; ++nt) qb[nt] = q_s[((i * 4 + j) * kTiles + nt) * 32 + lane];
+          for (int nt = 0; nt < kTiles; ++nt) qb[nt] = q_s[((c * 4 + j) * kTiles + nt) * 32 + lane];
 #pragma unroll
           for (int mt = 0; mt < kMt; ++mt) {
             uint32_t a0, a1, a2, a3;
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + mt * 16 + (e >> 1) * 8 + dp_row<D>(g), ps = pos[nt][e & 1];
               const bool see = (have >> box_of(mt) & 1u) && key <= ps &&
-                               (key > ps - po.win || key < po.sinks);
+                               (key > ps - p.win || key < p.sinks);
               if (!see) sv[mt][nt][e] = -INFINITY;
             }
       }
@@ -532,8 +557,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
           for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (paged_sees(key0 + box_of(mt) * box_rows, box_rows, pos[nt][e & 1], po.win,
-                             po.sinks))
+              if (paged_sees(key0 + box_of(mt) * box_rows, box_rows, pos[nt][e & 1], p.win,
+                             p.sinks))
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) o[j][nt][e] = NAN;
         }
@@ -584,111 +609,145 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       }
     }
 
-    // ---- merge of the warps, and the unit's result or its part
+    // ---- the unit's result or its part: a thread has D / 8 elements in a row of
+    // each of its rows
+    const int unit = (static_cast<int>(head) * p.row_blocks + at.block);
+    const size_t slot = 2 * static_cast<size_t>(run) + (pieces == 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        float lt = l[nt][e];
 #pragma unroll
-        for (int i = 4; i < 32; i *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], i);
-        if (m[nt][e] == -INFINITY) m[nt][e] = 0.f;
-        if (g == 0) ml_s[warp * L::kRows + nt * 8 + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
-      }
-    __syncthreads();
+        for (int k = 4; k < 32; k *= 2) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+        const float mt = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+        const int r = nt * 8 + 2 * t + e;
+        if (r >= rows) continue;
+        if (whole) {
+          const float f = lt != 0.f ? vref / lt : 0.f;
+          float x[2 * kJ];
 #pragma unroll
-    for (int nt = 0; nt < kTiles; ++nt) {
-      float f[2];
+          for (int j = 0; j < kJ; ++j) {
+            x[2 * j] = lt != 0.f ? o[j][nt][e] * f : 0.f;
+            x[2 * j + 1] = lt != 0.f ? o[j][nt][e + 2] * f : 0.f;
+          }
+          const size_t row = head * p.R + row0 + r;
+          uint4* const out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D) +
+                             g * (kJ / 4);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY;
+          for (int j = 0; j < kJ / 4; ++j)
+            out[j] = make_uint4(ptx::pack2<kBf16>(x[8 * j], x[8 * j + 1]),
+                                ptx::pack2<kBf16>(x[8 * j + 2], x[8 * j + 3]),
+                                ptx::pack2<kBf16>(x[8 * j + 4], x[8 * j + 5]),
+                                ptx::pack2<kBf16>(x[8 * j + 6], x[8 * j + 7]));
+          if (g == 0)
+            p.lse[row] = lt != 0.f ? (ptx::lg2(lt) + mt) * 0.693147180559945309f : -INFINITY;
+        } else {
+          float4* const out = p.part_o + (slot * p.slot_rows + r) * (D / 4) + g * (kJ / 2);
 #pragma unroll
-        for (int w = 0; w < L::kWarps; ++w) {
-          const float2 x = ml_s[w * L::kRows + nt * 8 + 2 * t + e];
-          if (x.y != 0.f) top = fmaxf(top, x.x);
+          for (int j = 0; j < kJ / 2; ++j)
+            out[j] = make_float4(o[2 * j][nt][e] * vref, o[2 * j][nt][e + 2] * vref,
+                                 o[2 * j + 1][nt][e] * vref, o[2 * j + 1][nt][e + 2] * vref);
+          if (g == 0) p.part_ml[slot * p.slot_rows + r] = make_float2(mt, lt);
         }
-        f[e] = l[nt][e] != 0.f ? ptx::ex2(m[nt][e] - top) * vref : 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[e & 1];
-    }
-    // a row's D floats as D / 4 pieces, permuted by the row so that the rows of
-    // a quarter warp use other banks
-    constexpr int kPieces = D / 4;
-    auto place = [&](int w, int r, int c) { return (w * L::kRows + r) * kPieces + (c ^ (r >> 1 & 3)); };
-    auto each = [&](auto&& f) {              // f(row, piece, its four values)
-#pragma unroll
-      for (int nt = 0; nt < kTiles; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < kJ / 2; ++i)
-            f(nt * 8 + 2 * t + e, g * (kJ / 2) + i, o[2 * i][nt][e], o[2 * i][nt][e + 2],
-              o[2 * i + 1][nt][e], o[2 * i + 1][nt][e + 2]);
-    };
-    if (warp >= L::kHalf)
-      each([&](int r, int c, float& x, float& y, float& z, float& w) {
-        sum_s[place(warp - L::kHalf, r, c)] = make_float4(x, y, z, w);
-      });
-    __syncthreads();
-    if (warp < L::kHalf)
-      each([&](int r, int c, float& x, float& y, float& z, float& w) {
-        float4& a = sum_s[place(warp, r, c)];
-        a = make_float4(x + a.x, y + a.y, z + a.z, w + a.w);
-      });
-    __syncthreads();
-    const size_t slot = 2 * static_cast<size_t>(run) + (pieces == 0 ? 0 : 1);
-    for (int i = threadIdx.x; i < rows * kPieces; i += L::kThreads) {
-      const int r = i / kPieces, c = i - r * kPieces;
-      float4 a = sum_s[place(0, r, c)];
-#pragma unroll
-      for (int w = 1; w < L::kHalf; ++w) {
-        const float4 x = sum_s[place(w, r, c)];
-        a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
-      }
-      float top = -INFINITY, lt = 0.f;
-#pragma unroll
-      for (int w = 0; w < L::kWarps; ++w) {
-        const float2 x = ml_s[w * L::kRows + r];
-        if (x.y != 0.f) top = fmaxf(top, x.x);
-      }
-#pragma unroll
-      for (int w = 0; w < L::kWarps; ++w) {
-        const float2 x = ml_s[w * L::kRows + r];
-        if (x.y != 0.f) lt = fmaf(x.y, ptx::ex2(x.x - top), lt);
-      }
-      if (whole) {
-        const float inv = lt != 0.f ? 1.0f / lt : 0.f;
-        const size_t out = head * po.R + row0 + r;
-        if (!(lt != 0.f)) a = make_float4(0.f, 0.f, 0.f, 0.f);
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(po.o) + out * D)[c] =
-            make_uint2(ptx::pack2<kBf16>(a.x * inv, a.y * inv),
-                       ptx::pack2<kBf16>(a.z * inv, a.w * inv));
-        if (c == 0)
-          po.lse[out] = lt != 0.f ? (ptx::lg2(lt) + top) * 0.693147180559945309f : -INFINITY;
-      } else {
-        *dec_part<D>(po, slot, r, c) = a;
-        if (c == 0) po.part_ml[slot * po.slot_rows + r] = make_float2(lt != 0.f ? -top : 0.f, lt);
-      }
-    }
-    if (tile0 == 0 && !whole && threadIdx.x == 0) {
-      // a unit that starts here and ends in a later run: its parts' place
-      const int last = dec_run_start(deal, run) + done + at.s.tiles - 1;
-      po.cut[run] = make_int4(static_cast<int>(head), block, static_cast<int>(slot),
-                              dec_run_of(deal, last));
-    }
-    cut_here |= tile0 == 0 && !whole;
-    ++pieces;
+    if (tile0 == 0 && lane == 0)
+      p.cut[unit] = whole ? make_int2(-1, 0)
+                          : make_int2(static_cast<int>(slot),
+                                      dec_run_of(deal, start + done + s.tiles - 1));
     done += n;
-    if (done < n_tiles) advance(at, n);
-    __syncthreads();                         // sums and queries have been read
+    __syncwarp();                            // the queries have been read
   }
-  if (threadIdx.x == 0 && !cut_here) po.cut[run] = make_int4(0, 0, 0, -1);
   // after a wait that ran out: the loads in flight land before the block ends
   cp_async_wait<0>();
   for (; waited < loaded; ++waited)
     ptx::wait_drain(bar(waited % kStages), waited / kStages & 1, 200000000ull);
+}
+
+// The cut units: a block takes `per_block` units for one row of a part and adds
+// up the unit's parts of that row, 4 columns a thread; kGroups groups of
+// threads take other parts each, kBatch loads in flight, and meet in shared
+// memory.  Every part is scaled to the largest maximum, and the sum divided
+// once.  A row without a visible key has no live part (a sum of NaN is live).
+template <int D, bool kBf16, int kGroups>
+__global__ void __launch_bounds__(kGroups * (D / 4))
+    fa_decode_paged_combine_kernel(const __grid_constant__ DecPagedParams p, int units,
+                                   int per_block) {
+  constexpr int kPer = D / 4, kBatch = 8;
+  __shared__ float4 acc_s[kGroups][kPer];
+  __shared__ float2 ml_s[kGroups];
+  const int c = threadIdx.x % kPer, group = threadIdx.x / kPer, r = blockIdx.y;
+  ptx::griddep_wait();   // the parts are complete, and this grid ends after the main one
+  const int u1 = min((static_cast<int>(blockIdx.x) + 1) * per_block, units);
+  for (int u = blockIdx.x * per_block; u < u1; ++u) {
+    const int2 cut = p.cut[u];
+    if (cut.x < 0) continue;
+    const int head = u / p.row_blocks, row = (u - head * p.row_blocks) * p.slot_rows + r;
+    if (row >= p.R) continue;
+    const int run0 = cut.x >> 1, parts = cut.y - run0 + 1;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = group; i < parts; i += kGroups * kBatch) {
+      float2 ml[kBatch];
+      float4 x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int part = i + k * kGroups;
+        ml[k] = make_float2(0.f, 0.f);
+        if (part < parts) {
+          const size_t slot = part == 0 ? cut.x : 2 * static_cast<size_t>(run0 + part);
+          ml[k] = p.part_ml[slot * p.slot_rows + r];
+          x[k] = p.part_o[(slot * p.slot_rows + r) * kPer + c];
+        }
+      }
+      float now = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (ml[k].y != 0.f) now = fmaxf(now, ml[k].x);
+      const float fo = m == -INFINITY ? 0.f : ptx::ex2(m - now);
+      acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
+      l *= fo;
+      m = now;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (ml[k].y != 0.f) {
+          const float f = ptx::ex2(ml[k].x - m);
+          acc.x = fmaf(f, x[k].x, acc.x);
+          acc.y = fmaf(f, x[k].y, acc.y);
+          acc.z = fmaf(f, x[k].z, acc.z);
+          acc.w = fmaf(f, x[k].w, acc.w);
+          l = fmaf(f, ml[k].y, l);
+        }
+    }
+    acc_s[group][c] = acc;
+    if (c == 0) ml_s[group] = make_float2(m, l);
+    __syncthreads();
+    if (group == 0) {
+      float top = -INFINITY, lt = 0.f;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+        if (ml_s[k].y != 0.f) top = fmaxf(top, ml_s[k].x);
+#pragma unroll 4
+      for (int k = 0; k < kGroups; ++k)
+        if (ml_s[k].y != 0.f) {
+          const float f = ptx::ex2(ml_s[k].x - top);
+          const float4 x = acc_s[k][c];
+          sum.x = fmaf(f, x.x, sum.x);
+          sum.y = fmaf(f, x.y, sum.y);
+          sum.z = fmaf(f, x.z, sum.z);
+          sum.w = fmaf(f, x.w, sum.w);
+          lt = fmaf(f, ml_s[k].y, lt);
+        }
+      const float inv = lt != 0.f ? 1.0f / lt : 0.f;
+      const size_t out = static_cast<size_t>(head) * p.R + row;
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D)[c] =
+          make_uint2(ptx::pack2<kBf16>(sum.x * inv, sum.y * inv),
+                     ptx::pack2<kBf16>(sum.z * inv, sum.w * inv));
+      if (c == 0) p.lse[out] = lt != 0.f ? (ptx::lg2(lt) + top) * 0.693147180559945309f : -INFINITY;
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace fa
