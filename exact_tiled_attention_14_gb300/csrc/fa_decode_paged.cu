@@ -11,6 +11,7 @@
 
 #include "fa.h"
 #include "fa_decode_paged_kernel.cuh"
+#include "fa_decode_paged_tc_kernel.cuh"
 #include "fa_host.cuh"
 
 using namespace fa::host;
@@ -36,11 +37,31 @@ cudaError_t launch_main(const DecPagedParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+constexpr int kManyTiles = kDtRows / 8;   // row tiles of a unit of the kernel for many rows
+
+template <int D, bool kBf16, bool kInt8>
+cudaError_t launch_tc(const DecPagedParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = fa_decode_paged_tc_kernel<D, kBf16, kInt8>;
+  constexpr int kAlloc = DtLayout<D>::kAlloc;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlloc);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit);
+  }
+  kernel<<<p.grid, kDtThreads, kAlloc, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, bool kBf16, bool kInt8>
 cudaError_t launch_variant(const DecPagedParams& p, int tiles, int sms, cudaStream_t stream) {
   cudaError_t e = tiles == 1   ? launch_main<D, kBf16, kInt8, 1>(p, stream)
                   : tiles == 2 ? launch_main<D, kBf16, kInt8, 2>(p, stream)
-                               : launch_main<D, kBf16, kInt8, 4>(p, stream);
+                               : launch_tc<D, kBf16, kInt8>(p, stream);
   if (e != cudaSuccess) return e;
   // Programmatic dependent launch: the combine grid is set up while the main
   // kernel runs its last CTAs, and waits on the device for the parts.  Blocks
@@ -66,16 +87,21 @@ cudaError_t launch_variant(const DecPagedParams& p, int tiles, int sms, cudaStre
 
 constexpr int kMaxTokens = 16;
 
-// Row tiles of a unit (1, 2 or 4 of 8 rows), runs (one per warp of a CTA per SM,
-// or fewer) and the workspace: two parts per run, and the units' table.
+// Row tiles of a unit (8 rows each), runs (one per warp of a CTA per SM, or one
+// per CTA for many rows, or fewer) and the workspace: two parts per run, and the units' table.
 struct Plan {
   int tiles, row_blocks, slot_rows, grid, runs;
   size_t o_bytes, ml_bytes, bytes;
 };
-int row_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : 4; }
+// Up to 16 rows the warps' own products win (16 rows of 8 caches to 32k, 4 heads,
+// d = 128: 54 us, 74 with the kernel for many rows; d = 64 37 and 72), from 17 on
+// the other (64 rows 75 us, 106 in blocks of 32 rows; 128 rows 82 and 194; 32
+// rows 76 and 78).
+int row_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : kManyTiles; }
+int tile_keys(int tiles, int d) { return tiles == kManyTiles ? kDtKeys : dp_keys(d); }
 // Tiles of all units at most: whole capacities, and one of each sequence's own.
-long long max_tiles(int B, int Hk, int row_blocks, int d, int capacity) {
-  const long long tiles = (static_cast<long long>(capacity) + dp_keys(d) - 1) / dp_keys(d) + 1;
+long long max_tiles(int B, int Hk, int row_blocks, int keys, int capacity) {
+  const long long tiles = (static_cast<long long>(capacity) + keys - 1) / keys + 1;
   return static_cast<long long>(B) * Hk * row_blocks * tiles;
 }
 int check_sizes(int B, int H, int Hk, int Nq, int d, int page_size, int pages_per_seq) {
@@ -85,7 +111,8 @@ int check_sizes(int B, int H, int Hk, int Nq, int d, int page_size, int pages_pe
   if (B == 0 || H == 0) return FA_OK;
   const int R = H / Hk * Nq, span = 8 * row_tiles(R);
   // the numbers of all tiles fit in int
-  if (max_tiles(B, Hk, (R + span - 1) / span, d, pages_per_seq * page_size) >= (1ll << 31))
+  if (max_tiles(B, Hk, (R + span - 1) / span, tile_keys(span / 8, d),
+                pages_per_seq * page_size) >= (1ll << 31))
     return FA_ERR_SHAPE;
   return FA_OK;
 }
@@ -95,8 +122,11 @@ Plan make_plan(int B, int H, int Hk, int Nq, int d, int capacity, int sms) {
   pl.tiles = row_tiles(R);
   pl.row_blocks = (R + 8 * pl.tiles - 1) / (8 * pl.tiles);
   pl.slot_rows = std::min(R, 8 * pl.tiles);
-  const long long min_tiles = dp_min_tiles(pl.tiles), warps = dp_warps(pl.tiles);
-  const long long all = (max_tiles(B, Hk, pl.row_blocks, d, capacity) + min_tiles - 1) / min_tiles;
+  const bool many = pl.tiles == kManyTiles;
+  const long long min_tiles = many ? 1 : dp_min_tiles(pl.tiles);
+  const long long warps = many ? 1 : dp_warps(pl.tiles);
+  const long long most = max_tiles(B, Hk, pl.row_blocks, tile_keys(pl.tiles, d), capacity);
+  const long long all = (most + min_tiles - 1) / min_tiles;
   pl.runs = static_cast<int>(std::min(all, sms * warps));
   pl.grid = std::min(pl.runs, sms);
   const size_t rows = 2 * static_cast<size_t>(pl.runs) * pl.slot_rows;
@@ -154,17 +184,20 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, con
   const DeviceInfo* info = device_info(&dev);
   if (!info || !info->supported) return FA_ERR_DEVICE;
   if (info->err != FA_OK) return info->err;
-  const int capacity = pages_per_seq * page_size, keys = fa::dp_keys(d);
+  const int capacity = pages_per_seq * page_size;
   const fa::Plan pl = fa::make_plan(B, H, Hk, Nq, d, capacity, info->sms);
+  const int keys = fa::tile_keys(pl.tiles, d);
   if (!workspace || workspace_bytes < pl.bytes) return FA_ERR_WORKSPACE;
   if (misaligned(workspace, 256)) return FA_ERR_ALIGN;
 
   fa::DecPagedParams p{};
-  // one box a tile where a page holds whole tiles, else one per 16 keys
-  p.boxes = page_size % keys == 0 ? 1 : keys / fa::kPageRows;
+  // the largest boxes that pages and tiles are both made of
+  int box = keys;
+  while (page_size % box != 0) box /= 2;
+  p.boxes = keys / box;
   const long long rows = static_cast<long long>(pages) * Hk * page_size;
-  if (!make_tmap_codes(&p.tm_k, k_cache, rows, d, keys / p.boxes) ||
-      !make_tmap_codes(&p.tm_v, v_cache, rows, d, keys / p.boxes))
+  if (!make_tmap_codes(&p.tm_k, k_cache, rows, d, box) ||
+      !make_tmap_codes(&p.tm_v, v_cache, rows, d, box))
     return FA_ERR_TENSORMAP;
   p.q = q;
   p.k_scale = k_scale;

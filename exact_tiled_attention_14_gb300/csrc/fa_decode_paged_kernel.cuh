@@ -48,13 +48,11 @@
 namespace fa {
 
 // Warps of a CTA by its row tiles (8 rows each).
-__host__ __device__ constexpr int dp_warps(int tiles) {
-  return tiles == 1 ? 12 : tiles == 2 ? 10 : 8;
-}
+__host__ __device__ constexpr int dp_warps(int tiles) { return tiles == 1 ? 12 : 10; }
 constexpr int kDpTileBytes = 4096;       // of K, and of V
-// A run takes this many tiles at least (2, 3, 4 by its row tiles): a part is 4 KB
-// for each row tile at d = 128, a tile 8 KB.
-__host__ __device__ constexpr int dp_min_tiles(int tiles) { return tiles < 3 ? tiles + 1 : 4; }
+// A run takes this many tiles at least: a part is 4 KB for each row tile at
+// d = 128, a tile 8 KB.
+__host__ __device__ constexpr int dp_min_tiles(int tiles) { return tiles + 1; }
 constexpr float kDpTau = 8.0f;           // lazy-rescale threshold, log2 units
 constexpr uint32_t kSiteDpFull = 50;
 __host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
@@ -80,8 +78,7 @@ struct DecPagedParams {
   int slot_rows;           // rows of a unit's part
   int per_seq, pages, page;
   uint32_t page_magic;     // ceil(2^32 / (page / 16)), 0 for pages of 16
-  int boxes;               // boxes of a tile: 1, or one per 16 keys where pages are no multiples
-                           // of a tile
+  int boxes;               // boxes of a tile, all of one page each: 16 to a tile's keys
   int runs;                // at most
   int grid;
   int win;                 // >= 1; larger than every position: no window
@@ -138,6 +135,7 @@ __host__ __device__ constexpr uint32_t dp_chunk(int r, int c) {
 // Shared memory: the warps' rings, then each warp's queries, weights and scales.
 template <int D, int kTiles>
 struct DpLayout {
+  static_assert(kTiles == 1 || kTiles == 2, "row tiles of 8 rows");
   static constexpr int kRows = 8 * kTiles;
   static constexpr int kWarps = dp_warps(kTiles), kThreads = 32 * kWarps;
   static constexpr int kStages = 2;
@@ -190,6 +188,80 @@ struct DpPlace {
   int b, hk, block, tile;
   PagedSpan s;
 };
+__device__ __forceinline__ PagedSpan dp_span(const DecPagedParams& p, int b, int keys) {
+  return paged_span(p.seqlens[b], p.per_seq * p.page, p.Nq, p.win, p.sinks, keys);
+}
+// (past the last unit: a place never used)
+__device__ __forceinline__ void dp_next_unit(const DecPagedParams& p, DpPlace& x, int keys) {
+  x.tile = 0;
+  if (++x.block < p.row_blocks) return;
+  x.block = 0;
+  if (++x.hk < p.Hk) return;
+  x.hk = 0;
+  if (++x.b < p.B) x.s = dp_span(p, x.b, keys);
+}
+
+// Run `run` of the deal of all tiles, at least min_tiles each, to at most `runs`
+// runs: its tiles start .. start + left - 1 and its first place; by one warp.
+struct DpRun {
+  DecDeal deal;
+  DpPlace at;
+  int start, left;
+};
+__device__ __forceinline__ DpRun dp_run(const DecPagedParams& p, int keys, int runs, int min_tiles,
+                                        int run) {
+  const int lane = threadIdx.x & 31, units = p.Hk * p.row_blocks;   // of a batch
+  DpRun r{};
+  int total = 0;
+  for (int b = lane; b < p.B; b += 32) total += dp_span(p, b, keys).tiles * units;
+  total = __reduce_add_sync(0xffffffffu, total);
+  r.deal = dec_deal(total, min(runs, (total + min_tiles - 1) / min_tiles));
+  if (run >= r.deal.runs) return r;
+  r.start = dec_run_start(r.deal, run);
+  r.left = dec_run_start(r.deal, run + 1) - r.start;
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int mine = b0 + lane < p.B ? dp_span(p, b0 + lane, keys).tiles * units : 0;
+    int upto = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, i);
+      if (lane >= i) upto += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > r.start);
+    if (past != 0) {
+      const int k = __ffs(past) - 1;
+      r.at.b = b0 + k;
+      r.at.s = dp_span(p, r.at.b, keys);
+      const int skip = r.start - (before + __shfl_sync(0xffffffffu, upto - mine, k));
+      const int unit = skip / r.at.s.tiles;
+      r.at.tile = skip - unit * r.at.s.tiles;
+      r.at.hk = unit / p.row_blocks;
+      r.at.block = unit - r.at.hk * p.row_blocks;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return r;
+}
+
+// Four elements a lane of a query row, times the power of two (returned) that
+// brings the row's largest to 2^12; by one warp.
+template <bool kBf16>
+__device__ __forceinline__ int dp_query_row(const uint2 raw, float* x) {
+  ptx::unpack2<kBf16>(raw.x, x[0], x[1]);
+  ptx::unpack2<kBf16>(raw.y, x[2], x[3]);
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  int shift = 0;
+  if (top != 0 && top < kInfBits) shift = min(12 - (static_cast<int>(top >> 23) - 127), 120);
+  const float mul = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] *= mul;
+  return shift;
+}
 
 template <int D, bool kBf16, bool kInt8, int kTiles>
 __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
@@ -206,7 +278,6 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
   uint8_t* const sgen = smem_raw + (sbase - raw_base);
   const int warp = ptx::warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int capacity = p.per_seq * p.page;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc);
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
   const uint32_t ring = sbase + warp * L::kRing;
@@ -232,53 +303,12 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
   __syncthreads();                           // (the abort flag; the only one)
 
   // ---- the warp's run and its first place
-  const int units = p.Hk * p.row_blocks;     // of a batch
-  auto span_of = [&](int b) {
-    return paged_span(p.seqlens[b], capacity, p.Nq, p.win, p.sinks, kKeys);
-  };
-  int total = 0;
-  for (int b = lane; b < p.B; b += 32) total += span_of(b).tiles * units;
-  total = __reduce_add_sync(0xffffffffu, total);
-  constexpr int kMin = dp_min_tiles(kTiles);
-  const DecDeal deal = dec_deal(total, min(p.runs, (total + kMin - 1) / kMin));
   const int run = warp * p.grid + blockIdx.x;    // few runs spread over the SMs
+  const DpRun rn = dp_run(p, kKeys, p.runs, dp_min_tiles(kTiles), run);
+  const DecDeal deal = rn.deal;
   if (run >= deal.runs) return;
-  const int start = dec_run_start(deal, run);
-  int left = dec_run_start(deal, run + 1) - start;   // tiles not begun
-  DpPlace at{};
-  {
-    int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int mine = b0 + lane < p.B ? span_of(b0 + lane).tiles * units : 0;
-      int upto = mine;
-#pragma unroll
-      for (int i = 1; i < 32; i *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, i);
-        if (lane >= i) upto += x;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > start);
-      if (past != 0) {
-        const int k = __ffs(past) - 1;
-        at.b = b0 + k;
-        at.s = span_of(at.b);
-        const int skip = start - (before + __shfl_sync(0xffffffffu, upto - mine, k));
-        const int unit = skip / at.s.tiles;
-        at.tile = skip - unit * at.s.tiles;
-        at.hk = unit / p.row_blocks;
-        at.block = unit - at.hk * p.row_blocks;
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
-  auto next_unit = [&](DpPlace& x) {         // (past the last unit: a place never used)
-    x.tile = 0;
-    if (++x.block < p.row_blocks) return;
-    x.block = 0;
-    if (++x.hk < p.Hk) return;
-    x.hk = 0;
-    if (++x.b < p.B) x.s = span_of(x.b);
-  };
+  DpPlace at = rn.at;
+  int left = rn.left;                        // tiles not begun
 
   // ---- the warp's loads
   const int box_rows = kKeys / p.boxes;
@@ -316,7 +346,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       }
       ++loaded;
       --nx_left;
-      if (++nx.tile == nx.s.tiles) next_unit(nx);
+      if (++nx.tile == nx.s.tiles) dp_next_unit(p, nx, kKeys);
       look();
     }
     cp_async_commit();                       // one group per tile, empty ones too
@@ -327,7 +357,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
   // ---- pieces of units, in the order of the run
   bool alive = true;
   int stage = 0, parity = 0, pieces = 0, done = 0;
-  for (; left > 0; next_unit(at), ++pieces) {
+  for (; left > 0; dp_next_unit(p, at, kKeys), ++pieces) {
     const int tile0 = at.tile;
     const int n = min(at.s.tiles - tile0, left);
     const bool whole = tile0 == 0 && n == at.s.tiles;
@@ -351,19 +381,10 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float x[4];
-        ptx::unpack2<kBf16>(raw[i].x, x[0], x[1]);
-        ptx::unpack2<kBf16>(raw[i].y, x[2], x[3]);
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-        top = __reduce_max_sync(0xffffffffu, top);
-        int shift = 0;                       // the row times 2^shift
-        if (top != 0 && top < kInfBits) shift = min(12 - (static_cast<int>(top >> 23) - 127), 120);
-        const float mul = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+        const int shift = dp_query_row<kBf16>(raw[i], x);
         if (lane * 4 < D)
           q_s[(lane % (D / 16) * kTiles + nt) * 32 + i * 4 + lane / (D / 16)] =
-              make_uint2(ptx::pack2<false>(x[0] * mul, x[1] * mul),
-                         ptx::pack2<false>(x[2] * mul, x[3] * mul));
+              make_uint2(ptx::pack2<false>(x[0], x[1]), ptx::pack2<false>(x[2], x[3]));
         if (lane == 0)
           qmul_s[nt * 8 + i] =
               p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
@@ -381,11 +402,12 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         const int r = nt * 8 + 2 * t + e;
         qmul[nt][e] = qmul_s[r];
         pos[nt][e] = s.len - p.Nq + (row0 + r) % p.Nq;
-        m[nt][e] = -INFINITY;
+        m[nt][e] = 0.f;                      // the reference, 0 before the first score
         l[nt][e] = 0.f;
       }
     float o[kJ][kTiles][4] = {};
-    float vref = 0.f;                        // unit of O (0: nothing summed yet)
+    float vref = 0.f, inv_vref = 0.f;        // unit of O (0: nothing summed yet)
+    uint32_t seen = 0;                       // rows (2 nt + e) with a reference
     const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
 
 #pragma unroll 1
@@ -402,7 +424,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       // every row sees every key of the tile
       const bool full = have == (1u << p.boxes) - 1u && key0 + kKeys - 1 <= pos_lo &&
                         (key0 > pos_hi - p.win || key0 + kKeys <= p.sinks);
-      auto box_of = [&](int mt) { return p.boxes == 1 ? 0 : mt; };
+      auto box_of = [&](int mt) { return mt * p.boxes / kMt; };
       if (!full) {
         // values that no row sees weigh 0, and 0 times what they hold must be 0
         for (int i = lane; i < kKeys; i += 32) {
@@ -450,12 +472,16 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         }
       }
 
-      // ---- scores, weights
+      // ---- scores less the row's reference, in log2 units
       float vs[kMt], vs_top = 0.f;
       bool odd = false;                      // a scale of values that is not finite
+      float mx[kTiles][2];
+#pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
         const float ks = sc[box_of(mt)];
+        const uint64_t k2 = ptx::f2_pack(ks, ks);
         vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
         if (!(fabsf(vs[mt]) < INFINITY)) {
           vs[mt] = 0.f;
@@ -463,9 +489,15 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         }
         vs_top = fmaxf(vs_top, fabsf(vs[mt]));
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt)
+        for (int nt = 0; nt < kTiles; ++nt) {
+          const uint64_t q2 = ptx::f2_pack(qmul[nt][0], qmul[nt][1]);
+          const uint64_t n2 = ptx::f2_pack(-m[nt][0], -m[nt][1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[mt][nt][e] = sv[mt][nt][e] * qmul[nt][e & 1] * ks;
+          for (int e = 0; e < 4; e += 2)
+            ptx::f2_unpack(
+                ptx::ffma2(ptx::fmul2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), q2), k2, n2),
+                sv[mt][nt][e], sv[mt][nt][e + 1]);
+        }
       }
       if (!full) {
 #pragma unroll
@@ -480,6 +512,13 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
               if (!see) sv[mt][nt][e] = -INFINITY;
             }
       }
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mx[nt][e] = ptx::max3(mx[nt][e], sv[mt][nt][e], sv[mt][nt][e + 2]);
       // O is held in units of vref, a power of two next to the scales of the
       // last pages: weights times their page's scale / vref round like weights
       if (vs_top > vref || vs_top < vref * (1.f / 64.f)) {
@@ -488,6 +527,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
           const float now = fminf(fmaxf(unit, 0x1p-120f), 0x1p120f);
           const float f = vref > 0.f ? fminf(vref / now, 0x1p120f) : 1.f;
           vref = now;
+          inv_vref = 1.f / now;
 #pragma unroll
           for (int j = 0; j < kJ; ++j)
 #pragma unroll
@@ -496,35 +536,38 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
               for (int e = 0; e < 4; ++e) o[j][nt][e] *= f;
         }
       }
-      const float inv_vref = vref > 0.f ? 1.f / vref : 0.f;
+      // a row keeps its reference until a score passes it by the threshold (or is
+      // its first): only then do its lanes look for its largest
       bool raise = false;
-      float mx[kTiles][2];
 #pragma unroll
       for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = -INFINITY;
-#pragma unroll
-          for (int mt = 0; mt < kMt; ++mt)
-            mx[nt][e] = ptx::max3(mx[nt][e], sv[mt][nt][e], sv[mt][nt][e + 2]);
-#pragma unroll
-          for (int i = 4; i < 32; i *= 2)
-            mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], i));
-          // a row keeps its reference until a score passes it by the threshold
-          if (!(mx[nt][e] > m[nt][e] + kDpTau)) mx[nt][e] = m[nt][e];
-          raise |= mx[nt][e] != m[nt][e];
-        }
+        for (int e = 0; e < 2; ++e)
+          raise |= mx[nt][e] > kDpTau || (!(seen >> (2 * nt + e) & 1u) && mx[nt][e] > -INFINITY);
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            // a row without a reference so far holds zeros (or NaN, which stays)
-            f[e] = m[nt][e] == -INFINITY || mx[nt][e] == m[nt][e] ? 1.f
-                                                                  : ptx::ex2(m[nt][e] - mx[nt][e]);
-            m[nt][e] = mx[nt][e];
-            l[nt][e] *= f[e];
+#pragma unroll
+            for (int i = 4; i < 32; i *= 2)
+              mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], i));
+            const uint32_t bit = 1u << (2 * nt + e);
+            const bool fresh = !(seen & bit);
+            f[e] = 1.f;
+            if (mx[nt][e] > kDpTau || (fresh && mx[nt][e] > -INFINITY)) {
+              // (a row without a reference so far holds zeros, or NaN, which stays)
+              if (!fresh) f[e] = ptx::ex2(-mx[nt][e]);
+              m[nt][e] += mx[nt][e];
+              l[nt][e] *= f[e];
+              seen |= bit;
+#pragma unroll
+              for (int mt = 0; mt < kMt; ++mt) {
+                sv[mt][nt][e] -= mx[nt][e];
+                sv[mt][nt][e + 2] -= mx[nt][e];
+              }
+            }
           }
 #pragma unroll
           for (int j = 0; j < kJ; ++j)
@@ -535,18 +578,20 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
         const float r = vs[mt] * inv_vref;
+        const uint64_t r2 = ptx::f2_pack(r, r);
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-          const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float a = ptx::ex2(sv[mt][nt][0] - m0), b = ptx::ex2(sv[mt][nt][1] - m1);
-          const float c = ptx::ex2(sv[mt][nt][2] - m0), d = ptx::ex2(sv[mt][nt][3] - m1);
-          l[nt][0] += a + c;
-          l[nt][1] += b + d;
+          const uint64_t ab = ptx::f2_pack(ptx::ex2(sv[mt][nt][0]), ptx::ex2(sv[mt][nt][1]));
+          const uint64_t cd = ptx::f2_pack(ptx::ex2(sv[mt][nt][2]), ptx::ex2(sv[mt][nt][3]));
+          const uint64_t sum =
+              ptx::fadd2(ptx::f2_pack(l[nt][0], l[nt][1]), ptx::fadd2(ab, cd));
+          ptx::f2_unpack(sum, l[nt][0], l[nt][1]);
+          float a, b, c, d;
+          ptx::f2_unpack(ptx::fmul2(ab, r2), a, b);
+          ptx::f2_unpack(ptx::fmul2(cd, r2), c, d);
           // P^T as the B operand
-          p_s[(mt * kTiles + nt) * 32 + lane] =
-              make_uint2(transpose8x8(ptx::pack2<false>(a * r, b * r)),
-                         transpose8x8(ptx::pack2<false>(c * r, d * r)));
+          p_s[(mt * kTiles + nt) * 32 + lane] = make_uint2(transpose8x8(ptx::pack2<false>(a, b)),
+                                                           transpose8x8(ptx::pack2<false>(c, d)));
         }
       }
       if (odd) {                             // rows that see such a page: NaN
@@ -620,7 +665,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         float lt = l[nt][e];
 #pragma unroll
         for (int k = 4; k < 32; k *= 2) lt += __shfl_xor_sync(0xffffffffu, lt, k);
-        const float mt = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+        const float mt = m[nt][e];
         const int r = nt * 8 + 2 * t + e;
         if (r >= rows) continue;
         if (whole) {
@@ -654,7 +699,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
     if (tile0 == 0 && lane == 0)
       p.cut[unit] = whole ? make_int2(-1, 0)
                           : make_int2(static_cast<int>(slot),
-                                      dec_run_of(deal, start + done + s.tiles - 1));
+                                      dec_run_of(deal, rn.start + done + s.tiles - 1));
     done += n;
     __syncwarp();                            // the queries have been read
   }

@@ -1,0 +1,684 @@
+// fa_decode_paged_tc_kernel.cuh — decoding over pages of 8-bit keys and values
+// (see fa_paged.cuh) for many rows: 9 to 128 query rows of a key/value head in
+// one unit, on the tensor cores through TMEM.
+//
+// The function, the queries' powers of two, the placing of the scales and the
+// unit of O are those of fa_decode_paged_kernel.cuh.  There a warp turns codes
+// into 16-bit registers for its own products, which costs as many issue slots
+// again for each 16 rows: 64 rows of 8 caches took 113 us against 25 of their
+// bytes.  Here codes are turned once for all rows, by warps of their own, into
+// half-precision tiles in shared memory, and a product of 128 rows costs a
+// tile 544 cycles whatever their number.
+//
+// Bound (d = 128, a tile of 128 keys, 32 KB): its share of HBM 1394 cycles of
+// an SM, the products 1088, the softmax of 128 rows about 900 issue cycles, the
+// turning of the codes 320, and 1800 cycles of shared-memory traffic (codes in
+// and out 64 KB, half-precision tiles in and out 128 KB, queries 32 KB): the
+// last bounds a tile.
+//
+// One CTA (26 warps) per SM, persistent over its run of key tiles:
+//   warps 0-15   softmax: warp w has rows 32 (w % 4) .. + 31, one a lane, and
+//                quarter w / 4 of a tile's keys; the four threads of a row agree
+//                on its reference;
+//   warps 16-19  K tiles to half precision, and the queries at a unit's start;
+//   warps 20-23  V tiles, rows that no row of the unit sees as zeros;
+//   warp 24      pages, scales and the TMA loads;
+//   warp 25      S = Q K^T of the next tile, then O += P V of this one.
+// A tile's softmax is one thread's chain, which takes longer than its issue
+// slots: 64 keys a thread took 1650 ns a tile, 32 take half.
+// S and P are double buffered in TMEM (at d = 128 it is full), O is not.  A unit
+// that lies in one run is finished there; parts of the others go to the
+// workspace for fa_decode_paged_combine_kernel.
+#pragma once
+
+#include "fa_decode_paged_kernel.cuh"
+
+namespace fa {
+
+constexpr int kDtKeys = 128, kDtRows = 128, kDtThreads = 832;
+constexpr int kDtConvert = 16, kDtLoad = 24, kDtMma = 25;   // first warp of a role
+constexpr int kDtTurners = 4;            // warps that turn K, and V
+constexpr int kDtMetas = 3;              // tiles whose scales are kept
+
+enum DtWaitSite : uint32_t {
+  kSiteDtCodesFull = 51, kSiteDtCodesEmpty = 52, kSiteDtMetaFull = 53, kSiteDtMetaEmpty = 54,
+  kSiteDtKFull = 55, kSiteDtKEmpty = 56, kSiteDtVFull = 57, kSiteDtVEmpty = 58, kSiteDtSFull = 59,
+  kSiteDtPFull = 60, kSiteDtPvDone = 61, kSiteDtOFree = 62,
+  kSiteDtQReady = 63
+};
+
+// Scales of a tile by 16 keys, and which of the eight name a page.
+struct DtMeta {
+  float ks[8], vs[8];
+  uint32_t have;
+  float top;               // the largest finite |vs| of them
+  uint32_t pad[2];
+};
+
+template <int D>
+struct DtLayout {
+  static constexpr int kChunks = D / 64, kChunkBytes = kDtKeys * 128;
+  static constexpr int kTile = kDtKeys * D * 2;               // half precision
+  static constexpr int kCodes = kDtKeys * D;                  // of K, and of V
+  static constexpr int kSlots = D == 128 ? 4 : 8;              // of the ring: K, V, K, V ...
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kTile;                       // two tiles each
+  static constexpr int kV = kK + 2 * kTile;
+  static constexpr int kRing = kV + 2 * kTile;
+  static constexpr int kMeet = kRing + kSlots * kCodes;  // [2][row], where a row's threads meet
+  static constexpr int kMeta = kMeet + 2 * kDtRows * 4;
+  // the queries' powers of two, of the units whose first tile has the meta's slot
+  static constexpr int kShift = kMeta + kDtMetas * static_cast<int>(sizeof(DtMeta));   // [row] int8
+  static constexpr int kBar = kShift + kDtMetas * kDtRows;
+  static constexpr int bCodesFull = 0, bCodesEmpty = kSlots, bMetaFull = 2 * kSlots,
+                       bMetaEmpty = bMetaFull + kDtMetas, bKFull = bMetaEmpty + kDtMetas,
+                       bKEmpty = bKFull + 2, bVFull = bKEmpty + 2, bVEmpty = bVFull + 2,
+                       bSFull = bVEmpty + 2, bPFull = bSFull + 2, bPvDone = bPFull + 2,
+                       bQReady = bPvDone + 2, bOFree = bQReady + kDtMetas,
+                       bFinal = bOFree + 1, kNumBars = bFinal + 1;
+  static constexpr int kMisc = kBar + 8 * kNumBars;           // TMEM base, abort flag
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kBar % 8 == 0 && kAlloc <= 232448, "shared memory budget");
+  static constexpr uint32_t s_col(int b) { return 128u * b; }
+  static constexpr uint32_t kOCol = 256;
+  static constexpr uint32_t p_col(int b) { return 256u + D + 64u * b; }
+};
+
+// Row and 16-byte piece of a lane in the turning of four (d = 128) or eight (64)
+// rows of codes: reads (swizzled by the copy) and both 16-byte writes of every
+// quarter warp touch all banks once.  At d = 128 a quarter takes every other
+// piece of two rows whose numbers differ in the two low bits, and pieces of the
+// second 64 columns write their halves in the other order.
+struct DtPiece {
+  int row, piece;
+};
+template <int D>
+__host__ __device__ __forceinline__ DtPiece dt_piece(int lane) {
+  DtPiece p;
+  if (D == 128) {
+    const int q = lane >> 3, i = lane & 7, a = q & 1;
+    p.row = i & 4 ? a ^ 3 : a;
+    p.piece = 2 * (i & 3) + (q >> 1);
+  } else {
+    p.row = lane >> 2;
+    p.piece = lane & 3;
+  }
+  return p;
+}
+// Where half h (8 elements, 16 bytes) of piece c of row r goes in a tile of half
+// precision: chunks of 64 columns, rows of 128 bytes, 128-byte swizzle.
+__host__ __device__ __forceinline__ uint32_t dt_place(int r, int c, int h) {
+  return (c >> 2) * static_cast<uint32_t>(kDtKeys * 128) + r * 128u +
+         (((2 * (c & 3) + h) ^ (r & 7)) << 4);
+}
+
+template <int D, bool kBf16, bool kInt8>
+__global__ void __launch_bounds__(kDtThreads, 1)
+    fa_decode_paged_tc_kernel(const __grid_constant__ DecPagedParams p) {
+  using L = DtLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = ptx::smem_u32(smem_raw);
+  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+  uint8_t* const sgen = smem_raw + (sbase - raw_base);
+  const int warp = ptx::warp_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * i; };
+  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
+  DtMeta* const metas = reinterpret_cast<DtMeta*>(sgen + L::kMeta);
+  signed char* const shift_s = reinterpret_cast<signed char*>(sgen + L::kShift);
+  const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
+
+  // softmax warps: with one unit a head, those that have rows
+  const int quarters = p.row_blocks > 1 ? 4 : (p.R + 31) / 32, active = 4 * quarters;
+
+  ptx::griddep_launch_dependents();
+  if (warp == kDtMma) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_ptr), 512);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == kDtLoad * 32) {
+    *abort_flag = 0;
+    for (int i = 0; i < L::kSlots; ++i) {
+      ptx::mbar_init(bar(L::bCodesFull + i), 1);
+      ptx::mbar_init(bar(L::bCodesEmpty + i), kDtTurners);
+    }
+    for (int i = 0; i < kDtMetas; ++i) {
+      ptx::mbar_init(bar(L::bMetaFull + i), 1);
+      ptx::mbar_init(bar(L::bMetaEmpty + i), active + kDtTurners);
+      ptx::mbar_init(bar(L::bQReady + i), kDtTurners);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(L::bKFull + i), kDtTurners);
+      ptx::mbar_init(bar(L::bKEmpty + i), 1);
+      ptx::mbar_init(bar(L::bVFull + i), kDtTurners);
+      ptx::mbar_init(bar(L::bVEmpty + i), 1);
+      ptx::mbar_init(bar(L::bSFull + i), 1);
+      ptx::mbar_init(bar(L::bPFull + i), active);
+      ptx::mbar_init(bar(L::bPvDone + i), 1);
+    }
+    ptx::mbar_init(bar(L::bOFree), active);
+    ptx::mbar_init(bar(L::bFinal), 1);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&p.tm_k);
+    ptx::prefetch_tmap(&p.tm_v);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ptx::warp_same(*tmem_ptr);
+
+  // ---- the CTA's run and its first place (each warp for itself)
+  const DpRun rn = dp_run(p, kDtKeys, p.runs, 1, blockIdx.x);
+  const DecDeal deal = rn.deal;
+  const int run = blockIdx.x;
+  DpPlace at = rn.at;
+  int left = rn.left;
+  const int box_rows = kDtKeys / p.boxes;
+  auto piece_of = [&](int& n, bool& whole) {     // of the place `at`
+    n = min(at.s.tiles - at.tile, left);
+    whole = at.tile == 0 && n == at.s.tiles;
+  };
+
+  if (warp == kDtLoad) {
+    // ============================================================ pages, scales, loads
+    DpPlace nx = at;                             // the tile whose page is looked up
+    int nx_left = left;
+    // a lane's box of a tile: its page (-1: none), head and first row in the page
+    struct Box {
+      int page = -1, hk = 0, row = 0;
+    };
+    auto look = [&]() {
+      Box x;
+      if (nx_left <= 0) return x;
+      if (lane < p.boxes) {
+        const int key = paged_key0(nx.s, nx.tile, kDtKeys) + lane * box_rows;
+        const int nth = p.page_magic ? __umulhi(key >> 4, p.page_magic) : key >> 4;
+        x.row = key - nth * p.page;
+        x.hk = nx.hk;
+        if (key < nx.s.len) x.page = p.table[static_cast<size_t>(nx.b) * p.per_seq + nth];
+      }
+      --nx_left;
+      if (++nx.tile == nx.s.tiles) dp_next_unit(p, nx, kDtKeys);
+      return x;
+    };
+    auto head_of = [&](const Box& x) {           // < 0: none
+      return x.page >= 0 && x.page < p.pages ? x.page * p.Hk + x.hk : -1;
+    };
+    bool alive = true;
+    int j = 0, issued = 0;                       // tiles, loads
+    auto load = [&](const CUtensorMap* tm, int head, int row, uint32_t bytes) {
+      const int slot = issued % L::kSlots;
+      if (issued >= L::kSlots)
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bCodesEmpty + slot),
+                                                         (issued / L::kSlots - 1) & 1, wd,
+                                                         kSiteDtCodesEmpty));
+      if (!alive) return;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::bCodesFull + slot), bytes);
+      __syncwarp();
+      if (head >= 0)
+        tma_load_rows(sbase + L::kRing + slot * L::kCodes + lane * box_rows * D, tm,
+                      bar(L::bCodesFull + slot), head * p.page + row);
+      ++issued;
+    };
+    // pages are asked for two tiles ahead, scales one
+    Box x0 = look(), x1 = look();
+    int head0 = head_of(x0);
+    float ks = 0.f, vs = 0.f;
+    if (head0 >= 0) {
+      ks = p.k_scale[head0];
+      vs = p.v_scale[head0];
+    }
+    for (; j < left && alive; ++j) {
+      const int ms = j % kDtMetas;
+      const uint32_t have = __ballot_sync(0xffffffffu, head0 >= 0);
+      const uint32_t bytes = __popc(have) * box_rows * D;
+      load(&p.tm_k, head0, x0.row, bytes);
+      load(&p.tm_v, head0, x0.row, bytes);
+      const int head1 = head_of(x1);
+      float ks1 = 0.f, vs1 = 0.f;
+      if (head1 >= 0) {
+        ks1 = p.k_scale[head1];
+        vs1 = p.v_scale[head1];
+      }
+      const Box x2 = look();
+      if (j >= kDtMetas)
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaEmpty + ms),
+                                                         (j / kDtMetas - 1) & 1, wd,
+                                                         kSiteDtMetaEmpty));
+      if (lane < p.boxes) {
+        const int per = 8 / p.boxes;
+        for (int i = lane * per; i < (lane + 1) * per; ++i) {
+          metas[ms].ks[i] = ks;
+          metas[ms].vs[i] = vs;
+        }
+      }
+      // (a box's bit for each 16 keys of it)
+      uint32_t bits = 0;
+      for (int i = 0; i < 8; ++i) bits |= (have >> (i * p.boxes / 8) & 1u) << i;
+      const float size = head0 >= 0 && fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+      if (lane == 0) {
+        metas[ms].have = bits;
+        metas[ms].top = __uint_as_float(top);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(L::bMetaFull + ms));
+      head0 = head1;
+      x0 = x1;
+      x1 = x2;
+      ks = ks1;
+      vs = vs1;
+    }
+    // the loads land before the block ends, whatever became of their readers
+    for (int i = max(issued - L::kSlots, 0); i < issued; ++i)
+      ptx::wait_drain(bar(L::bCodesFull + i % L::kSlots), i / L::kSlots & 1, 200000000ull);
+    __syncwarp();
+  } else if (warp == kDtMma) {
+    // ============================================================ products
+    constexpr uint32_t idesc_s = ptx::idesc_f16(kDtRows, kDtKeys, 0, 0);
+    constexpr uint32_t idesc_o = ptx::idesc_f16(kDtRows, D, 0, 1);
+    const uint32_t q_lo = ptx::desc_lo(sbase + L::kQ, 16);
+    const uint32_t k_lo = ptx::desc_lo(sbase + L::kK, 16);
+    const uint32_t v_lo = ptx::desc_lo(sbase + L::kV, L::kChunkBytes);
+    bool alive = true, issued = false;
+    auto issue_s = [&](int j) {
+      const int b = j & 1;
+      // (S of two tiles ago has been read: its P was waited for)
+      alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bKFull + b), j >> 1 & 1, wd,
+                                                       kSiteDtKFull));
+      ptx::tc_fence_after();
+      if (!alive) return;
+      issued = true;
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off =
+              static_cast<uint32_t>((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+          ptx::mma_ss(tmem + L::s_col(b), ptx::desc_sw128(q_lo + off),
+                      ptx::desc_sw128(k_lo + b * (L::kTile >> 4) + off), idesc_s, kk > 0);
+        }
+        ptx::mma_commit(bar(L::bSFull + b));
+        ptx::mma_commit(bar(L::bKEmpty + b));
+      }
+    };
+    const int total = left;
+    if (total > 0) issue_s(0);
+    int j = 0;
+    for (int pieces = 0; left > 0; ++pieces, dp_next_unit(p, at, kDtKeys)) {
+      int n;
+      bool whole;
+      piece_of(n, whole);
+      left -= n;
+      for (int i = 0; i < n; ++i, ++j) {
+        if (j + 1 < total) issue_s(j + 1);
+        const int b = j & 1;
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bVFull + b), j >> 1 & 1, wd,
+                                                         kSiteDtVFull));
+        if (i == 0 && pieces > 0)                // the previous unit's O has been read
+          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bOFree), (pieces - 1) & 1, wd,
+                                                           kSiteDtOFree));
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bPFull + b), j >> 1 & 1, wd,
+                                                         kSiteDtPFull));
+        ptx::tc_fence_after();
+        if (alive && ptx::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kDtKeys / 16; ++kk)
+            ptx::mma_ts(tmem + L::kOCol, tmem + L::p_col(b) + kk * 8,
+                        ptx::desc_sw128(v_lo + b * (L::kTile >> 4) + kk * (2048 >> 4)), idesc_o,
+                        kk > 0 || i > 0);
+          ptx::mma_commit(bar(L::bPvDone + b));
+          ptx::mma_commit(bar(L::bVEmpty + b));
+        }
+      }
+    }
+    if (issued) {                                // nothing is in flight when TMEM goes
+      if (ptx::elect_one()) ptx::mma_commit(bar(L::bFinal));
+      ptx::wait_drain(bar(L::bFinal), 0, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= kDtConvert) {
+    // ============================================================ codes to half precision
+    constexpr int kRowsOf = kDtKeys / kDtTurners;            // rows of a warp
+    constexpr int kStep = D == 128 ? 4 : 8, kSteps = kRowsOf / kStep;
+    const bool is_v = warp >= kDtConvert + kDtTurners;
+    const int first = (warp & (kDtTurners - 1)) * kRowsOf;
+    const DtPiece mine = dt_piece<D>(lane);
+    const int h = mine.piece >> 2;               // (0 at d = 64)
+    // rows r and r + 8 have the same place in their eight
+    auto at8 = [&](int i) { return first + (i * kStep & 7) + mine.row; };
+    uint8_t* const tiles = sgen + (is_v ? L::kV : L::kK);
+    const int b_full = is_v ? L::bVFull : L::bKFull, b_empty = is_v ? L::bVEmpty : L::bKEmpty;
+    const uint32_t site = is_v ? kSiteDtVEmpty : kSiteDtKEmpty;
+    bool alive = true;
+    int j = 0;
+    for (; left > 0; dp_next_unit(p, at, kDtKeys)) {
+      int n;
+      bool whole;
+      piece_of(n, whole);
+      left -= n;
+      const PagedSpan s = at.s;
+      const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
+      if (!is_v) {
+        // queries, once the previous unit's last S has read them and the slot of
+        // their powers of two is free with the first tile's meta
+        if (j > 0)
+          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bKEmpty + ((j - 1) & 1)),
+                                                           (j - 1) >> 1 & 1, wd, kSiteDtKEmpty));
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaFull + j % kDtMetas),
+                                                         j / kDtMetas & 1, wd, kSiteDtMetaFull));
+        signed char* const shifts = shift_s + j % kDtMetas * kDtRows;
+        const size_t head = static_cast<size_t>(at.b) * p.Hk + at.hk;
+        const int row0 = at.block * kDtRows, rows = min(p.R - row0, kDtRows);
+#pragma unroll 1
+        for (int r0 = first; r0 < first + kRowsOf; r0 += 8) {
+          uint2 raw[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            raw[i] = make_uint2(0, 0);
+            if (r0 + i < rows && lane * 4 < D)
+              raw[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
+                                                       (head * p.R + row0 + r0 + i) * D + lane * 4);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x[4];
+            const int shift = dp_query_row<kBf16>(raw[i], x);
+            if (lane * 4 < D)
+              *reinterpret_cast<uint2*>(sgen + L::kQ + dt_place(r0 + i, lane >> 2, lane >> 1 & 1) +
+                                        (lane & 1) * 8) =
+                  make_uint2(ptx::pack2<false>(x[0], x[1]), ptx::pack2<false>(x[2], x[3]));
+            if (lane == 0) shifts[r0 + i] = static_cast<signed char>(shift);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::bQReady + j % kDtMetas));
+      }
+      for (int i = 0; i < n; ++i, ++j) {
+        const int ms = j % kDtMetas, b = j & 1;
+        const int slot = 2 * j % L::kSlots + is_v;
+        const int key0 = paged_key0(s, at.tile + i, kDtKeys);
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaFull + ms), j / kDtMetas & 1,
+                                                         wd, kSiteDtMetaFull));
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bCodesFull + slot),
+                                                         2 * j / L::kSlots & 1, wd,
+                                                         kSiteDtCodesFull));
+        const uint8_t* const codes = sgen + L::kRing + slot * L::kCodes;
+        uint4 x[kSteps];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          x[k] = *reinterpret_cast<const uint4*>(codes + dp_chunk<D>(at8(k), mine.piece) +
+                                                 (k * kStep & ~7) * D);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
+        if (is_v) {
+          const uint32_t have = metas[ms].have;
+          const bool full = have == 255u && key0 + kDtKeys - 1 <= pos_hi &&
+                            (key0 > pos_lo - p.win || key0 + kDtKeys <= p.sinks);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(L::bMetaEmpty + ms));
+          if (!full) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              const int r = first + k * kStep + mine.row;
+              if (!(have >> (r >> 4) & 1u && key0 + r <= pos_hi &&
+                    (key0 + r > pos_lo - p.win || key0 + r < p.sinks)))
+                x[k] = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        if (j >= 2)
+          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(b_empty + b), (j - 2) >> 1 & 1, wd,
+                                                           site));
+        uint8_t* const tile = tiles + b * L::kTile;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint4 y, z;
+          codes4<kInt8>(h ? x[k].z : x[k].x, y.x, y.y);
+          codes4<kInt8>(h ? x[k].w : x[k].y, y.z, y.w);
+          codes4<kInt8>(h ? x[k].x : x[k].z, z.x, z.y);
+          codes4<kInt8>(h ? x[k].y : x[k].w, z.z, z.w);
+          uint8_t* const to = tile + (k * kStep & ~7) * 128;
+          *reinterpret_cast<uint4*>(to + dt_place(at8(k), mine.piece, h)) = y;
+          *reinterpret_cast<uint4*>(to + dt_place(at8(k), mine.piece, h ^ 1)) = z;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(b_full + b));
+      }
+    }
+  } else if ((warp & 3) < quarters) {
+    // ============================================================ softmax
+    const int quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* const meet = reinterpret_cast<float*>(sgen + L::kMeet) + r;
+    // the four threads of a row, in warps four apart, come to one value
+    auto row_sync = [&]() { ptx::named_bar_sync(1 + quarter, 128); };
+    auto row_all = [&](float v, auto&& join) {
+      if (part >= 2) meet[(part - 2) * kDtRows] = v;
+      row_sync();
+      if (part < 2) {
+        v = join(v, meet[part * kDtRows]);
+        meet[part * kDtRows] = v;
+      }
+      row_sync();
+      v = join(meet[0], meet[kDtRows]);
+      row_sync();
+      return v;
+    };
+    int j = 0;
+    uint32_t q_parity = 0;
+    for (int pieces = 0; left > 0; ++pieces, dp_next_unit(p, at, kDtKeys)) {
+      int n;
+      bool whole;
+      piece_of(n, whole);
+      const int done = rn.left - left;           // tiles of the run before the piece
+      left -= n;
+      const PagedSpan s = at.s;
+      const size_t head = static_cast<size_t>(at.b) * p.Hk + at.hk;
+      const int row0 = at.block * kDtRows, rows = min(p.R - row0, kDtRows);
+      const bool has = quarter * 32 < rows;      // a warp without rows only keeps the order
+      const int pos = s.len - p.Nq + (row0 + r) % p.Nq;
+      const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
+      float m = -INFINITY, l = 0.f, vref = 0.f, inv_vref = 0.f, qmul = 0.f;
+      bool poison = false;                       // a page's scale of values is not finite
+      for (int i = 0; i < n; ++i, ++j) {
+        const int ms = j % kDtMetas, b = j & 1;
+        const int key0 = paged_key0(s, at.tile + i, kDtKeys) + part * 32;   // of the thread's keys
+        ptx::wait_bounded(bar(L::bMetaFull + ms), j / kDtMetas & 1, wd, kSiteDtMetaFull);
+        ptx::wait_bounded(bar(L::bSFull + b), j >> 1 & 1, wd, kSiteDtSFull);
+        __syncwarp();
+        ptx::tc_fence_after();
+        const uint32_t have = metas[ms].have >> (2 * part) & 3u;
+        const float top = metas[ms].top;
+        float ks[2], vs[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          ks[k] = metas[ms].ks[2 * part + k];
+          vs[k] = (have >> k & 1u) ? metas[ms].vs[2 * part + k] : 0.f;
+          if (!(fabsf(vs[k]) < INFINITY)) {
+            poison |= paged_sees(key0 + 16 * k, 16, pos, p.win, p.sinks);
+            vs[k] = 0.f;
+          }
+        }
+        if (i == 0) {                            // (a slot's parity turns with each unit on it)
+          ptx::wait_bounded(bar(L::bQReady + ms), q_parity >> ms & 1, wd, kSiteDtQReady);
+          q_parity ^= 1u << ms;
+          const int shift = shift_s[ms * kDtRows + r];
+          qmul = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::bMetaEmpty + ms));
+        if (has) {
+          uint32_t sr[32];
+          ptx::tmem_ld32(lanes + L::s_col(b) + part * 32, sr);
+          ptx::tmem_wait_ld();
+          float x[32];
+          const uint64_t q2 = ptx::f2_pack(qmul, qmul);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t k2 = ptx::f2_pack(ks[k], ks[k]);
+#pragma unroll
+            for (int e = 16 * k; e < 16 * k + 16; e += 2)
+              ptx::f2_unpack(ptx::fmul2(ptx::fmul2(ptx::f2_pack(__uint_as_float(sr[e]),
+                                                                __uint_as_float(sr[e + 1])),
+                                                   q2),
+                                        k2),
+                             x[e], x[e + 1]);
+          }
+          const bool full = have == 3u && key0 + 31 <= pos_lo &&
+                            (key0 > pos_hi - p.win || key0 + 32 <= p.sinks);
+          if (!full) {
+            const uint32_t vis = (ptx::bit_range(pos - p.win + 1 - key0, pos + 1 - key0) |
+                                  ptx::bit_range(0, min(p.sinks, pos + 1) - key0)) &
+                                 ((have & 1u ? 0xffffu : 0u) | (have & 2u ? 0xffff0000u : 0u));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(vis >> e & 1u)) x[e] = -INFINITY;
+          }
+          float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            a0 = ptx::max3(a0, x[e + 0], x[e + 1]);
+            a1 = ptx::max3(a1, x[e + 2], x[e + 3]);
+          }
+          float mx = fmaxf(a0, a1);
+          // a row keeps its reference until a score passes it by the threshold;
+          // its threads meet only then
+          float f = 1.f;
+          if (ptx::named_bar_any(1 + quarter, 128, mx > m + kDpTau)) {
+            mx = row_all(mx, [](float u, float v) { return fmaxf(u, v); });
+            if (mx > m + kDpTau) {
+              if (m != -INFINITY) f = ptx::ex2(m - mx);
+              m = mx;
+              l *= f;
+            }
+          }
+          // the unit of O follows the tile's scales, alike in every thread
+          if (top > vref || (top > 0.f && top < vref * (1.f / 64.f))) {
+            const float unit = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
+            const float now = fminf(fmaxf(unit, 0x1p-120f), 0x1p120f);
+            if (vref > 0.f) f *= fminf(vref / now, 0x1p120f);
+            vref = now;
+            inv_vref = 1.f / now;
+          }
+          const float m0 = m == -INFINITY ? 0.f : m;
+          const uint64_t nm2 = ptx::f2_pack(-m0, -m0);
+          uint64_t acc = ptx::f2_pack(0.f, 0.f);
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float rv = vs[k] * inv_vref;
+            const uint64_t r2 = ptx::f2_pack(rv, rv);
+#pragma unroll
+            for (int e = 16 * k; e < 16 * k + 16; e += 2) {
+              float y0, y1, p0, p1;
+              ptx::f2_unpack(ptx::fadd2(ptx::f2_pack(x[e], x[e + 1]), nm2), y0, y1);
+              const uint64_t pr = ptx::f2_pack(ptx::ex2(y0), ptx::ex2(y1));
+              acc = ptx::fadd2(acc, pr);
+              ptx::f2_unpack(ptx::fmul2(pr, r2), p0, p1);
+              pk[e / 2] = ptx::pack2<false>(p0, p1);
+            }
+          }
+          float s0, s1;
+          ptx::f2_unpack(acc, s0, s1);
+          l += s0 + s1;
+          // O and the other P are in use until the previous products are done
+          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            ptx::wait_bounded(bar(L::bPvDone + (b ^ 1)), (j - 1) >> 1 & 1, wd, kSiteDtPvDone);
+            __syncwarp();
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {
+              uint32_t a[16];
+              ptx::tmem_ld16(lanes + L::kOCol + c, a);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
+              ptx::tmem_st16(lanes + L::kOCol + c, a);
+            }
+          }
+          if (j >= 2) {
+            ptx::wait_bounded(bar(L::bPvDone + b), (j - 2) >> 1 & 1, wd, kSiteDtPvDone);
+            __syncwarp();
+            ptx::tc_fence_after();
+          }
+          ptx::tmem_st16(lanes + L::p_col(b) + part * 16, pk);
+          ptx::tmem_wait_st();
+        } else if (j >= 2) {
+          ptx::wait_bounded(bar(L::bPvDone + b), (j - 2) >> 1 & 1, wd, kSiteDtPvDone);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::bPFull + b));
+      }
+
+      // ---- the unit's result or its part
+      ptx::wait_bounded(bar(L::bPvDone + ((j - 1) & 1)), (j - 1) >> 1 & 1, wd, kSiteDtPvDone);
+      __syncwarp();
+      ptx::tc_fence_after();
+      const int unit = static_cast<int>(head) * p.row_blocks + at.block;
+      const size_t slot = 2 * static_cast<size_t>(run) + (pieces == 0 ? 0 : 1);
+      if (has) {
+        auto sum = [](float u, float v) { return u + v; };
+        const float lt = row_all(l, sum);
+        poison = row_all(poison ? 1.f : 0.f, sum) != 0.f;
+        const float mt = m == -INFINITY ? 0.f : m;
+        const float f = whole ? (lt != 0.f ? vref / lt : 0.f) : vref;
+        const size_t row = head * p.R + row0 + r;
+#pragma unroll 1
+        for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {
+          uint32_t a[16];
+          ptx::tmem_ld16(lanes + L::kOCol + c, a);
+          ptx::tmem_wait_ld();
+          float x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[e] = __uint_as_float(a[e]) * f;
+            if (lt == 0.f) x[e] = 0.f;
+            if (poison) x[e] = NAN;
+          }
+          if (r < rows) {
+            if (whole) {
+              uint4* const out =
+                  reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D + c);
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                out[v] = make_uint4(ptx::pack2<kBf16>(x[8 * v], x[8 * v + 1]),
+                                    ptx::pack2<kBf16>(x[8 * v + 2], x[8 * v + 3]),
+                                    ptx::pack2<kBf16>(x[8 * v + 4], x[8 * v + 5]),
+                                    ptx::pack2<kBf16>(x[8 * v + 6], x[8 * v + 7]));
+            } else {
+              float4* const out = p.part_o + (slot * p.slot_rows + r) * (D / 4) + c / 4;
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                out[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+            }
+          }
+        }
+        if (part == 0 && r < rows) {
+          if (whole)
+            p.lse[row] = lt != 0.f ? (ptx::lg2(lt) + mt) * 0.693147180559945309f : -INFINITY;
+          else
+            p.part_ml[slot * p.slot_rows + r] = make_float2(mt, lt);
+        }
+      }
+      if (at.tile == 0 && threadIdx.x == 0)
+        p.cut[unit] = whole ? make_int2(-1, 0)
+                            : make_int2(static_cast<int>(slot),
+                                        dec_run_of(deal, rn.start + done + s.tiles - 1));
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(L::bOFree));
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kDtMma) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fa

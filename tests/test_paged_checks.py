@@ -101,10 +101,11 @@ def test_decode(args, code):
 
 
 @pytest.mark.parametrize("B,H,Nq,d,per_seq,ok", [
-    # units times (tiles of a capacity + 1) stay below 2^31: tiles of 32 keys at d = 128, 64 at 64
+    # units times (tiles of a capacity + 1) stay below 2^31: up to 8 rows a key/value head tiles
+    # of 32 keys at d = 128 and of 64 at 64, for more rows tiles of 128 keys
     (1 << 10, 1 << 10, 1, 128, 2047, False), (1 << 10, 1 << 10, 1, 128, 2046, True),
     (1 << 10, 1 << 10, 1, 64, 4094, False), (1 << 10, 1 << 10, 1, 64, 4092, True),
-    (1 << 10, 1 << 9, 16, 128, 4095, False), (1 << 10, 1 << 9, 16, 128, 4094, True),
+    (1 << 10, 1 << 9, 16, 128, 16380, False), (1 << 10, 1 << 9, 16, 64, 16376, True),
 ])
 def test_units_times_tiles(lib, B, H, Nq, d, per_seq, ok):
     if ok and torch.cuda.is_available():

@@ -7,6 +7,8 @@ and checked against the definitions slot by slot:
 * shared memory (dp_row, dp_chunk): slots are a permutation of a tile's rows,
   chunks of a row cover it, and the reads of a quarter (half) warp touch every
   bank once;
+  (dt_piece, dt_place) codes turned to half precision cover a tile, go where the
+  128-byte swizzle puts them, and do the same;
 * append (append_span, append_pages): new slots are those of the definition,
   and the launch has a block for each page that they touch;
 * scales (page_scale): the smallest power of two (e4m3) and the 127th part
@@ -29,7 +31,7 @@ PROGRAM = r'''
 #include <cstring>
 #include <set>
 #include <vector>
-#include "fa_decode_paged_kernel.cuh"
+#include "fa_decode_paged_tc_kernel.cuh"
 #include "fa_rotary.cuh"
 #define BAD(...) do { std::printf(__VA_ARGS__); std::printf("\n"); return 1; } while (0)
 
@@ -37,7 +39,7 @@ static int check_span(int Nq, int capacity, int count, int win, int sinks, int k
   const fa::PagedSpan s = fa::paged_span(count, capacity, Nq, win, sinks, keys);
   const int len = count < 0 ? 0 : count > capacity ? capacity : count;
   if (s.len != len || s.tiles < 1) BAD("len %d tiles %d", s.len, s.tiles);
-  if (s.tiles > (capacity + keys - 1) / keys + 1) BAD("tiles %d", s.tiles);
+  if (s.tiles > (capacity + keys - 1) / keys + 1 || s.tiles * keys > capacity + 2 * keys) BAD("tiles %d", s.tiles);
   std::vector<int> listed(capacity + 2 * keys, 0);
   for (int t = 0; t < s.tiles; ++t) {
     const int k0 = fa::paged_key0(s, t, keys);
@@ -103,6 +105,36 @@ static int check_layout() {
       }
       if (static_cast<int>(banks.size()) != n) BAD("V banks of %d", D);
     }
+  return 0;
+}
+
+// Turning codes to half precision: every piece of a step's rows once, no bank
+// twice in a quarter warp, neither reading nor writing.
+template <int D>
+static int check_pieces() {
+  const int step = D == 128 ? 4 : 8;
+  for (int r0 = 0; r0 < 128; r0 += step) {
+    std::set<int> seen;
+    for (int q = 0; q < 4; ++q) {
+      std::set<unsigned> read, write[2];
+      for (int lane = 8 * q; lane < 8 * q + 8; ++lane) {
+        const fa::DtPiece m = fa::dt_piece<D>(lane);
+        if (m.row < 0 || m.row >= step || m.piece < 0 || m.piece >= D / 16) BAD("piece of lane %d", lane);
+        const int r = r0 + m.row, h = m.piece >> 2;
+        seen.insert(m.row * 8 + m.piece);
+        read.insert(fa::dp_chunk<D>(r, m.piece) % 128 / 16);
+        for (int k = 0; k < 2; ++k) {
+          const unsigned at = fa::dt_place(r, m.piece, h ^ k);
+          write[k].insert(at % 128 / 16);
+          const int col = m.piece * 16 + (h ^ k) * 8;       // the 128-byte swizzle of a 64-column chunk
+          const unsigned plain = (col / 64) * 16384u + r * 128u + col % 64 * 2;
+          if (at != (plain ^ ((plain >> 7 & 7) << 4))) BAD("place of row %d column %d", r, col);
+        }
+      }
+      if (read.size() != 8 || write[0].size() != 8 || write[1].size() != 8) BAD("banks of %d", D);
+    }
+    if (static_cast<int>(seen.size()) != step * D / 16) BAD("pieces of %d", D);
+  }
   return 0;
 }
 
@@ -179,7 +211,7 @@ static int check_rotary() {
 }
 
 int main() {
-  if (check_layout<64>() || check_layout<128>() || check_scales() || check_rotary()) return 1;
+  if (check_layout<64>() || check_layout<128>() || check_pieces<64>() || check_pieces<128>() || check_scales() || check_rotary()) return 1;
   int op, a, b, c, d, e, f;
   while (std::scanf("%d %d %d %d %d %d %d", &op, &a, &b, &c, &d, &e, &f) == 7) {
     const int bad = op == 0 ? check_span(a, b, c, d, e, f) : check_append(a, b, c, d, e);
@@ -218,7 +250,7 @@ def test_tiles_of_a_sequence(program):
     rng = random.Random(21)
     cases = []
     for _ in range(1500):
-        keys, cap = rng.choice((32, 64)), 16 * rng.randint(1, 60)
+        keys, cap = rng.choice((32, 64, 128)), 16 * rng.randint(1, 60)
         Nq = rng.randint(1, 16)
         win = min(rng.choice((1, 2, 15, 31, 32, 33, 64, 100, 300, 9999)), cap + Nq + 1)
         count = rng.choice((cap, 0, 1, Nq - 1, rng.randint(0, cap), -5, cap + 7))
