@@ -1838,5 +1838,6 @@ def flash_attention_window(q, k, v, window, sinks=0, causal="bottom_right", seql
 
 def rotary_embedding(q, k, freqs, positions=None, seqlens=None, mscale=1.0, interleaved=False):
     """rotary_forward(q, k, ...), differentiable (first order) in q and k (k may
-    be None); the gradients are rotary_backward's."""
+    be None); the gradients are rotary_backward's.  For capture in a CUDA graph
+    see ``flash_attention_window``."""
     return _fns()[4].apply(q, k, freqs, positions, seqlens, float(mscale), bool(interleaved))

@@ -261,8 +261,10 @@ __global__ void __launch_bounds__(1024)
     const float inverse = __frcp_rn(scale);
     if (threadIdx.x == 0) scale_at[k] = scale;
     if (fresh) {
+      const uint64_t i2 = ptx::f2_pack(inverse, inverse);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] *= inverse;
+      for (int j = 0; j < 16; j += 2)
+        ptx::f2_unpack(ptx::fmul2(ptx::f2_pack(x[j], x[j + 1]), i2), x[j], x[j + 1]);
     } else if (row < keep && before < scale) {
       // codes under the old scale, quantised under the new one
       const float f = before * inverse;

@@ -64,15 +64,26 @@ __host__ __device__ __forceinline__ RotaryUnit rotary_unit(int u, int rot, bool 
   return r;
 }
 
-// Turn a unit's values x[0..7] (first vector), x[8..15] (second).
+// Turn a unit's values x[0..7] (first vector), x[8..15] (second), two pairs an
+// instruction where their registers are neighbours.
 template <bool kInterleaved>
 __device__ __forceinline__ void rotary_turn(float* x, const float* c, const float* s) {
+  if constexpr (kInterleaved) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ia = kInterleaved ? 2 * i : i, ib = kInterleaved ? 2 * i + 1 : i + 8;
-    const float a = x[ia], b = x[ib];
-    x[ia] = fmaf(a, c[i], -(b * s[i]));
-    x[ib] = fmaf(b, c[i], a * s[i]);
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = fmaf(a, c[i], -(b * s[i]));
+      x[2 * i + 1] = fmaf(b, c[i], a * s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t a = ptx::f2_pack(x[i], x[i + 1]), b = ptx::f2_pack(x[i + 8], x[i + 9]);
+      const uint64_t c2 = ptx::f2_pack(c[i], c[i + 1]), s2 = ptx::f2_pack(s[i], s[i + 1]);
+      const uint64_t n2 = ptx::f2_pack(-s[i], -s[i + 1]);
+      ptx::f2_unpack(ptx::ffma2(a, c2, ptx::fmul2(b, n2)), x[i], x[i + 1]);
+      ptx::f2_unpack(ptx::ffma2(b, c2, ptx::fmul2(a, s2)), x[i + 8], x[i + 9]);
+    }
   }
 }
 

@@ -835,7 +835,7 @@ int fa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale
  * Errors as fa_cache_append and fa_decode_window.  With R = H / Hk * Nq rows a
  * key/value head, FA_ERR_SHAPE also for B * H * Nq over 2^30, and for
  * B * Hk * (ceil(capacity / 32) + 1) of 2^31 or more (64 in the place of 32 at
- * d = 64); for R over 8, B * Hk * ceil(R / 128) * (ceil(capacity / 128) + 1).
+ * d = 64); for R over 16, B * Hk * ceil(R / 128) * (ceil(capacity / 128) + 1).
  */
 int fa_decode_paged(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                     const float *v_scale, void *o, float *lse, int B, int H, int Hk, int Nq, int d,

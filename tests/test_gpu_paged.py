@@ -117,6 +117,9 @@ APPEND = [
     (2, 2, 30, 80, 2, 128, "int8", "bf16", 128, True, [12, -4], None, 1.0),     # before slot 0
     (70, 2, 3, 16, 2, 64, "e4m3", "fp16", 64, False, [3 + 29 * b % 30 for b in range(70)], None, 30.0),
     (2, 2, 20, 16, 3, 64, "e4m3", "bf16", 64, False, [30, 20], [25, -3], 1e-36),  # least scales
+    (3, 5, 8, 16, 3, 128, "int8", "bf16", 112, True, [20, 8, 48], [8, 3, 5], 4.0),  # a warp's most
+    (3, 5, 9, 16, 3, 64, "e4m3", "fp16", 32, False, [20, 9, 48], [9, 3, 5], 4.0),
+    (2, 3, 300, 128, 3, 128, "e4m3", "bf16", 128, False, [384, 310], [300, 299], 1.0),
 ]
 
 
@@ -197,6 +200,32 @@ def test_append_leaves_bad_pages_and_nonfinite(code):
     assert torch.isfinite(cache.k_scale[1]).all()
 
 
+@pytest.mark.parametrize("T", [1, 40])
+def test_append_in_a_graph(T):
+    """A captured append reads lengths and counts when it is replayed: the steps of
+    a decoding loop by one graph, as by eager calls."""
+    B, Hk, page, per, d = 3, 2, 32, 6, 64
+    caches = [fa.make_paged_cache(B * per, Hk, page, d) for _ in range(2)]
+    table, f = deal(B, per, B * per, seed=30), fa.rotary_frequencies(64, device="cuda")
+    k, v = (torch.zeros(B, Hk, T, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n, c = ints([0] * B), ints([0] * B)
+    fa.cache_append(k, v, caches[1], table, n, counts=c, freqs=f)         # writes nothing
+    assert not any(x.view(torch.uint8).any() if x.element_size() == 1 else x.any() for x in caches[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.cache_append(k, v, caches[1], table, n, counts=c, freqs=f)
+    for step in range(4):
+        k.copy_(pc.normal((B, Hk, T, d), "bf16", 40 + step).cuda())
+        v.copy_(pc.normal((B, Hk, T, d), "bf16", 50 + step).cuda())
+        c.copy_(ints([T, max(T - step, 1), 0]))
+        n.add_(c)
+        fa.cache_append(k, v, caches[0], table, n, counts=c, freqs=f)
+        g.replay()
+    status_ok()
+    assert all(torch.equal(a.view(torch.uint8) if a.element_size() == 1 else a,
+                           b.view(torch.uint8) if b.element_size() == 1 else b) for a, b in zip(*caches))
+
+
 # ---------------------------------------------------------------- read
 
 @pytest.mark.parametrize("B,Hk,page,per,d,code,dtype,lens,length", [
@@ -246,6 +275,15 @@ DECODE = [
     (300, 2, 2, 1, 16, 9, 64, "int8", "bf16", 64, 2, [(7 * b) % 131 for b in range(300)]),
     (2, 40, 8, 4, 96, 30, 64, "e4m3", "fp16", None, 0, [2880, 2001]),
     (3, 5, 5, 5, 112, 5, 64, "int8", "bf16", 2 ** 31 - 1, 7, [560, 3, -9]),
+    # rows a key/value head: 9, 16 (one warp's most), 17 to 128 (one unit), 144
+    (2, 9, 1, 1, 16, 40, 128, "int8", "bf16", None, 0, [640, 77]),
+    (3, 4, 1, 4, 64, 12, 64, "e4m3", "fp16", 90, 2, [768, 5, 300]),
+    (2, 17, 1, 1, 128, 6, 128, "e4m3", "bf16", None, 0, [768, 129]),
+    (4, 12, 2, 6, 16, 20, 64, "int8", "fp16", 40, 130, [320, 190, 4, 0]),
+    (1, 8, 1, 16, 48, 60, 128, "e4m3", "bf16", None, 0, [2880]),
+    (2, 9, 1, 16, 32, 30, 64, "e4m3", "bf16", 500, 3, [960, 10]),
+    (1, 9, 1, 16, 80, 12, 128, "int8", "fp16", None, 0, [950]),
+    (70, 20, 1, 1, 32, 5, 128, "int8", "bf16", None, 0, [13 * b % 161 for b in range(70)]),
 ]
 
 
@@ -286,10 +324,11 @@ def test_decode_against_definition(case):
 
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
 @pytest.mark.parametrize("d", [64, 128])
-def test_unseen_slots_may_hold_anything(code, d):
+@pytest.mark.parametrize("H", [4, 8, 24])     # 8, 16 and 48 rows a key/value head
+def test_unseen_slots_may_hold_anything(code, d, H):
     """NaN codes and NaN or infinite scales in slots and pages that nobody sees,
     table entries that name no page, and tokens that do not see the last page."""
-    B, H, Hk, Nq, page, per = 3, 4, 2, 4, 16, 12
+    B, Hk, Nq, page, per = 3, 2, 4, 16, 12
     pages = B * per + 3
     cache = pc.random_cache(pages, Hk, page, d, code, seed=3)
     table = deal(B, per, pages, seed=4)
@@ -332,10 +371,11 @@ def test_unseen_slots_may_hold_anything(code, d):
 
 
 @pytest.mark.parametrize("page", [16, 64])
-def test_a_scale_that_is_not_finite_reaches_only_who_sees_it(page):
+@pytest.mark.parametrize("H", [2, 4, 20])     # 6, 12 and 60 rows
+def test_a_scale_that_is_not_finite_reaches_only_who_sees_it(page, H):
     """The last page's scale is NaN (its only token was): the tokens before it
     do not see the page and keep their results, the last one gets NaN."""
-    B, H, Hk, Nq, d = 1, 2, 1, 3, 128
+    B, Hk, Nq, d = 1, 1, 3, 128
     for which in ("k_scale", "v_scale"):
         cache = pc.random_cache(6, Hk, page, d, "e4m3", seed=6)
         table = ints([[4, 2, 0, 5]])
@@ -349,18 +389,22 @@ def test_a_scale_that_is_not_finite_reaches_only_who_sees_it(page):
         assert torch.isnan(got["o"][:, :, 2]).all()
 
 
-def test_nonfinite_scores():
+@pytest.mark.parametrize("heads", [1, 4, 12])   # 4, 16 and 48 rows
+def test_nonfinite_scores(heads):
     """A NaN or +inf score gives NaN, one of -inf weighs nothing."""
     cache = pc.random_cache(4, 1, 32, 64, "int8", seed=8)
     cache.k.view(torch.uint8)[:] = 0
     cache.k[1, 0, 3, 0] = 1                    # key 35's first element
     table, lens = ints([[0, 1]]), [40]
-    q = torch.zeros(1, 4, 1, 64, dtype=torch.float16, device="cuda")
+    q = torch.zeros(1, 4 * heads, 1, 64, dtype=torch.float16, device="cuda")
     cache.k_scale[1] = float("inf")            # 0 * inf is NaN: every score of the page is
     assert torch.isnan(run_decode(q, cache, table, lens)["o"]).all()
     cache.k_scale[1] = 3e38
     q[0, 0, 0, 0], q[0, 1, 0, 0], q[0, 2, 0, 0] = 6e4, -6e4, float("nan")
+    q = q[:, :4].repeat(1, heads, 1, 1)
     got = run_decode(q, cache, table, lens)
+    for x in got.values():
+        assert torch.equal(x[:, :4].repeat(1, heads, *[1] * (x.dim() - 2)).nan_to_num(7e4), x.nan_to_num(7e4))
     assert torch.isnan(got["o"][0, 0]).all() and torch.isnan(got["lse"][0, 0]).all()
     assert torch.isnan(got["o"][0, 2]).all()
     _, v = pc.values(cache, table, lens)
@@ -371,16 +415,17 @@ def test_nonfinite_scores():
         assert abs(got["lse"][0, h, 0].item() - np.log(len(list(keys)))) <= 2.0 ** -17
 
 
-def test_wide_ranges():
+@pytest.mark.parametrize("G", [1, 2, 5])
+def test_wide_ranges(G):
     """Queries of extreme magnitude and pages of very different scales: large
     values in pages of no weight, the weight in pages of small ones."""
-    B, H, Hk, Nq, page, d = 1, 8, 1, 1, 32, 128
+    B, H, Hk, Nq, page, d = 1, 8 * G, 1, 1, 32, 128
     cache = pc.random_cache(8, Hk, page, d, "e4m3", seed=9)
     table, lens = ints([[7, 6, 5, 4, 3, 2, 1, 0]]), [250]
     cache.v_scale[7:] = 2.0 ** 60 / 448
     cache.v_scale[3] = 2.0 ** -40
     q = pc.normal((B, H, Nq, d), "bf16", 10)
-    q = (q.float() * torch.exp2(torch.tensor([-120.0, -60, -20, 0, 0, 2, 2, 3]))[None, :, None, None]).bfloat16().cuda()
+    q = (q.float() * torch.exp2(torch.tensor([-120.0, -60, -20, 0, 0, 2, 2, 3] * G))[None, :, None, None]).bfloat16().cuda()
     for ks in (1.0, 1e-30):
         cache.k_scale[:] = ks / 100
         scale = pc.scale_of(d) / ks
@@ -417,10 +462,11 @@ def test_pool_beyond_two_gigabytes():
     pc.check(got, *pc.reference(q, kk, vv, masks_of(t2, 6, page, 2, lens, None, 0), pc.scale_of(d), "bf16"), "far")
 
 
-def test_two_graphs_and_streams():
+@pytest.mark.parametrize("H", [8, 24, 64])
+def test_two_graphs_and_streams(H):
     """Two captured calls with workspaces of their own replayed together on two
     streams, and a call on a stream that is not current."""
-    B, H, Hk, Nq, page, per, d = 4, 8, 2, 1, 32, 40, 128
+    B, Hk, Nq, page, per, d = 4, 2, 1, 32, 40, 128
     pages = B * per
     cache = pc.random_cache(pages, Hk, page, d, "e4m3", seed=14)
     table, lens = deal(B, per, pages, seed=15), [1280, 700, 33, 1000]

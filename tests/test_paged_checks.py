@@ -100,20 +100,23 @@ def test_decode(args, code):
     assert fa.fa_decode_paged(**{**DEC, **args}) == code
 
 
-@pytest.mark.parametrize("B,H,Nq,d,per_seq,ok", [
-    # units times (tiles of a capacity + 1) stay below 2^31: up to 8 rows a key/value head tiles
-    # of 32 keys at d = 128 and of 64 at 64, for more rows tiles of 128 keys
-    (1 << 10, 1 << 10, 1, 128, 2047, False), (1 << 10, 1 << 10, 1, 128, 2046, True),
-    (1 << 10, 1 << 10, 1, 64, 4094, False), (1 << 10, 1 << 10, 1, 64, 4092, True),
-    (1 << 10, 1 << 9, 16, 128, 16380, False), (1 << 10, 1 << 9, 16, 64, 16376, True),
+@pytest.mark.parametrize("B,Hk,G,Nq,d,per_seq,ok", [
+    # units times (tiles of a capacity + 1) stay below 2^31: up to 16 rows a key/value head tiles
+    # of 32 keys at d = 128 and of 64 at 64, for more rows units of 128 and tiles of 128 keys
+    (1 << 10, 1 << 10, 1, 1, 128, 2047, False), (1 << 10, 1 << 10, 1, 1, 128, 2046, True),
+    (1 << 10, 1 << 10, 1, 1, 64, 4094, False), (1 << 10, 1 << 10, 1, 1, 64, 4092, True),
+    (1 << 10, 1 << 9, 1, 16, 128, 4095, False), (1 << 10, 1 << 9, 1, 16, 128, 4094, True),
+    (1 << 10, 1 << 8, 2, 16, 128, 32764, False), (1 << 10, 1 << 8, 2, 16, 64, 32760, True),
+    (1 << 10, 1 << 7, 9, 16, 64, 32764, False), (1 << 10, 1 << 7, 9, 16, 128, 32760, True),
 ])
-def test_units_times_tiles(lib, B, H, Nq, d, per_seq, ok):
+def test_units_times_tiles(lib, B, Hk, G, Nq, d, per_seq, ok):
     if ok and torch.cuda.is_available():
         pytest.skip("a GPU is present")
-    a = dict(DEC, B=B, H=H, Hk=H, Nq=Nq, d=d, pages=3, page_size=32, pages_per_seq=per_seq)
+    H = Hk * G
+    a = dict(DEC, B=B, H=H, Hk=Hk, Nq=Nq, d=d, pages=3, page_size=32, pages_per_seq=per_seq)
     assert fa.fa_decode_paged(**a) == (fa.FA_ERR_DEVICE if ok else SHAPE)
     out = ctypes.c_size_t(0)
-    assert lib.fa_decode_paged_workspace_size(B, H, H, Nq, d, 32, per_seq, ctypes.byref(out)) == \
+    assert lib.fa_decode_paged_workspace_size(B, H, Hk, Nq, d, 32, per_seq, ctypes.byref(out)) == \
         (fa.FA_ERR_DEVICE if ok else SHAPE)
 
 
@@ -153,6 +156,19 @@ def test_binding_rotary():
         for a, b in ((q[0], k), (q, t(2, 2, 8, 64)), (q, t(1, 2, 9, 64)), (q, t(1, 2, 8, 128)), (q, k)):
             with pytest.raises(ValueError):     # the last: host tensors
                 call(a, b, f)
+
+
+def test_rotary_embedding_is_differentiable_once(monkeypatch):
+    """As the attention wrappers: a second differentiation raises."""
+    monkeypatch.setattr(fa, "rotary_forward", lambda q, k, *a, **kw: ((3.0 * q).detach(), None))
+    monkeypatch.setattr(fa, "rotary_backward", lambda q, k, *a, **kw: ((3.0 * q).detach(), None))
+    q = torch.ones(1, 1, 5, 8, requires_grad=True)
+    y, none = fa.rotary_embedding(q, None, fa.rotary_frequencies(16))
+    assert none is None
+    (g,) = torch.autograd.grad((y ** 2).sum(), q, create_graph=True)
+    assert torch.equal(g, torch.full_like(g, 18.0))
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        ((g ** 2).sum() + (q ** 2).sum()).backward()
 
 
 def test_binding_cache():
