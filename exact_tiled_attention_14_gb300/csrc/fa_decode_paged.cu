@@ -68,11 +68,12 @@ cudaError_t launch_variant(const DecPagedParams& p, int tiles, int sms, cudaStre
   // take several units where those are many, since most are whole then, and
   // more threads where a unit may have many parts.
   const int units = p.B * p.Hk * p.row_blocks, per_block = (units + 4 * sms - 1) / (4 * sms);
-  constexpr int kFew = 512 / D, kMany = 2048 / D;     // groups of D / 4 threads
-  const bool many = p.runs > 8 * kFew * units;
+  constexpr int kMany = 2048 / D;                     // groups of D / 4 threads
+  const bool many = p.runs > 16 * units;              // more than two batches of parts
+  const int rows = many ? 1 : kDpCombineThreads / (D / 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((units + per_block - 1) / per_block, p.slot_rows);
-  cfg.blockDim = dim3((many ? kMany : kFew) * (D / 4));
+  cfg.gridDim = dim3((units + per_block - 1) / per_block, (p.slot_rows + rows - 1) / rows);
+  cfg.blockDim = dim3(many ? kMany * (D / 4) : kDpCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -81,7 +82,7 @@ cudaError_t launch_variant(const DecPagedParams& p, int tiles, int sms, cudaStre
   cfg.numAttrs = 1;
   return many ? cudaLaunchKernelEx(&cfg, fa_decode_paged_combine_kernel<D, kBf16, kMany>, p, units,
                                    per_block)
-              : cudaLaunchKernelEx(&cfg, fa_decode_paged_combine_kernel<D, kBf16, kFew>, p, units,
+              : cudaLaunchKernelEx(&cfg, fa_decode_paged_combine_kernel<D, kBf16, 1>, p, units,
                                    per_block);
 }
 

@@ -709,26 +709,31 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
     ptx::wait_drain(bar(waited % kStages), waited / kStages & 1, 200000000ull);
 }
 
-// The cut units: a block takes `per_block` units for one row of a part and adds
-// up the unit's parts of that row, 4 columns a thread; kGroups groups of
-// threads take other parts each, kBatch loads in flight, and meet in shared
-// memory.  Every part is scaled to the largest maximum, and the sum divided
-// once.  A row without a visible key has no live part (a sum of NaN is live).
+// The cut units: a block takes `per_block` units and adds up the unit's parts of
+// a row, 4 columns a thread.  With few parts D / 4 threads do a row alone, and a
+// block several rows (kGroups = 1); with many, kGroups such groups take other
+// parts of one row each and meet in shared memory.  kBatch parts are in flight at
+// a time.  Every part is scaled to the largest maximum, and the sum divided once.
+// A row without a visible key has no live part (a sum of NaN is live).
+// (5 parts of 512 units, 4 rows: 8.0 us with four groups a row, 5.8 alone.)
+constexpr int kDpCombineThreads = 128;       // of kGroups = 1
 template <int D, bool kBf16, int kGroups>
-__global__ void __launch_bounds__(kGroups * (D / 4))
+__global__ void __launch_bounds__(kGroups == 1 ? kDpCombineThreads : kGroups * (D / 4))
     fa_decode_paged_combine_kernel(const __grid_constant__ DecPagedParams p, int units,
                                    int per_block) {
   constexpr int kPer = D / 4, kBatch = 8;
+  constexpr int kRowsOf = kGroups == 1 ? kDpCombineThreads / kPer : 1;   // of a block
   __shared__ float4 acc_s[kGroups][kPer];
   __shared__ float2 ml_s[kGroups];
-  const int c = threadIdx.x % kPer, group = threadIdx.x / kPer, r = blockIdx.y;
+  const int c = threadIdx.x % kPer, of = threadIdx.x / kPer;
+  const int group = kGroups == 1 ? 0 : of, r = blockIdx.y * kRowsOf + (kGroups == 1 ? of : 0);
   ptx::griddep_wait();   // the parts are complete, and this grid ends after the main one
   const int u1 = min((static_cast<int>(blockIdx.x) + 1) * per_block, units);
   for (int u = blockIdx.x * per_block; u < u1; ++u) {
     const int2 cut = p.cut[u];
     if (cut.x < 0) continue;
     const int head = u / p.row_blocks, row = (u - head * p.row_blocks) * p.slot_rows + r;
-    if (row >= p.R) continue;
+    if (r >= p.slot_rows || row >= p.R) continue;
     const int run0 = cut.x >> 1, parts = cut.y - run0 + 1;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -764,26 +769,33 @@ __global__ void __launch_bounds__(kGroups * (D / 4))
           l = fmaf(f, ml[k].y, l);
         }
     }
-    acc_s[group][c] = acc;
-    if (c == 0) ml_s[group] = make_float2(m, l);
-    __syncthreads();
-    if (group == 0) {
-      float top = -INFINITY, lt = 0.f;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = m, lt = l;
+    float4 sum = acc;
+    if constexpr (kGroups > 1) {
+      acc_s[group][c] = acc;
+      if (c == 0) ml_s[group] = make_float2(m, l);
+      __syncthreads();
+      if (group == 0) {
+        top = -INFINITY;
+        lt = 0.f;
+        sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k)
-        if (ml_s[k].y != 0.f) top = fmaxf(top, ml_s[k].x);
+        for (int k = 0; k < kGroups; ++k)
+          if (ml_s[k].y != 0.f) top = fmaxf(top, ml_s[k].x);
 #pragma unroll 4
-      for (int k = 0; k < kGroups; ++k)
-        if (ml_s[k].y != 0.f) {
-          const float f = ptx::ex2(ml_s[k].x - top);
-          const float4 x = acc_s[k][c];
-          sum.x = fmaf(f, x.x, sum.x);
-          sum.y = fmaf(f, x.y, sum.y);
-          sum.z = fmaf(f, x.z, sum.z);
-          sum.w = fmaf(f, x.w, sum.w);
-          lt = fmaf(f, ml_s[k].y, lt);
-        }
+        for (int k = 0; k < kGroups; ++k)
+          if (ml_s[k].y != 0.f) {
+            const float f = ptx::ex2(ml_s[k].x - top);
+            const float4 x = acc_s[k][c];
+            sum.x = fmaf(f, x.x, sum.x);
+            sum.y = fmaf(f, x.y, sum.y);
+            sum.z = fmaf(f, x.z, sum.z);
+            sum.w = fmaf(f, x.w, sum.w);
+            lt = fmaf(f, ml_s[k].y, lt);
+          }
+      }
+    }
+    if (group == 0) {
       const float inv = lt != 0.f ? 1.0f / lt : 0.f;
       const size_t out = static_cast<size_t>(head) * p.R + row;
       reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D)[c] =
@@ -791,7 +803,7 @@ __global__ void __launch_bounds__(kGroups * (D / 4))
                      ptx::pack2<kBf16>(sum.z * inv, sum.w * inv));
       if (c == 0) p.lse[out] = lt != 0.f ? (ptx::lg2(lt) + top) * 0.693147180559945309f : -INFINITY;
     }
-    __syncthreads();
+    if constexpr (kGroups > 1) __syncthreads();
   }
 }
 
