@@ -110,9 +110,29 @@ __host__ __device__ __forceinline__ PagedSpan paged_span(int count, int capacity
 __host__ __device__ __forceinline__ int paged_key0(const PagedSpan& s, int t, int keys) {
   return (t < s.sink_tiles ? t : s.first + t - s.sink_tiles) * keys;
 }
+// Whether some row of a batch, at positions len - Nq .. len - 1, sees some key of
+// [key0, key0 + n).
+__host__ __device__ __forceinline__ bool paged_seen(const PagedSpan& s, int Nq, int key0, int n,
+                                                    int win, int sinks) {
+  return key0 < s.len && (key0 + n - 1 > s.len - Nq - win || key0 < sinks);
+}
 // Whether the row at position pos sees some key of [key0, key0 + n).
 __host__ __device__ __forceinline__ bool paged_sees(int key0, int n, int pos, int win, int sinks) {
   return key0 <= pos && (key0 + n - 1 > pos - win || key0 < sinks);
+}
+
+// O is held in units of vref, a power of two next to the scales of the last
+// pages (their largest, top), so that weights times a page's scale / vref round
+// like weights.  The unit after `top`: it falls to 2^-60 of its largest value
+// (most) at most, so that O, at most 2^47 units before, stays finite.
+__host__ __device__ __forceinline__ bool paged_new_unit(float vref, float top) {
+  return top > vref || (top > 0.f && top < vref * (1.f / 64.f));
+}
+__device__ __forceinline__ float paged_unit(float top, float& most) {
+  const float up = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
+  const float unit = fmaxf(fminf(fmaxf(up, 0x1p-120f), 0x1p126f), most * 0x1p-60f);
+  most = fmaxf(most, unit);
+  return unit;
 }
 
 // Key rows of the 16 of a product.  At d = 128 a row is 128 bytes, its 16-byte
@@ -407,6 +427,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       }
     float o[kJ][kTiles][4] = {};
     float vref = 0.f, inv_vref = 0.f;        // unit of O (0: nothing summed yet)
+    float vref_most = 0.f;                   // its largest
     uint32_t seen = 0;                       // rows (2 nt + e) with a reference
     const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
 
@@ -483,6 +504,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         const float ks = sc[box_of(mt)];
         const uint64_t k2 = ptx::f2_pack(ks, ks);
         vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
+        // (a page that no row sees may have any scale)
+        if (!full && !paged_seen(s, p.Nq, key0 + mt * 16, 16, p.win, p.sinks)) vs[mt] = 0.f;
         if (!(fabsf(vs[mt]) < INFINITY)) {
           vs[mt] = 0.f;
           odd = true;
@@ -519,22 +542,17 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             mx[nt][e] = ptx::max3(mx[nt][e], sv[mt][nt][e], sv[mt][nt][e + 2]);
-      // O is held in units of vref, a power of two next to the scales of the
-      // last pages: weights times their page's scale / vref round like weights
-      if (vs_top > vref || vs_top < vref * (1.f / 64.f)) {
-        if (vs_top > 0.f) {
-          const float unit = __uint_as_float((__float_as_uint(vs_top) + 0x7fffffu) & 0x7f800000u);
-          const float now = fminf(fmaxf(unit, 0x1p-120f), 0x1p120f);
-          const float f = vref > 0.f ? fminf(vref / now, 0x1p120f) : 1.f;
-          vref = now;
-          inv_vref = 1.f / now;
+      if (paged_new_unit(vref, vs_top)) {
+        const float now = paged_unit(vs_top, vref_most);
+        const float f = vref > 0.f ? vref / now : 1.f;
+        vref = now;
+        inv_vref = 1.f / now;
 #pragma unroll
-          for (int j = 0; j < kJ; ++j)
+        for (int j = 0; j < kJ; ++j)
 #pragma unroll
-            for (int nt = 0; nt < kTiles; ++nt)
+          for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[j][nt][e] *= f;
-        }
+            for (int e = 0; e < 4; ++e) o[j][nt][e] *= f;
       }
       // a row keeps its reference until a score passes it by the threshold (or is
       // its first): only then do its lanes look for its largest

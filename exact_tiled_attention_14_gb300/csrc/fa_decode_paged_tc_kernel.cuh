@@ -51,7 +51,7 @@ enum DtWaitSite : uint32_t {
 struct DtMeta {
   float ks[8], vs[8];
   uint32_t have;
-  float top;               // the largest finite |vs| of them
+  float top;               // the largest finite |vs| of those that some row sees
   uint32_t pad[2];
 };
 
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     // a lane's box of a tile: its page (-1: none), head and first row in the page
     struct Box {
       int page = -1, hk = 0, row = 0;
+      bool seen = false;                         // by some row
     };
     auto look = [&]() {
       Box x;
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const int nth = p.page_magic ? __umulhi(key >> 4, p.page_magic) : key >> 4;
         x.row = key - nth * p.page;
         x.hk = nx.hk;
+        x.seen = paged_seen(nx.s, p.Nq, key, box_rows, p.win, p.sinks);
         if (key < nx.s.len) x.page = p.table[static_cast<size_t>(nx.b) * p.per_seq + nth];
       }
       --nx_left;
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       // (a box's bit for each 16 keys of it)
       uint32_t bits = 0;
       for (int i = 0; i < 8; ++i) bits |= (have >> (i * p.boxes / 8) & 1u) << i;
-      const float size = head0 >= 0 && fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
+      const float size = head0 >= 0 && x0.seen && fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
       const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
       if (lane == 0) {
         metas[ms].have = bits;
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const bool has = quarter * 32 < rows;      // a warp without rows only keeps the order
       const int pos = s.len - p.Nq + (row0 + r) % p.Nq;
       const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
-      float m = -INFINITY, l = 0.f, vref = 0.f, inv_vref = 0.f, qmul = 0.f;
+      float m = -INFINITY, l = 0.f, vref = 0.f, inv_vref = 0.f, vref_most = 0.f, qmul = 0.f;
       bool poison = false;                       // a page's scale of values is not finite
       for (int i = 0; i < n; ++i, ++j) {
         const int ms = j % kDtMetas, b = j & 1;
@@ -494,7 +496,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           ks[k] = metas[ms].ks[2 * part + k];
-          vs[k] = (have >> k & 1u) ? metas[ms].vs[2 * part + k] : 0.f;
+          vs[k] = (have >> k & 1u) && paged_seen(s, p.Nq, key0 + 16 * k, 16, p.win, p.sinks)
+                      ? metas[ms].vs[2 * part + k]
+                      : 0.f;
           if (!(fabsf(vs[k]) < INFINITY)) {
             poison |= paged_sees(key0 + 16 * k, 16, pos, p.win, p.sinks);
             vs[k] = 0.f;
@@ -554,10 +558,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             }
           }
           // the unit of O follows the tile's scales, alike in every thread
-          if (top > vref || (top > 0.f && top < vref * (1.f / 64.f))) {
-            const float unit = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
-            const float now = fminf(fmaxf(unit, 0x1p-120f), 0x1p120f);
-            if (vref > 0.f) f *= fminf(vref / now, 0x1p120f);
+          if (paged_new_unit(vref, top)) {
+            const float now = paged_unit(top, vref_most);
+            if (vref > 0.f) f *= vref / now;
             vref = now;
             inv_vref = 1.f / now;
           }

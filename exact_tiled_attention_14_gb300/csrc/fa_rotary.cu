@@ -60,7 +60,11 @@ __global__ void __launch_bounds__(kRotThreads)
   const int n = static_cast<int>(token - b * p.N);
   float c[8], s[8];
   if (u.turned) {
-    const int pos = p.positions ? p.positions[token] : p.seqlens ? p.seqlens[b] - p.N + n : n;
+    int pos = n;
+    if (p.positions)
+      pos = p.positions[token];
+    else if (p.seqlens)     // (wraps as integers wrap, like the angle)
+      pos = static_cast<int>(static_cast<uint32_t>(p.seqlens[b]) - p.N + n);
     const int pair = kInterleaved ? u.first / 2 : u.first;
     const ulonglong2* const f = reinterpret_cast<const ulonglong2*>(p.freqs + pair);
 #pragma unroll

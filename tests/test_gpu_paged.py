@@ -346,7 +346,7 @@ def test_unseen_slots_may_hold_anything(code, d, H):
             for x in bits:
                 x[p, :, torch.from_numpy(rows).cuda()] = 0x7f if code == "e4m3" else 0x80
             if rows.all():
-                bad.k_scale[p], bad.v_scale[p] = float("nan"), float("inf")
+                bad.k_scale[p], bad.v_scale[p] = float("nan"), (float("inf"), 1e38, -1e30)[n % 3]
     free = [p for p in range(pages) if p not in set(table.flatten().tolist())]
     for x in bits:
         x[free] = 0x7f

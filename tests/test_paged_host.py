@@ -55,6 +55,12 @@ static int check_span(int Nq, int capacity, int count, int win, int sinks, int k
           any |= key <= pos && (key > pos - win || key < sinks);
         if (any != fa::paged_sees(k0 + i, 16, pos, win, sinks)) BAD("sees %d row %d", k0 + i, r);
       }
+    // and seen at all iff by some row
+    for (int i = 0; i < keys; i += 16) {
+      bool some = false;
+      for (int r = 0; r < Nq; ++r) some |= fa::paged_sees(k0 + i, 16, len - Nq + r, win, sinks);
+      if (some != fa::paged_seen(s, Nq, k0 + i, 16, win, sinks)) BAD("seen %d", k0 + i);
+    }
   }
   for (int r = 0; r < Nq; ++r) {
     const int pos = len - Nq + r;
