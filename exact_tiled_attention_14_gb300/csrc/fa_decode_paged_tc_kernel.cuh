@@ -84,21 +84,21 @@ struct DtLayout {
   static constexpr uint32_t p_col(int b) { return 256u + D + 64u * b; }
 };
 
-// Row and 16-byte piece of a lane in the turning of four (d = 128) or eight (64)
-// rows of codes: reads (swizzled by the copy) and both 16-byte writes of every
-// quarter warp touch all banks once.  At d = 128 a quarter takes every other
-// piece of two rows whose numbers differ in the two low bits, and pieces of the
-// second 64 columns write their halves in the other order.
+// Row in its eight and 16-byte piece of a lane in step k of turning codes, four
+// (d = 128) or eight (64) rows a step: reads (swizzled by the copy) and both
+// 16-byte writes of every quarter warp touch all banks once.  At d = 128 a
+// quarter takes four pieces of one 64-column chunk of two rows whose numbers
+// differ in bits 0 (the writes' other banks) and 2 (the reads').
 struct DtPiece {
   int row, piece;
 };
 template <int D>
-__host__ __device__ __forceinline__ DtPiece dt_piece(int lane) {
+__host__ __device__ __forceinline__ DtPiece dt_piece(int lane, int k) {
   DtPiece p;
   if (D == 128) {
-    const int q = lane >> 3, i = lane & 7, a = q & 1;
-    p.row = i & 4 ? a ^ 3 : a;
-    p.piece = 2 * (i & 3) + (q >> 1);
+    const int q = lane >> 3, i = lane & 7, a = 2 * (k & 1) + (q & 1);
+    p.row = i & 4 ? a ^ 5 : a;
+    p.piece = (i & 3) + 4 * (q >> 1);
   } else {
     p.row = lane >> 2;
     p.piece = lane & 3;
@@ -344,10 +344,15 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     constexpr int kStep = D == 128 ? 4 : 8, kSteps = kRowsOf / kStep;
     const bool is_v = warp >= kDtConvert + kDtTurners;
     const int first = (warp & (kDtTurners - 1)) * kRowsOf;
-    const DtPiece mine = dt_piece<D>(lane);
-    const int h = mine.piece >> 2;               // (0 at d = 64)
-    // rows r and r + 8 have the same place in their eight
-    auto at8 = [&](int i) { return first + (i * kStep & 7) + mine.row; };
+    // where the lane's piece of step k comes from and goes to, but for its eight
+    // rows, in which a row has the same place in each
+    uint32_t from[2], to[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const DtPiece x = dt_piece<D>(lane, k);
+      from[k] = dp_chunk<D>(first + x.row, x.piece);
+      to[k] = dt_place(first + x.row, x.piece, 0);
+    }
     uint8_t* const tiles = sgen + (is_v ? L::kV : L::kK);
     const int b_full = is_v ? L::bVFull : L::bKFull, b_empty = is_v ? L::bVEmpty : L::bKEmpty;
     const uint32_t site = is_v ? kSiteDtVEmpty : kSiteDtKEmpty;
@@ -408,8 +413,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         uint4 x[kSteps];
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
-          x[k] = *reinterpret_cast<const uint4*>(codes + dp_chunk<D>(at8(k), mine.piece) +
-                                                 (k * kStep & ~7) * D);
+          x[k] = *reinterpret_cast<const uint4*>(codes + from[k & 1] + (k * kStep & ~7) * D);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
         if (is_v) {
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           if (!full) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-              const int r = first + k * kStep + mine.row;
+              const int r = first + (k * kStep & ~7) + dt_piece<D>(lane, k).row;
               if (!(have >> (r >> 4) & 1u && key0 + r <= pos_hi &&
                     (key0 + r > pos_lo - p.win || key0 + r < p.sinks)))
                 x[k] = make_uint4(0, 0, 0, 0);
@@ -435,13 +439,13 @@ __global__ void __launch_bounds__(kDtThreads, 1)
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           uint4 y, z;
-          codes4<kInt8>(h ? x[k].z : x[k].x, y.x, y.y);
-          codes4<kInt8>(h ? x[k].w : x[k].y, y.z, y.w);
-          codes4<kInt8>(h ? x[k].x : x[k].z, z.x, z.y);
-          codes4<kInt8>(h ? x[k].y : x[k].w, z.z, z.w);
-          uint8_t* const to = tile + (k * kStep & ~7) * 128;
-          *reinterpret_cast<uint4*>(to + dt_place(at8(k), mine.piece, h)) = y;
-          *reinterpret_cast<uint4*>(to + dt_place(at8(k), mine.piece, h ^ 1)) = z;
+          codes4<kInt8>(x[k].x, y.x, y.y);
+          codes4<kInt8>(x[k].y, y.z, y.w);
+          codes4<kInt8>(x[k].z, z.x, z.y);
+          codes4<kInt8>(x[k].w, z.z, z.w);
+          uint8_t* const eight = tile + (k * kStep & ~7) * 128;
+          *reinterpret_cast<uint4*>(eight + to[k & 1]) = y;
+          *reinterpret_cast<uint4*>(eight + (to[k & 1] ^ 16u)) = z;
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -481,8 +485,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const bool has = quarter * 32 < rows;      // a warp without rows only keeps the order
       const int pos = s.len - p.Nq + (row0 + r) % p.Nq;
       const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
-      float m = -INFINITY, l = 0.f, vref = 0.f, inv_vref = 0.f, vref_most = 0.f, qmul = 0.f;
-      bool poison = false;                       // a page's scale of values is not finite
+      float m = 0.f, l = 0.f,                    // the reference, 0 before the first score
+            vref = 0.f, inv_vref = 0.f, vref_most = 0.f, qmul = 0.f;
+      bool fresh = true, poison = false;         // no reference yet; a page's scale of values is not finite
       for (int i = 0; i < n; ++i, ++j) {
         const int ms = j % kDtMetas, b = j & 1;
         const int key0 = paged_key0(s, at.tile + i, kDtKeys) + part * 32;   // of the thread's keys
@@ -492,17 +497,24 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         ptx::tc_fence_after();
         const uint32_t have = metas[ms].have >> (2 * part) & 3u;
         const float top = metas[ms].top;
-        float ks[2], vs[2];
+        const float ks[2] = {metas[ms].ks[2 * part], metas[ms].ks[2 * part + 1]};
+        float vs[2] = {metas[ms].vs[2 * part], metas[ms].vs[2 * part + 1]};
+        // every row sees every key of the thread's
+        const bool full = have == 3u && key0 + 31 <= pos_lo &&
+                          (key0 > pos_hi - p.win || key0 + 32 <= p.sinks);
+        if (!full) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ks[k] = metas[ms].ks[2 * part + k];
-          vs[k] = (have >> k & 1u) && paged_seen(s, p.Nq, key0 + 16 * k, 16, p.win, p.sinks)
-                      ? metas[ms].vs[2 * part + k]
-                      : 0.f;
-          if (!(fabsf(vs[k]) < INFINITY)) {
-            poison |= paged_sees(key0 + 16 * k, 16, pos, p.win, p.sinks);
-            vs[k] = 0.f;
-          }
+          for (int k = 0; k < 2; ++k)
+            if (!(have >> k & 1u) || !paged_seen(s, p.Nq, key0 + 16 * k, 16, p.win, p.sinks))
+              vs[k] = 0.f;
+        }
+        if (!(fabsf(vs[0]) < INFINITY && fabsf(vs[1]) < INFINITY)) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (!(fabsf(vs[k]) < INFINITY)) {
+              poison |= paged_sees(key0 + 16 * k, 16, pos, p.win, p.sinks);
+              vs[k] = 0.f;
+            }
         }
         if (i == 0) {                            // (a slot's parity turns with each unit on it)
           ptx::wait_bounded(bar(L::bQReady + ms), q_parity >> ms & 1, wd, kSiteDtQReady);
@@ -516,21 +528,26 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           uint32_t sr[32];
           ptx::tmem_ld32(lanes + L::s_col(b) + part * 32, sr);
           ptx::tmem_wait_ld();
+          // scores less the row's reference, in log2 units
           float x[32];
-          const uint64_t q2 = ptx::f2_pack(qmul, qmul);
+          const uint64_t n2 = ptx::f2_pack(-m, -m);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint64_t k2 = ptx::f2_pack(ks[k], ks[k]);
+            const float c = qmul * ks[k];
+            if (fabsf(c) < 0x1p100f && fabsf(c) > 0x1p-100f) {
+              const uint64_t c2 = ptx::f2_pack(c, c);
 #pragma unroll
-            for (int e = 16 * k; e < 16 * k + 16; e += 2)
-              ptx::f2_unpack(ptx::fmul2(ptx::fmul2(ptx::f2_pack(__uint_as_float(sr[e]),
-                                                                __uint_as_float(sr[e + 1])),
-                                                   q2),
-                                        k2),
-                             x[e], x[e + 1]);
+              for (int e = 16 * k; e < 16 * k + 16; e += 2)
+                ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(__uint_as_float(sr[e]),
+                                                       __uint_as_float(sr[e + 1])),
+                                          c2, n2),
+                               x[e], x[e + 1]);
+            } else {   // factors whose product may leave the range that the score stays in
+#pragma unroll
+              for (int e = 16 * k; e < 16 * k + 16; ++e)
+                x[e] = fmaf(__uint_as_float(sr[e]) * qmul, ks[k], -m);
+            }
           }
-          const bool full = have == 3u && key0 + 31 <= pos_lo &&
-                            (key0 > pos_hi - p.win || key0 + 32 <= p.sinks);
           if (!full) {
             const uint32_t vis = (ptx::bit_range(pos - p.win + 1 - key0, pos + 1 - key0) |
                                   ptx::bit_range(0, min(p.sinks, pos + 1) - key0)) &
@@ -546,15 +563,19 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             a1 = ptx::max3(a1, x[e + 2], x[e + 3]);
           }
           float mx = fmaxf(a0, a1);
-          // a row keeps its reference until a score passes it by the threshold;
-          // its threads meet only then
+          // a row keeps its reference until a score passes it by the threshold (or
+          // is its first); its threads meet only then
           float f = 1.f;
-          if (ptx::named_bar_any(1 + quarter, 128, mx > m + kDpTau)) {
+          auto passes = [&]() { return mx > kDpTau || (fresh && mx > -INFINITY); };
+          if (ptx::named_bar_any(1 + quarter, 128, passes())) {
             mx = row_all(mx, [](float u, float v) { return fmaxf(u, v); });
-            if (mx > m + kDpTau) {
-              if (m != -INFINITY) f = ptx::ex2(m - mx);
-              m = mx;
+            if (passes()) {
+              if (!fresh) f = ptx::ex2(-mx);
+              fresh = false;
+              m += mx;
               l *= f;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] -= mx;
             }
           }
           // the unit of O follows the tile's scales, alike in every thread
@@ -564,8 +585,6 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             vref = now;
             inv_vref = 1.f / now;
           }
-          const float m0 = m == -INFINITY ? 0.f : m;
-          const uint64_t nm2 = ptx::f2_pack(-m0, -m0);
           uint64_t acc = ptx::f2_pack(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll
@@ -574,9 +593,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             const uint64_t r2 = ptx::f2_pack(rv, rv);
 #pragma unroll
             for (int e = 16 * k; e < 16 * k + 16; e += 2) {
-              float y0, y1, p0, p1;
-              ptx::f2_unpack(ptx::fadd2(ptx::f2_pack(x[e], x[e + 1]), nm2), y0, y1);
-              const uint64_t pr = ptx::f2_pack(ptx::ex2(y0), ptx::ex2(y1));
+              float p0, p1;
+              const uint64_t pr = ptx::f2_pack(ptx::ex2(x[e]), ptx::ex2(x[e + 1]));
               acc = ptx::fadd2(acc, pr);
               ptx::f2_unpack(ptx::fmul2(pr, r2), p0, p1);
               pk[e / 2] = ptx::pack2<false>(p0, p1);
@@ -625,7 +643,6 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         auto sum = [](float u, float v) { return u + v; };
         const float lt = row_all(l, sum);
         poison = row_all(poison ? 1.f : 0.f, sum) != 0.f;
-        const float mt = m == -INFINITY ? 0.f : m;
         const float f = whole ? (lt != 0.f ? vref / lt : 0.f) : vref;
         const size_t row = head * p.R + row0 + r;
 #pragma unroll 1
@@ -660,9 +677,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         }
         if (part == 0 && r < rows) {
           if (whole)
-            p.lse[row] = lt != 0.f ? (ptx::lg2(lt) + mt) * 0.693147180559945309f : -INFINITY;
+            p.lse[row] = lt != 0.f ? (ptx::lg2(lt) + m) * 0.693147180559945309f : -INFINITY;
           else
-            p.part_ml[slot * p.slot_rows + r] = make_float2(mt, lt);
+            p.part_ml[slot * p.slot_rows + r] = make_float2(m, lt);
         }
       }
       if (at.tile == 0 && threadIdx.x == 0)

@@ -119,28 +119,28 @@ static int check_layout() {
 template <int D>
 static int check_pieces() {
   const int step = D == 128 ? 4 : 8;
-  for (int r0 = 0; r0 < 128; r0 += step) {
-    std::set<int> seen;
+  std::set<int> all;
+  for (int k = 0; k < 128 / step; ++k)
     for (int q = 0; q < 4; ++q) {
       std::set<unsigned> read, write[2];
       for (int lane = 8 * q; lane < 8 * q + 8; ++lane) {
-        const fa::DtPiece m = fa::dt_piece<D>(lane);
-        if (m.row < 0 || m.row >= step || m.piece < 0 || m.piece >= D / 16) BAD("piece of lane %d", lane);
-        const int r = r0 + m.row, h = m.piece >> 2;
-        seen.insert(m.row * 8 + m.piece);
+        const fa::DtPiece m = fa::dt_piece<D>(lane, k);
+        if (m.row < 0 || m.row > 7 || m.piece < 0 || m.piece >= D / 16) BAD("piece of lane %d", lane);
+        const int r = (k * step & ~7) + m.row;
+        all.insert(r * 8 + m.piece);
         read.insert(fa::dp_chunk<D>(r, m.piece) % 128 / 16);
-        for (int k = 0; k < 2; ++k) {
-          const unsigned at = fa::dt_place(r, m.piece, h ^ k);
-          write[k].insert(at % 128 / 16);
-          const int col = m.piece * 16 + (h ^ k) * 8;       // the 128-byte swizzle of a 64-column chunk
+        for (int h = 0; h < 2; ++h) {
+          const unsigned at = fa::dt_place(r, m.piece, h);
+          write[h].insert(at % 128 / 16);
+          if (at != (fa::dt_place(r, m.piece, 0) ^ (16u * h))) BAD("halves of row %d", r);
+          const int col = m.piece * 16 + h * 8;             // the 128-byte swizzle of a 64-column chunk
           const unsigned plain = (col / 64) * 16384u + r * 128u + col % 64 * 2;
           if (at != (plain ^ ((plain >> 7 & 7) << 4))) BAD("place of row %d column %d", r, col);
         }
       }
       if (read.size() != 8 || write[0].size() != 8 || write[1].size() != 8) BAD("banks of %d", D);
     }
-    if (static_cast<int>(seen.size()) != step * D / 16) BAD("pieces of %d", D);
-  }
+  if (static_cast<int>(all.size()) != 128 * D / 16) BAD("pieces of %d", D);
   return 0;
 }
 
