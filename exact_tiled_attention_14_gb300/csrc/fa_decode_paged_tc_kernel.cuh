@@ -16,14 +16,14 @@
 // and out 64 KB, half-precision tiles in and out 128 KB, queries 32 KB): the
 // last bounds a tile.
 //
-// One CTA (26 warps) per SM, persistent over its run of key tiles:
+// One CTA (27 warps) per SM, persistent over its run of key tiles:
 //   warps 0-15   softmax: warp w has rows 32 (w % 4) .. + 31, one a lane, and
 //                quarter w / 4 of a tile's keys; the four threads of a row agree
 //                on its reference;
 //   warps 16-19  K tiles to half precision, and the queries at a unit's start;
 //   warps 20-23  V tiles, rows that no row of the unit sees as zeros;
-//   warp 24      pages, scales and the TMA loads;
-//   warp 25      S = Q K^T of the next tile, then O += P V of this one.
+//   warps 24, 25 pages, scales and the TMA loads, of K and of V;
+//   warp 26      S = Q K^T of the next tile, then O += P V of this one.
 // A tile's softmax is one thread's chain, which takes longer than its issue
 // slots: 64 keys a thread took 1650 ns a tile, 32 take half.
 // S and P are double buffered in TMEM (at d = 128 it is full), O is not.  A unit
@@ -35,8 +35,8 @@
 
 namespace fa {
 
-constexpr int kDtKeys = 128, kDtRows = 128, kDtThreads = 832;
-constexpr int kDtConvert = 16, kDtLoad = 24, kDtMma = 25;   // first warp of a role
+constexpr int kDtKeys = 128, kDtRows = 128, kDtThreads = 864;
+constexpr int kDtConvert = 16, kDtLoad = 24, kDtMma = 26;   // first warp of a role
 constexpr int kDtTurners = 4;            // warps that turn K, and V
 constexpr int kDtMetas = 3;              // tiles whose scales are kept
 
@@ -130,6 +130,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
 
   // softmax warps: with one unit a head, those that have rows
   const int quarters = p.row_blocks > 1 ? 4 : (p.R + 31) / 32, active = 4 * quarters;
+  // The turners' numbers.  A warp's softmax rows are given by the part of the SM that
+  // it runs on (w % 4), so up to 64 rows keep two of the four parts busy: there the
+  // other two parts' softmax warps, which have no rows, turn the codes.
+  const int turner = quarters > 2 ? (warp < kDtLoad ? warp - kDtConvert : -1)
+                     : warp < kDtConvert && (warp & 2) ? (warp >> 2) * 2 + (warp & 1)
+                                                       : -1;
 
   ptx::griddep_launch_dependents();
   if (warp == kDtMma) {
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       ptx::mbar_init(bar(L::bCodesEmpty + i), kDtTurners);
     }
     for (int i = 0; i < kDtMetas; ++i) {
-      ptx::mbar_init(bar(L::bMetaFull + i), 1);
+      ptx::mbar_init(bar(L::bMetaFull + i), 2);
       ptx::mbar_init(bar(L::bMetaEmpty + i), active + kDtTurners);
       ptx::mbar_init(bar(L::bQReady + i), kDtTurners);
     }
@@ -179,101 +185,113 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     whole = at.tile == 0 && n == at.s.tiles;
   };
 
-  if (warp == kDtLoad) {
+  if (warp == kDtLoad || warp == kDtLoad + 1) {
     // ============================================================ pages, scales, loads
-    DpPlace nx = at;                             // the tile whose page is looked up
-    int nx_left = left;
-    // a lane's box of a tile: its page (-1: none), head and first row in the page
+    // Lane 8 a + i looks up box i of every fourth tile from tile a on: pages are
+    // asked for eight tiles and scales four tiles before they are needed, and no
+    // tile waits for them.
+    const bool is_v = warp != kDtLoad;
+    const CUtensorMap* const tm = is_v ? &p.tm_v : &p.tm_k;
+    const float* const scales = is_v ? p.v_scale : p.k_scale;
+    const int box = lane & 7, ahead = lane >> 3;
+    DpPlace nx = at;                             // the lane's next tile, and its number
+    int nx_j = 0;
+    auto skip = [&](int n) {
+      nx_j += n;
+      nx.tile += n;
+      while (nx_j < left && nx.tile >= nx.s.tiles) {
+        const int over = nx.tile - nx.s.tiles;
+        dp_next_unit(p, nx, kDtKeys);
+        nx.tile = over;
+      }
+    };
+    skip(ahead);
     struct Box {
-      int page = -1, hk = 0, row = 0;
+      int page = -1, hk = 0, row = 0;            // page (-1: none), head, first row in the page
       bool seen = false;                         // by some row
     };
     auto look = [&]() {
       Box x;
-      if (nx_left <= 0) return x;
-      if (lane < p.boxes) {
-        const int key = paged_key0(nx.s, nx.tile, kDtKeys) + lane * box_rows;
+      if (nx_j < left && box < p.boxes) {
+        const int key = paged_key0(nx.s, nx.tile, kDtKeys) + box * box_rows;
         const int nth = p.page_magic ? __umulhi(key >> 4, p.page_magic) : key >> 4;
         x.row = key - nth * p.page;
         x.hk = nx.hk;
         x.seen = paged_seen(nx.s, p.Nq, key, box_rows, p.win, p.sinks);
         if (key < nx.s.len) x.page = p.table[static_cast<size_t>(nx.b) * p.per_seq + nth];
       }
-      --nx_left;
-      if (++nx.tile == nx.s.tiles) dp_next_unit(p, nx, kDtKeys);
+      skip(4);
       return x;
     };
-    auto head_of = [&](const Box& x) {           // < 0: none
-      return x.page >= 0 && x.page < p.pages ? x.page * p.Hk + x.hk : -1;
+    struct Code {
+      int row;                                   // of the cache (-1: none)
+      float scale;
+      bool seen;
     };
-    bool alive = true;
-    int j = 0, issued = 0;                       // tiles, loads
-    auto load = [&](const CUtensorMap* tm, int head, int row, uint32_t bytes) {
-      const int slot = issued % L::kSlots;
-      if (issued >= L::kSlots)
-        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bCodesEmpty + slot),
-                                                         (issued / L::kSlots - 1) & 1, wd,
-                                                         kSiteDtCodesEmpty));
-      if (!alive) return;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::bCodesFull + slot), bytes);
-      __syncwarp();
-      if (head >= 0)
-        tma_load_rows(sbase + L::kRing + slot * L::kCodes + lane * box_rows * D, tm,
-                      bar(L::bCodesFull + slot), head * p.page + row);
-      ++issued;
-    };
-    // pages are asked for two tiles ahead, scales one
-    Box x0 = look(), x1 = look();
-    int head0 = head_of(x0);
-    float ks = 0.f, vs = 0.f;
-    if (head0 >= 0) {
-      ks = p.k_scale[head0];
-      vs = p.v_scale[head0];
-    }
-    for (; j < left && alive; ++j) {
-      const int ms = j % kDtMetas;
-      const uint32_t have = __ballot_sync(0xffffffffu, head0 >= 0);
-      const uint32_t bytes = __popc(have) * box_rows * D;
-      load(&p.tm_k, head0, x0.row, bytes);
-      load(&p.tm_v, head0, x0.row, bytes);
-      const int head1 = head_of(x1);
-      float ks1 = 0.f, vs1 = 0.f;
-      if (head1 >= 0) {
-        ks1 = p.k_scale[head1];
-        vs1 = p.v_scale[head1];
+    auto resolve = [&](const Box& x) {
+      Code c{-1, 0.f, x.seen};
+      if (x.page >= 0 && x.page < p.pages) {
+        const int head = x.page * p.Hk + x.hk;
+        c.row = head * p.page + x.row;
+        c.scale = scales[head];
       }
-      const Box x2 = look();
+      return c;
+    };
+    Box x0 = look(), x1 = look();
+    Code now = resolve(x0), next = resolve(x1);
+    x0 = look();
+    bool alive = true;
+    int issued = 0;
+    const int per = 8 / p.boxes;
+#pragma unroll 1
+    for (int j = 0; j < left && alive; ++j) {
+      const int ms = j % kDtMetas, use = 2 * j + is_v, slot = use % L::kSlots;
+      const bool mine = ahead == (j & 3) && now.row >= 0;
+      const uint32_t have = __ballot_sync(0xffffffffu, mine) >> (8 * (j & 3)) & 255u;
+      if (use >= L::kSlots)
+        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bCodesEmpty + slot),
+                                                         (use / L::kSlots - 1) & 1, wd,
+                                                         kSiteDtCodesEmpty));
+      if (!alive) break;
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(bar(L::bCodesFull + slot), __popc(have) * box_rows * D);
+      __syncwarp();
+      if (mine)
+        tma_load_rows(sbase + L::kRing + slot * L::kCodes + box * box_rows * D, tm,
+                      bar(L::bCodesFull + slot), now.row);
+      ++issued;
       if (j >= kDtMetas)
         alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaEmpty + ms),
                                                          (j / kDtMetas - 1) & 1, wd,
                                                          kSiteDtMetaEmpty));
-      if (lane < p.boxes) {
-        const int per = 8 / p.boxes;
-        for (int i = lane * per; i < (lane + 1) * per; ++i) {
-          metas[ms].ks[i] = ks;
-          metas[ms].vs[i] = vs;
-        }
+      if (ahead == (j & 3) && box < p.boxes) {
+        float* const to = is_v ? metas[ms].vs : metas[ms].ks;
+        for (int i = box * per; i < (box + 1) * per; ++i) to[i] = now.scale;
       }
-      // (a box's bit for each 16 keys of it)
-      uint32_t bits = 0;
-      for (int i = 0; i < 8; ++i) bits |= (have >> (i * p.boxes / 8) & 1u) << i;
-      const float size = head0 >= 0 && x0.seen && fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
-      if (lane == 0) {
-        metas[ms].have = bits;
-        metas[ms].top = __uint_as_float(top);
+      if (is_v) {
+        const float size = mine && now.seen && fabsf(now.scale) < INFINITY ? fabsf(now.scale) : 0.f;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+        // (a box's bit for each 16 keys of it)
+        const uint32_t bits =
+            __ballot_sync(0xffffffffu, lane < 8 && (have >> (lane * p.boxes / 8) & 1u));
+        if (lane == 0) {
+          metas[ms].have = bits;
+          metas[ms].top = __uint_as_float(top);
+        }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(L::bMetaFull + ms));
-      head0 = head1;
-      x0 = x1;
-      x1 = x2;
-      ks = ks1;
-      vs = vs1;
+      if ((j & 3) == 3) {
+        now = next;
+        next = resolve(x0);
+        x0 = look();
+      }
     }
     // the loads land before the block ends, whatever became of their readers
-    for (int i = max(issued - L::kSlots, 0); i < issued; ++i)
-      ptx::wait_drain(bar(L::bCodesFull + i % L::kSlots), i / L::kSlots & 1, 200000000ull);
+    for (int i = max(issued - L::kSlots / 2, 0); i < issued; ++i) {
+      const int use = 2 * i + is_v;
+      ptx::wait_drain(bar(L::bCodesFull + use % L::kSlots), use / L::kSlots & 1, 200000000ull);
+    }
     __syncwarp();
   } else if (warp == kDtMma) {
     // ============================================================ products
@@ -338,12 +356,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       ptx::wait_drain(bar(L::bFinal), 0, 200000000ull);
     }
     __syncwarp();
-  } else if (warp >= kDtConvert) {
+  } else if (turner >= 0) {
     // ============================================================ codes to half precision
     constexpr int kRowsOf = kDtKeys / kDtTurners;            // rows of a warp
     constexpr int kStep = D == 128 ? 4 : 8, kSteps = kRowsOf / kStep;
-    const bool is_v = warp >= kDtConvert + kDtTurners;
-    const int first = (warp & (kDtTurners - 1)) * kRowsOf;
+    const bool is_v = turner >= kDtTurners;
+    const int first = (turner & (kDtTurners - 1)) * kRowsOf;
     // where the lane's piece of step k comes from and goes to, but for its eight
     // rows, in which a row has the same place in each
     uint32_t from[2], to[2];
@@ -452,7 +470,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         if (lane == 0) ptx::mbar_arrive(bar(b_full + b));
       }
     }
-  } else if ((warp & 3) < quarters) {
+  } else if (warp < kDtConvert && (warp & 3) < quarters) {
     // ============================================================ softmax
     const int quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
