@@ -1,5 +1,5 @@
 // fa_decode_paged_tc_kernel.cuh — decoding over pages of 8-bit keys and values
-// (see fa_paged.cuh) for many rows: 9 to 128 query rows of a key/value head in
+// (see fa_paged.cuh) for many rows: 17 to 128 query rows of a key/value head in
 // one unit, on the tensor cores through TMEM.
 //
 // The function, the queries' powers of two, the placing of the scales and the
@@ -10,22 +10,27 @@
 // half-precision tiles in shared memory, and a product of 128 rows costs a
 // tile 544 cycles whatever their number.
 //
-// Bound (d = 128, a tile of 128 keys, 32 KB): its share of HBM 1394 cycles of
-// an SM, the products 1088, the softmax of 128 rows about 900 issue cycles, the
-// turning of the codes 320, and 1800 cycles of shared-memory traffic (codes in
-// and out 64 KB, half-precision tiles in and out 128 KB, queries 32 KB): the
-// last bounds a tile.
+// Cost (d = 128, a tile of 128 keys, 32 KB): its share of HBM 1394 cycles of
+// an SM, the products 1088, 1800 of shared-memory traffic (codes in and out 64
+// KB, half-precision tiles in and out 128 KB, queries 32 KB).  What bounds it is
+// none of them but a softmax thread's chain, 3150 cycles a tile at 64 rows: 450
+// to read the scores, 550 to their maximum, 290 to meet, 900 for the weights, 500
+// to store them, 460 around the loop.  8 caches to 32768, 4 K/V heads (169 MB, 25
+// us): 32 rows 65 us, 64 rows 67, 128 rows 75; at d = 64 64 rows take 65.
 //
 // One CTA (27 warps) per SM, persistent over its run of key tiles:
 //   warps 0-15   softmax: warp w has rows 32 (w % 4) .. + 31, one a lane, and
 //                quarter w / 4 of a tile's keys; the four threads of a row agree
 //                on its reference;
 //   warps 16-19  K tiles to half precision, and the queries at a unit's start;
-//   warps 20-23  V tiles, rows that no row of the unit sees as zeros;
+//   warps 20-23  V tiles, rows that no row of the unit sees as zeros
+//                (up to 64 rows softmax warps without rows do both: see `turner`);
 //   warps 24, 25 pages, scales and the TMA loads, of K and of V;
 //   warp 26      S = Q K^T of the next tile, then O += P V of this one.
-// A tile's softmax is one thread's chain, which takes longer than its issue
-// slots: 64 keys a thread took 1650 ns a tile, 32 take half.
+// 64 keys a softmax thread instead of 32 took twice as long.  A second copy of up
+// to 64 rows in the idle lanes, which takes every other tile, gained 1 us of 71 and
+// cost 128 rows 12 (the products' order, the copies' sum); weights formed before
+// the row's threads have met, done again where a score passes, cost 20.
 // S and P are double buffered in TMEM (at d = 128 it is full), O is not.  A unit
 // that lies in one run is finished there; parts of the others go to the
 // workspace for fa_decode_paged_combine_kernel.

@@ -53,7 +53,7 @@ __device__ __forceinline__ void codes4_float(uint32_t four, float* x) {
   ptx::unpack2<false>(lo, x[0], x[1]);
   ptx::unpack2<false>(hi, x[2], x[3]);
 }
-// Four values as codes, to nearest even; NaN becomes 0x7f (e4m3) or 0.
+// Four values as codes, to nearest even (NaN becomes a NaN code as e4m3, 0 as int8).
 template <bool kInt8>
 __device__ __forceinline__ uint32_t to_codes4(const float* x) {
   if constexpr (kInt8) {

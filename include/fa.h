@@ -764,8 +764,8 @@ int fa_rotary(const void *q, const void *k, void *q_out, void *k_out, int B, int
  * tokens of the sequence keeps its scale s0 where s <= s0; otherwise those
  * tokens' codes become round(code * (s0 * (1 / s))).  (For FA_E4M3 that shifts
  * exponents; it rounds only below 2^-6 s.)  A NaN or infinite element makes
- * the scale of its page and head NaN, and everything read of it NaN, until the
- * page is filled from its first slot again.
+ * the scale of its page and head NaN (with new codes of 0), and everything read
+ * of it NaN, until the page is filled from its first slot again.
  *
  *   k, v      : T tokens of Hk heads of B sequences, dtype `dtype`, rows of d
  *               contiguous elements, 16-byte aligned.  Tokens from counts[b]
@@ -830,7 +830,9 @@ int fa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale
  * A token that sees no key gets O = 0 and LSE = -inf; keys in a page whose
  * number is outside 0 .. pages - 1 are not seen.  Slots that no token of a
  * sequence sees may hold anything; a page's scale that is not finite reaches
- * the tokens that see one of its slots.  Results do not depend on the order
+ * the tokens that see one of its slots, and only them.  (An e4m3 code that is NaN,
+ * which fa_cache_append never writes, reaches every token of the sequence if one
+ * sees it.)  Results do not depend on the order
  * CTAs run in.
  * Errors as fa_cache_append and fa_decode_window.  With R = H / Hk * Nq rows a
  * key/value head, FA_ERR_SHAPE also for B * H * Nq over 2^30, and for

@@ -389,6 +389,28 @@ def test_a_scale_that_is_not_finite_reaches_only_who_sees_it(page, H):
         assert torch.isnan(got["o"][:, :, 2]).all()
 
 
+@pytest.mark.parametrize("T", [1, 3, 12])
+@pytest.mark.parametrize("H", [1, 2, 10])     # 4 to 150 rows
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_a_spoilt_token_reaches_only_who_sees_its_page(code, H, T):
+    """The last append begins a page with a token that is not finite: the tokens
+    before that page keep their results, the others get NaN."""
+    d, page, Nq, lens = 128, 16, T + 3, 32 + T    # the append's first token begins a page
+    q = pc.normal((1, H, Nq, d), "bf16", 31).cuda()
+    table, results = ints([[3, 0, 2]]), []
+    for spoilt in (0.0, float("nan"), float("inf")):
+        cache = fa.make_paged_cache(4, 1, page, d, pc.CODE_DT[code])
+        k, v = pc.normal((1, 1, lens, d), "bf16", 32).cuda(), pc.normal((1, 1, lens, d), "bf16", 33).cuda()
+        fa.cache_append(k[:, :, :-T], v[:, :, :-T], cache, table, ints([lens - T]))
+        v[0, 0, -T, 5] += spoilt
+        fa.cache_append(k[:, :, -T:], v[:, :, -T:], cache, table, ints([lens]))
+        results.append(run_decode(q, cache, table, [lens]))
+    for bad in results[1:]:
+        assert torch.equal(bad["o"][:, :, :3], results[0]["o"][:, :, :3])
+        assert torch.equal(bad["lse"], results[0]["lse"])
+        assert torch.isnan(bad["o"][:, :, 3:]).all()
+
+
 @pytest.mark.parametrize("heads", [1, 4, 12])   # 4, 16 and 48 rows
 def test_nonfinite_scores(heads):
     """A NaN or +inf score gives NaN, one of -inf weighs nothing."""
