@@ -6,8 +6,10 @@ This module only marshals arguments to the C ABI in ``include/fa.h``
 ``_dropout`` forms; the backward ``fa_bwd``, ``fa_bwd_kv``, ``fa_bwd_varlen``,
 their ``_dropout`` forms, ``fa_bwd_onepass`` and ``fa_bwd_onepass_dropout``;
 ``fa_decode``; the sliding-window ``fa_fwd_window``, ``fa_bwd_window`` and
-``fa_decode_window`` and the drafted-tree ``fa_decode_tree``; the workspace
-sizes, status and settings), under the same names.  Every step of
+``fa_decode_window`` and the drafted-tree ``fa_decode_tree``; the rotation by
+positions ``fa_rotary`` and the paged 8-bit cache's ``fa_cache_append``,
+``fa_cache_read`` and ``fa_decode_paged``; the workspace sizes, status and
+settings), under the same names.  Every step of
 the attention computation runs in the CUDA kernels of ``_build/libfa.so``;
 there is no CPU or PyTorch fallback.  When the library has not been built,
 every call raises.
@@ -21,10 +23,12 @@ current CUDA stream.  ``attention_backward`` does the same for ``fa_bwd``
 ``fa_fwd_varlen``, ``attention_backward_onepass`` for ``fa_bwd_onepass``
 (and ``fa_bwd_onepass_dropout``), ``attention_forward_window`` for
 ``fa_fwd_window``, ``attention_backward_window`` for ``fa_bwd_window``,
-``attention_decode_window`` for ``fa_decode_window`` and
-``attention_decode_tree`` for ``fa_decode_tree``.  ``flash_attention``,
-``flash_attention_kv``, ``flash_attention_varlen`` and
-``flash_attention_window`` wrap the forward and backward entry points in
+``attention_decode_window`` for ``fa_decode_window``,
+``attention_decode_tree`` for ``fa_decode_tree``, ``rotary_forward`` and
+``rotary_backward`` for ``fa_rotary``, ``cache_append``, ``cache_read`` and
+``attention_decode_paged`` for the paged cache's calls.  ``flash_attention``,
+``flash_attention_kv``, ``flash_attention_varlen``, ``flash_attention_window``
+and ``rotary_embedding`` wrap the forward and backward entry points in
 torch.autograd functions.
 """
 import collections
@@ -1476,7 +1480,7 @@ def cache_append(k, v, cache, page_table, seqlens, counts=None, freqs=None, posi
     largest new element and only grows while it fills; when it does, the codes
     that the page holds are quantised again (see ``fa_cache_append`` in
     include/fa.h for the exact rules, NaN and infinities among them).  Pages
-    that the call writes must belong to one sequence each.
+    that the call writes must have one place in the table each.
     """
     what = "cache_append"
     dtype = k.dtype

@@ -24,7 +24,7 @@
 //    the blocks wait at a barrier for each head; one barrier for all four heads
 //    (41 us) and equal runs of heads for persistent blocks (39) were slower.
 // Read.  16 elements a thread and step, stored as 32 bytes at once so that every
-// sector is written whole: four caches of 2048 to 16384 tokens 57 us (71 as two
+// sector is written whole (where the outputs begin at one): four caches of 2048 to 16384 tokens 57 us (71 as two
 // halves), 6.1 TB/s with two thirds of it writes.
 #include <cuda_runtime.h>
 
@@ -309,13 +309,14 @@ struct ReadParams {
   int Hk, N, page, per_seq, pages;
   int per_row;
   long long units;            // of one head of one sequence: N * d / 16
+  bool sectors;               // both outputs begin at a multiple of 32 bytes
 };
 
 // A thread takes kReadUnits units of 16 elements, a block's width apart, of
 // one head of one sequence.
 constexpr int kReadThreads = 256, kReadUnits = 4;
 
-// 32 bytes in one store: whole sectors.
+// 32 bytes, at a multiple of 32, in one store: whole sectors.
 __device__ __forceinline__ void store32(void* at, const uint4 a, const uint4 b) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a.x),
                "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
@@ -363,7 +364,13 @@ __global__ void __launch_bounds__(kReadThreads)
       for (int j = 0; j < 4; ++j) codes4_float<kInt8>(w[j], x + 4 * j);
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] *= scale[i];
-      store32(out + unit * 16, pack8<kBf16>(x), pack8<kBf16>(x + 8));
+      const uint4 lo = pack8<kBf16>(x), hi = pack8<kBf16>(x + 8);
+      if (p.sectors) {
+        store32(out + unit * 16, lo, hi);
+      } else {
+        *reinterpret_cast<uint4*>(out + unit * 16) = lo;
+        *reinterpret_cast<uint4*>(out + unit * 16 + 8) = hi;
+      }
     }
   }
 }
@@ -517,6 +524,7 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale
   p.pages = pages;
   p.per_row = d == 128 ? 3 : 2;
   p.units = static_cast<long long>(N) << p.per_row;
+  p.sectors = !misaligned(k, 32) && !misaligned(v, 32);
   constexpr int kPer = fa::kReadThreads * fa::kReadUnits;
   const dim3 grid(static_cast<unsigned>((p.units + kPer - 1) / kPer),
                   static_cast<unsigned>(std::min(Hk, 65535)), static_cast<unsigned>(2 * B));

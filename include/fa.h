@@ -776,7 +776,7 @@ int fa_rotary(const void *q, const void *k, void *q_out, void *k_out, int B, int
  *   seqlens   : B int32; counts: NULL or B int32 (clamped to 0 .. T).  Tokens
  *               whose slot is negative, past the sequence's pages, or in a page
  *               whose number is outside 0 .. pages - 1 are not written.
- *   A page that a call writes belongs to one sequence of the call.  Slots from
+ *   A page that a call writes has one place in the table, of one sequence.  Slots from
  *   seqlens[b] on, and pages without new tokens, stay as they are.
  *   d, freqs, rot, mscale, interleaved : as fa_rotary.
  * Errors: FA_ERR_SHAPE (negative sizes; no pages; page_size; B * Hk, B * T,

@@ -259,6 +259,23 @@ def test_read(B, Hk, page, per, d, code, dtype, lens, length):
 
 # ---------------------------------------------------------------- decoding
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_into_any_aligned_buffer(d):
+    """Outputs that begin at a multiple of 16 bytes, of 32 or not."""
+    cache = pc.random_cache(5, 2, 48, d, "e4m3", seed=3)
+    table, lens = ints([[4, 1], [0, 2]]), ints([70, 33])
+    want = fa.cache_read(cache, table, lens, length=77)
+    n = want[0].numel()
+    for offsets in ((0, 8), (8, 16), (24, 8)):
+        whole = [torch.full((n + 32,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        out = [x[o:o + n].view(2, 2, 77, d) for x, o in zip(whole, offsets)]
+        fa.cache_read(cache, table, lens, length=77, out=out)
+        status_ok()
+        for x, y, z, o in zip(out, want, whole, offsets):
+            assert torch.equal(x, y)
+            assert (z[:o] == 7).all() and (z[o + n:] == 7).all()
+
+
 DECODE = [
     # B, H, Hk, Nq, page, per, d, code, dtype, window, sinks, lens
     (1, 1, 1, 1, 16, 1, 64, "e4m3", "bf16", None, 0, [1]),
