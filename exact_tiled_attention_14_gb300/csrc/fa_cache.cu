@@ -316,13 +316,6 @@ struct ReadParams {
 // one head of one sequence.
 constexpr int kReadThreads = 256, kReadUnits = 4;
 
-// 32 bytes, at a multiple of 32, in one store: whole sectors.
-__device__ __forceinline__ void store32(void* at, const uint4 a, const uint4 b) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a.x),
-               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-
 template <bool kBf16, bool kInt8>
 __global__ void __launch_bounds__(kReadThreads)
     fa_cache_read_kernel(const __grid_constant__ ReadParams p) {
@@ -366,7 +359,7 @@ __global__ void __launch_bounds__(kReadThreads)
       for (int j = 0; j < 16; ++j) x[j] *= scale[i];
       const uint4 lo = pack8<kBf16>(x), hi = pack8<kBf16>(x + 8);
       if (p.sectors) {
-        store32(out + unit * 16, lo, hi);
+        ptx::store32(out + unit * 16, lo, hi);
       } else {
         *reinterpret_cast<uint4*>(out + unit * 16) = lo;
         *reinterpret_cast<uint4*>(out + unit * 16 + 8) = hi;

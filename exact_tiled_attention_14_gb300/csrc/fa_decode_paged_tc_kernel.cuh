@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     ptx::tmem_alloc(ptx::smem_u32(tmem_ptr), 512);
     ptx::tmem_relinquish();
   }
-  if (threadIdx.x == kDtLoad * 32) {
+  if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < L::kSlots; ++i) {
       ptx::mbar_init(bar(L::bCodesFull + i), 1);
@@ -173,17 +173,17 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     ptx::prefetch_tmap(&p.tm_k);
     ptx::prefetch_tmap(&p.tm_v);
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = ptx::warp_same(*tmem_ptr);
-
   // ---- the CTA's run and its first place (each warp for itself)
   const DpRun rn = dp_run(p, kDtKeys, p.runs, 1, blockIdx.x);
   const DecDeal deal = rn.deal;
   const int run = blockIdx.x;
   DpPlace at = rn.at;
   int left = rn.left;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ptx::warp_same(*tmem_ptr);
+
   const int box_rows = kDtKeys / p.boxes;
   auto piece_of = [&](int& n, bool& whole) {     // of the place `at`
     n = min(at.s.tiles - at.tile, left);
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   } else if (turner >= 0) {
     // ============================================================ codes to half precision
     constexpr int kRowsOf = kDtKeys / kDtTurners;            // rows of a warp
+    constexpr int kBatch = 8;                                // query rows at a time
     constexpr int kStep = D == 128 ? 4 : 8, kSteps = kRowsOf / kStep;
     const bool is_v = turner >= kDtTurners;
     const int first = (turner & (kDtTurners - 1)) * kRowsOf;
@@ -389,28 +390,33 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const PagedSpan s = at.s;
       const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
       if (!is_v) {
-        // queries, once the previous unit's last S has read them and the slot of
-        // their powers of two is free with the first tile's meta
-        if (j > 0)
-          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bKEmpty + ((j - 1) & 1)),
-                                                           (j - 1) >> 1 & 1, wd, kSiteDtKEmpty));
-        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaFull + j % kDtMetas),
-                                                         j / kDtMetas & 1, wd, kSiteDtMetaFull));
-        signed char* const shifts = shift_s + j % kDtMetas * kDtRows;
+        // Queries, asked for before the previous unit's last S has read its own; rows
+        // that no softmax warp takes may hold anything.
         const size_t head = static_cast<size_t>(at.b) * p.Hk + at.hk;
         const int row0 = at.block * kDtRows, rows = min(p.R - row0, kDtRows);
+        signed char* const shifts = shift_s + j % kDtMetas * kDtRows;
+        const int of = 8 * quarters;             // the warp's rows
 #pragma unroll 1
-        for (int r0 = first; r0 < first + kRowsOf; r0 += 8) {
-          uint2 raw[8];
+        for (int r0 = turner * of; r0 < (turner + 1) * of; r0 += kBatch) {
+          uint2 raw[kBatch];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kBatch; ++i) {
             raw[i] = make_uint2(0, 0);
             if (r0 + i < rows && lane * 4 < D)
               raw[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
                                                        (head * p.R + row0 + r0 + i) * D + lane * 4);
           }
+          if (r0 == turner * of && j > 0) {
+            alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bKEmpty + ((j - 1) & 1)),
+                                                             (j - 1) >> 1 & 1, wd, kSiteDtKEmpty));
+            // (the powers' slot is free with the first tile's meta)
+            if (j >= kDtMetas)
+              alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaFull + j % kDtMetas),
+                                                               j / kDtMetas & 1, wd,
+                                                               kSiteDtMetaFull));
+          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kBatch; ++i) {
             float x[4];
             const int shift = dp_query_row<kBf16>(raw[i], x);
             if (lane * 4 < D)
@@ -427,8 +433,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const int ms = j % kDtMetas, b = j & 1;
         const int slot = 2 * j % L::kSlots + is_v;
         const int key0 = paged_key0(s, at.tile + i, kDtKeys);
-        alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaFull + ms), j / kDtMetas & 1,
-                                                         wd, kSiteDtMetaFull));
+        if (is_v)
+          alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaFull + ms), j / kDtMetas & 1,
+                                                           wd, kSiteDtMetaFull));
         alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bCodesFull + slot),
                                                          2 * j / L::kSlots & 1, wd,
                                                          kSiteDtCodesFull));
@@ -663,9 +670,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const int unit = static_cast<int>(head) * p.row_blocks + at.block;
       const size_t slot = 2 * static_cast<size_t>(run) + (pieces == 0 ? 0 : 1);
       if (has) {
-        auto sum = [](float u, float v) { return u + v; };
-        const float lt = row_all(l, sum);
-        poison = row_all(poison ? 1.f : 0.f, sum) != 0.f;
+        // (l is not negative: its sign carries the poison)
+        float lt = row_all(copysignf(l, poison ? -1.f : 1.f), [](float u, float v) {
+          return copysignf(fabsf(u) + fabsf(v), signbit(u) || signbit(v) ? -1.f : 1.f);
+        });
+        poison = signbit(lt);
+        lt = fabsf(lt);
         const float f = whole ? (lt != 0.f ? vref / lt : 0.f) : vref;
         const size_t row = head * p.R + row0 + r;
 #pragma unroll 1
@@ -693,8 +703,13 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             } else {
               float4* const out = p.part_o + (slot * p.slot_rows + r) * (D / 4) + c / 4;
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                out[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+              for (int v = 0; v < 2; ++v) {
+                auto bits = [&](int e) {
+                  return make_uint4(__float_as_uint(x[e]), __float_as_uint(x[e + 1]),
+                                    __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3]));
+                };
+                ptx::store32(out + 2 * v, bits(8 * v), bits(8 * v + 4));
+              }
             }
           }
         }

@@ -291,6 +291,12 @@ __host__ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 
 // registers -> 32 consecutive 32-bit TMEM columns of this thread's lane.
 // 32 lanes x 16 columns of 32 bits from 16 registers per thread (this warp's lanes).
+// 32 bytes, at a multiple of 32, in one store: whole sectors.
+__device__ __forceinline__ void store32(void* at, const uint4 a, const uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
