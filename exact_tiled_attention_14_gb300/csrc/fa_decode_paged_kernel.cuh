@@ -339,6 +339,23 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
   DpPlace at = rn.at;
   int left = rn.left;                        // tiles not begun
 
+  // ---- queries of row tile nt of the unit at `at`, four elements of each row a lane;
+  // with one row tile the first unit's are asked for before the loads, behind which
+  // they wait (5000 cycles of 33000 where every warp has five tiles)
+  uint2 raw[8];
+  auto ask = [&](int nt) {
+    const int row0 = at.block * L::kRows + nt * 8, rows = min(p.R - row0, 8);
+    const size_t first = (static_cast<size_t>(at.b) * p.Hk + at.hk) * p.R + row0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      raw[i] = make_uint2(0, 0);
+      if (i < rows && lane * 4 < D)
+        raw[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
+                                                 (first + i) * D + lane * 4);
+    }
+  };
+  if (kTiles == 1) ask(0);
+
   // ---- the warp's loads
   const int box_rows = kKeys / p.boxes;
   DpPlace nx = at;                           // the next tile to load
@@ -395,18 +412,11 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
     const PagedSpan s = at.s;
     left -= n;
 
-    // queries of the unit: row r, elements 4 c .. 4 c + 3 as the B operand's
+    // the queries: row r, elements 4 c .. 4 c + 3 as the B operand's
     // registers of lane (r % 8, 4 c / (D / 4)), in half precision
 #pragma unroll 1
     for (int nt = 0; nt < kTiles; ++nt) {
-      uint2 raw[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        raw[i] = make_uint2(0, 0);
-        if (nt * 8 + i < rows && lane * 4 < D)
-          raw[i] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) +
-                                                   (head * p.R + row0 + nt * 8 + i) * D + lane * 4);
-      }
+      if (kTiles > 1 || pieces > 0) ask(nt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float x[4];
