@@ -95,9 +95,9 @@ struct Plan {
   size_t o_bytes, ml_bytes, bytes;
 };
 // Up to 16 rows the warps' own products win (16 rows of 8 caches to 32k, 4 heads,
-// d = 128: 54 us, 64 with the kernel for many rows; d = 64 37 and 62), from 17 on
-// the other (32 rows 65 us, 76 in blocks of 16 rows; 64 rows 67 and 106; 128 rows
-// 75 and 194).
+// d = 128: 54 us, 60 with the kernel for many rows; d = 64 43 and 57), from 17 on
+// the other (32 rows 60 us, 76 in blocks of 16 rows; 64 rows 62 and 106; 128 rows
+// 72 and 194).
 int row_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : kManyTiles; }
 int tile_keys(int tiles, int d) { return tiles == kManyTiles ? kDtKeys : dp_keys(d); }
 // Tiles of all units at most: whole capacities, and one of each sequence's own.

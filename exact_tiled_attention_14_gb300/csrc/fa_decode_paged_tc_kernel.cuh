@@ -13,10 +13,12 @@
 // Cost (d = 128, a tile of 128 keys, 32 KB): its share of HBM 1394 cycles of
 // an SM, the products 1088, 1800 of shared-memory traffic (codes in and out 64
 // KB, half-precision tiles in and out 128 KB, queries 32 KB).  What bounds it is
-// none of them but a softmax thread's chain, 3150 cycles a tile at 64 rows: 450
-// to read the scores, 550 to their maximum, 290 to meet, 900 for the weights, 500
-// to store them, 460 around the loop.  8 caches to 32768, 4 K/V heads (169 MB, 25
-// us): 32 rows 65 us, 64 rows 67, 128 rows 75; at d = 64 64 rows take 65.
+// none of them but a softmax thread's chain, 2520 cycles a tile at 64 rows and
+// 2820 at 128 (of 20 parts about 3 to read the scores, 3 to their maximum, 2 to
+// meet, 6 for the weights, 3 to store them, 3 around the loop), and at the ends of a
+// run 12000 cycles to the first scores and 4000 to leave a part.  8 caches to
+// 32768, 4 K/V heads (169 MB, 25 us): 32 rows 60 us, 64 rows 62, 128 rows 72; at
+// d = 64 64 rows take 59.
 //
 // One CTA (27 warps) per SM, persistent over its run of key tiles:
 //   warps 0-15   softmax: warp w has rows 32 (w % 4) .. + 31, one a lane, and
@@ -30,7 +32,7 @@
 // 64 keys a softmax thread instead of 32 took twice as long.  A second copy of up
 // to 64 rows in the idle lanes, which takes every other tile, gained 1 us of 71 and
 // cost 128 rows 12 (the products' order, the copies' sum); weights formed before
-// the row's threads have met, done again where a score passes, cost 20.
+// the row's threads have met, done again where a score passes, cost 20 of 68.
 // S and P are double buffered in TMEM (at d = 128 it is full), O is not.  A unit
 // that lies in one run is finished there; parts of the others go to the
 // workspace for fa_decode_paged_combine_kernel.
