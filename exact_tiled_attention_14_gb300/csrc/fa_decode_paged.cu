@@ -96,7 +96,7 @@ struct Plan {
 };
 // Up to 16 rows the warps' own products win (16 rows of 8 caches to 32k, 4 heads,
 // d = 128: 54 us, 60 with the kernel for many rows; d = 64 43 and 57), from 17 on
-// the other (32 rows 60 us, 76 in blocks of 16 rows; 64 rows 62 and 106; 128 rows
+// the other (32 rows 61 us, 76 in blocks of 16 rows; 64 rows 63 and 106; 128 rows
 // 72 and 194).
 int row_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : kManyTiles; }
 int tile_keys(int tiles, int d) { return tiles == kManyTiles ? kDtKeys : dp_keys(d); }

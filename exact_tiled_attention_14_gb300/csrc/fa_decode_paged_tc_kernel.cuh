@@ -17,7 +17,7 @@
 // 2820 at 128 (of 20 parts about 3 to read the scores, 3 to their maximum, 2 to
 // meet, 6 for the weights, 3 to store them, 3 around the loop), and at the ends of a
 // run 12000 cycles to the first scores and 4000 to leave a part.  8 caches to
-// 32768, 4 K/V heads (169 MB, 25 us): 32 rows 60 us, 64 rows 62, 128 rows 72; at
+// 32768, 4 K/V heads (169 MB, 25 us): 32 rows 61 us, 64 rows 63, 128 rows 72; at
 // d = 64 64 rows take 59.
 //
 // One CTA (27 warps) per SM, persistent over its run of key tiles:
@@ -83,7 +83,7 @@ struct DtLayout {
                        bSFull = bVEmpty + 2, bPFull = bSFull + 2, bPvDone = bPFull + 2,
                        bQReady = bPvDone + 2, bOFree = bQReady + kDtMetas,
                        bFinal = bOFree + 1, kNumBars = bFinal + 1;
-  static constexpr int kMisc = kBar + 8 * kNumBars;           // TMEM base, abort flag
+  static constexpr int kMisc = kBar + 8 * kNumBars;           // TMEM base, abort flag, a word for stores
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kBar % 8 == 0 && kAlloc <= 232448, "shared memory budget");
   static constexpr uint32_t s_col(int b) { return 128u * b; }
@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(sgen + L::kMisc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sgen + L::kMisc + 4);
   DtMeta* const metas = reinterpret_cast<DtMeta*>(sgen + L::kMeta);
-  signed char* const shift_s = reinterpret_cast<signed char*>(sgen + L::kShift);
+  // (volatile: read before the slot is given back, not where the values are used)
+  auto meta_of = [&](int ms) { return static_cast<const volatile DtMeta*>(metas + ms); };
+  volatile signed char* const shift_s = reinterpret_cast<volatile signed char*>(sgen + L::kShift);
   const ptx::Watchdog wd{p.watchdog_cycles, abort_flag, p.status};
 
   // softmax warps: with one unit a head, those that have rows
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         // that no softmax warp takes may hold anything.
         const size_t head = static_cast<size_t>(at.b) * p.Hk + at.hk;
         const int row0 = at.block * kDtRows, rows = min(p.R - row0, kDtRows);
-        signed char* const shifts = shift_s + j % kDtMetas * kDtRows;
+        volatile signed char* const shifts = shift_s + j % kDtMetas * kDtRows;
         const int of = 8 * quarters;             // the warp's rows
 #pragma unroll 1
         for (int r0 = turner * of; r0 < (turner + 1) * of; r0 += kBatch) {
@@ -446,10 +448,20 @@ __global__ void __launch_bounds__(kDtThreads, 1)
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
           x[k] = *reinterpret_cast<const uint4*>(codes + from[k & 1] + (k * kStep & ~7) * D);
+        // The next copy may write the slot once this arrives, and nothing orders a copy
+        // behind loads whose results are not used yet: a store that needs all of them
+        // goes first (its word is never read).  Without it up to a third of the runs over
+        // short units had a tile with the next but one's codes; it costs 1 us of 63.
+        uint32_t all = 0;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) all |= x[k].x | x[k].y | x[k].z | x[k].w;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
+        if (lane == 0) {
+          ptx::st_shared(sbase + L::kMisc + 8, all);
+          ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
+        }
         if (is_v) {
-          const uint32_t have = metas[ms].have;
+          const uint32_t have = meta_of(ms)->have;
           const bool full = have == 255u && key0 + kDtKeys - 1 <= pos_hi &&
                             (key0 > pos_lo - p.win || key0 + kDtKeys <= p.sinks);
           __syncwarp();
@@ -527,10 +539,11 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         ptx::wait_bounded(bar(L::bSFull + b), j >> 1 & 1, wd, kSiteDtSFull);
         __syncwarp();
         ptx::tc_fence_after();
-        const uint32_t have = metas[ms].have >> (2 * part) & 3u;
-        const float top = metas[ms].top;
-        const float ks[2] = {metas[ms].ks[2 * part], metas[ms].ks[2 * part + 1]};
-        float vs[2] = {metas[ms].vs[2 * part], metas[ms].vs[2 * part + 1]};
+        const volatile DtMeta* const meta = meta_of(ms);
+        const uint32_t have = meta->have >> (2 * part) & 3u;
+        const float top = meta->top;
+        const float ks[2] = {meta->ks[2 * part], meta->ks[2 * part + 1]};
+        float vs[2] = {meta->vs[2 * part], meta->vs[2 * part + 1]};
         // every row sees every key of the thread's
         const bool full = have == 3u && key0 + 31 <= pos_lo &&
                           (key0 > pos_hi - p.win || key0 + 32 <= p.sinks);

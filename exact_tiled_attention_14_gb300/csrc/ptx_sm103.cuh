@@ -291,6 +291,9 @@ __host__ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 
 // registers -> 32 consecutive 32-bit TMEM columns of this thread's lane.
 // 32 lanes x 16 columns of 32 bits from 16 registers per thread (this warp's lanes).
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
 // 32 bytes, at a multiple of 32, in one store: whole sectors.
 __device__ __forceinline__ void store32(void* at, const uint4 a, const uint4 b) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a.x),

@@ -428,6 +428,27 @@ def test_a_spoilt_token_reaches_only_who_sees_its_page(code, H, T):
         assert torch.isnan(bad["o"][:, :, 3:]).all()
 
 
+@pytest.mark.parametrize("G,Nq,page,d,code", [(25, 4, 16, 128, "int8"), (25, 4, 64, 128, "e4m3"),
+                                              (14, 4, 16, 128, "int8"), (25, 4, 16, 64, "e4m3"),
+                                              (1, 4, 16, 128, "int8"), (4, 4, 64, 64, "e4m3")])
+def test_many_runs_of_short_units(G, Nq, page, d, code):
+    """Units of one to seven tiles, several to a run: every run gives the same bits."""
+    B, Hk, per = 60, 4, 912 // page
+    cache = pc.random_cache(B * per + 1, Hk, page, d, code, seed=2)
+    table = deal(B, per, B * per + 1, seed=3)
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, per * page + 1, (B,), generator=g, dtype=torch.int32).cuda()
+    q = pc.normal((B, Hk * G, Nq, d), "fp16", 5).cuda()
+    ws = fa.make_paged_workspace(q, cache, table)
+    want = fa.attention_decode_paged(q, cache, table, lens, workspace=ws)
+    differ = torch.zeros(400, dtype=torch.bool, device="cuda")
+    for i in range(400):
+        o, lse = fa.attention_decode_paged(q, cache, table, lens, workspace=ws)
+        differ[i] = (o != want[0]).any() | (lse != want[1]).any()
+    status_ok()
+    assert not differ.any()
+
+
 @pytest.mark.parametrize("heads", [1, 4, 12])   # 4, 16 and 48 rows
 def test_nonfinite_scores(heads):
     """A NaN or +inf score gives NaN, one of -inf weighs nothing."""
