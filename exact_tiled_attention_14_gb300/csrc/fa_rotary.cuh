@@ -14,7 +14,7 @@
 // radians.  The fraction is cut to the nearest quarter turn; the rest, at most
 // an eighth, goes in 32 bits (to 2^-34 turns) through the Taylor polynomials of
 // sine and cosine, of which the first terms left out are 2e-9 and 2.5e-8 there
-// (about 30 instructions a pair; sincospif with its own reduction took 70).
+// (about 30 operations a pair).
 #pragma once
 
 #include <cstdint>
