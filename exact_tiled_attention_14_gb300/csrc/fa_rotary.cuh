@@ -10,8 +10,8 @@
 // Angles.  w_j arrives as turns per position in units of 2^-64, so the
 // product with the position, wrapped at 64 bits as integers wrap, is the
 // angle's fraction of a turn with an error of p * 2^-65 turns whatever its
-// whole turns: 2^-44 at position 2^20, where a float32 angle is off by whole
-// radians.  The fraction is cut to the nearest quarter turn; the rest, at most
+// whole turns: 2^-45 at position 2^20, where a float32 angle is off by up to a
+// tenth of a radian.  The fraction is cut to the nearest quarter turn; the rest, at most
 // an eighth, goes in 32 bits (to 2^-34 turns) through the Taylor polynomials of
 // sine and cosine, of which the first terms left out are 2e-9 and 2.5e-8 there
 // (about 30 operations a pair).
