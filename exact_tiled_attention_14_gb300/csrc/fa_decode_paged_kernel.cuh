@@ -10,11 +10,15 @@
 // multiplied by a power of two that brings its largest element to 2^12 (what
 // falls below 2^-24 then is 2^-36 of the row's largest): the products
 // accumulate exactly what float32 sums of the codes' values do.  K's scale joins
-// the scores in float32.  V's scale joins the weights: O is held in units of a
-// power of two next to the scales of the last pages, and p * vs / unit, p in
-// [0, 2^8], rounded to 11 bits, is all that is rounded.  (As a multiply of each
-// page's product before it joined the output the scale took a second set of
-// accumulators and a quarter of a tile's instructions.)
+// the scores in float32.  V's scale joins the weights: O is held in units of
+// 2^-10 of a power of two next to the largest scale so far, and p * vs / unit, p
+// in [0, 2^4], is rounded to half precision, which is all that is rounded: 2^-11 of
+// a weight, or 2^-25 units where it is below 2^-14 of them.  While the scales stay
+// within 2^7 of one another that is 2^-28 of a weight of 1 at most.  Once they do
+// not, each 16 keys' weights are brought to 2^14 row by row before they are rounded
+// and their product joins O by a factor in float32.  (Every page's product joining O
+// by a factor took a second set of accumulators and a quarter of a tile's
+// instructions.)
 //
 // Bound.  A key costs 2 d bytes and 4 d R operations: HBM bounds it, an SM's
 // share is 23 bytes a cycle.  The codes have to be turned into 16-bit
@@ -62,7 +66,7 @@ constexpr int kDpTileBytes = 4096;       // of K, and of V
 // A run takes this many tiles at least: a part is 4 KB for each row tile at
 // d = 128, a tile 8 KB.
 __host__ __device__ constexpr int dp_min_tiles(int tiles) { return tiles + 1; }
-constexpr float kDpTau = 8.0f;           // lazy-rescale threshold, log2 units
+constexpr float kDpTau = 4.0f;           // lazy-rescale threshold, log2 units (headroom of weights)
 constexpr uint32_t kSiteDpFull = 50;
 __host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
 
@@ -130,18 +134,23 @@ __host__ __device__ __forceinline__ bool paged_sees(int key0, int n, int pos, in
   return key0 <= pos && (key0 + n - 1 > pos - win || key0 < sinks);
 }
 
-// O is held in units of vref, a power of two next to the scales of the last
-// pages (their largest, top), so that weights times a page's scale / vref round
-// like weights.  The unit after `top`: it falls to 2^-60 of its largest value
-// (most) at most, so that O, at most 2^47 units before, stays finite.
+// O is held in units of vref, 2^-10 of a power of two that is not below the scales
+// so far: a weight of up to 2^4 is at most 2^14 units (2^15 for scales over 2^127).
+// The unit rises with the scales; a piece whose smallest scale but 0 is below
+// 2^3 units (paged_apart) has weights that half precision would cut short.
 __host__ __device__ __forceinline__ bool paged_new_unit(float vref, float top) {
-  return top > vref || (top > 0.f && top < vref * (1.f / 64.f));
+  return top > vref * 0x1p10f;
 }
-__device__ __forceinline__ float paged_unit(float top, float& most) {
+__host__ __device__ __forceinline__ bool paged_apart(float vref, float least) {
+  return least < vref * 0x1p3f;
+}
+__device__ __forceinline__ float paged_unit(float top) {
   const float up = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
-  const float unit = fmaxf(fminf(fmaxf(up, 0x1p-120f), 0x1p126f), most * 0x1p-60f);
-  most = fmaxf(most, unit);
-  return unit;
+  return fminf(fmaxf(up, 0x1p-116f), 0x1p127f) * 0x1p-10f;
+}
+// 1 / unit, 0 before there is one
+__device__ __forceinline__ float paged_per_unit(float vref) {
+  return vref > 0.f ? __uint_as_float(0x7f000000u - __float_as_uint(vref)) : 0.f;
 }
 
 // Key rows of the 16 of a product.  At d = 128 a row is 128 bytes, its 16-byte
@@ -445,8 +454,9 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         l[nt][e] = 0.f;
       }
     float o[kJ][kTiles][4] = {};
-    float vref = 0.f, inv_vref = 0.f;        // unit of O (0: nothing summed yet)
-    float vref_most = 0.f;                   // its largest
+    float vref = 0.f;                        // unit of O (0: nothing summed yet)
+    float vs_least = INFINITY;               // smallest scale of values but 0
+    bool apart = false;                      // scales too far from one another for one unit
     uint32_t seen = 0;                       // rows (2 nt + e) with a reference
     const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
 
@@ -513,8 +523,19 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       }
 
       // ---- scores less the row's reference, in log2 units
-      float vs[kMt], vs_top = 0.f;
+      float vs_top = 0.f;
       bool odd = false;                      // a scale of values that is not finite
+      // the scale of 16 keys' values, 0 where it is not finite, names no page, or is of a
+      // page that no row sees (which may have any scale)
+      auto scale_of = [&](int mt, bool& not_finite) {
+        float x = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
+        if (!full && !paged_seen(s, p.Nq, key0 + mt * 16, 16, p.win, p.sinks)) x = 0.f;
+        if (!(fabsf(x) < INFINITY)) {
+          x = 0.f;
+          not_finite = true;
+        }
+        return x;
+      };
       float mx[kTiles][2];
 #pragma unroll
       for (int nt = 0; nt < kTiles; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
@@ -522,14 +543,9 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       for (int mt = 0; mt < kMt; ++mt) {
         const float ks = sc[box_of(mt)];
         const uint64_t k2 = ptx::f2_pack(ks, ks);
-        vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
-        // (a page that no row sees may have any scale)
-        if (!full && !paged_seen(s, p.Nq, key0 + mt * 16, 16, p.win, p.sinks)) vs[mt] = 0.f;
-        if (!(fabsf(vs[mt]) < INFINITY)) {
-          vs[mt] = 0.f;
-          odd = true;
-        }
-        vs_top = fmaxf(vs_top, fabsf(vs[mt]));
+        const float size = fabsf(scale_of(mt, odd));
+        vs_top = fmaxf(vs_top, size);
+        if (size > 0.f) vs_least = fminf(vs_least, size);
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
           const uint64_t q2 = ptx::f2_pack(qmul[nt][0], qmul[nt][1]);
@@ -562,10 +578,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
           for (int e = 0; e < 2; ++e)
             mx[nt][e] = ptx::max3(mx[nt][e], sv[mt][nt][e], sv[mt][nt][e + 2]);
       if (paged_new_unit(vref, vs_top)) {
-        const float now = paged_unit(vs_top, vref_most);
-        const float f = vref > 0.f ? vref / now : 1.f;
+        const float now = paged_unit(vs_top), f = vref * paged_per_unit(now);
         vref = now;
-        inv_vref = 1.f / now;
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
 #pragma unroll
@@ -573,6 +587,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][nt][e] *= f;
       }
+      apart = apart || paged_apart(vref, vs_least);
       // a row keeps its reference until a score passes it by the threshold (or is
       // its first): only then do its lanes look for its largest
       bool raise = false;
@@ -612,12 +627,28 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
             for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[e & 1];
         }
       }
+      const float per_unit = paged_per_unit(vref);
+      // of each row and, by bytes, 16 keys: the exponent that takes weights of 2^14 back
+      uint32_t back[kTiles][2] = {};
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
-        const float r = vs[mt] * inv_vref;
-        const uint64_t r2 = ptx::f2_pack(r, r);
+        const float r = scale_of(mt, odd) * per_unit;
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
+          uint64_t r2 = ptx::f2_pack(r, r);
+          if (apart) {
+            float up[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(sv[mt][nt][e], sv[mt][nt][e + 2]);
+#pragma unroll
+              for (int i = 4; i < 32; i *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+              const int k = static_cast<int>(ceilf(fminf(fmaxf(x, -100.f), kDpTau)));
+              up[e] = __uint_as_float(static_cast<uint32_t>(127 + 14 - k) << 23);
+              back[nt][e] |= static_cast<uint32_t>(127 - 14 + k) << (8 * mt);
+            }
+            r2 = ptx::f2_pack(up[0], up[1]);
+          }
           const uint64_t ab = ptx::f2_pack(ptx::ex2(sv[mt][nt][0]), ptx::ex2(sv[mt][nt][1]));
           const uint64_t cd = ptx::f2_pack(ptx::ex2(sv[mt][nt][2]), ptx::ex2(sv[mt][nt][3]));
           const uint64_t sum =
@@ -672,15 +703,40 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         uint2 pb[kTiles];
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) pb[nt] = p_s[(mt * kTiles + nt) * 32 + lane];
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          uint32_t a0, a1, a2, a3;
+        auto values = [&](int j, uint32_t* a) {
           constexpr uint32_t kSel[2] = {0x5140, 0x7362};
-          codes4<kInt8>(__byte_perm(v[0][j >> 1], v[1][j >> 1], kSel[j & 1]), a0, a1);
-          codes4<kInt8>(__byte_perm(v[2][j >> 1], v[3][j >> 1], kSel[j & 1]), a2, a3);
+          codes4<kInt8>(__byte_perm(v[0][j >> 1], v[1][j >> 1], kSel[j & 1]), a[0], a[1]);
+          codes4<kInt8>(__byte_perm(v[2][j >> 1], v[3][j >> 1], kSel[j & 1]), a[2], a[3]);
+        };
+        if (!apart) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            uint32_t a[4];
+            values(j, a);
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
+              mma16816(o[j][nt], a[0], a[1], a[2], a[3], pb[nt].x, pb[nt].y);
+          }
+        } else {
+          const float r = scale_of(mt, odd) * per_unit;
+          float w[kTiles][2];
 #pragma unroll
           for (int nt = 0; nt < kTiles; ++nt)
-            mma16816(o[j][nt], a0, a1, a2, a3, pb[nt].x, pb[nt].y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              w[nt][e] = r * __uint_as_float((back[nt][e] >> (8 * mt) & 255u) << 23);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            uint32_t a[4];
+            values(j, a);
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt) {
+              float x[4] = {};
+              mma16816(x, a[0], a[1], a[2], a[3], pb[nt].x, pb[nt].y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[j][nt][e] = fmaf(x[e], w[nt][e & 1], o[j][nt][e]);
+            }
+          }
         }
       }
       __syncwarp();                          // the stage has been read

@@ -58,8 +58,8 @@ enum DtWaitSite : uint32_t {
 struct DtMeta {
   float ks[8], vs[8];
   uint32_t have;
-  float top;               // the largest finite |vs| of those that some row sees
-  uint32_t pad[2];
+  float top, least;        // the largest and the smallest finite |vs| but 0 of those that some row sees
+  uint32_t pad;
 };
 
 template <int D>
@@ -280,12 +280,15 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       if (is_v) {
         const float size = mine && now.seen && fabsf(now.scale) < INFINITY ? fabsf(now.scale) : 0.f;
         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+        const uint32_t least =
+            __reduce_min_sync(0xffffffffu, size > 0.f ? __float_as_uint(size) : kInfBits);
         // (a box's bit for each 16 keys of it)
         const uint32_t bits =
             __ballot_sync(0xffffffffu, lane < 8 && (have >> (lane * p.boxes / 8) & 1u));
         if (lane == 0) {
           metas[ms].have = bits;
           metas[ms].top = __uint_as_float(top);
+          metas[ms].least = __uint_as_float(least);
         }
       }
       __syncwarp();
@@ -530,7 +533,11 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const int pos = s.len - p.Nq + (row0 + r) % p.Nq;
       const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
       float m = 0.f, l = 0.f,                    // the reference, 0 before the first score
-            vref = 0.f, inv_vref = 0.f, vref_most = 0.f, qmul = 0.f;
+            vref = 0.f, qmul = 0.f;              // the unit of O
+      // the smallest scale of values but 0; once the scales are apart, the largest unit
+      // that the row's weights called for, less what its reference has risen
+      float bound = INFINITY;
+      bool apart = false;
       bool fresh = true, poison = false;         // no reference yet; a page's scale of values is not finite
       for (int i = 0; i < n; ++i, ++j) {
         const int ms = j % kDtMetas, b = j & 1;
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         ptx::tc_fence_after();
         const volatile DtMeta* const meta = meta_of(ms);
         const uint32_t have = meta->have >> (2 * part) & 3u;
-        const float top = meta->top;
+        const float top = meta->top, least = meta->least;
         const float ks[2] = {meta->ks[2 * part], meta->ks[2 * part + 1]};
         float vs[2] = {meta->vs[2 * part], meta->vs[2 * part + 1]};
         // every row sees every key of the thread's
@@ -623,18 +630,50 @@ __global__ void __launch_bounds__(kDtThreads, 1)
               for (int e = 0; e < 32; ++e) x[e] -= mx;
             }
           }
-          // the unit of O follows the tile's scales, alike in every thread
-          if (paged_new_unit(vref, top)) {
-            const float now = paged_unit(top, vref_most);
-            if (vref > 0.f) f *= vref / now;
-            vref = now;
-            inv_vref = 1.f / now;
+          // The unit of O rises with the scales, alike in every thread, until they are
+          // apart; from then on it follows the row's largest product of a weight and its
+          // scale in the tile, so that what is next to that is rounded to 11 bits.  It falls
+          // to 2^-30 of the largest one at most, next to which the rest is nothing, and O
+          // stays finite.
+          if (apart) {
+            bound *= f;
+          } else {
+            bound = fminf(bound, least);
+            const float was = vref * f;
+            if (paged_new_unit(vref, top)) {
+              const float now = paged_unit(top);
+              if (vref > 0.f) f *= vref * paged_per_unit(now);
+              vref = now;
+            }
+            if (paged_apart(vref, bound)) {
+              apart = true;
+              bound = was;
+            }
           }
+          if (apart) {
+            float c = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float largest = -INFINITY;
+#pragma unroll
+              for (int e = 16 * k; e < 16 * k + 16; e += 2)
+                largest = ptx::max3(largest, x[e], x[e + 1]);
+              c = fmaxf(c, ptx::ex2(largest - kDpTau) * fabsf(vs[k]));
+            }
+            c = row_all(c, [](float u, float v) { return fmaxf(u, v); });
+            if (paged_new_unit(vref, c) || (c > 0.f && c < vref * 0x1p7f)) {
+              const float now = paged_unit(fmaxf(c, bound * 0x1p-20f));
+              f *= fminf(vref * paged_per_unit(now), 0x1p100f);
+              vref = now;
+            }
+            bound = fmaxf(bound, vref);
+          }
+          const float per_unit = paged_per_unit(vref);
           uint64_t acc = ptx::f2_pack(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float rv = vs[k] * inv_vref;
+            const float rv = vs[k] * per_unit;
             const uint64_t r2 = ptx::f2_pack(rv, rv);
 #pragma unroll
             for (int e = 16 * k; e < 16 * k + 16; e += 2) {

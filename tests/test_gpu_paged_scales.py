@@ -1,0 +1,182 @@
+"""Decoding over pages whose scales differ widely (fa_decode_paged), against the
+definition in float64.
+
+Bounds.  u = eps / 2 is half a step of the 16-bit type.  A score is a sum of d
+products of exact numbers in float32, off by at most e = 128 * 2^-23 * scale *
+sum |q||k|.  A weight p_j times the scale vs_j of its values' page is rounded
+to half precision: 2^-11 relative (11 significant bits: steps of 2^-10 from 1 on,
+half of one is off by 2^-11 of 1 at most), or half of the smallest step, 2^-25,
+in the unit of O, and by no more than itself.  While the scales so far are within
+2^7 of one another each is 2^3 units or more, and the half step at most 2^-28
+vs_j.  Where they are not, weights are brought next to 2^14 before they are
+rounded: those of 16 keys and a row (up to 16 rows a key/value head), or a row's
+p_j vs_j of 128 keys by a unit that is 2^-7 to 2^-10 of 2^-4 times the largest (more
+rows): 2^-25 - 7 - 4 max (p vs) a code, or 2^-24 - 30 of what the row had before.
+Weights are relative to a reference that only rises and that the row's sum is
+at least 1 times, so for codes b and values v = vs b
+    |dO| <= (2^-11 + 2 e + 2^-17 + s) A + u |O| + t,   A = sum_j p_j |v_j|,
+    t = sum min(p_j, 2^-28) |v_j| + 2^-35 max_j (p_j vs_j) sum |b_j|  over the keys
+the row sees, s = n / 16 * 2^-23 the sums of n keys, 16 a product, and 2^-17 the
+exponential, the factors of merging and the division.  |dLSE| <= e + 2^-17 + s
++ 2^-21 |LSE|.  fp16 results add half of their smallest step, 2^-25.
+"""
+import numpy as np
+import pytest
+import torch
+
+import exact_tiled_attention_14_gb300 as fa
+import paged_common as pc
+from gpu_common import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def status_ok():
+    torch.cuda.synchronize()
+    code, word = fa.fa_status()
+    assert code == fa.FA_OK, f"device status {word:#x}"
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def decode(q, cache, table, lens, **kw):
+    o, lse = fa.attention_decode_paged(q, cache, table, ints(lens), **kw)
+    status_ok()
+    return o.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def sequence(cache, pages, n):
+    """k, v, v's codes and v's scales of the first n slots of the pages, float64
+    [Hk, n, d] and [Hk, n]."""
+    out = []
+    for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        code = pc.numpy_codes(x[pages] if x.dtype == torch.int8 else
+                              x.view(torch.uint8)[pages].view(x.dtype))
+        scale = s[pages].double().cpu().numpy()
+        out.append((np.moveaxis(code, 1, 0).reshape(code.shape[1], -1, code.shape[3])[:, :n],
+                    np.repeat(scale.T, code.shape[2], 1)[:, :n]))
+    (ka, ks), (b, vs) = out
+    with np.errstate(invalid="ignore"):
+        return ka * ks[..., None], b * vs[..., None], np.abs(b), np.abs(vs)
+
+
+def check(got, q, cache, table, lens, b, window=None, sinks=0, scale=None, rows=None):
+    """O and LSE of sequence b (of its tokens `rows`) within their bounds."""
+    o, lse = got
+    H, Nq, d = q.shape[1:]
+    n, Hk = lens[b], cache.k.shape[1]
+    scale = pc.scale_of(d) if scale is None else scale
+    u = pc.wc.half_step("bf16" if q.dtype == torch.bfloat16 else "fp16")
+    tiny = 0.0 if q.dtype == torch.bfloat16 else 2.0 ** -25
+    page = cache.k.shape[2]
+    k, v, codes, vs = sequence(cache, table[b, :-(-n // page)].long(), n)
+    mask = pc.window_mask(Nq, n, n, "bottom_right", n + 99 if window is None else window, sinks)
+    qd = q[b].double().cpu().numpy()
+    for i in range(Nq) if rows is None else rows:
+        m = mask[i]
+        sums = m.sum() / 16 * 2.0 ** -23
+        for hk in range(Hk):
+            kk, vv = k[hk][m], v[hk][m]
+            for h in range(hk * (H // Hk), (hk + 1) * (H // Hk)):
+                s = scale * (kk @ qd[h, i])
+                e = 128 * 2.0 ** -23 * scale * (np.abs(kk) @ np.abs(qd[h, i])).max()
+                mx = s.max()
+                p = np.exp(s - mx)
+                l = p.sum()
+                p = p / l
+                ref, size = p @ vv, p @ np.abs(vv)
+                t = (np.minimum(p, 2.0 ** -28) @ np.abs(vv)
+                     + 2.0 ** -35 * (p * vs[hk][m]).max() * codes[hk][m].sum(0))
+                tol = (2.0 ** -11 + 2 * e + 2.0 ** -17 + sums) * size + u * np.abs(ref) + t + tiny
+                err = np.abs(o[b, h, i] - ref)
+                assert (err <= tol).all(), (f"token {i} head {h}: off {np.max(err - tol):.3e} more than "
+                                            f"the bound, |O| {np.abs(ref).max():.3e}, "
+                                            f"worst {np.max(err / tol):.3g} of it")
+                want = mx + np.log(l)
+                assert abs(lse[b, h, i] - want) <= e + 2.0 ** -17 + sums + 2.0 ** -21 * abs(want)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16, 20, 26, 40])
+@pytest.mark.parametrize("H", [4, 8, 24])      # 8, 16 and 48 rows a key/value head
+@pytest.mark.parametrize("d,code", [(64, "int8"), (64, "e4m3"), (128, "e4m3")])
+def test_a_large_scale_beside_ordinary_ones(d, code, H, bits):
+    """One page's values are 2^bits times the others': the last one, which only
+    the last token sees, or one at the window's start, which only the first sees.
+    Each token's result is as exact as its own keys allow."""
+    for large, window in ((3, None), (1, 17), (0, None)):
+        cache = pc.random_cache(5, 1, 16, d, code, seed=bits)
+        table, lens = ints([[4, 2, 0, 3]]), [49]
+        cache.v_scale[int(table[0, large])] *= 2.0 ** bits
+        q = pc.normal((1, H, 2, d), "bf16", 1).cuda()
+        check(decode(q, cache, table, lens, window=window), q, cache, table, lens, 0, window)
+
+
+@pytest.mark.parametrize("bits", [8, 16, 20, 30, 40])
+@pytest.mark.parametrize("H", [4, 8, 24])
+@pytest.mark.parametrize("d,code", [(64, "e4m3"), (128, "int8"), (128, "e4m3")])
+def test_large_values_of_no_weight(d, code, H, bits):
+    """A page of values 2^bits times the others' whose scores are 28 (d = 128) or
+    40 below them, anywhere in the sequence: the weight is on the small pages."""
+    for large in (0, 1, 4, 8):
+        cache = pc.random_cache(10, 1, 16, d, code, seed=bits + 1)
+        table, lens = ints([[7, 2, 5, 0, 3, 6, 8, 1, 9]]), [16 * 9 - 3]
+        p = int(table[0, large])
+        cache.v_scale[p] *= 2.0 ** bits
+        cache.k.view(torch.uint8)[:, :, :, 0] = 0
+        cache.k.view(torch.uint8)[p] = 0
+        cache.k[p, 0, :, 0] = torch.tensor(-80.0, device="cuda").to(cache.k.dtype)
+        cache.k_scale[p] = 0.5
+        q = pc.normal((1, H, 2, d), "bf16", 2)
+        q[..., 0] = 8.0
+        q = q.cuda()
+        check(decode(q, cache, table, lens), q, cache, table, lens, 0)
+
+
+@pytest.mark.parametrize("ratio", [1.5, 8.0, 60.0, 1000.0])
+@pytest.mark.parametrize("G,Hk", [(4, 8), (16, 8), (32, 4)])
+def test_many_light_keys(G, Hk, ratio):
+    """A key 14 above 32768 others and without values of its own, behind a page
+    of larger ones, in one run: the result is what the light keys add up to."""
+    d, page, n = 128, 128, 32768 + 256
+    warps = 12 if G <= 8 else 10 if G <= 16 else 1
+    B = torch.cuda.get_device_properties(0).multi_processor_count * warps // Hk
+    cache = pc.random_cache(10, Hk, page, d, "e4m3", seed=3, spread=0.0)
+    per = n // page
+    table = ints([[8, 9] + [i % 8 for i in range(per - 2)]]).expand(B, per).contiguous()
+    cache.v_scale[8] *= ratio
+    cache.k.view(torch.uint8)[:, :, :, 0] = 0
+    cache.k.view(torch.uint8)[9, :, 5] = 0
+    cache.v.copy_(cache.v.float().abs())           # the light keys' values add up
+    cache.v.view(torch.uint8)[9, :, 5] = 0
+    cache.k[9, :, 5, 0] = torch.tensor(160.0, device="cuda").to(cache.k.dtype)   # 1.6 * 9 q
+    q = pc.normal((1, Hk * G, 1, d), "fp16", 4)
+    q[..., 0] = 14 / 1.6 / pc.scale_of(d)
+    q = q.expand(B, -1, -1, -1).contiguous().cuda()
+    got = decode(q, cache, table, [n] * B)
+    check(got, q, cache, table, [n] * B, B // 2)
+    check(got, q, cache, table, [n] * B, 0)
+
+
+@pytest.mark.parametrize("H", [3, 10, 30])     # 12, 40 and 120 rows
+@pytest.mark.parametrize("page,d,code", [(16, 128, "e4m3"), (48, 64, "int8"), (128, 128, "int8")])
+def test_scales_that_rise_and_fall(page, d, code, H):
+    """Pages 2^-20 to 2^20 times the usual scale in random order, under a window
+    of 40 keys behind sequences of every length."""
+    per = 8
+    lens = [7 * i % (per * page + 1) for i in range(30)]
+    lens = [n for n in lens if n >= 4]
+    B = len(lens)
+    cache = pc.random_cache(per * B, 1, page, d, code, seed=5, spread=20.0)
+    cache.k_scale[:] = 0.01
+    table = torch.randperm(per * B, generator=torch.Generator().manual_seed(6)).view(B, per).int().cuda()
+    q = pc.normal((B, H, 4, d), "bf16", 7).cuda()
+    got = decode(q, cache, table, lens, window=40, sinks=2)
+    for b in range(B):
+        check(got, q, cache, table, lens, b, window=40, sinks=2)
