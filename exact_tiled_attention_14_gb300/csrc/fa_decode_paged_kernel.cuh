@@ -10,15 +10,18 @@
 // multiplied by a power of two that brings its largest element to 2^12 (what
 // falls below 2^-24 then is 2^-36 of the row's largest): the products
 // accumulate exactly what float32 sums of the codes' values do.  K's scale joins
-// the scores in float32.  V's scale joins the weights: O is held in units of
-// 2^-10 of a power of two next to the largest scale so far, and p * vs / unit, p
-// in [0, 2^4], is rounded to half precision, which is all that is rounded: 2^-11 of
-// a weight, or 2^-25 units where it is below 2^-14 of them.  While the scales stay
-// within 2^7 of one another that is 2^-28 of a weight of 1 at most.  Once they do
-// not, each 16 keys' weights are brought to 2^14 row by row before they are rounded
-// and their product joins O by a factor in float32.  (Every page's product joining O
-// by a factor took a second set of accumulators and a quarter of a tile's
-// instructions.)
+// the scores in float32.  V's scale joins the weights: O is held in units of a power
+// of two that follows the scales, and p * vs / unit is rounded to half precision:
+// by 2^-11 of a weight, or by 2^-25 units where it is below 2^-14 of them.  A weight
+// p is up to 2^6 (its row's reference rises with scores that pass it by more), the
+// largest scale up to 2^8 units, and while no scale but 0 is under 2^-6 of the largest
+// the smallest step is 2^-27 of a weight of 1 at most.  Once one is, each row
+// has a unit of its own (paged_row_unit), so that pages that a row does not see,
+// or gives no weight, cost it nothing.  (As a multiply of each page's product before
+// it joined the output the scale took a second set of accumulators and a quarter of
+// a tile's instructions.  A threshold of 2^4 with 2^10 units took the kernel for
+// many rows 71 us instead of 64 for 64 rows of 8 int8 caches at d = 64, scores of a
+// standard deviation of 2.5 powers of two.)
 //
 // Bound.  A key costs 2 d bytes and 4 d R operations: HBM bounds it, an SM's
 // share is 23 bytes a cycle.  The codes have to be turned into 16-bit
@@ -66,7 +69,7 @@ constexpr int kDpTileBytes = 4096;       // of K, and of V
 // A run takes this many tiles at least: a part is 4 KB for each row tile at
 // d = 128, a tile 8 KB.
 __host__ __device__ constexpr int dp_min_tiles(int tiles) { return tiles + 1; }
-constexpr float kDpTau = 4.0f;           // lazy-rescale threshold, log2 units (headroom of weights)
+constexpr float kDpTau = 6.0f;           // lazy-rescale threshold, log2 units
 constexpr uint32_t kSiteDpFull = 50;
 __host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
 
@@ -134,23 +137,31 @@ __host__ __device__ __forceinline__ bool paged_sees(int key0, int n, int pos, in
   return key0 <= pos && (key0 + n - 1 > pos - win || key0 < sinks);
 }
 
-// O is held in units of vref, 2^-10 of a power of two that is not below the scales
-// so far: a weight of up to 2^4 is at most 2^14 units (2^15 for scales over 2^127).
-// The unit rises with the scales; a piece whose smallest scale but 0 is below
-// 2^3 units (paged_apart) has weights that half precision would cut short.
-__host__ __device__ __forceinline__ bool paged_new_unit(float vref, float top) {
-  return top > vref * 0x1p10f;
+// The unit of O is 2^-8 of a power of two that is not below the scales so far: a
+// weight of up to 2^6 is at most 2^14 units (2^15 for scales over 2^127).  Once the
+// smallest scale but 0 is under 2^-6 of that power (they are apart), each row has
+// a unit of its own, by the largest product c of a weight (over 2^6) and its
+// scale: it falls as the row's reference rises, instead of O, and rises with c.
+constexpr float kDpUnit = 0x1p8f, kDpSpread = 0x1p6f;
+__host__ __device__ __forceinline__ bool paged_new_unit(float unit, float top) {
+  return top > unit * kDpUnit;
 }
-__host__ __device__ __forceinline__ bool paged_apart(float vref, float least) {
-  return least < vref * 0x1p3f;
+__host__ __device__ __forceinline__ bool paged_apart(float unit, float least) {
+  return least < unit * (kDpUnit / kDpSpread);
 }
 __device__ __forceinline__ float paged_unit(float top) {
   const float up = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
-  return fminf(fmaxf(up, 0x1p-116f), 0x1p127f) * 0x1p-10f;
+  return fminf(fmaxf(up, kDpUnit * 0x1p-126f), 0x1p127f) / kDpUnit;
 }
 // 1 / unit, 0 before there is one
-__device__ __forceinline__ float paged_per_unit(float vref) {
-  return vref > 0.f ? __uint_as_float(0x7f000000u - __float_as_uint(vref)) : 0.f;
+__device__ __forceinline__ float paged_per_unit(float unit) {
+  return unit > 0.f ? __uint_as_float(0x7f000000u - __float_as_uint(unit)) : 0.f;
+}
+// A row's next unit, its reference having made O a factor f smaller; returns O's factor.
+__device__ __forceinline__ float paged_row_unit(float& unit, float f, float c) {
+  const float was = unit * f;
+  unit = paged_unit(fmaxf(c, was * kDpUnit));
+  return was * paged_per_unit(unit);
 }
 
 // Key rows of the 16 of a product.  At d = 128 a row is 128 bytes, its 16-byte
@@ -454,9 +465,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         l[nt][e] = 0.f;
       }
     float o[kJ][kTiles][4] = {};
-    float vref = 0.f;                        // unit of O (0: nothing summed yet)
-    float vs_least = INFINITY;               // smallest scale of values but 0
-    bool apart = false;                      // scales too far from one another for one unit
+    float o_unit[kTiles][2] = {};              // of O, by rows (0: nothing summed yet)
+    float vs_least = INFINITY;               // smallest scale of values but 0; 0: they are apart
     uint32_t seen = 0;                       // rows (2 nt + e) with a reference
     const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
 
@@ -523,19 +533,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       }
 
       // ---- scores less the row's reference, in log2 units
-      float vs_top = 0.f;
+      float vs[kMt], vs_top = 0.f;
       bool odd = false;                      // a scale of values that is not finite
-      // the scale of 16 keys' values, 0 where it is not finite, names no page, or is of a
-      // page that no row sees (which may have any scale)
-      auto scale_of = [&](int mt, bool& not_finite) {
-        float x = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
-        if (!full && !paged_seen(s, p.Nq, key0 + mt * 16, 16, p.win, p.sinks)) x = 0.f;
-        if (!(fabsf(x) < INFINITY)) {
-          x = 0.f;
-          not_finite = true;
-        }
-        return x;
-      };
       float mx[kTiles][2];
 #pragma unroll
       for (int nt = 0; nt < kTiles; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
@@ -543,9 +542,15 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       for (int mt = 0; mt < kMt; ++mt) {
         const float ks = sc[box_of(mt)];
         const uint64_t k2 = ptx::f2_pack(ks, ks);
-        const float size = fabsf(scale_of(mt, odd));
-        vs_top = fmaxf(vs_top, size);
-        if (size > 0.f) vs_least = fminf(vs_least, size);
+        vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
+        // (a page that no row sees may have any scale)
+        if (!full && !paged_seen(s, p.Nq, key0 + mt * 16, 16, p.win, p.sinks)) vs[mt] = 0.f;
+        if (!(fabsf(vs[mt]) < INFINITY)) {
+          vs[mt] = 0.f;
+          odd = true;
+        }
+        vs_top = fmaxf(vs_top, fabsf(vs[mt]));
+        vs_least = fminf(vs_least, vs[mt] != 0.f ? fabsf(vs[mt]) : INFINITY);
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
           const uint64_t q2 = ptx::f2_pack(qmul[nt][0], qmul[nt][1]);
@@ -577,17 +582,10 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             mx[nt][e] = ptx::max3(mx[nt][e], sv[mt][nt][e], sv[mt][nt][e + 2]);
-      if (paged_new_unit(vref, vs_top)) {
-        const float now = paged_unit(vs_top), f = vref * paged_per_unit(now);
-        vref = now;
+      // what O is multiplied by
+      float f[kTiles][2];
 #pragma unroll
-        for (int j = 0; j < kJ; ++j)
-#pragma unroll
-          for (int nt = 0; nt < kTiles; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][nt][e] *= f;
-      }
-      apart = apart || paged_apart(vref, vs_least);
+      for (int nt = 0; nt < kTiles; ++nt) f[nt][0] = f[nt][1] = 1.f;
       // a row keeps its reference until a score passes it by the threshold (or is
       // its first): only then do its lanes look for its largest
       bool raise = false;
@@ -596,10 +594,10 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           raise |= mx[nt][e] > kDpTau || (!(seen >> (2 * nt + e) & 1u) && mx[nt][e] > -INFINITY);
-      if (__any_sync(0xffffffffu, raise)) {
+      raise = __any_sync(0xffffffffu, raise);
+      if (raise) {
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt) {
-          float f[2];
+        for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -607,12 +605,11 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
               mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], i));
             const uint32_t bit = 1u << (2 * nt + e);
             const bool fresh = !(seen & bit);
-            f[e] = 1.f;
             if (mx[nt][e] > kDpTau || (fresh && mx[nt][e] > -INFINITY)) {
               // (a row without a reference so far holds zeros, or NaN, which stays)
-              if (!fresh) f[e] = ptx::ex2(-mx[nt][e]);
+              f[nt][e] = fresh ? 0.f : ptx::ex2(-mx[nt][e]);
               m[nt][e] += mx[nt][e];
-              l[nt][e] *= f[e];
+              l[nt][e] *= f[nt][e];
               seen |= bit;
 #pragma unroll
               for (int mt = 0; mt < kMt; ++mt) {
@@ -621,34 +618,50 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
               }
             }
           }
-#pragma unroll
-          for (int j = 0; j < kJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[e & 1];
-        }
       }
-      const float per_unit = paged_per_unit(vref);
-      // of each row and, by bytes, 16 keys: the exponent that takes weights of 2^14 back
-      uint32_t back[kTiles][2] = {};
+      // the unit of O: alike for all rows, until the scales are apart
+      const bool rise = paged_new_unit(o_unit[0][0], vs_top);
+      const float now = rise ? paged_unit(vs_top) : o_unit[0][0];
+      if (paged_apart(now, vs_least)) {
+        vs_least = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < kMt; ++mt) {
-        const float r = scale_of(mt, odd) * per_unit;
+        for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt) {
-          uint64_t r2 = ptx::f2_pack(r, r);
-          if (apart) {
-            float up[2];
+          for (int e = 0; e < 2; ++e) {
+            float c = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(sv[mt][nt][e], sv[mt][nt][e + 2]);
+            for (int mt = 0; mt < kMt; ++mt)
+              c = fmaxf(c, ptx::ex2(fmaxf(sv[mt][nt][e], sv[mt][nt][e + 2]) - kDpTau) *
+                               fabsf(vs[mt]));
 #pragma unroll
-              for (int i = 4; i < 32; i *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
-              const int k = static_cast<int>(ceilf(fminf(fmaxf(x, -100.f), kDpTau)));
-              up[e] = __uint_as_float(static_cast<uint32_t>(127 + 14 - k) << 23);
-              back[nt][e] |= static_cast<uint32_t>(127 - 14 + k) << (8 * mt);
-            }
-            r2 = ptx::f2_pack(up[0], up[1]);
+            for (int i = 4; i < 32; i *= 2) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, i));
+            f[nt][e] = paged_row_unit(o_unit[nt][e], f[nt][e], c);
           }
+        raise = true;
+      } else if (rise) {
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            f[nt][e] *= o_unit[nt][e] * paged_per_unit(now);
+            o_unit[nt][e] = now;
+          }
+        raise = true;
+      }
+      if (raise) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+          for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][nt][e] *= f[nt][e & 1];
+      }
+#pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt) {
+        const uint64_t per = ptx::f2_pack(paged_per_unit(o_unit[nt][0]), paged_per_unit(o_unit[nt][1]));
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          const uint64_t r2 = ptx::fmul2(ptx::f2_pack(vs[mt], vs[mt]), per);
           const uint64_t ab = ptx::f2_pack(ptx::ex2(sv[mt][nt][0]), ptx::ex2(sv[mt][nt][1]));
           const uint64_t cd = ptx::f2_pack(ptx::ex2(sv[mt][nt][2]), ptx::ex2(sv[mt][nt][3]));
           const uint64_t sum =
@@ -703,40 +716,15 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         uint2 pb[kTiles];
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) pb[nt] = p_s[(mt * kTiles + nt) * 32 + lane];
-        auto values = [&](int j, uint32_t* a) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          uint32_t a0, a1, a2, a3;
           constexpr uint32_t kSel[2] = {0x5140, 0x7362};
-          codes4<kInt8>(__byte_perm(v[0][j >> 1], v[1][j >> 1], kSel[j & 1]), a[0], a[1]);
-          codes4<kInt8>(__byte_perm(v[2][j >> 1], v[3][j >> 1], kSel[j & 1]), a[2], a[3]);
-        };
-        if (!apart) {
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            uint32_t a[4];
-            values(j, a);
-#pragma unroll
-            for (int nt = 0; nt < kTiles; ++nt)
-              mma16816(o[j][nt], a[0], a[1], a[2], a[3], pb[nt].x, pb[nt].y);
-          }
-        } else {
-          const float r = scale_of(mt, odd) * per_unit;
-          float w[kTiles][2];
+          codes4<kInt8>(__byte_perm(v[0][j >> 1], v[1][j >> 1], kSel[j & 1]), a0, a1);
+          codes4<kInt8>(__byte_perm(v[2][j >> 1], v[3][j >> 1], kSel[j & 1]), a2, a3);
 #pragma unroll
           for (int nt = 0; nt < kTiles; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              w[nt][e] = r * __uint_as_float((back[nt][e] >> (8 * mt) & 255u) << 23);
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            uint32_t a[4];
-            values(j, a);
-#pragma unroll
-            for (int nt = 0; nt < kTiles; ++nt) {
-              float x[4] = {};
-              mma16816(x, a[0], a[1], a[2], a[3], pb[nt].x, pb[nt].y);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[j][nt][e] = fmaf(x[e], w[nt][e & 1], o[j][nt][e]);
-            }
-          }
+            mma16816(o[j][nt], a0, a1, a2, a3, pb[nt].x, pb[nt].y);
         }
       }
       __syncwarp();                          // the stage has been read
@@ -762,7 +750,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         const int r = nt * 8 + 2 * t + e;
         if (r >= rows) continue;
         if (whole) {
-          const float f = lt != 0.f ? vref / lt : 0.f;
+          const float f = lt != 0.f ? o_unit[nt][e] / lt : 0.f;
           float x[2 * kJ];
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
@@ -784,8 +772,9 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
           float4* const out = p.part_o + (slot * p.slot_rows + r) * (D / 4) + g * (kJ / 2);
 #pragma unroll
           for (int j = 0; j < kJ / 2; ++j)
-            out[j] = make_float4(o[2 * j][nt][e] * vref, o[2 * j][nt][e + 2] * vref,
-                                 o[2 * j + 1][nt][e] * vref, o[2 * j + 1][nt][e + 2] * vref);
+            out[j] = make_float4(o[2 * j][nt][e] * o_unit[nt][e], o[2 * j][nt][e + 2] * o_unit[nt][e],
+                                 o[2 * j + 1][nt][e] * o_unit[nt][e],
+                                 o[2 * j + 1][nt][e + 2] * o_unit[nt][e]);
           if (g == 0) p.part_ml[slot * p.slot_rows + r] = make_float2(mt, lt);
         }
       }

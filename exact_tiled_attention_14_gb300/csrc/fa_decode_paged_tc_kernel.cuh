@@ -533,11 +533,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const int pos = s.len - p.Nq + (row0 + r) % p.Nq;
       const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
       float m = 0.f, l = 0.f,                    // the reference, 0 before the first score
-            vref = 0.f, qmul = 0.f;              // the unit of O
-      // the smallest scale of values but 0; once the scales are apart, the largest unit
-      // that the row's weights called for, less what its reference has risen
-      float bound = INFINITY;
-      bool apart = false;
+            o_unit = 0.f, qmul = 0.f;              // the unit of O
+      float vs_least = INFINITY;                 // smallest scale of values but 0; 0: they are apart
       bool fresh = true, poison = false;         // no reference yet; a page's scale of values is not finite
       for (int i = 0; i < n; ++i, ++j) {
         const int ms = j % kDtMetas, b = j & 1;
@@ -574,6 +571,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           const int shift = shift_s[ms * kDtRows + r];
           qmul = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
         }
+        // the unit of O, alike in every thread until the scales are apart
+        vs_least = fminf(vs_least, least);
+        const float now = paged_new_unit(o_unit, top) ? paged_unit(top) : o_unit;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::bMetaEmpty + ms));
         if (has) {
@@ -610,9 +610,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           }
           float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            a0 = ptx::max3(a0, x[e + 0], x[e + 1]);
-            a1 = ptx::max3(a1, x[e + 2], x[e + 3]);
+          for (int e = 0; e < 16; e += 2) {
+            a0 = ptx::max3(a0, x[e], x[e + 1]);
+            a1 = ptx::max3(a1, x[e + 16], x[e + 17]);
           }
           float mx = fmaxf(a0, a1);
           // a row keeps its reference until a score passes it by the threshold (or
@@ -622,53 +622,25 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           if (ptx::named_bar_any(1 + quarter, 128, passes())) {
             mx = row_all(mx, [](float u, float v) { return fmaxf(u, v); });
             if (passes()) {
-              if (!fresh) f = ptx::ex2(-mx);
+              f = fresh ? 0.f : ptx::ex2(-mx);   // (nothing so far: zeros, or NaN, which stays)
               fresh = false;
               m += mx;
               l *= f;
+              a0 -= mx;
+              a1 -= mx;
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[e] -= mx;
             }
           }
-          // The unit of O rises with the scales, alike in every thread, until they are
-          // apart; from then on it follows the row's largest product of a weight and its
-          // scale in the tile, so that what is next to that is rounded to 11 bits.  It falls
-          // to 2^-30 of the largest one at most, next to which the rest is nothing, and O
-          // stays finite.
-          if (apart) {
-            bound *= f;
-          } else {
-            bound = fminf(bound, least);
-            const float was = vref * f;
-            if (paged_new_unit(vref, top)) {
-              const float now = paged_unit(top);
-              if (vref > 0.f) f *= vref * paged_per_unit(now);
-              vref = now;
-            }
-            if (paged_apart(vref, bound)) {
-              apart = true;
-              bound = was;
-            }
+          if (paged_apart(now, vs_least)) {
+            vs_least = 0.f;
+            const float c = fmaxf(ptx::ex2(a0 - kDpTau) * fabsf(vs[0]), ptx::ex2(a1 - kDpTau) * fabsf(vs[1]));
+            f = paged_row_unit(o_unit, f, row_all(c, [](float u, float v) { return fmaxf(u, v); }));
+          } else if (now != o_unit) {
+            f *= o_unit * paged_per_unit(now);
+            o_unit = now;
           }
-          if (apart) {
-            float c = 0.f;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float largest = -INFINITY;
-#pragma unroll
-              for (int e = 16 * k; e < 16 * k + 16; e += 2)
-                largest = ptx::max3(largest, x[e], x[e + 1]);
-              c = fmaxf(c, ptx::ex2(largest - kDpTau) * fabsf(vs[k]));
-            }
-            c = row_all(c, [](float u, float v) { return fmaxf(u, v); });
-            if (paged_new_unit(vref, c) || (c > 0.f && c < vref * 0x1p7f)) {
-              const float now = paged_unit(fmaxf(c, bound * 0x1p-20f));
-              f *= fminf(vref * paged_per_unit(now), 0x1p100f);
-              vref = now;
-            }
-            bound = fmaxf(bound, vref);
-          }
-          const float per_unit = paged_per_unit(vref);
+          const float per_unit = paged_per_unit(o_unit);
           uint64_t acc = ptx::f2_pack(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll
@@ -730,7 +702,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         });
         poison = signbit(lt);
         lt = fabsf(lt);
-        const float f = whole ? (lt != 0.f ? vref / lt : 0.f) : vref;
+        const float f = whole ? (lt != 0.f ? o_unit / lt : 0.f) : o_unit;
         const size_t row = head * p.R + row0 + r;
 #pragma unroll 1
         for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {

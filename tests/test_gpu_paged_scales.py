@@ -7,15 +7,14 @@ sum |q||k|.  A weight p_j times the scale vs_j of its values' page is rounded
 to half precision: 2^-11 relative (11 significant bits: steps of 2^-10 from 1 on,
 half of one is off by 2^-11 of 1 at most), or half of the smallest step, 2^-25,
 in the unit of O, and by no more than itself.  While the scales so far are within
-2^7 of one another each is 2^3 units or more, and the half step at most 2^-28
-vs_j.  Where they are not, weights are brought next to 2^14 before they are
-rounded: those of 16 keys and a row (up to 16 rows a key/value head), or a row's
-p_j vs_j of 128 keys by a unit that is 2^-7 to 2^-10 of 2^-4 times the largest (more
-rows): 2^-25 - 7 - 4 max (p vs) a code, or 2^-24 - 30 of what the row had before.
-Weights are relative to a reference that only rises and that the row's sum is
-at least 1 times, so for codes b and values v = vs b
+2^6 of one another each is 2^2 units or more, and the half step at most 2^-27
+vs_j.  Once they are not, a row's unit is at most 2^-8 of the power of two next to
+2^-6 of its largest p_j vs_j, or what it was while they were, 2^-2 of its
+scales then: 2^-27 max (p vs) a code covers both.  Weights are relative to a
+reference that only rises and that the row's sum is at least 1 times, so for
+codes b and values v = vs b
     |dO| <= (2^-11 + 2 e + 2^-17 + s) A + u |O| + t,   A = sum_j p_j |v_j|,
-    t = sum min(p_j, 2^-28) |v_j| + 2^-35 max_j (p_j vs_j) sum |b_j|  over the keys
+    t = sum min(p_j, 2^-27) |v_j| + 2^-27 max_j (p_j vs_j) sum |b_j|  over the keys
 the row sees, s = n / 16 * 2^-23 the sums of n keys, 16 a product, and 2^-17 the
 exponential, the factors of merging and the division.  |dLSE| <= e + 2^-17 + s
 + 2^-21 |LSE|.  fp16 results add half of their smallest step, 2^-25.
@@ -92,8 +91,8 @@ def check(got, q, cache, table, lens, b, window=None, sinks=0, scale=None, rows=
                 l = p.sum()
                 p = p / l
                 ref, size = p @ vv, p @ np.abs(vv)
-                t = (np.minimum(p, 2.0 ** -28) @ np.abs(vv)
-                     + 2.0 ** -35 * (p * vs[hk][m]).max() * codes[hk][m].sum(0))
+                t = (np.minimum(p, 2.0 ** -27) @ np.abs(vv)
+                     + 2.0 ** -27 * (p * vs[hk][m]).max() * codes[hk][m].sum(0))
                 tol = (2.0 ** -11 + 2 * e + 2.0 ** -17 + sums) * size + u * np.abs(ref) + t + tiny
                 err = np.abs(o[b, h, i] - ref)
                 assert (err <= tol).all(), (f"token {i} head {h}: off {np.max(err - tol):.3e} more than "
@@ -103,16 +102,17 @@ def check(got, q, cache, table, lens, b, window=None, sinks=0, scale=None, rows=
                 assert abs(lse[b, h, i] - want) <= e + 2.0 ** -17 + sums + 2.0 ** -21 * abs(want)
 
 
-@pytest.mark.parametrize("bits", [4, 8, 16, 20, 26, 40])
+@pytest.mark.parametrize("bits", [4, 8, 16, 20, 26, 40, 90])
 @pytest.mark.parametrize("H", [4, 8, 24])      # 8, 16 and 48 rows a key/value head
-@pytest.mark.parametrize("d,code", [(64, "int8"), (64, "e4m3"), (128, "e4m3")])
-def test_a_large_scale_beside_ordinary_ones(d, code, H, bits):
+@pytest.mark.parametrize("d,code,page", [(64, "int8", 16), (64, "e4m3", 128), (128, "e4m3", 16),
+                                         (128, "int8", 128)])
+def test_a_large_scale_beside_ordinary_ones(d, code, page, H, bits):
     """One page's values are 2^bits times the others': the last one, which only
     the last token sees, or one at the window's start, which only the first sees.
     Each token's result is as exact as its own keys allow."""
-    for large, window in ((3, None), (1, 17), (0, None)):
-        cache = pc.random_cache(5, 1, 16, d, code, seed=bits)
-        table, lens = ints([[4, 2, 0, 3]]), [49]
+    for large, window in ((3, None), (1, page + 1), (0, None)):
+        cache = pc.random_cache(5, 1, page, d, code, seed=bits)
+        table, lens = ints([[4, 2, 0, 3]]), [3 * page + 1]
         cache.v_scale[int(table[0, large])] *= 2.0 ** bits
         q = pc.normal((1, H, 2, d), "bf16", 1).cuda()
         check(decode(q, cache, table, lens, window=window), q, cache, table, lens, 0, window)
