@@ -79,7 +79,7 @@ struct DecPagedParams {
   const void* q;           // [B * Hk, R, d]
   void* o;                 // [B * Hk, R, d]
   float* lse;              // [B * Hk, R]
-  float4* part_o;          // [2 * runs, slot_rows, d / 4] unnormalised parts
+  float4* part_o;          // [2 * runs, slot_rows, d / 4] parts, each the mean of its values
   float2* part_ml;         // [2 * runs, slot_rows] (m in log2 units, l)
   int2* cut;               // [units] (slot of the unit's first part, run of its last), (-1, 0): whole
   const float* k_scale;    // [pages, Hk]
@@ -749,14 +749,15 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         const float mt = m[nt][e];
         const int r = nt * 8 + 2 * t + e;
         if (r >= rows) continue;
-        if (whole) {
-          const float f = lt != 0.f ? o_unit[nt][e] / lt : 0.f;
-          float x[2 * kJ];
+        // (in this order nothing leaves float32's range that the result does not)
+        const float inv = 1.f / lt;
+        float x[2 * kJ];
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            x[2 * j] = lt != 0.f ? o[j][nt][e] * f : 0.f;
-            x[2 * j + 1] = lt != 0.f ? o[j][nt][e + 2] * f : 0.f;
-          }
+        for (int j = 0; j < kJ; ++j) {
+          x[2 * j] = lt != 0.f ? o[j][nt][e] * inv * o_unit[nt][e] : 0.f;
+          x[2 * j + 1] = lt != 0.f ? o[j][nt][e + 2] * inv * o_unit[nt][e] : 0.f;
+        }
+        if (whole) {
           const size_t row = head * p.R + row0 + r;
           uint4* const out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D) +
                              g * (kJ / 4);
@@ -772,9 +773,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
           float4* const out = p.part_o + (slot * p.slot_rows + r) * (D / 4) + g * (kJ / 2);
 #pragma unroll
           for (int j = 0; j < kJ / 2; ++j)
-            out[j] = make_float4(o[2 * j][nt][e] * o_unit[nt][e], o[2 * j][nt][e + 2] * o_unit[nt][e],
-                                 o[2 * j + 1][nt][e] * o_unit[nt][e],
-                                 o[2 * j + 1][nt][e + 2] * o_unit[nt][e]);
+            out[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
           if (g == 0) p.part_ml[slot * p.slot_rows + r] = make_float2(mt, lt);
         }
       }
@@ -795,7 +794,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 // a row, 4 columns a thread.  With few parts D / 4 threads do a row alone, and a
 // block several rows (kGroups = 1); with many, kGroups such groups take other
 // parts of one row each and meet in shared memory.  kBatch parts are in flight at
-// a time.  Every part is scaled to the largest maximum, and the sum divided once.
+// a time.  Each part is a mean with its weight, and so is what they add up to: every
+// factor is at most 1, and values of any size stay in range.
 // A row without a visible key has no live part (a sum of NaN is live).
 // (5 parts of 512 units, 4 rows: 8.0 us with four groups a row, 5.8 alone.)
 constexpr int kDpCombineThreads = 128;       // of kGroups = 1
@@ -836,19 +836,27 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDpCombineThreads : kGroups * (
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (ml[k].y != 0.f) now = fmaxf(now, ml[k].x);
-      const float fo = m == -INFINITY ? 0.f : ptx::ex2(m - now);
-      acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
-      l *= fo;
+      // the weight of what there was, then those of the batch
+      const float was = m == -INFINITY ? 0.f : ptx::ex2(m - now) * l;
+      float w[kBatch];
+      l = was;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        w[k] = ml[k].y != 0.f ? ptx::ex2(ml[k].x - now) * ml[k].y : 0.f;
+        l += w[k];
+      }
       m = now;
+      if (l == 0.f) continue;
+      const float inv = 1.f / l, fo = was * inv;
+      acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (ml[k].y != 0.f) {
-          const float f = ptx::ex2(ml[k].x - m);
+          const float f = w[k] * inv;
           acc.x = fmaf(f, x[k].x, acc.x);
           acc.y = fmaf(f, x[k].y, acc.y);
           acc.z = fmaf(f, x[k].z, acc.z);
           acc.w = fmaf(f, x[k].w, acc.w);
-          l = fmaf(f, ml[k].y, l);
         }
     }
     float top = m, lt = l;
@@ -866,23 +874,24 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDpCombineThreads : kGroups * (
           if (ml_s[k].y != 0.f) top = fmaxf(top, ml_s[k].x);
 #pragma unroll 4
         for (int k = 0; k < kGroups; ++k)
+          if (ml_s[k].y != 0.f) lt += ptx::ex2(ml_s[k].x - top) * ml_s[k].y;
+        const float inv = 1.f / lt;
+#pragma unroll 4
+        for (int k = 0; k < kGroups; ++k)
           if (ml_s[k].y != 0.f) {
-            const float f = ptx::ex2(ml_s[k].x - top);
+            const float f = ptx::ex2(ml_s[k].x - top) * ml_s[k].y * inv;
             const float4 x = acc_s[k][c];
             sum.x = fmaf(f, x.x, sum.x);
             sum.y = fmaf(f, x.y, sum.y);
             sum.z = fmaf(f, x.z, sum.z);
             sum.w = fmaf(f, x.w, sum.w);
-            lt = fmaf(f, ml_s[k].y, lt);
           }
       }
     }
     if (group == 0) {
-      const float inv = lt != 0.f ? 1.0f / lt : 0.f;
       const size_t out = static_cast<size_t>(head) * p.R + row;
       reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D)[c] =
-          make_uint2(ptx::pack2<kBf16>(sum.x * inv, sum.y * inv),
-                     ptx::pack2<kBf16>(sum.z * inv, sum.w * inv));
+          make_uint2(ptx::pack2<kBf16>(sum.x, sum.y), ptx::pack2<kBf16>(sum.z, sum.w));
       if (c == 0) p.lse[out] = lt != 0.f ? (ptx::lg2(lt) + top) * 0.693147180559945309f : -INFINITY;
     }
     if constexpr (kGroups > 1) __syncthreads();

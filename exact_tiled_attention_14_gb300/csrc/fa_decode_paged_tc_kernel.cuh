@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         });
         poison = signbit(lt);
         lt = fabsf(lt);
-        const float f = whole ? (lt != 0.f ? o_unit / lt : 0.f) : o_unit;
+        const float inv = 1.f / lt;
         const size_t row = head * p.R + row0 + r;
 #pragma unroll 1
         for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           float x[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            x[e] = __uint_as_float(a[e]) * f;
+            x[e] = __uint_as_float(a[e]) * inv * o_unit;
             if (lt == 0.f) x[e] = 0.f;
             if (poison) x[e] = NAN;
           }

@@ -180,3 +180,25 @@ def test_scales_that_rise_and_fall(page, d, code, H):
     got = decode(q, cache, table, lens, window=40, sinks=2)
     for b in range(B):
         check(got, q, cache, table, lens, b, window=40, sinks=2)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 117, 2.0 ** -100])
+@pytest.mark.parametrize("H", [4, 12, 40])
+@pytest.mark.parametrize("n", [300, 30000])
+def test_values_near_the_ends_of_the_range(n, H, size):
+    """Values of up to 2^126, or of 2^-91, whether a unit lies in one run or is cut
+    into parts: results stay in range, and as exact as usual ones."""
+    page, d = 48, 64
+    per = -(-n // page)
+    for B, code in ((1, "e4m3"), (600, "e4m3"), (1, "int8")):
+        pages = 20 if B > 1 else per
+        cache = pc.random_cache(pages, 1, page, d, code, seed=8, spread=0.5)
+        cache.v.copy_(cache.v.float().abs())
+        cache.v_scale.copy_((cache.v_scale * 100).log2().round().exp2() * (size / 2))
+        table = ints([[i % pages for i in range(per)]] * B)
+        lens = [n - b % 3 for b in range(B)]
+        q = pc.normal((B, H, 1, d), "bf16", 9).cuda()
+        got = decode(q, cache, table, lens)
+        assert np.isfinite(got[0]).all() and np.isfinite(got[1]).all()
+        for b in sorted({0, B // 2, B - 1}):
+            check(got, q, cache, table, lens, b)
