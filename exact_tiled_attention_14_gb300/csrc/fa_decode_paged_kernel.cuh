@@ -540,7 +540,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
       for (int nt = 0; nt < kTiles; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
-        const float ks = sc[box_of(mt)];
+        // (an infinite one may make scores of -inf, which would weigh nothing)
+        const float ks = fabsf(sc[box_of(mt)]) < INFINITY ? sc[box_of(mt)] : NAN;
         const uint64_t k2 = ptx::f2_pack(ks, ks);
         vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
         // (a page that no row sees may have any scale)

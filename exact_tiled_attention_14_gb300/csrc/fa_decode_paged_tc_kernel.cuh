@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const int head = x.page * p.Hk + x.hk;
         c.row = head * p.page + x.row;
         c.scale = scales[head];
+        // (an infinite one of K may make scores of -inf, which would weigh nothing)
+        if (!is_v && !(fabsf(c.scale) < INFINITY)) c.scale = NAN;
       }
       return c;
     };

@@ -202,3 +202,28 @@ def test_values_near_the_ends_of_the_range(n, H, size):
         assert np.isfinite(got[0]).all() and np.isfinite(got[1]).all()
         for b in sorted({0, B // 2, B - 1}):
             check(got, q, cache, table, lens, b)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("H", [2, 5, 20])      # 6, 15 and 60 rows
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_keys_of_a_scale_that_is_not_finite(bad, H, page):
+    """Whatever the sign of its products, such a page gives NaN to the tokens that see
+    it (here the last, and the first in a window that the second does not reach back
+    to), and nothing to the others."""
+    d = 64
+    cache = pc.random_cache(6, 1, page, d, "int8", seed=10)
+    table, lens = ints([[4, 2, 0, 5]]), [3 * page + 1]
+    q = pc.normal((1, H, 3, d), "bf16", 11).abs().cuda()
+    cache.k.copy_(cache.k.float().abs())
+    for large, window, seen, other in ((3, None, [2], [0, 1]), (1, page, [0], [1, 2])):
+        ref = fa.attention_decode_paged(q, cache, table, ints(lens), window=window)
+        for sign in (1, -1):
+            spoilt = fa.PagedCache(*(x.clone() for x in cache))
+            spoilt.k_scale[int(table[0, large])] = bad
+            spoilt.k[int(table[0, large])] *= sign
+            o, lse = fa.attention_decode_paged(q, spoilt, table, ints(lens), window=window)
+            status_ok()
+            assert torch.isnan(o[:, :, seen]).all() and torch.isnan(lse[:, :, seen]).all()
+            assert torch.equal(o[:, :, other], ref[0][:, :, other])
+            assert torch.equal(lse[:, :, other], ref[1][:, :, other])
