@@ -556,11 +556,23 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         for (int nt = 0; nt < kTiles; ++nt) {
           const uint64_t q2 = ptx::f2_pack(qmul[nt][0], qmul[nt][1]);
           const uint64_t n2 = ptx::f2_pack(-m[nt][0], -m[nt][1]);
+          const uint64_t c2 = ptx::fmul2(q2, k2);
+          float c0, c1;
+          ptx::f2_unpack(c2, c0, c1);
+          if (fmaxf(fabsf(c0), fabsf(c1)) < 0x1p100f) {
 #pragma unroll
-          for (int e = 0; e < 4; e += 2)
-            ptx::f2_unpack(
-                ptx::ffma2(ptx::fmul2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), q2), k2, n2),
-                sv[mt][nt][e], sv[mt][nt][e + 1]);
+            for (int e = 0; e < 4; e += 2)
+              ptx::f2_unpack(
+                  ptx::ffma2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), c2, n2),
+                  sv[mt][nt][e], sv[mt][nt][e + 1]);
+          } else {   // a factor that may not be finite, although a score of 0 is (or it is NaN)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              ptx::f2_unpack(
+                  ptx::ffma2(ptx::fmul2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), q2), k2,
+                             n2),
+                  sv[mt][nt][e], sv[mt][nt][e + 1]);
+          }
         }
       }
       if (!full) {

@@ -227,3 +227,19 @@ def test_keys_of_a_scale_that_is_not_finite(bad, H, page):
             assert torch.isnan(o[:, :, seen]).all() and torch.isnan(lse[:, :, seen]).all()
             assert torch.equal(o[:, :, other], ref[0][:, :, other])
             assert torch.equal(lse[:, :, other], ref[1][:, :, other])
+
+
+@pytest.mark.parametrize("H", [4, 12, 40])
+@pytest.mark.parametrize("bits", [120, 60, -60])
+def test_queries_and_keys_of_opposite_size(bits, H):
+    """Queries of 2^bits and keys of 2^-bits, whose products are of usual size."""
+    for d, code in ((64, "int8"), (128, "e4m3")):
+        cache = pc.random_cache(7, 1, 48, d, code, seed=12)
+        cache.k_scale.mul_(2.0 ** (-bits / 2)).mul_(2.0 ** (-bits / 2))
+        table, lens = ints([[4, 2, 0, 5, 6]]), [230]
+        q = (pc.normal((1, H, 2, d), "bf16", 13).float() * 2.0 ** (bits / 2) * 2.0 ** (bits / 2)).bfloat16().cuda()
+        check(decode(q, cache, table, lens), q, cache, table, lens, 0)
+    # keys of 0 score 0, whatever their scale
+    cache.k.view(torch.uint8).zero_()
+    cache.k_scale.fill_(2.0 ** 40)
+    check(decode(q, cache, table, lens), q, cache, table, lens, 0)
