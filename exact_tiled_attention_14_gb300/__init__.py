@@ -1759,16 +1759,27 @@ def _autograd():
         def forward(ctx, q, k, freqs, positions, seqlens, mscale, interleaved):
             ctx.save_for_backward(freqs, positions, seqlens)
             ctx.args = (mscale, interleaved)
+            ctx.shapes = (q.shape, None if k is None else k.shape)
+            ctx.like = dict(dtype=q.dtype, device=q.device)
+            ctx.set_materialize_grads(False)
             return rotary_forward(q, k, freqs, positions, seqlens, mscale, interleaved)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, dq, dk):
-            freqs, positions, seqlens = ctx.saved_tensors
-            dq = _whole_rows(dq)
-            dk = None if dk is None else _whole_rows(dk)
-            return (*rotary_backward(dq, dk, freqs, positions, seqlens, *ctx.args), None, None, None,
-                    None, None)
+            # only what is asked for is rotated; an unused result's gradient is 0, and so is
+            # its rotation
+            grads, turn = [None, None], {}
+            for i, g in enumerate((dq, dk)):
+                if ctx.needs_input_grad[i] and g is not None:
+                    turn[i] = _whole_rows(g)
+                elif ctx.needs_input_grad[i]:
+                    grads[i] = torch.zeros(ctx.shapes[i], **ctx.like)
+            if turn:
+                out = rotary_backward(*(list(turn.values()) + [None])[:2], *ctx.saved_tensors, *ctx.args)
+                for i, g in zip(turn, out):
+                    grads[i] = g
+            return (*grads, None, None, None, None, None)
 
     return (_FlashAttention, _FlashAttentionKv, _FlashAttentionVarlen, _FlashAttentionWindow,
             _Rotary)
