@@ -454,17 +454,17 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         for (int k = 0; k < kSteps; ++k)
           x[k] = *reinterpret_cast<const uint4*>(codes + from[k & 1] + (k * kStep & ~7) * D);
         // The next copy may write the slot once this arrives, and nothing orders a copy
-        // behind loads whose results are not used yet: a store that needs all of them
-        // goes first (its word is never read).  Without it up to a third of the runs over
-        // short units had a tile with the next but one's codes; it costs 1 us of 63.
+        // behind loads whose results are not used yet.  So every lane first stores a word
+        // that it can form only from all of its loads (nobody reads it, and whose store
+        // stays does not matter); the warp meets behind the stores, and only then does
+        // one lane arrive.  Without it up to a third of the runs over short units had a
+        // tile with the next but one's codes; it costs 1 us of 63.
         uint32_t all = 0;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) all |= x[k].x | x[k].y | x[k].z | x[k].w;
+        ptx::st_shared(sbase + L::kMisc + 8, all);
         __syncwarp();
-        if (lane == 0) {
-          ptx::st_shared(sbase + L::kMisc + 8, all);
-          ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
-        }
+        if (lane == 0) ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
         if (is_v) {
           const uint32_t have = meta_of(ms)->have;
           const bool full = have == 255u && key0 + kDtKeys - 1 <= pos_hi &&

@@ -243,3 +243,31 @@ def test_queries_and_keys_of_opposite_size(bits, H):
     cache.k.view(torch.uint8).zero_()
     cache.k_scale.fill_(2.0 ** 40)
     check(decode(q, cache, table, lens), q, cache, table, lens, 0)
+
+
+@pytest.mark.parametrize("B,Hk,G,Nq,page,per,d,code", [
+    (8, 8, 8, 8, 128, 6, 64, "int8"), (150, 1, 17, 1, 16, 9, 128, "e4m3"), (40, 4, 8, 16, 32, 13, 128, "int8"),
+    (300, 2, 9, 2, 48, 3, 64, "e4m3"), (7, 5, 33, 3, 80, 21, 128, "e4m3"),
+])
+def test_every_run_of_many_rows_gives_the_same_bits(B, Hk, G, Nq, page, per, d, code):
+    """Codes are turned out of slots that the next copies write: a copy that came
+    before all lanes have their codes would change some run's result.  Other work on
+    a second stream moves the copies."""
+    cache = pc.random_cache(B * per, Hk, page, d, code, seed=14)
+    table = torch.randperm(B * per, generator=torch.Generator().manual_seed(15)).view(B, per).int().cuda()
+    lens = torch.randint(0, per * page + 1, (B,), generator=torch.Generator().manual_seed(16),
+                         dtype=torch.int32).cuda()
+    q = pc.normal((B, Hk * G, Nq, d), "fp16", 17).cuda()
+    ws = fa.make_paged_workspace(q, cache, table)
+    want = fa.attention_decode_paged(q, cache, table, lens, workspace=ws)
+    side, noise = torch.cuda.Stream(), torch.zeros(1 << 24, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    differ = torch.zeros(300, dtype=torch.bool, device="cuda")
+    for i in range(300):
+        if i % 3 == 0:
+            with torch.cuda.stream(side):
+                noise.add_(1.0)
+        o, lse = fa.attention_decode_paged(q, cache, table, lens, workspace=ws)
+        differ[i] = (o != want[0]).any() | (lse != want[1]).any()
+    status_ok()
+    assert not differ.any()
