@@ -1306,6 +1306,67 @@ def _rows_differ(t):
     return True
 
 
+def _overlap(a, b):
+    """Whether a and b [B, H, N, d] of one dtype share an element (False too where
+    neither their strides nor their density tell)."""
+    if not a.numel() or not b.numel():
+        return False
+    off = (b.data_ptr() - a.data_ptr()) // a.element_size()
+    _, s, n, _ = a.stride()
+    if a.stride() == b.stride() and 0 < s < n and a.stride(0) % n == 0:     # slices of tokens' rows
+        _, heads, _, d = a.shape
+        if (heads - 1) * s + d <= off % n and off % n + (b.shape[1] - 1) * s + d <= n:
+            return False
+
+    def reach(t):
+        return sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1
+    if off >= reach(a) or -off >= reach(b):
+        return False
+    dims = []                                   # (stride, lowest and highest difference of indices)
+    for m, n, s, t in zip(a.shape, b.shape, a.stride(), b.stride()):
+        if m > 1 and n > 1 and s != t:
+            return all(_rows_differ(x) and x.numel() == reach(x) for x in (a, b))
+        dims.append((s if m > 1 else t, 1 - n, m - 1))
+    dims.sort()
+
+    def meets(off, k):                          # a sum of the first k dims' steps that is off
+        if k == 0:
+            return off == 0
+        stride, lo, hi = dims[k - 1]
+        if stride == 0:
+            return meets(off, k - 1)
+        below = sum(s * x for s, x, _ in dims[:k - 1])
+        above = sum(s * x for s, _, x in dims[:k - 1])
+        first, last = -((above - off) // stride), (off - below) // stride
+        return any(meets(off - i * stride, k - 1) for i in range(max(first, lo), min(last, hi) + 1))
+    return meets(off, len(dims))
+
+
+def _check_apart(what, q, si, k, ki, qo, so, ko, so_k):
+    """Refuse results that overlap each other or an input that they are not
+    (tensors [B, H, N, d] of 16 bits, their first strides)."""
+    B, H, N, d = q.shape
+
+    def place(t, s, heads):
+        at = t.data_ptr()
+        return t, at, at + 2 * ((B - 1) * s[0] + (heads - 1) * s[1] + (N - 1) * s[2] + d), s
+    x, y = place(q, si, H), place(qo, so, H)
+    kept = x[1:] == y[1:]                       # in place
+    pairs = [] if kept else [(x, y)]
+    if k is not None:
+        Hk = k.shape[1]
+        z, w = place(k, ki, Hk), place(ko, so_k, Hk)
+        pairs.append((y, w))
+        if not kept:
+            pairs.append((x, w))
+        if z[1:] != w[1:]:
+            pairs += [(z, w), (z, y)]
+    for a, b in pairs:
+        if a[1] < b[2] and b[1] < a[2] and _overlap(a[0], b[0]):
+            raise ValueError(f"{what}: out may be q and k themselves, but not overlap them or itself "
+                             "otherwise")
+
+
 _NO_STRIDES = (0, 0, 0)
 
 
@@ -1346,6 +1407,7 @@ def _rotary(what, q, k, freqs, positions, seqlens, mscale, interleaved, inverse,
         so = _row_strides(qo, what)
         if k is not None:
             ko = _row_strides(ko_t, what)
+        _check_apart(what, q, si, k, ki, qo, so, ko_t, ko)
     with _on(stream, device):
         if out is None:
             import torch
@@ -1382,7 +1444,8 @@ def rotary_forward(q, k, freqs, positions=None, seqlens=None, mscale=1.0, interl
     [B, N]; or ``seqlens`` int32 [B], token i sitting at seqlens[b] - N + i
     (the last tokens of each sequence, as the decoding calls place them); or
     neither, token i sitting at i.  Returns contiguous tensors, or ``out``, a
-    pair of tensors that may be (q, k) themselves.  Calls ``fa_rotary``.
+    pair of tensors that may be (q, k) themselves, but must not overlap them or
+    each other otherwise.  Calls ``fa_rotary``.
     """
     return _rotary("rotary_forward", q, k, freqs, positions, seqlens, mscale, interleaved, 0, out,
                    stream)
