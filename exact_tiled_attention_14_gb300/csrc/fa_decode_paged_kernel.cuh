@@ -13,15 +13,14 @@
 // the scores in float32.  V's scale joins the weights: O is held in units of a power
 // of two that follows the scales, and p * vs / unit is rounded to half precision:
 // by 2^-11 of a weight, or by 2^-25 units where it is below 2^-14 of them.  A weight
-// p is up to 2^6 (its row's reference rises with scores that pass it by more), the
-// largest scale up to 2^8 units, and while no scale but 0 is under 2^-6 of the largest
+// p is up to 2^8 (its row's reference rises with scores that pass it by more), the
+// largest scale up to 2^6 units, and while no scale but 0 is under 2^-4 of the largest
 // the smallest step is 2^-27 of a weight of 1 at most.  Once one is, each row
 // has a unit of its own (paged_row_unit), so that pages that a row does not see,
 // or gives no weight, cost it nothing.  (As a multiply of each page's product before
 // it joined the output the scale took a second set of accumulators and a quarter of
-// a tile's instructions.  A threshold of 2^4 with 2^10 units took the kernel for
-// many rows 71 us instead of 64 for 64 rows of 8 int8 caches at d = 64, scores of a
-// standard deviation of 2.5 powers of two.)
+// a tile's instructions.  A threshold of 2^6 with 2^8 units, references that rise more
+// often, took 64 rows of 8 caches 66 us instead of 63.5.)
 //
 // Bound.  A key costs 2 d bytes and 4 d R operations: HBM bounds it, an SM's
 // share is 23 bytes a cycle.  The codes have to be turned into 16-bit
@@ -69,7 +68,7 @@ constexpr int kDpTileBytes = 4096;       // of K, and of V
 // A run takes this many tiles at least: a part is 4 KB for each row tile at
 // d = 128, a tile 8 KB.
 __host__ __device__ constexpr int dp_min_tiles(int tiles) { return tiles + 1; }
-constexpr float kDpTau = 6.0f;           // lazy-rescale threshold, log2 units
+constexpr float kDpTau = 8.0f;           // lazy-rescale threshold, log2 units
 constexpr uint32_t kSiteDpFull = 50;
 __host__ __device__ constexpr int dp_keys(int d) { return kDpTileBytes / d; }
 
@@ -137,12 +136,12 @@ __host__ __device__ __forceinline__ bool paged_sees(int key0, int n, int pos, in
   return key0 <= pos && (key0 + n - 1 > pos - win || key0 < sinks);
 }
 
-// The unit of O is 2^-8 of a power of two that is not below the scales so far: a
-// weight of up to 2^6 is at most 2^14 units (2^15 for scales over 2^127).  Once the
-// smallest scale but 0 is under 2^-6 of that power (they are apart), each row has
-// a unit of its own, by the largest product c of a weight (over 2^6) and its
+// The unit of O is 2^-6 of a power of two that is not below the scales so far: a
+// weight of up to 2^8 is at most 2^14 units (2^15 for scales over 2^127).  Once the
+// smallest scale but 0 is under 2^-4 of that power (they are apart), each row has
+// a unit of its own, by the largest product c of a weight (over 2^8) and its
 // scale: it falls as the row's reference rises, instead of O, and rises with c.
-constexpr float kDpUnit = 0x1p8f, kDpSpread = 0x1p6f;
+constexpr float kDpUnit = 0x1p6f, kDpSpread = 0x1p4f;
 __host__ __device__ __forceinline__ bool paged_new_unit(float unit, float top) {
   return top > unit * kDpUnit;
 }
@@ -230,6 +229,13 @@ __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uin
       " {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x, its magnitude at most `most` (NaN stays).
+__device__ __forceinline__ float dp_cap(float x, float most) {
+  float y;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+  return y;
 }
 
 // A place in the list of all tiles.
@@ -464,6 +470,13 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         m[nt][e] = 0.f;                      // the reference, 0 before the first score
         l[nt][e] = 0.f;
       }
+    // K's scales are capped where a factor of the scores would pass 2^120 and might not be
+    // finite where a score of 0 is (another one then passes 2^87)
+    float ks_most = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < kTiles; ++nt)
+      ks_most = fmaxf(ks_most, fmaxf(qmul[nt][0], qmul[nt][1]));
+    ks_most = 0x1p120f / ks_most;
     float o[kJ][kTiles][4] = {};
     float o_unit[kTiles][2] = {};              // of O, by rows (0: nothing summed yet)
     float vs_least = INFINITY;               // smallest scale of values but 0; 0: they are apart
@@ -541,7 +554,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
         // (an infinite one may make scores of -inf, which would weigh nothing)
-        const float ks = fabsf(sc[box_of(mt)]) < INFINITY ? sc[box_of(mt)] : NAN;
+        const float ks =
+            dp_cap(fabsf(sc[box_of(mt)]) < INFINITY ? sc[box_of(mt)] : NAN, ks_most);
         const uint64_t k2 = ptx::f2_pack(ks, ks);
         vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
         // (a page that no row sees may have any scale)
@@ -557,22 +571,10 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
           const uint64_t q2 = ptx::f2_pack(qmul[nt][0], qmul[nt][1]);
           const uint64_t n2 = ptx::f2_pack(-m[nt][0], -m[nt][1]);
           const uint64_t c2 = ptx::fmul2(q2, k2);
-          float c0, c1;
-          ptx::f2_unpack(c2, c0, c1);
-          if (fmaxf(fabsf(c0), fabsf(c1)) < 0x1p100f) {
 #pragma unroll
-            for (int e = 0; e < 4; e += 2)
-              ptx::f2_unpack(
-                  ptx::ffma2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), c2, n2),
-                  sv[mt][nt][e], sv[mt][nt][e + 1]);
-          } else {   // a factor that may not be finite, although a score of 0 is (or it is NaN)
-#pragma unroll
-            for (int e = 0; e < 4; e += 2)
-              ptx::f2_unpack(
-                  ptx::ffma2(ptx::fmul2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), q2), k2,
-                             n2),
-                  sv[mt][nt][e], sv[mt][nt][e + 1]);
-          }
+          for (int e = 0; e < 4; e += 2)
+            ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), c2, n2),
+                           sv[mt][nt][e], sv[mt][nt][e + 1]);
         }
       }
       if (!full) {
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         const int r = nt * 8 + 2 * t + e;
         if (r >= rows) continue;
         // (in this order nothing leaves float32's range that the result does not)
-        const float inv = 1.f / lt;
+        const float inv = ptx::rcp(lt);
         float x[2 * kJ];
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
@@ -859,8 +861,7 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDpCombineThreads : kGroups * (
         l += w[k];
       }
       m = now;
-      if (l == 0.f) continue;
-      const float inv = 1.f / l, fo = was * inv;
+      const float inv = l != 0.f ? ptx::rcp(l) : 0.f, fo = was * inv;
       acc = make_float4(acc.x * fo, acc.y * fo, acc.z * fo, acc.w * fo);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
@@ -878,27 +879,26 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDpCombineThreads : kGroups * (
       acc_s[group][c] = acc;
       if (c == 0) ml_s[group] = make_float2(m, l);
       __syncthreads();
-      if (group == 0) {
-        top = -INFINITY;
-        lt = 0.f;
-        sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (threadIdx.x < 32) {              // group 0's warp: a lane for each group's weight
+        const float2 part = threadIdx.x < kGroups ? ml_s[threadIdx.x] : make_float2(0.f, 0.f);
+        top = part.y != 0.f ? part.x : -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k)
-          if (ml_s[k].y != 0.f) top = fmaxf(top, ml_s[k].x);
+        for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        float f = part.y != 0.f ? ptx::ex2(part.x - top) * part.y : 0.f;
+        lt = f;
+#pragma unroll
+        for (int k = 1; k < 32; k *= 2) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+        f *= lt != 0.f ? ptx::rcp(lt) : 0.f;
+        sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = 0; k < kGroups; ++k)
-          if (ml_s[k].y != 0.f) lt += ptx::ex2(ml_s[k].x - top) * ml_s[k].y;
-        const float inv = 1.f / lt;
-#pragma unroll 4
-        for (int k = 0; k < kGroups; ++k)
-          if (ml_s[k].y != 0.f) {
-            const float f = ptx::ex2(ml_s[k].x - top) * ml_s[k].y * inv;
-            const float4 x = acc_s[k][c];
-            sum.x = fmaf(f, x.x, sum.x);
-            sum.y = fmaf(f, x.y, sum.y);
-            sum.z = fmaf(f, x.z, sum.z);
-            sum.w = fmaf(f, x.w, sum.w);
-          }
+        for (int k = 0; k < kGroups; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, k);
+          const float4 x = acc_s[k][c];
+          sum.x = fmaf(fk, x.x, sum.x);
+          sum.y = fmaf(fk, x.y, sum.y);
+          sum.z = fmaf(fk, x.z, sum.z);
+          sum.w = fmaf(fk, x.w, sum.w);
+        }
       }
     }
     if (group == 0) {

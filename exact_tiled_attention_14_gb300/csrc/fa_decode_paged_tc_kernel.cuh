@@ -54,12 +54,13 @@ enum DtWaitSite : uint32_t {
   kSiteDtQReady = 63
 };
 
-// Scales of a tile by 16 keys, and which of the eight name a page.
+// Scales of a tile by 16 keys (V's in units of `unit`, see paged_unit), and which of
+// the eight name a page; bit 8: the scales of V so far are apart (paged_apart).
 struct DtMeta {
   float ks[8], vs[8];
   uint32_t have;
-  float top, least;        // the largest and the smallest finite |vs| but 0 of those that some row sees
-  uint32_t pad;
+  float unit;
+  uint32_t pad[2];
 };
 
 template <int D>
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     struct Box {
       int page = -1, hk = 0, row = 0;            // page (-1: none), head, first row in the page
       bool seen = false;                         // by some row
+      bool first = false;                        // of a piece of a unit
     };
     auto look = [&]() {
       Box x;
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         x.row = key - nth * p.page;
         x.hk = nx.hk;
         x.seen = paged_seen(nx.s, p.Nq, key, box_rows, p.win, p.sinks);
+        x.first = nx_j == 0 || nx.tile == 0;
         if (key < nx.s.len) x.page = p.table[static_cast<size_t>(nx.b) * p.per_seq + nth];
       }
       skip(4);
@@ -235,10 +238,10 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     struct Code {
       int row;                                   // of the cache (-1: none)
       float scale;
-      bool seen;
+      bool seen, first;
     };
     auto resolve = [&](const Box& x) {
-      Code c{-1, 0.f, x.seen};
+      Code c{-1, 0.f, x.seen, x.first};
       if (x.page >= 0 && x.page < p.pages) {
         const int head = x.page * p.Hk + x.hk;
         c.row = head * p.page + x.row;
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     bool alive = true;
     int issued = 0;
     const int per = 8 / p.boxes;
+    float unit = 0.f, vs_least = INFINITY;       // of O, and the smallest scale of V but 0, in the piece
 #pragma unroll 1
     for (int j = 0; j < left && alive; ++j) {
       const int ms = j % kDtMetas, use = 2 * j + is_v, slot = use % L::kSlots;
@@ -275,23 +279,32 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         alive = ptx::warp_all(alive && ptx::wait_bounded(bar(L::bMetaEmpty + ms),
                                                          (j / kDtMetas - 1) & 1, wd,
                                                          kSiteDtMetaEmpty));
-      if (ahead == (j & 3) && box < p.boxes) {
-        float* const to = is_v ? metas[ms].vs : metas[ms].ks;
-        for (int i = box * per; i < (box + 1) * per; ++i) to[i] = now.scale;
-      }
+      float per_unit = 1.f;
       if (is_v) {
+        // the unit of O rises with the scales that some row sees, until they are apart
         const float size = mine && now.seen && fabsf(now.scale) < INFINITY ? fabsf(now.scale) : 0.f;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
-        const uint32_t least =
-            __reduce_min_sync(0xffffffffu, size > 0.f ? __float_as_uint(size) : kInfBits);
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(size)));
+        const float least = __uint_as_float(
+            __reduce_min_sync(0xffffffffu, size > 0.f ? __float_as_uint(size) : kInfBits));
+        if (__any_sync(0xffffffffu, ahead == (j & 3) && now.first)) {
+          unit = 0.f;
+          vs_least = INFINITY;
+        }
+        if (paged_new_unit(unit, top)) unit = paged_unit(top);
+        per_unit = paged_per_unit(unit);
+        vs_least = fminf(vs_least, least);
         // (a box's bit for each 16 keys of it)
         const uint32_t bits =
             __ballot_sync(0xffffffffu, lane < 8 && (have >> (lane * p.boxes / 8) & 1u));
         if (lane == 0) {
-          metas[ms].have = bits;
-          metas[ms].top = __uint_as_float(top);
-          metas[ms].least = __uint_as_float(least);
+          metas[ms].have = bits | (paged_apart(unit, vs_least) ? 256u : 0u);
+          metas[ms].unit = unit;
         }
+      }
+      if (ahead == (j & 3) && box < p.boxes) {
+        float* const to = is_v ? metas[ms].vs : metas[ms].ks;
+        const float x = is_v ? now.scale * per_unit : now.scale;
+        for (int i = box * per; i < (box + 1) * per; ++i) to[i] = x;
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(L::bMetaFull + ms));
@@ -466,7 +479,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::bCodesEmpty + slot));
         if (is_v) {
-          const uint32_t have = meta_of(ms)->have;
+          const uint32_t have = meta_of(ms)->have & 255u;
           const bool full = have == 255u && key0 + kDtKeys - 1 <= pos_hi &&
                             (key0 > pos_lo - p.win || key0 + kDtKeys <= p.sinks);
           __syncwarp();
@@ -535,8 +548,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const int pos = s.len - p.Nq + (row0 + r) % p.Nq;
       const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
       float m = 0.f, l = 0.f,                    // the reference, 0 before the first score
-            o_unit = 0.f, qmul = 0.f;              // the unit of O
-      float vs_least = INFINITY;                 // smallest scale of values but 0; 0: they are apart
+            o_unit = 0.f, qmul = 0.f;            // the unit of O
       bool fresh = true, poison = false;         // no reference yet; a page's scale of values is not finite
       for (int i = 0; i < n; ++i, ++j) {
         const int ms = j % kDtMetas, b = j & 1;
@@ -546,8 +558,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         __syncwarp();
         ptx::tc_fence_after();
         const volatile DtMeta* const meta = meta_of(ms);
-        const uint32_t have = meta->have >> (2 * part) & 3u;
-        const float top = meta->top, least = meta->least;
+        const uint32_t bits = meta->have, have = bits >> (2 * part) & 3u;
+        const float unit = meta->unit;
         const float ks[2] = {meta->ks[2 * part], meta->ks[2 * part + 1]};
         float vs[2] = {meta->vs[2 * part], meta->vs[2 * part + 1]};
         // every row sees every key of the thread's
@@ -573,9 +585,6 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           const int shift = shift_s[ms * kDtRows + r];
           qmul = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
         }
-        // the unit of O, alike in every thread until the scales are apart
-        vs_least = fminf(vs_least, least);
-        const float now = paged_new_unit(o_unit, top) ? paged_unit(top) : o_unit;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::bMetaEmpty + ms));
         if (has) {
@@ -634,21 +643,24 @@ __global__ void __launch_bounds__(kDtThreads, 1)
               for (int e = 0; e < 32; ++e) x[e] -= mx;
             }
           }
-          if (paged_apart(now, vs_least)) {
-            vs_least = 0.f;
+          // the unit of O: the tile's, until the scales are apart
+          if (bits & 256u) {
+            vs[0] *= unit;
+            vs[1] *= unit;
             const float c = fmaxf(ptx::ex2(a0 - kDpTau) * fabsf(vs[0]), ptx::ex2(a1 - kDpTau) * fabsf(vs[1]));
             f = paged_row_unit(o_unit, f, row_all(c, [](float u, float v) { return fmaxf(u, v); }));
-          } else if (now != o_unit) {
-            f *= o_unit * paged_per_unit(now);
-            o_unit = now;
+            const float per_unit = paged_per_unit(o_unit);
+            vs[0] *= per_unit;
+            vs[1] *= per_unit;
+          } else if (unit != o_unit) {
+            f *= o_unit * paged_per_unit(unit);
+            o_unit = unit;
           }
-          const float per_unit = paged_per_unit(o_unit);
           uint64_t acc = ptx::f2_pack(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float rv = vs[k] * per_unit;
-            const uint64_t r2 = ptx::f2_pack(rv, rv);
+            const uint64_t r2 = ptx::f2_pack(vs[k], vs[k]);
 #pragma unroll
             for (int e = 16 * k; e < 16 * k + 16; e += 2) {
               float p0, p1;
@@ -704,7 +716,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         });
         poison = signbit(lt);
         lt = fabsf(lt);
-        const float inv = 1.f / lt;
+        const float inv = ptx::rcp(lt);
         const size_t row = head * p.R + row0 + r;
 #pragma unroll 1
         for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {

@@ -828,7 +828,7 @@ int fa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale
  *   other arguments as fa_cache_append.  Any finite scales do, not only
  *   those that fa_cache_append writes: a weight is rounded to 11 bits, or by
  *   2^-27 of its row's largest where it is below 2^-16 of that; where the scales
- *   of a sequence's values differ by more than 2^6, the product of a weight and its
+ *   of a sequence's values differ by more than 2^4, the product of a weight and its
  *   scale is, or by 2^-27 of the row's largest.  (Sums are in float32: values 2^-100
  *   times the largest of a sequence and less may be lost.)
  * A token that sees no key gets O = 0 and LSE = -inf; keys in a page whose

@@ -7,9 +7,9 @@ sum |q||k|.  A weight p_j times the scale vs_j of its values' page is rounded
 to half precision: 2^-11 relative (11 significant bits: steps of 2^-10 from 1 on,
 half of one is off by 2^-11 of 1 at most), or half of the smallest step, 2^-25,
 in the unit of O, and by no more than itself.  While the scales so far are within
-2^6 of one another each is 2^2 units or more, and the half step at most 2^-27
-vs_j.  Once they are not, a row's unit is at most 2^-8 of the power of two next to
-2^-6 of its largest p_j vs_j, or what it was while they were, 2^-2 of its
+2^4 of one another each is 2^2 units or more, and the half step at most 2^-27
+vs_j.  Once they are not, a row's unit is at most 2^-6 of the power of two next to
+2^-8 of its largest p_j vs_j, or what it was while they were, 2^-2 of its
 scales then: 2^-27 max (p vs) a code covers both.  Weights are relative to a
 reference that only rises and that the row's sum is at least 1 times, so for
 codes b and values v = vs b
