@@ -1581,7 +1581,7 @@ def cache_read(cache, page_table, seqlens, length=None, dtype=None, out=None, st
     table's capacity) of each sequence in 16 bits (``dtype``: torch.bfloat16,
     None, or torch.float16), for ``attention_forward_kv`` or
     ``attention_forward_window`` over the cache.  Rows from ``seqlens[b]`` on
-    are zeros.  ``out``: a pair of such tensors.  Calls ``fa_cache_read``."""
+    are zeros.  ``out``: a pair of such tensors, apart from each other.  Calls ``fa_cache_read``."""
     import torch
     what = "cache_read"
     dtype = torch.bfloat16 if dtype is None else dtype
@@ -1597,6 +1597,8 @@ def cache_read(cache, page_table, seqlens, length=None, dtype=None, out=None, st
             raise ValueError(f"{what}: out must be a pair (k, v)")
         for x in out:
             _check_buffer(x, (B, Hk, N, d), dtype, device, "out")
+        if abs(out[0].data_ptr() - out[1].data_ptr()) < out[0].numel() * out[0].element_size():
+            raise ValueError(f"{what}: out's tensors must not overlap")
     with _on(stream, device):
         if out is None:
             out = tuple(torch.empty((B, Hk, N, d), dtype=dtype, device=device) for _ in range(2))

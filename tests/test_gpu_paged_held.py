@@ -68,3 +68,17 @@ def test_long_appends_of_int8(dtype, d, page, rot, inter):
                     freqs=fa.rotary_frequencies(rot, device="cuda"), interleaved=inter)
     status_ok()
     check_append(before, cache, k, v, table, lens, counts, "int8", pc.frequencies(rot), 1.0, inter)
+
+
+def test_read_into_one_tensor_twice_is_refused():
+    cache = pc.random_cache(4, 2, 16, 64, "int8", seed=44)
+    table, lens = ints([[0, 1], [2, 3]]), ints([20, 30])
+    whole = torch.zeros(2 * 2 * 2 * 32 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    n = 2 * 2 * 32 * 64
+    a, b, c = (whole[o:o + n].view(2, 2, 32, 64) for o in (0, n, n - 8))
+    for out in ((a, a), (a, c), (c, b)):
+        with pytest.raises(ValueError):
+            fa.cache_read(cache, table, lens, out=out)
+    want = fa.cache_read(cache, table, lens)
+    assert all(torch.equal(x, y) for x, y in zip(fa.cache_read(cache, table, lens, out=(b, a)), want))
+    status_ok()
