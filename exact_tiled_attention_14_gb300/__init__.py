@@ -1581,7 +1581,8 @@ def cache_read(cache, page_table, seqlens, length=None, dtype=None, out=None, st
     table's capacity) of each sequence in 16 bits (``dtype``: torch.bfloat16,
     None, or torch.float16), for ``attention_forward_kv`` or
     ``attention_forward_window`` over the cache.  Rows from ``seqlens[b]`` on
-    are zeros.  ``out``: a pair of such tensors, apart from each other.  Calls ``fa_cache_read``."""
+    are zeros.  ``out``: a pair of such tensors, apart from each other.  Calls
+    ``fa_cache_read``."""
     import torch
     what = "cache_read"
     dtype = torch.bfloat16 if dtype is None else dtype

@@ -9,12 +9,14 @@
 //
 // Angles.  w_j arrives as turns per position in units of 2^-64, so the
 // product with the position, wrapped at 64 bits as integers wrap, is the
-// angle's fraction of a turn with an error of p * 2^-65 turns whatever its
-// whole turns: 2^-45 at position 2^20, where a float32 angle is off by up to a
-// tenth of a radian.  The fraction is cut to the nearest quarter turn; the rest, at most
-// an eighth, goes in 32 bits (to 2^-34 turns) through the Taylor polynomials of
-// sine and cosine, of which the first terms left out are 2e-9 and 2.5e-8 there
-// (about 30 operations a pair).
+// angle's fraction of a turn, and whole turns cost no bits, where a float32 angle is
+// off by up to a tenth of a radian at position 2^20.  What is off is the
+// frequency: p * 2^-65 turns for one that is rounded to its unit, up to p * 2^-56 for
+// the fastest pairs of one that comes from float64.  The fraction is cut to the
+// nearest quarter turn; the rest, at most an eighth, is cut to 2^-34 turns and goes
+// through the Taylor polynomials of sine and cosine in float32, of which the first
+// terms left out are 2e-9 and 2.5e-8 there (about 30 operations a pair): cosine and
+// sine are off by less than 2^-22, before the product with mscale.
 #pragma once
 
 #include <cstdint>

@@ -289,8 +289,6 @@ __host__ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   return below_b & ~below_a;
 }
 
-// registers -> 32 consecutive 32-bit TMEM columns of this thread's lane.
-// 32 lanes x 16 columns of 32 bits from 16 registers per thread (this warp's lanes).
 __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
 }
@@ -300,6 +298,7 @@ __device__ __forceinline__ void store32(void* at, const uint4 a, const uint4 b) 
                "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                : "memory");
 }
+// 32 lanes x 16 columns of 32 bits from 16 registers per thread (this warp's lanes).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -308,6 +307,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// registers -> 32 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "

@@ -725,8 +725,9 @@ int fa_decode_window_workspace_size(int B, int H, int Hk, int Nq, int Nk, int d,
  *               An input's may be 0 (a broadcast); an output's rows must differ.
  *   d         : 64 or 128.   rot : 16 .. d, a multiple of 16.
  *   freqs     : [rot / 2] w_j as turns per position in units of 2^-64 (device,
- *               16-byte aligned): w_j * 2^64 / (2 pi), rounded.  The angle is
- *               exact to p * 2^-65 turns at any position.
+ *               16-byte aligned): w_j * 2^64 / (2 pi), rounded.  Whole turns
+ *               cost no bits at any position: an angle is p times the given
+ *               frequency to 2^-34 turns, its cosine and sine to 2^-22.
  *   mscale    : finite and > 0 (1; another for some long-context scalings).
  *   interleaved : 0: pair j is elements j and j + rot / 2; else 2 j and 2 j + 1.
  *   positions : NULL or [B, N] int32 (device).
