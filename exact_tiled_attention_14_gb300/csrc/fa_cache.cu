@@ -19,13 +19,13 @@
 //    of all heads are copied to shared memory at once, each thread's own, and
 //    arrive while the cosines and sines, the same for all heads, are formed.
 //    Four prompts of 2049 to 8192 tokens, 8 heads, d = 128 (84 MB in, 42 out): 38
-//    us against 18.5 of their bytes.  15 instructions an element (angles,
+//    us against 18.5 of their bytes, 43 as int8 codes.  15 instructions an element (angles,
 //    unpacking, two reductions, the codes) take half of the issue slots, and
 //    the blocks wait at a barrier for each head; one barrier for all four heads
 //    (41 us) and equal runs of heads for persistent blocks (39) were slower.
 // Read.  16 elements a thread and step, stored as 32 bytes at once so that every
 // sector is written whole (where the outputs begin at one): four caches of 2048 to 16384 tokens 57 us (71 as two
-// halves), 6.1 TB/s with two thirds of it writes.
+// halves; int8 62), 6.1 TB/s with two thirds of it writes.
 #include <cuda_runtime.h>
 
 #include <algorithm>

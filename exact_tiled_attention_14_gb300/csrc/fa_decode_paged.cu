@@ -94,10 +94,12 @@ struct Plan {
   int tiles, row_blocks, slot_rows, grid, runs;
   size_t o_bytes, ml_bytes, bytes;
 };
-// Up to 16 rows the warps' own products win (16 rows of 8 caches to 32k, 4 heads,
-// d = 128: 54 us, 60 with the kernel for many rows; d = 64 43 and 57), from 17 on
-// the other (32 rows 61 us, 76 in blocks of 16 rows; 64 rows 63 and 106; 128 rows
-// 72 and 194).
+// Up to 16 rows the warps' own products win, from 17 on the other kernel (8 caches to
+// 32768, 4 heads; the first kernel in blocks of 16 rows, us):
+//     rows            9    16   17   32   64  128  129   d = 64: 16   32   64
+//     by warps       50    56   82   88  135  248  277           42   64   85
+//     through TMEM   62    63   63   63   64   73  121           59   58   60
+// (16 rows of int8 57 and 63; 129 rows are two units, the second nearly empty.)
 int row_tiles(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : kManyTiles; }
 int tile_keys(int tiles, int d) { return tiles == kManyTiles ? kDtKeys : dp_keys(d); }
 // Tiles of all units at most: whole capacities, and one of each sequence's own.

@@ -29,13 +29,13 @@
 // every 174 cycles), and mma.sync takes registers as they are.  tcgen05 would
 // need them written to shared memory or TMEM first, and its 8-bit kinds would
 // need the queries and weights in 8 bits too.  Measured: 64 caches of 16384, 8
-// K/V heads, 4 rows, d = 128 (1.34 GB): 211 us for this kernel, 6.4 TB/s of 6.8,
+// K/V heads, 4 rows, d = 128 (1.34 GB): 213 us for this kernel, 6.3 TB/s of 6.8,
 // and 6 for the second; 8 caches of 131072 as int8, 8 rows: 325 to 345 us, 6.2 to
 // 6.6 TB/s.  One cache of 8192 takes 14 us against 2.5 of its bytes: two launches
 // and the chain of a run's start, two tiles and the parts' sum.
 // The tile's loops stay rolled where registers allow it: all of them unrolled were
 // 24 KB of code, warps waited 3.3 of 8.4 cycles an instruction for it to arrive,
-// and the 217 us above were 298.
+// and the 219 us above were 298.
 //
 // Layout.  S^T = K Q^T and O^T += V^T P^T: the 16-row side of m16n8k16 goes
 // to keys (head elements for O), the 8-row side to the query rows, since few

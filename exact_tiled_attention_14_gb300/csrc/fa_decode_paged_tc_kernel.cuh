@@ -5,20 +5,20 @@
 // The function, the queries' powers of two, the placing of the scales and the
 // unit of O are those of fa_decode_paged_kernel.cuh.  There a warp turns codes
 // into 16-bit registers for its own products, which costs as many issue slots
-// again for each 16 rows: 64 rows of 8 caches took 113 us against 25 of their
-// bytes.  Here codes are turned once for all rows, by warps of their own, into
+// again for each 16 rows (figures at row_tiles in fa_decode_paged.cu).  Here codes are turned once for all rows, by warps of their own, into
 // half-precision tiles in shared memory, and a product of 128 rows costs a
 // tile 544 cycles whatever their number.
 //
 // Cost (d = 128, a tile of 128 keys, 32 KB): its share of HBM 1394 cycles of
 // an SM, the products 1088, 1800 of shared-memory traffic (codes in and out 64
 // KB, half-precision tiles in and out 128 KB, queries 32 KB).  What bounds it is
-// none of them but a softmax thread's chain, 2520 cycles a tile at 64 rows and
-// 2820 at 128 (of 20 parts about 3 to read the scores, 3 to their maximum, 2 to
+// none of them but a softmax thread's chain, some 2650 cycles a tile at 64 rows and
+// 2900 at 128 (of 20 parts about 3 to read the scores, 3 to their maximum, 2 to
 // meet, 6 for the weights, 3 to store them, 3 around the loop), and at the ends of a
 // run 12000 cycles to the first scores and 4000 to leave a part.  8 caches to
-// 32768, 4 K/V heads (169 MB, 25 us): 32 rows 61 us, 64 rows 63, 128 rows 72; at
-// d = 64 64 rows take 59.
+// 32768, 4 K/V heads (169 MB, 25 us): 32 and 64 rows 63.5 us, 128 rows 73.5; at
+// d = 64 64 rows take 59.5.  Scales of V that differ by more than 2^4, for which a
+// row's threads meet in every tile, add 10 %.
 //
 // One CTA (27 warps) per SM, persistent over its run of key tiles:
 //   warps 0-15   softmax: warp w has rows 32 (w % 4) .. + 31, one a lane, and
@@ -27,7 +27,8 @@
 //   warps 16-19  K tiles to half precision, and the queries at a unit's start;
 //   warps 20-23  V tiles, rows that no row of the unit sees as zeros
 //                (up to 64 rows softmax warps without rows do both: see `turner`);
-//   warps 24, 25 pages, scales and the TMA loads, of K and of V;
+//   warps 24, 25 pages, scales and the TMA loads, of K and of V (and, with V's
+//                scales, the unit of O that they call for);
 //   warp 26      S = Q K^T of the next tile, then O += P V of this one.
 // 64 keys a softmax thread instead of 32 took twice as long.  A second copy of up
 // to 64 rows in the idle lanes, which takes every other tile, gained 1 us of 71 and
