@@ -7,8 +7,8 @@
 // v_j = vs * b_j (codes a, b, scales of the key's page),
 //     s_rj = scale * ks * (q_r . a_j),   O_r = sum_j softmax_j(s_r) vs b_j.
 // Codes are exact in half precision, and so are the queries once each row is
-// multiplied by a power of two that brings its largest element to 2^12 (what
-// falls below 2^-24 then is 2^-36 of the row's largest): the products
+// multiplied by a power of two that brings its largest element to 2^12 (an element
+// under 2^-26 of it, 2^-29 of bf16, loses bits): the products
 // accumulate exactly what float32 sums of the codes' values do.  K's scale joins
 // the scores in float32.  V's scale joins the weights: O is held in units of a power
 // of two that follows the scales, and p * vs / unit is rounded to half precision:
@@ -470,15 +470,8 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         m[nt][e] = 0.f;                      // the reference, 0 before the first score
         l[nt][e] = 0.f;
       }
-    // K's scales are capped where a factor of the scores would pass 2^120 and might not be
-    // finite where a score of 0 is (another one then passes 2^87)
-    float ks_most = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < kTiles; ++nt)
-      ks_most = fmaxf(ks_most, fmaxf(qmul[nt][0], qmul[nt][1]));
-    ks_most = 0x1p120f / ks_most;
     float o[kJ][kTiles][4] = {};
-    float o_unit[kTiles][2] = {};              // of O, by rows (0: nothing summed yet)
+    float o_unit[kTiles][2] = {};            // of O, by rows (0: nothing summed yet)
     float vs_least = INFINITY;               // smallest scale of values but 0; 0: they are apart
     uint32_t seen = 0;                       // rows (2 nt + e) with a reference
     const int pos_lo = s.len - p.Nq, pos_hi = s.len - 1;
@@ -554,8 +547,7 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
         // (an infinite one may make scores of -inf, which would weigh nothing)
-        const float ks =
-            dp_cap(fabsf(sc[box_of(mt)]) < INFINITY ? sc[box_of(mt)] : NAN, ks_most);
+        const float ks = fabsf(sc[box_of(mt)]) < INFINITY ? sc[box_of(mt)] : NAN;
         const uint64_t k2 = ptx::f2_pack(ks, ks);
         vs[mt] = (have >> box_of(mt) & 1u) ? sc[4 + box_of(mt)] : 0.f;
         // (a page that no row sees may have any scale)
@@ -570,7 +562,10 @@ __global__ void __launch_bounds__(32 * dp_warps(kTiles), 1)
         for (int nt = 0; nt < kTiles; ++nt) {
           const uint64_t q2 = ptx::f2_pack(qmul[nt][0], qmul[nt][1]);
           const uint64_t n2 = ptx::f2_pack(-m[nt][0], -m[nt][1]);
-          const uint64_t c2 = ptx::fmul2(q2, k2);
+          // (a score of 0 is one whatever its factor; another one passes 2^87 at 2^120)
+          float c0, c1;
+          ptx::f2_unpack(ptx::fmul2(q2, k2), c0, c1);
+          const uint64_t c2 = ptx::f2_pack(dp_cap(c0, 0x1p120f), dp_cap(c1, 0x1p120f));
 #pragma unroll
           for (int e = 0; e < 4; e += 2)
             ptx::f2_unpack(ptx::ffma2(ptx::f2_pack(sv[mt][nt][e], sv[mt][nt][e + 1]), c2, n2),

@@ -831,7 +831,9 @@ int fa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale
  *   2^-27 of its row's largest where it is below 2^-16 of that; where the scales
  *   of a sequence's values differ by more than 2^4, the product of a weight and its
  *   scale is, or by 2^-27 of the row's largest.  (Sums are in float32: values 2^-100
- *   times the largest of a sequence and less may be lost.)
+ *   times the largest of a sequence and less may be lost.)  A query is held in
+ *   half precision next to a power of two: an element under 2^-26 (bf16: 2^-29) of
+ *   its row's largest loses bits.
  * A token that sees no key gets O = 0 and LSE = -inf; keys in a page whose
  * number is outside 0 .. pages - 1 are not seen.  Slots that no token of a
  * sequence sees may hold anything; a page's scale that is not finite reaches

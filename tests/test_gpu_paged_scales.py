@@ -271,3 +271,20 @@ def test_every_run_of_many_rows_gives_the_same_bits(B, Hk, G, Nq, page, per, d, 
         differ[i] = (o != want[0]).any() | (lse != want[1]).any()
     status_ok()
     assert not differ.any()
+
+
+@pytest.mark.parametrize("H", [4, 8, 40])
+def test_a_head_of_extreme_queries_costs_the_others_nothing(H):
+    """Keys of 2^33, queries of 2^-38, and one head of 2^110, whose scores leave
+    float32's range: the other heads' results are as usual."""
+    for d, code in ((64, "int8"), (128, "e4m3")):
+        cache = pc.random_cache(7, 1, 48, d, code, seed=18)
+        cache.k_scale.mul_(2.0 ** 38)
+        table, lens = ints([[4, 2, 0, 5, 6]]), [230]
+        q = pc.normal((1, H, 2, d), "bf16", 19).float() * 2.0 ** -38
+        q[:, 1] *= 2.0 ** 74
+        q[:, 1] *= 2.0 ** 74
+        q = q.bfloat16().cuda()
+        rest = [h for h in range(H) if h != 1]
+        o, lse = decode(q, cache, table, lens)
+        check((o[:, rest], lse[:, rest]), q[:, rest].contiguous(), cache, table, lens, 0)
