@@ -764,7 +764,9 @@ int fa_rotary(const void *q, const void *k, void *q_out, void *k_out, int B, int
  * and codes round(x * (1 / s)), to nearest even.  A page that holds earlier
  * tokens of the sequence keeps its scale s0 where s <= s0; otherwise those
  * tokens' codes become round(code * (s0 * (1 / s))).  (For FA_E4M3 that shifts
- * exponents; it rounds only below 2^-6 s.)  A NaN or infinite element makes
+ * exponents; it rounds only below 2^-6 s.  For FA_INT8 every raise rounds by up to
+ * half a code more: a page whose largest element grows with each of its calls is
+ * off by half a code for each of them.)  A NaN or infinite element makes
  * the scale of its page and head NaN (with new codes of 0), and everything read
  * of it NaN, until the page is filled from its first slot again.
  *

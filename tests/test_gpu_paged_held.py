@@ -82,3 +82,59 @@ def test_read_into_one_tensor_twice_is_refused():
     want = fa.cache_read(cache, table, lens)
     assert all(torch.equal(x, y) for x, y in zip(fa.cache_read(cache, table, lens, out=(b, a)), want))
     status_ok()
+
+
+@pytest.mark.parametrize("H,Nq", [(4, 1), (8, 3), (24, 2)])     # 2, 12 and 24 rows a key/value head
+def test_a_captured_decoding_loop(H, Nq):
+    """Append and decoding captured once: replays read lengths, counts and the page
+    table of their time, as eager calls do, down to empty sequences."""
+    B, Hk, page, per, d = 5, 2, 16, 40, 64
+    caches = [fa.make_paged_cache(2 * B * per, Hk, page, d) for _ in range(2)]
+    tables = [deal(B, per, B * per, seed=60) + x for x in (0, B * per)]
+    table = tables[0].clone()
+    k, v = (torch.zeros(B, Hk, Nq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, n = torch.zeros(B, H, Nq, d, dtype=torch.bfloat16, device="cuda"), ints([0] * B)
+    ws = fa.make_paged_workspace(q, caches[1], table)
+    out, lse = torch.empty_like(q), torch.empty(B, H, Nq, device="cuda")
+
+    def step(cache, **kw):
+        fa.cache_append(k, v, cache, table, n)
+        return fa.attention_decode_paged(q, cache, table, n, window=300, sinks=2, **kw)
+    step(caches[1], out=out, lse=lse, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(caches[1], out=out, lse=lse, workspace=ws)
+    for i, lens in enumerate(([Nq] * B, [600, 17, 0, 33, 640], [640, 1, 16, 0, 0], [0] * B, [5, 300, 301, 640, 2])):
+        for x, t in enumerate((k, v, q)):
+            t.copy_(pc.normal(tuple(t.shape), "bf16", 70 + 3 * i + x).cuda())
+        n.copy_(ints(lens))
+        table.copy_(tables[i % 2])
+        want = step(caches[0])
+        g.replay()
+        status_ok()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), i
+        assert (lse[[b for b, m in enumerate(lens) if m == 0]] == float("-inf")).all()
+
+
+def test_many_short_sequences():
+    """A sequence's result beside 2999 others and alone: each is rounded to bf16 (2^-8
+    of its value), and its weights to 11 bits (2^-11 of at most the largest value); LSE
+    adds up to 48 weights in another order (48 * 2^-24 and the logarithm's own)."""
+    B, Hk, page, per, d = 3000, 1, 16, 3, 64
+    cache = pc.random_cache(50, Hk, page, d, "int8", seed=61)
+    g = torch.Generator().manual_seed(62)
+    table = torch.randint(0, 50, (B, per), generator=g, dtype=torch.int32).cuda()
+    lens = torch.randint(0, per * page + 1, (B,), generator=g, dtype=torch.int32).cuda()
+    q = pc.normal((B, 20, 1, d), "bf16", 63).cuda()
+    vmax = (cache.v.float().abs().amax((1, 2, 3)) * cache.v_scale[:, 0]).max()
+    for heads in (2, 10, 20):
+        o, lse = fa.attention_decode_paged(q[:, :heads].contiguous(), cache, table, lens)
+        status_ok()
+        some = list(range(0, B, 499)) + [B - 1]           # alone: whole units in other places
+        for b in some:
+            x, y = fa.attention_decode_paged(q[b:b + 1, :heads].contiguous(), cache, table[b:b + 1].contiguous(),
+                                             lens[b:b + 1])
+            assert ((o[b] - x[0]).abs().float() <= 2.0 ** -7 * x[0].abs().float() + 2.0 ** -10 * vmax).all()
+            assert torch.equal(lse[b].isinf(), y[0].isinf())
+            assert (lse[b] - y[0]).nan_to_num(0.0, 0.0, 0.0).abs().max() <= 2.0 ** -15
+    status_ok()
